@@ -65,9 +65,11 @@ typedef enum dsa_status {
   DSA_ERR_DEVICE_TIMEOUT = 6,    /* a kernel's bounded wait ran out */
   DSA_ERR_DEVICE_BAD_INDEX = 7,  /* a kernel read an out-of-range pool index */
   DSA_ERR_SCRATCH_CAP = 8,       /* one score chunk would exceed scratch_cap */
-  DSA_ERR_DEVICE_CHECK = 9       /* debug build (DSA_CHECKS) only: a kernel computed an
+  DSA_ERR_DEVICE_CHECK = 9,      /* debug build (DSA_CHECKS) only: a kernel computed an
                                     out-of-range shared-memory, TMEM or global offset; the
                                     access was skipped */
+  DSA_ERR_DEVICE_NO_PAGES = 10   /* dsa_build_page_tables: the free list is shorter than
+                                    the pages that the requests need */
 } dsa_status_t;
 
 /* Problem description (one sequence per call; batch = 1).
@@ -362,6 +364,116 @@ DSA_API dsa_status_t dsa_index_scores_topk_static(const dsa_config_t* cfg,
  * read the status word that their kernels latch into *device_status
  * (DSA_OK if nothing was latched) and clear it.  Allocates nothing. */
 DSA_API dsa_status_t dsa_static_device_status(void* stream, uint32_t* device_status);
+
+/* ------------------------------------------------------------- serving
+ * A group of rollouts continues one long prompt ("Scaling Training to 1M
+ * Token Context on GLM-5.3-Flash", "Results": the trainer's log-probs are
+ * compared with those of the engine that sampled the tokens).  The calls
+ * below are that engine's side for a layer whose queries read every cached
+ * key: a cache of pages, its tables, and the attention of a batch of requests
+ * over one shared prefix, read once for all of them, and over their own
+ * tokens.  The key/value layout is the library's: one NoPE K and one V row
+ * per token shared by all heads, or one tensor for both (K = V).
+ *
+ * Cache: k_pages, v_pages [n_pages, page_size, d] bf16.  A token's slot is
+ * page * page_size + offset.  Row b of block_table [batch, max_blocks] int32
+ * lists the pages of request b's own tokens in order (entries past its
+ * length are never read); the prefix has a list of pages of its own.
+ *
+ * Layout is fixed for foreign callers: 48 bytes, natural alignment. */
+typedef struct dsa_serve_config {
+  int64_t n_pages;    /* pages of the cache, >= 1; n_pages * page_size < 2^31 - 256 */
+  int64_t max_tokens; /* T, rows of q, slot_map and k_new, >= 1 (< 2^30) */
+  int32_t page_size;  /* tokens per page: 16, 32, 64 or 128 */
+  int32_t batch;      /* B, requests: 1..65536 */
+  int32_t max_blocks; /* entries per block-table row, >= 1; times page_size < 2^30 */
+  int32_t attn_heads; /* H, 1..128 */
+  int32_t d_qk;       /* NoPE q/k dim in {128,256,512} */
+  int32_t d_v;        /* must equal d_qk */
+  float sm_scale;     /* softmax scale; 0 -> 1/sqrt(d_qk) */
+} dsa_serve_config_t;
+
+/* Workspace kinds for dsa_serve_workspace_size(). */
+#define DSA_SERVE_WS_TABLES 0 /* dsa_build_page_tables */
+#define DSA_SERVE_WS_APPEND 1 /* dsa_append_cache */
+#define DSA_SERVE_WS_PREFIX 2 /* dsa_prefix_attn */
+
+/* Bytes of device workspace the serving call `which` needs for `cfg`; the
+ * 256-byte header, dsa_workspace_init() and dsa_get_device_status() are
+ * those of every other workspace.  Two calls whose work may overlap on the
+ * GPU (two streams, two captured graphs replayed side by side) need a
+ * workspace each. */
+DSA_API dsa_status_t dsa_serve_workspace_size(const dsa_serve_config_t* cfg, int32_t which,
+                                              size_t* bytes);
+
+/* Page tables and slots of one step from the requests' lengths.  Request b
+ * holds cached_lens[b] tokens and gets new_lens[b] more:
+ *   have_b = ceil(cached_b / page_size), need_b = ceil((cached_b + new_b) / page_size),
+ *   first_b = sum_{a<b} (need_a - have_a),
+ *   block_table[b, have_b + j] = free_pages[first_b + j]   (0 <= j < need_b - have_b),
+ *   cu_tokens[b] = sum_{a<b} new_a  (b = 0..B),   seq_lens[b] = cached_b + new_b,
+ *   slot_map[cu_tokens[b] + i] = the slot of b's token cached_b + i, by its table row,
+ *   slot_map[t] = -1 for cu_tokens[B] <= t < T,   pages_taken[0] = sum_b (need_b - have_b).
+ * Other entries of block_table are left as they are; those of the pages that
+ * b already holds are read where a slot falls into them.
+ * cached_lens, new_lens, seq_lens [B], cu_tokens [B+1], free_pages [n_free],
+ * pages_taken [1], slot_map [T]: int32.  free_pages may point anywhere into
+ * a longer list (4-byte alignment suffices), so that the next step can start
+ * pages_taken entries further on.
+ * Device-side errors (latched; nothing is written out of bounds): a negative
+ * length or cached + new > max_blocks * page_size gives that request no new
+ * tokens and length 0 (DSA_ERR_DEVICE_BAD_INDEX); a page id outside the
+ * cache gives -1 entries and slots (DSA_ERR_DEVICE_BAD_INDEX); so do pages
+ * past the end of the free list (DSA_ERR_DEVICE_NO_PAGES; pages_taken then
+ * still says how many are needed); tokens past T have no slot and cu_tokens
+ * stops at T (DSA_ERR_DEVICE_BAD_INDEX).  ws: DSA_SERVE_WS_TABLES. */
+DSA_API dsa_status_t dsa_build_page_tables(
+    const dsa_serve_config_t* cfg, const int32_t* cached_lens, const int32_t* new_lens,
+    const int32_t* free_pages, int64_t n_free, int32_t* block_table, int32_t* slot_map,
+    int32_t* cu_tokens, int32_t* seq_lens, int32_t* pages_taken, void* ws,
+    size_t ws_bytes, void* stream);
+
+/* Write the rows of k_new [T, d_qk] (and v_new [T, d_v]) bf16 to their
+ * slots: k_pages row slot_map[t] = k_new[t], v_pages likewise; a negative
+ * slot skips its row, one past the cache latches DSA_ERR_DEVICE_BAD_INDEX and
+ * skips it.  v_new == NULL and v_pages == NULL: K = V, one tensor.  The slots
+ * of one call must be distinct (two rows with one slot leave that slot with
+ * an unspecified mix of both); k_pages must not overlap k_new or v_pages.
+ * ws: DSA_SERVE_WS_APPEND. */
+DSA_API dsa_status_t dsa_append_cache(const dsa_serve_config_t* cfg,
+                                      const int32_t* slot_map, const void* k_new,
+                                      const void* v_new, void* k_pages, void* v_pages,
+                                      void* ws, size_t ws_bytes, void* stream);
+
+/* Attention of a batch over a shared prefix and each request's own tokens.
+ * Query row t belongs to request b when cu_tokens[b] <= t < cu_tokens[b+1];
+ * with new_b = cu_tokens[b+1] - cu_tokens[b] and i = t - cu_tokens[b] its
+ * keys are the prefix tokens 0 .. prefix_len-1 and b's own tokens
+ * 0 .. seq_lens[b] - new_b + i (those at or before its own place, which is
+ * among them once dsa_append_cache has run):
+ *   O[t,h] = sum_j softmax_j(scale * q[t,h] . k_j) v_j,
+ *   LSE[t,h] = log sum_j exp(scale * q[t,h] . k_j)          (natural log).
+ * No keys (prefix_len 0 and no own token at or before it): O = 0, LSE = -inf.
+ * Rows t >= cu_tokens[B] (and rows of no request) of o and lse are left as
+ * they were.  Rows of a page past its request's length, or past prefix_len,
+ * may hold anything, NaN included.
+ * q [T, H, d_qk] bf16; k_pages, v_pages (NULL: K = V) as above;
+ * prefix_table [ceil(prefix_len / page_size)] int32 (NULL when prefix_len is
+ * 0), 0 <= prefix_len < 2^30; block_table [B, max_blocks], seq_lens [B],
+ * cu_tokens [B+1] int32 -> o [T, H, d_v] bf16, lse [T, H] fp32.
+ * T * H <= 2^20, else DSA_ERR_UNSUPPORTED_SHAPE.
+ * Device-side errors (latched as DSA_ERR_DEVICE_BAD_INDEX; nothing is read or
+ * written out of bounds, the affected requests' results are unspecified):
+ * a page id outside the cache in a place that is read, a length below 0 or
+ * above max_blocks * page_size, cu_tokens that start below 0, descend or end
+ * past T.  Results repeat bit for bit on the same inputs and device.
+ * ws: DSA_SERVE_WS_PREFIX. */
+DSA_API dsa_status_t dsa_prefix_attn(const dsa_serve_config_t* cfg, const void* q,
+                                     const void* k_pages, const void* v_pages,
+                                     const int32_t* prefix_table, int64_t prefix_len,
+                                     const int32_t* block_table, const int32_t* seq_lens,
+                                     const int32_t* cu_tokens, void* o, float* lse,
+                                     void* ws, size_t ws_bytes, void* stream);
 
 /* Synchronise `stream`, read the workspace status word into *device_status
  * (a dsa_status_t value, DSA_OK if nothing was latched) and clear it. */

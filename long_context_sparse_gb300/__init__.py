@@ -16,6 +16,7 @@ import dataclasses
 import math
 import os
 import threading
+import typing
 
 import torch
 
@@ -28,6 +29,9 @@ __all__ = [
     "sparse_attn_fwd", "sparse_attn_bwd", "get_device_status",
     "status_string", "library_path", "WS_INDEX", "WS_FWD", "WS_BWD",
     "WS_STATUS",
+    "ServeConfig", "PageTables", "serve_workspace_size", "serve_workspace",
+    "build_page_tables", "append_cache", "prefix_attn", "SERVE_WS_TABLES",
+    "SERVE_WS_APPEND", "SERVE_WS_PREFIX",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -41,12 +45,14 @@ _lock = threading.Lock()
 _lib = None
 
 WS_INDEX, WS_FWD, WS_BWD, WS_STATUS, WS_STREAM, WS_BWD_ROWS, WS_STEP = range(7)
+SERVE_WS_TABLES, SERVE_WS_APPEND, SERVE_WS_PREFIX = range(3)
 
 STATUS_NAMES = {
     0: "DSA_OK", 1: "DSA_ERR_INVALID_ARG", 2: "DSA_ERR_UNSUPPORTED_SHAPE",
     3: "DSA_ERR_WORKSPACE_TOO_SMALL", 4: "DSA_ERR_MISALIGNED",
     5: "DSA_ERR_CUDA", 6: "DSA_ERR_DEVICE_TIMEOUT",
     7: "DSA_ERR_DEVICE_BAD_INDEX", 8: "DSA_ERR_SCRATCH_CAP", 9: "DSA_ERR_DEVICE_CHECK",
+    10: "DSA_ERR_DEVICE_NO_PAGES",
 }
 
 # every symbol include/dsa.h declares
@@ -60,6 +66,8 @@ EXPORTS = [
     "dsa_index_topk_streaming", "dsa_sparse_attn_fwd_range",
     "dsa_sparse_attn_bwd_range", "dsa_accum_to_bf16", "dsa_step",
     "dsa_step_host", "dsa_check_wait_timeout", "dsa_static_device_status",
+    "dsa_serve_workspace_size", "dsa_build_page_tables", "dsa_append_cache",
+    "dsa_prefix_attn",
 ]
 
 
@@ -82,6 +90,18 @@ class _CConfig(ctypes.Structure):
 
 
 assert ctypes.sizeof(_CConfig) == 56
+
+class _CServeConfig(ctypes.Structure):
+    _fields_ = [
+        ("n_pages", ctypes.c_int64), ("max_tokens", ctypes.c_int64),
+        ("page_size", ctypes.c_int32), ("batch", ctypes.c_int32),
+        ("max_blocks", ctypes.c_int32), ("attn_heads", ctypes.c_int32),
+        ("d_qk", ctypes.c_int32), ("d_v", ctypes.c_int32),
+        ("sm_scale", ctypes.c_float),
+    ]
+
+
+assert ctypes.sizeof(_CServeConfig) == 48
 
 # dsa_step_tensors_t: the step's tensors, in declaration order
 STEP_FIELDS = ("q_idx", "k_idx", "w", "k_gate", "q", "k", "v", "dO",
@@ -119,6 +139,29 @@ class Config:
                         float(self.sm_scale), self.scratch_cap)
 
 
+@dataclasses.dataclass(frozen=True)
+class ServeConfig:
+    """Mirror of dsa_serve_config_t."""
+    n_pages: int
+    max_tokens: int
+    batch: int
+    max_blocks: int
+    page_size: int = 64
+    attn_heads: int = 64
+    d_qk: int = 512
+    d_v: int = 512
+    sm_scale: float = 0.0
+
+    @property
+    def scale(self) -> float:
+        return self.sm_scale if self.sm_scale > 0 else 1.0 / math.sqrt(self.d_qk)
+
+    def c(self) -> _CServeConfig:
+        return _CServeConfig(self.n_pages, self.max_tokens, self.page_size,
+                             self.batch, self.max_blocks, self.attn_heads,
+                             self.d_qk, self.d_v, float(self.sm_scale))
+
+
 def config_for(wl: Workload, **over) -> Config:
     cfg = Config(seq_len=wl.S, topk_pools=wl.K_p, n_local=wl.n_loc,
                  idx_heads=wl.H_I, idx_dim=wl.D_I, attn_heads=wl.H,
@@ -144,7 +187,7 @@ def _load():
         lib = ctypes.CDLL(_LIB_PATH)
         P, I32, I64, SZ = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
                            ctypes.c_size_t)
-        CP = ctypes.POINTER(_CConfig)
+        CP, SP = ctypes.POINTER(_CConfig), ctypes.POINTER(_CServeConfig)
         sig = {
             "dsa_workspace_size": [CP, I32, ctypes.POINTER(SZ)],
             "dsa_workspace_init": [P, SZ, P],
@@ -173,6 +216,10 @@ def _load():
             "dsa_step_host": [CP, ctypes.POINTER(_CStepTensors),
                               ctypes.POINTER(_CStepTensors), I32, P, SZ, P, P,
                               P],
+            "dsa_serve_workspace_size": [SP, I32, ctypes.POINTER(SZ)],
+            "dsa_build_page_tables": [SP, P, P, P, I64, P, P, P, P, P, P, SZ, P],
+            "dsa_append_cache": [SP, P, P, P, P, P, P, SZ, P],
+            "dsa_prefix_attn": [SP, P, P, P, P, I64, P, P, P, P, P, P, SZ, P],
         }
         for name, args in sig.items():
             f = getattr(lib, name)
@@ -760,3 +807,151 @@ def get_device_status(ws: torch.Tensor) -> int:
                                          ctypes.byref(v)),
            "dsa_get_device_status")
     return v.value
+
+
+# ---------------------------------------------------------------- serving
+
+
+def serve_workspace_size(cfg: ServeConfig, which: int) -> int:
+    n = ctypes.c_size_t(0)
+    cc = cfg.c()
+    _check(_load().dsa_serve_workspace_size(ctypes.byref(cc), which, ctypes.byref(n)),
+           "dsa_serve_workspace_size")
+    return n.value
+
+
+def serve_workspace(cfg: ServeConfig, which: int, device="cuda") -> torch.Tensor:
+    """A zero-initialised workspace for the serving call `which` (uint8
+    tensor).  Calls that may overlap on the GPU need one each."""
+    dev = torch.device(device)
+    nbytes = serve_workspace_size(cfg, which)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    with torch.cuda.device(dev):
+        _check(_load().dsa_workspace_init(_ptr(ws), nbytes, _stream(dev)),
+               "dsa_workspace_init")
+    return ws
+
+
+def _serve_ws(cfg, which, ws, dev):
+    if ws is None:
+        return serve_workspace(cfg, which, dev)
+    _need(ws, "ws", torch.uint8, device=dev)
+    return ws
+
+
+def _serve_call(name, dev, *args):
+    """One C call on `dev`'s current stream, with `dev` the current device."""
+    if torch.cuda.current_device() == dev.index:
+        _check(getattr(_load(), name)(*args, _stream(dev)), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(getattr(_load(), name)(*args, _stream(dev)), name)
+
+
+class PageTables(typing.NamedTuple):
+    """What build_page_tables writes (see dsa_build_page_tables)."""
+    block_table: torch.Tensor  # [batch, max_blocks] int32, the caller's, in place
+    slot_map: torch.Tensor     # [max_tokens] int32
+    cu_tokens: torch.Tensor    # [batch + 1] int32
+    seq_lens: torch.Tensor     # [batch] int32
+    pages_taken: torch.Tensor  # [1] int32
+
+
+def build_page_tables(cfg: ServeConfig, cached_lens, new_lens, free_pages,
+                      block_table, out: PageTables = None, ws=None) -> PageTables:
+    """Page tables and slots of one step: request b holds cached_lens[b]
+    tokens and gets new_lens[b] more; the pages that it needs come from
+    free_pages [n_free], in request order, and are entered in block_table
+    [batch, max_blocks] in place (other entries stay).  All int32."""
+    B, T, i32 = cfg.batch, cfg.max_tokens, torch.int32
+    _need(cached_lens, "cached_lens", i32, (B,))
+    dev = cached_lens.device
+    _need(new_lens, "new_lens", i32, (B,), dev)
+    _need(free_pages, "free_pages", i32, device=dev)
+    if free_pages.dim() != 1:
+        raise ValueError("free_pages must be [n_free]")
+    _need(block_table, "block_table", i32, (B, cfg.max_blocks), dev)
+    if out is None:
+        out = PageTables(block_table, *(torch.empty(n, dtype=i32, device=dev)
+                                        for n in (T, B + 1, B, 1)))
+    elif out.block_table is not block_table:
+        raise ValueError("out.block_table must be block_table")
+    else:
+        _need(out.slot_map, "slot_map", i32, (T,), dev)
+        _need(out.cu_tokens, "cu_tokens", i32, (B + 1,), dev)
+        _need(out.seq_lens, "seq_lens", i32, (B,), dev)
+        _need(out.pages_taken, "pages_taken", i32, (1,), dev)
+    ws = _serve_ws(cfg, SERVE_WS_TABLES, ws, dev)
+    cc = cfg.c()
+    _serve_call("dsa_build_page_tables", dev, ctypes.byref(cc), _ptr(cached_lens),
+                _ptr(new_lens), _ptr(free_pages), free_pages.numel(),
+                _ptr(block_table), _ptr(out.slot_map), _ptr(out.cu_tokens),
+                _ptr(out.seq_lens), _ptr(out.pages_taken), _ptr(ws), ws.numel())
+    return out
+
+
+def append_cache(cfg: ServeConfig, slot_map, k_new, k_pages, v_new=None,
+                 v_pages=None, ws=None):
+    """Write the rows of k_new [max_tokens, d_qk] (and v_new) to their slots
+    of k_pages (and v_pages) [n_pages, page_size, d], in place; slots below
+    0 are skipped, the others must be distinct.  Without v: K = V."""
+    T, bf = cfg.max_tokens, torch.bfloat16
+    _need(slot_map, "slot_map", torch.int32, (T,))
+    dev = slot_map.device
+    _need(k_new, "k_new", bf, (T, cfg.d_qk), dev)
+    _need(k_pages, "k_pages", bf, (cfg.n_pages, cfg.page_size, cfg.d_qk), dev)
+    if (v_new is None) != (v_pages is None):
+        raise ValueError("v_new and v_pages go together")
+    if v_new is not None:
+        _need(v_new, "v_new", bf, (T, cfg.d_v), dev)
+        _need(v_pages, "v_pages", bf, (cfg.n_pages, cfg.page_size, cfg.d_v), dev)
+    ws = _serve_ws(cfg, SERVE_WS_APPEND, ws, dev)
+    cc = cfg.c()
+    _serve_call("dsa_append_cache", dev, ctypes.byref(cc), _ptr(slot_map),
+                _ptr(k_new), _ptr(v_new), _ptr(k_pages), _ptr(v_pages), _ptr(ws),
+                ws.numel())
+
+
+def prefix_attn(cfg: ServeConfig, q, k_pages, prefix_table, prefix_len: int,
+                block_table, seq_lens, cu_tokens, v_pages=None, o=None, lse=None,
+                ws=None):
+    """Attention of a batch over a shared prefix (prefix_len tokens in the
+    pages prefix_table, read once for all requests) and each request's own
+    tokens (its row of block_table): (o [T,H,d_v] bf16, lse [T,H] fp32), T =
+    max_tokens.  Rows cu_tokens[b] .. cu_tokens[b+1]-1 of q [T,H,d_qk] are
+    the last tokens of request b's seq_lens[b]; a row sees its own place and
+    those before it.  Rows of no request are not written (new outputs hold
+    zeros there).  Without v_pages: K = V.  prefix_table may be None when
+    prefix_len is 0."""
+    T, H, B, bf, i32 = (cfg.max_tokens, cfg.attn_heads, cfg.batch, torch.bfloat16,
+                        torch.int32)
+    _need(q, "q", bf, (T, H, cfg.d_qk))
+    dev = q.device
+    _need(k_pages, "k_pages", bf, (cfg.n_pages, cfg.page_size, cfg.d_qk), dev)
+    if v_pages is not None:
+        _need(v_pages, "v_pages", bf, (cfg.n_pages, cfg.page_size, cfg.d_v), dev)
+    if prefix_len < 0:
+        raise ValueError("prefix_len must not be negative")
+    if prefix_table is None:
+        if prefix_len > 0:
+            raise ValueError("prefix_len > 0 needs a prefix_table")
+    else:
+        _need(prefix_table, "prefix_table", i32, device=dev)
+        if prefix_table.dim() != 1 or prefix_table.numel() * cfg.page_size < prefix_len:
+            raise ValueError("prefix_table must be [>= ceil(prefix_len / page_size)]")
+    _need(block_table, "block_table", i32, (B, cfg.max_blocks), dev)
+    _need(seq_lens, "seq_lens", i32, (B,), dev)
+    _need(cu_tokens, "cu_tokens", i32, (B + 1,), dev)
+    if o is None:
+        o = torch.zeros((T, H, cfg.d_v), dtype=bf, device=dev)
+    if lse is None:
+        lse = torch.zeros((T, H), dtype=torch.float32, device=dev)
+    _need(o, "o", bf, (T, H, cfg.d_v), dev)
+    _need(lse, "lse", torch.float32, (T, H), dev)
+    ws = _serve_ws(cfg, SERVE_WS_PREFIX, ws, dev)
+    cc = cfg.c()
+    _serve_call("dsa_prefix_attn", dev, ctypes.byref(cc), _ptr(q), _ptr(k_pages),
+                _ptr(v_pages), _ptr(prefix_table), int(prefix_len),
+                _ptr(block_table), _ptr(seq_lens), _ptr(cu_tokens), _ptr(o),
+                _ptr(lse), _ptr(ws), ws.numel())
+    return o, lse

@@ -38,13 +38,8 @@ class NvtxRange {
   NvtxRange& operator=(const NvtxRange&) = delete;
 };
 
-constexpr size_t kHeader = 256;        // status word + padding
 constexpr int64_t kPoolTile = 128;     // score row pitch granularity
 constexpr int kMaxDevices = 64;
-
-size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Name of the CUDA error behind the last DSA_ERR_CUDA of this thread.
 thread_local const char* t_last_cuda_error = "no error";
@@ -98,7 +93,8 @@ dsa_status_t get_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn) {
   return DSA_OK;
 }
 
-// 2D bf16 row-major [rows, cols] tensor, box {64 cols, box_rows}, 128B swizzle.
+}  // namespace
+
 dsa_status_t encode_2d(CUtensorMap* map, const void* base, uint64_t rows,
                        uint64_t cols, uint32_t box_rows) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -118,6 +114,8 @@ dsa_status_t encode_2d(CUtensorMap* map, const void* base, uint64_t rows,
   }
   return DSA_OK;
 }
+
+namespace {
 
 uint64_t timeout_ns() {
   static uint64_t v = [] {
@@ -197,6 +195,8 @@ size_t ws_bytes_for(const dsa_config_t* c, int which) {
   }
 }
 
+}  // namespace
+
 dsa_status_t make_ctx(void* ws, void* stream, LaunchCtx* ctx) {
   DeviceInfo d;
   dsa_status_t st = device_info(&d);
@@ -218,6 +218,8 @@ dsa_status_t cuda_status(cudaError_t e) {
   }
   return DSA_ERR_CUDA;
 }
+
+namespace {
 
 dsa_status_t check_ws(const dsa_config_t* cfg, int which, void* ws, size_t ws_bytes) {
   if (!ws) return DSA_ERR_INVALID_ARG;
@@ -291,6 +293,7 @@ const char* dsa_status_string(dsa_status_t s) {
     case DSA_ERR_DEVICE_BAD_INDEX: return "DSA_ERR_DEVICE_BAD_INDEX";
     case DSA_ERR_SCRATCH_CAP: return "DSA_ERR_SCRATCH_CAP";
     case DSA_ERR_DEVICE_CHECK: return "DSA_ERR_DEVICE_CHECK";
+    case DSA_ERR_DEVICE_NO_PAGES: return "DSA_ERR_DEVICE_NO_PAGES";
   }
   return "DSA_ERR_UNKNOWN";
 }

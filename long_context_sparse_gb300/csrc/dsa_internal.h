@@ -7,11 +7,18 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "../../include/dsa.h"
+
 namespace dsa {
 
 // Record a printf-style detail for the calling thread's next DSA_ERR_CUDA
 // (returned by dsa_last_cuda_error).
 void set_error_detail(const char* fmt, ...);
+
+constexpr size_t kHeader = 256;  // workspace header: status word + padding
+
+inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 struct LaunchCtx {
   cudaStream_t stream;
@@ -19,6 +26,15 @@ struct LaunchCtx {
   uint64_t timeout_ns;  // bounded-wait limit for every spin in the kernels
   int num_sms;
 };
+
+// Host helpers of the C-ABI layer: the launch context of the current device,
+// a CUDA error as a status (its name kept for dsa_last_cuda_error), and the
+// tensor map of a row-major bf16 [rows, cols] tensor, box {64 cols,
+// box_rows}, 128-byte swizzle.
+dsa_status_t make_ctx(void* ws, void* stream, LaunchCtx* ctx);
+dsa_status_t cuda_status(cudaError_t e);
+dsa_status_t encode_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
+                       uint32_t box_rows);
 
 // a1: k_pool[p] = bf16(((k0 + k1) + (k2 + k3)) * 0.25), fp32.
 cudaError_t launch_pool(const LaunchCtx& c, const __nv_bfloat16* k_idx,
@@ -108,5 +124,37 @@ cudaError_t launch_f32_to_bf16(const LaunchCtx& c, const float* a, __nv_bfloat16
 cudaError_t launch_attn_bwd_finalize(const LaunchCtx& c, const AttnShape& s,
                                      const float* dk_acc, const float* dv_acc,
                                      __nv_bfloat16* dk, __nv_bfloat16* dv);
+
+// ------------------------------------------------------------- serving
+struct ServeShape {
+  int64_t n_pages;
+  int64_t T;           // rows of q, slot_map, k_new
+  int page, page_log2;
+  int B, max_blocks;
+  int H, D;
+  float scale;
+};
+
+// Page tables, slots, offsets and lengths of one step.
+cudaError_t launch_page_tables(const LaunchCtx& c, const ServeShape& s,
+                               const int32_t* cached, const int32_t* fresh,
+                               const int32_t* free_pages, int64_t n_free, int32_t* table,
+                               int32_t* slots, int32_t* cu, int32_t* seq, int32_t* taken);
+
+// Rows of k_new (and v_new unless nullptr) to their slots.
+cudaError_t launch_append(const LaunchCtx& c, const ServeShape& s, const int32_t* slots,
+                          const __nv_bfloat16* k_new, const __nv_bfloat16* v_new,
+                          __nv_bfloat16* k_pages, __nv_bfloat16* v_pages);
+
+// Workspace bytes past the header of launch_prefix_attn.
+size_t prefix_attn_ws(const ServeShape& s);
+
+// Shared-prefix attention; work: the workspace past the header.
+cudaError_t launch_prefix_attn(const LaunchCtx& c, const ServeShape& s,
+                               const __nv_bfloat16* q, const __nv_bfloat16* k,
+                               const __nv_bfloat16* v, const int32_t* prefix_table,
+                               int64_t prefix_len, const int32_t* table,
+                               const int32_t* seq, const int32_t* cu, __nv_bfloat16* o,
+                               float* lse, uint8_t* work);
 
 }  // namespace dsa
