@@ -149,10 +149,12 @@ cudaError_t launch_append(const LaunchCtx& c, const ServeShape& s, const int32_t
 // Workspace bytes past the header of launch_prefix_attn.
 size_t prefix_attn_ws(const ServeShape& s);
 
-// Shared-prefix attention; work: the workspace past the header.
+// Shared-prefix attention; work: the workspace past the header.  q_map: q as
+// [T * H, D], box {64, 64}; k_map, v_map: the cache as [n_pages * page, D], box
+// {64, min(page, 64)}.
 cudaError_t launch_prefix_attn(const LaunchCtx& c, const ServeShape& s,
-                               const __nv_bfloat16* q, const __nv_bfloat16* k,
-                               const __nv_bfloat16* v, const int32_t* prefix_table,
+                               const CUtensorMap& q_map, const CUtensorMap& k_map,
+                               const CUtensorMap& v_map, const int32_t* prefix_table,
                                int64_t prefix_len, const int32_t* table,
                                const int32_t* seq, const int32_t* cu, __nv_bfloat16* o,
                                float* lse, uint8_t* work);

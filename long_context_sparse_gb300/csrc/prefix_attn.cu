@@ -1,113 +1,1052 @@
 // prefix_attn.cu -- attention of a batch of requests over one shared prefix
-// and each request's own tokens, both in a paged cache.
+// and each request's own tokens, both in a paged cache, on 5th-generation
+// tensor cores by pairs of SMs.
 //
-// One warp per (token, head) row walks the prefix's keys, then the request's
-// own up to the token's place, with the running maximum m and sum l of the
-// softmax and O in registers (fp32):
-//   m' = max(m, s),  O' = O 2^(m - m') + 2^(s - m') v,  l' likewise.
+// Rows.  K and V are shared by all heads, so the (token, head) rows of every
+// request form one tall operand against the prefix: 128 of them are a row
+// block.  A unit is one row block against one list of keys: the prefix (row
+// blocks over all rows) or a request's own tokens (row blocks over its rows).
+//
+// Products of a tile of 256 keys, by a cluster of two CTAs (cta_group::2, M =
+// 256), with the keys or the value dims on the accumulators' lanes:
+//   S^T[key, row]  = K_tile . Q^T     A: 128 keys of each CTA, B: 64 rows of Q each
+//   O^T[dv, row]  += V_tile^T . P^T   A: 128 dv of each CTA,   B: 64 rows of P each
+// Each CTA so reads half of the keys' K and half of the dims' V, and holds
+// half of Q and of P: with 128 rows a pair each byte brought into shared memory
+// feeds twice the products that one CTA with 64 rows would make of it, and an
+// MMA of 256 x 128 x 16 reads 6 KB of shared memory per SM in its 64 cycles
+// where 128 x 64 would read 6 KB in 32.  TMEM: two S^T buffers (2 x 128
+// columns) and O^T (128 columns per 256 dv): all 512 at d = 512.
+//
+// Softmax.  A thread owns one key (a TMEM lane) and 64 rows; the running
+// maximum m of a row is shared by the pair and only raised when a tile beats
+// it by more than 2^8, so that the usual tile needs one exchange of flags
+// between the CTAs and no reduction:
+//   P = 2^(s - m),  l += P,  O^T += V^T P^T      (O, l, m in fp32, P in bf16:
+//   the tensor core's operand type, one rounding of 2^-9 for each weight).
+// P of rows 0-63 goes to CTA 0, of rows 64-127 to CTA 1 (distributed shared
+// memory), which is the B operand's split.
+//
+// Work.  Units cost their tiles plus kUnitCost; the pairs share the sum
+// evenly in unit order, so a long prefix is split over all of them and short
+// requests are packed together.  Every (unit, pair) that meet leaves O, m and
+// l (fp32, not normalised) in a slot of the workspace, and a second kernel
+// joins each row's slots: sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
 #include "attn_common.cuh"
 #include "dsa_internal.h"
 
 namespace dsa {
 namespace {
 
-template <int D>
-__global__ void __launch_bounds__(256) prefix_attn_kernel(
-    const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k,
-    const __nv_bfloat16* __restrict__ v, const int32_t* __restrict__ prefix_table,
-    int32_t prefix_len, const int32_t* __restrict__ table, const int32_t* __restrict__ seq,
-    const int32_t* __restrict__ cu, __nv_bfloat16* __restrict__ o, float* __restrict__ lse,
-    int64_t T, int B, int H, int max_blocks, int page_log2, int64_t n_pages,
-    float scale_log2, uint32_t* status) {
-  constexpr int P = D / 64;  // bf16 pairs of a lane: 2 * lane + 64 * p
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
-  if (row >= T * H) return;
-  const int64_t t = row / H;
-  int lo = 0, hi = B;  // the request: the last b with cu[b] <= t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(cu + mid) <= t) lo = mid;
-    else hi = mid;
+constexpr int kRows = 128;           // rows of a unit
+constexpr int kKeys = 256;           // keys of a tile
+constexpr int kMaxPairs = 80;        // workspace bound on the pairs of a launch
+constexpr int kUnitCost = 2;         // a unit's Q load and epilogue, in tiles
+constexpr int kSoftWarps = 8;
+constexpr int kProdWarp = 8, kRelayWarp = 9, kMmaWarp = 10;
+constexpr int kThreads = 32 * 12;
+constexpr uint32_t kStageBytes = 16384;
+constexpr float kSlack = 8.0f;       // log2 headroom before a maximum is raised
+
+// ------------------------------------------------------------------- plan
+// The division of work, written by plan_kernel, read by the other two.
+struct Plan {
+  int64_t total;        // cost of all units; 0: nothing to do
+  int64_t chunk;        // cost of a pair's share
+  int64_t prefix_cost;  // of the prefix units, which come first
+  int32_t n_prefix;     // prefix units
+  int32_t prefix_tiles;
+};
+// ccum[b], ucum[b]: cost and unit number of request b's first unit (b = 0..B)
+
+struct PlanView {
+  Plan* p;
+  int64_t* ccum;
+  int32_t* ucum;
+  float2* ml;  // [slots][2][128]: m, and l of each CTA's keys
+  float* o;    // [slots][128][D]
+};
+
+size_t plan_bytes(int B) { return 256 + round_up((size_t)(B + 1) * 12, 256); }
+
+int64_t max_slots(const ServeShape& s) {
+  const int64_t n = (s.T * s.H + kRows - 1) / kRows;
+  return 2 * n + s.B + kMaxPairs;
+}
+
+PlanView plan_view(const ServeShape& s, uint8_t* work) {
+  PlanView v;
+  v.p = reinterpret_cast<Plan*>(work);
+  v.ccum = reinterpret_cast<int64_t*>(work + 256);
+  v.ucum = reinterpret_cast<int32_t*>(work + 256 + (size_t)(s.B + 1) * 8);
+  uint8_t* at = work + plan_bytes(s.B);
+  v.ml = reinterpret_cast<float2*>(at);
+  at += (size_t)max_slots(s) * 2 * kRows * sizeof(float2);
+  v.o = reinterpret_cast<float*>(at);
+  return v;
+}
+
+struct Lens {
+  const int32_t *seq, *cu;
+  int32_t cap;  // tokens that a table row holds
+  int H;
+};
+
+struct ReqShape {
+  int32_t row0;    // first row (token * H)
+  int32_t n_rows;  // rows
+  int32_t len;     // own tokens
+  int32_t tiles;   // of its longest row
+  int32_t n_new;   // query tokens
+};
+
+__device__ __forceinline__ ReqShape req_shape(const Lens& L, int b) {
+  const int32_t c0 = __ldg(L.cu + b), c1 = __ldg(L.cu + b + 1);
+  int32_t len = __ldg(L.seq + b);
+  if (len < 0 || len > L.cap) len = 0;  // latched by the plan
+  return {c0 * L.H, (c1 - c0) * L.H, len, (len + kKeys - 1) / kKeys, c1 - c0};
+}
+
+// Own tokens that row r (from the request's first) of a request sees.
+__device__ __forceinline__ int32_t row_limit(const ReqShape& r, int H, int32_t row) {
+  return max(0, r.len - r.n_new + row / H + 1);
+}
+
+__global__ void __launch_bounds__(1024) plan_kernel(Lens L, int B, int64_t T,
+                                                    int32_t prefix_len, int pairs,
+                                                    Plan* plan, int64_t* ccum,
+                                                    int32_t* ucum, uint32_t* status) {
+  __shared__ int64_t wc[32];
+  __shared__ int32_t wu[32];
+  __shared__ int bad;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) bad = 0;
+  __syncthreads();
+  const int32_t first = __ldg(L.cu), last = __ldg(L.cu + B);
+  if (tid == 0 && (first < 0 || last > T)) bad = 1;
+  for (int b = tid; b < B; b += 1024)
+    if (__ldg(L.cu + b) > __ldg(L.cu + b + 1)) bad = 1;
+  __syncthreads();
+  if (bad) {  // offsets that do not ascend within [0, T]: nothing is computed
+    if (tid == 0) {
+      latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
+      plan->total = 0;
+      plan->chunk = 1;
+    }
+    return;
   }
-  const int32_t c0 = __ldg(cu + lo), c1 = __ldg(cu + lo + 1);
-  if (c0 < 0 || c1 > T) latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
-  if (t < c0 || t >= c1) return;
-  int32_t len = __ldg(seq + lo);
-  if (len < 0 || len > (max_blocks << page_log2)) {
-    latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
-    len = 0;
+  const int32_t ptiles = (prefix_len + kKeys - 1) / kKeys;
+  const int32_t np = ptiles ? (int32_t)(((int64_t)last * L.H + kRows - 1) / kRows) : 0;
+  int64_t c = (int64_t)np * (ptiles + kUnitCost);
+  int32_t u = np;
+  if (tid == 0) {
+    plan->prefix_cost = c;
+    plan->n_prefix = np;
+    plan->prefix_tiles = ptiles;
   }
-  const int32_t own = max(0, len - (c1 - c0) + (int32_t)(t - c0) + 1);
-  float qv[2 * P], acc[2 * P];
+  for (int b0 = 0; b0 < B; b0 += 1024) {
+    const int b = b0 + tid;
+    int64_t mc = 0;
+    int32_t mu = 0;
+    if (b < B) {
+      const int32_t n = __ldg(L.seq + b);
+      if (n < 0 || n > L.cap) latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
+      const ReqShape r = req_shape(L, b);
+      if (r.tiles) mu = (r.n_rows + kRows - 1) / kRows;
+      mc = (int64_t)mu * (r.tiles + kUnitCost);
+    }
+    int64_t ic = mc;
+    int32_t iu = mu;
 #pragma unroll
-  for (int p = 0; p < P; ++p) {
-    const uint32_t x = reinterpret_cast<const uint32_t*>(q + row * D)[lane + 32 * p];
-    qv[2 * p] = bf16_lo(x) * scale_log2;
-    qv[2 * p + 1] = bf16_hi(x) * scale_log2;
-    acc[2 * p] = acc[2 * p + 1] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  for (int part = 0; part < 2; ++part) {
-    const int32_t* pages = part ? table + (int64_t)lo * max_blocks : prefix_table;
-    const int32_t n = part ? own : prefix_len;
-    for (int32_t j = 0; j < n; ++j) {
-      const int32_t pg = __ldg(pages + (j >> page_log2));
-      if (pg < 0 || pg >= n_pages) {
-        latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
-        continue;
+    for (int s = 1; s < 32; s <<= 1) {
+      const int64_t a = __shfl_up_sync(0xffffffffu, ic, s);
+      const int32_t d = __shfl_up_sync(0xffffffffu, iu, s);
+      if (lane >= s) {
+        ic += a;
+        iu += d;
       }
-      const int64_t r = ((int64_t)pg << page_log2) + (j & ((1 << page_log2) - 1));
-      float s = 0.f;
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const uint32_t x = __ldg(reinterpret_cast<const uint32_t*>(k + r * D) + lane + 32 * p);
-        s = fmaf(qv[2 * p], bf16_lo(x), s);
-        s = fmaf(qv[2 * p + 1], bf16_hi(x), s);
+    }
+    __syncthreads();
+    if (lane == 31) {
+      wc[warp] = ic;
+      wu[warp] = iu;
+    }
+    __syncthreads();
+    int64_t tc = 0;
+    int32_t tu = 0;
+    for (int w = 0; w < 32; ++w) {
+      if (w == warp) {
+        ic += tc;
+        iu += tu;
       }
-#pragma unroll
-      for (int sh = 16; sh > 0; sh >>= 1) s += __shfl_xor_sync(0xffffffffu, s, sh);
-      const float mn = fmaxf(m, s);
-      const float a = mn == -INFINITY ? 1.f : exp2f(m - mn);
-      const float e = mn == -INFINITY ? 0.f : exp2f(s - mn);
-      m = mn;
-      l = l * a + e;
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const uint32_t x = __ldg(reinterpret_cast<const uint32_t*>(v + r * D) + lane + 32 * p);
-        acc[2 * p] = fmaf(e, bf16_lo(x), acc[2 * p] * a);
-        acc[2 * p + 1] = fmaf(e, bf16_hi(x), acc[2 * p + 1] * a);
+      tc += wc[w];
+      tu += wu[w];
+    }
+    if (b < B) {
+      ccum[b] = c + ic - mc;
+      ucum[b] = u + iu - mu;
+    }
+    c += tc;
+    u += tu;
+  }
+  if (tid == 0) {
+    ccum[B] = c;
+    ucum[B] = u;
+    plan->total = c;
+    plan->chunk = c > pairs ? (c + pairs - 1) / pairs : 1;
+  }
+}
+
+// Tiles [a, z) of a unit of `tiles` tiles that starts at cost c0, for the
+// pair whose share is [s, e).
+__device__ __forceinline__ void share_of(int64_t c0, int32_t tiles, int64_t s, int64_t e,
+                                         int32_t& a, int32_t& z) {
+  const int64_t lo = s - c0 - kUnitCost;
+  const int64_t hi = min(e - c0, (int64_t)tiles + kUnitCost) - kUnitCost;
+  a = lo > 0 ? (int32_t)lo : 0;
+  z = hi > 0 ? (int32_t)hi : 0;
+}
+
+struct Item {
+  int32_t unit;
+  int32_t tile0, tile1;   // tiles [tile0, tile1) of the unit
+  int32_t row0, n_rows;   // first row of the block, rows of it that count
+  int32_t len;            // keys of the list
+  const int32_t* pages;   // its page list
+  int32_t b;              // request, or -1: the prefix
+  int32_t rel0;           // row0 from the request's first row
+};
+
+// Walks the units of one pair's share, in order.
+struct Walk {
+  const Plan* plan;
+  const int64_t* ccum;
+  const int32_t* ucum;
+  Lens L;
+  const int32_t* prefix_table;
+  const int32_t* table;
+  int32_t prefix_len, max_blocks, rows_all;
+  int64_t pos, start, end;
+  int b;  // request at or before pos, once pos is past the prefix units
+
+  __device__ __forceinline__ bool next(Item& it) {
+    while (pos < end) {
+      int64_t c0;
+      int32_t tiles;
+      if (pos < plan->prefix_cost) {
+        tiles = plan->prefix_tiles;
+        const int32_t u = (int32_t)(pos / (tiles + kUnitCost));
+        c0 = (int64_t)u * (tiles + kUnitCost);
+        it.unit = u;
+        it.row0 = it.rel0 = u * kRows;
+        it.n_rows = min(kRows, rows_all - it.row0);
+        it.len = prefix_len;
+        it.pages = prefix_table;
+        it.b = -1;
+        share_of(c0, tiles, start, end, it.tile0, it.tile1);
+      } else {
+        while (__ldg(ccum + b + 1) <= pos) ++b;
+        const ReqShape r = req_shape(L, b);
+        const int64_t cb = __ldg(ccum + b);
+        tiles = r.tiles;
+        const int32_t j = (int32_t)((pos - cb) / (tiles + kUnitCost));
+        c0 = cb + (int64_t)j * (tiles + kUnitCost);
+        it.unit = __ldg(ucum + b) + j;
+        it.rel0 = j * kRows;
+        it.row0 = r.row0 + it.rel0;
+        it.n_rows = min(kRows, r.n_rows - it.rel0);
+        // keys beyond the block's last row are seen by no row of it
+        it.len = min(r.len, row_limit(r, L.H, it.rel0 + it.n_rows - 1));
+        it.pages = table + (int64_t)b * max_blocks;
+        it.b = b;
+        share_of(c0, tiles, start, end, it.tile0, it.tile1);
+        it.tile1 = min(it.tile1, (it.len + kKeys - 1) / kKeys);
+      }
+      pos = min(end, c0 + tiles + kUnitCost);
+      if (it.tile0 < it.tile1) return true;
+    }
+    return false;
+  }
+};
+
+// ---------------------------------------------------- pair (cluster) PTX
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t at_rank(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+               ::: "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+__device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity, uint32_t hint) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(hint)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, const uint32_t (&v)[4]) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+__device__ __forceinline__ void fence_proxy_async_all() {
+  asm volatile("fence.proxy.async;" ::: "memory");
+}
+__device__ __forceinline__ void tc_mma2(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive on the barrier at this offset in both CTAs when the MMAs so far are done.
+__device__ __forceinline__ void tc_commit2(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Bounded waits of the pair: as Waiter, with cluster scope; a failure stops
+// both CTAs.  wait() is for whole warps and gives every lane the same answer,
+// so that no lane is left behind at a warp's barrier; wait1() is one thread's.
+struct PairWaiter {
+  volatile uint32_t* abort_flag;
+  uint32_t peer_flag;  // cluster address of the other CTA's flag
+  uint32_t* status;
+  uint64_t timeout_ns;
+  __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const {
+    return __all_sync(0xffffffffu, wait1(bar, parity));
+  }
+  __device__ __forceinline__ bool wait1(uint32_t bar, uint32_t parity) const {
+    if (mbar_try_cluster(bar, parity, 0u)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+      if (mbar_try_cluster(bar, parity, 20000u)) return true;
+      if (*abort_flag) return false;
+      if (globaltimer_ns() - t0 > timeout_ns) {
+        latch_error(status, DSA_ERR_DEVICE_TIMEOUT);
+        *abort_flag = 1u;
+        st_cluster_u32(peer_flag, 1u);
+        return false;
       }
     }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+};
+
+// ------------------------------------------------------------ main kernel
+template <int D>
+struct PCfg {
+  static constexpr int kAtoms = D / 64;               // K stages of a tile
+  static constexpr int kBlocks = D > 256 ? D / 256 : 1;  // 256-dv blocks of O^T
+  static constexpr uint32_t kQBytes = 64 * D * 2;     // this CTA's 64 rows
+  static constexpr uint32_t kPBytes = kKeys * 128;    // 256 keys x 64 rows
+  static constexpr int kStages = 7;
+  static constexpr uint32_t kTail = 16 * 1024;
+  static constexpr uint32_t kSmem = 1024 + kQBytes + kPBytes + kStages * kStageBytes + kTail;
+  static_assert(kSmem <= 232448, "shared memory");
+};
+
+// One butterfly step of column_reduce: lanes keep half of the H2 * 2 columns.
+template <int H2, bool MAX>
+__device__ __forceinline__ void column_step(float (&x)[64], int lane) {
+  const bool up = (lane & H2 / 2) != 0;
 #pragma unroll
-  for (int p = 0; p < P; ++p)
-    reinterpret_cast<uint32_t*>(o + row * D)[lane + 32 * p] =
-        pack_bf16(acc[2 * p] * inv, acc[2 * p + 1] * inv);
-  if (lane == 0) lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  for (int i = 0; i < H2; ++i) {
+    const float keep = up ? x[i + H2] : x[i], give = up ? x[i] : x[i + H2];
+    const float got = __shfl_xor_sync(0xffffffffu, give, H2 / 2);
+    x[i] = MAX ? fmaxf(keep, got) : keep + got;
+  }
+}
+// Reduce 64 columns over the warp's 32 lanes: lane i ends with columns 2i and
+// 2i+1 in x[0], x[1] (62 shuffles; each step halves the columns that a lane keeps).
+template <bool MAX>
+__device__ __forceinline__ void column_reduce(float (&x)[64], int lane) {
+  column_step<32, MAX>(x, lane);
+  column_step<16, MAX>(x, lane);
+  column_step<8, MAX>(x, lane);
+  column_step<4, MAX>(x, lane);
+  column_step<2, MAX>(x, lane);
+}
+
+template <int D>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    prefix_attn_kernel(const __grid_constant__ CUtensorMap q_map,
+                       const __grid_constant__ CUtensorMap k_map,
+                       const __grid_constant__ CUtensorMap v_map, PlanView view, Lens L,
+                       const int32_t* __restrict__ prefix_table, int32_t prefix_len,
+                       const int32_t* __restrict__ table, int B, int max_blocks,
+                       int page_log2, int32_t n_pages, int64_t n_slots, float scale_log2,
+                       uint32_t* status, uint64_t timeout_ns) {
+  using C = PCfg<D>;
+  constexpr int kStages = C::kStages;
+  constexpr uint32_t IDESC_S = idesc_bf16(256, 128, 0, 0);
+  constexpr uint32_t IDESC_O = idesc_bf16(256, 128, 1, 1);
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gb = smem_raw + (base - raw);
+  const uint32_t sQ = base;
+  const uint32_t sP = sQ + C::kQBytes;
+  const uint32_t sStage = sP + C::kPBytes;
+  uint8_t* tail = gb + C::kQBytes + C::kPBytes + kStages * kStageBytes;
+  float* red = carve<float>(tail, 8 * kRows);     // [rank * 4 + quadrant][row] maxima
+  float* lred = carve<float>(tail, 4 * kRows);    // [quadrant][row] sums
+  float* thr_s = carve<float>(tail, kRows);       // raise a row's maximum above this
+  float* nm_s = carve<float>(tail, kRows);        // -m (0 while m = -inf)
+  float* alpha_s = carve<float>(tail, kRows);
+  int32_t* lim_s = carve<int32_t>(tail, kRows);   // keys that a row sees
+  uint64_t* bars = carve<uint64_t>(tail, 3 * kStages + 20);
+  uint32_t* misc = carve<uint32_t>(tail, 8);      // abort, tmem, flags[2], start request
+  const uint32_t bar0 = smem_u32(bars);
+  auto full_loc = [&](int s) { return bar0 + 8u * s; };               // own TMA landed
+  auto full = [&](int s) { return bar0 + 8u * (kStages + s); };       // leader: both landed
+  auto empty = [&](int s) { return bar0 + 8u * (2 * kStages + s); };  // stage read
+  const uint32_t bx = bar0 + 8u * (3 * kStages);
+  const uint32_t q_loc = bx, q_full = bx + 8, q_empty = bx + 16;
+  auto s_full = [&](uint32_t b) { return bx + 24 + 8 * b; };
+  auto s_free = [&](uint32_t b) { return bx + 40 + 8 * b; };          // leader
+  const uint32_t p_full = bx + 56;                                    // leader
+  const uint32_t p_done = bx + 64;
+  const uint32_t o_empty = bx + 72;                                   // leader
+  const uint32_t xs = bx + 80;     // the softmax warps of both CTAs
+  const uint32_t grp = bx + 88;    // the softmax warps of this CTA
+  const uint32_t done_bar = bx + 96;
+  volatile uint32_t* flags = misc + 2;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank(), peer = rank ^ 1u;
+  const PairWaiter W{misc, at_rank(smem_u32(misc), peer), status, timeout_ns};
+
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full_loc(s), 1);
+      mbar_init(full(s), 2);
+      mbar_init(empty(s), 1);
+    }
+    mbar_init(q_loc, 1);
+    mbar_init(q_full, 2);
+    mbar_init(q_empty, 1);
+    for (uint32_t b = 0; b < 2; ++b) {
+      mbar_init(s_full(b), 1);
+      mbar_init(s_free(b), 2 * kSoftWarps);
+    }
+    mbar_init(p_full, 2 * kSoftWarps);
+    mbar_init(p_done, 1);
+    mbar_init(o_empty, 2 * kSoftWarps);
+    mbar_init(xs, 2 * kSoftWarps);
+    mbar_init(grp, kSoftWarps);
+    mbar_init(done_bar, 1);
+    misc[0] = 0u;
+    misc[2] = misc[3] = 0u;
+    misc[4] = 0u;
+    fence_mbar_init();
+    prefetch_tensormap(&q_map);
+    prefetch_tensormap(&k_map);
+    prefetch_tensormap(&v_map);
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(misc + 1)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  // the share of this pair and the request that it starts in
+  const Plan* plan = view.p;
+  Walk walk;
+  walk.plan = plan;
+  walk.ccum = view.ccum;
+  walk.ucum = view.ucum;
+  walk.L = L;
+  walk.prefix_table = prefix_table;
+  walk.table = table;
+  walk.prefix_len = prefix_len;
+  walk.max_blocks = max_blocks;
+  walk.rows_all = __ldg(L.cu + B) * L.H;
+  const int64_t pair = blockIdx.x >> 1;
+  walk.start = walk.pos = min(plan->total, pair * plan->chunk);
+  walk.end = min(plan->total, walk.start + plan->chunk);
+  __syncthreads();
+  if (walk.start < walk.end && walk.start >= plan->prefix_cost)
+    for (int b = tid; b < B; b += kThreads)
+      if (__ldg(view.ccum + b) <= walk.start && walk.start < __ldg(view.ccum + b + 1))
+        misc[4] = (uint32_t)b;
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  walk.b = (int)misc[4];
+  const uint32_t tmem = misc[1];
+  const uint32_t tO = tmem + 2 * kRows;
+  Item it;
+
+  if (warp == kProdWarp) {
+    // ====================================================== TMA producer
+    const int page = 1 << page_log2, box = min(page, 64);
+    const int32_t n_rows_cache = n_pages << page_log2;  // out of range: zero rows
+    const int kb = 128 / box, vb = 64 / box;            // boxes of a K stage, a V atom
+    uint32_t u = 0, nq = 0;
+    bool ok = true;
+    while (ok && walk.next(it)) {
+      if (!(ok = W.wait(q_empty, (nq & 1u) ^ 1u))) break;
+      if (lane == 0) mbar_expect_tx(q_loc, C::kQBytes);
+      __syncwarp();
+      if (lane < C::kAtoms)
+        tma_load_2d(sQ + lane * 8192, &q_map, lane * 64, it.row0 + (int32_t)rank * 64, q_loc);
+      ++nq;
+      // first cache row of the page that holds key x of tile j, in lane x / page
+      auto page_rows = [&](int32_t j) {
+        const int32_t pos = j * kKeys + (lane << page_log2);
+        if ((lane << page_log2) >= kKeys || j >= it.tile1 || pos >= it.len) return n_rows_cache;
+        const int32_t p = __ldg(it.pages + (pos >> page_log2));
+        if (p < 0 || p >= n_pages) {
+          latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
+          return n_rows_cache;
+        }
+        return p << page_log2;
+      };
+      auto key_row = [&](int32_t j, int32_t rows, int key) {
+        const int32_t r = __shfl_sync(0xffffffffu, rows, key >> page_log2);
+        return r == n_rows_cache || j * kKeys + key >= it.len ? n_rows_cache
+                                                              : r + (key & (page - 1));
+      };
+      int32_t rows_v = n_rows_cache, rows_k = page_rows(it.tile0);
+      for (int32_t j = it.tile0; j <= it.tile1 && ok; ++j) {
+        const int32_t rows_n = page_rows(j + 1);
+        if (j < it.tile1) {  // K of tile j: this CTA's 128 keys, 64 dims a stage
+          const int key = (int)rank * 128 + (lane < kb ? lane : 0) * box;
+          const int32_t row = key_row(j, rows_k, key);
+          for (int a = 0; a < C::kAtoms; ++a, ++u) {
+            const int s = (int)(u % kStages);
+            if (!(ok = W.wait(empty(s), ((u / kStages) & 1u) ^ 1u))) break;
+            if (lane == 0) mbar_expect_tx(full_loc(s), kStageBytes);
+            __syncwarp();
+            if (lane < kb)
+              tma_load_2d(sStage + s * kStageBytes + lane * box * 128, &k_map, a * 64, row,
+                          full_loc(s));
+          }
+        }
+        if (j > it.tile0 && ok) {  // V of tile j-1: 64 keys, this CTA's 128 dv a stage
+          const int i = lane < 2 * vb ? lane : 0;
+          const int a = i / vb, kk = (i % vb) * box;
+          for (int m = 0; m < C::kBlocks && ok; ++m)
+            for (int g = 0; g < 4; ++g, ++u) {
+              const int s = (int)(u % kStages);
+              const int32_t row = key_row(j - 1, rows_v, g * 64 + kk);
+              if (!(ok = W.wait(empty(s), ((u / kStages) & 1u) ^ 1u))) break;
+              if (lane == 0) mbar_expect_tx(full_loc(s), kStageBytes);
+              __syncwarp();
+              if (lane < 2 * vb)
+                tma_load_2d(sStage + s * kStageBytes + a * 8192 + kk * 128, &v_map,
+                            m * 256 + (int)rank * 128 + a * 64, row, full_loc(s));
+            }
+        }
+        rows_v = rows_k;
+        rows_k = rows_n;
+      }
+    }
+    if (!ok) {  // copies in flight land before the CTA goes
+      if (lane == 0) {
+        for (uint32_t x = u > kStages ? u - kStages : 0; x < u; ++x)
+          drain(full_loc((int)(x % kStages)), (x / kStages) & 1u, timeout_ns);
+        if (nq) drain(q_loc, (nq - 1) & 1u, timeout_ns);
+      }
+    }
+  } else if (warp == kRelayWarp) {
+    // ==================== relay: landed copies -> the leader's barriers
+    // Rows of V past the list's end may hold NaN, which a zero weight does not
+    // cancel: they are cleared here, between the copy and the product.
+    uint32_t u = 0, nq = 0;
+    bool ok = true;
+    const uint32_t lead_q = at_rank(q_full, 0);
+    auto pass = [&](int s) {
+      if (lane == 0) mbar_arrive_cluster(at_rank(full(s), 0));
+    };
+    while (ok && walk.next(it)) {
+      if (!(ok = W.wait(q_loc, nq & 1u))) break;
+      if (lane == 0) mbar_arrive_cluster(lead_q);
+      ++nq;
+      for (int32_t j = it.tile0; j <= it.tile1 && ok; ++j) {
+        if (j < it.tile1)
+          for (int a = 0; a < C::kAtoms; ++a, ++u) {
+            const int s = (int)(u % kStages);
+            if (!(ok = W.wait(full_loc(s), (u / kStages) & 1u))) break;
+            pass(s);
+          }
+        if (j > it.tile0 && ok)
+          for (int m = 0; m < C::kBlocks && ok; ++m)
+            for (int g = 0; g < 4; ++g, ++u) {
+              const int s = (int)(u % kStages);
+              if (!(ok = W.wait(full_loc(s), (u / kStages) & 1u))) break;
+              const int32_t left = it.len - ((j - 1) * kKeys + g * 64);  // rows that count
+              if (left < 64) {
+                const int from = left > 0 ? left : 0;
+                for (int x = from * 8 + lane; x < 64 * 8; x += 32)
+#pragma unroll
+                  for (int a = 0; a < 2; ++a)
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
+                                     sStage + s * kStageBytes + a * 8192 + x * 16),
+                                 "r"(0u)
+                                 : "memory");
+                fence_proxy_async_all();
+                __syncwarp();
+              }
+              pass(s);
+            }
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ============================================ MMA issuer (leader only)
+    if (rank == 0 && lane == 0) {
+      uint32_t u = 0, nt = 0, nq = 0;
+      bool issued = false, ok = true;
+      while (ok && walk.next(it)) {
+        if (!(ok = W.wait1(q_full, nq & 1u))) break;
+        const int n = it.tile1 - it.tile0;
+        for (int j = 0; j <= n && ok; ++j) {
+          if (j < n) {
+            const uint32_t t = nt + (uint32_t)j, b = t & 1u;
+            if (!(ok = W.wait1(s_free(b), ((t >> 1) & 1u) ^ 1u))) break;
+            for (int a = 0; a < C::kAtoms; ++a, ++u) {
+              const int s = (int)(u % kStages);
+              if (!(ok = W.wait1(full(s), (u / kStages) & 1u))) break;
+              tc_fence_after();
+              const uint32_t st = sStage + s * kStageBytes;
+#pragma unroll
+              for (int kin = 0; kin < 4; ++kin)
+                tc_mma2(tmem + b * kRows, sdesc_sw128(st + kin * 32, 16, 1024),
+                        sdesc_sw128(sQ + a * 8192 + kin * 32, 16, 1024), IDESC_S,
+                        (a | kin) != 0 ? 1u : 0u);
+              issued = true;
+              tc_commit2(empty(s));
+            }
+            if (!ok) break;
+            if (j == n - 1) tc_commit2(q_empty);
+            tc_commit2(s_full(b));
+          }
+          if (j >= 1) {
+            const uint32_t t = nt + (uint32_t)j - 1u;
+            if (!(ok = W.wait1(p_full, t & 1u))) break;
+            if (j == 1 && !(ok = W.wait1(o_empty, (nq & 1u) ^ 1u))) break;
+            for (int m = 0; m < C::kBlocks && ok; ++m)
+              for (int g = 0; g < 4; ++g, ++u) {
+                const int s = (int)(u % kStages);
+                if (!(ok = W.wait1(full(s), (u / kStages) & 1u))) break;
+                tc_fence_after();
+                const uint32_t st = sStage + s * kStageBytes;
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                  tc_mma2(tO + m * kRows, sdesc_sw128(st + ks * 2048, 8192, 1024),
+                          sdesc_sw128(sP + (g * 4 + ks) * 2048, 16, 1024), IDESC_O,
+                          ((j - 1) | g | ks) != 0 ? 1u : 0u);
+                tc_commit2(empty(s));
+              }
+            if (!ok) break;
+            tc_commit2(p_done);
+          }
+        }
+        nt += (uint32_t)n;
+        ++nq;
+      }
+      if (issued) {
+        tc_commit2(done_bar);
+        drain(done_bar, 0, timeout_ns);
+      }
+    }
+    __syncwarp();
+  } else if (warp < kSoftWarps) {
+    // ================================================ softmax, epilogue
+    const int quad = warp & 3, g = warp >> 2;      // TMEM lanes, rows 64 g .. 64 g + 63
+    const int key = (int)rank * 128 + quad * 32 + lane;
+    const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+    const uint32_t xs_own = at_rank(xs, rank), xs_peer = at_rank(xs, peer);
+    const uint32_t flag_own = at_rank(smem_u32(misc + 2), rank);
+    const uint32_t flag_peer = at_rank(smem_u32(misc + 2), peer);
+    const uint32_t red_own = at_rank(smem_u32(red), rank), red_peer = at_rank(smem_u32(red), peer);
+    const uint32_t l_s_free0 = at_rank(s_free(0), 0), l_p_full = at_rank(p_full, 0);
+    const uint32_t l_o_empty = at_rank(o_empty, 0);
+    const uint32_t p_row = at_rank(sP, (uint32_t)g) + (uint32_t)key * 128u;
+    const uint32_t p_sw = (uint32_t)(key & 7);
+    uint32_t nx = 0, ng = 0, nt = 0;
+    // all softmax warps of the pair / of this CTA
+    auto pair_sync = [&]() {
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive_cluster(xs_own);
+        mbar_arrive_cluster(xs_peer);
+      }
+      return W.wait(xs, nx++ & 1u);
+    };
+    auto group_sync = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(grp);
+      return W.wait(grp, ng++ & 1u);
+    };
+    bool ok = true;
+    while (ok && walk.next(it)) {
+      const bool live = it.n_rows > 64 * g;  // this group has rows that count
+      int32_t lim_min = it.len;              // keys that every row of the block sees
+      if (it.b >= 0) {
+        const ReqShape r = req_shape(L, it.b);
+        lim_min = row_limit(r, L.H, it.rel0);
+        if (tid < kRows)
+          lim_s[tid] = min(it.len, row_limit(r, L.H, it.rel0 + min(tid, it.n_rows - 1)));
+      } else if (tid < kRows) {
+        lim_s[tid] = it.len;
+      }
+      if (tid < kRows) {
+        thr_s[tid] = -INFINITY;
+        nm_s[tid] = 0.f;
+      }
+      float l[64];
+#pragma unroll
+      for (int h = 0; h < 64; ++h) l[h] = 0.f;
+      const int n = it.tile1 - it.tile0;
+      for (int j = 0; j < n; ++j, ++nt) {
+        const uint32_t b = nt & 1u;
+        const uint32_t tS = tmem + b * kRows + lane_base + 64 * g;
+        if (!(ok = W.wait(s_full(b), (nt >> 1) & 1u))) break;
+        tc_fence_after();
+        const int32_t pos = (it.tile0 + j) * kKeys + key;
+        const bool masked = (it.tile0 + j + 1) * kKeys > lim_min;  // uniform
+        // ---- does a score beat its row's maximum by more than 2^8?  (Always
+        // taken on a unit's first tile, whose maxima are not set yet.)
+        bool need = j == 0;
+        if (j > 0 && live) {
+#pragma unroll
+          for (int h0 = 0; h0 < 64; h0 += 16) {
+            uint32_t r[16];
+            tmem_ld16(tS + h0, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int h = 64 * g + h0 + e;
+              const bool over = __uint_as_float(r[e]) * scale_log2 > thr_s[h];
+              need |= over && (!masked || pos < lim_s[h]);
+            }
+          }
+        }
+        // the flag carries the tile's number, so it never needs clearing
+        if (__any_sync(0xffffffffu, need) && lane == 0) {
+          st_cluster_u32(flag_own + 4 * b, nt + 1u);
+          st_cluster_u32(flag_peer + 4 * b, nt + 1u);
+        }
+        if (!(ok = pair_sync())) break;
+        // the previous tile's PV is done: O^T is current and P free
+        if (nt > 0 && !(ok = W.wait(p_done, (nt - 1u) & 1u))) break;
+        tc_fence_after();
+        if (flags[b] == nt + 1u) {
+          // ---- exact maxima of the tile, over both CTAs' keys
+          float x[64];
+#pragma unroll
+          for (int h0 = 0; h0 < 64; h0 += 16) {
+            uint32_t r[16];
+            tmem_ld16(tS + h0, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              x[h0 + e] = !masked || pos < lim_s[64 * g + h0 + e]
+                              ? __uint_as_float(r[e]) * scale_log2
+                              : -INFINITY;
+          }
+          column_reduce<true>(x, lane);
+          const uint32_t at = 4u * (uint32_t)(((int)rank * 4 + quad) * kRows + 64 * g + 2 * lane);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            st_cluster_u32(red_own + at + 4 * e, __float_as_uint(x[e]));
+            st_cluster_u32(red_peer + at + 4 * e, __float_as_uint(x[e]));
+          }
+          if (!(ok = pair_sync())) break;
+          if (tid < kRows) {
+            float t = red[tid];
+#pragma unroll
+            for (int w = 1; w < 8; ++w) t = fmaxf(t, red[w * kRows + tid]);
+            const float th = thr_s[tid];
+            const bool raise = t > th;
+            alpha_s[tid] = raise && th != -INFINITY ? ex2(-nm_s[tid] - t) : 1.f;
+            if (raise) {
+              thr_s[tid] = t + kSlack;
+              nm_s[tid] = -t;
+            }
+          }
+          if (!(ok = group_sync())) break;
+          if (j > 0) {
+            bool rescale = false;
+#pragma unroll
+            for (int h = 0; h < 64; ++h) {
+              const float a = alpha_s[64 * g + h];
+              l[h] *= a;
+              rescale |= a != 1.f;
+            }
+            if (rescale) {  // the same in every lane
+#pragma unroll 1
+              for (int m = 0; m < C::kBlocks; ++m)
+#pragma unroll 1
+                for (int h0 = 0; h0 < 64; h0 += 16) {
+                  uint32_t r[16];
+                  const uint32_t ta = tO + m * kRows + lane_base + 64 * g + h0;
+                  tmem_ld16(ta, r);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int e = 0; e < 16; ++e)
+                    r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha_s[64 * g + h0 + e]);
+                  tmem_st16(ta, r);
+                }
+              tmem_wait_st();
+            }
+          }
+        }
+        // ---- P = 2^(s - m): row sums, and bf16 P into the CTA that owns the rows
+        if (live) {
+#pragma unroll
+          for (int h0 = 0; h0 < 64; h0 += 16) {
+            uint32_t r[16];
+            tmem_ld16(tS + h0, r);
+            tmem_wait_ld();
+            float p[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int h = 64 * g + h0 + e;
+              p[e] = ex2(fmaf(__uint_as_float(r[e]), scale_log2, nm_s[h]));
+              if (masked && pos >= lim_s[h]) p[e] = 0.f;
+              l[h0 + e] += p[e];
+            }
+#pragma unroll
+            for (int c8 = 0; c8 < 2; ++c8) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack_bf16(p[8 * c8 + 2 * e], p[8 * c8 + 2 * e + 1]);
+              st_cluster_v4(p_row + (((uint32_t)(h0 / 8 + c8) ^ p_sw) << 4), w);
+            }
+          }
+        }
+        fence_proxy_async_all();  // P -> the tensor core's reads
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_cluster(l_s_free0 + 8 * b);
+          mbar_arrive_cluster(l_p_full);
+        }
+      }
+      if (!ok) break;
+      // ---- epilogue: m, l and O of this (unit, pair) to its slot
+      const int64_t slot = (int64_t)it.unit + pair;
+      if (!(ok = W.wait(p_done, (nt - 1u) & 1u))) break;
+      tc_fence_after();
+      column_reduce<false>(l, lane);
+      lred[quad * kRows + 64 * g + 2 * lane] = l[0];
+      lred[quad * kRows + 64 * g + 2 * lane + 1] = l[1];
+      if (!(ok = group_sync())) break;
+      if (DSA_IN_BOUNDS(slot < n_slots, status)) {
+        if (tid < it.n_rows) {
+          const float sum = lred[tid] + lred[kRows + tid] + lred[2 * kRows + tid] +
+                            lred[3 * kRows + tid];
+          const float th = thr_s[tid];
+          view.ml[(slot * 2 + rank) * kRows + tid] =
+              make_float2(th == -INFINITY ? -INFINITY : -nm_s[tid], sum);
+        }
+        float* out = view.o + slot * (int64_t)(kRows * D);
+#pragma unroll 1
+        for (int m = 0; m < C::kBlocks; ++m) {
+          const int dv = m * 256 + (int)rank * 128 + quad * 32 + lane;
+          if (dv >= D) break;  // D = 128: the second CTA's lanes are padding
+#pragma unroll 1
+          for (int h0 = 64 * g; h0 < min(64 * g + 64, it.n_rows); h0 += 16) {
+            uint32_t r[16];
+            tmem_ld16(tO + m * kRows + lane_base + h0, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (h0 + e < it.n_rows) out[(int64_t)(h0 + e) * D + dv] = __uint_as_float(r[e]);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(l_o_empty);
+    }
+  }
+
+  // ---- teardown: every role has left its loop
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  if (warp == kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
+                 : "memory");
+}
+
+// ---------------------------------------------------------------- joining
+// Row by row, D / 4 threads each: the slots of the row's prefix unit and of
+// its own unit, weighted by 2^(m_i - M).  Reads each partial result once;
+// kJoin of them in flight.
+constexpr int kJoin = 8;
+
+template <int D>
+__global__ void __launch_bounds__(128) join_kernel(PlanView view, Lens L,
+                                                   __nv_bfloat16* __restrict__ o,
+                                                   float* __restrict__ lse, int B,
+                                                   int64_t n_rows, int64_t n_slots,
+                                                   uint32_t* status) {
+  constexpr int kPer = 512 / D, kLanes = D / 4;  // rows of a block, threads of a row
+  const int sub = threadIdx.x / kLanes, th = threadIdx.x % kLanes;
+  const int64_t row = blockIdx.x * (int64_t)kPer + sub;
+  if (row >= n_rows) return;
+  const Plan* plan = view.p;
+  const int64_t t = row / L.H, chunk = plan->chunk, total = plan->total;
+  if (t < __ldg(L.cu) || t >= __ldg(L.cu + B)) return;
+  int lo = 0, hi = B;  // the last b with cu[b] <= t
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(L.cu + mid) <= t) lo = mid;
+    else hi = mid;
+  }
+  const ReqShape r = req_shape(L, lo);
+  // the two units: first cost, tiles, tiles that hold keys, number, row in it
+  int64_t c0[2];
+  int32_t tiles[2], used[2], unit[2], at[2];
+  int n_units = 0;
+  if (plan->prefix_cost > 0 && total > 0) {
+    tiles[0] = used[0] = plan->prefix_tiles;
+    unit[0] = (int32_t)(row / kRows);
+    at[0] = (int32_t)(row % kRows);
+    c0[0] = (int64_t)unit[0] * (tiles[0] + kUnitCost);
+    n_units = 1;
+  }
+  if (r.tiles && total > 0) {
+    const int32_t rel = (int32_t)row - r.row0, j = rel / kRows;
+    const int32_t last = min((j + 1) * kRows, r.n_rows) - 1;
+    tiles[n_units] = r.tiles;
+    used[n_units] = (min(r.len, row_limit(r, L.H, last)) + kKeys - 1) / kKeys;
+    unit[n_units] = __ldg(view.ucum + lo) + j;
+    at[n_units] = rel % kRows;
+    c0[n_units] = __ldg(view.ccum + lo) + (int64_t)j * (r.tiles + kUnitCost);
+    ++n_units;
+  }
+  float m = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int x = 0; x < n_units; ++x) {
+    const int64_t i0 = c0[x] / chunk, i1 = (c0[x] + tiles[x] + kUnitCost - 1) / chunk;
+    for (int64_t i = i0; i <= i1; i += kJoin) {
+      float mi[kJoin], li[kJoin];
+      float4 oi[kJoin];
+      float top = m;
+#pragma unroll
+      for (int e = 0; e < kJoin; ++e) {
+        mi[e] = -INFINITY;
+        li[e] = 0.f;
+        oi[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i + e > i1) continue;
+        int32_t a, z;
+        share_of(c0[x], tiles[x], (i + e) * chunk, min(total, (i + e + 1) * chunk), a, z);
+        if (a >= min(z, used[x])) continue;
+        const int64_t slot = unit[x] + i + e;
+        if (!DSA_IN_BOUNDS(slot < n_slots, status)) continue;
+        const float2 p0 = view.ml[(slot * 2) * kRows + at[x]];
+        const float2 p1 = view.ml[(slot * 2 + 1) * kRows + at[x]];
+        mi[e] = p0.x;
+        li[e] = p0.y + p1.y;
+        oi[e] = reinterpret_cast<const float4*>(view.o + (slot * kRows + at[x]) * D)[th];
+      }
+#pragma unroll
+      for (int e = 0; e < kJoin; ++e) top = fmaxf(top, mi[e]);
+      const float keep = top == -INFINITY ? 1.f : ex2(m - top);
+      l *= keep;
+      acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
+      m = top;
+#pragma unroll
+      for (int e = 0; e < kJoin; ++e) {
+        if (mi[e] == -INFINITY) continue;  // nothing there, or no key seen
+        const float w = ex2(mi[e] - top);
+        l = fmaf(w, li[e], l);
+        acc.x = fmaf(w, oi[e].x, acc.x);
+        acc.y = fmaf(w, oi[e].y, acc.y);
+        acc.z = fmaf(w, oi[e].z, acc.z);
+        acc.w = fmaf(w, oi[e].w, acc.w);
+      }
+    }
+  }
+  const bool none = m == -INFINITY;
+  const float inv = none ? 0.f : 1.f / l;
+  reinterpret_cast<uint2*>(o + row * D)[th] =
+      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (th == 0) lse[row] = none ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+template <int D>
+cudaError_t launch_t(const LaunchCtx& c, const ServeShape& s, const CUtensorMap& qm,
+                     const CUtensorMap& km, const CUtensorMap& vm,
+                     const int32_t* prefix_table, int32_t prefix_len, const int32_t* table,
+                     const Lens& L, __nv_bfloat16* o, float* lse, uint8_t* work) {
+  using C = PCfg<D>;
+  const PlanView view = plan_view(s, work);
+  cudaError_t e = cudaFuncSetAttribute(prefix_attn_kernel<D>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)C::kSmem);
+  if (e != cudaSuccess) return e;
+  const int pairs = c.num_sms / 2 < kMaxPairs ? c.num_sms / 2 : kMaxPairs;
+  plan_kernel<<<1, 1024, 0, c.stream>>>(L, s.B, s.T, prefix_len, pairs, view.p, view.ccum,
+                                        view.ucum, c.status);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const int64_t slots = max_slots(s);
+  prefix_attn_kernel<D><<<2 * pairs, kThreads, C::kSmem, c.stream>>>(
+      qm, km, vm, view, L, prefix_table, prefix_len, table, s.B, s.max_blocks, s.page_log2,
+      (int32_t)s.n_pages, slots, s.scale * kLog2e, c.status, c.timeout_ns);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const int64_t rows = s.T * s.H;
+  constexpr int per = 512 / D;
+  join_kernel<D><<<(unsigned)((rows + per - 1) / per), 128, 0, c.stream>>>(
+      view, L, o, lse, s.B, rows, slots, c.status);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t prefix_attn_ws(const ServeShape&) { return 0; }
+size_t prefix_attn_ws(const ServeShape& s) {
+  return plan_bytes(s.B) + (size_t)max_slots(s) * kRows * (2 * sizeof(float2) + (size_t)s.D * 4);
+}
 
 cudaError_t launch_prefix_attn(const LaunchCtx& c, const ServeShape& s,
-                               const __nv_bfloat16* q, const __nv_bfloat16* k,
-                               const __nv_bfloat16* v, const int32_t* prefix_table,
+                               const CUtensorMap& q_map, const CUtensorMap& k_map,
+                               const CUtensorMap& v_map, const int32_t* prefix_table,
                                int64_t prefix_len, const int32_t* table,
                                const int32_t* seq, const int32_t* cu, __nv_bfloat16* o,
-                               float* lse, uint8_t*) {
-  const int64_t rows = s.T * s.H;
-  auto run = [&](auto kern) {
-    kern<<<(unsigned)((rows + 7) / 8), 256, 0, c.stream>>>(
-        q, k, v, prefix_table, (int32_t)prefix_len, table, seq, cu, o, lse, s.T, s.B, s.H,
-        s.max_blocks, s.page_log2, s.n_pages, s.scale * kLog2e, c.status);
+                               float* lse, uint8_t* work) {
+  const Lens L{seq, cu, s.max_blocks << s.page_log2, s.H};
+  auto run = [&](auto launch) {
+    return launch(c, s, q_map, k_map, v_map, prefix_table, (int32_t)prefix_len, table, L, o,
+                  lse, work);
   };
-  if (s.D == 128) run(prefix_attn_kernel<128>);
-  else if (s.D == 256) run(prefix_attn_kernel<256>);
-  else run(prefix_attn_kernel<512>);
-  return cudaGetLastError();
+  if (s.D == 128) return run(launch_t<128>);
+  if (s.D == 256) return run(launch_t<256>);
+  return run(launch_t<512>);
 }
 
 }  // namespace dsa

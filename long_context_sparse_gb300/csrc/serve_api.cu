@@ -141,12 +141,18 @@ dsa_status_t dsa_prefix_attn(const dsa_serve_config_t* cfg, const void* q,
     if (!aligned16(p)) return DSA_ERR_MISALIGNED;
   LaunchCtx ctx;
   if ((st = make_ctx(ws, stream, &ctx)) != DSA_OK) return st;
-  const auto* k = static_cast<const __nv_bfloat16*>(k_pages);
-  return cuda_status(launch_prefix_attn(
-      ctx, serve_shape(cfg), static_cast<const __nv_bfloat16*>(q), k,
-      v_pages ? static_cast<const __nv_bfloat16*>(v_pages) : k, prefix_table, prefix_len,
-      block_table, seq_lens, cu_tokens, static_cast<__nv_bfloat16*>(o), lse,
-      static_cast<uint8_t*>(ws) + kHeader));
+  const ServeShape sh = serve_shape(cfg);
+  CUtensorMap qm, km, vm;
+  const uint64_t cache_rows = (uint64_t)sh.n_pages * sh.page, d = (uint64_t)sh.D;
+  const uint32_t box = sh.page < 64 ? sh.page : 64;
+  if ((st = encode_2d(&qm, q, (uint64_t)(sh.T * sh.H), d, 64)) != DSA_OK) return st;
+  if ((st = encode_2d(&km, k_pages, cache_rows, d, box)) != DSA_OK) return st;
+  if ((st = encode_2d(&vm, v_pages ? v_pages : k_pages, cache_rows, d, box)) != DSA_OK)
+    return st;
+  return cuda_status(launch_prefix_attn(ctx, sh, qm, km, vm, prefix_table, prefix_len,
+                                        block_table, seq_lens, cu_tokens,
+                                        static_cast<__nv_bfloat16*>(o), lse,
+                                        static_cast<uint8_t*>(ws) + kHeader));
 }
 
 }  // extern "C"
