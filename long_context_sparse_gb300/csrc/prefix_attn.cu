@@ -24,8 +24,13 @@
 // between the CTAs and no reduction:
 //   P = 2^(s - m),  l += P,  O^T += V^T P^T      (O, l, m in fp32, P in bf16:
 //   the tensor core's operand type, one rounding of 2^-9 for each weight).
-// P of rows 0-63 goes to CTA 0, of rows 64-127 to CTA 1 (distributed shared
-// memory), which is the B operand's split.
+// P of rows 0-63 goes to CTA 0, of rows 64-127 to CTA 1, which is the B
+// operand's split: what crosses goes by st.async, whose bytes the receiving
+// CTA's barrier counts.  Signals between the CTAs on the usual path carry no
+// cluster-scope fence (measured: a release.cluster arrival waits about 1500
+// cycles under load, a plain one none): data that crosses is counted by a
+// barrier (TMA, st.async), and what a CTA's own threads wrote to its own
+// shared memory was handed to the relaying thread inside the CTA.
 //
 // Work.  Units cost their tiles plus kUnitCost; the pairs share the sum
 // evenly in unit order, so a long prefix is split over all of them and short
@@ -42,9 +47,10 @@ constexpr int kRows = 128;           // rows of a unit
 constexpr int kKeys = 256;           // keys of a tile
 constexpr int kMaxPairs = 80;        // workspace bound on the pairs of a launch
 constexpr int kUnitCost = 2;         // a unit's Q load and epilogue, in tiles
-constexpr int kSoftWarps = 8;
-constexpr int kProdWarp = 8, kRelayWarp = 9, kMmaWarp = 10;
-constexpr int kThreads = 32 * 12;
+constexpr int kSoftWarps = 16;       // 4 TMEM lane quadrants x 4 groups of rows
+constexpr int kGroupRows = 32;
+constexpr int kProdWarp = 16, kFixWarp = 17, kMmaWarp = 18, kPassWarp = 19;
+constexpr int kThreads = 32 * 20;
 constexpr uint32_t kStageBytes = 16384;
 constexpr float kSlack = 8.0f;       // log2 headroom before a maximum is raised
 
@@ -284,9 +290,14 @@ __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
                ::: "memory");
 }
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+// Arrivals at a barrier of either CTA: with a cluster-scope release of this
+// thread's writes, and without.
+__device__ __forceinline__ void mbar_release_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
+}
+__device__ __forceinline__ void mbar_signal(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 __device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity, uint32_t hint) {
   uint32_t ok;
@@ -302,13 +313,22 @@ __device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity, 
 __device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-__device__ __forceinline__ void st_cluster_v4(uint32_t addr, const uint32_t (&v)[4]) {
-  asm volatile("st.shared::cluster.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v[0]),
-               "r"(v[1]), "r"(v[2]), "r"(v[3])
-               : "memory");
+// 16 bytes into either CTA's shared memory; its barrier `bar` counts them.
+__device__ __forceinline__ void st_async_v4(uint32_t addr, const uint32_t (&v)[4],
+                                            uint32_t bar) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1,%2,%3,%4}, [%5];"
+      ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(bar)
+      : "memory");
 }
-__device__ __forceinline__ void fence_proxy_async_all() {
-  asm volatile("fence.proxy.async;" ::: "memory");
+// TMA load into this CTA, its bytes counted by a barrier of either CTA.
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, int32_t c0,
+                                              int32_t c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
 }
 __device__ __forceinline__ void tc_mma2(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                         uint32_t accumulate) {
@@ -366,32 +386,34 @@ struct PCfg {
   static constexpr int kBlocks = D > 256 ? D / 256 : 1;  // 256-dv blocks of O^T
   static constexpr uint32_t kQBytes = 64 * D * 2;     // this CTA's 64 rows
   static constexpr uint32_t kPBytes = kKeys * 128;    // 256 keys x 64 rows
-  static constexpr int kStages = 7;
+  static constexpr int kStages = D == 512 ? 7 : 9;
   static constexpr uint32_t kTail = 16 * 1024;
+  // stages between the second-next ragged V stages (see the producer)
+  static_assert(2 * (kAtoms + 4 * kBlocks) >= kStages, "ragged stages in flight");
   static constexpr uint32_t kSmem = 1024 + kQBytes + kPBytes + kStages * kStageBytes + kTail;
   static_assert(kSmem <= 232448, "shared memory");
 };
 
-// One butterfly step of column_reduce: lanes keep half of the H2 * 2 columns.
-template <int H2, bool MAX>
-__device__ __forceinline__ void column_step(float (&x)[64], int lane) {
-  const bool up = (lane & H2 / 2) != 0;
+// One butterfly step of column_reduce: lanes keep half of the 2 * H columns.
+template <int H, bool MAX>
+__device__ __forceinline__ void column_step(float (&x)[32], int lane) {
+  const bool up = (lane & H) != 0;
 #pragma unroll
-  for (int i = 0; i < H2; ++i) {
-    const float keep = up ? x[i + H2] : x[i], give = up ? x[i] : x[i + H2];
-    const float got = __shfl_xor_sync(0xffffffffu, give, H2 / 2);
+  for (int i = 0; i < H; ++i) {
+    const float keep = up ? x[i + H] : x[i], give = up ? x[i] : x[i + H];
+    const float got = __shfl_xor_sync(0xffffffffu, give, H);
     x[i] = MAX ? fmaxf(keep, got) : keep + got;
   }
 }
-// Reduce 64 columns over the warp's 32 lanes: lane i ends with columns 2i and
-// 2i+1 in x[0], x[1] (62 shuffles; each step halves the columns that a lane keeps).
+// Reduce 32 columns over the warp's lanes: lane i ends with column i in x[0]
+// (31 shuffles: each step halves the columns that a lane keeps).
 template <bool MAX>
-__device__ __forceinline__ void column_reduce(float (&x)[64], int lane) {
-  column_step<32, MAX>(x, lane);
+__device__ __forceinline__ void column_reduce(float (&x)[32], int lane) {
   column_step<16, MAX>(x, lane);
   column_step<8, MAX>(x, lane);
   column_step<4, MAX>(x, lane);
   column_step<2, MAX>(x, lane);
+  column_step<1, MAX>(x, lane);
 }
 
 template <int D>
@@ -417,26 +439,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint8_t* tail = gb + C::kQBytes + C::kPBytes + kStages * kStageBytes;
   float* red = carve<float>(tail, 8 * kRows);     // [rank * 4 + quadrant][row] maxima
   float* lred = carve<float>(tail, 4 * kRows);    // [quadrant][row] sums
-  float* thr_s = carve<float>(tail, kRows);       // raise a row's maximum above this
-  float* nm_s = carve<float>(tail, kRows);        // -m (0 while m = -inf)
+  // per row: -m (0 while m = -inf), and -(m + slack), above which the maximum
+  // is raised (inf while m = -inf)
+  float* nm_s = carve<float>(tail, kRows);
+  float* nt_s = carve<float>(tail, kRows);
   float* alpha_s = carve<float>(tail, kRows);
   int32_t* lim_s = carve<int32_t>(tail, kRows);   // keys that a row sees
-  uint64_t* bars = carve<uint64_t>(tail, 3 * kStages + 20);
+  uint64_t* bars = carve<uint64_t>(tail, 2 * kStages + 20);
   uint32_t* misc = carve<uint32_t>(tail, 8);      // abort, tmem, flags[2], start request
   const uint32_t bar0 = smem_u32(bars);
-  auto full_loc = [&](int s) { return bar0 + 8u * s; };               // own TMA landed
-  auto full = [&](int s) { return bar0 + 8u * (kStages + s); };       // leader: both landed
-  auto empty = [&](int s) { return bar0 + 8u * (2 * kStages + s); };  // stage read
-  const uint32_t bx = bar0 + 8u * (3 * kStages);
-  const uint32_t q_loc = bx, q_full = bx + 8, q_empty = bx + 16;
-  auto s_full = [&](uint32_t b) { return bx + 24 + 8 * b; };
-  auto s_free = [&](uint32_t b) { return bx + 40 + 8 * b; };          // leader
-  const uint32_t p_full = bx + 56;                                    // leader
+  auto full = [&](int s) { return bar0 + 8u * s; };               // leader: both landed
+  auto empty = [&](int s) { return bar0 + 8u * (kStages + s); };  // stage read
+  const uint32_t bx = bar0 + 8u * (2 * kStages);
+  const uint32_t q_full = bx;                                     // leader
+  const uint32_t q_empty = bx + 8;
+  auto s_full = [&](uint32_t b) { return bx + 16 + 8 * b; };
+  auto s_free = [&](uint32_t b) { return bx + 32 + 8 * b; };      // leader
+  const uint32_t p_in = bx + 48;     // this CTA's P is written
+  const uint32_t p_full = bx + 56;   // leader: both CTAs' P are
   const uint32_t p_done = bx + 64;
-  const uint32_t o_empty = bx + 72;                                   // leader
-  const uint32_t xs = bx + 80;     // the softmax warps of both CTAs
-  const uint32_t grp = bx + 88;    // the softmax warps of this CTA
+  const uint32_t o_empty = bx + 72;  // leader
+  const uint32_t xs = bx + 80;       // the softmax warps of both CTAs
+  const uint32_t grp = bx + 88;      // the softmax warps of this CTA
   const uint32_t done_bar = bx + 96;
+  auto rag = [&](uint32_t r) { return bx + 104 + 8 * (r & 1u); };  // own ragged V stage
+  auto fixed = [&](uint32_t r) { return bx + 120 + 8 * (r & 1u); };  // leader: the other's is
   volatile uint32_t* flags = misc + 2;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank(), peer = rank ^ 1u;
@@ -444,18 +471,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(full_loc(s), 1);
-      mbar_init(full(s), 2);
+      mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
     }
-    mbar_init(q_loc, 1);
-    mbar_init(q_full, 2);
+    mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     for (uint32_t b = 0; b < 2; ++b) {
       mbar_init(s_full(b), 1);
       mbar_init(s_free(b), 2 * kSoftWarps);
+      mbar_init(rag(b), 1);
+      mbar_init(fixed(b), 1);
     }
-    mbar_init(p_full, 2 * kSoftWarps);
+    mbar_init(p_in, kSoftWarps / 2 + 1);
+    mbar_init(p_full, 2);
     mbar_init(p_done, 1);
     mbar_init(o_empty, 2 * kSoftWarps);
     mbar_init(xs, 2 * kSoftWarps);
@@ -510,14 +538,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int page = 1 << page_log2, box = min(page, 64);
     const int32_t n_rows_cache = n_pages << page_log2;  // out of range: zero rows
     const int kb = 128 / box, vb = 64 / box;            // boxes of a K stage, a V atom
-    uint32_t u = 0, nq = 0;
+    uint32_t u = 0, nq = 0, nr = 0;
     bool ok = true;
+    const uint32_t lead_q = at_rank(q_full, 0), lead_full = at_rank(full(0), 0);
     while (ok && walk.next(it)) {
       if (!(ok = W.wait(q_empty, (nq & 1u) ^ 1u))) break;
-      if (lane == 0) mbar_expect_tx(q_loc, C::kQBytes);
-      __syncwarp();
+      if (rank == 0 && lane == 0) mbar_expect_tx(q_full, 2 * C::kQBytes);
       if (lane < C::kAtoms)
-        tma_load_2d(sQ + lane * 8192, &q_map, lane * 64, it.row0 + (int32_t)rank * 64, q_loc);
+        tma_load_pair(sQ + lane * 8192, &q_map, lane * 64, it.row0 + (int32_t)rank * 64, lead_q);
       ++nq;
       // first cache row of the page that holds key x of tile j, in lane x / page
       auto page_rows = [&](int32_t j) {
@@ -544,11 +572,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int a = 0; a < C::kAtoms; ++a, ++u) {
             const int s = (int)(u % kStages);
             if (!(ok = W.wait(empty(s), ((u / kStages) & 1u) ^ 1u))) break;
-            if (lane == 0) mbar_expect_tx(full_loc(s), kStageBytes);
-            __syncwarp();
+            if (rank == 0 && lane == 0) mbar_expect_tx(full(s), 2 * kStageBytes);
             if (lane < kb)
-              tma_load_2d(sStage + s * kStageBytes + lane * box * 128, &k_map, a * 64, row,
-                          full_loc(s));
+              tma_load_pair(sStage + s * kStageBytes + lane * box * 128, &k_map, a * 64, row,
+                            lead_full + 8u * s);
           }
         }
         if (j > it.tile0 && ok) {  // V of tile j-1: 64 keys, this CTA's 128 dv a stage
@@ -559,65 +586,79 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               const int s = (int)(u % kStages);
               const int32_t row = key_row(j - 1, rows_v, g * 64 + kk);
               if (!(ok = W.wait(empty(s), ((u / kStages) & 1u) ^ 1u))) break;
-              if (lane == 0) mbar_expect_tx(full_loc(s), kStageBytes);
-              __syncwarp();
+              const int32_t left = it.len - ((j - 1) * kKeys + g * 64);
+              const bool ragged = left > 0 && left < 64;
+              if (ragged) {  // lands here first: kFixWarp passes it on
+                if (lane == 0) mbar_expect_tx(rag(nr), kStageBytes);
+                __syncwarp();
+              } else if (rank == 0 && lane == 0) {
+                mbar_expect_tx(full(s), 2 * kStageBytes);
+              }
               if (lane < 2 * vb)
-                tma_load_2d(sStage + s * kStageBytes + a * 8192 + kk * 128, &v_map,
-                            m * 256 + (int)rank * 128 + a * 64, row, full_loc(s));
+                tma_load_pair(sStage + s * kStageBytes + a * 8192 + kk * 128, &v_map,
+                              m * 256 + (int)rank * 128 + a * 64, row,
+                              ragged ? at_rank(rag(nr), rank) : lead_full + 8u * s);
+              if (ragged) ++nr;
             }
         }
         rows_v = rows_k;
         rows_k = rows_n;
       }
     }
-    if (!ok) {  // copies in flight land before the CTA goes
-      if (lane == 0) {
-        for (uint32_t x = u > kStages ? u - kStages : 0; x < u; ++x)
-          drain(full_loc((int)(x % kStages)), (x / kStages) & 1u, timeout_ns);
-        if (nq) drain(q_loc, (nq - 1) & 1u, timeout_ns);
+  } else if (warp == kFixWarp) {
+    // ============================================= ragged stages of V
+    // Rows of V past the list's end may hold NaN, which a zero weight does not
+    // cancel: the stage that holds the end is cleared behind it in both CTAs,
+    // and then handed to the leader's barrier.  (Stages wholly past the end
+    // are zero by TMA's out-of-range fill.)
+    uint32_t u = 0, nr = 0;
+    bool ok = true;
+    while (ok && walk.next(it)) {
+      for (int32_t j = it.tile0; j <= it.tile1 && ok; ++j) {
+        if (j < it.tile1) u += C::kAtoms;
+        if (j == it.tile0) continue;
+        for (int m = 0; m < C::kBlocks && ok; ++m)
+          for (int g = 0; g < 4; ++g, ++u) {
+            const int32_t left = it.len - ((j - 1) * kKeys + g * 64);
+            if (left <= 0 || left >= 64) continue;
+            const int s = (int)(u % kStages);
+            if (!(ok = W.wait(rag(nr), (nr >> 1) & 1u))) break;
+            for (int x = left * 8 + lane; x < 64 * 8; x += 32)
+#pragma unroll
+              for (int a = 0; a < 2; ++a)
+                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
+                                 sStage + s * kStageBytes + a * 8192 + x * 16),
+                             "r"(0u)
+                             : "memory");
+            fence_proxy_async();
+            __syncwarp();
+            if (rank != 0) {
+              if (lane == 0) mbar_release_cluster(at_rank(fixed(nr), 0));
+            } else {
+              if (!(ok = W.wait(fixed(nr), (nr >> 1) & 1u))) break;
+              if (lane == 0) mbar_arrive(full(s));
+            }
+            ++nr;
+          }
       }
     }
-  } else if (warp == kRelayWarp) {
-    // ==================== relay: landed copies -> the leader's barriers
-    // Rows of V past the list's end may hold NaN, which a zero weight does not
-    // cancel: they are cleared here, between the copy and the product.
-    uint32_t u = 0, nq = 0;
+  } else if (warp == kPassWarp) {
+    // ================= this CTA's P complete -> the leader's barrier
+    uint32_t nt = 0;
     bool ok = true;
-    const uint32_t lead_q = at_rank(q_full, 0);
-    auto pass = [&](int s) {
-      if (lane == 0) mbar_arrive_cluster(at_rank(full(s), 0));
-    };
+    const uint32_t lead_p = at_rank(p_full, 0);
     while (ok && walk.next(it)) {
-      if (!(ok = W.wait(q_loc, nq & 1u))) break;
-      if (lane == 0) mbar_arrive_cluster(lead_q);
-      ++nq;
-      for (int32_t j = it.tile0; j <= it.tile1 && ok; ++j) {
-        if (j < it.tile1)
-          for (int a = 0; a < C::kAtoms; ++a, ++u) {
-            const int s = (int)(u % kStages);
-            if (!(ok = W.wait(full_loc(s), (u / kStages) & 1u))) break;
-            pass(s);
-          }
-        if (j > it.tile0 && ok)
-          for (int m = 0; m < C::kBlocks && ok; ++m)
-            for (int g = 0; g < 4; ++g, ++u) {
-              const int s = (int)(u % kStages);
-              if (!(ok = W.wait(full_loc(s), (u / kStages) & 1u))) break;
-              const int32_t left = it.len - ((j - 1) * kKeys + g * 64);  // rows that count
-              if (left < 64) {
-                const int from = left > 0 ? left : 0;
-                for (int x = from * 8 + lane; x < 64 * 8; x += 32)
-#pragma unroll
-                  for (int a = 0; a < 2; ++a)
-                    asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
-                                     sStage + s * kStageBytes + a * 8192 + x * 16),
-                                 "r"(0u)
-                                 : "memory");
-                fence_proxy_async_all();
-                __syncwarp();
-              }
-              pass(s);
-            }
+      // bytes from the other CTA's keys, for this CTA's groups with rows
+      const int mine = (it.n_rows - 64 * (int)rank + kGroupRows - 1) / kGroupRows;
+      const uint32_t bytes = (uint32_t)max(0, min(2, mine)) * (128 * kGroupRows * 2);
+      for (int32_t j = it.tile0; j < it.tile1; ++j, ++nt) {
+        if (lane == 0) mbar_expect_tx(p_in, bytes);
+        if (!(ok = W.wait(p_in, nt & 1u))) break;
+        if (lane == 0) {
+          fence_proxy_async();
+          mbar_signal(lead_p);
+        }
+        __syncwarp();
       }
     }
   } else if (warp == kMmaWarp) {
@@ -679,38 +720,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp < kSoftWarps) {
+  } else {
     // ================================================ softmax, epilogue
-    const int quad = warp & 3, g = warp >> 2;      // TMEM lanes, rows 64 g .. 64 g + 63
+    const int quad = warp & 3, g = warp >> 2;  // TMEM lanes, rows 32 g .. 32 g + 31
+    const int r0 = kGroupRows * g;
     const int key = (int)rank * 128 + quad * 32 + lane;
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
-    const uint32_t xs_own = at_rank(xs, rank), xs_peer = at_rank(xs, peer);
+    const uint32_t xs_peer = at_rank(xs, peer), xs_own = at_rank(xs, rank);
     const uint32_t flag_own = at_rank(smem_u32(misc + 2), rank);
     const uint32_t flag_peer = at_rank(smem_u32(misc + 2), peer);
     const uint32_t red_own = at_rank(smem_u32(red), rank), red_peer = at_rank(smem_u32(red), peer);
-    const uint32_t l_s_free0 = at_rank(s_free(0), 0), l_p_full = at_rank(p_full, 0);
-    const uint32_t l_o_empty = at_rank(o_empty, 0);
-    const uint32_t p_row = at_rank(sP, (uint32_t)g) + (uint32_t)key * 128u;
-    const uint32_t p_sw = (uint32_t)(key & 7);
+    const uint32_t l_s_free0 = at_rank(s_free(0), 0), l_o_empty = at_rank(o_empty, 0);
+    const uint32_t owner = (uint32_t)g >> 1;  // the CTA that holds P of these rows
+    const uint32_t p_row = (owner == rank ? sP : at_rank(sP, peer)) + (uint32_t)key * 128u;
+    const uint32_t p_in_peer = at_rank(p_in, peer);
+    const uint32_t p_c0 = (uint32_t)(g & 1) * 4u, p_sw = (uint32_t)(key & 7);
     uint32_t nx = 0, ng = 0, nt = 0;
-    // all softmax warps of the pair / of this CTA
-    auto pair_sync = [&]() {
+    // all softmax warps of the pair; `publish`: with this warp's writes to both
+    // CTAs before it
+    auto pair_sync = [&](bool publish) {
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive_cluster(xs_own);
-        mbar_arrive_cluster(xs_peer);
+        if (publish) {
+          mbar_release_cluster(xs_own);
+          mbar_release_cluster(xs_peer);
+        } else {
+          mbar_signal(xs_own);
+          mbar_signal(xs_peer);
+        }
       }
       return W.wait(xs, nx++ & 1u);
     };
-    auto group_sync = [&]() {
+    auto group_sync = [&]() {  // all softmax warps of this CTA
       __syncwarp();
       if (lane == 0) mbar_arrive(grp);
       return W.wait(grp, ng++ & 1u);
     };
     bool ok = true;
     while (ok && walk.next(it)) {
-      const bool live = it.n_rows > 64 * g;  // this group has rows that count
-      int32_t lim_min = it.len;              // keys that every row of the block sees
+      const bool live = it.n_rows > r0;  // this group has rows that count
+      int32_t lim_min = it.len;          // keys that every row of the block sees
       if (it.b >= 0) {
         const ReqShape r = req_shape(L, it.b);
         lim_min = row_limit(r, L.H, it.rel0);
@@ -720,16 +769,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         lim_s[tid] = it.len;
       }
       if (tid < kRows) {
-        thr_s[tid] = -INFINITY;
         nm_s[tid] = 0.f;
+        nt_s[tid] = INFINITY;
       }
-      float l[64];
+      float l[32];
 #pragma unroll
-      for (int h = 0; h < 64; ++h) l[h] = 0.f;
+      for (int h = 0; h < 32; ++h) l[h] = 0.f;
       const int n = it.tile1 - it.tile0;
       for (int j = 0; j < n; ++j, ++nt) {
         const uint32_t b = nt & 1u;
-        const uint32_t tS = tmem + b * kRows + lane_base + 64 * g;
+        const uint32_t tS = tmem + b * kRows + lane_base + r0;
         if (!(ok = W.wait(s_full(b), (nt >> 1) & 1u))) break;
         tc_fence_after();
         const int32_t pos = (it.tile0 + j) * kKeys + key;
@@ -738,68 +787,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // taken on a unit's first tile, whose maxima are not set yet.)
         bool need = j == 0;
         if (j > 0 && live) {
+          float over = -INFINITY;
 #pragma unroll
-          for (int h0 = 0; h0 < 64; h0 += 16) {
+          for (int h0 = 0; h0 < 32; h0 += 16) {
             uint32_t r[16];
             tmem_ld16(tS + h0, r);
             tmem_wait_ld();
+            const float4* nt4 = reinterpret_cast<const float4*>(nt_s + r0 + h0);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int h = 64 * g + h0 + e;
-              const bool over = __uint_as_float(r[e]) * scale_log2 > thr_s[h];
-              need |= over && (!masked || pos < lim_s[h]);
+            for (int e = 0; e < 16; e += 4) {
+              const float4 c = nt4[e / 4];
+              const float y[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const float d = fmaf(__uint_as_float(r[e + x]), scale_log2, y[x]);
+                if (!masked || pos < lim_s[r0 + h0 + e + x]) over = fmaxf(over, d);
+              }
             }
           }
+          need = over > 0.f;
         }
+        need = __any_sync(0xffffffffu, need);
         // the flag carries the tile's number, so it never needs clearing
-        if (__any_sync(0xffffffffu, need) && lane == 0) {
+        if (need && lane == 0) {
           st_cluster_u32(flag_own + 4 * b, nt + 1u);
           st_cluster_u32(flag_peer + 4 * b, nt + 1u);
         }
-        if (!(ok = pair_sync())) break;
+        if (!(ok = pair_sync(need))) break;
         // the previous tile's PV is done: O^T is current and P free
         if (nt > 0 && !(ok = W.wait(p_done, (nt - 1u) & 1u))) break;
         tc_fence_after();
         if (flags[b] == nt + 1u) {
           // ---- exact maxima of the tile, over both CTAs' keys
-          float x[64];
+          float x[32];
 #pragma unroll
-          for (int h0 = 0; h0 < 64; h0 += 16) {
+          for (int h0 = 0; h0 < 32; h0 += 16) {
             uint32_t r[16];
             tmem_ld16(tS + h0, r);
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              x[h0 + e] = !masked || pos < lim_s[64 * g + h0 + e]
+              x[h0 + e] = !masked || pos < lim_s[r0 + h0 + e]
                               ? __uint_as_float(r[e]) * scale_log2
                               : -INFINITY;
           }
           column_reduce<true>(x, lane);
-          const uint32_t at = 4u * (uint32_t)(((int)rank * 4 + quad) * kRows + 64 * g + 2 * lane);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            st_cluster_u32(red_own + at + 4 * e, __float_as_uint(x[e]));
-            st_cluster_u32(red_peer + at + 4 * e, __float_as_uint(x[e]));
-          }
-          if (!(ok = pair_sync())) break;
+          const uint32_t at = 4u * (uint32_t)(((int)rank * 4 + quad) * kRows + r0 + lane);
+          st_cluster_u32(red_own + at, __float_as_uint(x[0]));
+          st_cluster_u32(red_peer + at, __float_as_uint(x[0]));
+          if (!(ok = pair_sync(true))) break;
           if (tid < kRows) {
             float t = red[tid];
 #pragma unroll
             for (int w = 1; w < 8; ++w) t = fmaxf(t, red[w * kRows + tid]);
-            const float th = thr_s[tid];
-            const bool raise = t > th;
-            alpha_s[tid] = raise && th != -INFINITY ? ex2(-nm_s[tid] - t) : 1.f;
+            const float nt_old = nt_s[tid];
+            const bool first = nt_old == INFINITY;
+            const bool raise = first ? t > -INFINITY : t + nt_old > 0.f;
+            alpha_s[tid] = raise && !first ? ex2(-nm_s[tid] - t) : 1.f;
             if (raise) {
-              thr_s[tid] = t + kSlack;
               nm_s[tid] = -t;
+              nt_s[tid] = -(t + kSlack);
             }
           }
           if (!(ok = group_sync())) break;
           if (j > 0) {
             bool rescale = false;
 #pragma unroll
-            for (int h = 0; h < 64; ++h) {
-              const float a = alpha_s[64 * g + h];
+            for (int h = 0; h < 32; ++h) {
+              const float a = alpha_s[r0 + h];
               l[h] *= a;
               rescale |= a != 1.f;
             }
@@ -807,14 +862,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
               for (int m = 0; m < C::kBlocks; ++m)
 #pragma unroll 1
-                for (int h0 = 0; h0 < 64; h0 += 16) {
+                for (int h0 = 0; h0 < 32; h0 += 16) {
                   uint32_t r[16];
-                  const uint32_t ta = tO + m * kRows + lane_base + 64 * g + h0;
+                  const uint32_t ta = tO + m * kRows + lane_base + r0 + h0;
                   tmem_ld16(ta, r);
                   tmem_wait_ld();
 #pragma unroll
                   for (int e = 0; e < 16; ++e)
-                    r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha_s[64 * g + h0 + e]);
+                    r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha_s[r0 + h0 + e]);
                   tmem_st16(ta, r);
                 }
               tmem_wait_st();
@@ -824,34 +879,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ---- P = 2^(s - m): row sums, and bf16 P into the CTA that owns the rows
         if (live) {
 #pragma unroll
-          for (int h0 = 0; h0 < 64; h0 += 16) {
+          for (int h0 = 0; h0 < 32; h0 += 16) {
             uint32_t r[16];
             tmem_ld16(tS + h0, r);
             tmem_wait_ld();
-            float p[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int h = 64 * g + h0 + e;
-              p[e] = ex2(fmaf(__uint_as_float(r[e]), scale_log2, nm_s[h]));
-              if (masked && pos >= lim_s[h]) p[e] = 0.f;
-              l[h0 + e] += p[e];
+            if (h0 == 16) {  // the last read of this S^T buffer
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_signal(l_s_free0 + 8 * b);
             }
+            float p[16];
+            const float4* nm4 = reinterpret_cast<const float4*>(nm_s + r0 + h0);
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              const float4 c = nm4[e / 4];
+              p[e] = ex2(fmaf(__uint_as_float(r[e]), scale_log2, c.x));
+              p[e + 1] = ex2(fmaf(__uint_as_float(r[e + 1]), scale_log2, c.y));
+              p[e + 2] = ex2(fmaf(__uint_as_float(r[e + 2]), scale_log2, c.z));
+              p[e + 3] = ex2(fmaf(__uint_as_float(r[e + 3]), scale_log2, c.w));
+            }
+            if (masked) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (pos >= lim_s[r0 + h0 + e]) p[e] = 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) l[h0 + e] += p[e];
 #pragma unroll
             for (int c8 = 0; c8 < 2; ++c8) {
               uint32_t w[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 w[e] = pack_bf16(p[8 * c8 + 2 * e], p[8 * c8 + 2 * e + 1]);
-              st_cluster_v4(p_row + (((uint32_t)(h0 / 8 + c8) ^ p_sw) << 4), w);
+              const uint32_t a = p_row + (((p_c0 + (uint32_t)(h0 / 8 + c8)) ^ p_sw) << 4);
+              if (owner == rank)
+                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(w[0]),
+                             "r"(w[1]), "r"(w[2]), "r"(w[3])
+                             : "memory");
+              else
+                st_async_v4(a, w, p_in_peer);
             }
           }
+        } else {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_signal(l_s_free0 + 8 * b);
         }
-        fence_proxy_async_all();  // P -> the tensor core's reads
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive_cluster(l_s_free0 + 8 * b);
-          mbar_arrive_cluster(l_p_full);
+        if (owner == rank) {  // what crosses is counted by its bytes
+          fence_proxy_async();  // P -> the tensor core's reads
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_in);
         }
       }
       if (!ok) break;
@@ -860,16 +937,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!(ok = W.wait(p_done, (nt - 1u) & 1u))) break;
       tc_fence_after();
       column_reduce<false>(l, lane);
-      lred[quad * kRows + 64 * g + 2 * lane] = l[0];
-      lred[quad * kRows + 64 * g + 2 * lane + 1] = l[1];
+      lred[quad * kRows + r0 + lane] = l[0];
       if (!(ok = group_sync())) break;
       if (DSA_IN_BOUNDS(slot < n_slots, status)) {
         if (tid < it.n_rows) {
           const float sum = lred[tid] + lred[kRows + tid] + lred[2 * kRows + tid] +
                             lred[3 * kRows + tid];
-          const float th = thr_s[tid];
           view.ml[(slot * 2 + rank) * kRows + tid] =
-              make_float2(th == -INFINITY ? -INFINITY : -nm_s[tid], sum);
+              make_float2(nt_s[tid] == INFINITY ? -INFINITY : -nm_s[tid], sum);
         }
         float* out = view.o + slot * (int64_t)(kRows * D);
 #pragma unroll 1
@@ -877,7 +952,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int dv = m * 256 + (int)rank * 128 + quad * 32 + lane;
           if (dv >= D) break;  // D = 128: the second CTA's lanes are padding
 #pragma unroll 1
-          for (int h0 = 64 * g; h0 < min(64 * g + 64, it.n_rows); h0 += 16) {
+          for (int h0 = r0; h0 < min(r0 + kGroupRows, it.n_rows); h0 += 16) {
             uint32_t r[16];
             tmem_ld16(tO + m * kRows + lane_base + h0, r);
             tmem_wait_ld();
@@ -889,11 +964,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(l_o_empty);
+      if (lane == 0) mbar_signal(l_o_empty);
     }
   }
 
-  // ---- teardown: every role has left its loop
+  // ---- teardown: every role has left its loop.  After a wait that gave up,
+  // copies may be in flight to either CTA: they get 2 ms to land before the
+  // CTAs go.
+  if (tid == 0 && *W.abort_flag) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 2000000u) __nanosleep(100000);
+  }
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();
