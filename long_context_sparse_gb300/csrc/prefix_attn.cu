@@ -379,6 +379,18 @@ struct PairWaiter {
   }
 };
 
+// Position in the ring of N stages: the stage and its phase's parity.
+template <int N>
+struct Ring {
+  uint32_t s = 0, ph = 0;
+  __device__ __forceinline__ void step() {
+    if (++s == N) {
+      s = 0;
+      ph ^= 1u;
+    }
+  }
+};
+
 // ------------------------------------------------------------ main kernel
 template <int D>
 struct PCfg {
@@ -538,12 +550,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int page = 1 << page_log2, box = min(page, 64);
     const int32_t n_rows_cache = n_pages << page_log2;  // out of range: zero rows
     const int kb = 128 / box, vb = 64 / box;            // boxes of a K stage, a V atom
-    uint32_t u = 0, nq = 0, nr = 0;
+    Ring<kStages> ring;
+    uint32_t nq = 0, nr = 0;
     bool ok = true;
     const uint32_t lead_q = at_rank(q_full, 0), lead_full = at_rank(full(0), 0);
+    // lane's part: box i of a K stage, box i % vb of atom i / vb of a V stage
+    const bool k_on = lane < kb, v_on = lane < 2 * vb;
+    const int k_key = (int)rank * 128 + (k_on ? lane : 0) * box;
+    const int v_atom = v_on ? lane / vb : 0, v_key = v_on ? (lane % vb) * box : 0;
+    const uint32_t k_dst = sStage + (uint32_t)lane * box * 128;
+    const uint32_t v_dst = sStage + v_atom * 8192 + v_key * 128;
+    const int v_col = (int)rank * 128 + v_atom * 64;
+    const bool arms = rank == 0 && lane == 0;
     while (ok && walk.next(it)) {
       if (!(ok = W.wait(q_empty, (nq & 1u) ^ 1u))) break;
-      if (rank == 0 && lane == 0) mbar_expect_tx(q_full, 2 * C::kQBytes);
+      if (arms) mbar_expect_tx(q_full, 2 * C::kQBytes);
       if (lane < C::kAtoms)
         tma_load_pair(sQ + lane * 8192, &q_map, lane * 64, it.row0 + (int32_t)rank * 64, lead_q);
       ++nq;
@@ -563,45 +584,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         return r == n_rows_cache || j * kKeys + key >= it.len ? n_rows_cache
                                                               : r + (key & (page - 1));
       };
-      int32_t rows_v = n_rows_cache, rows_k = page_rows(it.tile0);
+      int32_t rows_k = page_rows(it.tile0);
+      int32_t v_row[4] = {};  // of this lane's box in the four 64-key groups of V
       for (int32_t j = it.tile0; j <= it.tile1 && ok; ++j) {
         const int32_t rows_n = page_rows(j + 1);
         if (j < it.tile1) {  // K of tile j: this CTA's 128 keys, 64 dims a stage
-          const int key = (int)rank * 128 + (lane < kb ? lane : 0) * box;
-          const int32_t row = key_row(j, rows_k, key);
-          for (int a = 0; a < C::kAtoms; ++a, ++u) {
-            const int s = (int)(u % kStages);
-            if (!(ok = W.wait(empty(s), ((u / kStages) & 1u) ^ 1u))) break;
-            if (rank == 0 && lane == 0) mbar_expect_tx(full(s), 2 * kStageBytes);
-            if (lane < kb)
-              tma_load_pair(sStage + s * kStageBytes + lane * box * 128, &k_map, a * 64, row,
-                            lead_full + 8u * s);
+          const int32_t row = key_row(j, rows_k, k_key);
+#pragma unroll 1
+          for (int a = 0; a < C::kAtoms; ++a) {
+            if (!(ok = W.wait(empty(ring.s), ring.ph ^ 1u))) break;
+            if (arms) mbar_expect_tx(full(ring.s), 2 * kStageBytes);
+            if (k_on)
+              tma_load_pair(k_dst + ring.s * kStageBytes, &k_map, a * 64, row,
+                            lead_full + 8u * ring.s);
+            ring.step();
           }
         }
         if (j > it.tile0 && ok) {  // V of tile j-1: 64 keys, this CTA's 128 dv a stage
-          const int i = lane < 2 * vb ? lane : 0;
-          const int a = i / vb, kk = (i % vb) * box;
+          const int32_t left0 = it.len - (j - 1) * kKeys;
+#pragma unroll 1
           for (int m = 0; m < C::kBlocks && ok; ++m)
-            for (int g = 0; g < 4; ++g, ++u) {
-              const int s = (int)(u % kStages);
-              const int32_t row = key_row(j - 1, rows_v, g * 64 + kk);
-              if (!(ok = W.wait(empty(s), ((u / kStages) & 1u) ^ 1u))) break;
-              const int32_t left = it.len - ((j - 1) * kKeys + g * 64);
-              const bool ragged = left > 0 && left < 64;
-              if (ragged) {  // lands here first: kFixWarp passes it on
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              if (!(ok = W.wait(empty(ring.s), ring.ph ^ 1u))) break;
+              const bool ragged = left0 > 64 * g && left0 < 64 * g + 64;
+              uint32_t bar = lead_full + 8u * ring.s;
+              if (ragged) {  // lands at this CTA's barrier: kFixWarp passes it on
                 if (lane == 0) mbar_expect_tx(rag(nr), kStageBytes);
                 __syncwarp();
-              } else if (rank == 0 && lane == 0) {
-                mbar_expect_tx(full(s), 2 * kStageBytes);
+                bar = at_rank(rag(nr), rank);
+                ++nr;
+              } else if (arms) {
+                mbar_expect_tx(full(ring.s), 2 * kStageBytes);
               }
-              if (lane < 2 * vb)
-                tma_load_pair(sStage + s * kStageBytes + a * 8192 + kk * 128, &v_map,
-                              m * 256 + (int)rank * 128 + a * 64, row,
-                              ragged ? at_rank(rag(nr), rank) : lead_full + 8u * s);
-              if (ragged) ++nr;
+              if (v_on)
+                tma_load_pair(v_dst + ring.s * kStageBytes, &v_map, m * 256 + v_col, v_row[g],
+                              bar);
+              ring.step();
             }
         }
-        rows_v = rows_k;
+        if (j < it.tile1)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) v_row[g] = key_row(j, rows_k, g * 64 + v_key);
         rows_k = rows_n;
       }
     }
@@ -611,36 +635,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // cancel: the stage that holds the end is cleared behind it in both CTAs,
     // and then handed to the leader's barrier.  (Stages wholly past the end
     // are zero by TMA's out-of-range fill.)
-    uint32_t u = 0, nr = 0;
+    uint32_t u = 0, nr = 0;  // stages before this item, ragged stages so far
     bool ok = true;
     while (ok && walk.next(it)) {
-      for (int32_t j = it.tile0; j <= it.tile1 && ok; ++j) {
-        if (j < it.tile1) u += C::kAtoms;
-        if (j == it.tile0) continue;
-        for (int m = 0; m < C::kBlocks && ok; ++m)
-          for (int g = 0; g < 4; ++g, ++u) {
-            const int32_t left = it.len - ((j - 1) * kKeys + g * 64);
-            if (left <= 0 || left >= 64) continue;
-            const int s = (int)(u % kStages);
-            if (!(ok = W.wait(rag(nr), (nr >> 1) & 1u))) break;
-            for (int x = left * 8 + lane; x < 64 * 8; x += 32)
+      const int32_t last = it.tile1 - 1;            // only the last tile can hold the end
+      const int32_t end = it.len - last * kKeys;    // keys of it that count
+      const int n = it.tile1 - it.tile0;
+      if (end < kKeys && (end & 63) != 0) {
+        // its V stages are the item's last 4 * kBlocks; the end is in group end / 64
+        for (int m = 0; m < C::kBlocks && ok; ++m, ++nr) {
+          const uint32_t at = u + (uint32_t)n * (C::kAtoms + 4 * C::kBlocks) -
+                              4 * (C::kBlocks - m) + (uint32_t)(end >> 6);
+          const uint32_t s = at % kStages;
+          if (!(ok = W.wait(rag(nr), (nr >> 1) & 1u))) break;
+          for (int x = (end & 63) * 8 + lane; x < 64 * 8; x += 32)
 #pragma unroll
-              for (int a = 0; a < 2; ++a)
-                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
-                                 sStage + s * kStageBytes + a * 8192 + x * 16),
-                             "r"(0u)
-                             : "memory");
-            fence_proxy_async();
-            __syncwarp();
-            if (rank != 0) {
-              if (lane == 0) mbar_release_cluster(at_rank(fixed(nr), 0));
-            } else {
-              if (!(ok = W.wait(fixed(nr), (nr >> 1) & 1u))) break;
-              if (lane == 0) mbar_arrive(full(s));
-            }
-            ++nr;
+            for (int a = 0; a < 2; ++a)
+              asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
+                               sStage + s * kStageBytes + a * 8192 + x * 16),
+                           "r"(0u)
+                           : "memory");
+          fence_proxy_async();
+          __syncwarp();
+          if (rank != 0) {
+            if (lane == 0) mbar_release_cluster(at_rank(fixed(nr), 0));
+          } else {
+            if (!(ok = W.wait(fixed(nr), (nr >> 1) & 1u))) break;
+            if (lane == 0) mbar_arrive(full(s));
           }
+        }
       }
+      u += (uint32_t)n * (C::kAtoms + 4 * C::kBlocks);
     }
   } else if (warp == kPassWarp) {
     // ================= this CTA's P complete -> the leader's barrier
@@ -664,8 +689,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == kMmaWarp) {
     // ============================================ MMA issuer (leader only)
     if (rank == 0 && lane == 0) {
-      uint32_t u = 0, nt = 0, nq = 0;
+      Ring<kStages> ring;
+      uint32_t nt = 0, nq = 0;
       bool issued = false, ok = true;
+      // descriptors of stage 0, Q and P; an address 16 bytes on is 1 more
+      const uint64_t dK = sdesc_sw128(sStage, 16, 1024), dV = sdesc_sw128(sStage, 8192, 1024);
+      const uint64_t dQ = sdesc_sw128(sQ, 16, 1024), dP = sdesc_sw128(sP, 16, 1024);
+      constexpr uint32_t kStep = kStageBytes >> 4;
       while (ok && walk.next(it)) {
         if (!(ok = W.wait1(q_full, nq & 1u))) break;
         const int n = it.tile1 - it.tile0;
@@ -673,18 +703,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (j < n) {
             const uint32_t t = nt + (uint32_t)j, b = t & 1u;
             if (!(ok = W.wait1(s_free(b), ((t >> 1) & 1u) ^ 1u))) break;
-            for (int a = 0; a < C::kAtoms; ++a, ++u) {
-              const int s = (int)(u % kStages);
-              if (!(ok = W.wait1(full(s), (u / kStages) & 1u))) break;
+            issued = true;
+#pragma unroll 2
+            for (int a = 0; a < C::kAtoms; ++a) {
+              const uint64_t da = dK + ring.s * kStep, db = dQ + (uint32_t)a * 512u;
+              if (!(ok = W.wait1(full(ring.s), ring.ph))) break;
               tc_fence_after();
-              const uint32_t st = sStage + s * kStageBytes;
 #pragma unroll
-              for (int kin = 0; kin < 4; ++kin)
-                tc_mma2(tmem + b * kRows, sdesc_sw128(st + kin * 32, 16, 1024),
-                        sdesc_sw128(sQ + a * 8192 + kin * 32, 16, 1024), IDESC_S,
+              for (uint32_t kin = 0; kin < 4; ++kin)
+                tc_mma2(tmem + b * kRows, da + 2 * kin, db + 2 * kin, IDESC_S,
                         (a | kin) != 0 ? 1u : 0u);
-              issued = true;
-              tc_commit2(empty(s));
+              tc_commit2(empty(ring.s));
+              ring.step();
             }
             if (!ok) break;
             if (j == n - 1) tc_commit2(q_empty);
@@ -694,18 +724,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t t = nt + (uint32_t)j - 1u;
             if (!(ok = W.wait1(p_full, t & 1u))) break;
             if (j == 1 && !(ok = W.wait1(o_empty, (nq & 1u) ^ 1u))) break;
+#pragma unroll 1
             for (int m = 0; m < C::kBlocks && ok; ++m)
-              for (int g = 0; g < 4; ++g, ++u) {
-                const int s = (int)(u % kStages);
-                if (!(ok = W.wait1(full(s), (u / kStages) & 1u))) break;
-                tc_fence_after();
-                const uint32_t st = sStage + s * kStageBytes;
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                  tc_mma2(tO + m * kRows, sdesc_sw128(st + ks * 2048, 8192, 1024),
-                          sdesc_sw128(sP + (g * 4 + ks) * 2048, 16, 1024), IDESC_O,
-                          ((j - 1) | g | ks) != 0 ? 1u : 0u);
-                tc_commit2(empty(s));
+              for (uint32_t g = 0; g < 4; ++g) {
+                const uint64_t da = dV + ring.s * kStep;
+                if (!(ok = W.wait1(full(ring.s), ring.ph))) break;
+                tc_fence_after();
+#pragma unroll
+                for (uint32_t ks = 0; ks < 4; ++ks)
+                  tc_mma2(tO + m * kRows, da + 128 * ks, dP + 128 * (4 * g + ks), IDESC_O,
+                          (j > 1 || (g | ks) != 0) ? 1u : 0u);
+                tc_commit2(empty(ring.s));
+                ring.step();
               }
             if (!ok) break;
             tc_commit2(p_done);
