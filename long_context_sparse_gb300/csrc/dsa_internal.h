@@ -151,7 +151,7 @@ size_t prefix_attn_ws(const ServeShape& s);
 
 // Shared-prefix attention; work: the workspace past the header.  q_map: q as
 // [T * H, D], box {64, 64}; k_map, v_map: the cache as [n_pages * page, D], box
-// {64, min(page, 64)}.
+// {64, page}.
 cudaError_t launch_prefix_attn(const LaunchCtx& c, const ServeShape& s,
                                const CUtensorMap& q_map, const CUtensorMap& k_map,
                                const CUtensorMap& v_map, const int32_t* prefix_table,

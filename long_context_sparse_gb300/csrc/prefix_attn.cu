@@ -18,12 +18,19 @@
 // where 128 x 64 would read 6 KB in 32.  TMEM: two S^T buffers (2 x 128
 // columns) and O^T (128 columns per 256 dv): all 512 at d = 512.
 //
-// Softmax.  A thread owns one key (a TMEM lane) and 64 rows; the running
-// maximum m of a row is shared by the pair and only raised when a tile beats
-// it by more than 2^8, so that the usual tile needs one exchange of flags
-// between the CTAs and no reduction:
+// Softmax.  A thread owns one key (a TMEM lane) and 32 rows:
 //   P = 2^(s - m),  l += P,  O^T += V^T P^T      (O, l, m in fp32, P in bf16:
-//   the tensor core's operand type, one rounding of 2^-9 for each weight).
+//   the tensor core's operand type, one rounding of each weight).
+// m of a row is a reference near its maximum, shared by the pair: the exact
+// maximum of the unit's first tile, afterwards raised only when a score passes
+// it by more than 2^20.  (Any reference gives the same result as long as nothing
+// overflows: the weights are floating point, and fp32 leaves 2^107 above.)  So
+// the usual tile has no exchange of maxima: P is computed while the tensor
+// cores work on the tile before, and a warp that meets a larger score objects
+// before it hands its P over.  The issuing thread then withholds the product;
+// every warp takes the exact maxima, rescales l and O^T, writes that tile's P
+// again, and the work goes on.  One read of S^T, no reduction and no barrier
+// among the softmax warps per tile.
 // P of rows 0-63 goes to CTA 0, of rows 64-127 to CTA 1, which is the B
 // operand's split: what crosses goes by st.async, whose bytes the receiving
 // CTA's barrier counts.  Signals between the CTAs on the usual path carry no
@@ -51,8 +58,11 @@ constexpr int kSoftWarps = 16;       // 4 TMEM lane quadrants x 4 groups of rows
 constexpr int kGroupRows = 32;
 constexpr int kProdWarp = 16, kFixWarp = 17, kMmaWarp = 18, kPassWarp = 19;
 constexpr int kThreads = 32 * 20;
-constexpr uint32_t kStageBytes = 16384;
-constexpr float kSlack = 8.0f;       // log2 headroom before a maximum is raised
+constexpr uint32_t kAtom = 16384;    // 128 rows of 128 bytes
+constexpr uint32_t kStageBytes = 2 * kAtom;
+constexpr int kSoftRegs = 104, kServiceRegs = 64;  // of the 96 that each thread starts with
+static_assert(32 * (16 * kSoftRegs + 4 * kServiceRegs) <= kThreads * 96, "register split");
+constexpr float kSlack = 20.0f;      // log2 headroom before a row's reference is raised
 
 // ------------------------------------------------------------------- plan
 // The division of work, written by plan_kernel, read by the other two.
@@ -69,7 +79,7 @@ struct PlanView {
   Plan* p;
   int64_t* ccum;
   int32_t* ucum;
-  float2* ml;  // [slots][2][128]: m, and l of each CTA's keys
+  float2* ml;  // [slots][2][128]: m, and l over each CTA's keys
   float* o;    // [slots][128][D]
 };
 
@@ -223,41 +233,47 @@ struct Item {
   int32_t rel0;           // row0 from the request's first row
 };
 
+// What a pair's walk over its share reads, in shared memory.
+struct Share {
+  int64_t start, end;    // the share, in cost
+  int64_t prefix_cost;
+  int32_t prefix_tiles, prefix_len;
+  int32_t rows_all;      // rows of all requests
+  int32_t first_b;       // request at start, past the prefix units
+};
+
 // Walks the units of one pair's share, in order.
 struct Walk {
-  const Plan* plan;
-  const int64_t* ccum;
-  const int32_t* ucum;
-  Lens L;
-  const int32_t* prefix_table;
-  const int32_t* table;
-  int32_t prefix_len, max_blocks, rows_all;
-  int64_t pos, start, end;
-  int b;  // request at or before pos, once pos is past the prefix units
+  const Share* sh;
+  int64_t pos;
+  int32_t b;  // request at or before pos, once pos is past the prefix units
 
-  __device__ __forceinline__ bool next(Item& it) {
+  __device__ __forceinline__ bool next(const PlanView& view, const Lens& L,
+                                       const int32_t* prefix_table, const int32_t* table,
+                                       int max_blocks, Item& it) {
+    const int64_t end = sh->end;
     while (pos < end) {
       int64_t c0;
       int32_t tiles;
-      if (pos < plan->prefix_cost) {
-        tiles = plan->prefix_tiles;
+      if (pos < sh->prefix_cost) {
+        tiles = sh->prefix_tiles;
         const int32_t u = (int32_t)(pos / (tiles + kUnitCost));
         c0 = (int64_t)u * (tiles + kUnitCost);
         it.unit = u;
         it.row0 = it.rel0 = u * kRows;
-        it.n_rows = min(kRows, rows_all - it.row0);
-        it.len = prefix_len;
+        it.n_rows = min(kRows, sh->rows_all - it.row0);
+        it.len = sh->prefix_len;
         it.pages = prefix_table;
         it.b = -1;
-        share_of(c0, tiles, start, end, it.tile0, it.tile1);
+        share_of(c0, tiles, sh->start, end, it.tile0, it.tile1);
       } else {
-        while (__ldg(ccum + b + 1) <= pos) ++b;
+        while (__ldg(view.ccum + b + 1) <= pos) ++b;
         const ReqShape r = req_shape(L, b);
-        const int64_t cb = __ldg(ccum + b);
+        const int64_t cb = __ldg(view.ccum + b);
         tiles = r.tiles;
         const int32_t j = (int32_t)((pos - cb) / (tiles + kUnitCost));
         c0 = cb + (int64_t)j * (tiles + kUnitCost);
-        it.unit = __ldg(ucum + b) + j;
+        it.unit = __ldg(view.ucum + b) + j;
         it.rel0 = j * kRows;
         it.row0 = r.row0 + it.rel0;
         it.n_rows = min(kRows, r.n_rows - it.rel0);
@@ -265,7 +281,7 @@ struct Walk {
         it.len = min(r.len, row_limit(r, L.H, it.rel0 + it.n_rows - 1));
         it.pages = table + (int64_t)b * max_blocks;
         it.b = b;
-        share_of(c0, tiles, start, end, it.tile0, it.tile1);
+        share_of(c0, tiles, sh->start, end, it.tile0, it.tile1);
         it.tile1 = min(it.tile1, (it.len + kKeys - 1) / kKeys);
       }
       pos = min(end, c0 + tiles + kUnitCost);
@@ -309,6 +325,9 @@ __device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity, 
       : "r"(bar), "r"(parity), "r"(hint)
       : "memory");
   return ok != 0;
+}
+__device__ __forceinline__ void fence_cluster() {
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
 }
 __device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
@@ -379,53 +398,41 @@ struct PairWaiter {
   }
 };
 
-// Position in the ring of N stages: the stage and its phase's parity.
-template <int N>
-struct Ring {
-  uint32_t s = 0, ph = 0;
-  __device__ __forceinline__ void step() {
-    if (++s == N) {
-      s = 0;
-      ph ^= 1u;
-    }
-  }
-};
-
 // ------------------------------------------------------------ main kernel
+// Shared memory at D = 512: Q 64 KB, P 32 KB, four stages of 32 KB, 2 KB of
+// row constants and barriers, 1 KB to align: all of the 227 KB.
+constexpr int kStages = 4;
+
 template <int D>
 struct PCfg {
-  static constexpr int kAtoms = D / 64;               // K stages of a tile
+  static constexpr int kKStages = D / 128;               // stages of a tile's K
   static constexpr int kBlocks = D > 256 ? D / 256 : 1;  // 256-dv blocks of O^T
-  static constexpr uint32_t kQBytes = 64 * D * 2;     // this CTA's 64 rows
-  static constexpr uint32_t kPBytes = kKeys * 128;    // 256 keys x 64 rows
-  static constexpr int kStages = D == 512 ? 7 : 9;
-  static constexpr uint32_t kTail = 16 * 1024;
-  // stages between the second-next ragged V stages (see the producer)
-  static_assert(2 * (kAtoms + 4 * kBlocks) >= kStages, "ragged stages in flight");
+  static constexpr int kVStages = 2 * kBlocks;           // 128 keys of a block each
+  static constexpr uint32_t kQBytes = 64 * D * 2;        // this CTA's 64 rows
+  static constexpr uint32_t kPBytes = kKeys * 128;       // 256 keys x 64 rows
+  static constexpr uint32_t kTail = 2048;
   static constexpr uint32_t kSmem = 1024 + kQBytes + kPBytes + kStages * kStageBytes + kTail;
   static_assert(kSmem <= 232448, "shared memory");
+  // at most two ragged V stages are in flight (rag and fixed barriers)
+  static_assert(2 * (kKStages + kVStages) >= kStages, "ragged stages in flight");
 };
 
-// One butterfly step of column_reduce: lanes keep half of the 2 * H columns.
-template <int H, bool MAX>
-__device__ __forceinline__ void column_step(float (&x)[32], int lane) {
-  const bool up = (lane & H) != 0;
-#pragma unroll
-  for (int i = 0; i < H; ++i) {
-    const float keep = up ? x[i + H] : x[i], give = up ? x[i] : x[i + H];
-    const float got = __shfl_xor_sync(0xffffffffu, give, H);
-    x[i] = MAX ? fmaxf(keep, got) : keep + got;
-  }
-}
-// Reduce 32 columns over the warp's lanes: lane i ends with column i in x[0]
-// (31 shuffles: each step halves the columns that a lane keeps).
+// Reduce 16 columns over the warp's lanes: lanes i and i + 16 end with column i
+// (16 shuffles: each step halves the columns that a lane keeps).
 template <bool MAX>
-__device__ __forceinline__ void column_reduce(float (&x)[32], int lane) {
-  column_step<16, MAX>(x, lane);
-  column_step<8, MAX>(x, lane);
-  column_step<4, MAX>(x, lane);
-  column_step<2, MAX>(x, lane);
-  column_step<1, MAX>(x, lane);
+__device__ __forceinline__ float column_reduce(float (&x)[16], int lane) {
+#pragma unroll
+  for (int H = 8; H > 0; H >>= 1) {
+    const bool up = (lane & H) != 0;
+#pragma unroll
+    for (int i = 0; i < H; ++i) {
+      const float keep = up ? x[i + H] : x[i], give = up ? x[i] : x[i + H];
+      const float got = __shfl_xor_sync(0xffffffffu, give, H);
+      x[i] = MAX ? fmaxf(keep, got) : keep + got;
+    }
+  }
+  const float got = __shfl_xor_sync(0xffffffffu, x[0], 16);
+  return MAX ? fmaxf(x[0], got) : x[0] + got;
 }
 
 template <int D>
@@ -438,7 +445,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                        int page_log2, int32_t n_pages, int64_t n_slots, float scale_log2,
                        uint32_t* status, uint64_t timeout_ns) {
   using C = PCfg<D>;
-  constexpr int kStages = C::kStages;
   constexpr uint32_t IDESC_S = idesc_bf16(256, 128, 0, 0);
   constexpr uint32_t IDESC_O = idesc_bf16(256, 128, 1, 1);
   extern __shared__ uint8_t smem_raw[];
@@ -449,40 +455,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t sP = sQ + C::kQBytes;
   const uint32_t sStage = sP + C::kPBytes;
   uint8_t* tail = gb + C::kQBytes + C::kPBytes + kStages * kStageBytes;
-  float* red = carve<float>(tail, 8 * kRows);     // [rank * 4 + quadrant][row] maxima
-  float* lred = carve<float>(tail, 4 * kRows);    // [quadrant][row] sums
-  // per row: -m (0 while m = -inf), and -(m + slack), above which the maximum
-  // is raised (inf while m = -inf)
-  float* nm_s = carve<float>(tail, kRows);
-  float* nt_s = carve<float>(tail, kRows);
-  float* alpha_s = carve<float>(tail, kRows);
-  int32_t* lim_s = carve<int32_t>(tail, kRows);   // keys that a row sees
-  uint64_t* bars = carve<uint64_t>(tail, 2 * kStages + 20);
-  uint32_t* misc = carve<uint32_t>(tail, 8);      // abort, tmem, flags[2], start request
+  float* nm_s = reinterpret_cast<float*>(tail);           // [row] -m
+  float* nmo_s = nm_s + kRows;                            // [row] -m before it was last raised
+  int32_t* lim_s = reinterpret_cast<int32_t*>(nmo_s + kRows);  // [row] keys that it sees
+  uint64_t* bars = reinterpret_cast<uint64_t*>(lim_s + kRows);
+  uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 24);     // abort, tmem, objected, redo
+  Share* share = reinterpret_cast<Share*>(misc + 4);
+  static_assert(3 * kRows * 4 + 24 * 8 + 16 + sizeof(Share) <= C::kTail, "tail");
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const uint32_t rank = cluster_rank(), peer = rank ^ 1u;
+  // scratch in the part of P that only this CTA's warps write: used while no
+  // product reads P and before this CTA's warps write it again
+  float* red = reinterpret_cast<float*>(gb + C::kQBytes + rank * 128 * 128);  // [8][row]
+  float* lred = red + 8 * kRows;                                             // [4][row]
   const uint32_t bar0 = smem_u32(bars);
-  auto full = [&](int s) { return bar0 + 8u * s; };               // leader: both landed
-  auto empty = [&](int s) { return bar0 + 8u * (kStages + s); };  // stage read
+  auto full = [&](uint32_t s) { return bar0 + 8u * s; };              // leader: both landed
+  auto empty = [&](uint32_t s) { return bar0 + 8u * (kStages + s); };  // stage read
   const uint32_t bx = bar0 + 8u * (2 * kStages);
   const uint32_t q_full = bx;                                     // leader
   const uint32_t q_empty = bx + 8;
   auto s_full = [&](uint32_t b) { return bx + 16 + 8 * b; };
-  auto s_free = [&](uint32_t b) { return bx + 32 + 8 * b; };      // leader
-  const uint32_t p_in = bx + 48;     // this CTA's P is written
-  const uint32_t p_full = bx + 56;   // leader: both CTAs' P are
-  const uint32_t p_done = bx + 64;
-  const uint32_t o_empty = bx + 72;  // leader
-  const uint32_t xs = bx + 80;       // the softmax warps of both CTAs
-  const uint32_t grp = bx + 88;      // the softmax warps of this CTA
-  const uint32_t done_bar = bx + 96;
-  auto rag = [&](uint32_t r) { return bx + 104 + 8 * (r & 1u); };  // own ragged V stage
-  auto fixed = [&](uint32_t r) { return bx + 120 + 8 * (r & 1u); };  // leader: the other's is
-  volatile uint32_t* flags = misc + 2;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = cluster_rank(), peer = rank ^ 1u;
+  const uint32_t p_in = bx + 32;     // this CTA's P is written
+  const uint32_t p_full = bx + 40;   // leader: both CTAs' P are
+  const uint32_t p_done = bx + 48;
+  const uint32_t o_empty = bx + 56;  // leader
+  const uint32_t xs = bx + 64;       // the softmax warps of both CTAs
+  const uint32_t grp = bx + 72;      // the softmax warps of this CTA
+  const uint32_t done_bar = bx + 80;
+  auto rag = [&](uint32_t r) { return bx + 88 + 8 * (r & 1u); };      // own ragged V stage
+  auto fixed = [&](uint32_t r) { return bx + 104 + 8 * (r & 1u); };   // leader: the other's is
+  static_assert(2 * kStages + 15 <= 24, "barriers");
+  // tile number + 1 of the last tile objected to (leader), to be done again
+  volatile uint32_t *objected = misc + 2, *redo = misc + 3;
   const PairWaiter W{misc, at_rank(smem_u32(misc), peer), status, timeout_ns};
 
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (uint32_t s = 0; s < kStages; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
     }
@@ -490,7 +499,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(q_empty, 1);
     for (uint32_t b = 0; b < 2; ++b) {
       mbar_init(s_full(b), 1);
-      mbar_init(s_free(b), 2 * kSoftWarps);
       mbar_init(rag(b), 1);
       mbar_init(fixed(b), 1);
     }
@@ -501,9 +509,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(xs, 2 * kSoftWarps);
     mbar_init(grp, kSoftWarps);
     mbar_init(done_bar, 1);
-    misc[0] = 0u;
-    misc[2] = misc[3] = 0u;
-    misc[4] = 0u;
+    misc[0] = misc[2] = misc[3] = 0u;
     fence_mbar_init();
     prefetch_tensormap(&q_map);
     prefetch_tensormap(&k_map);
@@ -517,142 +523,136 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   // the share of this pair and the request that it starts in
-  const Plan* plan = view.p;
-  Walk walk;
-  walk.plan = plan;
-  walk.ccum = view.ccum;
-  walk.ucum = view.ucum;
-  walk.L = L;
-  walk.prefix_table = prefix_table;
-  walk.table = table;
-  walk.prefix_len = prefix_len;
-  walk.max_blocks = max_blocks;
-  walk.rows_all = __ldg(L.cu + B) * L.H;
   const int64_t pair = blockIdx.x >> 1;
-  walk.start = walk.pos = min(plan->total, pair * plan->chunk);
-  walk.end = min(plan->total, walk.start + plan->chunk);
+  const Plan* plan = view.p;
+  const int64_t start = min(plan->total, pair * plan->chunk);
+  const int64_t end = min(plan->total, start + plan->chunk);
+  if (tid == 0) {
+    share->start = start;
+    share->end = end;
+    share->prefix_cost = plan->prefix_cost;
+    share->prefix_tiles = plan->prefix_tiles;
+    share->prefix_len = prefix_len;
+    share->rows_all = __ldg(L.cu + B) * L.H;
+    share->first_b = 0;
+  }
   __syncthreads();
-  if (walk.start < walk.end && walk.start >= plan->prefix_cost)
+  if (start < end && start >= plan->prefix_cost)
     for (int b = tid; b < B; b += kThreads)
-      if (__ldg(view.ccum + b) <= walk.start && walk.start < __ldg(view.ccum + b + 1))
-        misc[4] = (uint32_t)b;
+      if (__ldg(view.ccum + b) <= start && start < __ldg(view.ccum + b + 1)) share->first_b = b;
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();
   tc_fence_after();
-  walk.b = (int)misc[4];
-  const uint32_t tmem = misc[1];
-  const uint32_t tO = tmem + 2 * kRows;
+  Walk walk{share, start, share->first_b};
+  auto next = [&](Item& i) {
+    return walk.next(view, L, prefix_table, table, max_blocks, i);
+  };
+  constexpr uint32_t tmem = 0;  // an allocation of all 512 columns starts at column 0
+  constexpr uint32_t tO = tmem + 2 * kRows;
   Item it;
 
-  if (warp == kProdWarp) {
-    // ====================================================== TMA producer
-    const int page = 1 << page_log2, box = min(page, 64);
-    const int32_t n_rows_cache = n_pages << page_log2;  // out of range: zero rows
-    const int kb = 128 / box, vb = 64 / box;            // boxes of a K stage, a V atom
-    Ring<kStages> ring;
-    uint32_t nq = 0, nr = 0;
-    bool ok = true;
-    const uint32_t lead_q = at_rank(q_full, 0), lead_full = at_rank(full(0), 0);
-    // lane's part: box i of a K stage, box i % vb of atom i / vb of a V stage
-    const bool k_on = lane < kb, v_on = lane < 2 * vb;
-    const int k_key = (int)rank * 128 + (k_on ? lane : 0) * box;
-    const int v_atom = v_on ? lane / vb : 0, v_key = v_on ? (lane % vb) * box : 0;
-    const uint32_t k_dst = sStage + (uint32_t)lane * box * 128;
-    const uint32_t v_dst = sStage + v_atom * 8192 + v_key * 128;
-    const int v_col = (int)rank * 128 + v_atom * 64;
-    const bool arms = rank == 0 && lane == 0;
-    while (ok && walk.next(it)) {
-      if (!(ok = W.wait(q_empty, (nq & 1u) ^ 1u))) break;
-      if (arms) mbar_expect_tx(q_full, 2 * C::kQBytes);
-      if (lane < C::kAtoms)
-        tma_load_pair(sQ + lane * 8192, &q_map, lane * 64, it.row0 + (int32_t)rank * 64, lead_q);
-      ++nq;
-      // first cache row of the page that holds key x of tile j, in lane x / page
-      auto page_rows = [&](int32_t j) {
-        const int32_t pos = j * kKeys + (lane << page_log2);
-        if ((lane << page_log2) >= kKeys || j >= it.tile1 || pos >= it.len) return n_rows_cache;
-        const int32_t p = __ldg(it.pages + (pos >> page_log2));
-        if (p < 0 || p >= n_pages) {
-          latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
-          return n_rows_cache;
-        }
-        return p << page_log2;
-      };
-      auto key_row = [&](int32_t j, int32_t rows, int key) {
-        const int32_t r = __shfl_sync(0xffffffffu, rows, key >> page_log2);
-        return r == n_rows_cache || j * kKeys + key >= it.len ? n_rows_cache
-                                                              : r + (key & (page - 1));
-      };
-      int32_t rows_k = page_rows(it.tile0);
-      int32_t v_row[4] = {};  // of this lane's box in the four 64-key groups of V
-      for (int32_t j = it.tile0; j <= it.tile1 && ok; ++j) {
-        const int32_t rows_n = page_rows(j + 1);
-        if (j < it.tile1) {  // K of tile j: this CTA's 128 keys, 64 dims a stage
-          const int32_t row = key_row(j, rows_k, k_key);
-#pragma unroll 1
-          for (int a = 0; a < C::kAtoms; ++a) {
-            if (!(ok = W.wait(empty(ring.s), ring.ph ^ 1u))) break;
-            if (arms) mbar_expect_tx(full(ring.s), 2 * kStageBytes);
-            if (k_on)
-              tma_load_pair(k_dst + ring.s * kStageBytes, &k_map, a * 64, row,
-                            lead_full + 8u * ring.s);
-            ring.step();
+  if (warp >= kSoftWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kServiceRegs));
+    if (warp == kProdWarp) {
+      // ==================================================== TMA producer
+      // A stage is 128 keys by two 64-wide column blocks: of K this CTA's keys
+      // and 128 dims, of V 128 keys of either CTA and this CTA's 128 dv.
+      const int32_t n_rows_cache = n_pages << page_log2;  // out of range: zero rows
+      const int nb = 128 >> page_log2;                    // page boxes of a column block
+      const bool on = lane < 2 * nb;
+      const int col = on ? (lane >> (7 - page_log2)) * 64 : 0;     // of this lane's box
+      const int key0 = on ? (lane & (nb - 1)) << page_log2 : 0;    // its first key
+      const uint32_t dst = sStage + (uint32_t)(col / 64) * kAtom + (uint32_t)key0 * 128;
+      const bool arms = rank == 0 && lane == 0;
+      const uint32_t lead_q = at_rank(q_full, 0), lead_full = at_rank(full(0), 0);
+      uint32_t u = 0, nq = 0, nr = 0;  // stages, items, ragged stages so far
+      bool ok = true;
+      while (ok && next(it)) {
+        if (!(ok = W.wait(q_empty, (nq & 1u) ^ 1u))) break;
+        if (arms) mbar_expect_tx(q_full, 2 * C::kQBytes);
+        if (lane < D / 64)
+          tma_load_pair(sQ + lane * 8192, &q_map, lane * 64, it.row0 + (int32_t)rank * 64,
+                        lead_q);
+        ++nq;
+        // first cache row of the page at key `half * 128 + key0` of tile j
+        auto page_row = [&](int32_t j, int half) {
+          const int32_t pos = j * kKeys + half * 128 + key0;
+          if (j >= it.tile1 || pos >= it.len) return n_rows_cache;
+          const int32_t p = __ldg(it.pages + (pos >> page_log2));
+          if (p < 0 || p >= n_pages) {
+            latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
+            return n_rows_cache;
           }
-        }
-        if (j > it.tile0 && ok) {  // V of tile j-1: 64 keys, this CTA's 128 dv a stage
-          const int32_t left0 = it.len - (j - 1) * kKeys;
+          return p << page_log2;
+        };
+        int32_t v_row[2] = {n_rows_cache, n_rows_cache};
+        int32_t n_row[2] = {page_row(it.tile0, 0), page_row(it.tile0, 1)};
+        for (int32_t j = it.tile0; j <= it.tile1 && ok; ++j) {
+          const int32_t c_row[2] = {n_row[0], n_row[1]};
+          n_row[0] = page_row(j + 1, 0);
+          n_row[1] = page_row(j + 1, 1);
+          if (j < it.tile1) {  // K of tile j
+            const int32_t row = rank ? c_row[1] : c_row[0];
 #pragma unroll 1
-          for (int m = 0; m < C::kBlocks && ok; ++m)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              if (!(ok = W.wait(empty(ring.s), ring.ph ^ 1u))) break;
-              const bool ragged = left0 > 64 * g && left0 < 64 * g + 64;
-              uint32_t bar = lead_full + 8u * ring.s;
+            for (int a = 0; a < C::kKStages; ++a, ++u) {
+              const uint32_t s = u % kStages;
+              if (!(ok = W.wait(empty(s), ((u / kStages) & 1u) ^ 1u))) break;
+              if (arms) mbar_expect_tx(full(s), 2 * kStageBytes);
+              if (on)
+                tma_load_pair(dst + s * kStageBytes, &k_map, a * 128 + col, row,
+                              lead_full + 8u * s);
+            }
+          }
+          if (j > it.tile0 && ok) {  // V of tile j-1
+            const int32_t left0 = it.len - (j - 1) * kKeys;
+#pragma unroll 1
+            for (int x = 0; x < C::kVStages; ++x, ++u) {
+              const uint32_t s = u % kStages;
+              const int half = x & 1;
+              if (!(ok = W.wait(empty(s), ((u / kStages) & 1u) ^ 1u))) break;
+              const bool ragged = left0 > 128 * half && left0 < 128 * half + 128;
+              uint32_t bar = lead_full + 8u * s;
               if (ragged) {  // lands at this CTA's barrier: kFixWarp passes it on
                 if (lane == 0) mbar_expect_tx(rag(nr), kStageBytes);
                 __syncwarp();
                 bar = at_rank(rag(nr), rank);
                 ++nr;
               } else if (arms) {
-                mbar_expect_tx(full(ring.s), 2 * kStageBytes);
+                mbar_expect_tx(full(s), 2 * kStageBytes);
               }
-              if (v_on)
-                tma_load_pair(v_dst + ring.s * kStageBytes, &v_map, m * 256 + v_col, v_row[g],
-                              bar);
-              ring.step();
+              if (on)
+                tma_load_pair(dst + s * kStageBytes, &v_map,
+                              (x >> 1) * 256 + (int)rank * 128 + col,
+                              half ? v_row[1] : v_row[0], bar);
             }
+          }
+          v_row[0] = c_row[0];
+          v_row[1] = c_row[1];
         }
-        if (j < it.tile1)
-#pragma unroll
-          for (int g = 0; g < 4; ++g) v_row[g] = key_row(j, rows_k, g * 64 + v_key);
-        rows_k = rows_n;
       }
-    }
-  } else if (warp == kFixWarp) {
-    // ============================================= ragged stages of V
-    // Rows of V past the list's end may hold NaN, which a zero weight does not
-    // cancel: the stage that holds the end is cleared behind it in both CTAs,
-    // and then handed to the leader's barrier.  (Stages wholly past the end
-    // are zero by TMA's out-of-range fill.)
-    uint32_t u = 0, nr = 0;  // stages before this item, ragged stages so far
-    bool ok = true;
-    while (ok && walk.next(it)) {
-      const int32_t last = it.tile1 - 1;            // only the last tile can hold the end
-      const int32_t end = it.len - last * kKeys;    // keys of it that count
-      const int n = it.tile1 - it.tile0;
-      if (end < kKeys && (end & 63) != 0) {
-        // its V stages are the item's last 4 * kBlocks; the end is in group end / 64
+    } else if (warp == kFixWarp) {
+      // =========================================== ragged stages of V
+      // Rows of V past the list's end may hold NaN, which a zero weight does
+      // not cancel: the stage that holds the end is cleared behind it in both
+      // CTAs, and then handed to the leader's barrier.  (Pages wholly past the
+      // end are zero by TMA's out-of-range fill.)
+      uint32_t u = 0, nr = 0;  // stages before this item, ragged stages so far
+      bool ok = true;
+      while (ok && next(it)) {
+        const int32_t last = it.tile1 - 1;          // only the last tile can hold the end
+        const int32_t keys = it.len - last * kKeys;  // keys of it that count
+        u += (uint32_t)(it.tile1 - it.tile0) * (C::kKStages + C::kVStages);
+        if (keys >= kKeys || (keys & 127) == 0) continue;
         for (int m = 0; m < C::kBlocks && ok; ++m, ++nr) {
-          const uint32_t at = u + (uint32_t)n * (C::kAtoms + 4 * C::kBlocks) -
-                              4 * (C::kBlocks - m) + (uint32_t)(end >> 6);
-          const uint32_t s = at % kStages;
+          // its V stages are the item's last; the end is in half keys / 128
+          const uint32_t s = (u - 2 * (C::kBlocks - m) + (uint32_t)(keys >> 7)) % kStages;
           if (!(ok = W.wait(rag(nr), (nr >> 1) & 1u))) break;
-          for (int x = (end & 63) * 8 + lane; x < 64 * 8; x += 32)
+          for (int x = (keys & 127) * 8 + lane; x < 128 * 8; x += 32)
 #pragma unroll
             for (int a = 0; a < 2; ++a)
               asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
-                               sStage + s * kStageBytes + a * 8192 + x * 16),
+                               sStage + s * kStageBytes + a * kAtom + x * 16),
                            "r"(0u)
                            : "memory");
           fence_proxy_async();
@@ -665,130 +665,132 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
       }
-      u += (uint32_t)n * (C::kAtoms + 4 * C::kBlocks);
-    }
-  } else if (warp == kPassWarp) {
-    // ================= this CTA's P complete -> the leader's barrier
-    uint32_t nt = 0;
-    bool ok = true;
-    const uint32_t lead_p = at_rank(p_full, 0);
-    while (ok && walk.next(it)) {
-      // bytes from the other CTA's keys, for this CTA's groups with rows
-      const int mine = (it.n_rows - 64 * (int)rank + kGroupRows - 1) / kGroupRows;
-      const uint32_t bytes = (uint32_t)max(0, min(2, mine)) * (128 * kGroupRows * 2);
-      for (int32_t j = it.tile0; j < it.tile1; ++j, ++nt) {
-        if (lane == 0) mbar_expect_tx(p_in, bytes);
-        if (!(ok = W.wait(p_in, nt & 1u))) break;
-        if (lane == 0) {
-          fence_proxy_async();
-          mbar_signal(lead_p);
-        }
-        __syncwarp();
+    } else if (warp == kPassWarp) {
+      // =============== this CTA's P complete -> the leader's barrier
+      uint32_t nt = 0, np = 0;  // tiles, and times that a P was handed over
+      bool ok = true;
+      const uint32_t lead_p = at_rank(p_full, 0);
+      while (ok && next(it)) {
+        // bytes from the other CTA's keys, for this CTA's groups with rows
+        const int mine = (it.n_rows - 64 * (int)rank + kGroupRows - 1) / kGroupRows;
+        const uint32_t bytes = (uint32_t)max(0, min(2, mine)) * (128 * kGroupRows * 2);
+        for (int32_t j = it.tile0; j < it.tile1 && ok; ++j, ++nt)
+          for (int time = 0; time < 2; ++time) {
+            if (lane == 0) mbar_expect_tx(p_in, bytes);
+            if (!(ok = W.wait(p_in, np & 1u))) break;
+            if (lane == 0) {
+              fence_proxy_async();
+              mbar_signal(lead_p);
+            }
+            __syncwarp();
+            if (!(ok = W.wait(p_done, np & 1u))) break;
+            ++np;
+            if (*redo != nt + 1u) break;
+          }
       }
-    }
-  } else if (warp == kMmaWarp) {
-    // ============================================ MMA issuer (leader only)
-    if (rank == 0 && lane == 0) {
-      Ring<kStages> ring;
-      uint32_t nt = 0, nq = 0;
+    } else if (rank == 0) {
+      // ========================================== MMA issuer (leader only)
+      // The whole warp runs the loop, so that addresses and descriptors stay
+      // uniform; one lane issues.  Shared memory descriptors: an address 16
+      // bytes on is 1 more.
+      uint32_t u = 0, nt = 0, nq = 0, np = 0;
       bool issued = false, ok = true;
-      // descriptors of stage 0, Q and P; an address 16 bytes on is 1 more
-      const uint64_t dK = sdesc_sw128(sStage, 16, 1024), dV = sdesc_sw128(sStage, 8192, 1024);
+      const uint64_t dK = sdesc_sw128(sStage, 16, 1024), dV = sdesc_sw128(sStage, kAtom, 1024);
       const uint64_t dQ = sdesc_sw128(sQ, 16, 1024), dP = sdesc_sw128(sP, 16, 1024);
-      constexpr uint32_t kStep = kStageBytes >> 4;
-      while (ok && walk.next(it)) {
-        if (!(ok = W.wait1(q_full, nq & 1u))) break;
+      const bool one = lane == 0;
+      while (ok && next(it)) {
+        if (!(ok = W.wait(q_full, nq & 1u))) break;
         const int n = it.tile1 - it.tile0;
         for (int j = 0; j <= n && ok; ++j) {
           if (j < n) {
-            const uint32_t t = nt + (uint32_t)j, b = t & 1u;
-            if (!(ok = W.wait1(s_free(b), ((t >> 1) & 1u) ^ 1u))) break;
+            // the softmax has read this S^T buffer's last tile: that tile's PV,
+            // which waited for it, is ahead in this order
+            const uint32_t d = tmem + ((nt + (uint32_t)j) & 1u) * kRows;
             issued = true;
-#pragma unroll 2
-            for (int a = 0; a < C::kAtoms; ++a) {
-              const uint64_t da = dK + ring.s * kStep, db = dQ + (uint32_t)a * 512u;
-              if (!(ok = W.wait1(full(ring.s), ring.ph))) break;
-              tc_fence_after();
 #pragma unroll
-              for (uint32_t kin = 0; kin < 4; ++kin)
-                tc_mma2(tmem + b * kRows, da + 2 * kin, db + 2 * kin, IDESC_S,
-                        (a | kin) != 0 ? 1u : 0u);
-              tc_commit2(empty(ring.s));
-              ring.step();
+            for (uint32_t c = 0; c < C::kKStages; ++c, ++u) {
+              const uint32_t s = u % kStages;
+              if (!(ok = W.wait(full(s), (u / kStages) & 1u))) break;
+              tc_fence_after();
+              const uint64_t da = dK + s * (kStageBytes >> 4);
+              if (one) {
+#pragma unroll
+                for (uint32_t x = 0; x < 8; ++x)  // 64-dim atom x / 4, 16 dims each
+                  tc_mma2(d, da + (x >> 2) * (kAtom >> 4) + (x & 3) * 2,
+                          dQ + (2 * c + (x >> 2)) * 512 + (x & 3) * 2, IDESC_S,
+                          c + x != 0 ? 1u : 0u);
+                tc_commit2(empty(s));
+              }
             }
             if (!ok) break;
-            if (j == n - 1) tc_commit2(q_empty);
-            tc_commit2(s_full(b));
+            if (one) {
+              if (j == n - 1) tc_commit2(q_empty);
+              tc_commit2(s_full((nt + (uint32_t)j) & 1u));
+            }
           }
           if (j >= 1) {
             const uint32_t t = nt + (uint32_t)j - 1u;
-            if (!(ok = W.wait1(p_full, t & 1u))) break;
-            if (j == 1 && !(ok = W.wait1(o_empty, (nq & 1u) ^ 1u))) break;
-#pragma unroll 1
-            for (int m = 0; m < C::kBlocks && ok; ++m)
-#pragma unroll
-              for (uint32_t g = 0; g < 4; ++g) {
-                const uint64_t da = dV + ring.s * kStep;
-                if (!(ok = W.wait1(full(ring.s), ring.ph))) break;
-                tc_fence_after();
-#pragma unroll
-                for (uint32_t ks = 0; ks < 4; ++ks)
-                  tc_mma2(tO + m * kRows, da + 128 * ks, dP + 128 * (4 * g + ks), IDESC_O,
-                          (j > 1 || (g | ks) != 0) ? 1u : 0u);
-                tc_commit2(empty(ring.s));
-                ring.step();
+            if (!(ok = W.wait(p_full, np++ & 1u))) break;
+            if (*objected == t + 1u) {
+              if (one) {
+                for (uint32_t r = 0; r < 2; ++r)
+                  st_cluster_u32(at_rank(smem_u32(misc + 3), r), t + 1u);
+                for (uint32_t r = 0; r < 2; ++r) mbar_release_cluster(at_rank(p_done, r));
               }
+              __syncwarp();
+              if (!(ok = W.wait(p_full, np++ & 1u))) break;
+            }
+            if (j == 1 && !(ok = W.wait(o_empty, (nq & 1u) ^ 1u))) break;
+#pragma unroll
+            for (uint32_t c = 0; c < C::kVStages; ++c, ++u) {
+              const uint32_t s = u % kStages;
+              if (!(ok = W.wait(full(s), (u / kStages) & 1u))) break;
+              tc_fence_after();
+              const uint64_t da = dV + s * (kStageBytes >> 4);
+              if (one) {
+#pragma unroll
+                for (uint32_t x = 0; x < 8; ++x)  // 16 keys each
+                  tc_mma2(tO + (c >> 1) * kRows, da + x * 128, dP + ((c & 1) * 8 + x) * 128,
+                          IDESC_O, j > 1 || (c & 1) + x != 0 ? 1u : 0u);
+                tc_commit2(empty(s));
+              }
+            }
             if (!ok) break;
-            tc_commit2(p_done);
+            if (one) tc_commit2(p_done);
           }
         }
         nt += (uint32_t)n;
         ++nq;
       }
       if (issued) {
-        tc_commit2(done_bar);
+        if (one) tc_commit2(done_bar);
+        __syncwarp();
         drain(done_bar, 0, timeout_ns);
       }
     }
-    __syncwarp();
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // ================================================ softmax, epilogue
     const int quad = warp & 3, g = warp >> 2;  // TMEM lanes, rows 32 g .. 32 g + 31
     const int r0 = kGroupRows * g;
     const int key = (int)rank * 128 + quad * 32 + lane;
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
-    const uint32_t xs_peer = at_rank(xs, peer), xs_own = at_rank(xs, rank);
-    const uint32_t flag_own = at_rank(smem_u32(misc + 2), rank);
-    const uint32_t flag_peer = at_rank(smem_u32(misc + 2), peer);
-    const uint32_t red_own = at_rank(smem_u32(red), rank), red_peer = at_rank(smem_u32(red), peer);
-    const uint32_t l_s_free0 = at_rank(s_free(0), 0), l_o_empty = at_rank(o_empty, 0);
+    const uint32_t xs_peer = at_rank(xs, peer);
+    const uint32_t objected_lead = at_rank(smem_u32(misc + 2), 0);
+    const uint32_t red_peer = at_rank(sP + peer * 128 * 128, peer);  // the other's red
+    const uint32_t l_o_empty = at_rank(o_empty, 0);
     const uint32_t owner = (uint32_t)g >> 1;  // the CTA that holds P of these rows
     const uint32_t p_row = (owner == rank ? sP : at_rank(sP, peer)) + (uint32_t)key * 128u;
     const uint32_t p_in_peer = at_rank(p_in, peer);
     const uint32_t p_c0 = (uint32_t)(g & 1) * 4u, p_sw = (uint32_t)(key & 7);
-    uint32_t nx = 0, ng = 0, nt = 0;
-    // all softmax warps of the pair; `publish`: with this warp's writes to both
-    // CTAs before it
-    auto pair_sync = [&](bool publish) {
-      __syncwarp();
-      if (lane == 0) {
-        if (publish) {
-          mbar_release_cluster(xs_own);
-          mbar_release_cluster(xs_peer);
-        } else {
-          mbar_signal(xs_own);
-          mbar_signal(xs_peer);
-        }
-      }
-      return W.wait(xs, nx++ & 1u);
-    };
+    uint32_t nx = 0, ng = 0, nt = 0, np = 0;
     auto group_sync = [&]() {  // all softmax warps of this CTA
       __syncwarp();
       if (lane == 0) mbar_arrive(grp);
       return W.wait(grp, ng++ & 1u);
     };
     bool ok = true;
-    while (ok && walk.next(it)) {
+    while (ok && next(it)) {
       const bool live = it.n_rows > r0;  // this group has rows that count
       int32_t lim_min = it.len;          // keys that every row of the block sees
       if (it.b >= 0) {
@@ -799,183 +801,217 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       } else if (tid < kRows) {
         lim_s[tid] = it.len;
       }
-      if (tid < kRows) {
-        nm_s[tid] = 0.f;
-        nt_s[tid] = INFINITY;
-      }
+      if (tid < kRows) nm_s[tid] = 0.f;
+      if (!(ok = group_sync())) break;
       float l[32];
 #pragma unroll
       for (int h = 0; h < 32; ++h) l[h] = 0.f;
-      const int n = it.tile1 - it.tile0;
-      for (int j = 0; j < n; ++j, ++nt) {
-        const uint32_t b = nt & 1u;
-        const uint32_t tS = tmem + b * kRows + lane_base + r0;
-        if (!(ok = W.wait(s_full(b), (nt >> 1) & 1u))) break;
-        tc_fence_after();
+      uint32_t pk[16];  // this thread's P, bf16 pairs
+      float over = 0.f;
+
+      // Raise the references to the exact maxima of tile j (S^T in buffer b)
+      // where they are passed by more than `slack`
+      auto raise = [&](int j, uint32_t b, float slack) {
+        const int32_t pos = (it.tile0 + j) * kKeys + key;
+        const bool masked = (it.tile0 + j + 1) * kKeys > lim_min;
+#pragma unroll 1
+        for (int h0 = r0; h0 < r0 + kGroupRows; h0 += 16) {
+          float x[16];
+          uint32_t r[16];
+          if (live) {
+            tmem_ld16(tmem + b * kRows + lane_base + h0, r);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            x[e] = live && (!masked || pos < lim_s[h0 + e])
+                       ? fmaf(__uint_as_float(r[e]), scale_log2, nm_s[h0 + e])
+                       : -INFINITY;
+          const float t = column_reduce<true>(x, lane);
+          const uint32_t at = (uint32_t)(((int)rank * 4 + quad) * kRows + h0 + lane);
+          if (lane < 16) {
+            st_cluster_u32(red_peer + 4 * at, __float_as_uint(t));
+            red[at] = t;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_signal(at_rank(xs, rank));
+          mbar_release_cluster(xs_peer);
+        }
+        if (!W.wait(xs, nx++ & 1u)) return false;
+        if (tid < kRows) {
+          float by = red[tid];
+#pragma unroll
+          for (int w = 1; w < 8; ++w) by = fmaxf(by, red[w * kRows + tid]);
+          const float nm = nm_s[tid];
+          nmo_s[tid] = nm;
+          if (by > slack) nm_s[tid] = nm - by;
+        }
+        return group_sync();
+      };
+      // P of tile j from S^T in buffer b, the largest s - m, and l.  Weights of
+      // 16 rows among which one passes the slack are left out of l, which so
+      // stays finite; the tile is objected to, and the weights are added when
+      // it is visited again (`revisit`) under references that hold them.
+      auto weights = [&](int j, uint32_t b, bool revisit) {
+        over = -INFINITY;
+        if (!live) return;
         const int32_t pos = (it.tile0 + j) * kKeys + key;
         const bool masked = (it.tile0 + j + 1) * kKeys > lim_min;  // uniform
-        // ---- does a score beat its row's maximum by more than 2^8?  (Always
-        // taken on a unit's first tile, whose maxima are not set yet.)
-        bool need = j == 0;
-        if (j > 0 && live) {
-          float over = -INFINITY;
 #pragma unroll
-          for (int h0 = 0; h0 < 32; h0 += 16) {
-            uint32_t r[16];
-            tmem_ld16(tS + h0, r);
-            tmem_wait_ld();
-            const float4* nt4 = reinterpret_cast<const float4*>(nt_s + r0 + h0);
-#pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              const float4 c = nt4[e / 4];
-              const float y[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                const float d = fmaf(__uint_as_float(r[e + x]), scale_log2, y[x]);
-                if (!masked || pos < lim_s[r0 + h0 + e + x]) over = fmaxf(over, d);
-              }
-            }
-          }
-          need = over > 0.f;
-        }
-        need = __any_sync(0xffffffffu, need);
-        // the flag carries the tile's number, so it never needs clearing
-        if (need && lane == 0) {
-          st_cluster_u32(flag_own + 4 * b, nt + 1u);
-          st_cluster_u32(flag_peer + 4 * b, nt + 1u);
-        }
-        if (!(ok = pair_sync(need))) break;
-        // the previous tile's PV is done: O^T is current and P free
-        if (nt > 0 && !(ok = W.wait(p_done, (nt - 1u) & 1u))) break;
-        tc_fence_after();
-        if (flags[b] == nt + 1u) {
-          // ---- exact maxima of the tile, over both CTAs' keys
-          float x[32];
-#pragma unroll
-          for (int h0 = 0; h0 < 32; h0 += 16) {
-            uint32_t r[16];
-            tmem_ld16(tS + h0, r);
-            tmem_wait_ld();
+        for (int h0 = 0; h0 < 32; h0 += 16) {
+          uint32_t r[16];
+          float d[16];
+          tmem_ld16(tmem + b * kRows + lane_base + r0 + h0, r);
+          tmem_wait_ld();
+          float top = -INFINITY, top_old = INFINITY;
+          if (revisit) {
+            top_old = -INFINITY;
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              x[h0 + e] = !masked || pos < lim_s[r0 + h0 + e]
-                              ? __uint_as_float(r[e]) * scale_log2
-                              : -INFINITY;
+              if (!masked || pos < lim_s[r0 + h0 + e])
+                top_old = fmaxf(top_old, fmaf(__uint_as_float(r[e]), scale_log2,
+                                              nmo_s[r0 + h0 + e]));
           }
-          column_reduce<true>(x, lane);
-          const uint32_t at = 4u * (uint32_t)(((int)rank * 4 + quad) * kRows + r0 + lane);
-          st_cluster_u32(red_own + at, __float_as_uint(x[0]));
-          st_cluster_u32(red_peer + at, __float_as_uint(x[0]));
-          if (!(ok = pair_sync(true))) break;
-          if (tid < kRows) {
-            float t = red[tid];
+          const float4* nm4 = reinterpret_cast<const float4*>(nm_s + r0 + h0);
 #pragma unroll
-            for (int w = 1; w < 8; ++w) t = fmaxf(t, red[w * kRows + tid]);
-            const float nt_old = nt_s[tid];
-            const bool first = nt_old == INFINITY;
-            const bool raise = first ? t > -INFINITY : t + nt_old > 0.f;
-            alpha_s[tid] = raise && !first ? ex2(-nm_s[tid] - t) : 1.f;
-            if (raise) {
-              nm_s[tid] = -t;
-              nt_s[tid] = -(t + kSlack);
-            }
+          for (int e = 0; e < 16; e += 4) {
+            const float4 c = nm4[e / 4];
+            d[e] = fmaf(__uint_as_float(r[e]), scale_log2, c.x);
+            d[e + 1] = fmaf(__uint_as_float(r[e + 1]), scale_log2, c.y);
+            d[e + 2] = fmaf(__uint_as_float(r[e + 2]), scale_log2, c.z);
+            d[e + 3] = fmaf(__uint_as_float(r[e + 3]), scale_log2, c.w);
           }
-          if (!(ok = group_sync())) break;
-          if (j > 0) {
-            bool rescale = false;
+          if (masked) {
 #pragma unroll
-            for (int h = 0; h < 32; ++h) {
-              const float a = alpha_s[r0 + h];
-              l[h] *= a;
-              rescale |= a != 1.f;
-            }
-            if (rescale) {  // the same in every lane
-#pragma unroll 1
-              for (int m = 0; m < C::kBlocks; ++m)
-#pragma unroll 1
-                for (int h0 = 0; h0 < 32; h0 += 16) {
-                  uint32_t r[16];
-                  const uint32_t ta = tO + m * kRows + lane_base + r0 + h0;
-                  tmem_ld16(ta, r);
-                  tmem_wait_ld();
-#pragma unroll
-                  for (int e = 0; e < 16; ++e)
-                    r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha_s[r0 + h0 + e]);
-                  tmem_st16(ta, r);
-                }
-              tmem_wait_st();
-            }
+            for (int e = 0; e < 16; ++e)
+              if (pos >= lim_s[r0 + h0 + e]) d[e] = -INFINITY;
           }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            top = fmaxf(top, d[e]);
+            d[e] = ex2(d[e]);
+          }
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) pk[(h0 + e) / 2] = pack_bf16(d[e], d[e + 1]);
+          if (!(top > kSlack) && (!revisit || top_old > kSlack)) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) l[h0 + e] += d[e];
+          }
+          over = fmaxf(over, top);
         }
-        // ---- P = 2^(s - m): row sums, and bf16 P into the CTA that owns the rows
+      };
+      // P into the CTA that owns the rows; what crosses is counted by its bytes
+      auto hand_over = [&]() {
+        tc_fence_before();  // S^T has been read
         if (live) {
 #pragma unroll
-          for (int h0 = 0; h0 < 32; h0 += 16) {
-            uint32_t r[16];
-            tmem_ld16(tS + h0, r);
-            tmem_wait_ld();
-            if (h0 == 16) {  // the last read of this S^T buffer
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_signal(l_s_free0 + 8 * b);
-            }
-            float p[16];
-            const float4* nm4 = reinterpret_cast<const float4*>(nm_s + r0 + h0);
-#pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              const float4 c = nm4[e / 4];
-              p[e] = ex2(fmaf(__uint_as_float(r[e]), scale_log2, c.x));
-              p[e + 1] = ex2(fmaf(__uint_as_float(r[e + 1]), scale_log2, c.y));
-              p[e + 2] = ex2(fmaf(__uint_as_float(r[e + 2]), scale_log2, c.z));
-              p[e + 3] = ex2(fmaf(__uint_as_float(r[e + 3]), scale_log2, c.w));
-            }
-            if (masked) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (pos >= lim_s[r0 + h0 + e]) p[e] = 0.f;
-            }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) l[h0 + e] += p[e];
-#pragma unroll
-            for (int c8 = 0; c8 < 2; ++c8) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = pack_bf16(p[8 * c8 + 2 * e], p[8 * c8 + 2 * e + 1]);
-              const uint32_t a = p_row + (((p_c0 + (uint32_t)(h0 / 8 + c8)) ^ p_sw) << 4);
-              if (owner == rank)
-                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(w[0]),
-                             "r"(w[1]), "r"(w[2]), "r"(w[3])
-                             : "memory");
-              else
-                st_async_v4(a, w, p_in_peer);
-            }
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t a = p_row + (((p_c0 + (uint32_t)c) ^ p_sw) << 4);
+            const uint32_t w[4] = {pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]};
+            if (owner == rank)
+              asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(w[0]),
+                           "r"(w[1]), "r"(w[2]), "r"(w[3])
+                           : "memory");
+            else
+              st_async_v4(a, w, p_in_peer);
           }
-        } else {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_signal(l_s_free0 + 8 * b);
         }
-        if (owner == rank) {  // what crosses is counted by its bytes
+        if (owner == rank) {
           fence_proxy_async();  // P -> the tensor core's reads
           __syncwarp();
           if (lane == 0) mbar_arrive(p_in);
         }
+      };
+      // l and O^T times 2^(m_old - m_new)
+      auto rescale = [&]() {
+        bool any = false;
+#pragma unroll
+        for (int h = 0; h < 32; ++h) {
+          const float a = nm_s[r0 + h] - nmo_s[r0 + h];
+          any |= a != 0.f;
+          l[h] *= ex2(a);
+        }
+        if (!any || !live) return;  // the same in every lane
+#pragma unroll 1
+        for (int c = 0; c < 2 * C::kBlocks; ++c) {
+          uint32_t r[16];
+          const int h0 = r0 + 16 * (c & 1);
+          const uint32_t ta = tO + (c >> 1) * kRows + lane_base + h0;
+          tmem_ld16(ta, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            r[e] = __float_as_uint(__uint_as_float(r[e]) * ex2(nm_s[h0 + e] - nmo_s[h0 + e]));
+          tmem_st16(ta, r);
+        }
+        tmem_wait_st();
+      };
+
+      // Step j: P of tile j, then the verdict on tile j-1 (done, or to be done
+      // again), then tile j's P is handed over; step n: the last verdict alone.
+      const int n = it.tile1 - it.tile0;
+      for (int j = 0; j <= n && ok; ++j) {
+        if (j < n) {
+          if (!(ok = W.wait(s_full(nt & 1u), (nt >> 1) & 1u))) break;
+          tc_fence_after();
+        }
+        int jw = j;            // tile of this pass
+        bool renew = j == 0;   // take its maxima first
+        bool asked = j == 0;   // the verdict is known
+        bool revisit = false;
+        for (;;) {
+          const uint32_t b = (nt + (uint32_t)(jw - j)) & 1u;
+          if (renew) {
+            if (!(ok = raise(jw, b, j == 0 ? -INFINITY : kSlack))) break;
+            if (j > 0) rescale();
+          }
+          if (jw < n) weights(jw, b, revisit);
+          if (!asked) {
+            asked = true;
+            if (!(ok = W.wait(p_done, np++ & 1u))) break;
+            tc_fence_after();
+            if (*redo == nt) {
+              jw = j - 1;
+              renew = revisit = true;
+              continue;
+            }
+          }
+          if (jw == n) break;
+          if (jw == j && __any_sync(0xffffffffu, j > 0 && over > kSlack)) {
+            if (lane == 0) {
+              st_cluster_u32(objected_lead, nt + 1u);
+              fence_cluster();
+            }
+            __syncwarp();
+          }
+          hand_over();
+          if (jw == j) break;
+          if (!(ok = W.wait(p_done, np++ & 1u))) break;
+          tc_fence_after();
+          jw = j;
+          renew = false;
+        }
+        if (j < n) ++nt;
       }
       if (!ok) break;
       // ---- epilogue: m, l and O of this (unit, pair) to its slot
       const int64_t slot = (int64_t)it.unit + pair;
-      if (!(ok = W.wait(p_done, (nt - 1u) & 1u))) break;
-      tc_fence_after();
-      column_reduce<false>(l, lane);
-      lred[quad * kRows + r0 + lane] = l[0];
+#pragma unroll
+      for (int h0 = 0; h0 < 32; h0 += 16) {
+        float x[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = l[h0 + e];
+        const float t = column_reduce<false>(x, lane);
+        if (lane < 16) lred[quad * kRows + r0 + h0 + lane] = t;
+      }
       if (!(ok = group_sync())) break;
       if (DSA_IN_BOUNDS(slot < n_slots, status)) {
         if (tid < it.n_rows) {
           const float sum = lred[tid] + lred[kRows + tid] + lred[2 * kRows + tid] +
                             lred[3 * kRows + tid];
-          view.ml[(slot * 2 + rank) * kRows + tid] =
-              make_float2(nt_s[tid] == INFINITY ? -INFINITY : -nm_s[tid], sum);
+          view.ml[(slot * 2 + rank) * kRows + tid] = make_float2(-nm_s[tid], sum);
         }
         float* out = view.o + slot * (int64_t)(kRows * D);
 #pragma unroll 1
@@ -1083,8 +1119,9 @@ __global__ void __launch_bounds__(128) join_kernel(PlanView view, Lens L,
         if (!DSA_IN_BOUNDS(slot < n_slots, status)) continue;
         const float2 p0 = view.ml[(slot * 2) * kRows + at[x]];
         const float2 p1 = view.ml[(slot * 2 + 1) * kRows + at[x]];
-        mi[e] = p0.x;
         li[e] = p0.y + p1.y;
+        if (li[e] == 0.f) continue;  // no key seen
+        mi[e] = p0.x;
         oi[e] = reinterpret_cast<const float4*>(view.o + (slot * kRows + at[x]) * D)[th];
       }
 #pragma unroll
@@ -1095,7 +1132,7 @@ __global__ void __launch_bounds__(128) join_kernel(PlanView view, Lens L,
       m = top;
 #pragma unroll
       for (int e = 0; e < kJoin; ++e) {
-        if (mi[e] == -INFINITY) continue;  // nothing there, or no key seen
+        if (mi[e] == -INFINITY) continue;  // nothing there
         const float w = ex2(mi[e] - top);
         l = fmaf(w, li[e], l);
         acc.x = fmaf(w, oi[e].x, acc.x);

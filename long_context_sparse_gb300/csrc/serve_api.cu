@@ -144,7 +144,7 @@ dsa_status_t dsa_prefix_attn(const dsa_serve_config_t* cfg, const void* q,
   const ServeShape sh = serve_shape(cfg);
   CUtensorMap qm, km, vm;
   const uint64_t cache_rows = (uint64_t)sh.n_pages * sh.page, d = (uint64_t)sh.D;
-  const uint32_t box = sh.page < 64 ? sh.page : 64;
+  const uint32_t box = (uint32_t)sh.page;
   if ((st = encode_2d(&qm, q, (uint64_t)(sh.T * sh.H), d, 64)) != DSA_OK) return st;
   if ((st = encode_2d(&km, k_pages, cache_rows, d, box)) != DSA_OK) return st;
   if ((st = encode_2d(&vm, v_pages ? v_pages : k_pages, cache_rows, d, box)) != DSA_OK)
