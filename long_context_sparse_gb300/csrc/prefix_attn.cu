@@ -60,7 +60,7 @@ constexpr int kProdWarp = 16, kFixWarp = 17, kMmaWarp = 18, kPassWarp = 19;
 constexpr int kThreads = 32 * 20;
 constexpr uint32_t kAtom = 16384;    // 128 rows of 128 bytes
 constexpr uint32_t kStageBytes = 2 * kAtom;
-constexpr int kSoftRegs = 104, kServiceRegs = 64;  // of the 96 that each thread starts with
+constexpr int kSoftRegs = 112, kServiceRegs = 32;  // of the 96 that each thread starts with
 static_assert(32 * (16 * kSoftRegs + 4 * kServiceRegs) <= kThreads * 96, "register split");
 constexpr float kSlack = 20.0f;      // log2 headroom before a row's reference is raised
 
@@ -242,6 +242,15 @@ struct Share {
   int32_t first_b;       // request at start, past the prefix units
 };
 
+// What the softmax warps need of an item; n = 0: no more.
+struct Post {
+  int32_t tile0, n;     // first tile, tiles
+  int32_t len;          // keys of the list
+  int32_t lim_min;      // keys that every row of the block sees
+  int32_t n_rows, unit;
+  int32_t b, rel0;
+};
+
 // Walks the units of one pair's share, in order.
 struct Walk {
   const Share* sh;
@@ -326,6 +335,17 @@ __device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity, 
       : "memory");
   return ok != 0;
 }
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ void fence_cluster() {
   asm volatile("fence.acq_rel.cluster;" ::: "memory");
 }
@@ -371,6 +391,26 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // Bounded waits of the pair: as Waiter, with cluster scope; a failure stops
 // both CTAs.  wait() is for whole warps and gives every lane the same answer,
 // so that no lane is left behind at a warp's barrier; wait1() is one thread's.
@@ -402,6 +442,8 @@ struct PairWaiter {
 // Shared memory at D = 512: Q 64 KB, P 32 KB, four stages of 32 KB, 2 KB of
 // row constants and barriers, 1 KB to align: all of the 227 KB.
 constexpr int kStages = 4;
+constexpr int kBars = 28;
+constexpr uint32_t kPeek = 5;  // MMAs of a stage before the look at the next one
 
 template <int D>
 struct PCfg {
@@ -459,9 +501,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   float* nmo_s = nm_s + kRows;                            // [row] -m before it was last raised
   int32_t* lim_s = reinterpret_cast<int32_t*>(nmo_s + kRows);  // [row] keys that it sees
   uint64_t* bars = reinterpret_cast<uint64_t*>(lim_s + kRows);
-  uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 24);     // abort, tmem, objected, redo
+  uint32_t* misc = reinterpret_cast<uint32_t*>(bars + kBars);  // abort, tmem, objected, redo
   Share* share = reinterpret_cast<Share*>(misc + 4);
-  static_assert(3 * kRows * 4 + 24 * 8 + 16 + sizeof(Share) <= C::kTail, "tail");
+  Post* posts = reinterpret_cast<Post*>(share + 1);            // [2]
+  static_assert(3 * kRows * 4 + kBars * 8 + 16 + sizeof(Share) + 2 * sizeof(Post) <= C::kTail,
+                "tail");
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const uint32_t rank = cluster_rank(), peer = rank ^ 1u;
@@ -485,7 +529,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t done_bar = bx + 80;
   auto rag = [&](uint32_t r) { return bx + 88 + 8 * (r & 1u); };      // own ragged V stage
   auto fixed = [&](uint32_t r) { return bx + 104 + 8 * (r & 1u); };   // leader: the other's is
-  static_assert(2 * kStages + 15 <= 24, "barriers");
+  auto post_full = [&](uint32_t i) { return bx + 120 + 8 * (i & 1u); };
+  auto post_free = [&](uint32_t i) { return bx + 136 + 8 * (i & 1u); };
+  static_assert(2 * kStages + 19 <= kBars, "barriers");
   // tile number + 1 of the last tile objected to (leader), to be done again
   volatile uint32_t *objected = misc + 2, *redo = misc + 3;
   const PairWaiter W{misc, at_rank(smem_u32(misc), peer), status, timeout_ns};
@@ -501,6 +547,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(s_full(b), 1);
       mbar_init(rag(b), 1);
       mbar_init(fixed(b), 1);
+      mbar_init(post_full(b), 1);
+      mbar_init(post_free(b), kSoftWarps);
     }
     mbar_init(p_in, kSoftWarps / 2 + 1);
     mbar_init(p_full, 2);
@@ -575,11 +623,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tma_load_pair(sQ + lane * 8192, &q_map, lane * 64, it.row0 + (int32_t)rank * 64,
                         lead_q);
         ++nq;
-        // first cache row of the page at key `half * 128 + key0` of tile j
-        auto page_row = [&](int32_t j, int half) {
+        // page of key `half * 128 + key0` of tile j (0 where nothing is read)
+        auto page_at = [&](int32_t j, int half) {
           const int32_t pos = j * kKeys + half * 128 + key0;
-          if (j >= it.tile1 || pos >= it.len) return n_rows_cache;
-          const int32_t p = __ldg(it.pages + (pos >> page_log2));
+          return j < it.tile1 && pos < it.len ? __ldg(it.pages + (pos >> page_log2)) : 0;
+        };
+        // its first cache row, or out of range past the end
+        auto row_of = [&](int32_t j, int half, int32_t p) {
+          if (j >= it.tile1 || j * kKeys + half * 128 + key0 >= it.len) return n_rows_cache;
           if (p < 0 || p >= n_pages) {
             latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
             return n_rows_cache;
@@ -587,11 +638,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           return p << page_log2;
         };
         int32_t v_row[2] = {n_rows_cache, n_rows_cache};
-        int32_t n_row[2] = {page_row(it.tile0, 0), page_row(it.tile0, 1)};
+        int32_t page[2] = {page_at(it.tile0, 0), page_at(it.tile0, 1)};
         for (int32_t j = it.tile0; j <= it.tile1 && ok; ++j) {
-          const int32_t c_row[2] = {n_row[0], n_row[1]};
-          n_row[0] = page_row(j + 1, 0);
-          n_row[1] = page_row(j + 1, 1);
+          const int32_t c_row[2] = {row_of(j, 0, page[0]), row_of(j, 1, page[1])};
+          page[0] = page_at(j + 1, 0);  // looked at in the next round
+          page[1] = page_at(j + 1, 1);
           if (j < it.tile1) {  // K of tile j
             const int32_t row = rank ? c_row[1] : c_row[0];
 #pragma unroll 1
@@ -666,15 +717,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
     } else if (warp == kPassWarp) {
-      // =============== this CTA's P complete -> the leader's barrier
-      uint32_t nt = 0, np = 0;  // tiles, and times that a P was handed over
+      // ===== items to the softmax warps; this CTA's P complete -> the leader
+      uint32_t nt = 0, np = 0, ni = 0;  // tiles, times that a P was handed over, items
       bool ok = true;
       const uint32_t lead_p = at_rank(p_full, 0);
-      while (ok && next(it)) {
+      Post cur, nxt;
+      auto post = [&]() {  // the next item, one ahead of its tiles
+        nxt.n = 0;
+        if (next(it)) {
+          nxt = Post{it.tile0, it.tile1 - it.tile0, it.len, it.len, it.n_rows, it.unit, it.b,
+                     it.rel0};
+          if (it.b >= 0) nxt.lim_min = row_limit(req_shape(L, it.b), L.H, it.rel0);
+        }
+        if (!W.wait(post_free(ni), ((ni >> 1) & 1u) ^ 1u)) return false;
+        if (lane == 0) {
+          posts[ni & 1u] = nxt;
+          mbar_arrive(post_full(ni));
+        }
+        __syncwarp();
+        ++ni;
+        return true;
+      };
+      ok = post();
+      while (ok && nxt.n > 0) {
+        cur = nxt;
+        if (!(ok = post())) break;
         // bytes from the other CTA's keys, for this CTA's groups with rows
-        const int mine = (it.n_rows - 64 * (int)rank + kGroupRows - 1) / kGroupRows;
+        const int mine = (cur.n_rows - 64 * (int)rank + kGroupRows - 1) / kGroupRows;
         const uint32_t bytes = (uint32_t)max(0, min(2, mine)) * (128 * kGroupRows * 2);
-        for (int32_t j = it.tile0; j < it.tile1 && ok; ++j, ++nt)
+        for (int32_t j = 0; j < cur.n && ok; ++j, ++nt)
           for (int time = 0; time < 2; ++time) {
             if (lane == 0) mbar_expect_tx(p_in, bytes);
             if (!(ok = W.wait(p_in, np & 1u))) break;
@@ -691,13 +762,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (rank == 0) {
       // ========================================== MMA issuer (leader only)
       // The whole warp runs the loop, so that addresses and descriptors stay
-      // uniform; one lane issues.  Shared memory descriptors: an address 16
-      // bytes on is 1 more.
+      // uniform; one lane issues.  The queue of the tensor core is short: what
+      // the warp does between two stages leaves the pipe idle (a look at a
+      // barrier is about 100 cycles), so the next stage's barrier is looked at
+      // amid the MMAs of this one.  Descriptors: an address 16 bytes on is 1
+      // more.
       uint32_t u = 0, nt = 0, nq = 0, np = 0;
-      bool issued = false, ok = true;
+      bool issued = false, ok = true, ready = false;
       const uint64_t dK = sdesc_sw128(sStage, 16, 1024), dV = sdesc_sw128(sStage, kAtom, 1024);
       const uint64_t dQ = sdesc_sw128(sQ, 16, 1024), dP = sdesc_sw128(sP, 16, 1024);
       const bool one = lane == 0;
+      // eight MMAs of a stage: mma(descriptor offset of the stage, x)
+      auto stage = [&](auto mma) {
+        const uint32_t s = u % kStages;
+        if (!ready && !W.wait(full(s), (u / kStages) & 1u)) return false;
+        tc_fence_after();
+        ++u;
+        if (one) {
+#pragma unroll
+          for (uint32_t x = 0; x < kPeek; ++x) mma(s * (kStageBytes >> 4), x);
+        }
+        ready = __all_sync(0xffffffffu, mbar_test(full(u % kStages), (u / kStages) & 1u));
+        if (one) {
+#pragma unroll
+          for (uint32_t x = kPeek; x < 8; ++x) mma(s * (kStageBytes >> 4), x);
+          tc_commit2(empty(s));
+        }
+        return true;
+      };
       while (ok && next(it)) {
         if (!(ok = W.wait(q_full, nq & 1u))) break;
         const int n = it.tile1 - it.tile0;
@@ -708,20 +800,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t d = tmem + ((nt + (uint32_t)j) & 1u) * kRows;
             issued = true;
 #pragma unroll
-            for (uint32_t c = 0; c < C::kKStages; ++c, ++u) {
-              const uint32_t s = u % kStages;
-              if (!(ok = W.wait(full(s), (u / kStages) & 1u))) break;
-              tc_fence_after();
-              const uint64_t da = dK + s * (kStageBytes >> 4);
-              if (one) {
-#pragma unroll
-                for (uint32_t x = 0; x < 8; ++x)  // 64-dim atom x / 4, 16 dims each
-                  tc_mma2(d, da + (x >> 2) * (kAtom >> 4) + (x & 3) * 2,
-                          dQ + (2 * c + (x >> 2)) * 512 + (x & 3) * 2, IDESC_S,
-                          c + x != 0 ? 1u : 0u);
-                tc_commit2(empty(s));
-              }
-            }
+            for (uint32_t c = 0; c < C::kKStages && ok; ++c)
+              ok = stage([&](uint32_t at, uint32_t x) {  // 64-dim atom x / 4, 16 dims each
+                tc_mma2(d, dK + at + (x >> 2) * (kAtom >> 4) + (x & 3) * 2,
+                        dQ + (2 * c + (x >> 2)) * 512 + (x & 3) * 2, IDESC_S,
+                        c + x != 0 ? 1u : 0u);
+              });
             if (!ok) break;
             if (one) {
               if (j == n - 1) tc_commit2(q_empty);
@@ -742,19 +826,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             if (j == 1 && !(ok = W.wait(o_empty, (nq & 1u) ^ 1u))) break;
 #pragma unroll
-            for (uint32_t c = 0; c < C::kVStages; ++c, ++u) {
-              const uint32_t s = u % kStages;
-              if (!(ok = W.wait(full(s), (u / kStages) & 1u))) break;
-              tc_fence_after();
-              const uint64_t da = dV + s * (kStageBytes >> 4);
-              if (one) {
-#pragma unroll
-                for (uint32_t x = 0; x < 8; ++x)  // 16 keys each
-                  tc_mma2(tO + (c >> 1) * kRows, da + x * 128, dP + ((c & 1) * 8 + x) * 128,
-                          IDESC_O, j > 1 || (c & 1) + x != 0 ? 1u : 0u);
-                tc_commit2(empty(s));
-              }
-            }
+            for (uint32_t c = 0; c < C::kVStages && ok; ++c)
+              ok = stage([&](uint32_t at, uint32_t x) {  // 16 keys each
+                tc_mma2(tO + (c >> 1) * kRows, dV + at + x * 128, dP + ((c & 1) * 8 + x) * 128,
+                        IDESC_O, j > 1 || (c & 1) + x != 0 ? 1u : 0u);
+              });
             if (!ok) break;
             if (one) tc_commit2(p_done);
           }
@@ -775,14 +851,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int r0 = kGroupRows * g;
     const int key = (int)rank * 128 + quad * 32 + lane;
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
-    const uint32_t xs_peer = at_rank(xs, peer);
-    const uint32_t objected_lead = at_rank(smem_u32(misc + 2), 0);
-    const uint32_t red_peer = at_rank(sP + peer * 128 * 128, peer);  // the other's red
-    const uint32_t l_o_empty = at_rank(o_empty, 0);
     const uint32_t owner = (uint32_t)g >> 1;  // the CTA that holds P of these rows
     const uint32_t p_row = (owner == rank ? sP : at_rank(sP, peer)) + (uint32_t)key * 128u;
     const uint32_t p_in_peer = at_rank(p_in, peer);
     const uint32_t p_c0 = (uint32_t)(g & 1) * 4u, p_sw = (uint32_t)(key & 7);
+    const uint64_t scale2 = pair2(scale_log2, scale_log2);
     uint32_t nx = 0, ng = 0, nt = 0, np = 0;
     auto group_sync = [&]() {  // all softmax warps of this CTA
       __syncwarp();
@@ -790,30 +863,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       return W.wait(grp, ng++ & 1u);
     };
     bool ok = true;
-    while (ok && next(it)) {
-      const bool live = it.n_rows > r0;  // this group has rows that count
-      int32_t lim_min = it.len;          // keys that every row of the block sees
-      if (it.b >= 0) {
-        const ReqShape r = req_shape(L, it.b);
-        lim_min = row_limit(r, L.H, it.rel0);
-        if (tid < kRows)
-          lim_s[tid] = min(it.len, row_limit(r, L.H, it.rel0 + min(tid, it.n_rows - 1)));
-      } else if (tid < kRows) {
-        lim_s[tid] = it.len;
+    for (uint32_t ni = 0; ok; ++ni) {
+      if (!(ok = W.wait(post_full(ni), (ni >> 1) & 1u))) break;
+      const volatile Post* post = posts + (ni & 1u);
+      const int n = post->n;
+      if (n == 0) break;
+      const int32_t tile0 = post->tile0, lim_min = post->lim_min;
+      const bool live = post->n_rows > r0;  // this group has rows that count
+      if (tid < kRows) {
+        const int32_t len = post->len, pb = post->b;
+        lim_s[tid] = pb < 0 ? len
+                            : min(len, row_limit(req_shape(L, pb), L.H,
+                                                 post->rel0 + min(tid, post->n_rows - 1)));
+        nm_s[tid] = 0.f;
       }
-      if (tid < kRows) nm_s[tid] = 0.f;
       if (!(ok = group_sync())) break;
-      float l[32];
+      uint64_t l[16];  // this thread's row sums, in pairs
 #pragma unroll
-      for (int h = 0; h < 32; ++h) l[h] = 0.f;
+      for (int h = 0; h < 16; ++h) l[h] = 0ull;
       uint32_t pk[16];  // this thread's P, bf16 pairs
       float over = 0.f;
 
       // Raise the references to the exact maxima of tile j (S^T in buffer b)
       // where they are passed by more than `slack`
       auto raise = [&](int j, uint32_t b, float slack) {
-        const int32_t pos = (it.tile0 + j) * kKeys + key;
-        const bool masked = (it.tile0 + j + 1) * kKeys > lim_min;
+        const int32_t pos = (tile0 + j) * kKeys + key;
+        const bool masked = (tile0 + j + 1) * kKeys > lim_min;
 #pragma unroll 1
         for (int h0 = r0; h0 < r0 + kGroupRows; h0 += 16) {
           float x[16];
@@ -830,14 +905,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const float t = column_reduce<true>(x, lane);
           const uint32_t at = (uint32_t)(((int)rank * 4 + quad) * kRows + h0 + lane);
           if (lane < 16) {
-            st_cluster_u32(red_peer + 4 * at, __float_as_uint(t));
+            st_cluster_u32(at_rank(sP + peer * 128 * 128, peer) + 4 * at, __float_as_uint(t));
             red[at] = t;
           }
         }
         __syncwarp();
         if (lane == 0) {
           mbar_signal(at_rank(xs, rank));
-          mbar_release_cluster(xs_peer);
+          mbar_release_cluster(at_rank(xs, peer));
         }
         if (!W.wait(xs, nx++ & 1u)) return false;
         if (tid < kRows) {
@@ -850,56 +925,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         return group_sync();
       };
-      // P of tile j from S^T in buffer b, the largest s - m, and l.  Weights of
-      // 16 rows among which one passes the slack are left out of l, which so
+      // P of tile j from S^T in buffer b, the largest s - m, and l.  Weights of 8
+      // rows among which one passes the slack are left out of l, which so
       // stays finite; the tile is objected to, and the weights are added when
       // it is visited again (`revisit`) under references that hold them.
       auto weights = [&](int j, uint32_t b, bool revisit) {
         over = -INFINITY;
         if (!live) return;
-        const int32_t pos = (it.tile0 + j) * kKeys + key;
-        const bool masked = (it.tile0 + j + 1) * kKeys > lim_min;  // uniform
+        const int32_t pos = (tile0 + j) * kKeys + key;
+        const bool masked = (tile0 + j + 1) * kKeys > lim_min;  // uniform
 #pragma unroll
-        for (int h0 = 0; h0 < 32; h0 += 16) {
-          uint32_t r[16];
-          float d[16];
-          tmem_ld16(tmem + b * kRows + lane_base + r0 + h0, r);
+        for (int h0 = 0; h0 < 32; h0 += 8) {
+          uint32_t r[8];
+          float d[8];
+          tmem_ld8(tmem + b * kRows + lane_base + r0 + h0, r);
           tmem_wait_ld();
-          float top = -INFINITY, top_old = INFINITY;
-          if (revisit) {
-            top_old = -INFINITY;
+          const ulonglong2* nm4 = reinterpret_cast<const ulonglong2*>(nm_s + r0 + h0);
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (!masked || pos < lim_s[r0 + h0 + e])
-                top_old = fmaxf(top_old, fmaf(__uint_as_float(r[e]), scale_log2,
-                                              nmo_s[r0 + h0 + e]));
-          }
-          const float4* nm4 = reinterpret_cast<const float4*>(nm_s + r0 + h0);
-#pragma unroll
-          for (int e = 0; e < 16; e += 4) {
-            const float4 c = nm4[e / 4];
-            d[e] = fmaf(__uint_as_float(r[e]), scale_log2, c.x);
-            d[e + 1] = fmaf(__uint_as_float(r[e + 1]), scale_log2, c.y);
-            d[e + 2] = fmaf(__uint_as_float(r[e + 2]), scale_log2, c.z);
-            d[e + 3] = fmaf(__uint_as_float(r[e + 3]), scale_log2, c.w);
+          for (int e = 0; e < 8; e += 4) {
+            const ulonglong2 c = nm4[e / 4];
+            unpair2(fma2(pair2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), scale2, c.x),
+                    d[e], d[e + 1]);
+            unpair2(fma2(pair2(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])), scale2, c.y),
+                    d[e + 2], d[e + 3]);
           }
           if (masked) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
+            for (int e = 0; e < 8; ++e)
               if (pos >= lim_s[r0 + h0 + e]) d[e] = -INFINITY;
           }
+          float top = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            top = fmaxf(top, d[e]);
-            d[e] = ex2(d[e]);
-          }
+          for (int e = 0; e < 8; e += 2) top = fmaxf(top, fmaxf(d[e], d[e + 1]));
+          bool add = !(top > kSlack);
+          if (revisit) {  // those that were left out under the references before
+            float old = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) pk[(h0 + e) / 2] = pack_bf16(d[e], d[e + 1]);
-          if (!(top > kSlack) && (!revisit || top_old > kSlack)) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) l[h0 + e] += d[e];
+            for (int e = 0; e < 8; ++e)
+              if (!masked || pos < lim_s[r0 + h0 + e])
+                old = fmaxf(old, fmaf(__uint_as_float(r[e]), scale_log2, nmo_s[r0 + h0 + e]));
+            add = add && old > kSlack;
           }
           over = fmaxf(over, top);
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            d[e] = ex2(d[e]);
+            d[e + 1] = ex2(d[e + 1]);
+            pk[(h0 + e) / 2] = pack_bf16(d[e], d[e + 1]);
+          }
+          if (add) {
+#pragma unroll
+            for (int e = 0; e < 8; e += 2)
+              l[(h0 + e) / 2] = add2(l[(h0 + e) / 2], pair2(d[e], d[e + 1]));
+          }
         }
       };
       // P into the CTA that owns the rows; what crosses is counted by its bytes
@@ -928,10 +1006,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       auto rescale = [&]() {
         bool any = false;
 #pragma unroll
-        for (int h = 0; h < 32; ++h) {
-          const float a = nm_s[r0 + h] - nmo_s[r0 + h];
-          any |= a != 0.f;
-          l[h] *= ex2(a);
+        for (int h = 0; h < 16; ++h) {
+          const float a = nm_s[r0 + 2 * h] - nmo_s[r0 + 2 * h];
+          const float c = nm_s[r0 + 2 * h + 1] - nmo_s[r0 + 2 * h + 1];
+          any |= a != 0.f || c != 0.f;
+          float x, y;
+          unpair2(l[h], x, y);
+          l[h] = pair2(x * ex2(a), y * ex2(c));
         }
         if (!any || !live) return;  // the same in every lane
 #pragma unroll 1
@@ -951,7 +1032,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
       // Step j: P of tile j, then the verdict on tile j-1 (done, or to be done
       // again), then tile j's P is handed over; step n: the last verdict alone.
-      const int n = it.tile1 - it.tile0;
       for (int j = 0; j <= n && ok; ++j) {
         if (j < n) {
           if (!(ok = W.wait(s_full(nt & 1u), (nt >> 1) & 1u))) break;
@@ -981,7 +1061,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (jw == n) break;
           if (jw == j && __any_sync(0xffffffffu, j > 0 && over > kSlack)) {
             if (lane == 0) {
-              st_cluster_u32(objected_lead, nt + 1u);
+              st_cluster_u32(at_rank(smem_u32(misc + 2), 0), nt + 1u);
               fence_cluster();
             }
             __syncwarp();
@@ -997,18 +1077,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // ---- epilogue: m, l and O of this (unit, pair) to its slot
-      const int64_t slot = (int64_t)it.unit + pair;
+      const int64_t slot = (int64_t)post->unit + pair;
+      const int n_rows = post->n_rows;
 #pragma unroll
       for (int h0 = 0; h0 < 32; h0 += 16) {
         float x[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = l[h0 + e];
+        for (int e = 0; e < 16; e += 2) unpair2(l[(h0 + e) / 2], x[e], x[e + 1]);
         const float t = column_reduce<false>(x, lane);
         if (lane < 16) lred[quad * kRows + r0 + h0 + lane] = t;
       }
       if (!(ok = group_sync())) break;
       if (DSA_IN_BOUNDS(slot < n_slots, status)) {
-        if (tid < it.n_rows) {
+        if (tid < n_rows) {
           const float sum = lred[tid] + lred[kRows + tid] + lred[2 * kRows + tid] +
                             lred[3 * kRows + tid];
           view.ml[(slot * 2 + rank) * kRows + tid] = make_float2(-nm_s[tid], sum);
@@ -1019,19 +1100,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int dv = m * 256 + (int)rank * 128 + quad * 32 + lane;
           if (dv >= D) break;  // D = 128: the second CTA's lanes are padding
 #pragma unroll 1
-          for (int h0 = r0; h0 < min(r0 + kGroupRows, it.n_rows); h0 += 16) {
+          for (int h0 = r0; h0 < min(r0 + kGroupRows, n_rows); h0 += 16) {
             uint32_t r[16];
             tmem_ld16(tO + m * kRows + lane_base + h0, r);
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              if (h0 + e < it.n_rows) out[(int64_t)(h0 + e) * D + dv] = __uint_as_float(r[e]);
+              if (h0 + e < n_rows) out[(int64_t)(h0 + e) * D + dv] = __uint_as_float(r[e]);
           }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_signal(l_o_empty);
+      if (lane == 0) {
+        mbar_signal(at_rank(o_empty, 0));
+        mbar_arrive(post_free(ni));
+      }
     }
   }
 
