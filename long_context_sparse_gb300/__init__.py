@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import math
 import os
 import threading
@@ -160,6 +161,11 @@ class ServeConfig:
         return _CServeConfig(self.n_pages, self.max_tokens, self.page_size,
                              self.batch, self.max_blocks, self.attn_heads,
                              self.d_qk, self.d_v, float(self.sm_scale))
+
+    @functools.cached_property
+    def _ref(self):
+        """The C struct by reference (the calls read it only)."""
+        return ctypes.byref(self.c())
 
 
 def config_for(wl: Workload, **over) -> Config:
@@ -832,20 +838,47 @@ def serve_workspace(cfg: ServeConfig, which: int, device="cuda") -> torch.Tensor
     return ws
 
 
+# A serving step is a few small calls, so the host's share of each counts:
+# tensors that are as they should be pass one expression, pointers go as
+# integers, and the C struct of a config is built once.
+
+
+def _check_tensor(t, name, dtype, shape, dev):
+    """_need, said briefly when all is well."""
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.device == dev
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, name, dtype, shape, dev)
+    return t.data_ptr()
+
+
+def _first_tensor(t, name, dtype, shape):
+    """As _check_tensor for the tensor that says which device a call is on."""
+    _need(t, name, dtype, shape)
+    return t.device
+
+
 def _serve_ws(cfg, which, ws, dev):
     if ws is None:
         return serve_workspace(cfg, which, dev)
-    _need(ws, "ws", torch.uint8, device=dev)
+    if ws.dtype is not torch.uint8 or ws.device != dev or not ws.is_contiguous():
+        _need(ws, "ws", torch.uint8, device=dev)
     return ws
 
 
 def _serve_call(name, dev, *args):
     """One C call on `dev`'s current stream, with `dev` the current device."""
+    fn = getattr(_lib or _load(), name)
     if torch.cuda.current_device() == dev.index:
-        _check(getattr(_load(), name)(*args, _stream(dev)), name)
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     else:
         with torch.cuda.device(dev):
-            _check(getattr(_load(), name)(*args, _stream(dev)), name)
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc:
+        _check(rc, name)
 
 
 class PageTables(typing.NamedTuple):
@@ -864,29 +897,24 @@ def build_page_tables(cfg: ServeConfig, cached_lens, new_lens, free_pages,
     free_pages [n_free], in request order, and are entered in block_table
     [batch, max_blocks] in place (other entries stay).  All int32."""
     B, T, i32 = cfg.batch, cfg.max_tokens, torch.int32
-    _need(cached_lens, "cached_lens", i32, (B,))
-    dev = cached_lens.device
-    _need(new_lens, "new_lens", i32, (B,), dev)
-    _need(free_pages, "free_pages", i32, device=dev)
-    if free_pages.dim() != 1:
-        raise ValueError("free_pages must be [n_free]")
-    _need(block_table, "block_table", i32, (B, cfg.max_blocks), dev)
+    dev = _first_tensor(cached_lens, "cached_lens", i32, (B,))
+    p_new = _check_tensor(new_lens, "new_lens", i32, (B,), dev)
+    n_free = free_pages.numel() if isinstance(free_pages, torch.Tensor) else 0
+    p_free = _check_tensor(free_pages, "free_pages", i32, (n_free,), dev)
+    p_table = _check_tensor(block_table, "block_table", i32, (B, cfg.max_blocks), dev)
     if out is None:
         out = PageTables(block_table, *(torch.empty(n, dtype=i32, device=dev)
                                         for n in (T, B + 1, B, 1)))
     elif out.block_table is not block_table:
         raise ValueError("out.block_table must be block_table")
-    else:
-        _need(out.slot_map, "slot_map", i32, (T,), dev)
-        _need(out.cu_tokens, "cu_tokens", i32, (B + 1,), dev)
-        _need(out.seq_lens, "seq_lens", i32, (B,), dev)
-        _need(out.pages_taken, "pages_taken", i32, (1,), dev)
+    p_slots = _check_tensor(out.slot_map, "slot_map", i32, (T,), dev)
+    p_cu = _check_tensor(out.cu_tokens, "cu_tokens", i32, (B + 1,), dev)
+    p_seq = _check_tensor(out.seq_lens, "seq_lens", i32, (B,), dev)
+    p_taken = _check_tensor(out.pages_taken, "pages_taken", i32, (1,), dev)
     ws = _serve_ws(cfg, SERVE_WS_TABLES, ws, dev)
-    cc = cfg.c()
-    _serve_call("dsa_build_page_tables", dev, ctypes.byref(cc), _ptr(cached_lens),
-                _ptr(new_lens), _ptr(free_pages), free_pages.numel(),
-                _ptr(block_table), _ptr(out.slot_map), _ptr(out.cu_tokens),
-                _ptr(out.seq_lens), _ptr(out.pages_taken), _ptr(ws), ws.numel())
+    _serve_call("dsa_build_page_tables", dev, cfg._ref, cached_lens.data_ptr(), p_new,
+                p_free, n_free, p_table, p_slots, p_cu, p_seq, p_taken, ws.data_ptr(),
+                ws.numel())
     return out
 
 
@@ -896,20 +924,18 @@ def append_cache(cfg: ServeConfig, slot_map, k_new, k_pages, v_new=None,
     of k_pages (and v_pages) [n_pages, page_size, d], in place; slots below
     0 are skipped, the others must be distinct.  Without v: K = V."""
     T, bf = cfg.max_tokens, torch.bfloat16
-    _need(slot_map, "slot_map", torch.int32, (T,))
-    dev = slot_map.device
-    _need(k_new, "k_new", bf, (T, cfg.d_qk), dev)
-    _need(k_pages, "k_pages", bf, (cfg.n_pages, cfg.page_size, cfg.d_qk), dev)
+    dev = _first_tensor(slot_map, "slot_map", torch.int32, (T,))
+    p_new = _check_tensor(k_new, "k_new", bf, (T, cfg.d_qk), dev)
+    p_k = _check_tensor(k_pages, "k_pages", bf, (cfg.n_pages, cfg.page_size, cfg.d_qk), dev)
     if (v_new is None) != (v_pages is None):
         raise ValueError("v_new and v_pages go together")
+    p_vnew = p_v = None
     if v_new is not None:
-        _need(v_new, "v_new", bf, (T, cfg.d_v), dev)
-        _need(v_pages, "v_pages", bf, (cfg.n_pages, cfg.page_size, cfg.d_v), dev)
+        p_vnew = _check_tensor(v_new, "v_new", bf, (T, cfg.d_v), dev)
+        p_v = _check_tensor(v_pages, "v_pages", bf, (cfg.n_pages, cfg.page_size, cfg.d_v), dev)
     ws = _serve_ws(cfg, SERVE_WS_APPEND, ws, dev)
-    cc = cfg.c()
-    _serve_call("dsa_append_cache", dev, ctypes.byref(cc), _ptr(slot_map),
-                _ptr(k_new), _ptr(v_new), _ptr(k_pages), _ptr(v_pages), _ptr(ws),
-                ws.numel())
+    _serve_call("dsa_append_cache", dev, cfg._ref, slot_map.data_ptr(), p_new, p_vnew, p_k,
+                p_v, ws.data_ptr(), ws.numel())
 
 
 def prefix_attn(cfg: ServeConfig, q, k_pages, prefix_table, prefix_len: int,
@@ -925,33 +951,33 @@ def prefix_attn(cfg: ServeConfig, q, k_pages, prefix_table, prefix_len: int,
     prefix_len is 0."""
     T, H, B, bf, i32 = (cfg.max_tokens, cfg.attn_heads, cfg.batch, torch.bfloat16,
                         torch.int32)
-    _need(q, "q", bf, (T, H, cfg.d_qk))
-    dev = q.device
-    _need(k_pages, "k_pages", bf, (cfg.n_pages, cfg.page_size, cfg.d_qk), dev)
+    dev = _first_tensor(q, "q", bf, (T, H, cfg.d_qk))
+    p_k = _check_tensor(k_pages, "k_pages", bf, (cfg.n_pages, cfg.page_size, cfg.d_qk), dev)
+    p_v = None
     if v_pages is not None:
-        _need(v_pages, "v_pages", bf, (cfg.n_pages, cfg.page_size, cfg.d_v), dev)
+        p_v = _check_tensor(v_pages, "v_pages", bf, (cfg.n_pages, cfg.page_size, cfg.d_v), dev)
+    prefix_len = int(prefix_len)
     if prefix_len < 0:
         raise ValueError("prefix_len must not be negative")
+    p_prefix = None
     if prefix_table is None:
         if prefix_len > 0:
             raise ValueError("prefix_len > 0 needs a prefix_table")
     else:
-        _need(prefix_table, "prefix_table", i32, device=dev)
-        if prefix_table.dim() != 1 or prefix_table.numel() * cfg.page_size < prefix_len:
+        n = prefix_table.numel() if isinstance(prefix_table, torch.Tensor) else 0
+        p_prefix = _check_tensor(prefix_table, "prefix_table", i32, (n,), dev)
+        if n * cfg.page_size < prefix_len:
             raise ValueError("prefix_table must be [>= ceil(prefix_len / page_size)]")
-    _need(block_table, "block_table", i32, (B, cfg.max_blocks), dev)
-    _need(seq_lens, "seq_lens", i32, (B,), dev)
-    _need(cu_tokens, "cu_tokens", i32, (B + 1,), dev)
+    p_table = _check_tensor(block_table, "block_table", i32, (B, cfg.max_blocks), dev)
+    p_seq = _check_tensor(seq_lens, "seq_lens", i32, (B,), dev)
+    p_cu = _check_tensor(cu_tokens, "cu_tokens", i32, (B + 1,), dev)
     if o is None:
         o = torch.zeros((T, H, cfg.d_v), dtype=bf, device=dev)
     if lse is None:
         lse = torch.zeros((T, H), dtype=torch.float32, device=dev)
-    _need(o, "o", bf, (T, H, cfg.d_v), dev)
-    _need(lse, "lse", torch.float32, (T, H), dev)
+    p_o = _check_tensor(o, "o", bf, (T, H, cfg.d_v), dev)
+    p_lse = _check_tensor(lse, "lse", torch.float32, (T, H), dev)
     ws = _serve_ws(cfg, SERVE_WS_PREFIX, ws, dev)
-    cc = cfg.c()
-    _serve_call("dsa_prefix_attn", dev, ctypes.byref(cc), _ptr(q), _ptr(k_pages),
-                _ptr(v_pages), _ptr(prefix_table), int(prefix_len),
-                _ptr(block_table), _ptr(seq_lens), _ptr(cu_tokens), _ptr(o),
-                _ptr(lse), _ptr(ws), ws.numel())
+    _serve_call("dsa_prefix_attn", dev, cfg._ref, q.data_ptr(), p_k, p_v, p_prefix,
+                prefix_len, p_table, p_seq, p_cu, p_o, p_lse, ws.data_ptr(), ws.numel())
     return o, lse

@@ -47,6 +47,7 @@ thread_local char t_detail[512] = "";
 thread_local bool t_detail_set = false;
 
 struct DeviceInfo {
+  int ordinal = 0;
   int num_sms = 0;
   int cc_major = 0, cc_minor = 0;
 };
@@ -72,6 +73,7 @@ dsa_status_t device_info(DeviceInfo* out) {
       return DSA_ERR_CUDA;
     }
   }
+  d.ordinal = dev;
   *out = d;
   return DSA_OK;
 }
@@ -205,6 +207,7 @@ dsa_status_t make_ctx(void* ws, void* stream, LaunchCtx* ctx) {
   ctx->status = reinterpret_cast<uint32_t*>(ws);
   ctx->timeout_ns = timeout_ns();
   ctx->num_sms = d.num_sms;
+  ctx->device = d.ordinal;
   return DSA_OK;
 }
 

@@ -25,6 +25,7 @@ struct LaunchCtx {
   uint32_t* status;     // device status word (workspace header)
   uint64_t timeout_ns;  // bounded-wait limit for every spin in the kernels
   int num_sms;
+  int device;           // ordinal, < 64
 };
 
 // Host helpers of the C-ABI layer: the launch context of the current device,

@@ -18,12 +18,12 @@
 // where 128 x 64 would read 6 KB in 32.  TMEM: two S^T buffers (2 x 128
 // columns) and O^T (128 columns per 256 dv): all 512 at d = 512.
 //
-// Softmax.  A thread owns one key (a TMEM lane) and 32 rows:
+// Softmax.  A thread owns one key (a TMEM lane) and 64 rows:
 //   P = 2^(s - m),  l += P,  O^T += V^T P^T      (O, l, m in fp32, P in bf16:
 //   the tensor core's operand type, one rounding of each weight).
-// m of a row is a reference near its maximum, shared by the pair: the exact
-// maximum of the unit's first tile, afterwards raised only when a score passes
-// it by more than 2^20.  (Any reference gives the same result as long as nothing
+// m of a row is a reference near its maximum, shared by the pair: the maximum
+// over the first 32 keys of the unit's first tile, afterwards raised only when
+// a score passes it by more than 2^20.  (Any reference gives the same result as long as nothing
 // overflows: the weights are floating point, and fp32 leaves 2^107 above.)  So
 // the usual tile has no exchange of maxima: P is computed while the tensor
 // cores work on the tile before, and a warp that meets a larger score objects
@@ -44,6 +44,8 @@
 // requests are packed together.  Every (unit, pair) that meet leaves O, m and
 // l (fp32, not normalised) in a slot of the workspace, and a second kernel
 // joins each row's slots: sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
+#include <atomic>
+
 #include "attn_common.cuh"
 #include "dsa_internal.h"
 
@@ -54,23 +56,23 @@ constexpr int kRows = 128;           // rows of a unit
 constexpr int kKeys = 256;           // keys of a tile
 constexpr int kMaxPairs = 80;        // workspace bound on the pairs of a launch
 constexpr int kUnitCost = 2;         // a unit's Q load and epilogue, in tiles
-constexpr int kSoftWarps = 16;       // 4 TMEM lane quadrants x 4 groups of rows
-constexpr int kGroupRows = 32;
-constexpr int kProdWarp = 16, kFixWarp = 17, kMmaWarp = 18, kPassWarp = 19;
-constexpr int kThreads = 32 * 20;
+constexpr int kSoftWarps = 8;        // 4 TMEM lane quadrants x 2 groups of rows
+constexpr int kGroupRows = 64;
+constexpr int kProdWarp = 8, kFixWarp = 9, kMmaWarp = 10, kPassWarp = 11;
+constexpr int kThreads = 32 * 12;
 constexpr uint32_t kAtom = 16384;    // 128 rows of 128 bytes
 constexpr uint32_t kStageBytes = 2 * kAtom;
-constexpr int kSoftRegs = 112, kServiceRegs = 32;  // of the 96 that each thread starts with
-static_assert(32 * (16 * kSoftRegs + 4 * kServiceRegs) <= kThreads * 96, "register split");
+constexpr int kSoftRegs = 216, kServiceRegs = 72;  // of the 168 that each thread starts with
+static_assert(32 * (8 * kSoftRegs + 4 * kServiceRegs) <= kThreads * 168, "register split");
 constexpr float kSlack = 20.0f;      // log2 headroom before a row's reference is raised
 
 // ------------------------------------------------------------------- plan
-// The division of work, written by plan_kernel, read by the other two.
+// The division of work: every CTA of the main kernel derives it from the
+// lengths; CTA 0 writes it down for the joining kernel.
 struct Plan {
   int64_t total;        // cost of all units; 0: nothing to do
   int64_t chunk;        // cost of a pair's share
   int64_t prefix_cost;  // of the prefix units, which come first
-  int32_t n_prefix;     // prefix units
   int32_t prefix_tiles;
 };
 // ccum[b], ucum[b]: cost and unit number of request b's first unit (b = 0..B)
@@ -119,7 +121,7 @@ struct ReqShape {
 __device__ __forceinline__ ReqShape req_shape(const Lens& L, int b) {
   const int32_t c0 = __ldg(L.cu + b), c1 = __ldg(L.cu + b + 1);
   int32_t len = __ldg(L.seq + b);
-  if (len < 0 || len > L.cap) len = 0;  // latched by the plan
+  if (len < 0 || len > L.cap) len = 0;  // latched by CTA 0
   return {c0 * L.H, (c1 - c0) * L.H, len, (len + kKeys - 1) / kKeys, c1 - c0};
 }
 
@@ -128,89 +130,13 @@ __device__ __forceinline__ int32_t row_limit(const ReqShape& r, int H, int32_t r
   return max(0, r.len - r.n_new + row / H + 1);
 }
 
-__global__ void __launch_bounds__(1024) plan_kernel(Lens L, int B, int64_t T,
-                                                    int32_t prefix_len, int pairs,
-                                                    Plan* plan, int64_t* ccum,
-                                                    int32_t* ucum, uint32_t* status) {
-  __shared__ int64_t wc[32];
-  __shared__ int32_t wu[32];
-  __shared__ int bad;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) bad = 0;
-  __syncthreads();
-  const int32_t first = __ldg(L.cu), last = __ldg(L.cu + B);
-  if (tid == 0 && (first < 0 || last > T)) bad = 1;
-  for (int b = tid; b < B; b += 1024)
-    if (__ldg(L.cu + b) > __ldg(L.cu + b + 1)) bad = 1;
-  __syncthreads();
-  if (bad) {  // offsets that do not ascend within [0, T]: nothing is computed
-    if (tid == 0) {
-      latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
-      plan->total = 0;
-      plan->chunk = 1;
-    }
-    return;
-  }
-  const int32_t ptiles = (prefix_len + kKeys - 1) / kKeys;
-  const int32_t np = ptiles ? (int32_t)(((int64_t)last * L.H + kRows - 1) / kRows) : 0;
-  int64_t c = (int64_t)np * (ptiles + kUnitCost);
-  int32_t u = np;
-  if (tid == 0) {
-    plan->prefix_cost = c;
-    plan->n_prefix = np;
-    plan->prefix_tiles = ptiles;
-  }
-  for (int b0 = 0; b0 < B; b0 += 1024) {
-    const int b = b0 + tid;
-    int64_t mc = 0;
-    int32_t mu = 0;
-    if (b < B) {
-      const int32_t n = __ldg(L.seq + b);
-      if (n < 0 || n > L.cap) latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
-      const ReqShape r = req_shape(L, b);
-      if (r.tiles) mu = (r.n_rows + kRows - 1) / kRows;
-      mc = (int64_t)mu * (r.tiles + kUnitCost);
-    }
-    int64_t ic = mc;
-    int32_t iu = mu;
-#pragma unroll
-    for (int s = 1; s < 32; s <<= 1) {
-      const int64_t a = __shfl_up_sync(0xffffffffu, ic, s);
-      const int32_t d = __shfl_up_sync(0xffffffffu, iu, s);
-      if (lane >= s) {
-        ic += a;
-        iu += d;
-      }
-    }
-    __syncthreads();
-    if (lane == 31) {
-      wc[warp] = ic;
-      wu[warp] = iu;
-    }
-    __syncthreads();
-    int64_t tc = 0;
-    int32_t tu = 0;
-    for (int w = 0; w < 32; ++w) {
-      if (w == warp) {
-        ic += tc;
-        iu += tu;
-      }
-      tc += wc[w];
-      tu += wu[w];
-    }
-    if (b < B) {
-      ccum[b] = c + ic - mc;
-      ucum[b] = u + iu - mu;
-    }
-    c += tc;
-    u += tu;
-  }
-  if (tid == 0) {
-    ccum[B] = c;
-    ucum[B] = u;
-    plan->total = c;
-    plan->chunk = c > pairs ? (c + pairs - 1) / pairs : 1;
-  }
+__device__ __forceinline__ int32_t unit_count(const ReqShape& r) {
+  return r.tiles ? (r.n_rows + kRows - 1) / kRows : 0;
+}
+
+// x / y for x >= 0, y > 0: by 32 bits where they do (64 take ten times as long)
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+  return ((x | y) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
 }
 
 // Tiles [a, z) of a unit of `tiles` tiles that starts at cost c0, for the
@@ -237,9 +163,12 @@ struct Item {
 struct Share {
   int64_t start, end;    // the share, in cost
   int64_t prefix_cost;
+  int64_t first_cost;    // cost before request first_b
+  int32_t first_b;       // request at start, or the first one
+  int32_t first_unit;    // its first unit
   int32_t prefix_tiles, prefix_len;
   int32_t rows_all;      // rows of all requests
-  int32_t first_b;       // request at start, past the prefix units
+  int32_t pad;
 };
 
 // What the softmax warps need of an item; n = 0: no more.
@@ -255,18 +184,18 @@ struct Post {
 struct Walk {
   const Share* sh;
   int64_t pos;
-  int32_t b;  // request at or before pos, once pos is past the prefix units
+  int64_t cb;   // cost and units before request b, which is at or before pos
+  int32_t ub, b;
 
-  __device__ __forceinline__ bool next(const PlanView& view, const Lens& L,
-                                       const int32_t* prefix_table, const int32_t* table,
-                                       int max_blocks, Item& it) {
+  __device__ __forceinline__ bool next(const Lens& L, const int32_t* prefix_table,
+                                       const int32_t* table, int max_blocks, Item& it) {
     const int64_t end = sh->end;
     while (pos < end) {
       int64_t c0;
       int32_t tiles;
       if (pos < sh->prefix_cost) {
         tiles = sh->prefix_tiles;
-        const int32_t u = (int32_t)(pos / (tiles + kUnitCost));
+        const int32_t u = (int32_t)quotient(pos, tiles + kUnitCost);
         c0 = (int64_t)u * (tiles + kUnitCost);
         it.unit = u;
         it.row0 = it.rel0 = u * kRows;
@@ -276,13 +205,19 @@ struct Walk {
         it.b = -1;
         share_of(c0, tiles, sh->start, end, it.tile0, it.tile1);
       } else {
-        while (__ldg(view.ccum + b + 1) <= pos) ++b;
-        const ReqShape r = req_shape(L, b);
-        const int64_t cb = __ldg(view.ccum + b);
+        ReqShape r = req_shape(L, b);
+        for (;;) {
+          const int32_t units = unit_count(r);
+          const int64_t next_cb = cb + (int64_t)units * (r.tiles + kUnitCost);
+          if (pos < next_cb) break;
+          cb = next_cb;
+          ub += units;
+          r = req_shape(L, ++b);
+        }
         tiles = r.tiles;
-        const int32_t j = (int32_t)((pos - cb) / (tiles + kUnitCost));
+        const int32_t j = (int32_t)quotient(pos - cb, tiles + kUnitCost);
         c0 = cb + (int64_t)j * (tiles + kUnitCost);
-        it.unit = __ldg(view.ucum + b) + j;
+        it.unit = ub + j;
         it.rel0 = j * kRows;
         it.row0 = r.row0 + it.rel0;
         it.n_rows = min(kRows, r.n_rows - it.rel0);
@@ -299,6 +234,117 @@ struct Walk {
     return false;
   }
 };
+
+__device__ __forceinline__ int64_t warp_sum64(int64_t x) {
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
+  return x;
+}
+
+// The share of pair `pair` of `pairs`; all threads of the CTA, `scratch` in
+// shared memory.  The requests are summed once for the total and scanned for
+// the one at the share's start (B <= kThreads: one step each).  `out`: CTA 0
+// writes the plan down and latches what is wrong with the lengths.
+__device__ __forceinline__ void divide(const Lens& L, int B, int64_t T, int32_t prefix_len,
+                                       int64_t pair, int pairs, const PlanView* out,
+                                       uint32_t* status, Share* share, int64_t* scratch) {
+  constexpr int kWarps = kThreads / 32;
+  int32_t* scratch_u = reinterpret_cast<int32_t*>(scratch + kWarps);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int32_t first = __ldg(L.cu), last = __ldg(L.cu + B);
+  int bad = first < 0 || last > T;
+  int64_t sum = 0;
+  for (int b = tid; b < B; b += kThreads) {
+    const ReqShape r = req_shape(L, b);
+    bad |= r.n_new < 0;
+    sum += (int64_t)unit_count(r) * (r.tiles + kUnitCost);
+    if (out) {
+      const int32_t n = __ldg(L.seq + b);
+      if (n < 0 || n > L.cap) latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
+    }
+  }
+  sum = warp_sum64(sum);
+  if (lane == 0) scratch[warp] = sum;
+  bad = __syncthreads_or(bad);
+  const int32_t ptiles = (prefix_len + kKeys - 1) / kKeys;
+  const int32_t np = ptiles ? (int32_t)(((int64_t)last * L.H + kRows - 1) / kRows) : 0;
+  const int64_t prefix_cost = (int64_t)np * (ptiles + kUnitCost);
+  int64_t total = prefix_cost;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) total += scratch[w];
+  if (bad) total = 0;  // offsets that do not ascend within [0, T]: nothing is computed
+  const int64_t chunk = total > pairs ? quotient(total + pairs - 1, pairs) : 1;
+  const int64_t start = min(total, pair * chunk);
+  if (tid == 0) {
+    share->start = start;
+    share->end = min(total, start + chunk);
+    share->prefix_cost = prefix_cost;
+    share->prefix_tiles = ptiles;
+    share->prefix_len = prefix_len;
+    share->rows_all = last * L.H;
+    share->first_b = 0;
+    share->first_cost = prefix_cost;
+    share->first_unit = np;
+    if (out) {
+      *out->p = Plan{total, chunk, prefix_cost, ptiles};
+      if (bad) latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
+    }
+  }
+  int64_t c = prefix_cost;
+  int32_t u = np;
+  // (the other CTAs stop at their own start, those with nothing at once)
+  for (int b0 = 0; b0 < B && !bad && (out || (c <= start && start < total)); b0 += kThreads) {
+    const int b = b0 + tid;
+    int64_t mc = 0;
+    int32_t mu = 0;
+    if (b < B) {
+      const ReqShape r = req_shape(L, b);
+      mu = unit_count(r);
+      mc = (int64_t)mu * (r.tiles + kUnitCost);
+    }
+    int64_t ic = mc;
+    int32_t iu = mu;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, ic, s);
+      const int32_t y = __shfl_up_sync(0xffffffffu, iu, s);
+      if (lane >= s) {
+        ic += x;
+        iu += y;
+      }
+    }
+    __syncthreads();
+    if (lane == 31) {
+      scratch[warp] = ic;
+      scratch_u[warp] = iu;
+    }
+    __syncthreads();
+    int64_t tc = 0;
+    int32_t tu = 0;
+#pragma unroll 4
+    for (int w = 0; w < kWarps; ++w) {
+      if (w == warp) {
+        ic += tc;
+        iu += tu;
+      }
+      tc += scratch[w];
+      tu += scratch_u[w];
+    }
+    const int64_t c0 = c + ic - mc;
+    const int32_t u0 = u + iu - mu;
+    if (b < B && c0 <= start && start < c0 + mc) {
+      share->first_b = b;
+      share->first_cost = c0;
+      share->first_unit = u0;
+    }
+    if (out && b < B) {
+      out->ccum[b] = c0;
+      out->ucum[b] = u0;
+    }
+    c += tc;
+    u += tu;
+  }
+}
 
 // ---------------------------------------------------- pair (cluster) PTX
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -483,12 +529,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                        const __grid_constant__ CUtensorMap k_map,
                        const __grid_constant__ CUtensorMap v_map, PlanView view, Lens L,
                        const int32_t* __restrict__ prefix_table, int32_t prefix_len,
-                       const int32_t* __restrict__ table, int B, int max_blocks,
-                       int page_log2, int32_t n_pages, int64_t n_slots, float scale_log2,
+                       const int32_t* __restrict__ table, int B, int64_t T,
+                       int max_blocks, int page_log2, int32_t n_pages, int64_t n_slots, float scale_log2,
                        uint32_t* status, uint64_t timeout_ns) {
   using C = PCfg<D>;
   constexpr uint32_t IDESC_S = idesc_bf16(256, 128, 0, 0);
   constexpr uint32_t IDESC_O = idesc_bf16(256, 128, 1, 1);
+  asm volatile("griddepcontrol.launch_dependents;");  // the joining kernel waits for the end
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -497,14 +544,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t sP = sQ + C::kQBytes;
   const uint32_t sStage = sP + C::kPBytes;
   uint8_t* tail = gb + C::kQBytes + C::kPBytes + kStages * kStageBytes;
-  float* nm_s = reinterpret_cast<float*>(tail);           // [row] -m
-  float* nmo_s = nm_s + kRows;                            // [row] -m before it was last raised
-  int32_t* lim_s = reinterpret_cast<int32_t*>(nmo_s + kRows);  // [row] keys that it sees
+  float* nm2_s = reinterpret_cast<float*>(tail);          // [item & 1][row] -m
+  float* nmo_s = nm2_s + 2 * kRows;                       // [row] -m before it was last raised
+  uint8_t* lim_s = reinterpret_cast<uint8_t*>(nmo_s + kRows);  // [row] keys past lim_min
   uint64_t* bars = reinterpret_cast<uint64_t*>(lim_s + kRows);
   uint32_t* misc = reinterpret_cast<uint32_t*>(bars + kBars);  // abort, tmem, objected, redo
   Share* share = reinterpret_cast<Share*>(misc + 4);
   Post* posts = reinterpret_cast<Post*>(share + 1);            // [2]
-  static_assert(3 * kRows * 4 + kBars * 8 + 16 + sizeof(Share) + 2 * sizeof(Post) <= C::kTail,
+  static_assert(3 * kRows * 4 + kRows + kBars * 8 + 16 + sizeof(Share) + 2 * sizeof(Post) <= C::kTail,
                 "tail");
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -531,7 +578,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   auto fixed = [&](uint32_t r) { return bx + 104 + 8 * (r & 1u); };   // leader: the other's is
   auto post_full = [&](uint32_t i) { return bx + 120 + 8 * (i & 1u); };
   auto post_free = [&](uint32_t i) { return bx + 136 + 8 * (i & 1u); };
-  static_assert(2 * kStages + 19 <= kBars, "barriers");
+  const uint32_t refs = bx + 152;    // a unit's first references
+  static_assert(2 * kStages + 20 <= kBars, "barriers");
   // tile number + 1 of the last tile objected to (leader), to be done again
   volatile uint32_t *objected = misc + 2, *redo = misc + 3;
   const PairWaiter W{misc, at_rank(smem_u32(misc), peer), status, timeout_ns};
@@ -556,6 +604,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(o_empty, 2 * kSoftWarps);
     mbar_init(xs, 2 * kSoftWarps);
     mbar_init(grp, kSoftWarps);
+    mbar_init(refs, kRows / kGroupRows);
     mbar_init(done_bar, 1);
     misc[0] = misc[2] = misc[3] = 0u;
     fence_mbar_init();
@@ -570,32 +619,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
-  // the share of this pair and the request that it starts in
   const int64_t pair = blockIdx.x >> 1;
-  const Plan* plan = view.p;
-  const int64_t start = min(plan->total, pair * plan->chunk);
-  const int64_t end = min(plan->total, start + plan->chunk);
-  if (tid == 0) {
-    share->start = start;
-    share->end = end;
-    share->prefix_cost = plan->prefix_cost;
-    share->prefix_tiles = plan->prefix_tiles;
-    share->prefix_len = prefix_len;
-    share->rows_all = __ldg(L.cu + B) * L.H;
-    share->first_b = 0;
-  }
-  __syncthreads();
-  if (start < end && start >= plan->prefix_cost)
-    for (int b = tid; b < B; b += kThreads)
-      if (__ldg(view.ccum + b) <= start && start < __ldg(view.ccum + b + 1)) share->first_b = b;
+  divide(L, B, T, prefix_len, pair, gridDim.x >> 1, blockIdx.x == 0 ? &view : nullptr, status,
+         share, reinterpret_cast<int64_t*>(red));
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();
   tc_fence_after();
-  Walk walk{share, start, share->first_b};
-  auto next = [&](Item& i) {
-    return walk.next(view, L, prefix_table, table, max_blocks, i);
-  };
+  Walk walk{share, share->start, share->first_cost, share->first_unit, share->first_b};
+  auto next = [&](Item& i) { return walk.next(L, prefix_table, table, max_blocks, i); };
   constexpr uint32_t tmem = 0;  // an allocation of all 512 columns starts at column 0
   constexpr uint32_t tO = tmem + 2 * kRows;
   Item it;
@@ -742,9 +774,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       while (ok && nxt.n > 0) {
         cur = nxt;
         if (!(ok = post())) break;
-        // bytes from the other CTA's keys, for this CTA's groups with rows
-        const int mine = (cur.n_rows - 64 * (int)rank + kGroupRows - 1) / kGroupRows;
-        const uint32_t bytes = (uint32_t)max(0, min(2, mine)) * (128 * kGroupRows * 2);
+        // bytes from the other CTA's keys, if this CTA's group has rows
+        const uint32_t bytes =
+            cur.n_rows > kGroupRows * (int)rank ? 128 * kGroupRows * 2 : 0;
         for (int32_t j = 0; j < cur.n && ok; ++j, ++nt)
           for (int time = 0; time < 2; ++time) {
             if (lane == 0) mbar_expect_tx(p_in, bytes);
@@ -847,16 +879,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // ================================================ softmax, epilogue
-    const int quad = warp & 3, g = warp >> 2;  // TMEM lanes, rows 32 g .. 32 g + 31
+    const int quad = warp & 3, g = warp >> 2;  // TMEM lanes, rows 64 g .. 64 g + 63
     const int r0 = kGroupRows * g;
     const int key = (int)rank * 128 + quad * 32 + lane;
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
-    const uint32_t owner = (uint32_t)g >> 1;  // the CTA that holds P of these rows
+    const uint32_t owner = (uint32_t)g;  // the CTA that holds P of these rows
     const uint32_t p_row = (owner == rank ? sP : at_rank(sP, peer)) + (uint32_t)key * 128u;
     const uint32_t p_in_peer = at_rank(p_in, peer);
-    const uint32_t p_c0 = (uint32_t)(g & 1) * 4u, p_sw = (uint32_t)(key & 7);
+    const uint32_t p_sw = (uint32_t)(key & 7);
     const uint64_t scale2 = pair2(scale_log2, scale_log2);
-    uint32_t nx = 0, ng = 0, nt = 0, np = 0;
+    uint32_t nx = 0, nf = 0, ng = 0, nt = 0, np = 0;
     auto group_sync = [&]() {  // all softmax warps of this CTA
       __syncwarp();
       if (lane == 0) mbar_arrive(grp);
@@ -870,25 +902,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (n == 0) break;
       const int32_t tile0 = post->tile0, lim_min = post->lim_min;
       const bool live = post->n_rows > r0;  // this group has rows that count
-      if (tid < kRows) {
-        const int32_t len = post->len, pb = post->b;
-        lim_s[tid] = pb < 0 ? len
-                            : min(len, row_limit(req_shape(L, pb), L.H,
-                                                 post->rel0 + min(tid, post->n_rows - 1)));
-        nm_s[tid] = 0.f;
+      // references in turns: the other CTA may still read the last item's when
+      // this item's arrive there
+      float* nm_s = nm2_s + (ni & 1u) * kRows;
+      if (tid < kRows) {  // at most one key more a row
+        const int32_t pb = post->b;
+        lim_s[tid] = pb < 0 ? 0
+                            : (uint8_t)(row_limit(req_shape(L, pb), L.H,
+                                                  post->rel0 + min(tid, post->n_rows - 1)) -
+                                        lim_min);
       }
       if (!(ok = group_sync())) break;
-      uint64_t l[16];  // this thread's row sums, in pairs
+      uint64_t l[32];  // this thread's row sums, in pairs
 #pragma unroll
-      for (int h = 0; h < 16; ++h) l[h] = 0ull;
-      uint32_t pk[16];  // this thread's P, bf16 pairs
+      for (int h = 0; h < 32; ++h) l[h] = 0ull;
+      uint32_t pk[32];  // this thread's P, bf16 pairs
       float over = 0.f;
 
-      // Raise the references to the exact maxima of tile j (S^T in buffer b)
-      // where they are passed by more than `slack`
-      auto raise = [&](int j, uint32_t b, float slack) {
+      // The first references: the maxima over the unit's first 32 keys, which
+      // every row that sees a key sees one of.  One warp a group has them and
+      // tells both CTAs.
+      auto first_refs = [&](uint32_t b) {
+        if (rank == 0 && quad == 0) {
+          const int32_t pos = tile0 * kKeys + lane;
+#pragma unroll 1
+          for (int h0 = r0; h0 < r0 + kGroupRows; h0 += 16) {
+            float x[16];
+            uint32_t r[16];
+            if (live) {
+              tmem_ld16(tmem + b * kRows + h0, r);
+              tmem_wait_ld();
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              x[e] = live && pos < lim_min + lim_s[h0 + e] ? __uint_as_float(r[e]) * scale_log2 : -INFINITY;
+            float t = column_reduce<true>(x, lane);
+            t = t == -INFINITY ? 0.f : -t;
+            if (lane < 16) {
+              nm_s[h0 + lane] = t;
+              st_cluster_u32(at_rank(smem_u32(nm_s + h0 + lane), 1), __float_as_uint(t));
+            }
+          }
+          __syncwarp();
+          if (lane == 0) {
+            mbar_signal(at_rank(refs, 0));
+            mbar_release_cluster(at_rank(refs, 1));
+          }
+        }
+        return W.wait(refs, nf++ & 1u);
+      };
+      // After an objection: the references of the rows where tile j (S^T in
+      // buffer b) passes them by more than the slack become its exact maxima
+      auto raise = [&](int j, uint32_t b) {
         const int32_t pos = (tile0 + j) * kKeys + key;
-        const bool masked = (tile0 + j + 1) * kKeys > lim_min;
 #pragma unroll 1
         for (int h0 = r0; h0 < r0 + kGroupRows; h0 += 16) {
           float x[16];
@@ -899,7 +965,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            x[e] = live && (!masked || pos < lim_s[h0 + e])
+            x[e] = live && pos < lim_min + lim_s[h0 + e]
                        ? fmaf(__uint_as_float(r[e]), scale_log2, nm_s[h0 + e])
                        : -INFINITY;
           const float t = column_reduce<true>(x, lane);
@@ -921,11 +987,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int w = 1; w < 8; ++w) by = fmaxf(by, red[w * kRows + tid]);
           const float nm = nm_s[tid];
           nmo_s[tid] = nm;
-          if (by > slack) nm_s[tid] = nm - by;
+          if (by > kSlack) nm_s[tid] = nm - by;
         }
         return group_sync();
       };
-      // P of tile j from S^T in buffer b, the largest s - m, and l.  Weights of 8
+      // P of tile j from S^T in buffer b, the largest s - m, and l.  Weights of 16
       // rows among which one passes the slack are left out of l, which so
       // stays finite; the tile is objected to, and the weights are added when
       // it is visited again (`revisit`) under references that hold them.
@@ -935,14 +1001,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int32_t pos = (tile0 + j) * kKeys + key;
         const bool masked = (tile0 + j + 1) * kKeys > lim_min;  // uniform
 #pragma unroll
-        for (int h0 = 0; h0 < 32; h0 += 8) {
-          uint32_t r[8];
-          float d[8];
-          tmem_ld8(tmem + b * kRows + lane_base + r0 + h0, r);
+        for (int h0 = 0; h0 < kGroupRows; h0 += 16) {
+          uint32_t r[16];
+          float d[16];
+          tmem_ld16(tmem + b * kRows + lane_base + r0 + h0, r);
           tmem_wait_ld();
           const ulonglong2* nm4 = reinterpret_cast<const ulonglong2*>(nm_s + r0 + h0);
 #pragma unroll
-          for (int e = 0; e < 8; e += 4) {
+          for (int e = 0; e < 16; e += 4) {
             const ulonglong2 c = nm4[e / 4];
             unpair2(fma2(pair2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), scale2, c.x),
                     d[e], d[e + 1]);
@@ -951,31 +1017,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           if (masked) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (pos >= lim_s[r0 + h0 + e]) d[e] = -INFINITY;
+            for (int e = 0; e < 16; ++e)
+              if (pos >= lim_min + lim_s[r0 + h0 + e]) d[e] = -INFINITY;
           }
           float top = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) top = fmaxf(top, fmaxf(d[e], d[e + 1]));
+          for (int e = 0; e < 16; e += 2) top = fmaxf(top, fmaxf(d[e], d[e + 1]));
           bool add = !(top > kSlack);
           if (revisit) {  // those that were left out under the references before
             float old = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (!masked || pos < lim_s[r0 + h0 + e])
+            for (int e = 0; e < 16; ++e)
+              if (!masked || pos < lim_min + lim_s[r0 + h0 + e])
                 old = fmaxf(old, fmaf(__uint_as_float(r[e]), scale_log2, nmo_s[r0 + h0 + e]));
             add = add && old > kSlack;
           }
           over = fmaxf(over, top);
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) {
+          for (int e = 0; e < 16; e += 2) {
             d[e] = ex2(d[e]);
             d[e + 1] = ex2(d[e + 1]);
             pk[(h0 + e) / 2] = pack_bf16(d[e], d[e + 1]);
           }
           if (add) {
 #pragma unroll
-            for (int e = 0; e < 8; e += 2)
+            for (int e = 0; e < 16; e += 2)
               l[(h0 + e) / 2] = add2(l[(h0 + e) / 2], pair2(d[e], d[e + 1]));
           }
         }
@@ -985,8 +1051,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_before();  // S^T has been read
         if (live) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t a = p_row + (((p_c0 + (uint32_t)c) ^ p_sw) << 4);
+          for (int c = 0; c < 8; ++c) {
+            const uint32_t a = p_row + (((uint32_t)c ^ p_sw) << 4);
             const uint32_t w[4] = {pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]};
             if (owner == rank)
               asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(w[0]),
@@ -1006,7 +1072,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       auto rescale = [&]() {
         bool any = false;
 #pragma unroll
-        for (int h = 0; h < 16; ++h) {
+        for (int h = 0; h < kGroupRows / 2; ++h) {
           const float a = nm_s[r0 + 2 * h] - nmo_s[r0 + 2 * h];
           const float c = nm_s[r0 + 2 * h + 1] - nmo_s[r0 + 2 * h + 1];
           any |= a != 0.f || c != 0.f;
@@ -1016,10 +1082,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (!any || !live) return;  // the same in every lane
 #pragma unroll 1
-        for (int c = 0; c < 2 * C::kBlocks; ++c) {
+        for (int c = 0; c < 4 * C::kBlocks; ++c) {
           uint32_t r[16];
-          const int h0 = r0 + 16 * (c & 1);
-          const uint32_t ta = tO + (c >> 1) * kRows + lane_base + h0;
+          const int h0 = r0 + 16 * (c & 3);
+          const uint32_t ta = tO + (c >> 2) * kRows + lane_base + h0;
           tmem_ld16(ta, r);
           tmem_wait_ld();
 #pragma unroll
@@ -1038,13 +1104,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tc_fence_after();
         }
         int jw = j;            // tile of this pass
-        bool renew = j == 0;   // take its maxima first
+        bool renew = j == 0;   // take references from it first
         bool asked = j == 0;   // the verdict is known
         bool revisit = false;
         for (;;) {
           const uint32_t b = (nt + (uint32_t)(jw - j)) & 1u;
           if (renew) {
-            if (!(ok = raise(jw, b, j == 0 ? -INFINITY : kSlack))) break;
+            if (!(ok = j == 0 ? first_refs(b) : raise(jw, b))) break;
             if (j > 0) rescale();
           }
           if (jw < n) weights(jw, b, revisit);
@@ -1059,7 +1125,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
           if (jw == n) break;
-          if (jw == j && __any_sync(0xffffffffu, j > 0 && over > kSlack)) {
+          if (jw == j && __any_sync(0xffffffffu, over > kSlack)) {
             if (lane == 0) {
               st_cluster_u32(at_rank(smem_u32(misc + 2), 0), nt + 1u);
               fence_cluster();
@@ -1080,7 +1146,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int64_t slot = (int64_t)post->unit + pair;
       const int n_rows = post->n_rows;
 #pragma unroll
-      for (int h0 = 0; h0 < 32; h0 += 16) {
+      for (int h0 = 0; h0 < kGroupRows; h0 += 16) {
         float x[16];
 #pragma unroll
         for (int e = 0; e < 16; e += 2) unpair2(l[(h0 + e) / 2], x[e], x[e + 1]);
@@ -1150,6 +1216,7 @@ __global__ void __launch_bounds__(128) join_kernel(PlanView view, Lens L,
   constexpr int kPer = 512 / D, kLanes = D / 4;  // rows of a block, threads of a row
   const int sub = threadIdx.x / kLanes, th = threadIdx.x % kLanes;
   const int64_t row = blockIdx.x * (int64_t)kPer + sub;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the main kernel's results
   if (row >= n_rows) return;
   const Plan* plan = view.p;
   const int64_t t = row / L.H, chunk = plan->chunk, total = plan->total;
@@ -1185,40 +1252,40 @@ __global__ void __launch_bounds__(128) join_kernel(PlanView view, Lens L,
   float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int x = 0; x < n_units; ++x) {
-    const int64_t i0 = c0[x] / chunk, i1 = (c0[x] + tiles[x] + kUnitCost - 1) / chunk;
+    const int64_t i0 = quotient(c0[x], chunk);
+    const int64_t i1 = quotient(c0[x] + tiles[x] + kUnitCost - 1, chunk);
     for (int64_t i = i0; i <= i1; i += kJoin) {
-      float mi[kJoin], li[kJoin];
+      float2 p0[kJoin], p1[kJoin];
       float4 oi[kJoin];
+#pragma unroll
+      for (int e = 0; e < kJoin; ++e) {
+        p0[e] = p1[e] = make_float2(-INFINITY, 0.f);
+        oi[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        int32_t a, z;
+        share_of(c0[x], tiles[x], (i + e) * chunk, min(total, (i + e + 1) * chunk), a, z);
+        const int64_t slot = unit[x] + i + e;
+        if (i + e <= i1 && a < min(z, used[x]) && DSA_IN_BOUNDS(slot < n_slots, status)) {
+          p0[e] = view.ml[(slot * 2) * kRows + at[x]];
+          p1[e] = view.ml[(slot * 2 + 1) * kRows + at[x]];
+          oi[e] = reinterpret_cast<const float4*>(view.o + (slot * kRows + at[x]) * D)[th];
+        }
+      }
       float top = m;
 #pragma unroll
       for (int e = 0; e < kJoin; ++e) {
-        mi[e] = -INFINITY;
-        li[e] = 0.f;
-        oi[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i + e > i1) continue;
-        int32_t a, z;
-        share_of(c0[x], tiles[x], (i + e) * chunk, min(total, (i + e + 1) * chunk), a, z);
-        if (a >= min(z, used[x])) continue;
-        const int64_t slot = unit[x] + i + e;
-        if (!DSA_IN_BOUNDS(slot < n_slots, status)) continue;
-        const float2 p0 = view.ml[(slot * 2) * kRows + at[x]];
-        const float2 p1 = view.ml[(slot * 2 + 1) * kRows + at[x]];
-        li[e] = p0.y + p1.y;
-        if (li[e] == 0.f) continue;  // no key seen
-        mi[e] = p0.x;
-        oi[e] = reinterpret_cast<const float4*>(view.o + (slot * kRows + at[x]) * D)[th];
+        p1[e].y += p0[e].y;                        // l; 0: no key seen
+        if (p1[e].y == 0.f) p0[e].x = -INFINITY;
+        top = fmaxf(top, p0[e].x);
       }
-#pragma unroll
-      for (int e = 0; e < kJoin; ++e) top = fmaxf(top, mi[e]);
       const float keep = top == -INFINITY ? 1.f : ex2(m - top);
       l *= keep;
       acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
       m = top;
 #pragma unroll
       for (int e = 0; e < kJoin; ++e) {
-        if (mi[e] == -INFINITY) continue;  // nothing there
-        const float w = ex2(mi[e] - top);
-        l = fmaf(w, li[e], l);
+        if (p0[e].x == -INFINITY) continue;
+        const float w = ex2(p0[e].x - top);
+        l = fmaf(w, p1[e].y, l);
         acc.x = fmaf(w, oi[e].x, acc.x);
         acc.y = fmaf(w, oi[e].y, acc.y);
         acc.z = fmaf(w, oi[e].z, acc.z);
@@ -1240,24 +1307,34 @@ cudaError_t launch_t(const LaunchCtx& c, const ServeShape& s, const CUtensorMap&
                      const Lens& L, __nv_bfloat16* o, float* lse, uint8_t* work) {
   using C = PCfg<D>;
   const PlanView view = plan_view(s, work);
-  cudaError_t e = cudaFuncSetAttribute(prefix_attn_kernel<D>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)C::kSmem);
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
+  static std::atomic<uint64_t> prepared{0};  // devices whose kernel has its attribute
+  const uint64_t bit = 1ull << (c.device & 63);
+  if (!(prepared.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(prefix_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)C::kSmem);
+    if (e != cudaSuccess) return e;
+    prepared.fetch_or(bit, std::memory_order_relaxed);
+  }
   const int pairs = c.num_sms / 2 < kMaxPairs ? c.num_sms / 2 : kMaxPairs;
-  plan_kernel<<<1, 1024, 0, c.stream>>>(L, s.B, s.T, prefix_len, pairs, view.p, view.ccum,
-                                        view.ucum, c.status);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int64_t slots = max_slots(s);
   prefix_attn_kernel<D><<<2 * pairs, kThreads, C::kSmem, c.stream>>>(
-      qm, km, vm, view, L, prefix_table, prefix_len, table, s.B, s.max_blocks, s.page_log2,
-      (int32_t)s.n_pages, slots, s.scale * kLog2e, c.status, c.timeout_ns);
+      qm, km, vm, view, L, prefix_table, prefix_len, table, s.B, s.T, s.max_blocks,
+      s.page_log2, (int32_t)s.n_pages, slots, s.scale * kLog2e, c.status, c.timeout_ns);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  // launched while the main kernel runs, which it waits for on the device
   const int64_t rows = s.T * s.H;
   constexpr int per = 512 / D;
-  join_kernel<D><<<(unsigned)((rows + per - 1) / per), 128, 0, c.stream>>>(
-      view, L, o, lse, s.B, rows, slots, c.status);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((rows + per - 1) / per));
+  cfg.blockDim = dim3(128);
+  cfg.stream = c.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<D>, view, L, o, lse, s.B, rows, slots, c.status);
 }
 
 }  // namespace
