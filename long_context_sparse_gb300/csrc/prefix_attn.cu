@@ -925,17 +925,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       auto first_refs = [&](uint32_t b) {
         if (rank == 0 && quad == 0) {
           const int32_t pos = tile0 * kKeys + lane;
+          const bool masked = tile0 * kKeys + 32 > lim_min;  // uniform
 #pragma unroll 1
           for (int h0 = r0; h0 < r0 + kGroupRows; h0 += 16) {
             float x[16];
             uint32_t r[16];
             if (live) {
               tmem_ld16(tmem + b * kRows + h0, r);
-              tmem_wait_ld();
+              tmem_wait_ld_dep(r);
             }
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              x[e] = live && pos < lim_min + lim_s[h0 + e] ? __uint_as_float(r[e]) * scale_log2 : -INFINITY;
+              x[e] = live && (!masked || pos < lim_min + lim_s[h0 + e])
+                         ? __uint_as_float(r[e]) * scale_log2
+                         : -INFINITY;
             float t = column_reduce<true>(x, lane);
             t = t == -INFINITY ? 0.f : -t;
             if (lane < 16) {
@@ -961,7 +964,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           uint32_t r[16];
           if (live) {
             tmem_ld16(tmem + b * kRows + lane_base + h0, r);
-            tmem_wait_ld();
+            tmem_wait_ld_dep(r);
           }
 #pragma unroll
           for (int e = 0; e < 16; ++e)
@@ -1000,19 +1003,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!live) return;
         const int32_t pos = (tile0 + j) * kKeys + key;
         const bool masked = (tile0 + j + 1) * kKeys > lim_min;  // uniform
+        // the next 16 columns and their references are on the way while these
+        // are worked on: with MMAs and TMA at shared memory, a load from it
+        // takes 100 to 200 cycles
+        uint32_t rr[2][16];
+        const uint32_t tS = tmem + b * kRows + lane_base + r0;
+        const ulonglong2* refs2 = reinterpret_cast<const ulonglong2*>(nm_s + r0);
+        tmem_ld16(tS, rr[0]);
 #pragma unroll
         for (int h0 = 0; h0 < kGroupRows; h0 += 16) {
-          uint32_t r[16];
+          uint32_t(&r)[16] = rr[(h0 / 16) & 1];
+          ulonglong2 c[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) c[e] = refs2[h0 / 4 + e];
+          tmem_wait_ld_dep(r);
+          if (h0 + 16 < kGroupRows) tmem_ld16(tS + h0 + 16, rr[(h0 / 16 + 1) & 1]);
           float d[16];
-          tmem_ld16(tmem + b * kRows + lane_base + r0 + h0, r);
-          tmem_wait_ld();
-          const ulonglong2* nm4 = reinterpret_cast<const ulonglong2*>(nm_s + r0 + h0);
 #pragma unroll
           for (int e = 0; e < 16; e += 4) {
-            const ulonglong2 c = nm4[e / 4];
-            unpair2(fma2(pair2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), scale2, c.x),
+            unpair2(fma2(pair2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), scale2,
+                         c[e / 4].x),
                     d[e], d[e + 1]);
-            unpair2(fma2(pair2(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])), scale2, c.y),
+            unpair2(fma2(pair2(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])), scale2,
+                         c[e / 4].y),
                     d[e + 2], d[e + 3]);
           }
           if (masked) {
@@ -1087,7 +1100,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int h0 = r0 + 16 * (c & 3);
           const uint32_t ta = tO + (c >> 2) * kRows + lane_base + h0;
           tmem_ld16(ta, r);
-          tmem_wait_ld();
+          tmem_wait_ld_dep(r);
 #pragma unroll
           for (int e = 0; e < 16; ++e)
             r[e] = __float_as_uint(__uint_as_float(r[e]) * ex2(nm_s[h0 + e] - nmo_s[h0 + e]));
@@ -1169,7 +1182,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int h0 = r0; h0 < min(r0 + kGroupRows, n_rows); h0 += 16) {
             uint32_t r[16];
             tmem_ld16(tO + m * kRows + lane_base + h0, r);
-            tmem_wait_ld();
+            tmem_wait_ld_dep(r);
 #pragma unroll
             for (int e = 0; e < 16; ++e)
               if (h0 + e < n_rows) out[(int64_t)(h0 + e) * D + dv] = __uint_as_float(r[e]);
