@@ -523,6 +523,25 @@ __device__ __forceinline__ float column_reduce(float (&x)[16], int lane) {
   return MAX ? fmaxf(x[0], got) : x[0] + got;
 }
 
+// The maxima of N times 16 columns, N reductions in step.
+template <int N>
+__device__ __forceinline__ void column_max(float (&x)[N][16], float (&top)[N], int lane) {
+#pragma unroll
+  for (int H = 8; H > 0; H >>= 1) {
+    const bool up = (lane & H) != 0;
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+#pragma unroll
+      for (int i = 0; i < H; ++i) {
+        const float keep = up ? x[c][i + H] : x[c][i], give = up ? x[c][i] : x[c][i + H];
+        x[c][i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, H));
+      }
+  }
+#pragma unroll
+  for (int c = 0; c < N; ++c)
+    top[c] = fmaxf(x[c][0], __shfl_xor_sync(0xffffffffu, x[c][0], 16));
+}
+
 template <int D>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefix_attn_kernel(const __grid_constant__ CUtensorMap q_map,
@@ -926,25 +945,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (rank == 0 && quad == 0) {
           const int32_t pos = tile0 * kKeys + lane;
           const bool masked = tile0 * kKeys + 32 > lim_min;  // uniform
-#pragma unroll 1
-          for (int h0 = r0; h0 < r0 + kGroupRows; h0 += 16) {
-            float x[16];
-            uint32_t r[16];
-            if (live) {
-              tmem_ld16(tmem + b * kRows + h0, r);
-              tmem_wait_ld_dep(r);
-            }
+          // 16 rows at a time, the four reductions side by side (a shuffle waits
+          // at shared memory's door like a load)
+          float x[kGroupRows / 16][16];
+          if (live) {
+            uint32_t r[kGroupRows / 16][16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              x[e] = live && (!masked || pos < lim_min + lim_s[h0 + e])
-                         ? __uint_as_float(r[e]) * scale_log2
-                         : -INFINITY;
-            float t = column_reduce<true>(x, lane);
-            t = t == -INFINITY ? 0.f : -t;
-            if (lane < 16) {
-              nm_s[h0 + lane] = t;
-              st_cluster_u32(at_rank(smem_u32(nm_s + h0 + lane), 1), __float_as_uint(t));
+            for (int c = 0; c < kGroupRows / 16; ++c)
+              tmem_ld16(tmem + b * kRows + r0 + 16 * c, r[c]);
+#pragma unroll
+            for (int c = 0; c < kGroupRows / 16; ++c) {
+              tmem_wait_ld_dep(r[c]);
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                x[c][e] = !masked || pos < lim_min + lim_s[r0 + 16 * c + e]
+                              ? __uint_as_float(r[c][e]) * scale_log2
+                              : -INFINITY;
             }
+          } else {
+#pragma unroll
+            for (int c = 0; c < kGroupRows / 16; ++c)
+#pragma unroll
+              for (int e = 0; e < 16; ++e) x[c][e] = -INFINITY;
+          }
+          float top[kGroupRows / 16];
+          column_max<kGroupRows / 16>(x, top, lane);
+#pragma unroll
+          for (int c = 0; c < kGroupRows / 16; c += 2) {  // lanes 0-15 and 16-31: one each
+            const float t = lane < 16 ? top[c] : top[c + 1];
+            const float* at = nm_s + r0 + 16 * c + lane;
+            const float v = t == -INFINITY ? 0.f : -t;
+            nm_s[r0 + 16 * c + lane] = v;
+            st_cluster_u32(at_rank(smem_u32(at), 1), __float_as_uint(v));
           }
           __syncwarp();
           if (lane == 0) {
