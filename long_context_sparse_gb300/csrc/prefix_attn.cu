@@ -58,7 +58,7 @@ constexpr int kMaxPairs = 80;        // workspace bound on the pairs of a launch
 constexpr int kUnitCost = 2;         // a unit's Q load and epilogue, in tiles
 constexpr int kSoftWarps = 8;        // 4 TMEM lane quadrants x 2 groups of rows
 constexpr int kGroupRows = 64;
-constexpr int kProdWarp = 8, kFixWarp = 9, kMmaWarp = 10, kPassWarp = 11;
+constexpr int kProdWarp = 8, kScoutWarp = 9, kMmaWarp = 10, kPassWarp = 11;
 constexpr int kThreads = 32 * 12;
 constexpr uint32_t kAtom = 16384;    // 128 rows of 128 bytes
 constexpr uint32_t kStageBytes = 2 * kAtom;
@@ -381,17 +381,6 @@ __device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity, 
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 __device__ __forceinline__ void fence_cluster() {
   asm volatile("fence.acq_rel.cluster;" ::: "memory");
 }
@@ -489,7 +478,6 @@ struct PairWaiter {
 // row constants and barriers, 1 KB to align: all of the 227 KB.
 constexpr int kStages = 4;
 constexpr int kBars = 28;
-constexpr uint32_t kPeek = 5;  // MMAs of a stage before the look at the next one
 
 template <int D>
 struct PCfg {
@@ -715,7 +703,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               if (!(ok = W.wait(empty(s), ((u / kStages) & 1u) ^ 1u))) break;
               const bool ragged = left0 > 128 * half && left0 < 128 * half + 128;
               uint32_t bar = lead_full + 8u * s;
-              if (ragged) {  // lands at this CTA's barrier: kFixWarp passes it on
+              if (ragged) {  // lands at this CTA's barrier: kScoutWarp passes it on
                 if (lane == 0) mbar_expect_tx(rag(nr), kStageBytes);
                 __syncwarp();
                 bar = at_rank(rag(nr), rank);
@@ -733,39 +721,84 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           v_row[1] = c_row[1];
         }
       }
-    } else if (warp == kFixWarp) {
-      // =========================================== ragged stages of V
-      // Rows of V past the list's end may hold NaN, which a zero weight does
-      // not cancel: the stage that holds the end is cleared behind it in both
-      // CTAs, and then handed to the leader's barrier.  (Pages wholly past the
-      // end are zero by TMA's out-of-range fill.)
-      uint32_t u = 0, nr = 0;  // stages before this item, ragged stages so far
+    } else if (warp == kScoutWarp) {
+      // ================ scout (leader): waits for the MMA issuer's operands
+      // A wait on an mbarrier queues behind the MMAs that the same thread has
+      // issued, and the tensor core idles until it returns: a loop that waits
+      // and issues took 610 to 670 cycles a stage of 512 (MMAs and TMA alone),
+      // one that is let in at a named barrier 530.  So this warp does the
+      // waiting and meets the issuer at one barrier a stage.  When a wait gives
+      // up it lets the issuer through what is left (on whatever shared memory
+      // holds), so that no thread is left behind at a barrier.
+      //
+      // Ragged stages of V: rows past the list's end may hold NaN, which a zero
+      // weight does not cancel.  The stage that holds the end lands at a barrier
+      // of its own CTA and is cleared behind it: by this warp in both CTAs.
+      // (Pages wholly past the end are zero by TMA's out-of-range fill.)
+      uint32_t u = 0, nt = 0, nq = 0, np = 0, nr = 0;
       bool ok = true;
-      while (ok && next(it)) {
-        const int32_t last = it.tile1 - 1;          // only the last tile can hold the end
-        const int32_t keys = it.len - last * kKeys;  // keys of it that count
-        u += (uint32_t)(it.tile1 - it.tile0) * (C::kKStages + C::kVStages);
-        if (keys >= kKeys || (keys & 127) == 0) continue;
-        for (int m = 0; m < C::kBlocks && ok; ++m, ++nr) {
-          // its V stages are the item's last; the end is in half keys / 128
-          const uint32_t s = (u - 2 * (C::kBlocks - m) + (uint32_t)(keys >> 7)) % kStages;
-          if (!(ok = W.wait(rag(nr), (nr >> 1) & 1u))) break;
-          for (int x = (keys & 127) * 8 + lane; x < 128 * 8; x += 32)
+      auto clear = [&](uint32_t s, int keys) {  // the stage's rows from keys & 127 on
+        for (int x = (keys & 127) * 8 + lane; x < 128 * 8; x += 32)
 #pragma unroll
-            for (int a = 0; a < 2; ++a)
-              asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
-                               sStage + s * kStageBytes + a * kAtom + x * 16),
-                           "r"(0u)
-                           : "memory");
-          fence_proxy_async();
-          __syncwarp();
-          if (rank != 0) {
+          for (int a = 0; a < 2; ++a)
+            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
+                             sStage + s * kStageBytes + a * kAtom + x * 16),
+                         "r"(0u)
+                         : "memory");
+        fence_proxy_async();
+        __syncwarp();
+      };
+      auto let_in = [&]() {
+        if (ok) ok = W.wait(full(u % kStages), (u / kStages) & 1u);
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + (u & 1u)) : "memory");
+        ++u;
+      };
+      while ((rank == 0 || ok) && next(it)) {
+        const int n = it.tile1 - it.tile0;
+        const int keys = it.len - (it.tile1 - 1) * kKeys;  // of the last tile, that count
+        const bool ragged = keys < kKeys && (keys & 127) != 0;
+        if (rank != 0) {
+          u += (uint32_t)n * (C::kKStages + C::kVStages);
+          for (int m = 0; ragged && m < C::kBlocks && ok; ++m, ++nr) {
+            // the item's last V stages; the end is in half keys / 128
+            if (!(ok = W.wait(rag(nr), (nr >> 1) & 1u))) break;
+            clear((u - 2 * (C::kBlocks - m) + (uint32_t)(keys >> 7)) % kStages, keys);
             if (lane == 0) mbar_release_cluster(at_rank(fixed(nr), 0));
-          } else {
-            if (!(ok = W.wait(fixed(nr), (nr >> 1) & 1u))) break;
-            if (lane == 0) mbar_arrive(full(s));
+          }
+          continue;
+        }
+        if (ok) ok = W.wait(q_full, nq & 1u);
+        for (int j = 0; j <= n; ++j) {
+          if (j < n)
+            for (int c = 0; c < C::kKStages; ++c) let_in();
+          if (j == 0) continue;
+          const uint32_t t = nt + (uint32_t)j - 1u;
+          if (ok) ok = W.wait(p_full, np++ & 1u);
+          if (ok && *objected == t + 1u) {  // withhold the product: this tile again
+            if (lane == 0) {
+              for (uint32_t r = 0; r < 2; ++r)
+                st_cluster_u32(at_rank(smem_u32(misc + 3), r), t + 1u);
+              for (uint32_t r = 0; r < 2; ++r) mbar_release_cluster(at_rank(p_done, r));
+            }
+            __syncwarp();
+            ok = W.wait(p_full, np++ & 1u);
+          }
+          if (ok && j == 1) ok = W.wait(o_empty, (nq & 1u) ^ 1u);
+          for (int c = 0; c < C::kVStages; ++c) {
+            if (ragged && j == n && (c & 1) == (keys >> 7)) {
+              if (ok) ok = W.wait(rag(nr), (nr >> 1) & 1u);
+              if (ok) {
+                clear(u % kStages, keys);
+                ok = W.wait(fixed(nr), (nr >> 1) & 1u);
+              }
+              if (ok && lane == 0) mbar_arrive(full(u % kStages));
+              ++nr;
+            }
+            let_in();
           }
         }
+        nt += (uint32_t)n;
+        ++nq;
       }
     } else if (warp == kPassWarp) {
       // ===== items to the softmax warps; this CTA's P complete -> the leader
@@ -812,84 +845,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     } else if (rank == 0) {
       // ========================================== MMA issuer (leader only)
-      // The whole warp runs the loop, so that addresses and descriptors stay
-      // uniform; one lane issues.  The queue of the tensor core is short: what
-      // the warp does between two stages leaves the pipe idle (a look at a
-      // barrier is about 100 cycles), so the next stage's barrier is looked at
-      // amid the MMAs of this one.  Descriptors: an address 16 bytes on is 1
-      // more.
-      uint32_t u = 0, nt = 0, nq = 0, np = 0;
-      bool issued = false, ok = true, ready = false;
+      // Descriptors: an address 16 bytes on is 1 more.
+      uint32_t u = 0, nt = 0;
       const uint64_t dK = sdesc_sw128(sStage, 16, 1024), dV = sdesc_sw128(sStage, kAtom, 1024);
       const uint64_t dQ = sdesc_sw128(sQ, 16, 1024), dP = sdesc_sw128(sP, 16, 1024);
       const bool one = lane == 0;
-      // eight MMAs of a stage: mma(descriptor offset of the stage, x)
+      // eight MMAs of a stage, let in by the scout: mma(descriptor offset, x)
       auto stage = [&](auto mma) {
         const uint32_t s = u % kStages;
-        if (!ready && !W.wait(full(s), (u / kStages) & 1u)) return false;
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + (u & 1u)) : "memory");
         tc_fence_after();
-        ++u;
         if (one) {
 #pragma unroll
-          for (uint32_t x = 0; x < kPeek; ++x) mma(s * (kStageBytes >> 4), x);
-        }
-        ready = __all_sync(0xffffffffu, mbar_test(full(u % kStages), (u / kStages) & 1u));
-        if (one) {
-#pragma unroll
-          for (uint32_t x = kPeek; x < 8; ++x) mma(s * (kStageBytes >> 4), x);
+          for (uint32_t x = 0; x < 8; ++x) mma(s * (kStageBytes >> 4), x);
           tc_commit2(empty(s));
         }
-        return true;
+        ++u;
       };
-      while (ok && next(it)) {
-        if (!(ok = W.wait(q_full, nq & 1u))) break;
+      while (next(it)) {
         const int n = it.tile1 - it.tile0;
-        for (int j = 0; j <= n && ok; ++j) {
+        for (int j = 0; j <= n; ++j) {
           if (j < n) {
             // the softmax has read this S^T buffer's last tile: that tile's PV,
             // which waited for it, is ahead in this order
             const uint32_t d = tmem + ((nt + (uint32_t)j) & 1u) * kRows;
-            issued = true;
 #pragma unroll
-            for (uint32_t c = 0; c < C::kKStages && ok; ++c)
-              ok = stage([&](uint32_t at, uint32_t x) {  // 64-dim atom x / 4, 16 dims each
+            for (uint32_t c = 0; c < C::kKStages; ++c)
+              stage([&](uint32_t at, uint32_t x) {  // 64-dim atom x / 4, 16 dims each
                 tc_mma2(d, dK + at + (x >> 2) * (kAtom >> 4) + (x & 3) * 2,
                         dQ + (2 * c + (x >> 2)) * 512 + (x & 3) * 2, IDESC_S,
                         c + x != 0 ? 1u : 0u);
               });
-            if (!ok) break;
             if (one) {
               if (j == n - 1) tc_commit2(q_empty);
               tc_commit2(s_full((nt + (uint32_t)j) & 1u));
             }
           }
           if (j >= 1) {
-            const uint32_t t = nt + (uint32_t)j - 1u;
-            if (!(ok = W.wait(p_full, np++ & 1u))) break;
-            if (*objected == t + 1u) {
-              if (one) {
-                for (uint32_t r = 0; r < 2; ++r)
-                  st_cluster_u32(at_rank(smem_u32(misc + 3), r), t + 1u);
-                for (uint32_t r = 0; r < 2; ++r) mbar_release_cluster(at_rank(p_done, r));
-              }
-              __syncwarp();
-              if (!(ok = W.wait(p_full, np++ & 1u))) break;
-            }
-            if (j == 1 && !(ok = W.wait(o_empty, (nq & 1u) ^ 1u))) break;
 #pragma unroll
-            for (uint32_t c = 0; c < C::kVStages && ok; ++c)
-              ok = stage([&](uint32_t at, uint32_t x) {  // 16 keys each
+            for (uint32_t c = 0; c < C::kVStages; ++c)
+              stage([&](uint32_t at, uint32_t x) {  // 16 keys each
                 tc_mma2(tO + (c >> 1) * kRows, dV + at + x * 128, dP + ((c & 1) * 8 + x) * 128,
                         IDESC_O, j > 1 || (c & 1) + x != 0 ? 1u : 0u);
               });
-            if (!ok) break;
             if (one) tc_commit2(p_done);
           }
         }
         nt += (uint32_t)n;
-        ++nq;
       }
-      if (issued) {
+      if (u > 0) {
         if (one) tc_commit2(done_bar);
         __syncwarp();
         drain(done_bar, 0, timeout_ns);
