@@ -23,14 +23,12 @@
 //   the tensor core's operand type, one rounding of each weight).
 // m of a row is a reference near its maximum, shared by the pair: the maximum
 // over the first 32 keys of the unit's first tile, afterwards raised only when
-// a score passes it by more than 2^20.  (Any reference gives the same result as long as nothing
-// overflows: the weights are floating point, and fp32 leaves 2^107 above.)  So
-// the usual tile has no exchange of maxima: P is computed while the tensor
-// cores work on the tile before, and a warp that meets a larger score objects
-// before it hands its P over.  The issuing thread then withholds the product;
-// every warp takes the exact maxima, rescales l and O^T, writes that tile's P
-// again, and the work goes on.  One read of S^T, no reduction and no barrier
-// among the softmax warps per tile.
+// a score passes it by more than 2^20.  (Any reference gives the same result as
+// long as nothing overflows: the weights are floating point, and fp32 leaves
+// 2^107 above.)  So the usual tile has no maxima to exchange.  A warp that meets
+// a larger score raises a flag; the softmax warps of the pair meet once a tile,
+// behind the tensor cores' work on the tile before, and where the flag is up
+// they take the exact maxima and rescale l and O^T before they hand P over.
 // P of rows 0-63 goes to CTA 0, of rows 64-127 to CTA 1, which is the B
 // operand's split: what crosses goes by st.async, whose bytes the receiving
 // CTA's barrier counts.  Signals between the CTAs on the usual path carry no
@@ -166,9 +164,8 @@ struct Share {
   int64_t first_cost;    // cost before request first_b
   int32_t first_b;       // request at start, or the first one
   int32_t first_unit;    // its first unit
-  int32_t prefix_tiles, prefix_len;
+  int32_t prefix_tiles;
   int32_t rows_all;      // rows of all requests
-  int32_t pad;
 };
 
 // What the softmax warps need of an item; n = 0: no more.
@@ -188,7 +185,8 @@ struct Walk {
   int32_t ub, b;
 
   __device__ __forceinline__ bool next(const Lens& L, const int32_t* prefix_table,
-                                       const int32_t* table, int max_blocks, Item& it) {
+                                       int32_t prefix_len, const int32_t* table,
+                                       int max_blocks, Item& it) {
     const int64_t end = sh->end;
     while (pos < end) {
       int64_t c0;
@@ -200,7 +198,7 @@ struct Walk {
         it.unit = u;
         it.row0 = it.rel0 = u * kRows;
         it.n_rows = min(kRows, sh->rows_all - it.row0);
-        it.len = sh->prefix_len;
+        it.len = prefix_len;
         it.pages = prefix_table;
         it.b = -1;
         share_of(c0, tiles, sh->start, end, it.tile0, it.tile1);
@@ -280,7 +278,6 @@ __device__ __forceinline__ void divide(const Lens& L, int B, int64_t T, int32_t 
     share->end = min(total, start + chunk);
     share->prefix_cost = prefix_cost;
     share->prefix_tiles = ptiles;
-    share->prefix_len = prefix_len;
     share->rows_all = last * L.H;
     share->first_b = 0;
     share->first_cost = prefix_cost;
@@ -488,10 +485,11 @@ struct PairWaiter {
 };
 
 // ------------------------------------------------------------ main kernel
-// Shared memory at D = 512: Q 64 KB, P 32 KB, four stages of 32 KB, 2 KB of
-// row constants and barriers, 1 KB to align: all of the 227 KB.
+// Shared memory at D = 512: Q 64 KB, P 32 KB, four stages of 32 KB, 2 KB of row
+// constants and barriers, 1 KB to align: all of the 227 KB; at 256 and 128 a
+// second P.
 constexpr int kStages = 4;
-constexpr int kBars = 28;
+constexpr int kBars = 32;
 
 template <int D>
 struct PCfg {
@@ -500,8 +498,10 @@ struct PCfg {
   static constexpr int kVStages = 2 * kBlocks;           // 128 keys of a block each
   static constexpr uint32_t kQBytes = 64 * D * 2;        // this CTA's 64 rows
   static constexpr uint32_t kPBytes = kKeys * 128;       // 256 keys x 64 rows
+  // P buffers: where two fit, a tile's P is written while the one before is read
+  static constexpr uint32_t kPBufs = D == 512 ? 1 : 2;
   static constexpr uint32_t kTail = 2048;
-  static constexpr uint32_t kSmem = 1024 + kQBytes + kPBytes + kStages * kStageBytes + kTail;
+  static constexpr uint32_t kSmem = 1024 + kQBytes + kPBufs * kPBytes + kStages * kStageBytes + kTail;
   static_assert(kSmem <= 232448, "shared memory");
   // at most two ragged V stages are in flight (rag and fixed barriers)
   static_assert(2 * (kKStages + kVStages) >= kStages, "ragged stages in flight");
@@ -563,13 +563,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint8_t* gb = smem_raw + (base - raw);
   const uint32_t sQ = base;
   const uint32_t sP = sQ + C::kQBytes;
-  const uint32_t sStage = sP + C::kPBytes;
-  uint8_t* tail = gb + C::kQBytes + C::kPBytes + kStages * kStageBytes;
+  const uint32_t sStage = sP + C::kPBufs * C::kPBytes;
+  uint8_t* tail = gb + C::kQBytes + C::kPBufs * C::kPBytes + kStages * kStageBytes;
   float* nm2_s = reinterpret_cast<float*>(tail);          // [item & 1][row] -m
   float* nmo_s = nm2_s + 2 * kRows;                       // [row] -m before it was last raised
   uint8_t* lim_s = reinterpret_cast<uint8_t*>(nmo_s + kRows);  // [row] keys past lim_min
   uint64_t* bars = reinterpret_cast<uint64_t*>(lim_s + kRows);
-  uint32_t* misc = reinterpret_cast<uint32_t*>(bars + kBars);  // abort, tmem, objected, redo
+  uint32_t* misc = reinterpret_cast<uint32_t*>(bars + kBars);  // abort, tmem, beyond
   Share* share = reinterpret_cast<Share*>(misc + 4);
   Post* posts = reinterpret_cast<Post*>(share + 1);            // [2]
   static_assert(3 * kRows * 4 + kRows + kBars * 8 + 16 + sizeof(Share) + 2 * sizeof(Post) <= C::kTail,
@@ -588,21 +588,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t q_full = bx;                                     // leader
   const uint32_t q_empty = bx + 8;
   auto s_full = [&](uint32_t b) { return bx + 16 + 8 * b; };
-  const uint32_t p_in = bx + 32;     // this CTA's P is written
-  const uint32_t p_full = bx + 40;   // leader: both CTAs' P are
-  const uint32_t p_done = bx + 48;
-  const uint32_t o_empty = bx + 56;  // leader
-  const uint32_t xs = bx + 64;       // the softmax warps of both CTAs
-  const uint32_t grp = bx + 72;      // the softmax warps of this CTA
-  const uint32_t done_bar = bx + 80;
-  auto rag = [&](uint32_t r) { return bx + 88 + 8 * (r & 1u); };      // own ragged V stage
-  auto fixed = [&](uint32_t r) { return bx + 104 + 8 * (r & 1u); };   // leader: the other's is
-  auto post_full = [&](uint32_t i) { return bx + 120 + 8 * (i & 1u); };
-  auto post_free = [&](uint32_t i) { return bx + 136 + 8 * (i & 1u); };
-  const uint32_t refs = bx + 152;    // a unit's first references
-  static_assert(2 * kStages + 20 <= kBars, "barriers");
-  // tile number + 1 of the last tile objected to (leader), to be done again
-  volatile uint32_t *objected = misc + 2, *redo = misc + 3;
+  auto p_in = [&](uint32_t t) { return bx + 32 + 8 * (t & 1u); };     // own P is written
+  auto p_full = [&](uint32_t t) { return bx + 48 + 8 * (t & 1u); };   // leader: both CTAs' are
+  auto p_done = [&](uint32_t t) { return bx + 64 + 8 * (t & 1u); };   // and have been read
+  const uint32_t o_empty = bx + 80;  // leader
+  const uint32_t xs = bx + 88;       // the softmax warps of both CTAs
+  const uint32_t grp = bx + 96;      // the softmax warps of this CTA
+  const uint32_t done_bar = bx + 104;
+  auto rag = [&](uint32_t r) { return bx + 112 + 8 * (r & 1u); };     // own ragged V stage
+  auto fixed = [&](uint32_t r) { return bx + 128 + 8 * (r & 1u); };   // leader: the other's is
+  auto post_full = [&](uint32_t i) { return bx + 144 + 8 * (i & 1u); };
+  auto post_free = [&](uint32_t i) { return bx + 160 + 8 * (i & 1u); };
+  const uint32_t refs = bx + 176;    // a unit's first references
+  static_assert(2 * kStages + 23 <= kBars, "barriers");
+  // phase parity of a barrier that serves every other tile, in tile t
+  auto turn = [](uint32_t t) { return (t >> 1) & 1u; };
+  // tile number + 1 of the last tile with a score beyond its reference
+  volatile uint32_t* beyond_s = misc + 2;
   const PairWaiter W{misc, at_rank(smem_u32(misc), peer), status, timeout_ns};
 
   if (tid == 0) {
@@ -614,20 +616,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(q_empty, 1);
     for (uint32_t b = 0; b < 2; ++b) {
       mbar_init(s_full(b), 1);
+      mbar_init(p_in(b), kSoftWarps / 2 + 1);
+      mbar_init(p_full(b), 2);
+      mbar_init(p_done(b), 1);
       mbar_init(rag(b), 1);
       mbar_init(fixed(b), 1);
       mbar_init(post_full(b), 1);
       mbar_init(post_free(b), kSoftWarps);
     }
-    mbar_init(p_in, kSoftWarps / 2 + 1);
-    mbar_init(p_full, 2);
-    mbar_init(p_done, 1);
     mbar_init(o_empty, 2 * kSoftWarps);
     mbar_init(xs, 2 * kSoftWarps);
     mbar_init(grp, kSoftWarps);
     mbar_init(refs, kRows / kGroupRows);
     mbar_init(done_bar, 1);
-    misc[0] = misc[2] = misc[3] = 0u;
+    misc[0] = misc[2] = 0u;
     fence_mbar_init();
     prefetch_tensormap(&q_map);
     prefetch_tensormap(&k_map);
@@ -648,7 +650,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync_all();
   tc_fence_after();
   Walk walk{share, share->start, share->first_cost, share->first_unit, share->first_b};
-  auto next = [&](Item& i) { return walk.next(L, prefix_table, table, max_blocks, i); };
+  auto next = [&](Item& i) {
+    return walk.next(L, prefix_table, prefix_len, table, max_blocks, i);
+  };
   constexpr uint32_t tmem = 0;  // an allocation of all 512 columns starts at column 0
   constexpr uint32_t tO = tmem + 2 * kRows;
   Item it;
@@ -749,7 +753,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // weight does not cancel.  The stage that holds the end lands at a barrier
       // of its own CTA and is cleared behind it: by this warp in both CTAs.
       // (Pages wholly past the end are zero by TMA's out-of-range fill.)
-      uint32_t u = 0, nt = 0, nq = 0, np = 0, nr = 0;
+      uint32_t u = 0, nt = 0, nq = 0, nr = 0;
       bool ok = true;
       auto clear = [&](uint32_t s, int keys) {  // the stage's rows from keys & 127 on
         for (int x = (keys & 127) * 8 + lane; x < 128 * 8; x += 32)
@@ -787,16 +791,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int c = 0; c < C::kKStages; ++c) let_in();
           if (j == 0) continue;
           const uint32_t t = nt + (uint32_t)j - 1u;
-          if (ok) ok = W.wait(p_full, np++ & 1u);
-          if (ok && *objected == t + 1u) {  // withhold the product: this tile again
-            if (lane == 0) {
-              for (uint32_t r = 0; r < 2; ++r)
-                st_cluster_u32(at_rank(smem_u32(misc + 3), r), t + 1u);
-              for (uint32_t r = 0; r < 2; ++r) mbar_release_cluster(at_rank(p_done, r));
-            }
-            __syncwarp();
-            ok = W.wait(p_full, np++ & 1u);
-          }
+          if (ok) ok = W.wait(p_full(t), turn(t));
           if (ok && j == 1) ok = W.wait(o_empty, (nq & 1u) ^ 1u);
           for (int c = 0; c < C::kVStages; ++c) {
             if (ragged && j == n && (c & 1) == (keys >> 7)) {
@@ -816,9 +811,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     } else if (warp == kPassWarp) {
       // ===== items to the softmax warps; this CTA's P complete -> the leader
-      uint32_t nt = 0, np = 0, ni = 0;  // tiles, times that a P was handed over, items
+      uint32_t nt = 0, ni = 0;  // tiles, items
       bool ok = true;
-      const uint32_t lead_p = at_rank(p_full, 0);
       Post cur, nxt;
       auto post = [&]() {  // the next item, one ahead of its tiles
         nxt.n = 0;
@@ -843,19 +837,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // bytes from the other CTA's keys, if this CTA's group has rows
         const uint32_t bytes =
             cur.n_rows > kGroupRows * (int)rank ? 128 * kGroupRows * 2 : 0;
-        for (int32_t j = 0; j < cur.n && ok; ++j, ++nt)
-          for (int time = 0; time < 2; ++time) {
-            if (lane == 0) mbar_expect_tx(p_in, bytes);
-            if (!(ok = W.wait(p_in, np & 1u))) break;
-            if (lane == 0) {
-              fence_proxy_async();
-              mbar_signal(lead_p);
-            }
-            __syncwarp();
-            if (!(ok = W.wait(p_done, np & 1u))) break;
-            ++np;
-            if (*redo != nt + 1u) break;
+        for (int32_t j = 0; j < cur.n; ++j, ++nt) {
+          if (lane == 0) mbar_expect_tx(p_in(nt), bytes);
+          if (!(ok = W.wait(p_in(nt), turn(nt)))) break;
+          if (lane == 0) {
+            fence_proxy_async();
+            mbar_signal(at_rank(p_full(nt), 0));
           }
+          __syncwarp();
+        }
       }
     } else if (rank == 0) {
       // ========================================== MMA issuer (leader only)
@@ -895,13 +885,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
           if (j >= 1) {
+            const uint32_t t = nt + (uint32_t)j - 1u;
+            const uint64_t db = dP + (t & (C::kPBufs - 1)) * (C::kPBytes >> 4);
 #pragma unroll
             for (uint32_t c = 0; c < C::kVStages; ++c)
               stage([&](uint32_t at, uint32_t x) {  // 16 keys each
-                tc_mma2(tO + (c >> 1) * kRows, dV + at + x * 128, dP + ((c & 1) * 8 + x) * 128,
+                tc_mma2(tO + (c >> 1) * kRows, dV + at + x * 128, db + ((c & 1) * 8 + x) * 128,
                         IDESC_O, j > 1 || (c & 1) + x != 0 ? 1u : 0u);
               });
-            if (elect_one()) tc_commit2(p_done);
+            if (elect_one()) tc_commit2(p_done(t));
           }
         }
         nt += (uint32_t)n;
@@ -921,10 +913,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
     const uint32_t owner = (uint32_t)g;  // the CTA that holds P of these rows
     const uint32_t p_row = (owner == rank ? sP : at_rank(sP, peer)) + (uint32_t)key * 128u;
-    const uint32_t p_in_peer = at_rank(p_in, peer);
     const uint32_t p_sw = (uint32_t)(key & 7);
     const uint64_t scale2 = pair2(scale_log2, scale_log2);
-    uint32_t nx = 0, nf = 0, ng = 0, nt = 0, np = 0;
+    uint32_t nx = 0, nf = 0, ng = 0, nt = 0;
+    // all softmax warps of the pair; `publish`: with this warp's writes to both
+    // CTAs before it
+    auto pair_sync = [&](bool publish) {
+      __syncwarp();
+      if (lane == 0) {
+        if (publish) fence_cluster();
+        mbar_signal(at_rank(xs, rank));
+        mbar_signal(at_rank(xs, peer));
+      }
+      return W.wait(xs, nx++ & 1u);
+    };
     auto group_sync = [&]() {  // all softmax warps of this CTA
       __syncwarp();
       if (lane == 0) mbar_arrive(grp);
@@ -1003,8 +1005,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         return W.wait(refs, nf++ & 1u);
       };
-      // After an objection: the references of the rows where tile j (S^T in
-      // buffer b) passes them by more than the slack become its exact maxima
+      // The references of the rows where tile j (S^T in buffer b) passes them by
+      // more than the slack become its exact maxima
       auto raise = [&](int j, uint32_t b) {
         const int32_t pos = (tile0 + j) * kKeys + key;
 #pragma unroll 1
@@ -1027,12 +1029,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             red[at] = t;
           }
         }
-        __syncwarp();
-        if (lane == 0) {
-          mbar_signal(at_rank(xs, rank));
-          mbar_release_cluster(at_rank(xs, peer));
-        }
-        if (!W.wait(xs, nx++ & 1u)) return false;
+        if (!pair_sync(true)) return false;
         if (tid < kRows) {
           float by = red[tid];
 #pragma unroll
@@ -1045,8 +1042,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       };
       // P of tile j from S^T in buffer b, the largest s - m, and l.  Weights of 16
       // rows among which one passes the slack are left out of l, which so
-      // stays finite; the tile is objected to, and the weights are added when
-      // it is visited again (`revisit`) under references that hold them.
+      // stays finite, and are added when the tile is visited again (`revisit`)
+      // under references that hold them.
       auto weights = [&](int j, uint32_t b, bool revisit) {
         over = -INFINITY;
         if (!live) return;
@@ -1111,27 +1108,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // P into the CTA that owns the rows; what crosses is counted by its bytes
       auto hand_over = [&]() {
         tc_fence_before();  // S^T has been read
+        const uint32_t p_to = p_row + (nt & (C::kPBufs - 1)) * C::kPBytes;
+        const uint32_t counts = at_rank(p_in(nt), peer);
         if (live) {
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            const uint32_t a = p_row + (((uint32_t)c ^ p_sw) << 4);
+            const uint32_t a = p_to + (((uint32_t)c ^ p_sw) << 4);
             const uint32_t w[4] = {pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]};
             if (owner == rank)
               asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(w[0]),
                            "r"(w[1]), "r"(w[2]), "r"(w[3])
                            : "memory");
             else
-              st_async_v4(a, w, p_in_peer);
+              st_async_v4(a, w, counts);
           }
         }
         if (owner == rank) {
           fence_proxy_async();  // P -> the tensor core's reads
           __syncwarp();
-          if (lane == 0) mbar_arrive(p_in);
+          if (lane == 0) mbar_arrive(p_in(nt));
         }
       };
       // l and O^T times 2^(m_old - m_new)
-      auto rescale = [&]() {
+      auto rescale = [&](bool o_too) {
         bool any = false;
 #pragma unroll
         for (int h = 0; h < kGroupRows / 2; ++h) {
@@ -1142,7 +1141,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           unpair2(l[h], x, y);
           l[h] = pair2(x * ex2(a), y * ex2(c));
         }
-        if (!any || !live) return;  // the same in every lane
+        if (!any || !live || !o_too) return;  // the same in every lane
 #pragma unroll 1
         for (int c = 0; c < 4 * C::kBlocks; ++c) {
           uint32_t r[16];
@@ -1158,52 +1157,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tmem_wait_st();
       };
 
-      // Step j: P of tile j, then the verdict on tile j-1 (done, or to be done
-      // again), then tile j's P is handed over; step n: the last verdict alone.
-      for (int j = 0; j <= n && ok; ++j) {
-        if (j < n) {
-          if (!(ok = W.wait(s_full(nt & 1u), (nt >> 1) & 1u))) break;
+      for (int j = 0; j < n; ++j, ++nt) {
+        const uint32_t b = nt & 1u;
+        if (!(ok = W.wait(s_full(b), turn(nt)))) break;
+        tc_fence_after();
+        if (j == 0 && !(ok = first_refs(b))) break;
+        for (bool revisit = false;; revisit = true) {
+          weights(j, b, revisit);
+          if (revisit) break;
+          const bool beyond = __any_sync(0xffffffffu, over > kSlack);
+          if (beyond && lane == 0) {
+            st_cluster_u32(at_rank(smem_u32(misc + 2), 0), nt + 1u);
+            st_cluster_u32(at_rank(smem_u32(misc + 2), 1), nt + 1u);
+          }
+          if (!(ok = pair_sync(beyond))) break;
+          if (*beyond_s != nt + 1u) break;
+          // O^T holds every tile before this one
+          if (j > 0 && !(ok = W.wait(p_done(nt - 1u), turn(nt - 1u)))) break;
           tc_fence_after();
+          if (!(ok = raise(j, b))) break;
+          rescale(j > 0);
         }
-        int jw = j;            // tile of this pass
-        bool renew = j == 0;   // take references from it first
-        bool asked = j == 0;   // the verdict is known
-        bool revisit = false;
-        for (;;) {
-          const uint32_t b = (nt + (uint32_t)(jw - j)) & 1u;
-          if (renew) {
-            if (!(ok = j == 0 ? first_refs(b) : raise(jw, b))) break;
-            if (j > 0) rescale();
-          }
-          if (jw < n) weights(jw, b, revisit);
-          if (!asked) {
-            asked = true;
-            if (!(ok = W.wait(p_done, np++ & 1u))) break;
-            tc_fence_after();
-            if (*redo == nt) {
-              jw = j - 1;
-              renew = revisit = true;
-              continue;
-            }
-          }
-          if (jw == n) break;
-          if (jw == j && __any_sync(0xffffffffu, over > kSlack)) {
-            if (lane == 0) {
-              st_cluster_u32(at_rank(smem_u32(misc + 2), 0), nt + 1u);
-              fence_cluster();
-            }
-            __syncwarp();
-          }
-          hand_over();
-          if (jw == j) break;
-          if (!(ok = W.wait(p_done, np++ & 1u))) break;
-          tc_fence_after();
-          jw = j;
-          renew = false;
-        }
-        if (j < n) ++nt;
+        if (!ok) break;
+        // the P buffer's last tile has been read
+        if (nt >= C::kPBufs && !(ok = W.wait(p_done(nt - C::kPBufs), turn(nt - C::kPBufs)))) break;
+        hand_over();
       }
-      if (!ok) break;
+      if (!ok || !(ok = W.wait(p_done(nt - 1u), turn(nt - 1u)))) break;
+      tc_fence_after();
       // ---- epilogue: m, l and O of this (unit, pair) to its slot
       const int64_t slot = (int64_t)post->unit + pair;
       const int n_rows = post->n_rows;
