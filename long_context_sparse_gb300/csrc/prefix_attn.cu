@@ -43,6 +43,7 @@
 // l (fp32, not normalised) in a slot of the workspace, and a second kernel
 // joins each row's slots: sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
 #include <atomic>
+#include <type_traits>
 
 #include "attn_common.cuh"
 #include "dsa_internal.h"
@@ -455,6 +456,31 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+// 32 columns of this thread's TMEM lane; the values are there after the wait,
+// which the compiler sees as writing them.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
 }
 
 // Bounded waits of the pair: as Waiter, with cluster scope; a failure stops
@@ -955,7 +981,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int h = 0; h < 32; ++h) l[h] = 0ull;
       uint32_t pk[32];  // this thread's P, bf16 pairs
-      float over = 0.f;
 
       // The first references: the maxima over the unit's first 32 keys, which
       // every row that sees a key sees one of.  One warp a group has them and
@@ -1040,70 +1065,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         return group_sync();
       };
-      // P of tile j from S^T in buffer b, the largest s - m, and l.  Weights of 16
-      // rows among which one passes the slack are left out of l, which so
-      // stays finite, and are added when the tile is visited again (`revisit`)
-      // under references that hold them.
-      auto weights = [&](int j, uint32_t b, bool revisit) {
-        over = -INFINITY;
-        if (!live) return;
+      // P of tile j from S^T in buffer b, whether a score is beyond its
+      // reference, and l.  The weights of 32 rows among which one is beyond are
+      // left out of l, which so stays finite, and are added when the tile is
+      // visited again (`revisit`) under references that hold them.  `Plain`: no
+      // mask, first visit; without branches, so that the work on one half of
+      // the rows overlaps the other's loads.
+      uint32_t left = 0;
+      auto weights = [&](auto plain, int j, uint32_t b, bool revisit) {
+        constexpr bool Plain = decltype(plain)::value;
         const int32_t pos = (tile0 + j) * kKeys + key;
-        const bool masked = (tile0 + j + 1) * kKeys > lim_min;  // uniform
-        // the next 16 columns and their references are on the way while these
-        // are worked on: with MMAs and TMA at shared memory, a load from it
-        // takes 100 to 200 cycles
-        uint32_t rr[2][16];
+        const bool masked = !Plain && (tile0 + j + 1) * kKeys > lim_min;  // uniform
+        uint32_t r[2][32];
         const uint32_t tS = tmem + b * kRows + lane_base + r0;
         const ulonglong2* refs2 = reinterpret_cast<const ulonglong2*>(nm_s + r0);
-        tmem_ld16(tS, rr[0]);
+        tmem_ld32(tS, r[0]);
+        bool any = false;
+        const uint32_t out_before = left;
+        left = 0;
 #pragma unroll
-        for (int h0 = 0; h0 < kGroupRows; h0 += 16) {
-          uint32_t(&r)[16] = rr[(h0 / 16) & 1];
-          ulonglong2 c[4];
+        for (int h = 0; h < 2; ++h) {
+          ulonglong2 c[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) c[e] = refs2[h0 / 4 + e];
-          tmem_wait_ld_dep(r);
-          if (h0 + 16 < kGroupRows) tmem_ld16(tS + h0 + 16, rr[(h0 / 16 + 1) & 1]);
-          float d[16];
+          for (int e = 0; e < 8; ++e) c[e] = refs2[8 * h + e];
+          tmem_wait_ld32(r[h]);
+          if (h == 0) tmem_ld32(tS + 32, r[1]);
+          float d[32];
 #pragma unroll
-          for (int e = 0; e < 16; e += 4) {
-            unpair2(fma2(pair2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), scale2,
+          for (int e = 0; e < 32; e += 4) {
+            unpair2(fma2(pair2(__uint_as_float(r[h][e]), __uint_as_float(r[h][e + 1])), scale2,
                          c[e / 4].x),
                     d[e], d[e + 1]);
-            unpair2(fma2(pair2(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])), scale2,
-                         c[e / 4].y),
+            unpair2(fma2(pair2(__uint_as_float(r[h][e + 2]), __uint_as_float(r[h][e + 3])),
+                         scale2, c[e / 4].y),
                     d[e + 2], d[e + 3]);
           }
-          if (masked) {
+          if (!Plain && masked) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (pos >= lim_min + lim_s[r0 + h0 + e]) d[e] = -INFINITY;
+            for (int e = 0; e < 32; ++e)
+              if (pos >= lim_min + lim_s[r0 + 32 * h + e]) d[e] = -INFINITY;
           }
-          float top = -INFINITY;
+          float top[4];
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) top = fmaxf(top, fmaxf(d[e], d[e + 1]));
-          bool add = !(top > kSlack);
-          if (revisit) {  // those that were left out under the references before
-            float old = -INFINITY;
+          for (int e = 0; e < 4; ++e) top[e] = d[e];
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (!masked || pos < lim_min + lim_s[r0 + h0 + e])
-                old = fmaxf(old, fmaf(__uint_as_float(r[e]), scale_log2, nmo_s[r0 + h0 + e]));
-            add = add && old > kSlack;
-          }
-          over = fmaxf(over, top);
+          for (int e = 4; e < 32; e += 8)
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            d[e] = ex2(d[e]);
-            d[e + 1] = ex2(d[e + 1]);
-            pk[(h0 + e) / 2] = pack_bf16(d[e], d[e + 1]);
-          }
-          if (add) {
+            for (int y = 0; y < 4; ++y)
+              top[y] = e + 4 < 32 ? fmaxf(top[y], fmaxf(d[e + y], d[e + 4 + y]))
+                                  : fmaxf(top[y], d[e + y]);
+          const bool beyond = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > kSlack;
+          any |= beyond;
+          left |= beyond ? 1u << h : 0u;
+          const bool add = !beyond && (Plain || !revisit || (out_before >> h & 1u) != 0u);
 #pragma unroll
-            for (int e = 0; e < 16; e += 2)
-              l[(h0 + e) / 2] = add2(l[(h0 + e) / 2], pair2(d[e], d[e + 1]));
+          for (int e = 0; e < 32; e += 2) {
+            const float p0 = ex2(d[e]), p1 = ex2(d[e + 1]);
+            pk[16 * h + e / 2] = pack_bf16(p0, p1);
+            if (add) l[16 * h + e / 2] = add2(l[16 * h + e / 2], pair2(p0, p1));
           }
         }
+        return any;
       };
       // P into the CTA that owns the rows; what crosses is counted by its bytes
       auto hand_over = [&]() {
@@ -1163,9 +1185,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (j == 0 && !(ok = first_refs(b))) break;
         for (bool revisit = false;; revisit = true) {
-          weights(j, b, revisit);
+          bool beyond = false;
+          if (live)
+            beyond = !revisit && (tile0 + j + 1) * kKeys <= lim_min
+                         ? weights(std::true_type{}, j, b, false)
+                         : weights(std::false_type{}, j, b, revisit);
           if (revisit) break;
-          const bool beyond = __any_sync(0xffffffffu, over > kSlack);
+          beyond = __any_sync(0xffffffffu, beyond);
           if (beyond && lane == 0) {
             st_cluster_u32(at_rank(smem_u32(misc + 2), 0), nt + 1u);
             st_cluster_u32(at_rank(smem_u32(misc + 2), 1), nt + 1u);
