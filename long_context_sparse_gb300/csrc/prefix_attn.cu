@@ -148,9 +148,15 @@ __device__ __forceinline__ void share_of(int64_t c0, int32_t tiles, int64_t s, i
   z = hi > 0 ? (int32_t)hi : 0;
 }
 
+// The tiles of an item are taken in turn from `rot` on, wrapping around, so that
+// the pairs, which walk other row blocks of the same prefix, are at the same
+// tile at the same time (each tile then comes from HBM once, whatever the
+// prefix's length): the tile at cost t of a share is t modulo the shorter of a
+// share and a unit, where the item has it.
 struct Item {
   int32_t unit;
   int32_t tile0, tile1;   // tiles [tile0, tile1) of the unit
+  int32_t rot;            // its first turn
   int32_t row0, n_rows;   // first row of the block, rows of it that count
   int32_t len;            // keys of the list
   const int32_t* pages;   // its page list
@@ -169,10 +175,16 @@ struct Share {
   int32_t rows_all;      // rows of all requests
 };
 
+// The tile of an item's turn j.
+__device__ __forceinline__ int32_t tile_at(int32_t tile0, int32_t n, int32_t rot, int32_t j) {
+  const int32_t x = j + rot;
+  return tile0 + (x < n ? x : x - n);
+}
+
 // What the softmax warps need of an item; n = 0: no more.
 struct Post {
   int32_t tile0, n;     // first tile, tiles
-  int32_t len;          // keys of the list
+  int32_t rot;          // first turn
   int32_t lim_min;      // keys that every row of the block sees
   int32_t n_rows, unit;
   int32_t b, rel0;
@@ -203,7 +215,13 @@ struct Walk {
         it.pages = prefix_table;
         it.b = -1;
         share_of(c0, tiles, sh->start, end, it.tile0, it.tile1);
+        const int64_t turn = min(end - sh->start, (int64_t)tiles + kUnitCost);
+        const int64_t ahead = c0 + kUnitCost - sh->start;
+        const int64_t x = ahead < 0 ? -ahead : ahead, y = x - quotient(x, turn) * turn;
+        it.rot = (int32_t)(ahead < 0 && y ? turn - y : y);
+        if (it.rot >= it.tile1 - it.tile0) it.rot = 0;
       } else {
+        it.rot = 0;
         ReqShape r = req_shape(L, b);
         for (;;) {
           const int32_t units = unit_count(r);
@@ -709,11 +727,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // page of key `half * 128 + key0` of tile j (0 where nothing is read)
         auto page_at = [&](int32_t j, int half) {
           const int32_t pos = j * kKeys + half * 128 + key0;
-          return j < it.tile1 && pos < it.len ? __ldg(it.pages + (pos >> page_log2)) : 0;
+          return pos < it.len ? __ldg(it.pages + (pos >> page_log2)) : 0;
         };
         // its first cache row, or out of range past the end
         auto row_of = [&](int32_t j, int half, int32_t p) {
-          if (j >= it.tile1 || j * kKeys + half * 128 + key0 >= it.len) return n_rows_cache;
+          if (j * kKeys + half * 128 + key0 >= it.len) return n_rows_cache;
           if (p < 0 || p >= n_pages) {
             latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
             return n_rows_cache;
@@ -721,12 +739,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           return p << page_log2;
         };
         int32_t v_row[2] = {n_rows_cache, n_rows_cache};
-        int32_t page[2] = {page_at(it.tile0, 0), page_at(it.tile0, 1)};
-        for (int32_t j = it.tile0; j <= it.tile1 && ok; ++j) {
-          const int32_t c_row[2] = {row_of(j, 0, page[0]), row_of(j, 1, page[1])};
-          page[0] = page_at(j + 1, 0);  // looked at in the next round
-          page[1] = page_at(j + 1, 1);
-          if (j < it.tile1) {  // K of tile j
+        const int32_t n = it.tile1 - it.tile0;
+        int32_t tile = it.tile0 + it.rot, last = 0;  // this turn's tile, the turn's before
+        int32_t page[2] = {page_at(tile, 0), page_at(tile, 1)};
+        for (int32_t j = 0; j <= n && ok; ++j) {
+          const int32_t c_row[2] = {row_of(tile, 0, page[0]), row_of(tile, 1, page[1])};
+          const int32_t ahead = tile_at(it.tile0, n, it.rot, j + 1 < n ? j + 1 : 0);
+          page[0] = page_at(ahead, 0);  // looked at in the next round
+          page[1] = page_at(ahead, 1);
+          if (j < n) {  // K of this turn's tile
             const int32_t row = rank ? c_row[1] : c_row[0];
 #pragma unroll 1
             for (int a = 0; a < C::kKStages; ++a, ++u) {
@@ -738,8 +759,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                               lead_full + 8u * s);
             }
           }
-          if (j > it.tile0 && ok) {  // V of tile j-1
-            const int32_t left0 = it.len - (j - 1) * kKeys;
+          if (j > 0 && ok) {  // V of the turn's before
+            const int32_t left0 = it.len - last * kKeys;
 #pragma unroll 1
             for (int x = 0; x < C::kVStages; ++x, ++u) {
               const uint32_t s = u % kStages;
@@ -763,6 +784,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           v_row[0] = c_row[0];
           v_row[1] = c_row[1];
+          last = tile;
+          tile = ahead;
         }
       }
     } else if (warp == kScoutWarp) {
@@ -801,14 +824,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int n = it.tile1 - it.tile0;
         const int keys = it.len - (it.tile1 - 1) * kKeys;  // of the last tile, that count
         const bool ragged = keys < kKeys && (keys & 127) != 0;
+        const int jr = n - 1 - it.rot;                     // the last tile's turn
         if (rank != 0) {
-          u += (uint32_t)n * (C::kKStages + C::kVStages);
-          for (int m = 0; ragged && m < C::kBlocks && ok; ++m, ++nr) {
-            // the item's last V stages; the end is in half keys / 128
+          // its V stages; the end is in half keys / 128 of each block
+          const uint32_t v = u + (uint32_t)(min(jr + 2, n) * C::kKStages + jr * C::kVStages) +
+                             (uint32_t)(keys >> 7);
+          for (uint32_t m = 0; ragged && m < C::kBlocks && ok; ++m, ++nr) {
             if (!(ok = W.wait(rag(nr), (nr >> 1) & 1u))) break;
-            clear((u - 2 * (C::kBlocks - m) + (uint32_t)(keys >> 7)) % kStages, keys);
+            clear((v + 2 * m) % kStages, keys);
             if (lane == 0) mbar_release_cluster(at_rank(fixed(nr), 0));
           }
+          u += (uint32_t)n * (C::kKStages + C::kVStages);
           continue;
         }
         if (ok) ok = W.wait(q_full, nq & 1u);
@@ -820,7 +846,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (ok) ok = W.wait(p_full(t), turn(t));
           if (ok && j == 1) ok = W.wait(o_empty, (nq & 1u) ^ 1u);
           for (int c = 0; c < C::kVStages; ++c) {
-            if (ragged && j == n && (c & 1) == (keys >> 7)) {
+            if (ragged && j - 1 == jr && (c & 1) == (keys >> 7)) {
               if (ok) ok = W.wait(rag(nr), (nr >> 1) & 1u);
               if (ok) {
                 clear(u % kStages, keys);
@@ -843,7 +869,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       auto post = [&]() {  // the next item, one ahead of its tiles
         nxt.n = 0;
         if (next(it)) {
-          nxt = Post{it.tile0, it.tile1 - it.tile0, it.len, it.len, it.n_rows, it.unit, it.b,
+          nxt = Post{it.tile0, it.tile1 - it.tile0, it.rot, it.len, it.n_rows, it.unit, it.b,
                      it.rel0};
           if (it.b >= 0) nxt.lim_min = row_limit(req_shape(L, it.b), L.H, it.rel0);
         }
@@ -964,7 +990,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const volatile Post* post = posts + (ni & 1u);
       const int n = post->n;
       if (n == 0) break;
-      const int32_t tile0 = post->tile0, lim_min = post->lim_min;
+      const int32_t tile0 = post->tile0, rot = post->rot, lim_min = post->lim_min;
       const bool live = post->n_rows > r0;  // this group has rows that count
       // references in turns: the other CTA may still read the last item's when
       // this item's arrive there
@@ -982,13 +1008,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int h = 0; h < 32; ++h) l[h] = 0ull;
       uint32_t pk[32];  // this thread's P, bf16 pairs
 
-      // The first references: the maxima over the unit's first 32 keys, which
-      // every row that sees a key sees one of.  One warp a group has them and
-      // tells both CTAs.
-      auto first_refs = [&](uint32_t b) {
+      // The first references: the maxima over the first 32 keys of the item's
+      // first tile, which every row that sees a key of the item sees one of (the
+      // requests' own tokens, of which some rows see few, are taken in order).
+      // One warp a group has them and tells both CTAs.
+      auto first_refs = [&](int32_t tile, uint32_t b) {
         if (rank == 0 && quad == 0) {
-          const int32_t pos = tile0 * kKeys + lane;
-          const bool masked = tile0 * kKeys + 32 > lim_min;  // uniform
+          const int32_t pos = tile * kKeys + lane;
+          const bool masked = tile * kKeys + 32 > lim_min;  // uniform
           // 16 rows at a time, the four reductions side by side (a shuffle waits
           // at shared memory's door like a load)
           float x[kGroupRows / 16][16];
@@ -1030,10 +1057,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         return W.wait(refs, nf++ & 1u);
       };
-      // The references of the rows where tile j (S^T in buffer b) passes them by
+      // The references of the rows where a tile (S^T in buffer b) passes them by
       // more than the slack become its exact maxima
-      auto raise = [&](int j, uint32_t b) {
-        const int32_t pos = (tile0 + j) * kKeys + key;
+      auto raise = [&](int32_t tile, uint32_t b) {
+        const int32_t pos = tile * kKeys + key;
 #pragma unroll 1
         for (int h0 = r0; h0 < r0 + kGroupRows; h0 += 16) {
           float x[16];
@@ -1065,17 +1092,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         return group_sync();
       };
-      // P of tile j from S^T in buffer b, whether a score is beyond its
+      // P of a tile from S^T in buffer b, whether a score is beyond its
       // reference, and l.  The weights of 32 rows among which one is beyond are
       // left out of l, which so stays finite, and are added when the tile is
       // visited again (`revisit`) under references that hold them.  `Plain`: no
       // mask, first visit; without branches, so that the work on one half of
       // the rows overlaps the other's loads.
       uint32_t left = 0;
-      auto weights = [&](auto plain, int j, uint32_t b, bool revisit) {
+      auto weights = [&](auto plain, int32_t tile, uint32_t b, bool revisit) {
         constexpr bool Plain = decltype(plain)::value;
-        const int32_t pos = (tile0 + j) * kKeys + key;
-        const bool masked = !Plain && (tile0 + j + 1) * kKeys > lim_min;  // uniform
+        const int32_t pos = tile * kKeys + key;
+        const bool masked = !Plain && (tile + 1) * kKeys > lim_min;  // uniform
         uint32_t r[2][32];
         const uint32_t tS = tmem + b * kRows + lane_base + r0;
         const ulonglong2* refs2 = reinterpret_cast<const ulonglong2*>(nm_s + r0);
@@ -1181,15 +1208,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
       for (int j = 0; j < n; ++j, ++nt) {
         const uint32_t b = nt & 1u;
+        const int32_t tile = tile_at(tile0, n, rot, j);
         if (!(ok = W.wait(s_full(b), turn(nt)))) break;
         tc_fence_after();
-        if (j == 0 && !(ok = first_refs(b))) break;
+        if (j == 0 && !(ok = first_refs(tile, b))) break;
         for (bool revisit = false;; revisit = true) {
           bool beyond = false;
           if (live)
-            beyond = !revisit && (tile0 + j + 1) * kKeys <= lim_min
-                         ? weights(std::true_type{}, j, b, false)
-                         : weights(std::false_type{}, j, b, revisit);
+            beyond = !revisit && (tile + 1) * kKeys <= lim_min
+                         ? weights(std::true_type{}, tile, b, false)
+                         : weights(std::false_type{}, tile, b, revisit);
           if (revisit) break;
           beyond = __any_sync(0xffffffffu, beyond);
           if (beyond && lane == 0) {
@@ -1201,7 +1229,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // O^T holds every tile before this one
           if (j > 0 && !(ok = W.wait(p_done(nt - 1u), turn(nt - 1u)))) break;
           tc_fence_after();
-          if (!(ok = raise(j, b))) break;
+          if (!(ok = raise(tile, b))) break;
           rescale(j > 0);
         }
         if (!ok) break;
