@@ -154,17 +154,17 @@ __device__ __forceinline__ void share_of(int64_t c0, int32_t tiles, int64_t s, i
 // prefix's length): the tile at cost t of a share is t modulo the shorter of a
 // share and a unit, where the item has it.
 struct Item {
-  int32_t unit;
-  int32_t tile0, tile1;   // tiles [tile0, tile1) of the unit
+  int32_t tile0, n;       // its first tile, its tiles; n = 0: no more items
   int32_t rot;            // its first turn
-  int32_t row0, n_rows;   // first row of the block, rows of it that count
   int32_t len;            // keys of the list
-  const int32_t* pages;   // its page list
+  int32_t lim_min;        // keys of it that every row of the block sees
+  int32_t row0, n_rows;   // first row of the block, rows of it that count
+  int32_t unit;
   int32_t b;              // request, or -1: the prefix
   int32_t rel0;           // row0 from the request's first row
 };
 
-// What a pair's walk over its share reads, in shared memory.
+// A pair's share and where it starts.
 struct Share {
   int64_t start, end;    // the share, in cost
   int64_t prefix_cost;
@@ -181,47 +181,37 @@ __device__ __forceinline__ int32_t tile_at(int32_t tile0, int32_t n, int32_t rot
   return tile0 + (x < n ? x : x - n);
 }
 
-// What the softmax warps need of an item; n = 0: no more.
-struct Post {
-  int32_t tile0, n;     // first tile, tiles
-  int32_t rot;          // first turn
-  int32_t lim_min;      // keys that every row of the block sees
-  int32_t n_rows, unit;
-  int32_t b, rel0;
-};
-
 // Walks the units of one pair's share, in order.
 struct Walk {
-  const Share* sh;
+  Share sh;
   int64_t pos;
   int64_t cb;   // cost and units before request b, which is at or before pos
   int32_t ub, b;
 
-  __device__ __forceinline__ bool next(const Lens& L, const int32_t* prefix_table,
-                                       int32_t prefix_len, const int32_t* table,
-                                       int max_blocks, Item& it) {
-    const int64_t end = sh->end;
-    while (pos < end) {
+  // the next item, or one of no tiles
+  __device__ __forceinline__ void next(const Lens& L, int32_t prefix_len, Item& it) {
+    const int64_t start = sh.start, end = sh.end;
+    it.n = 0;
+    while (it.n <= 0 && pos < end) {
       int64_t c0;
-      int32_t tiles;
-      if (pos < sh->prefix_cost) {
-        tiles = sh->prefix_tiles;
+      int32_t tiles, last;
+      it.rot = 0;
+      if (pos < sh.prefix_cost) {
+        tiles = sh.prefix_tiles;
         const int32_t u = (int32_t)quotient(pos, tiles + kUnitCost);
         c0 = (int64_t)u * (tiles + kUnitCost);
         it.unit = u;
         it.row0 = it.rel0 = u * kRows;
-        it.n_rows = min(kRows, sh->rows_all - it.row0);
-        it.len = prefix_len;
-        it.pages = prefix_table;
+        it.n_rows = min(kRows, sh.rows_all - it.row0);
+        it.len = it.lim_min = prefix_len;
         it.b = -1;
-        share_of(c0, tiles, sh->start, end, it.tile0, it.tile1);
-        const int64_t turn = min(end - sh->start, (int64_t)tiles + kUnitCost);
-        const int64_t ahead = c0 + kUnitCost - sh->start;
+        share_of(c0, tiles, start, end, it.tile0, last);
+        const int64_t turn = min(end - start, (int64_t)tiles + kUnitCost);
+        const int64_t ahead = c0 + kUnitCost - start;
         const int64_t x = ahead < 0 ? -ahead : ahead, y = x - quotient(x, turn) * turn;
         it.rot = (int32_t)(ahead < 0 && y ? turn - y : y);
-        if (it.rot >= it.tile1 - it.tile0) it.rot = 0;
+        if (it.rot >= last - it.tile0) it.rot = 0;
       } else {
-        it.rot = 0;
         ReqShape r = req_shape(L, b);
         for (;;) {
           const int32_t units = unit_count(r);
@@ -240,15 +230,15 @@ struct Walk {
         it.n_rows = min(kRows, r.n_rows - it.rel0);
         // keys beyond the block's last row are seen by no row of it
         it.len = min(r.len, row_limit(r, L.H, it.rel0 + it.n_rows - 1));
-        it.pages = table + (int64_t)b * max_blocks;
+        it.lim_min = row_limit(r, L.H, it.rel0);
         it.b = b;
-        share_of(c0, tiles, sh->start, end, it.tile0, it.tile1);
-        it.tile1 = min(it.tile1, (it.len + kKeys - 1) / kKeys);
+        share_of(c0, tiles, start, end, it.tile0, last);
+        last = min(last, (it.len + kKeys - 1) / kKeys);
       }
       pos = min(end, c0 + tiles + kUnitCost);
-      if (it.tile0 < it.tile1) return true;
+      it.n = last - it.tile0;
     }
-    return false;
+    if (it.n < 0) it.n = 0;
   }
 };
 
@@ -386,14 +376,14 @@ __device__ __forceinline__ void mbar_release_cluster(uint32_t cluster_addr) {
 __device__ __forceinline__ void mbar_signal(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-__device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity, uint32_t hint) {
+__device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(hint)
+      : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
 }
@@ -513,10 +503,10 @@ struct PairWaiter {
     return __all_sync(0xffffffffu, wait1(bar, parity));
   }
   __device__ __forceinline__ bool wait1(uint32_t bar, uint32_t parity) const {
-    if (mbar_try_cluster(bar, parity, 0u)) return true;
+    if (mbar_try_cluster(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     for (;;) {
-      if (mbar_try_cluster(bar, parity, 20000u)) return true;
+      if (mbar_try_cluster(bar, parity)) return true;
       if (*abort_flag) return false;
       if (globaltimer_ns() - t0 > timeout_ns) {
         latch_error(status, DSA_ERR_DEVICE_TIMEOUT);
@@ -613,11 +603,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   float* nmo_s = nm2_s + 2 * kRows;                       // [row] -m before it was last raised
   uint8_t* lim_s = reinterpret_cast<uint8_t*>(nmo_s + kRows);  // [row] keys past lim_min
   uint64_t* bars = reinterpret_cast<uint64_t*>(lim_s + kRows);
-  uint32_t* misc = reinterpret_cast<uint32_t*>(bars + kBars);  // abort, tmem, beyond
-  Share* share = reinterpret_cast<Share*>(misc + 4);
-  Post* posts = reinterpret_cast<Post*>(share + 1);            // [2]
-  static_assert(3 * kRows * 4 + kRows + kBars * 8 + 16 + sizeof(Share) + 2 * sizeof(Post) <= C::kTail,
-                "tail");
+  uint32_t* misc = reinterpret_cast<uint32_t*>(bars + kBars);  // abort, tmem, beyond, issuer's tiles
+  Item* posts = reinterpret_cast<Item*>(misc + 4);             // [2]
+  static_assert(3 * kRows * 4 + kRows + kBars * 8 + 16 + 2 * sizeof(Item) <= C::kTail, "tail");
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const uint32_t rank = cluster_rank(), peer = rank ^ 1u;
@@ -625,6 +613,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // product reads P and before this CTA's warps write it again
   float* red = reinterpret_cast<float*>(gb + C::kQBytes + rank * 128 * 128);  // [8][row]
   float* lred = red + 8 * kRows;                                             // [4][row]
+  Share* share = reinterpret_cast<Share*>(lred);  // until the first item is posted
   const uint32_t bar0 = smem_u32(bars);
   auto full = [&](uint32_t s) { return bar0 + 8u * s; };              // leader: both landed
   auto empty = [&](uint32_t s) { return bar0 + 8u * (kStages + s); };  // stage read
@@ -666,7 +655,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(rag(b), 1);
       mbar_init(fixed(b), 1);
       mbar_init(post_full(b), 1);
-      mbar_init(post_free(b), kSoftWarps);
+      mbar_init(post_free(b), kSoftWarps + 2);
     }
     mbar_init(o_empty, 2 * kSoftWarps);
     mbar_init(xs, 2 * kSoftWarps);
@@ -693,9 +682,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_sync_all();
   tc_fence_after();
-  Walk walk{share, share->start, share->first_cost, share->first_unit, share->first_b};
-  auto next = [&](Item& i) {
-    return walk.next(L, prefix_table, prefix_len, table, max_blocks, i);
+  // item ni, as kPassWarp posted it, one ahead of its tiles
+  uint32_t ni = 0;
+  auto take = [&](Item& i) {
+    if (!W.wait(post_full(ni), (ni >> 1) & 1u)) return false;
+    i = posts[ni & 1u];
+    return i.n > 0;
+  };
+  auto give_back = [&]() {  // the item's slot
+    __syncwarp();
+    if (lane == 0) mbar_arrive(post_free(ni));
+    ++ni;
   };
   constexpr uint32_t tmem = 0;  // an allocation of all 512 columns starts at column 0
   constexpr uint32_t tO = tmem + 2 * kRows;
@@ -717,7 +714,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t lead_q = at_rank(q_full, 0), lead_full = at_rank(full(0), 0);
       uint32_t u = 0, nq = 0, nr = 0;  // stages, items, ragged stages so far
       bool ok = true;
-      while (ok && next(it)) {
+      while (ok && take(it)) {
+        const int32_t* pages = it.b < 0 ? prefix_table : table + (int64_t)it.b * max_blocks;
+        give_back();
         if (!(ok = W.wait(q_empty, (nq & 1u) ^ 1u))) break;
         if (arms) mbar_expect_tx(q_full, 2 * C::kQBytes);
         if (lane < D / 64)
@@ -727,7 +726,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // page of key `half * 128 + key0` of tile j (0 where nothing is read)
         auto page_at = [&](int32_t j, int half) {
           const int32_t pos = j * kKeys + half * 128 + key0;
-          return pos < it.len ? __ldg(it.pages + (pos >> page_log2)) : 0;
+          return pos < it.len ? __ldg(pages + (pos >> page_log2)) : 0;
         };
         // its first cache row, or out of range past the end
         auto row_of = [&](int32_t j, int half, int32_t p) {
@@ -739,7 +738,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           return p << page_log2;
         };
         int32_t v_row[2] = {n_rows_cache, n_rows_cache};
-        const int32_t n = it.tile1 - it.tile0;
+        const int32_t n = it.n;
         int32_t tile = it.tile0 + it.rot, last = 0;  // this turn's tile, the turn's before
         int32_t page[2] = {page_at(tile, 0), page_at(tile, 1)};
         for (int32_t j = 0; j <= n && ok; ++j) {
@@ -820,9 +819,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         asm volatile("bar.sync %0, 64;" ::"r"(1 + (u & 1u)) : "memory");
         ++u;
       };
-      while ((rank == 0 || ok) && next(it)) {
-        const int n = it.tile1 - it.tile0;
-        const int keys = it.len - (it.tile1 - 1) * kKeys;  // of the last tile, that count
+      for (;;) {
+        const int n = ok && take(it) ? it.n : 0;
+        if (rank == 0) {  // the issuer walks the same tiles
+          if (lane == 0) misc[3] = (uint32_t)n;
+          asm volatile("bar.sync 3, 64;" ::: "memory");
+        }
+        if (n == 0) break;
+        give_back();
+        const int keys = it.len - (it.tile0 + n - 1) * kKeys;  // of the last tile, that count
         const bool ragged = keys < kKeys && (keys & 127) != 0;
         const int jr = n - 1 - it.rot;                     // the last tile's turn
         if (rank != 0) {
@@ -863,19 +868,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     } else if (warp == kPassWarp) {
       // ===== items to the softmax warps; this CTA's P complete -> the leader
-      uint32_t nt = 0, ni = 0;  // tiles, items
+      uint32_t nt = 0;
       bool ok = true;
-      Post cur, nxt;
+      Walk walk{*share, share->start, share->first_cost, share->first_unit, share->first_b};
+      __syncwarp();
       auto post = [&]() {  // the next item, one ahead of its tiles
-        nxt.n = 0;
-        if (next(it)) {
-          nxt = Post{it.tile0, it.tile1 - it.tile0, it.rot, it.len, it.n_rows, it.unit, it.b,
-                     it.rel0};
-          if (it.b >= 0) nxt.lim_min = row_limit(req_shape(L, it.b), L.H, it.rel0);
-        }
+        walk.next(L, prefix_len, it);
         if (!W.wait(post_free(ni), ((ni >> 1) & 1u) ^ 1u)) return false;
         if (lane == 0) {
-          posts[ni & 1u] = nxt;
+          posts[ni & 1u] = it;
           mbar_arrive(post_full(ni));
         }
         __syncwarp();
@@ -883,13 +884,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         return true;
       };
       ok = post();
-      while (ok && nxt.n > 0) {
-        cur = nxt;
+      while (ok && it.n > 0) {
+        const int32_t n = it.n, n_rows = it.n_rows;
         if (!(ok = post())) break;
         // bytes from the other CTA's keys, if this CTA's group has rows
         const uint32_t bytes =
-            cur.n_rows > kGroupRows * (int)rank ? 128 * kGroupRows * 2 : 0;
-        for (int32_t j = 0; j < cur.n; ++j, ++nt) {
+            n_rows > kGroupRows * (int)rank ? 128 * kGroupRows * 2 : 0;
+        for (int32_t j = 0; j < n; ++j, ++nt) {
           if (lane == 0) mbar_expect_tx(p_in(nt), bytes);
           if (!(ok = W.wait(p_in(nt), turn(nt)))) break;
           if (lane == 0) {
@@ -917,8 +918,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         ++u;
       };
-      while (next(it)) {
-        const int n = it.tile1 - it.tile0;
+      for (;;) {
+        asm volatile("bar.sync 3, 64;" ::: "memory");
+        const int n = (int)*reinterpret_cast<volatile uint32_t*>(misc + 3);
+        if (n == 0) break;
         for (int j = 0; j <= n; ++j) {
           if (j < n) {
             // the softmax has read this S^T buffer's last tile: that tile's PV,
@@ -985,9 +988,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       return W.wait(grp, ng++ & 1u);
     };
     bool ok = true;
-    for (uint32_t ni = 0; ok; ++ni) {
-      if (!(ok = W.wait(post_full(ni), (ni >> 1) & 1u))) break;
-      const volatile Post* post = posts + (ni & 1u);
+    while (ok && W.wait(post_full(ni), (ni >> 1) & 1u)) {
+      const volatile Item* post = posts + (ni & 1u);
       const int n = post->n;
       if (n == 0) break;
       const int32_t tile0 = post->tile0, rot = post->rot, lim_min = post->lim_min;
@@ -1275,10 +1277,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_signal(at_rank(o_empty, 0));
-        mbar_arrive(post_free(ni));
-      }
+      if (lane == 0) mbar_signal(at_rank(o_empty, 0));
+      give_back();
     }
   }
 
