@@ -559,25 +559,6 @@ __device__ __forceinline__ float column_reduce(float (&x)[16], int lane) {
   return MAX ? fmaxf(x[0], got) : x[0] + got;
 }
 
-// The maxima of N times 16 columns, N reductions in step.
-template <int N>
-__device__ __forceinline__ void column_max(float (&x)[N][16], float (&top)[N], int lane) {
-#pragma unroll
-  for (int H = 8; H > 0; H >>= 1) {
-    const bool up = (lane & H) != 0;
-#pragma unroll
-    for (int c = 0; c < N; ++c)
-#pragma unroll
-      for (int i = 0; i < H; ++i) {
-        const float keep = up ? x[c][i + H] : x[c][i], give = up ? x[c][i] : x[c][i + H];
-        x[c][i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, H));
-      }
-  }
-#pragma unroll
-  for (int c = 0; c < N; ++c)
-    top[c] = fmaxf(x[c][0], __shfl_xor_sync(0xffffffffu, x[c][0], 16));
-}
-
 template <int D>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefix_attn_kernel(const __grid_constant__ CUtensorMap q_map,
@@ -660,7 +641,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(o_empty, 2 * kSoftWarps);
     mbar_init(xs, 2 * kSoftWarps);
     mbar_init(grp, kSoftWarps);
-    mbar_init(refs, kRows / kGroupRows);
+    mbar_init(refs, kSoftWarps);
     mbar_init(done_bar, 1);
     misc[0] = misc[2] = 0u;
     fence_mbar_init();
@@ -994,6 +975,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (n == 0) break;
       const int32_t tile0 = post->tile0, rot = post->rot, lim_min = post->lim_min;
       const bool live = post->n_rows > r0;  // this group has rows that count
+      const bool same = post->len == lim_min;  // every row sees as many keys
       // references in turns: the other CTA may still read the last item's when
       // this item's arrive there
       float* nm_s = nm2_s + (ni & 1u) * kRows;
@@ -1010,46 +992,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int h = 0; h < 32; ++h) l[h] = 0ull;
       uint32_t pk[32];  // this thread's P, bf16 pairs
 
-      // The first references: the maxima over the first 32 keys of the item's
-      // first tile, which every row that sees a key of the item sees one of (the
-      // requests' own tokens, of which some rows see few, are taken in order).
-      // One warp a group has them and tells both CTAs.
+      // The first references, of 16 rows a warp of CTA 0: the maxima over the
+      // 32 keys of its lanes in the item's first tile.  Where some row does not
+      // see all of that tile, over its first 32 keys, by the first warp of the
+      // group: every row that sees a key of the item sees one of those (the
+      // requests' own tokens are taken in order).
       auto first_refs = [&](int32_t tile, uint32_t b) {
-        if (rank == 0 && quad == 0) {
-          const int32_t pos = tile * kKeys + lane;
-          const bool masked = tile * kKeys + 32 > lim_min;  // uniform
-          // 16 rows at a time, the four reductions side by side (a shuffle waits
-          // at shared memory's door like a load)
-          float x[kGroupRows / 16][16];
-          if (live) {
-            uint32_t r[kGroupRows / 16][16];
+        if (rank == 0) {
+          const bool whole = (tile + 1) * kKeys <= lim_min;  // uniform
+          const int32_t pos = tile * kKeys + quad * 32 + lane;
+#pragma unroll 1
+          for (int c = whole ? quad : 0; live && c < (whole ? quad + 1 : quad ? 0 : 4); ++c) {
+            const int h0 = r0 + 16 * c;
+            float x[16];
+            uint32_t r[16];
+            tmem_ld16(tmem + b * kRows + lane_base + h0, r);
+            tmem_wait_ld_dep(r);
 #pragma unroll
-            for (int c = 0; c < kGroupRows / 16; ++c)
-              tmem_ld16(tmem + b * kRows + r0 + 16 * c, r[c]);
-#pragma unroll
-            for (int c = 0; c < kGroupRows / 16; ++c) {
-              tmem_wait_ld_dep(r[c]);
+            for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(r[e]) * scale_log2;
+            if (!whole) {
 #pragma unroll
               for (int e = 0; e < 16; ++e)
-                x[c][e] = !masked || pos < lim_min + lim_s[r0 + 16 * c + e]
-                              ? __uint_as_float(r[c][e]) * scale_log2
-                              : -INFINITY;
+                if (pos >= lim_min + lim_s[h0 + e]) x[e] = -INFINITY;
             }
-          } else {
-#pragma unroll
-            for (int c = 0; c < kGroupRows / 16; ++c)
-#pragma unroll
-              for (int e = 0; e < 16; ++e) x[c][e] = -INFINITY;
-          }
-          float top[kGroupRows / 16];
-          column_max<kGroupRows / 16>(x, top, lane);
-#pragma unroll
-          for (int c = 0; c < kGroupRows / 16; c += 2) {  // lanes 0-15 and 16-31: one each
-            const float t = lane < 16 ? top[c] : top[c + 1];
-            const float* at = nm_s + r0 + 16 * c + lane;
-            const float v = t == -INFINITY ? 0.f : -t;
-            nm_s[r0 + 16 * c + lane] = v;
-            st_cluster_u32(at_rank(smem_u32(at), 1), __float_as_uint(v));
+            const float t = column_reduce<true>(x, lane), ref = t == -INFINITY ? 0.f : -t;
+            // lanes 0-15 tell this CTA, 16-31 the other
+            st_cluster_u32(at_rank(smem_u32(nm_s + h0 + (lane & 15)), (uint32_t)lane >> 4),
+                           __float_as_uint(ref));
           }
           __syncwarp();
           if (lane == 0) {
@@ -1130,9 +1099,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     d[e + 2], d[e + 3]);
           }
           if (!Plain && masked) {
+            if (same) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (pos >= lim_min + lim_s[r0 + 32 * h + e]) d[e] = -INFINITY;
+              for (int e = 0; e < 32; ++e) d[e] = pos < lim_min ? d[e] : -INFINITY;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (pos >= lim_min + lim_s[r0 + 32 * h + e]) d[e] = -INFINITY;
+            }
           }
           float top[4];
 #pragma unroll
@@ -1242,10 +1216,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!ok || !(ok = W.wait(p_done(nt - 1u), turn(nt - 1u)))) break;
       tc_fence_after();
       // ---- epilogue: m, l and O of this (unit, pair) to its slot
-      const int64_t slot = (int64_t)post->unit + pair;
       const int n_rows = post->n_rows;
+      const int64_t slot = (int64_t)post->unit + pair;
 #pragma unroll
       for (int h0 = 0; h0 < kGroupRows; h0 += 16) {
+        if (r0 + h0 >= n_rows) break;
         float x[16];
 #pragma unroll
         for (int e = 0; e < 16; e += 2) unpair2(l[(h0 + e) / 2], x[e], x[e + 1]);
@@ -1312,82 +1287,87 @@ __global__ void __launch_bounds__(128) join_kernel(PlanView view, Lens L,
                                                    uint32_t* status) {
   constexpr int kPer = 512 / D, kLanes = D / 4;  // rows of a block, threads of a row
   const int sub = threadIdx.x / kLanes, th = threadIdx.x % kLanes;
-  const int64_t row = blockIdx.x * (int64_t)kPer + sub;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the main kernel's results
-  if (row >= n_rows) return;
-  const Plan* plan = view.p;
-  const int64_t t = row / L.H, chunk = plan->chunk, total = plan->total;
-  if (t < __ldg(L.cu) || t >= __ldg(L.cu + B)) return;
-  int lo = 0, hi = B;  // the last b with cu[b] <= t
+  const int64_t row = blockIdx.x * (int64_t)kPer + sub, t = row / L.H;
+  // the row's request, from the call's inputs: before the main kernel's end
+  const bool mine = row < n_rows && t >= __ldg(L.cu) && t < __ldg(L.cu + B);
+  int lo = 0, hi = mine ? B : 0;  // the last b with cu[b] <= t
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (__ldg(L.cu + mid) <= t) lo = mid;
     else hi = mid;
   }
-  const ReqShape r = req_shape(L, lo);
-  // the two units: first cost, tiles, tiles that hold keys, number, row in it
-  int64_t c0[2];
-  int32_t tiles[2], used[2], unit[2], at[2];
-  int n_units = 0;
-  if (plan->prefix_cost > 0 && total > 0) {
-    tiles[0] = used[0] = plan->prefix_tiles;
-    unit[0] = (int32_t)(row / kRows);
-    at[0] = (int32_t)(row % kRows);
-    c0[0] = (int64_t)unit[0] * (tiles[0] + kUnitCost);
-    n_units = 1;
-  }
-  if (r.tiles && total > 0) {
-    const int32_t rel = (int32_t)row - r.row0, j = rel / kRows;
-    const int32_t last = min((j + 1) * kRows, r.n_rows) - 1;
-    tiles[n_units] = r.tiles;
-    used[n_units] = (min(r.len, row_limit(r, L.H, last)) + kKeys - 1) / kKeys;
-    unit[n_units] = __ldg(view.ucum + lo) + j;
-    at[n_units] = rel % kRows;
-    c0[n_units] = __ldg(view.ccum + lo) + (int64_t)j * (r.tiles + kUnitCost);
-    ++n_units;
+  ReqShape r{};
+  if (mine) r = req_shape(L, lo);
+  const int32_t rel = (int32_t)row - r.row0, block = rel / kRows;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the main kernel's results
+  if (!mine) return;
+  const Plan plan = *view.p;
+  const int64_t cost = view.ccum[lo];
+  const int32_t first_unit = view.ucum[lo];
+  // The prefix unit and the request's own: first cost, tiles, tiles that hold
+  // keys, number, row in it; and the first pair and the pairs that share it.
+  int64_t c0[2], i0[2];
+  int32_t tiles[2], used[2], unit[2], at[2], pairs[2];
+  tiles[0] = used[0] = plan.prefix_cost > 0 ? plan.prefix_tiles : 0;
+  unit[0] = (int32_t)(row / kRows);
+  at[0] = (int32_t)(row % kRows);
+  c0[0] = (int64_t)unit[0] * (tiles[0] + kUnitCost);
+  tiles[1] = r.tiles;
+  used[1] = (min(r.len, row_limit(r, L.H, min((block + 1) * kRows, r.n_rows) - 1)) + kKeys - 1) /
+            kKeys;
+  unit[1] = first_unit + block;
+  at[1] = rel % kRows;
+  c0[1] = cost + (int64_t)block * (tiles[1] + kUnitCost);
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    i0[x] = quotient(c0[x], plan.chunk);
+    pairs[x] = plan.total > 0 && tiles[x] > 0
+                   ? (int32_t)(quotient(c0[x] + tiles[x] + kUnitCost - 1, plan.chunk) - i0[x]) + 1
+                   : 0;
   }
   float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int x = 0; x < n_units; ++x) {
-    const int64_t i0 = quotient(c0[x], chunk);
-    const int64_t i1 = quotient(c0[x] + tiles[x] + kUnitCost - 1, chunk);
-    for (int64_t i = i0; i <= i1; i += kJoin) {
-      float2 p0[kJoin], p1[kJoin];
-      float4 oi[kJoin];
+  for (int i = 0; i < pairs[0] + pairs[1]; i += kJoin) {
+    float2 p0[kJoin], p1[kJoin];
+    float4 oi[kJoin];
 #pragma unroll
-      for (int e = 0; e < kJoin; ++e) {
-        p0[e] = p1[e] = make_float2(-INFINITY, 0.f);
-        oi[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-        int32_t a, z;
-        share_of(c0[x], tiles[x], (i + e) * chunk, min(total, (i + e + 1) * chunk), a, z);
-        const int64_t slot = unit[x] + i + e;
-        if (i + e <= i1 && a < min(z, used[x]) && DSA_IN_BOUNDS(slot < n_slots, status)) {
-          p0[e] = view.ml[(slot * 2) * kRows + at[x]];
-          p1[e] = view.ml[(slot * 2 + 1) * kRows + at[x]];
-          oi[e] = reinterpret_cast<const float4*>(view.o + (slot * kRows + at[x]) * D)[th];
-        }
+    for (int e = 0; e < kJoin; ++e) {
+      p0[e] = p1[e] = make_float2(-INFINITY, 0.f);
+      oi[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      const bool own = i + e >= pairs[0];
+      const int64_t p = own ? i0[1] + (i + e - pairs[0]) : i0[0] + (i + e);
+      int32_t a, z;
+      share_of(own ? c0[1] : c0[0], own ? tiles[1] : tiles[0], p * plan.chunk,
+               min(plan.total, (p + 1) * plan.chunk), a, z);
+      const int64_t slot = (own ? unit[1] : unit[0]) + p;
+      if (i + e < pairs[0] + pairs[1] && a < min(z, own ? used[1] : used[0]) &&
+          DSA_IN_BOUNDS(slot < n_slots, status)) {
+        const int32_t rr = own ? at[1] : at[0];
+        p0[e] = view.ml[(slot * 2) * kRows + rr];
+        p1[e] = view.ml[(slot * 2 + 1) * kRows + rr];
+        oi[e] = reinterpret_cast<const float4*>(view.o + (slot * kRows + rr) * D)[th];
       }
-      float top = m;
+    }
+    float top = m;
 #pragma unroll
-      for (int e = 0; e < kJoin; ++e) {
-        p1[e].y += p0[e].y;                        // l; 0: no key seen
-        if (p1[e].y == 0.f) p0[e].x = -INFINITY;
-        top = fmaxf(top, p0[e].x);
-      }
-      const float keep = top == -INFINITY ? 1.f : ex2(m - top);
-      l *= keep;
-      acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
-      m = top;
+    for (int e = 0; e < kJoin; ++e) {
+      p1[e].y += p0[e].y;                        // l; 0: no key seen
+      if (p1[e].y == 0.f) p0[e].x = -INFINITY;
+      top = fmaxf(top, p0[e].x);
+    }
+    const float keep = top == -INFINITY ? 1.f : ex2(m - top);
+    l *= keep;
+    acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
+    m = top;
 #pragma unroll
-      for (int e = 0; e < kJoin; ++e) {
-        if (p0[e].x == -INFINITY) continue;
-        const float w = ex2(p0[e].x - top);
-        l = fmaf(w, p1[e].y, l);
-        acc.x = fmaf(w, oi[e].x, acc.x);
-        acc.y = fmaf(w, oi[e].y, acc.y);
-        acc.z = fmaf(w, oi[e].z, acc.z);
-        acc.w = fmaf(w, oi[e].w, acc.w);
-      }
+    for (int e = 0; e < kJoin; ++e) {
+      if (p0[e].x == -INFINITY) continue;
+      const float w = ex2(p0[e].x - top);
+      l = fmaf(w, p1[e].y, l);
+      acc.x = fmaf(w, oi[e].x, acc.x);
+      acc.y = fmaf(w, oi[e].y, acc.y);
+      acc.z = fmaf(w, oi[e].z, acc.z);
+      acc.w = fmaf(w, oi[e].w, acc.w);
     }
   }
   const bool none = m == -INFINITY;
