@@ -151,11 +151,11 @@ cudaError_t launch_append(const LaunchCtx& c, const ServeShape& s, const int32_t
 size_t prefix_attn_ws(const ServeShape& s);
 
 // Shared-prefix attention; work: the workspace past the header.  q_map: q as
-// [T * H, D], box {64, 64}; k_map, v_map: the cache as [n_pages * page, D], box
-// {64, page}.
+// [T * H, D], box {64, 64}; k_map, v_maps: the cache as [n_pages * page, D], box
+// {64, page}, and of V also {64, 8} and {64, 1}.
 cudaError_t launch_prefix_attn(const LaunchCtx& c, const ServeShape& s,
                                const CUtensorMap& q_map, const CUtensorMap& k_map,
-                               const CUtensorMap& v_map, const int32_t* prefix_table,
+                               const CUtensorMap (&v_maps)[3], const int32_t* prefix_table,
                                int64_t prefix_len, const int32_t* table,
                                const int32_t* seq, const int32_t* cu, __nv_bfloat16* o,
                                float* lse, uint8_t* work);

@@ -523,7 +523,7 @@ struct PairWaiter {
 // constants and barriers, 1 KB to align: all of the 227 KB; at 256 and 128 a
 // second P.
 constexpr int kStages = 4;
-constexpr int kBars = 32;
+constexpr int kBars = 28;
 
 template <int D>
 struct PCfg {
@@ -537,8 +537,6 @@ struct PCfg {
   static constexpr uint32_t kTail = 2048;
   static constexpr uint32_t kSmem = 1024 + kQBytes + kPBufs * kPBytes + kStages * kStageBytes + kTail;
   static_assert(kSmem <= 232448, "shared memory");
-  // at most two ragged V stages are in flight (rag and fixed barriers)
-  static_assert(2 * (kKStages + kVStages) >= kStages, "ragged stages in flight");
 };
 
 // Reduce 16 columns over the warp's lanes: lanes i and i + 16 end with column i
@@ -563,7 +561,9 @@ template <int D>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefix_attn_kernel(const __grid_constant__ CUtensorMap q_map,
                        const __grid_constant__ CUtensorMap k_map,
-                       const __grid_constant__ CUtensorMap v_map, PlanView view, Lens L,
+                       const __grid_constant__ CUtensorMap v_map,
+                       const __grid_constant__ CUtensorMap v8_map,
+                       const __grid_constant__ CUtensorMap v1_map, PlanView view, Lens L,
                        const int32_t* __restrict__ prefix_table, int32_t prefix_len,
                        const int32_t* __restrict__ table, int B, int64_t T,
                        int max_blocks, int page_log2, int32_t n_pages, int64_t n_slots, float scale_log2,
@@ -609,12 +609,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t xs = bx + 88;       // the softmax warps of both CTAs
   const uint32_t grp = bx + 96;      // the softmax warps of this CTA
   const uint32_t done_bar = bx + 104;
-  auto rag = [&](uint32_t r) { return bx + 112 + 8 * (r & 1u); };     // own ragged V stage
-  auto fixed = [&](uint32_t r) { return bx + 128 + 8 * (r & 1u); };   // leader: the other's is
-  auto post_full = [&](uint32_t i) { return bx + 144 + 8 * (i & 1u); };
-  auto post_free = [&](uint32_t i) { return bx + 160 + 8 * (i & 1u); };
-  const uint32_t refs = bx + 176;    // a unit's first references
-  static_assert(2 * kStages + 23 <= kBars, "barriers");
+  auto post_full = [&](uint32_t i) { return bx + 112 + 8 * (i & 1u); };
+  auto post_free = [&](uint32_t i) { return bx + 128 + 8 * (i & 1u); };
+  const uint32_t refs = bx + 144;    // an item's first references
+  static_assert(2 * kStages + 19 <= kBars, "barriers");
   // phase parity of a barrier that serves every other tile, in tile t
   auto turn = [](uint32_t t) { return (t >> 1) & 1u; };
   // tile number + 1 of the last tile with a score beyond its reference
@@ -633,10 +631,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(p_in(b), kSoftWarps / 2 + 1);
       mbar_init(p_full(b), 2);
       mbar_init(p_done(b), 1);
-      mbar_init(rag(b), 1);
-      mbar_init(fixed(b), 1);
       mbar_init(post_full(b), 1);
-      mbar_init(post_free(b), kSoftWarps + 2);
+      mbar_init(post_free(b), kSoftWarps + (rank == 0 ? 2 : 1));
     }
     mbar_init(o_empty, 2 * kSoftWarps);
     mbar_init(xs, 2 * kSoftWarps);
@@ -693,7 +689,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t dst = sStage + (uint32_t)(col / 64) * kAtom + (uint32_t)key0 * 128;
       const bool arms = rank == 0 && lane == 0;
       const uint32_t lead_q = at_rank(q_full, 0), lead_full = at_rank(full(0), 0);
-      uint32_t u = 0, nq = 0, nr = 0;  // stages, items, ragged stages so far
+      uint32_t u = 0, nq = 0;  // stages, items so far
+      const int page = 1 << page_log2;
       bool ok = true;
       while (ok && take(it)) {
         const int32_t* pages = it.b < 0 ? prefix_table : table + (int64_t)it.b * max_blocks;
@@ -721,12 +718,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int32_t v_row[2] = {n_rows_cache, n_rows_cache};
         const int32_t n = it.n;
         int32_t tile = it.tile0 + it.rot, last = 0;  // this turn's tile, the turn's before
-        int32_t page[2] = {page_at(tile, 0), page_at(tile, 1)};
+        int32_t ids[2] = {page_at(tile, 0), page_at(tile, 1)};
         for (int32_t j = 0; j <= n && ok; ++j) {
-          const int32_t c_row[2] = {row_of(tile, 0, page[0]), row_of(tile, 1, page[1])};
+          const int32_t c_row[2] = {row_of(tile, 0, ids[0]), row_of(tile, 1, ids[1])};
           const int32_t ahead = tile_at(it.tile0, n, it.rot, j + 1 < n ? j + 1 : 0);
-          page[0] = page_at(ahead, 0);  // looked at in the next round
-          page[1] = page_at(ahead, 1);
+          ids[0] = page_at(ahead, 0);  // looked at in the next round
+          ids[1] = page_at(ahead, 1);
           if (j < n) {  // K of this turn's tile
             const int32_t row = rank ? c_row[1] : c_row[0];
 #pragma unroll 1
@@ -746,20 +743,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               const uint32_t s = u % kStages;
               const int half = x & 1;
               if (!(ok = W.wait(empty(s), ((u / kStages) & 1u) ^ 1u))) break;
-              const bool ragged = left0 > 128 * half && left0 < 128 * half + 128;
-              uint32_t bar = lead_full + 8u * s;
-              if (ragged) {  // lands at this CTA's barrier: kScoutWarp passes it on
-                if (lane == 0) mbar_expect_tx(rag(nr), kStageBytes);
-                __syncwarp();
-                bar = at_rank(rag(nr), rank);
-                ++nr;
-              } else if (arms) {
-                mbar_expect_tx(full(s), 2 * kStageBytes);
+              const int keys = left0 - 128 * half;  // of this stage, that count
+              const int32_t rows = half ? v_row[1] : v_row[0];
+              const int x0 = (x >> 1) * 256 + (int)rank * 128;
+              if (arms) mbar_expect_tx(full(s), 2 * kStageBytes);
+              if (keys <= 0 || (keys & (page - 1)) == 0 || keys >= 128) {
+                if (on)
+                  tma_load_pair(dst + s * kStageBytes, &v_map, x0 + col, rows,
+                                lead_full + 8u * s);
+                continue;
               }
-              if (on)
-                tma_load_pair(dst + s * kStageBytes, &v_map,
-                              (x >> 1) * 256 + (int)rank * 128 + col,
-                              half ? v_row[1] : v_row[0], bar);
+              // The list ends inside a page.  The rows behind may hold NaN, which a
+              // zero weight does not cancel, so none of them is loaded: eight rows
+              // a lane, those around the end one by one, and zeros (out of range)
+              // past it.
+              const int end8 = keys & 7 ? keys >> 3 : 16;
+              const int r = lane < 16 ? 8 * lane : 8 * end8 + (lane & 7);
+              const int32_t from = __shfl_sync(0xffffffffu, rows, (r & 127) >> page_log2) +
+                                   (r & (page - 1));
+              if (lane < 16 ? lane != end8 : lane < 24 && end8 < 16)
+                for (int a = 0; a < 2; ++a)
+                  tma_load_pair(sStage + s * kStageBytes + a * kAtom + r * 128,
+                                lane < 16 ? &v8_map : &v1_map, x0 + a * 64,
+                                r < keys ? from : n_rows_cache, lead_full + 8u * s);
             }
           }
           v_row[0] = c_row[0];
@@ -768,8 +774,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tile = ahead;
         }
       }
-    } else if (warp == kScoutWarp) {
-      // ================ scout (leader): waits for the MMA issuer's operands
+      // the leader's last arrival here is done_bar's: the CTA outlives it
+      if (ok && rank != 0 && u > 0) W.wait(done_bar, 0);
+    } else if (warp == kScoutWarp && rank == 0) {
+      // ================ scout (leader only): waits for the MMA issuer's operands
       // A wait on an mbarrier queues behind the MMAs that the same thread has
       // issued, and the tensor core idles until it returns: a loop that waits
       // and issues took 610 to 670 cycles a stage of 512 (MMAs and TMA alone),
@@ -777,24 +785,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // waiting and meets the issuer at one barrier a stage.  When a wait gives
       // up it lets the issuer through what is left (on whatever shared memory
       // holds), so that no thread is left behind at a barrier.
-      //
-      // Ragged stages of V: rows past the list's end may hold NaN, which a zero
-      // weight does not cancel.  The stage that holds the end lands at a barrier
-      // of its own CTA and is cleared behind it: by this warp in both CTAs.
-      // (Pages wholly past the end are zero by TMA's out-of-range fill.)
-      uint32_t u = 0, nt = 0, nq = 0, nr = 0;
+      uint32_t u = 0, nt = 0, nq = 0;
       bool ok = true;
-      auto clear = [&](uint32_t s, int keys) {  // the stage's rows from keys & 127 on
-        for (int x = (keys & 127) * 8 + lane; x < 128 * 8; x += 32)
-#pragma unroll
-          for (int a = 0; a < 2; ++a)
-            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
-                             sStage + s * kStageBytes + a * kAtom + x * 16),
-                         "r"(0u)
-                         : "memory");
-        fence_proxy_async();
-        __syncwarp();
-      };
       auto let_in = [&]() {
         if (ok) ok = W.wait(full(u % kStages), (u / kStages) & 1u);
         asm volatile("bar.sync %0, 64;" ::"r"(1 + (u & 1u)) : "memory");
@@ -802,27 +794,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       };
       for (;;) {
         const int n = ok && take(it) ? it.n : 0;
-        if (rank == 0) {  // the issuer walks the same tiles
-          if (lane == 0) misc[3] = (uint32_t)n;
-          asm volatile("bar.sync 3, 64;" ::: "memory");
-        }
+        if (lane == 0) misc[3] = (uint32_t)n;  // the issuer walks the same tiles
+        asm volatile("bar.sync 3, 64;" ::: "memory");
         if (n == 0) break;
         give_back();
-        const int keys = it.len - (it.tile0 + n - 1) * kKeys;  // of the last tile, that count
-        const bool ragged = keys < kKeys && (keys & 127) != 0;
-        const int jr = n - 1 - it.rot;                     // the last tile's turn
-        if (rank != 0) {
-          // its V stages; the end is in half keys / 128 of each block
-          const uint32_t v = u + (uint32_t)(min(jr + 2, n) * C::kKStages + jr * C::kVStages) +
-                             (uint32_t)(keys >> 7);
-          for (uint32_t m = 0; ragged && m < C::kBlocks && ok; ++m, ++nr) {
-            if (!(ok = W.wait(rag(nr), (nr >> 1) & 1u))) break;
-            clear((v + 2 * m) % kStages, keys);
-            if (lane == 0) mbar_release_cluster(at_rank(fixed(nr), 0));
-          }
-          u += (uint32_t)n * (C::kKStages + C::kVStages);
-          continue;
-        }
         if (ok) ok = W.wait(q_full, nq & 1u);
         for (int j = 0; j <= n; ++j) {
           if (j < n)
@@ -831,18 +806,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t t = nt + (uint32_t)j - 1u;
           if (ok) ok = W.wait(p_full(t), turn(t));
           if (ok && j == 1) ok = W.wait(o_empty, (nq & 1u) ^ 1u);
-          for (int c = 0; c < C::kVStages; ++c) {
-            if (ragged && j - 1 == jr && (c & 1) == (keys >> 7)) {
-              if (ok) ok = W.wait(rag(nr), (nr >> 1) & 1u);
-              if (ok) {
-                clear(u % kStages, keys);
-                ok = W.wait(fixed(nr), (nr >> 1) & 1u);
-              }
-              if (ok && lane == 0) mbar_arrive(full(u % kStages));
-              ++nr;
-            }
-            let_in();
-          }
+          for (int c = 0; c < C::kVStages; ++c) let_in();
         }
         nt += (uint32_t)n;
         ++nq;
@@ -881,7 +845,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
       }
-    } else if (rank == 0) {
+    } else if (warp == kMmaWarp && rank == 0) {
       // ========================================== MMA issuer (leader only)
       // Descriptors: an address 16 bytes on is 1 more.
       uint32_t u = 0, nt = 0;
@@ -1379,7 +1343,7 @@ __global__ void __launch_bounds__(128) join_kernel(PlanView view, Lens L,
 
 template <int D>
 cudaError_t launch_t(const LaunchCtx& c, const ServeShape& s, const CUtensorMap& qm,
-                     const CUtensorMap& km, const CUtensorMap& vm,
+                     const CUtensorMap& km, const CUtensorMap (&vm)[3],
                      const int32_t* prefix_table, int32_t prefix_len, const int32_t* table,
                      const Lens& L, __nv_bfloat16* o, float* lse, uint8_t* work) {
   using C = PCfg<D>;
@@ -1396,7 +1360,7 @@ cudaError_t launch_t(const LaunchCtx& c, const ServeShape& s, const CUtensorMap&
   const int pairs = c.num_sms / 2 < kMaxPairs ? c.num_sms / 2 : kMaxPairs;
   const int64_t slots = max_slots(s);
   prefix_attn_kernel<D><<<2 * pairs, kThreads, C::kSmem, c.stream>>>(
-      qm, km, vm, view, L, prefix_table, prefix_len, table, s.B, s.T, s.max_blocks,
+      qm, km, vm[0], vm[1], vm[2], view, L, prefix_table, prefix_len, table, s.B, s.T, s.max_blocks,
       s.page_log2, (int32_t)s.n_pages, slots, s.scale * kLog2e, c.status, c.timeout_ns);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // launched while the main kernel runs, which it waits for on the device
@@ -1422,13 +1386,13 @@ size_t prefix_attn_ws(const ServeShape& s) {
 
 cudaError_t launch_prefix_attn(const LaunchCtx& c, const ServeShape& s,
                                const CUtensorMap& q_map, const CUtensorMap& k_map,
-                               const CUtensorMap& v_map, const int32_t* prefix_table,
+                               const CUtensorMap (&v_maps)[3], const int32_t* prefix_table,
                                int64_t prefix_len, const int32_t* table,
                                const int32_t* seq, const int32_t* cu, __nv_bfloat16* o,
                                float* lse, uint8_t* work) {
   const Lens L{seq, cu, s.max_blocks << s.page_log2, s.H};
   auto run = [&](auto launch) {
-    return launch(c, s, q_map, k_map, v_map, prefix_table, (int32_t)prefix_len, table, L, o,
+    return launch(c, s, q_map, k_map, v_maps, prefix_table, (int32_t)prefix_len, table, L, o,
                   lse, work);
   };
   if (s.D == 128) return run(launch_t<128>);

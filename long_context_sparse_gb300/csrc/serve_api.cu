@@ -142,13 +142,16 @@ dsa_status_t dsa_prefix_attn(const dsa_serve_config_t* cfg, const void* q,
   LaunchCtx ctx;
   if ((st = make_ctx(ws, stream, &ctx)) != DSA_OK) return st;
   const ServeShape sh = serve_shape(cfg);
-  CUtensorMap qm, km, vm;
+  CUtensorMap qm, km, vm[3];
   const uint64_t cache_rows = (uint64_t)sh.n_pages * sh.page, d = (uint64_t)sh.D;
   const uint32_t box = (uint32_t)sh.page;
   if ((st = encode_2d(&qm, q, (uint64_t)(sh.T * sh.H), d, 64)) != DSA_OK) return st;
   if ((st = encode_2d(&km, k_pages, cache_rows, d, box)) != DSA_OK) return st;
-  if ((st = encode_2d(&vm, v_pages ? v_pages : k_pages, cache_rows, d, box)) != DSA_OK)
-    return st;
+  vm[0] = km;
+  const void* v = v_pages ? v_pages : k_pages;
+  if (v != k_pages && (st = encode_2d(&vm[0], v, cache_rows, d, box)) != DSA_OK) return st;
+  if ((st = encode_2d(&vm[1], v, cache_rows, d, 8)) != DSA_OK) return st;
+  if ((st = encode_2d(&vm[2], v, cache_rows, d, 1)) != DSA_OK) return st;
   return cuda_status(launch_prefix_attn(ctx, sh, qm, km, vm, prefix_table, prefix_len,
                                         block_table, seq_lens, cu_tokens,
                                         static_cast<__nv_bfloat16*>(o), lse,

@@ -1,7 +1,12 @@
 """The serving calls: page tables, cache append and shared-prefix attention,
 against plain definitions (integers in Python, attention in fp64)."""
 import ctypes
+import dataclasses
+import json
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -481,6 +486,118 @@ def test_attn_on_a_side_stream_and_in_a_graph():
     check((o.cpu(), lse.cpu()), c2.plain())
 
 
+@gpu
+@pytest.mark.parametrize("at", [300, 5, 255, 256, 700, 1999])
+@pytest.mark.parametrize("jump", [15.0, 30.0, 120.0, 5000.0])
+def test_attn_scores_far_beyond_the_first_reference(at, jump):
+    """One key (and a few after it) whose score passes everything before by up
+    to thousands: exact scores, so the bound stays that of P's rounding.  Some
+    rows have the jump, some its negative, some none."""
+    c = Case([1, 1], [40, 300], 2000, 16, 512, 64, 2, seed=at)
+    c.cfg = dataclasses.replace(c.cfg, sm_scale=1.0)
+    c.q[:] = 0
+    c.q[:, :, 0] = 1.0
+    c.q[:, 5::3, 0] = -1.0
+    c.q[:, 6::3, 0] = 0.0
+    live = ~torch.isnan(c.k)
+    c.k = torch.where(live, (2 * torch.rand(c.k.shape, generator=torch.Generator().manual_seed(1))
+                             ).round().to(BF), c.k)
+    page = c.cfg.page_size
+    for n, j in enumerate(range(at, min(at + 3, 2000))):
+        c.k[c.prefix_table[j // page].item(), j % page, 0] = jump * (1 + n)
+    # the last own token of request 1 passes that again
+    c.k[c.table[1, 299 // page].item(), 299 % page, 0] = 4 * jump
+    check_case(c)
+
+
+@gpu
+def test_attn_large_values_and_scales():
+    c = Case([1, 2], [30, 300], 600, 16, 256, 32, 2, seed=21)
+    c.cfg = dataclasses.replace(c.cfg, sm_scale=0.01)
+    c.v = (c.v.float() * 1e30).to(BF)
+    check_case(c)
+
+
+@gpu
+def test_attn_shares_that_begin_inside_units():
+    """384 and 1152 rows behind a prefix of odd length: shares that begin and
+    end inside units, whose tiles are taken from the middle on."""
+    check_case(Case([3], [40], 30011, 128, 128, 64, 1, seed=31))
+    check_case(Case([2, 1, 6], [2, 300, 77], 9999, 128, 128, 16, 2, seed=32))
+
+
+@gpu
+@pytest.mark.parametrize("B,H", [(1000, 8), (3000, 1)])
+def test_attn_many_requests(B, H):
+    """More requests than threads in a block; some idle, some without own
+    tokens before this step."""
+    r = np.random.default_rng(B)
+    new = r.integers(0, 3, B).tolist()
+    seq = [n + int(x) for n, x in zip(new, r.integers(0, 20, B))]
+    check_case(Case(new, seq, 70, H, 128, 16, 2, pad=5, seed=B))
+
+
+@gpu
+def test_attn_padding_rows_may_hold_anything():
+    c = Case([2, 1], [70, 5], 300, 16, 512, 64, 1, pad=9, seed=12)
+    c.q[3:] = math.nan
+    check_case(c)
+    c.q[3:] = math.inf
+    check_case(c)
+
+
+@gpu
+def test_cache_beyond_32_bit_offsets():
+    """A cache of 5 GiB whose last pages are used: byte offsets past 2^32."""
+    page, d, n_pages = 128, 512, 40960
+    k = torch.zeros((n_pages, page, d), dtype=BF, device=DEV)
+    c = Case([1, 1], [100, 130], 300, 16, d, page, 1, seed=41)
+    far = n_pages - c.cfg.n_pages
+    k[far:] = c.k.to(DEV)
+    c.prefix_table += far
+    c.table[c.table >= 0] += far
+    c.cfg = dataclasses.replace(c.cfg, n_pages=n_pages)
+    ref = plain_attn(c.q, c.k, c.v, c.prefix_table - far, c.prefix,
+                     torch.where(c.table >= 0, c.table - far, c.table), c.seq, c.cu, c.cfg.scale)
+    got = c.run(k=k)
+    assert got[2] == 0
+    check(got, ref)
+    # and the append to the cache's last rows
+    ac = dsa.ServeConfig(n_pages=n_pages, max_tokens=3, batch=1, max_blocks=1, page_size=page)
+    slots = torch.tensor([n_pages * page - 1, -1, n_pages * page - 200], dtype=torch.int32,
+                         device=DEV)
+    new = torch.randn(3, d, device=DEV).to(BF)
+    dsa.append_cache(ac, slots, new, k)
+    assert torch.equal(k.view(-1, d)[-1], new[0]) and torch.equal(k.view(-1, d)[-200], new[2])
+
+
+@gpu
+def test_attn_two_calls_at_once():
+    """Two streams, a workspace each."""
+    cs = [Case([1, 2], [40, 300], 3000, 16, 512, 64, 1, seed=51),
+          Case([1] * 9, [33] * 9, 2000, 64, 256, 32, 2, seed=52)]
+    streams = [torch.cuda.Stream() for _ in cs]
+    ins = []
+    dv = lambda t: t.to(DEV)
+    for c in cs:
+        i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)
+        k = dv(c.k)
+        ins.append((dv(c.q), k, dv(c.prefix_table), dv(c.table), i32(c.seq), i32(c.cu),
+                    None if c.kv == 1 else dv(c.v),
+                    dsa.serve_workspace(c.cfg, dsa.SERVE_WS_PREFIX, DEV)))
+    torch.cuda.synchronize()
+    outs = [None, None]
+    for _ in range(5):
+        for x, (c, s) in enumerate(zip(cs, streams)):
+            q, k, pt, tb, seq, cu, v, ws = ins[x]
+            with torch.cuda.stream(s):
+                outs[x] = dsa.prefix_attn(c.cfg, q, k, pt, c.prefix, tb, seq, cu, v_pages=v, ws=ws)
+    torch.cuda.synchronize()
+    for c, (o, lse), i in zip(cs, outs, ins):
+        assert dsa.get_device_status(i[-1]) == 0
+        check((o.cpu(), lse.cpu()), c.plain())
+
+
 # ------------------------------------------------- the calls as one engine
 
 
@@ -540,3 +657,100 @@ def test_serving_steps_together(kv, page, d):
                       ((p @ vv[:m])[None], torch.logsumexp(s, -1)[None],
                        (p @ vv[:m].abs())[None]))
         assert (o[cu[-1]:] == 0).all()
+
+
+@gpu
+def test_serving_step_in_a_graph():
+    """Tables, append and attention of one step, captured once and replayed
+    on new lengths, rows and free pages."""
+    B, H, P, page, d, n_pages, width, T = 2, 16, 200, 32, 256, 40, 10, 12
+    cfg = dsa.ServeConfig(n_pages=n_pages, max_tokens=T, batch=B, max_blocks=width,
+                          page_size=page, attn_heads=H, d_qk=d, d_v=d)
+    g = torch.Generator().manual_seed(3)
+    bf = lambda *s: torch.randn(s, generator=g).to(BF).to(DEV)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    k = bf(n_pages, page, d)
+    ptab = i32(list(range(7)))
+    ws = [dsa.serve_workspace(cfg, w, DEV) for w in range(3)]
+    table = torch.full((B, width), -1, dtype=torch.int32, device=DEV)
+    lens, new, free = i32([0, 0]), i32([5, 3]), i32(list(range(39, 6, -1)))
+    rows, q = bf(T, d), bf(T, H, d)
+    out = dsa.PageTables(table, *(torch.zeros(n, dtype=torch.int32, device=DEV)
+                                  for n in (T, B + 1, B, 1)))
+    o = torch.zeros((T, H, d), dtype=BF, device=DEV)
+    lse = torch.zeros((T, H), device=DEV)
+
+    def step():
+        dsa.build_page_tables(cfg, lens, new, free, table, out=out, ws=ws[0])
+        dsa.append_cache(cfg, out.slot_map, rows, k, ws=ws[1])
+        dsa.prefix_attn(cfg, q, k, ptab, P, table, out.seq_lens, out.cu_tokens, o=o, lse=lse,
+                        ws=ws[2])
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    table.fill_(-1)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    held, taken = [0, 0], 0
+    for n in ([5, 3], [1, 1], [0, 12], [4, 0]):
+        new.copy_(i32(n))
+        lens.copy_(i32(held))
+        free.copy_(i32((list(range(39, 6, -1))[taken:] + [0] * 33)[:33]))
+        rows.copy_(bf(T, d))
+        q.copy_(bf(T, H, d))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert [dsa.get_device_status(w) for w in ws] == [0, 0, 0]
+        taken += int(out.pages_taken)
+        held = [a + b for a, b in zip(held, n)]
+        assert out.seq_lens.tolist() == held
+        cu = out.cu_tokens.tolist()
+        slots = out.slot_map.tolist()
+        for x in range(cu[-1]):
+            assert torch.equal(k.view(-1, d)[slots[x]], rows[x])
+        ref = plain_attn(q.cpu(), k.cpu(), k.cpu(), ptab.cpu(), P, table.cpu(), held, cu, cfg.scale)
+        check((o.cpu(), lse.cpu()), ref)
+
+
+CHECKS_CHILD = r"""
+import json, sys
+import numpy as np, torch
+sys.path.insert(0, {root!r})
+import long_context_sparse_gb300 as dsa
+from tests.test_serving import Case, tables_case, run_tables
+out, status = {{}}, []
+for x, c in enumerate((Case([1, 3, 0], [50, 300, 7], 700, 16, 512, 64, 1, pad=2, seed=1),
+                       Case([2] * 5, [9] * 5, 300, 8, 128, 16, 2, seed=2),
+                       Case([1], [33], 20000, 64, 256, 128, 2, seed=3))):
+    o, lse, st = c.run()
+    out["o%d" % x], out["lse%d" % x] = o.float().numpy(), lse.numpy()
+    status.append(st)
+got, st = run_tables(*tables_case(300, 16, 0, 40, 50, 3, 5))
+status.append(st)
+out["tables"] = np.array(got[1])
+np.savez(sys.argv[1], **out)
+print(json.dumps({{"library": dsa.library_path(), "status": status}}))
+"""
+
+
+@gpu
+def test_serving_in_the_checks_build(tmp_path):
+    """The bounds-checking build runs the serving calls clean and agrees bit
+    for bit."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    runs = []
+    for checks in ("1", "0"):
+        path = str(tmp_path / f"c{checks}.npz")
+        r = subprocess.run([sys.executable, "-c", CHECKS_CHILD.format(root=root), path],
+                           env=dict(os.environ, DSA_GB300_CHECKS=checks), cwd=root,
+                           capture_output=True, text=True, timeout=600)
+        assert r.returncode == 0, r.stderr[-2000:]
+        info = json.loads(r.stdout.strip().splitlines()[-1])
+        assert info["status"] == [0, 0, 0, 0]
+        assert info["library"].endswith("_checks.so") == (checks == "1")
+        runs.append(np.load(path))
+    for key in runs[0].files:
+        assert np.array_equal(runs[0][key], runs[1][key]), key
