@@ -846,37 +846,40 @@ def serve_workspace(cfg: ServeConfig, which: int, device="cuda") -> torch.Tensor
 def _check_tensor(t, name, dtype, shape, dev):
     """_need, said briefly when all is well."""
     try:
-        if (t.dtype is dtype and t.shape == shape and t.device == dev
+        if (t.get_device() == dev and t.dtype is dtype and t.shape == shape
                 and t.is_contiguous()):
             return t.data_ptr()
     except AttributeError:
         pass
-    _need(t, name, dtype, shape, dev)
+    _need(t, name, dtype, shape, torch.device("cuda", dev))
     return t.data_ptr()
 
 
 def _first_tensor(t, name, dtype, shape):
-    """As _check_tensor for the tensor that says which device a call is on."""
-    _need(t, name, dtype, shape)
-    return t.device
+    """As _check_tensor for the tensor that says which device a call is on:
+    that device's number, and the pointer."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _need(t, name, dtype, shape)
+    dev = t.get_device()
+    return dev, _check_tensor(t, name, dtype, shape, dev)
 
 
 def _serve_ws(cfg, which, ws, dev):
     if ws is None:
-        return serve_workspace(cfg, which, dev)
-    if ws.dtype is not torch.uint8 or ws.device != dev or not ws.is_contiguous():
-        _need(ws, "ws", torch.uint8, device=dev)
-    return ws
+        ws = serve_workspace(cfg, which, torch.device("cuda", dev))
+    n = ws.numel() if isinstance(ws, torch.Tensor) else 0
+    return ws, _check_tensor(ws, "ws", torch.uint8, (n,), dev), n
 
 
 def _serve_call(name, dev, *args):
-    """One C call on `dev`'s current stream, with `dev` the current device."""
+    """One C call on the current stream of device `dev`, made current (its
+    tensors exist, so CUDA is up and the short queries hold)."""
     fn = getattr(_lib or _load(), name)
-    if torch.cuda.current_device() == dev.index:
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if torch._C._cuda_getDevice() == dev:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     if rc:
         _check(rc, name)
 
@@ -897,7 +900,7 @@ def build_page_tables(cfg: ServeConfig, cached_lens, new_lens, free_pages,
     free_pages [n_free], in request order, and are entered in block_table
     [batch, max_blocks] in place (other entries stay).  All int32."""
     B, T, i32 = cfg.batch, cfg.max_tokens, torch.int32
-    dev = _first_tensor(cached_lens, "cached_lens", i32, (B,))
+    dev, p_cached = _first_tensor(cached_lens, "cached_lens", i32, (B,))
     p_new = _check_tensor(new_lens, "new_lens", i32, (B,), dev)
     n_free = free_pages.numel() if isinstance(free_pages, torch.Tensor) else 0
     p_free = _check_tensor(free_pages, "free_pages", i32, (n_free,), dev)
@@ -911,10 +914,9 @@ def build_page_tables(cfg: ServeConfig, cached_lens, new_lens, free_pages,
     p_cu = _check_tensor(out.cu_tokens, "cu_tokens", i32, (B + 1,), dev)
     p_seq = _check_tensor(out.seq_lens, "seq_lens", i32, (B,), dev)
     p_taken = _check_tensor(out.pages_taken, "pages_taken", i32, (1,), dev)
-    ws = _serve_ws(cfg, SERVE_WS_TABLES, ws, dev)
-    _serve_call("dsa_build_page_tables", dev, cfg._ref, cached_lens.data_ptr(), p_new,
-                p_free, n_free, p_table, p_slots, p_cu, p_seq, p_taken, ws.data_ptr(),
-                ws.numel())
+    ws, p_ws, n_ws = _serve_ws(cfg, SERVE_WS_TABLES, ws, dev)
+    _serve_call("dsa_build_page_tables", dev, cfg._ref, p_cached, p_new, p_free, n_free,
+                p_table, p_slots, p_cu, p_seq, p_taken, p_ws, n_ws)
     return out
 
 
@@ -924,7 +926,7 @@ def append_cache(cfg: ServeConfig, slot_map, k_new, k_pages, v_new=None,
     of k_pages (and v_pages) [n_pages, page_size, d], in place; slots below
     0 are skipped, the others must be distinct.  Without v: K = V."""
     T, bf = cfg.max_tokens, torch.bfloat16
-    dev = _first_tensor(slot_map, "slot_map", torch.int32, (T,))
+    dev, p_slots = _first_tensor(slot_map, "slot_map", torch.int32, (T,))
     p_new = _check_tensor(k_new, "k_new", bf, (T, cfg.d_qk), dev)
     p_k = _check_tensor(k_pages, "k_pages", bf, (cfg.n_pages, cfg.page_size, cfg.d_qk), dev)
     if (v_new is None) != (v_pages is None):
@@ -933,9 +935,9 @@ def append_cache(cfg: ServeConfig, slot_map, k_new, k_pages, v_new=None,
     if v_new is not None:
         p_vnew = _check_tensor(v_new, "v_new", bf, (T, cfg.d_v), dev)
         p_v = _check_tensor(v_pages, "v_pages", bf, (cfg.n_pages, cfg.page_size, cfg.d_v), dev)
-    ws = _serve_ws(cfg, SERVE_WS_APPEND, ws, dev)
-    _serve_call("dsa_append_cache", dev, cfg._ref, slot_map.data_ptr(), p_new, p_vnew, p_k,
-                p_v, ws.data_ptr(), ws.numel())
+    ws, p_ws, n_ws = _serve_ws(cfg, SERVE_WS_APPEND, ws, dev)
+    _serve_call("dsa_append_cache", dev, cfg._ref, p_slots, p_new, p_vnew, p_k, p_v, p_ws,
+                n_ws)
 
 
 def prefix_attn(cfg: ServeConfig, q, k_pages, prefix_table, prefix_len: int,
@@ -951,7 +953,7 @@ def prefix_attn(cfg: ServeConfig, q, k_pages, prefix_table, prefix_len: int,
     prefix_len is 0."""
     T, H, B, bf, i32 = (cfg.max_tokens, cfg.attn_heads, cfg.batch, torch.bfloat16,
                         torch.int32)
-    dev = _first_tensor(q, "q", bf, (T, H, cfg.d_qk))
+    dev, p_q = _first_tensor(q, "q", bf, (T, H, cfg.d_qk))
     p_k = _check_tensor(k_pages, "k_pages", bf, (cfg.n_pages, cfg.page_size, cfg.d_qk), dev)
     p_v = None
     if v_pages is not None:
@@ -977,7 +979,7 @@ def prefix_attn(cfg: ServeConfig, q, k_pages, prefix_table, prefix_len: int,
         lse = torch.zeros((T, H), dtype=torch.float32, device=dev)
     p_o = _check_tensor(o, "o", bf, (T, H, cfg.d_v), dev)
     p_lse = _check_tensor(lse, "lse", torch.float32, (T, H), dev)
-    ws = _serve_ws(cfg, SERVE_WS_PREFIX, ws, dev)
-    _serve_call("dsa_prefix_attn", dev, cfg._ref, q.data_ptr(), p_k, p_v, p_prefix,
-                prefix_len, p_table, p_seq, p_cu, p_o, p_lse, ws.data_ptr(), ws.numel())
+    ws, p_ws, n_ws = _serve_ws(cfg, SERVE_WS_PREFIX, ws, dev)
+    _serve_call("dsa_prefix_attn", dev, cfg._ref, p_q, p_k, p_v, p_prefix, prefix_len,
+                p_table, p_seq, p_cu, p_o, p_lse, p_ws, n_ws)
     return o, lse
