@@ -898,7 +898,9 @@ def build_page_tables(cfg: ServeConfig, cached_lens, new_lens, free_pages,
     """Page tables and slots of one step: request b holds cached_lens[b]
     tokens and gets new_lens[b] more; the pages that it needs come from
     free_pages [n_free], in request order, and are entered in block_table
-    [batch, max_blocks] in place (other entries stay).  All int32."""
+    [batch, max_blocks] in place (other entries stay).  All int32.  `out` may
+    not be the tables whose seq_lens are this step's cached_lens: steps that
+    reuse their buffers take two sets in turn."""
     B, T, i32 = cfg.batch, cfg.max_tokens, torch.int32
     dev, p_cached = _first_tensor(cached_lens, "cached_lens", i32, (B,))
     p_new = _check_tensor(new_lens, "new_lens", i32, (B,), dev)

@@ -61,6 +61,29 @@ dsa_status_t check_serve_ws(const dsa_serve_config_t* c, int which, void* ws,
   return DSA_OK;
 }
 
+struct Span {
+  const void* at;
+  size_t bytes;
+};
+
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+  return x && y && (x <= y ? y - x < a.bytes : x - y < b.bytes);
+}
+
+// Whether what a call writes meets what it reads, or itself: its blocks read
+// and write in no order.
+template <int W, int R>
+bool written_meets(const Span (&w)[W], const Span (&r)[R]) {
+  for (int i = 0; i < W; ++i) {
+    for (int j = 0; j < R; ++j)
+      if (overlap(w[i], r[j])) return true;
+    for (int j = 0; j < i; ++j)
+      if (overlap(w[i], w[j])) return true;
+  }
+  return false;
+}
+
 }  // namespace
 }  // namespace dsa
 
@@ -95,6 +118,14 @@ dsa_status_t dsa_build_page_tables(const dsa_serve_config_t* cfg, const int32_t*
   for (const void* p : ptrs)
     if (!aligned16(p)) return DSA_ERR_MISALIGNED;
   if ((reinterpret_cast<uintptr_t>(free_pages) & 3u) != 0) return DSA_ERR_MISALIGNED;
+  const size_t B = (size_t)cfg->batch, frees = n_free < (int64_t)1 << 40 ? n_free : (int64_t)1 << 40;
+  const Span reads[] = {{cached_lens, B * 4}, {new_lens, B * 4}, {free_pages, frees * 4}};
+  const Span writes[] = {{block_table, B * (size_t)cfg->max_blocks * 4},
+                         {slot_map, (size_t)cfg->max_tokens * 4},
+                         {cu_tokens, (B + 1) * 4},
+                         {seq_lens, B * 4},
+                         {pages_taken, 4}};
+  if (written_meets(writes, reads)) return DSA_ERR_INVALID_ARG;
   LaunchCtx ctx;
   if ((st = make_ctx(ws, stream, &ctx)) != DSA_OK) return st;
   return cuda_status(launch_page_tables(ctx, serve_shape(cfg), cached_lens, new_lens,
@@ -113,6 +144,11 @@ dsa_status_t dsa_append_cache(const dsa_serve_config_t* cfg, const int32_t* slot
   const void* ptrs[] = {slot_map, k_new, v_new, k_pages, v_pages};
   for (const void* p : ptrs)
     if (!aligned16(p)) return DSA_ERR_MISALIGNED;
+  const size_t T = (size_t)cfg->max_tokens, row = (size_t)cfg->d_qk * 2;
+  const size_t cache = (size_t)cfg->n_pages * cfg->page_size * row;
+  const Span reads[] = {{slot_map, T * 4}, {k_new, T * row}, {v_new, T * row}};
+  const Span writes[] = {{k_pages, cache}, {v_pages, cache}};
+  if (written_meets(writes, reads)) return DSA_ERR_INVALID_ARG;
   LaunchCtx ctx;
   if ((st = make_ctx(ws, stream, &ctx)) != DSA_OK) return st;
   return cuda_status(launch_append(ctx, serve_shape(cfg), slot_map,

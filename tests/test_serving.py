@@ -226,6 +226,40 @@ def test_serving_calls_check_arguments_before_launch(lib):
     assert f(r, p, p, p, p, 5, p, p, p, p, p, None, nb, None) == 1
 
 
+def test_serving_calls_refuse_what_overlaps(lib):
+    """What a call writes may not meet what it reads, or itself; neighbours
+    may touch."""
+    c = scfg(max_tokens=512, d_qk=128, d_v=128)
+    r, ws = ctypes.byref(c.c()), ctypes.c_void_p(1 << 24)
+    at = {n: 4096 * (i + 1) for i, n in enumerate(
+        ("cached", "new", "free", "table", "slots", "cu", "seq", "taken"))}
+    size = dict(cached=16, new=16, free=400, table=160, slots=2048, cu=20, seq=16, taken=4)
+
+    def tables(**over):
+        a = [ctypes.c_void_p(x) for x in {**at, **over}.values()]
+        return lib.dsa_build_page_tables(r, *a[:3], 100, *a[3:], ws, 256, None)
+
+    for w in ("table", "slots", "cu", "seq", "taken"):
+        for x in at:
+            if x != w:
+                assert tables(**{w: at[x]}) == 1, (w, x)             # the same place
+                assert tables(**{w: at[x] + (size[x] - 1) // 16 * 16}) == 1, (w, x)  # its end
+    page, row = 64, 256
+    cache = c.n_pages * page * row
+    at = dict(slots=1 << 20, k_new=2 << 20, v_new=3 << 20, k=1 << 30, v=2 << 30)
+
+    def append(**over):
+        a = [ctypes.c_void_p(x) for x in {**at, **over}.values()]
+        return lib.dsa_append_cache(r, *a, ws, 256, None)
+
+    for w in ("k", "v"):
+        assert append(**{w: at["slots"] + 2032}) == 1
+        assert append(**{w: at["k_new"] - cache + 16}) == 1
+        assert append(**{w: at["v_new"] + 512 * row - 16}) == 1
+    assert append(v=at["k"] + cache - 16) == 1
+    assert append(k=at["v"] + cache - 16) == 1
+
+
 def test_python_refuses_wrong_tensors():
     c = scfg()
     i = torch.zeros(4, dtype=torch.int32)
