@@ -15,6 +15,7 @@ import ctypes
 import dataclasses
 import functools
 import math
+import operator
 import os
 import threading
 import typing
@@ -166,6 +167,9 @@ class ServeConfig:
     def _ref(self):
         """The C struct by reference (the calls read it only)."""
         return ctypes.byref(self.c())
+
+    def __getstate__(self):  # copies and pickles are without it
+        return {k: v for k, v in self.__dict__.items() if k != "_ref"}
 
 
 def config_for(wl: Workload, **over) -> Config:
@@ -960,7 +964,7 @@ def prefix_attn(cfg: ServeConfig, q, k_pages, prefix_table, prefix_len: int,
     p_v = None
     if v_pages is not None:
         p_v = _check_tensor(v_pages, "v_pages", bf, (cfg.n_pages, cfg.page_size, cfg.d_v), dev)
-    prefix_len = int(prefix_len)
+    prefix_len = operator.index(prefix_len)
     if prefix_len < 0:
         raise ValueError("prefix_len must not be negative")
     p_prefix = None

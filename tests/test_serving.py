@@ -1,10 +1,12 @@
 """The serving calls: page tables, cache append and shared-prefix attention,
 against plain definitions (integers in Python, attention in fp64)."""
+import copy
 import ctypes
 import dataclasses
 import json
 import math
 import os
+import pickle
 import subprocess
 import sys
 
@@ -168,6 +170,15 @@ def test_serve_config_layout():
     C = dsa._CServeConfig
     assert ctypes.sizeof(C) == 48 and C.max_tokens.offset == 8
     assert C.page_size.offset == 16 and C.d_v.offset == 36 and C.sm_scale.offset == 40
+
+
+def test_serve_config_is_copied_and_pickled_after_use():
+    c = scfg()
+    c._ref
+    for d in (pickle.loads(pickle.dumps(c)), copy.copy(c), copy.deepcopy(c)):
+        assert d == c and "_ref" not in vars(d)
+        d._ref
+    assert dataclasses.replace(c, batch=9)._ref._obj.batch == 9
 
 
 @pytest.mark.parametrize("over,code", [
