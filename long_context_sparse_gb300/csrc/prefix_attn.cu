@@ -1173,8 +1173,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           rescale(j > 0);
         }
         if (!ok) break;
-        // the P buffer's last tile has been read
-        if (nt >= C::kPBufs && !(ok = W.wait(p_done(nt - C::kPBufs), turn(nt - C::kPBufs)))) break;
+        // the P buffer's last tile has been read (a group without rows writes none,
+        // and nothing waits for it: it could come after the buffer's next tile)
+        if (live && nt >= C::kPBufs && !(ok = W.wait(p_done(nt - C::kPBufs), turn(nt - C::kPBufs)))) break;
         hand_over();
       }
       if (!ok || !(ok = W.wait(p_done(nt - 1u), turn(nt - 1u)))) break;
