@@ -181,7 +181,7 @@ __device__ __forceinline__ int32_t tile_at(int32_t tile0, int32_t n, int32_t rot
   return tile0 + (x < n ? x : x - n);
 }
 
-// Walks the units of one pair's share, in order.
+// Walks the units of one pair's share, in order; a whole warp, in step.
 struct Walk {
   Share sh;
   int64_t pos;
@@ -189,7 +189,7 @@ struct Walk {
   int32_t ub, b;
 
   // the next item, or one of no tiles
-  __device__ __forceinline__ void next(const Lens& L, int32_t prefix_len, Item& it) {
+  __device__ __forceinline__ void next(const Lens& L, int B, int32_t prefix_len, Item& it) {
     const int64_t start = sh.start, end = sh.end;
     it.n = 0;
     while (it.n <= 0 && pos < end) {
@@ -219,7 +219,18 @@ struct Walk {
           if (pos < next_cb) break;
           cb = next_cb;
           ub += units;
-          r = req_shape(L, ++b);
+          // the next request with units; the idle ones are passed 32 at a time
+          uint32_t some = 0;
+          while (!some && ++b < B) {
+            const int x = b + (int)(threadIdx.x & 31);
+            some = __ballot_sync(0xffffffffu, x < B && unit_count(req_shape(L, x)) > 0);
+            b += some ? __ffs(some) - 1 : 31;
+          }
+          if (!some) {  // lengths that changed under the kernel
+            pos = end;
+            return;
+          }
+          r = req_shape(L, b);
         }
         tiles = r.tiles;
         const int32_t j = (int32_t)quotient(pos - cb, tiles + kUnitCost);
@@ -818,7 +829,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       Walk walk{*share, share->start, share->first_cost, share->first_unit, share->first_b};
       __syncwarp();
       auto post = [&]() {  // the next item, one ahead of its tiles
-        walk.next(L, prefix_len, it);
+        walk.next(L, B, prefix_len, it);
         if (!W.wait(post_free(ni), ((ni >> 1) & 1u) ^ 1u)) return false;
         if (lane == 0) {
           posts[ni & 1u] = it;

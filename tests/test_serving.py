@@ -583,6 +583,18 @@ def test_attn_many_requests(B, H):
 
 
 @gpu
+@pytest.mark.parametrize("live", [[0], [2046], [31, 32, 33, 64, 1000, 1031, 2047],
+                                  [1, 30, 63, 65, 95, 97, 500, 501, 2000]])
+def test_attn_idle_requests_between(live):
+    """A batch that is mostly idle, some of it with tokens but no query."""
+    new, seq = [0] * 2048, [0, 5] * 1024
+    for b in live:
+        new[b], seq[b] = 1 + b % 3, 40 + b % 300
+    check_case(Case(new, seq, 0, 8, 128, 16, 2, seed=len(live)))
+    check_case(Case(new, seq, 300, 8, 128, 16, 2, seed=len(live)))
+
+
+@gpu
 def test_attn_padding_rows_may_hold_anything():
     c = Case([2, 1], [70, 5], 300, 16, 512, 64, 1, pad=9, seed=12)
     c.q[3:] = math.nan
