@@ -412,6 +412,12 @@ __device__ __forceinline__ void st_async_v4(uint32_t addr, const uint32_t (&v)[4
       ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(bar)
       : "memory");
 }
+__device__ __forceinline__ void st_async_f32(uint32_t addr, float v, uint32_t bar) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr),
+      "r"(__float_as_uint(v)), "r"(bar)
+      : "memory");
+}
 // TMA load into this CTA, its bytes counted by a barrier of either CTA.
 __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, int32_t c0,
                                               int32_t c1, uint32_t bar) {
@@ -451,6 +457,7 @@ __device__ __forceinline__ bool elect_one() {
       : "=r"(is));
   return is != 0;
 }
+__device__ __forceinline__ uint32_t round16(int x) { return ((uint32_t)x + 15u) & ~15u; }
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -648,7 +655,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(o_empty, 2 * kSoftWarps);
     mbar_init(xs, 2 * kSoftWarps);
     mbar_init(grp, kSoftWarps);
-    mbar_init(refs, kSoftWarps);
+    mbar_init(refs, rank == 0 ? kSoftWarps : 1);
     mbar_init(done_bar, 1);
     misc[0] = misc[2] = 0u;
     fence_mbar_init();
@@ -703,88 +710,101 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t u = 0, nq = 0;  // stages, items so far
       const int page = 1 << page_log2;
       bool ok = true;
-      while (ok && take(it)) {
-        const int32_t* pages = it.b < 0 ? prefix_table : table + (int64_t)it.b * max_blocks;
-        give_back();
-        if (!(ok = W.wait(q_empty, (nq & 1u) ^ 1u))) break;
-        if (arms) mbar_expect_tx(q_full, 2 * C::kQBytes);
-        if (lane < D / 64)
-          tma_load_pair(sQ + lane * 8192, &q_map, lane * 64, it.row0 + (int32_t)rank * 64,
-                        lead_q);
-        ++nq;
-        // page of key `half * 128 + key0` of tile j (0 where nothing is read)
-        auto page_at = [&](int32_t j, int half) {
-          const int32_t pos = j * kKeys + half * 128 + key0;
-          return pos < it.len ? __ldg(pages + (pos >> page_log2)) : 0;
-        };
-        // its first cache row, or out of range past the end
-        auto row_of = [&](int32_t j, int half, int32_t p) {
-          if (j * kKeys + half * 128 + key0 >= it.len) return n_rows_cache;
-          if (p < 0 || p >= n_pages) {
-            latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
-            return n_rows_cache;
-          }
-          return p << page_log2;
-        };
-        int32_t v_row[2] = {n_rows_cache, n_rows_cache};
-        const int32_t n = it.n;
-        int32_t tile = it.tile0 + it.rot, last = 0;  // this turn's tile, the turn's before
-        int32_t ids[2] = {page_at(tile, 0), page_at(tile, 1)};
-        for (int32_t j = 0; j <= n && ok; ++j) {
-          const int32_t c_row[2] = {row_of(tile, 0, ids[0]), row_of(tile, 1, ids[1])};
-          const int32_t ahead = tile_at(it.tile0, n, it.rot, j + 1 < n ? j + 1 : 0);
-          ids[0] = page_at(ahead, 0);  // looked at in the next round
-          ids[1] = page_at(ahead, 1);
-          if (j < n) {  // K of this turn's tile
-            const int32_t row = rank ? c_row[1] : c_row[0];
-#pragma unroll 1
-            for (int a = 0; a < C::kKStages; ++a, ++u) {
-              const uint32_t s = u % kStages;
-              if (!(ok = W.wait(empty(s), ((u / kStages) & 1u) ^ 1u))) break;
-              if (arms) mbar_expect_tx(full(s), 2 * kStageBytes);
-              if (on)
-                tma_load_pair(dst + s * kStageBytes, &k_map, a * 128 + col, row,
-                              lead_full + 8u * s);
-            }
-          }
-          if (j > 0 && ok) {  // V of the turn's before
-            const int32_t left0 = it.len - last * kKeys;
-#pragma unroll 1
-            for (int x = 0; x < C::kVStages; ++x, ++u) {
-              const uint32_t s = u % kStages;
-              const int half = x & 1;
-              if (!(ok = W.wait(empty(s), ((u / kStages) & 1u) ^ 1u))) break;
-              const int keys = left0 - 128 * half;  // of this stage, that count
-              const int32_t rows = half ? v_row[1] : v_row[0];
-              const int x0 = (x >> 1) * 256 + (int)rank * 128;
-              if (arms) mbar_expect_tx(full(s), 2 * kStageBytes);
-              if (keys <= 0 || (keys & (page - 1)) == 0 || keys >= 128) {
-                if (on)
-                  tma_load_pair(dst + s * kStageBytes, &v_map, x0 + col, rows,
-                                lead_full + 8u * s);
-                continue;
-              }
-              // The list ends inside a page.  The rows behind may hold NaN, which a
-              // zero weight does not cancel, so none of them is loaded: eight rows
-              // a lane, those around the end one by one, and zeros (out of range)
-              // past it.
-              const int end8 = keys & 7 ? keys >> 3 : 16;
-              const int r = lane < 16 ? 8 * lane : 8 * end8 + (lane & 7);
-              const int32_t from = __shfl_sync(0xffffffffu, rows, (r & 127) >> page_log2) +
-                                   (r & (page - 1));
-              if (lane < 16 ? lane != end8 : lane < 24 && end8 < 16)
-                for (int a = 0; a < 2; ++a)
-                  tma_load_pair(sStage + s * kStageBytes + a * kAtom + r * 128,
-                                lane < 16 ? &v8_map : &v1_map, x0 + a * 64,
-                                r < keys ? from : n_rows_cache, lead_full + 8u * s);
-            }
-          }
-          v_row[0] = c_row[0];
-          v_row[1] = c_row[1];
-          last = tile;
-          tile = ahead;
+      const int32_t* pages = nullptr;
+      int32_t tile = 0, turns = 0;  // this turn's tile, the item's turns so far
+      int32_t ids[2] = {0, 0};      // its pages
+      int32_t v_row[2] = {0, 0}, v_left = 0;  // the turn's before: V rows, keys from it on
+      bool k_on = false, v_on = false;        // is there a K tile, a V tile this turn
+      it.n = 0;
+      // page of key `half * 128 + key0` of tile j (0 where nothing is read)
+      auto page_at = [&](int32_t j, int half) {
+        const int32_t pos = j * kKeys + half * 128 + key0;
+        return pos < it.len ? __ldg(pages + (pos >> page_log2)) : 0;
+      };
+      // its first cache row, or out of range past the end
+      auto row_of = [&](int32_t j, int half, int32_t p) {
+        if (j * kKeys + half * 128 + key0 >= it.len) return n_rows_cache;
+        if (p < 0 || p >= n_pages) {
+          latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
+          return n_rows_cache;
         }
-      }
+        return p << page_log2;
+      };
+      // A turn: K of a tile and V of the tile before, across items
+      do {
+        if (turns == it.n) {
+          turns = 0;
+          k_on = take(it);
+          if (k_on) {
+            pages = it.b < 0 ? prefix_table : table + (int64_t)it.b * max_blocks;
+            give_back();
+            if (!(ok = W.wait(q_empty, (nq & 1u) ^ 1u))) break;
+            if (arms) mbar_expect_tx(q_full, 2 * C::kQBytes);
+            if (lane < D / 64)
+              tma_load_pair(sQ + lane * 8192, &q_map, lane * 64, it.row0 + (int32_t)rank * 64,
+                            lead_q);
+            ++nq;
+            tile = it.tile0 + it.rot;
+            ids[0] = page_at(tile, 0);
+            ids[1] = page_at(tile, 1);
+          }
+        }
+        int32_t c_row[2] = {0, 0}, c_left = 0;
+        if (k_on) {  // K of this turn's tile
+          c_row[0] = row_of(tile, 0, ids[0]);
+          c_row[1] = row_of(tile, 1, ids[1]);
+          c_left = it.len - tile * kKeys;
+          ++turns;
+          tile = tile_at(it.tile0, it.n, it.rot, turns < it.n ? turns : 0);
+          ids[0] = page_at(tile, 0);  // looked at in the next turn
+          ids[1] = page_at(tile, 1);
+          const int32_t row = rank ? c_row[1] : c_row[0];
+#pragma unroll 1
+          for (int a = 0; a < C::kKStages; ++a, ++u) {
+            const uint32_t s = u % kStages;
+            if (!(ok = W.wait(empty(s), ((u / kStages) & 1u) ^ 1u))) break;
+            if (arms) mbar_expect_tx(full(s), 2 * kStageBytes);
+            if (on)
+              tma_load_pair(dst + s * kStageBytes, &k_map, a * 128 + col, row,
+                            lead_full + 8u * s);
+          }
+        }
+        if (v_on && ok) {  // V of the turn's before
+#pragma unroll 1
+          for (int x = 0; x < C::kVStages; ++x, ++u) {
+            const uint32_t s = u % kStages;
+            const int half = x & 1;
+            if (!(ok = W.wait(empty(s), ((u / kStages) & 1u) ^ 1u))) break;
+            const int keys = v_left - 128 * half;  // of this stage, that count
+            const int32_t rows = half ? v_row[1] : v_row[0];
+            const int x0 = (x >> 1) * 256 + (int)rank * 128;
+            if (arms) mbar_expect_tx(full(s), 2 * kStageBytes);
+            if (keys <= 0 || (keys & (page - 1)) == 0 || keys >= 128) {
+              if (on)
+                tma_load_pair(dst + s * kStageBytes, &v_map, x0 + col, rows,
+                              lead_full + 8u * s);
+              continue;
+            }
+            // The list ends inside a page.  The rows behind may hold NaN, which a
+            // zero weight does not cancel, so none of them is loaded: eight rows
+            // a lane, those around the end one by one, and zeros (out of range)
+            // past it.
+            const int end8 = keys & 7 ? keys >> 3 : 16;
+            const int r = lane < 16 ? 8 * lane : 8 * end8 + (lane & 7);
+            const int32_t from = __shfl_sync(0xffffffffu, rows, (r & 127) >> page_log2) +
+                                 (r & (page - 1));
+            if (lane < 16 ? lane != end8 : lane < 24 && end8 < 16)
+              for (int a = 0; a < 2; ++a)
+                tma_load_pair(sStage + s * kStageBytes + a * kAtom + r * 128,
+                              lane < 16 ? &v8_map : &v1_map, x0 + a * 64,
+                              r < keys ? from : n_rows_cache, lead_full + 8u * s);
+          }
+        }
+        v_row[0] = c_row[0];
+        v_row[1] = c_row[1];
+        v_left = c_left;
+        v_on = k_on;
+      } while (ok && k_on);
       // the leader's last arrival here is done_bar's: the CTA outlives it
       if (ok && rank != 0 && u > 0) W.wait(done_bar, 0);
     } else if (warp == kScoutWarp && rank == 0) {
@@ -796,32 +816,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // waiting and meets the issuer at one barrier a stage.  When a wait gives
       // up it lets the issuer through what is left (on whatever shared memory
       // holds), so that no thread is left behind at a barrier.
-      uint32_t u = 0, nt = 0, nq = 0;
+      uint32_t u = 0, nt = 0, nq = 0, no = 0;  // stages, tiles, items by S^T and by O^T
       bool ok = true;
       auto let_in = [&]() {
         if (ok) ok = W.wait(full(u % kStages), (u / kStages) & 1u);
         asm volatile("bar.sync %0, 64;" ::"r"(1 + (u & 1u)) : "memory");
         ++u;
       };
-      for (;;) {
-        const int n = ok && take(it) ? it.n : 0;
-        if (lane == 0) misc[3] = (uint32_t)n;  // the issuer walks the same tiles
-        asm volatile("bar.sync 3, 64;" ::: "memory");
-        if (n == 0) break;
-        give_back();
-        if (ok) ok = W.wait(q_full, nq & 1u);
-        for (int j = 0; j <= n; ++j) {
-          if (j < n)
-            for (int c = 0; c < C::kKStages; ++c) let_in();
-          if (j == 0) continue;
-          const uint32_t t = nt + (uint32_t)j - 1u;
-          if (ok) ok = W.wait(p_full(t), turn(t));
-          if (ok && j == 1) ok = W.wait(o_empty, (nq & 1u) ^ 1u);
-          for (int c = 0; c < C::kVStages; ++c) let_in();
+      int left = 0;  // tiles of the item whose S^T is to come
+      bool s_on, o_on = false, o_first = false;
+      do {
+        const bool fresh = left == 0;
+        if (fresh) {
+          left = ok && take(it) ? it.n : 0;
+          if (lane == 0) misc[3] = (uint32_t)left;  // the issuer takes the same turns
+          asm volatile("bar.sync 3, 64;" ::: "memory");
+          if (left > 0) {
+            give_back();
+            if (ok) ok = W.wait(q_full, nq & 1u);
+            ++nq;
+          }
         }
-        nt += (uint32_t)n;
-        ++nq;
-      }
+        s_on = left > 0;
+        if (s_on) {
+          --left;
+          for (int c = 0; c < C::kKStages; ++c) let_in();
+        }
+        if (o_on) {
+          if (ok) ok = W.wait(p_full(nt), turn(nt));
+          if (o_first) {
+            if (ok) ok = W.wait(o_empty, (no & 1u) ^ 1u);
+            ++no;
+          }
+          for (int c = 0; c < C::kVStages; ++c) let_in();
+          ++nt;
+        }
+        o_on = s_on;
+        o_first = fresh;
+      } while (s_on);
     } else if (warp == kPassWarp) {
       // ===== items to the softmax warps; this CTA's P complete -> the leader
       uint32_t nt = 0;
@@ -874,41 +906,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         ++u;
       };
-      for (;;) {
-        asm volatile("bar.sync 3, 64;" ::: "memory");
-        const int n = (int)*reinterpret_cast<volatile uint32_t*>(misc + 3);
-        if (n == 0) break;
-        for (int j = 0; j <= n; ++j) {
-          if (j < n) {
-            // the softmax has read this S^T buffer's last tile: that tile's PV,
-            // which waited for it, is ahead in this order
-            const uint32_t d = tmem + ((nt + (uint32_t)j) & 1u) * kRows;
-#pragma unroll
-            for (uint32_t c = 0; c < C::kKStages; ++c)
-              stage([&](uint32_t at, uint32_t x) {  // 64-dim atom x / 4, 16 dims each
-                tc_mma2(d, dK + at + (x >> 2) * (kAtom >> 4) + (x & 3) * 2,
-                        dQ + (2 * c + (x >> 2)) * 512 + (x & 3) * 2, IDESC_S,
-                        c + x != 0 ? 1u : 0u);
-              });
-            if (elect_one()) {
-              if (j == n - 1) tc_commit2(q_empty);
-              tc_commit2(s_full((nt + (uint32_t)j) & 1u));
-            }
-          }
-          if (j >= 1) {
-            const uint32_t t = nt + (uint32_t)j - 1u;
-            const uint64_t db = dP + (t & (C::kPBufs - 1)) * (C::kPBytes >> 4);
-#pragma unroll
-            for (uint32_t c = 0; c < C::kVStages; ++c)
-              stage([&](uint32_t at, uint32_t x) {  // 16 keys each
-                tc_mma2(tO + (c >> 1) * kRows, dV + at + x * 128, db + ((c & 1) * 8 + x) * 128,
-                        IDESC_O, j > 1 || (c & 1) + x != 0 ? 1u : 0u);
-              });
-            if (elect_one()) tc_commit2(p_done(t));
-          }
+      int left = 0;
+      bool s_on, o_on = false, o_first = false;
+      do {  // a turn: S^T of a tile and O^T of the tile before, across items
+        const bool fresh = left == 0;
+        if (fresh) {
+          asm volatile("bar.sync 3, 64;" ::: "memory");
+          left = (int)*reinterpret_cast<volatile uint32_t*>(misc + 3);
         }
-        nt += (uint32_t)n;
-      }
+        s_on = left > 0;
+        if (s_on) {
+          // the softmax has read this S^T buffer's last tile: that tile's PV,
+          // which waited for it, is ahead in this order
+          const uint32_t b = (nt + (o_on ? 1u : 0u)) & 1u, d = tmem + b * kRows;
+#pragma unroll 1
+          for (uint32_t c = 0; c < C::kKStages; ++c)
+            stage([&](uint32_t at, uint32_t x) {  // 64-dim atom x / 4, 16 dims each
+              tc_mma2(d, dK + at + (x >> 2) * (kAtom >> 4) + (x & 3) * 2,
+                      dQ + (2 * c + (x >> 2)) * 512 + (x & 3) * 2, IDESC_S,
+                      c + x != 0 ? 1u : 0u);
+            });
+          if (elect_one()) {
+            if (left == 1) tc_commit2(q_empty);
+            tc_commit2(s_full(b));
+          }
+          --left;
+        }
+        if (o_on) {
+          const uint64_t db = dP + (nt & (C::kPBufs - 1)) * (C::kPBytes >> 4);
+#pragma unroll 1
+          for (uint32_t c = 0; c < C::kVStages; ++c)
+            stage([&](uint32_t at, uint32_t x) {  // 16 keys each
+              tc_mma2(tO + (c >> 1) * kRows, dV + at + x * 128, db + ((c & 1) * 8 + x) * 128,
+                      IDESC_O, !o_first || (c & 1) + x != 0 ? 1u : 0u);
+            });
+          if (elect_one()) tc_commit2(p_done(nt));
+          ++nt;
+        }
+        o_on = s_on;
+        o_first = fresh;
+      } while (s_on);
       if (u > 0) {
         if (elect_one()) tc_commit2(done_bar);
         __syncwarp();
@@ -960,6 +997,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             : (uint8_t)(row_limit(req_shape(L, pb), L.H,
                                                   post->rel0 + min(tid, post->n_rows - 1)) -
                                         lim_min);
+        // rows without a reference have no weights
+        if (tid >= (int)round16(post->n_rows)) nm_s[tid] = -INFINITY;
       }
       if (!(ok = group_sync())) break;
       uint64_t l[32];  // this thread's row sums, in pairs
@@ -971,14 +1010,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // 32 keys of its lanes in the item's first tile.  Where some row does not
       // see all of that tile, over its first 32 keys, by the first warp of the
       // group: every row that sees a key of the item sees one of those (the
-      // requests' own tokens are taken in order).
+      // requests' own tokens are taken in order).  CTA 1 counts theirs by bytes.
       auto first_refs = [&](int32_t tile, uint32_t b) {
+        const int n_rows = post->n_rows;
         if (rank == 0) {
           const bool whole = (tile + 1) * kKeys <= lim_min;  // uniform
           const int32_t pos = tile * kKeys + quad * 32 + lane;
+          const int h_end = min(n_rows, r0 + (whole ? 16 * (quad + 1) : quad ? 0 : kGroupRows));
 #pragma unroll 1
-          for (int c = whole ? quad : 0; live && c < (whole ? quad + 1 : quad ? 0 : 4); ++c) {
-            const int h0 = r0 + 16 * c;
+          for (int h0 = r0 + (whole ? 16 * quad : 0); h0 < h_end; h0 += 16) {
             float x[16];
             uint32_t r[16];
             tmem_ld16(tmem + b * kRows + lane_base + h0, r);
@@ -991,15 +1031,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (pos >= lim_min + lim_s[h0 + e]) x[e] = -INFINITY;
             }
             const float t = column_reduce<true>(x, lane), ref = t == -INFINITY ? 0.f : -t;
-            // lanes 0-15 tell this CTA, 16-31 the other
-            st_cluster_u32(at_rank(smem_u32(nm_s + h0 + (lane & 15)), (uint32_t)lane >> 4),
-                           __float_as_uint(ref));
+            float* to = nm_s + h0 + (lane & 15);
+            if (lane < 16) *to = ref;
+            else st_async_f32(at_rank(smem_u32(to), 1), ref, at_rank(refs, 1));
           }
           __syncwarp();
-          if (lane == 0) {
-            mbar_signal(at_rank(refs, 0));
-            mbar_release_cluster(at_rank(refs, 1));
-          }
+          if (lane == 0) mbar_arrive(refs);
+        } else if (tid == 0) {
+          mbar_expect_tx(refs, 4 * round16(n_rows));
         }
         return W.wait(refs, nf++ & 1u);
       };
@@ -1041,14 +1080,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // P of a tile from S^T in buffer b, whether a score is beyond its
       // reference, and l.  The weights of 32 rows among which one is beyond are
       // left out of l, which so stays finite, and are added when the tile is
-      // visited again (`revisit`) under references that hold them.  `Plain`: no
-      // mask, first visit; without branches, so that the work on one half of
-      // the rows overlaps the other's loads.
+      // visited again (`revisit`) under references that hold them.  `Plain`: each
+      // key is seen by all rows or by none, first visit; without branches, so that
+      // the work on one half of the rows overlaps the other's loads.
       uint32_t left = 0;
       auto weights = [&](auto plain, int32_t tile, uint32_t b, bool revisit) {
         constexpr bool Plain = decltype(plain)::value;
         const int32_t pos = tile * kKeys + key;
         const bool masked = !Plain && (tile + 1) * kKeys > lim_min;  // uniform
+        const bool seen = !Plain || pos < lim_min;
         uint32_t r[2][32];
         const uint32_t tS = tmem + b * kRows + lane_base + r0;
         const ulonglong2* refs2 = reinterpret_cast<const ulonglong2*>(nm_s + r0);
@@ -1074,14 +1114,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     d[e + 2], d[e + 3]);
           }
           if (!Plain && masked) {
-            if (same) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) d[e] = pos < lim_min ? d[e] : -INFINITY;
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (pos >= lim_min + lim_s[r0 + 32 * h + e]) d[e] = -INFINITY;
-            }
+            for (int e = 0; e < 32; ++e)
+              if (pos >= lim_min + lim_s[r0 + 32 * h + e]) d[e] = -INFINITY;
           }
           float top[4];
 #pragma unroll
@@ -1092,14 +1127,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int y = 0; y < 4; ++y)
               top[y] = e + 4 < 32 ? fmaxf(top[y], fmaxf(d[e + y], d[e + 4 + y]))
                                   : fmaxf(top[y], d[e + y]);
-          const bool beyond = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > kSlack;
+          const bool beyond =
+              fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > kSlack && seen;
           any |= beyond;
           left |= beyond ? 1u << h : 0u;
-          const bool add = !beyond && (Plain || !revisit || (out_before >> h & 1u) != 0u);
+          const bool add = !beyond && seen && (Plain || !revisit || (out_before >> h & 1u) != 0u);
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             const float p0 = ex2(d[e]), p1 = ex2(d[e + 1]);
-            pk[16 * h + e / 2] = pack_bf16(p0, p1);
+            pk[16 * h + e / 2] = seen ? pack_bf16(p0, p1) : 0u;
             if (add) l[16 * h + e / 2] = add2(l[16 * h + e / 2], pair2(p0, p1));
           }
         }
@@ -1166,7 +1202,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (bool revisit = false;; revisit = true) {
           bool beyond = false;
           if (live)
-            beyond = !revisit && (tile + 1) * kKeys <= lim_min
+            beyond = !revisit && (same || (tile + 1) * kKeys <= lim_min)
                          ? weights(std::true_type{}, tile, b, false)
                          : weights(std::false_type{}, tile, b, revisit);
           if (revisit) break;
@@ -1266,11 +1302,15 @@ __global__ void __launch_bounds__(128) join_kernel(PlanView view, Lens L,
   const int64_t row = blockIdx.x * (int64_t)kPer + sub, t = row / L.H;
   // the row's request, from the call's inputs: before the main kernel's end
   const bool mine = row < n_rows && t >= __ldg(L.cu) && t < __ldg(L.cu + B);
-  int lo = 0, hi = mine ? B : 0;  // the last b with cu[b] <= t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(L.cu + mid) <= t) lo = mid;
-    else hi = mid;
+  // the last b in [lo, lo + n) with cu[b] <= t, a 32nd at a time (a warp has one row)
+  const int lane = threadIdx.x & 31;
+  int lo = 0;
+  for (int n = mine ? B : 0; n > 1;) {
+    const int step = (n + 31) >> 5, x = lane * step;
+    const uint32_t le = __ballot_sync(0xffffffffu, x < n && __ldg(L.cu + lo + min(x, n - 1)) <= t);
+    const int at = (31 - __clz(le | 1u)) * step;
+    lo += at;
+    n = min(step, n - at);
   }
   ReqShape r{};
   if (mine) r = req_shape(L, lo);
