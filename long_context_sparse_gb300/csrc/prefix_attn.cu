@@ -1286,20 +1286,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- joining
-// Row by row, D / 4 threads each: the slots of the row's prefix unit and of
-// its own unit, weighted by 2^(m_i - M).  Reads each partial result once;
-// kJoin of them in flight.
+// Row by row, D / 4 threads each: the slots of the row's prefix unit and of its
+// own unit, weighted by 2^(m_i - M).  A tile at cost c belongs to pair
+// c / chunk, so a unit's slots are those of the pairs of its first tile to its
+// last.  Each lane takes one slot's m and l; then every partial result is read
+// once, kJoin of them in flight.
 constexpr int kJoin = 8;
 
 template <int D>
-__global__ void __launch_bounds__(128) join_kernel(PlanView view, Lens L,
-                                                   __nv_bfloat16* __restrict__ o,
-                                                   float* __restrict__ lse, int B,
-                                                   int64_t n_rows, int64_t n_slots,
-                                                   uint32_t* status) {
+__global__ void __launch_bounds__(128, 8) join_kernel(PlanView view, Lens L,
+                                                      __nv_bfloat16* __restrict__ o,
+                                                      float* __restrict__ lse, int B,
+                                                      int64_t n_rows, int64_t n_slots,
+                                                      uint32_t* status) {
   constexpr int kPer = 512 / D, kLanes = D / 4;  // rows of a block, threads of a row
   const int sub = threadIdx.x / kLanes, th = threadIdx.x % kLanes;
-  const int64_t row = blockIdx.x * (int64_t)kPer + sub, t = row / L.H;
+  const int64_t row = blockIdx.x * (int64_t)kPer + sub;
+  const int32_t t = (int32_t)row / L.H;  // n_rows <= 2^20
   // the row's request, from the call's inputs: before the main kernel's end
   const bool mine = row < n_rows && t >= __ldg(L.cu) && t < __ldg(L.cu + B);
   // the last b in [lo, lo + n) with cu[b] <= t, a 32nd at a time (a warp has one row)
@@ -1320,70 +1323,67 @@ __global__ void __launch_bounds__(128) join_kernel(PlanView view, Lens L,
   const Plan plan = *view.p;
   const int64_t cost = view.ccum[lo];
   const int32_t first_unit = view.ucum[lo];
-  // The prefix unit and the request's own: first cost, tiles, tiles that hold
-  // keys, number, row in it; and the first pair and the pairs that share it.
-  int64_t c0[2], i0[2];
-  int32_t tiles[2], used[2], unit[2], at[2], pairs[2];
-  tiles[0] = used[0] = plan.prefix_cost > 0 ? plan.prefix_tiles : 0;
-  unit[0] = (int32_t)(row / kRows);
-  at[0] = (int32_t)(row % kRows);
-  c0[0] = (int64_t)unit[0] * (tiles[0] + kUnitCost);
-  tiles[1] = r.tiles;
-  used[1] = (min(r.len, row_limit(r, L.H, min((block + 1) * kRows, r.n_rows) - 1)) + kKeys - 1) /
-            kKeys;
-  unit[1] = first_unit + block;
-  at[1] = rel % kRows;
-  c0[1] = cost + (int64_t)block * (tiles[1] + kUnitCost);
+  // slots s[x] .. s[x] + n[x] - 1: of the prefix unit, of the request's own
+  int32_t s[2] = {0, 0}, n[2] = {0, 0};
+  const int32_t at[2] = {(int32_t)(row % kRows), rel % kRows};
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
-    i0[x] = quotient(c0[x], plan.chunk);
-    pairs[x] = plan.total > 0 && tiles[x] > 0
-                   ? (int32_t)(quotient(c0[x] + tiles[x] + kUnitCost - 1, plan.chunk) - i0[x]) + 1
-                   : 0;
+    const int32_t tiles = x ? r.tiles : plan.prefix_tiles;
+    // tiles that hold keys which some row of the block sees
+    const int32_t used =
+        x ? (min(r.len, row_limit(r, L.H, min((block + 1) * kRows, r.n_rows) - 1)) + kKeys - 1) /
+                kKeys
+          : tiles;
+    if (plan.total == 0 || used == 0) continue;
+    const int32_t u = x ? block : (int32_t)(row / kRows);
+    const int64_t c = (x ? cost : 0) + (int64_t)u * (tiles + kUnitCost) + kUnitCost;
+    const int32_t first = (int32_t)quotient(c, plan.chunk);
+    n[x] = (int32_t)(quotient(c + used - 1, plan.chunk) - first) + 1;
+    s[x] = (x ? first_unit : 0) + u + first;
   }
+  const int count = n[0] + n[1];
   float m = -INFINITY, l = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = 0; i < pairs[0] + pairs[1]; i += kJoin) {
-    float2 p0[kJoin], p1[kJoin];
-    float4 oi[kJoin];
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f), oi[kJoin];
+  // row of the partial results with slot number k of this row's
+  auto part = [&](int k) { return (k < n[0] ? s[0] + k : s[1] + (k - n[0])) * (int64_t)kRows; };
+  auto in_part = [&](int k) { return k < n[0] ? at[0] : at[1]; };
+  auto load = [&](int k0) {
 #pragma unroll
-    for (int e = 0; e < kJoin; ++e) {
-      p0[e] = p1[e] = make_float2(-INFINITY, 0.f);
-      oi[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-      const bool own = i + e >= pairs[0];
-      const int64_t p = own ? i0[1] + (i + e - pairs[0]) : i0[0] + (i + e);
-      int32_t a, z;
-      share_of(own ? c0[1] : c0[0], own ? tiles[1] : tiles[0], p * plan.chunk,
-               min(plan.total, (p + 1) * plan.chunk), a, z);
-      const int64_t slot = (own ? unit[1] : unit[0]) + p;
-      if (i + e < pairs[0] + pairs[1] && a < min(z, own ? used[1] : used[0]) &&
-          DSA_IN_BOUNDS(slot < n_slots, status)) {
-        const int32_t rr = own ? at[1] : at[0];
-        p0[e] = view.ml[(slot * 2) * kRows + rr];
-        p1[e] = view.ml[(slot * 2 + 1) * kRows + rr];
-        oi[e] = reinterpret_cast<const float4*>(view.o + (slot * kRows + rr) * D)[th];
-      }
+    for (int e = 0; e < kJoin; ++e)
+      if (k0 + e < count && DSA_IN_BOUNDS(part(k0 + e) < n_slots * kRows, status))
+        oi[e] = reinterpret_cast<const float4*>(view.o + (part(k0 + e) + in_part(k0 + e)) * D)[th];
+  };
+  for (int i = 0; i < count; i += 32) {
+    load(i);  // on the way while the weights are worked out
+    float mi = -INFINITY, li = 0.f;
+    if (i + lane < count && DSA_IN_BOUNDS(part(i + lane) < n_slots * kRows, status)) {
+      const float2* ml = view.ml + 2 * part(i + lane) + in_part(i + lane);
+      const float2 a = ml[0], b = ml[kRows];
+      li = a.y + b.y;  // 0: no key seen
+      if (li != 0.f) mi = a.x;
     }
-    float top = m;
+    float top = fmaxf(m, mi);
 #pragma unroll
-    for (int e = 0; e < kJoin; ++e) {
-      p1[e].y += p0[e].y;                        // l; 0: no key seen
-      if (p1[e].y == 0.f) p0[e].x = -INFINITY;
-      top = fmaxf(top, p0[e].x);
-    }
-    const float keep = top == -INFINITY ? 1.f : ex2(m - top);
-    l *= keep;
+    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    const float keep = m == -INFINITY ? 0.f : ex2(m - top);
+    const float w = mi == -INFINITY ? 0.f : ex2(mi - top);
+    li *= w;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) li += __shfl_xor_sync(0xffffffffu, li, x);
+    l = fmaf(l, keep, li);
     acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
     m = top;
+    for (int j = 0; j < 32 && i + j < count; j += kJoin) {
+      if (j > 0) load(i + j);
 #pragma unroll
-    for (int e = 0; e < kJoin; ++e) {
-      if (p0[e].x == -INFINITY) continue;
-      const float w = ex2(p0[e].x - top);
-      l = fmaf(w, p1[e].y, l);
-      acc.x = fmaf(w, oi[e].x, acc.x);
-      acc.y = fmaf(w, oi[e].y, acc.y);
-      acc.z = fmaf(w, oi[e].z, acc.z);
-      acc.w = fmaf(w, oi[e].w, acc.w);
+      for (int e = 0; e < kJoin; ++e) {
+        const float we = __shfl_sync(0xffffffffu, w, j + e);  // 0 past the last slot
+        if (we == 0.f) continue;  // what no key went into may be anything
+        acc.x = fmaf(we, oi[e].x, acc.x);
+        acc.y = fmaf(we, oi[e].y, acc.y);
+        acc.z = fmaf(we, oi[e].z, acc.z);
+        acc.w = fmaf(we, oi[e].w, acc.w);
+      }
     }
   }
   const bool none = m == -INFINITY;
