@@ -1286,21 +1286,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- joining
-// Row by row, D / 4 threads each: the slots of the row's prefix unit and of its
+// Row by row, Lanes threads each: the slots of the row's prefix unit and of its
 // own unit, weighted by 2^(m_i - M).  A tile at cost c belongs to pair
 // c / chunk, so a unit's slots are those of the pairs of its first tile to its
 // last.  Each lane takes one slot's m and l; then every partial result is read
 // once, kJoin of them in flight.
-constexpr int kJoin = 8;
+constexpr int kJoinBlocks = 8;  // of 128 threads on an SM
 
-template <int D>
-__global__ void __launch_bounds__(128, 8) join_kernel(PlanView view, Lens L,
+template <int D, int Lanes>
+__global__ void __launch_bounds__(128, D == 16 * Lanes ? 6 : kJoinBlocks) join_kernel(PlanView view, Lens L,
                                                       __nv_bfloat16* __restrict__ o,
                                                       float* __restrict__ lse, int B,
                                                       int64_t n_rows, int64_t n_slots,
                                                       uint32_t* status) {
-  constexpr int kPer = 512 / D, kLanes = D / 4;  // rows of a block, threads of a row
-  const int sub = threadIdx.x / kLanes, th = threadIdx.x % kLanes;
+  constexpr int kPer = 128 / Lanes;      // rows of a block
+  constexpr int kVec = D / (4 * Lanes);  // float4 of a thread in a row
+  constexpr int kJoin = 8 / kVec;        // partial results in flight
+  const int sub = threadIdx.x / Lanes, th = threadIdx.x % Lanes;
   const int64_t row = blockIdx.x * (int64_t)kPer + sub;
   const int32_t t = (int32_t)row / L.H;  // n_rows <= 2^20
   // the row's request, from the call's inputs: before the main kernel's end
@@ -1343,7 +1345,9 @@ __global__ void __launch_bounds__(128, 8) join_kernel(PlanView view, Lens L,
   }
   const int count = n[0] + n[1];
   float m = -INFINITY, l = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f), oi[kJoin];
+  float4 acc[kVec], oi[kJoin][kVec];
+#pragma unroll
+  for (int v = 0; v < kVec; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
   // row of the partial results with slot number k of this row's
   auto part = [&](int k) { return (k < n[0] ? s[0] + k : s[1] + (k - n[0])) * (int64_t)kRows; };
   auto in_part = [&](int k) { return k < n[0] ? at[0] : at[1]; };
@@ -1351,7 +1355,10 @@ __global__ void __launch_bounds__(128, 8) join_kernel(PlanView view, Lens L,
 #pragma unroll
     for (int e = 0; e < kJoin; ++e)
       if (k0 + e < count && DSA_IN_BOUNDS(part(k0 + e) < n_slots * kRows, status))
-        oi[e] = reinterpret_cast<const float4*>(view.o + (part(k0 + e) + in_part(k0 + e)) * D)[th];
+#pragma unroll
+        for (int v = 0; v < kVec; ++v)
+          oi[e][v] = reinterpret_cast<const float4*>(view.o + (part(k0 + e) + in_part(k0 + e)) *
+                                                                  D)[v * Lanes + th];
   };
   for (int i = 0; i < count; i += 32) {
     load(i);  // on the way while the weights are worked out
@@ -1371,7 +1378,9 @@ __global__ void __launch_bounds__(128, 8) join_kernel(PlanView view, Lens L,
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) li += __shfl_xor_sync(0xffffffffu, li, x);
     l = fmaf(l, keep, li);
-    acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
+#pragma unroll
+    for (int v = 0; v < kVec; ++v)
+      acc[v] = make_float4(acc[v].x * keep, acc[v].y * keep, acc[v].z * keep, acc[v].w * keep);
     m = top;
     for (int j = 0; j < 32 && i + j < count; j += kJoin) {
       if (j > 0) load(i + j);
@@ -1379,17 +1388,23 @@ __global__ void __launch_bounds__(128, 8) join_kernel(PlanView view, Lens L,
       for (int e = 0; e < kJoin; ++e) {
         const float we = __shfl_sync(0xffffffffu, w, j + e);  // 0 past the last slot
         if (we == 0.f) continue;  // what no key went into may be anything
-        acc.x = fmaf(we, oi[e].x, acc.x);
-        acc.y = fmaf(we, oi[e].y, acc.y);
-        acc.z = fmaf(we, oi[e].z, acc.z);
-        acc.w = fmaf(we, oi[e].w, acc.w);
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) {
+          acc[v].x = fmaf(we, oi[e][v].x, acc[v].x);
+          acc[v].y = fmaf(we, oi[e][v].y, acc[v].y);
+          acc[v].z = fmaf(we, oi[e][v].z, acc[v].z);
+          acc[v].w = fmaf(we, oi[e][v].w, acc[v].w);
+        }
       }
     }
   }
   const bool none = m == -INFINITY;
   const float inv = none ? 0.f : 1.f / l;
-  reinterpret_cast<uint2*>(o + row * D)[th] =
-      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+#pragma unroll
+  for (int v = 0; v < kVec; ++v)
+    reinterpret_cast<uint2*>(o + row * D)[v * Lanes + th] =
+        make_uint2(pack_bf16(acc[v].x * inv, acc[v].y * inv),
+                   pack_bf16(acc[v].z * inv, acc[v].w * inv));
   if (th == 0) lse[row] = none ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
@@ -1417,7 +1432,10 @@ cudaError_t launch_t(const LaunchCtx& c, const ServeShape& s, const CUtensorMap&
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // launched while the main kernel runs, which it waits for on the device
   const int64_t rows = s.T * s.H;
-  constexpr int per = 512 / D;
+  // D / 4 threads a row while all rows are on the SMs at once, else a warp each,
+  // which looks a row up once
+  const bool wide = rows * (D / 4) <= (int64_t)c.num_sms * kJoinBlocks * 128;
+  const int64_t per = wide ? 512 / D : 4;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((rows + per - 1) / per));
   cfg.blockDim = dim3(128);
@@ -1427,7 +1445,7 @@ cudaError_t launch_t(const LaunchCtx& c, const ServeShape& s, const CUtensorMap&
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D>, view, L, o, lse, s.B, rows, slots, c.status);
+  return cudaLaunchKernelEx(&cfg, wide ? join_kernel<D, D / 4> : join_kernel<D, 32>, view, L, o, lse, s.B, rows, slots, c.status);
 }
 
 }  // namespace
