@@ -374,9 +374,11 @@ __device__ __forceinline__ uint32_t at_rank(uint32_t saddr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
   return r;
 }
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
-               ::: "memory");
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // Arrivals at a barrier of either CTA: with a cluster-scope release of this
 // thread's writes, and without.
@@ -670,12 +672,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
+  // the barriers and TMEM are ready: the CTAs meet while they divide the work
+  tc_fence_before();
+  __syncwarp();
+  cluster_arrive();
   const int64_t pair = blockIdx.x >> 1;
   divide(L, B, T, prefix_len, pair, gridDim.x >> 1, blockIdx.x == 0 ? &view : nullptr, status,
          share, reinterpret_cast<int64_t*>(red));
-  tc_fence_before();
   __syncthreads();
-  cluster_sync_all();
+  cluster_wait();
   tc_fence_after();
   // item ni, as kPassWarp posted it, one ahead of its tiles
   uint32_t ni = 0;
@@ -1278,7 +1283,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();
+  cluster_arrive();
+  cluster_wait();
   tc_fence_after();
   if (warp == kMmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
