@@ -14,7 +14,8 @@ namespace {
 // reads 512 KB), so no block waits for another and one launch does it all.
 // Blocks of one column (gridDim.y) share the owned requests' pages and
 // tokens.  Bound by latency: one read of the lengths, one reduction, one
-// scan, then independent writes.
+// scan, then a binary search in shared memory, a page id and a write a slot.
+// 64 requests of one token: 2.9 us; 2047 requests, 1.05M slots (4.8 MB): 8.7.
 constexpr int kReq = 256;
 
 struct ReqLens {
@@ -166,6 +167,8 @@ __global__ void __launch_bounds__(kReq) page_tables_kernel(
 // ---------------------------------------------------------------- append
 // One 16-byte piece of a row per thread and tensor, kUnroll rows' pieces in
 // flight: a copy, bound by HBM (each row read once and written once).
+// 131071 rows of K and V, d = 512 (537 MB): 81.3 us, 6.6 TB/s, 97% of a plain
+// copy's rate; 64 rows of one tensor: 1.5 us.
 constexpr int kUnroll = 4;
 
 template <int D>
@@ -207,9 +210,10 @@ cudaError_t launch_page_tables(const LaunchCtx& c, const ServeShape& s,
                                const int32_t* free_pages, int64_t n_free, int32_t* table,
                                int32_t* slots, int32_t* cu, int32_t* seq, int32_t* taken) {
   const int chunks = (s.B + kReq - 1) / kReq;
-  // about 4 slots a thread, at most two blocks an SM
+  // about 4 slots a thread, at most four blocks an SM (2047 requests, 1.05M slots:
+  // 8.7 us, with two 10.8, with eight 11.0: each adds up the requests before it)
   int64_t y = (s.T + 4 * kReq - 1) / (4 * kReq);
-  const int64_t most = 2 * (int64_t)c.num_sms / chunks;
+  const int64_t most = 4 * (int64_t)c.num_sms / chunks;
   if (y > most) y = most;
   if (y < 1) y = 1;
   page_tables_kernel<<<dim3(chunks, (unsigned)y), kReq, 0, c.stream>>>(
