@@ -22,10 +22,10 @@
 //   P = 2^(s - m),  l += P,  O^T += V^T P^T      (O, l, m in fp32, P in bf16:
 //   the tensor core's operand type, one rounding of each weight).
 // m of a row is a reference near its maximum, shared by the pair: the maximum
-// over the first 32 keys of the unit's first tile, afterwards raised only when
-// a score passes it by more than 2^20.  (Any reference gives the same result as
-// long as nothing overflows: the weights are floating point, and fp32 leaves
-// 2^107 above.)  So the usual tile has no maxima to exchange.  A warp that meets
+// over 32 keys of the first tile, afterwards raised only when a weight would
+// pass 2^20.  (Any reference gives the same result as long as nothing
+// overflows: the weights are floating point, and fp32 leaves 2^107 above.)
+// So the usual tile has no maxima to exchange.  A warp that meets
 // a larger score raises a flag; the softmax warps of the pair meet once a tile,
 // behind the tensor cores' work on the tile before, and where the flag is up
 // they take the exact maxima and rescale l and O^T before they hand P over.
@@ -39,9 +39,20 @@
 //
 // Work.  Units cost their tiles plus kUnitCost; the pairs share the sum
 // evenly in unit order, so a long prefix is split over all of them and short
-// requests are packed together.  Every (unit, pair) that meet leaves O, m and
-// l (fp32, not normalised) in a slot of the workspace, and a second kernel
-// joins each row's slots: sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
+// requests are packed together.  What a pair has of a unit is an item.  Every
+// (unit, pair) that meet leaves O, m and l (fp32, not normalised) in a slot of
+// the workspace, and a second kernel joins each row's slots:
+// sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
+//
+// Bounds.  Many rows (64 requests of 64 heads of 512 behind 128k keys, 1107
+// GFLOP): 784 us, 1412 TFLOP/s, 73% of the measured bf16 peak; a stage of the
+// ring takes about 740 cycles of which its products need 512: the loads' way
+// from L2 (about 1500 cycles under load, four stages on the way) and the
+// hand-over between the warps; the softmax warps' arithmetic is 3%.  Two stages
+// more would need the shared memory that Q takes.  Few rows behind 1M keys (8
+// requests of 16 heads): 248 us for 1.08 GB, 4.4 TB/s.  Small calls: 15 us on the
+// GPU, a chain of lookups, loads and hand-overs; each item takes about 10 us from
+// its first tile's loads to its results, overlapped with the next one's loads.
 #include <atomic>
 #include <type_traits>
 
@@ -54,7 +65,10 @@ namespace {
 constexpr int kRows = 128;           // rows of a unit
 constexpr int kKeys = 256;           // keys of a tile
 constexpr int kMaxPairs = 80;        // workspace bound on the pairs of a launch
-constexpr int kUnitCost = 2;         // a unit's Q load and epilogue, in tiles
+// A unit's Q load and epilogue, in tiles (us a call of 16 requests of 64 heads
+// behind 16k, ragged drafts, ragged prompts, 64 behind 128k: with 1 51.5, 128, 541,
+// 771; with 2 47.8, 120, 516, 743; with 3 49.6, 120, 522, 737).
+constexpr int kUnitCost = 2;
 constexpr int kSoftWarps = 8;        // 4 TMEM lane quadrants x 2 groups of rows
 constexpr int kGroupRows = 64;
 constexpr int kProdWarp = 8, kScoutWarp = 9, kMmaWarp = 10, kPassWarp = 11;
@@ -555,7 +569,8 @@ struct PCfg {
   // P buffers: where two fit, a tile's P is written while the one before is read
   static constexpr uint32_t kPBufs = D == 512 ? 1 : 2;
   static constexpr uint32_t kTail = 2048;
-  static constexpr uint32_t kSmem = 1024 + kQBytes + kPBufs * kPBytes + kStages * kStageBytes + kTail;
+  static constexpr uint32_t kSmem =
+      1024 + kQBytes + kPBufs * kPBytes + kStages * kStageBytes + kTail;
   static_assert(kSmem <= 232448, "shared memory");
 };
 
@@ -586,8 +601,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                        const __grid_constant__ CUtensorMap v1_map, PlanView view, Lens L,
                        const int32_t* __restrict__ prefix_table, int32_t prefix_len,
                        const int32_t* __restrict__ table, int B, int64_t T,
-                       int max_blocks, int page_log2, int32_t n_pages, int64_t n_slots, float scale_log2,
-                       uint32_t* status, uint64_t timeout_ns) {
+                       int max_blocks, int page_log2, int32_t n_pages, int64_t n_slots,
+                       float scale_log2, uint32_t* status, uint64_t timeout_ns) {
   using C = PCfg<D>;
   constexpr uint32_t IDESC_S = idesc_bf16(256, 128, 0, 0);
   constexpr uint32_t IDESC_O = idesc_bf16(256, 128, 1, 1);
@@ -604,7 +619,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   float* nmo_s = nm2_s + 2 * kRows;                       // [row] -m before it was last raised
   uint8_t* lim_s = reinterpret_cast<uint8_t*>(nmo_s + kRows);  // [row] keys past lim_min
   uint64_t* bars = reinterpret_cast<uint64_t*>(lim_s + kRows);
-  uint32_t* misc = reinterpret_cast<uint32_t*>(bars + kBars);  // abort, tmem, beyond, issuer's tiles
+  // abort, tmem, beyond, issuer's tiles
+  uint32_t* misc = reinterpret_cast<uint32_t*>(bars + kBars);
   Item* posts = reinterpret_cast<Item*>(misc + 4);             // [2]
   static_assert(3 * kRows * 4 + kRows + kBars * 8 + 16 + 2 * sizeof(Item) <= C::kTail, "tail");
   const int tid = threadIdx.x, lane = tid & 31;
@@ -1227,7 +1243,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!ok) break;
         // the P buffer's last tile has been read (a group without rows writes none,
         // and nothing waits for it: it could come after the buffer's next tile)
-        if (live && nt >= C::kPBufs && !(ok = W.wait(p_done(nt - C::kPBufs), turn(nt - C::kPBufs)))) break;
+        if (live && nt >= C::kPBufs &&
+            !(ok = W.wait(p_done(nt - C::kPBufs), turn(nt - C::kPBufs))))
+          break;
         hand_over();
       }
       if (!ok || !(ok = W.wait(p_done(nt - 1u), turn(nt - 1u)))) break;
@@ -1296,15 +1314,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // own unit, weighted by 2^(m_i - M).  A tile at cost c belongs to pair
 // c / chunk, so a unit's slots are those of the pairs of its first tile to its
 // last.  Each lane takes one slot's m and l; then every partial result is read
-// once, kJoin of them in flight.
+// once, kJoin of them in flight.  1024 rows of 512: 8.7 us, latency (lookups, m
+// and l, partial results); 25600 rows, 190 MB: 24 us.
 constexpr int kJoinBlocks = 8;  // of 128 threads on an SM
 
 template <int D, int Lanes>
-__global__ void __launch_bounds__(128, D == 16 * Lanes ? 6 : kJoinBlocks) join_kernel(PlanView view, Lens L,
-                                                      __nv_bfloat16* __restrict__ o,
-                                                      float* __restrict__ lse, int B,
-                                                      int64_t n_rows, int64_t n_slots,
-                                                      uint32_t* status) {
+__global__ void __launch_bounds__(128, D == 16 * Lanes ? 6 : kJoinBlocks)
+    join_kernel(PlanView view, Lens L, __nv_bfloat16* __restrict__ o, float* __restrict__ lse,
+                int B, int64_t n_rows, int64_t n_slots, uint32_t* status) {
   constexpr int kPer = 128 / Lanes;      // rows of a block
   constexpr int kVec = D / (4 * Lanes);  // float4 of a thread in a row
   constexpr int kJoin = 8 / kVec;        // partial results in flight
@@ -1438,8 +1455,9 @@ cudaError_t launch_t(const LaunchCtx& c, const ServeShape& s, const CUtensorMap&
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // launched while the main kernel runs, which it waits for on the device
   const int64_t rows = s.T * s.H;
-  // D / 4 threads a row while all rows are on the SMs at once, else a warp each,
-  // which looks a row up once
+  // D / 4 threads a row while all rows are on the SMs at once (1024 rows of 512:
+  // 47.3 us a call against 50.5 with a warp each), else a warp each, which looks a
+  // row up once (25600 rows: 516 us a call against 540)
   const bool wide = rows * (D / 4) <= (int64_t)c.num_sms * kJoinBlocks * 128;
   const int64_t per = wide ? 512 / D : 4;
   cudaLaunchConfig_t cfg = {};
@@ -1451,7 +1469,8 @@ cudaError_t launch_t(const LaunchCtx& c, const ServeShape& s, const CUtensorMap&
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, wide ? join_kernel<D, D / 4> : join_kernel<D, 32>, view, L, o, lse, s.B, rows, slots, c.status);
+  return cudaLaunchKernelEx(&cfg, wide ? join_kernel<D, D / 4> : join_kernel<D, 32>, view, L, o,
+                            lse, s.B, rows, slots, c.status);
 }
 
 }  // namespace

@@ -118,7 +118,8 @@ dsa_status_t dsa_build_page_tables(const dsa_serve_config_t* cfg, const int32_t*
   for (const void* p : ptrs)
     if (!aligned16(p)) return DSA_ERR_MISALIGNED;
   if ((reinterpret_cast<uintptr_t>(free_pages) & 3u) != 0) return DSA_ERR_MISALIGNED;
-  const size_t B = (size_t)cfg->batch, frees = n_free < (int64_t)1 << 40 ? n_free : (int64_t)1 << 40;
+  const size_t B = (size_t)cfg->batch;
+  const size_t frees = n_free < (int64_t)1 << 40 ? n_free : (int64_t)1 << 40;
   const Span reads[] = {{cached_lens, B * 4}, {new_lens, B * 4}, {free_pages, frees * 4}};
   const Span writes[] = {{block_table, B * (size_t)cfg->max_blocks * 4},
                          {slot_map, (size_t)cfg->max_tokens * 4},
