@@ -394,12 +394,7 @@ __device__ __forceinline__ void cluster_arrive() {
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Arrivals at a barrier of either CTA: with a cluster-scope release of this
-// thread's writes, and without.
-__device__ __forceinline__ void mbar_release_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-               : "memory");
-}
+// Arrival at a barrier of either CTA.
 __device__ __forceinline__ void mbar_signal(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
@@ -443,12 +438,15 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void tc_mma2(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                        uint32_t accumulate) {
+// Operands by the low words of their descriptors (the address field, 16 bytes a
+// step, does not carry out of them) and one high word.
+__device__ __forceinline__ void tc_mma2(uint32_t d, uint32_t a, uint32_t b, uint32_t hi,
+                                        uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 // Arrive on the barrier at this offset in both CTAs when the MMAs so far are done.
@@ -913,8 +911,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // ========================================== MMA issuer (leader only)
       // Descriptors: an address 16 bytes on is 1 more.
       uint32_t u = 0, nt = 0;
-      const uint64_t dK = sdesc_sw128(sStage, 16, 1024), dV = sdesc_sw128(sStage, kAtom, 1024);
-      const uint64_t dQ = sdesc_sw128(sQ, 16, 1024), dP = sdesc_sw128(sP, 16, 1024);
+      const uint32_t dK = (uint32_t)sdesc_sw128(sStage, 16, 1024);
+      const uint32_t dV = (uint32_t)sdesc_sw128(sStage, kAtom, 1024);
+      const uint32_t dQ = (uint32_t)sdesc_sw128(sQ, 16, 1024);
+      const uint32_t dP = (uint32_t)sdesc_sw128(sP, 16, 1024);
+      const uint32_t hi = (uint32_t)(sdesc_sw128(0, 16, 1024) >> 32);
+      // a tile's stages one by one in the code where they are many (d = 512: 505 and
+      // 725 us for ragged prompts and 64 requests behind 128k, rolled 517 and 741; at
+      // 256 the drafts' 119.5 became 121.5)
+      constexpr int kUnroll = D == 512 ? 4 : 1;
       // eight MMAs of a stage, let in by the scout: mma(descriptor offset, x)
       auto stage = [&](auto mma) {
         const uint32_t s = u % kStages;
@@ -940,11 +945,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // the softmax has read this S^T buffer's last tile: that tile's PV,
           // which waited for it, is ahead in this order
           const uint32_t b = (nt + (o_on ? 1u : 0u)) & 1u, d = tmem + b * kRows;
-#pragma unroll 1
+#pragma unroll kUnroll
           for (uint32_t c = 0; c < C::kKStages; ++c)
             stage([&](uint32_t at, uint32_t x) {  // 64-dim atom x / 4, 16 dims each
               tc_mma2(d, dK + at + (x >> 2) * (kAtom >> 4) + (x & 3) * 2,
-                      dQ + (2 * c + (x >> 2)) * 512 + (x & 3) * 2, IDESC_S,
+                      dQ + (2 * c + (x >> 2)) * 512 + (x & 3) * 2, hi, IDESC_S,
                       c + x != 0 ? 1u : 0u);
             });
           if (elect_one()) {
@@ -954,12 +959,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           --left;
         }
         if (o_on) {
-          const uint64_t db = dP + (nt & (C::kPBufs - 1)) * (C::kPBytes >> 4);
-#pragma unroll 1
+          const uint32_t db = dP + (nt & (C::kPBufs - 1)) * (C::kPBytes >> 4);
+#pragma unroll kUnroll
           for (uint32_t c = 0; c < C::kVStages; ++c)
             stage([&](uint32_t at, uint32_t x) {  // 16 keys each
               tc_mma2(tO + (c >> 1) * kRows, dV + at + x * 128, db + ((c & 1) * 8 + x) * 128,
-                      IDESC_O, !o_first || (c & 1) + x != 0 ? 1u : 0u);
+                      hi, IDESC_O, !o_first || (c & 1) + x != 0 ? 1u : 0u);
             });
           if (elect_one()) tc_commit2(p_done(nt));
           ++nt;
@@ -1162,28 +1167,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         return any;
       };
-      // P into the CTA that owns the rows; what crosses is counted by its bytes
+      // P into the CTA that owns the rows.  What crosses is counted by its bytes
+      // and goes 64 bytes of a key at a time: four lanes exchange their 16-byte
+      // pieces so that they write one key's (lane by lane, 16 bytes of as many
+      // keys, the same took 729 us instead of 678 for 64 requests behind 128k, 503
+      // instead of 448 for ragged prompts, the exchange aside).
       auto hand_over = [&]() {
         tc_fence_before();  // S^T has been read
         const uint32_t p_to = p_row + (nt & (C::kPBufs - 1)) * C::kPBytes;
-        const uint32_t counts = at_rank(p_in(nt), peer);
-        if (live) {
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const uint32_t a = p_to + (((uint32_t)c ^ p_sw) << 4);
-            const uint32_t w[4] = {pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]};
-            if (owner == rank)
-              asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(w[0]),
-                           "r"(w[1]), "r"(w[2]), "r"(w[3])
-                           : "memory");
-            else
-              st_async_v4(a, w, counts);
-          }
-        }
         if (owner == rank) {
+          if (live) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
+                               p_to + (((uint32_t)c ^ p_sw) << 4)),
+                           "r"(pk[4 * c]), "r"(pk[4 * c + 1]), "r"(pk[4 * c + 2]),
+                           "r"(pk[4 * c + 3])
+                           : "memory");
+          }
           fence_proxy_async();  // P -> the tensor core's reads
           __syncwarp();
           if (lane == 0) mbar_arrive(p_in(nt));
+        } else if (live) {
+          const uint32_t counts = at_rank(p_in(nt), peer);
+          const uint32_t to = p_to - (uint32_t)(lane & 3) * (128 - 16);
+#pragma unroll
+          for (uint32_t h = 0; h < 2; ++h) {
+            uint32_t w[4][4];  // w[x]: piece 4 h + x of the key of lane ^ x
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[x][e] = __shfl_xor_sync(0xffffffffu, pk[4 * (4 * h + x) + e], x);
+            // w[x]: of the group's key x, at place 4 h + (lane & 3) of its line
+#pragma unroll
+            for (int x = 0; x < 4; x += 2)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t a = w[x][e], b = w[x + 1][e];
+                w[x][e] = lane & 1 ? b : a;
+                w[x + 1][e] = lane & 1 ? a : b;
+              }
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t a = w[x][e], b = w[x + 2][e];
+                w[x][e] = lane & 2 ? b : a;
+                w[x + 2][e] = lane & 2 ? a : b;
+              }
+            const uint32_t half = (h << 6) ^ ((uint32_t)(lane & 4) << 4);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) st_async_v4(to + 128 * x + half, w[x], counts);
+          }
         }
       };
       // l and O^T times 2^(m_old - m_new)
