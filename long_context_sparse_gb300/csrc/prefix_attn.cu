@@ -65,10 +65,12 @@ namespace {
 constexpr int kRows = 128;           // rows of a unit
 constexpr int kKeys = 256;           // keys of a tile
 constexpr int kMaxPairs = 80;        // workspace bound on the pairs of a launch
-// A unit's Q load and epilogue, in tiles (us a call of 16 requests of 64 heads
-// behind 16k, ragged drafts, ragged prompts, 64 behind 128k: with 1 51.5, 128, 541,
-// 771; with 2 47.8, 120, 516, 743; with 3 49.6, 120, 522, 737).
-constexpr int kUnitCost = 2;
+// A unit's Q load and epilogue, in tiles: 3, and 2 where shares are short, so
+// that a tile more or less for a pair weighs more than what it stands for (us a
+// call of 64 requests behind 128k keys, shares of 222 tiles: with 1 762, 2 682, 3
+// 656; ragged prompts, 146: 518, 454, 456; drafts, 46: 123, 112, 112; 16 requests
+// of 64 heads behind 16k, 8: 50.4, 43.8, 46.0).
+constexpr int kUnitCost = 3, kShortCost = 2, kShortShare = 32;
 constexpr int kSoftWarps = 8;        // 4 TMEM lane quadrants x 2 groups of rows
 constexpr int kGroupRows = 64;
 constexpr int kProdWarp = 8, kScoutWarp = 9, kMmaWarp = 10, kPassWarp = 11;
@@ -87,6 +89,7 @@ struct Plan {
   int64_t chunk;        // cost of a pair's share
   int64_t prefix_cost;  // of the prefix units, which come first
   int32_t prefix_tiles;
+  int32_t unit_cost;
 };
 // ccum[b], ucum[b]: cost and unit number of request b's first unit (b = 0..B)
 
@@ -154,10 +157,10 @@ __device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
 
 // Tiles [a, z) of a unit of `tiles` tiles that starts at cost c0, for the
 // pair whose share is [s, e).
-__device__ __forceinline__ void share_of(int64_t c0, int32_t tiles, int64_t s, int64_t e,
-                                         int32_t& a, int32_t& z) {
-  const int64_t lo = s - c0 - kUnitCost;
-  const int64_t hi = min(e - c0, (int64_t)tiles + kUnitCost) - kUnitCost;
+__device__ __forceinline__ void share_of(int64_t c0, int32_t tiles, int32_t unit_cost,
+                                         int64_t s, int64_t e, int32_t& a, int32_t& z) {
+  const int64_t lo = s - c0 - unit_cost;
+  const int64_t hi = min(e - c0, (int64_t)tiles + unit_cost) - unit_cost;
   a = lo > 0 ? (int32_t)lo : 0;
   z = hi > 0 ? (int32_t)hi : 0;
 }
@@ -187,6 +190,7 @@ struct Share {
   int32_t first_unit;    // its first unit
   int32_t prefix_tiles;
   int32_t rows_all;      // rows of all requests
+  int32_t unit_cost;
 };
 
 // The tile of an item's turn j.
@@ -205,6 +209,7 @@ struct Walk {
   // the next item, or one of no tiles
   __device__ __forceinline__ void next(const Lens& L, int B, int32_t prefix_len, Item& it) {
     const int64_t start = sh.start, end = sh.end;
+    const int32_t unit_cost = sh.unit_cost;
     it.n = 0;
     while (it.n <= 0 && pos < end) {
       int64_t c0;
@@ -212,16 +217,16 @@ struct Walk {
       it.rot = 0;
       if (pos < sh.prefix_cost) {
         tiles = sh.prefix_tiles;
-        const int32_t u = (int32_t)quotient(pos, tiles + kUnitCost);
-        c0 = (int64_t)u * (tiles + kUnitCost);
+        const int32_t u = (int32_t)quotient(pos, tiles + unit_cost);
+        c0 = (int64_t)u * (tiles + unit_cost);
         it.unit = u;
         it.row0 = it.rel0 = u * kRows;
         it.n_rows = min(kRows, sh.rows_all - it.row0);
         it.len = it.lim_min = prefix_len;
         it.b = -1;
-        share_of(c0, tiles, start, end, it.tile0, last);
-        const int64_t turn = min(end - start, (int64_t)tiles + kUnitCost);
-        const int64_t ahead = c0 + kUnitCost - start;
+        share_of(c0, tiles, unit_cost, start, end, it.tile0, last);
+        const int64_t turn = min(end - start, (int64_t)tiles + unit_cost);
+        const int64_t ahead = c0 + unit_cost - start;
         const int64_t x = ahead < 0 ? -ahead : ahead, y = x - quotient(x, turn) * turn;
         it.rot = (int32_t)(ahead < 0 && y ? turn - y : y);
         if (it.rot >= last - it.tile0) it.rot = 0;
@@ -229,7 +234,7 @@ struct Walk {
         ReqShape r = req_shape(L, b);
         for (;;) {
           const int32_t units = unit_count(r);
-          const int64_t next_cb = cb + (int64_t)units * (r.tiles + kUnitCost);
+          const int64_t next_cb = cb + (int64_t)units * (r.tiles + unit_cost);
           if (pos < next_cb) break;
           cb = next_cb;
           ub += units;
@@ -247,8 +252,8 @@ struct Walk {
           r = req_shape(L, b);
         }
         tiles = r.tiles;
-        const int32_t j = (int32_t)quotient(pos - cb, tiles + kUnitCost);
-        c0 = cb + (int64_t)j * (tiles + kUnitCost);
+        const int32_t j = (int32_t)quotient(pos - cb, tiles + unit_cost);
+        c0 = cb + (int64_t)j * (tiles + unit_cost);
         it.unit = ub + j;
         it.rel0 = j * kRows;
         it.row0 = r.row0 + it.rel0;
@@ -257,10 +262,10 @@ struct Walk {
         it.len = min(r.len, row_limit(r, L.H, it.rel0 + it.n_rows - 1));
         it.lim_min = row_limit(r, L.H, it.rel0);
         it.b = b;
-        share_of(c0, tiles, start, end, it.tile0, last);
+        share_of(c0, tiles, unit_cost, start, end, it.tile0, last);
         last = min(last, (it.len + kKeys - 1) / kKeys);
       }
-      pos = min(end, c0 + tiles + kUnitCost);
+      pos = min(end, c0 + tiles + unit_cost);
       it.n = last - it.tile0;
     }
     if (it.n < 0) it.n = 0;
@@ -289,7 +294,8 @@ __device__ __forceinline__ void divide(const Lens& L, int B, int64_t T, int32_t 
   for (int b = tid; b < B; b += kThreads) {
     const ReqShape r = req_shape(L, b);
     bad |= r.n_new < 0;
-    sum += (int64_t)unit_count(r) * (r.tiles + kUnitCost);
+    const int64_t units = unit_count(r);
+    sum += units * r.tiles + (units << 40);  // tiles (below 2^39), units
     if (out) {
       const int32_t n = __ldg(L.seq + b);
       if (n < 0 || n > L.cap) latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
@@ -300,11 +306,15 @@ __device__ __forceinline__ void divide(const Lens& L, int B, int64_t T, int32_t 
   bad = __syncthreads_or(bad);
   const int32_t ptiles = (prefix_len + kKeys - 1) / kKeys;
   const int32_t np = ptiles ? (int32_t)(((int64_t)last * L.H + kRows - 1) / kRows) : 0;
-  const int64_t prefix_cost = (int64_t)np * (ptiles + kUnitCost);
-  int64_t total = prefix_cost;
+  int64_t total = (int64_t)np * ptiles + ((int64_t)np << 40);
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) total += scratch[w];
   if (bad) total = 0;  // offsets that do not ascend within [0, T]: nothing is computed
+  const int64_t tiles = total & (((int64_t)1 << 40) - 1), units = total >> 40;
+  const int32_t unit_cost =
+      tiles + kUnitCost * units < (int64_t)kShortShare * pairs ? kShortCost : kUnitCost;
+  total = tiles + unit_cost * units;
+  const int64_t prefix_cost = (int64_t)np * (ptiles + unit_cost);
   const int64_t chunk = total > pairs ? quotient(total + pairs - 1, pairs) : 1;
   const int64_t start = min(total, pair * chunk);
   if (tid == 0) {
@@ -312,12 +322,13 @@ __device__ __forceinline__ void divide(const Lens& L, int B, int64_t T, int32_t 
     share->end = min(total, start + chunk);
     share->prefix_cost = prefix_cost;
     share->prefix_tiles = ptiles;
+    share->unit_cost = unit_cost;
     share->rows_all = last * L.H;
     share->first_b = 0;
     share->first_cost = prefix_cost;
     share->first_unit = np;
     if (out) {
-      *out->p = Plan{total, chunk, prefix_cost, ptiles};
+      *out->p = Plan{total, chunk, prefix_cost, ptiles, unit_cost};
       if (bad) latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
     }
   }
@@ -331,7 +342,7 @@ __device__ __forceinline__ void divide(const Lens& L, int B, int64_t T, int32_t 
     if (b < B) {
       const ReqShape r = req_shape(L, b);
       mu = unit_count(r);
-      mc = (int64_t)mu * (r.tiles + kUnitCost);
+      mc = (int64_t)mu * (r.tiles + unit_cost);
     }
     int64_t ic = mc;
     int32_t iu = mu;
@@ -916,10 +927,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t dQ = (uint32_t)sdesc_sw128(sQ, 16, 1024);
       const uint32_t dP = (uint32_t)sdesc_sw128(sP, 16, 1024);
       const uint32_t hi = (uint32_t)(sdesc_sw128(0, 16, 1024) >> 32);
-      // a tile's stages one by one in the code where they are many (d = 512: 505 and
-      // 725 us for ragged prompts and 64 requests behind 128k, rolled 517 and 741; at
-      // 256 the drafts' 119.5 became 121.5)
-      constexpr int kUnroll = D == 512 ? 4 : 1;
       // eight MMAs of a stage, let in by the scout: mma(descriptor offset, x)
       auto stage = [&](auto mma) {
         const uint32_t s = u % kStages;
@@ -945,7 +952,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // the softmax has read this S^T buffer's last tile: that tile's PV,
           // which waited for it, is ahead in this order
           const uint32_t b = (nt + (o_on ? 1u : 0u)) & 1u, d = tmem + b * kRows;
-#pragma unroll kUnroll
+#pragma unroll 1
           for (uint32_t c = 0; c < C::kKStages; ++c)
             stage([&](uint32_t at, uint32_t x) {  // 64-dim atom x / 4, 16 dims each
               tc_mma2(d, dK + at + (x >> 2) * (kAtom >> 4) + (x & 3) * 2,
@@ -960,7 +967,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (o_on) {
           const uint32_t db = dP + (nt & (C::kPBufs - 1)) * (C::kPBytes >> 4);
-#pragma unroll kUnroll
+#pragma unroll 1
           for (uint32_t c = 0; c < C::kVStages; ++c)
             stage([&](uint32_t at, uint32_t x) {  // 16 keys each
               tc_mma2(tO + (c >> 1) * kRows, dV + at + x * 128, db + ((c & 1) * 8 + x) * 128,
@@ -1397,7 +1404,8 @@ __global__ void __launch_bounds__(128, D == 16 * Lanes ? 6 : kJoinBlocks)
           : tiles;
     if (plan.total == 0 || used == 0) continue;
     const int32_t u = x ? block : (int32_t)(row / kRows);
-    const int64_t c = (x ? cost : 0) + (int64_t)u * (tiles + kUnitCost) + kUnitCost;
+    const int64_t c =
+        (x ? cost : 0) + (int64_t)u * (tiles + plan.unit_cost) + plan.unit_cost;
     const int32_t first = (int32_t)quotient(c, plan.chunk);
     n[x] = (int32_t)(quotient(c + used - 1, plan.chunk) - first) + 1;
     s[x] = (x ? first_unit : 0) + u + first;
