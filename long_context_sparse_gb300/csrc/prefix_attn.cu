@@ -45,14 +45,17 @@
 // sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
 //
 // Bounds.  Many rows (64 requests of 64 heads of 512 behind 128k keys, 1107
-// GFLOP): 784 us, 1412 TFLOP/s, 73% of the measured bf16 peak; a stage of the
-// ring takes about 740 cycles of which its products need 512: the loads' way
-// from L2 (about 1500 cycles under load, four stages on the way) and the
-// hand-over between the warps; the softmax warps' arithmetic is 3%.  Two stages
-// more would need the shared memory that Q takes.  Few rows behind 1M keys (8
-// requests of 16 heads): 248 us for 1.08 GB, 4.4 TB/s.  Small calls: 15 us on the
-// GPU, a chain of lookups, loads and hand-overs; each item takes about 10 us from
-// its first tile's loads to its results, overlapped with the next one's loads.
+// GFLOP): 722 us, 1534 TFLOP/s, 80% of the measured bf16 peak and 89% of the rate
+// that the power limit sustains.  A tile of 256 keys takes about 4950 cycles, of
+// which its products need 4096; the rest is the loads' way into the ring (issue
+// to arrival under load about 1500 cycles, four stages of 32 KB on the way) and
+// shared memory, which a stage writes once and reads one and a half times in its
+// 512 cycles of products.  Two stages more would need the shared memory that Q
+// takes; stages of half the size took 806 us where these took 686.  Few rows
+// behind 1M keys (8 requests of 16 heads): 245 us for 1.08 GB, 4.4 TB/s, the same
+// ring with loads from HBM.  d = 256 (ragged drafts): 109 us, 998 TFLOP/s: half the
+// products a tile for the same softmax.  Small calls: 15 us on the GPU, a chain of
+// lookups, loads and hand-overs; each further item of a pair about 10 us.
 #include <atomic>
 #include <type_traits>
 
@@ -1358,7 +1361,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // c / chunk, so a unit's slots are those of the pairs of its first tile to its
 // last.  Each lane takes one slot's m and l; then every partial result is read
 // once, kJoin of them in flight.  1024 rows of 512: 8.7 us, latency (lookups, m
-// and l, partial results); 25600 rows, 190 MB: 24 us.
+// and l, partial results); 25600 rows, 190 MB: 23 us.
 constexpr int kJoinBlocks = 8;  // of 128 threads on an SM
 
 template <int D, int Lanes>
