@@ -595,6 +595,52 @@ def test_attn_idle_requests_between(live):
 
 
 @gpu
+@pytest.mark.parametrize("B,new,H,prefix", [(3, 2720, 128, 300), (65536, 1, 16, 40),
+                                            (65536, 0, 16, 40)])
+def test_attn_largest_row_counts(B, new, H, prefix):
+    """Up to 2^20 rows and 65536 requests (one in seven idle, or all but two);
+    64 rows are compared."""
+    d, page = 128, 16
+    r = np.random.default_rng(B + new)
+    news = np.where(np.arange(B) % 7 == 3, 0, new) if B > 3 else np.full(B, new)
+    if new == 0:
+        news[[5, B - 1]] = [3, 1000]
+    seqs = news + r.integers(0, 20, B)
+    cu = np.concatenate([[0], np.cumsum(news)])
+    own = -(-seqs // page)
+    width, n_pre = int(own.max()), -(-prefix // page)
+    n_pages = n_pre + int(own.sum())
+    table = np.full((B, width), -1, dtype=np.int32)
+    table[np.arange(width)[None] < own[:, None]] = n_pre + np.arange(int(own.sum()))
+    T = (1 << 20) // H
+    g = torch.Generator(device=DEV).manual_seed(B + new)
+    rand = lambda *n: torch.randn(n, generator=g, device=DEV, dtype=BF)
+    q, k, v = 2 * rand(T, H, d), rand(n_pages, page, d), rand(n_pages, page, d)
+    cfg = dsa.ServeConfig(n_pages=n_pages, max_tokens=T, batch=B, max_blocks=width,
+                          page_size=page, attn_heads=H, d_qk=d, d_v=d)
+    i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device=DEV)
+    ws = dsa.serve_workspace(cfg, dsa.SERVE_WS_PREFIX)
+    o, lse = dsa.prefix_attn(cfg, q, k, i32(np.arange(n_pre)), prefix, i32(table), i32(seqs),
+                             i32(cu), v_pages=v, ws=ws)
+    assert dsa.get_device_status(ws) == 0
+    n = int(cu[-1])
+    for t in sorted({0, n - 1, *r.integers(0, n, 62).tolist()}):
+        b = int(np.searchsorted(cu, t, side="right")) - 1
+        keys = int(seqs[b] - news[b] + t - cu[b] + 1)
+        rows = lambda x: torch.cat([
+            x[:n_pre].reshape(-1, d)[:prefix],
+            x[i32(table[b, : own[b]]).long()].reshape(-1, d)[:keys]]).double().cpu()
+        kk, vv = rows(k), rows(v)
+        sc = q[t].double().cpu() @ kk.T * cfg.scale
+        p = torch.softmax(sc, -1)
+        ref, mag = p @ vv, p @ vv.abs()
+        err = (o[t].double().cpu() - ref).abs()
+        assert (err <= P_TOL * mag + O_TOL * ref.abs()).all(), (t, b)
+        assert (lse[t].double().cpu() - torch.logsumexp(sc, -1)).abs().max() <= LSE_TOL
+    assert not o[n:].any() and not lse[n:].any()
+
+
+@gpu
 def test_attn_padding_rows_may_hold_anything():
     c = Case([2, 1], [70, 5], 300, 16, 512, 64, 1, pad=9, seed=12)
     c.q[3:] = math.nan
