@@ -45,16 +45,16 @@
 // sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
 //
 // Bounds.  Many rows (64 requests of 64 heads of 512 behind 128k keys, 1107
-// GFLOP): 722 us, 1534 TFLOP/s, 80% of the measured bf16 peak and 89% of the rate
+// GFLOP): 713 us, 1553 TFLOP/s, 81% of the measured bf16 peak and 90% of the rate
 // that the power limit sustains.  A tile of 256 keys takes about 4950 cycles, of
 // which its products need 4096; the rest is the loads' way into the ring (issue
 // to arrival under load about 1500 cycles, four stages of 32 KB on the way) and
 // shared memory, which a stage writes once and reads one and a half times in its
 // 512 cycles of products.  Two stages more would need the shared memory that Q
 // takes; stages of half the size took 806 us where these took 686.  Few rows
-// behind 1M keys (8 requests of 16 heads): 245 us for 1.08 GB, 4.4 TB/s, the same
-// ring with loads from HBM.  d = 256 (ragged drafts): 109 us, 998 TFLOP/s: half the
-// products a tile for the same softmax.  Small calls: 15 us on the GPU, a chain of
+// behind 1M keys (8 requests of 16 heads): 241 us for 1.08 GB, 4.5 TB/s, the same
+// ring with loads from HBM.  d = 256 (ragged drafts): 106 us, 1028 TFLOP/s: half the
+// products a tile for the same softmax.  Small calls: 14 us on the GPU, a chain of
 // lookups, loads and hand-overs; each further item of a pair about 10 us.
 #include <atomic>
 #include <type_traits>
@@ -618,7 +618,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   using C = PCfg<D>;
   constexpr uint32_t IDESC_S = idesc_bf16(256, 128, 0, 0);
   constexpr uint32_t IDESC_O = idesc_bf16(256, 128, 1, 1);
-  asm volatile("griddepcontrol.launch_dependents;");  // the joining kernel waits for the end
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -704,6 +703,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncwarp();
   cluster_arrive();
+  // the stream's work before; then the joining kernel may start, which reads the
+  // lengths before it waits for this kernel's end
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t pair = blockIdx.x >> 1;
   divide(L, B, T, prefix_len, pair, gridDim.x >> 1, blockIdx.x == 0 ? &view : nullptr, status,
          share, reinterpret_cast<int64_t*>(red));
@@ -1371,6 +1374,7 @@ __global__ void __launch_bounds__(128, D == 16 * Lanes ? 6 : kJoinBlocks)
   constexpr int kPer = 128 / Lanes;      // rows of a block
   constexpr int kVec = D / (4 * Lanes);  // float4 of a thread in a row
   constexpr int kJoin = 8 / kVec;        // partial results in flight
+  asm volatile("griddepcontrol.launch_dependents;");  // a next call's kernel waits for the end
   const int sub = threadIdx.x / Lanes, th = threadIdx.x % Lanes;
   const int64_t row = blockIdx.x * (int64_t)kPer + sub;
   const int32_t t = (int32_t)row / L.H;  // n_rows <= 2^20
@@ -1496,26 +1500,32 @@ cudaError_t launch_t(const LaunchCtx& c, const ServeShape& s, const CUtensorMap&
   }
   const int pairs = c.num_sms / 2 < kMaxPairs ? c.num_sms / 2 : kMaxPairs;
   const int64_t slots = max_slots(s);
-  prefix_attn_kernel<D><<<2 * pairs, kThreads, C::kSmem, c.stream>>>(
-      qm, km, vm[0], vm[1], vm[2], view, L, prefix_table, prefix_len, table, s.B, s.T, s.max_blocks,
-      s.page_log2, (int32_t)s.n_pages, slots, s.scale * kLog2e, c.status, c.timeout_ns);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  // launched while the main kernel runs, which it waits for on the device
+  // Both kernels are launched while what is before them in the stream runs, and
+  // wait for its end on the device (one request behind 1021 keys, call after call:
+  // 14.8 us, with the first launched behind it 17.4).
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * pairs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = c.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, prefix_attn_kernel<D>, qm, km, vm[0], vm[1], vm[2], view, L,
+                         prefix_table, prefix_len, table, s.B, s.T, s.max_blocks, s.page_log2,
+                         (int32_t)s.n_pages, slots, s.scale * kLog2e, c.status, c.timeout_ns);
+  if (e != cudaSuccess) return e;
   const int64_t rows = s.T * s.H;
   // D / 4 threads a row while all rows are on the SMs at once (1024 rows of 512:
   // 47.3 us a call against 50.5 with a warp each), else a warp each, which looks a
   // row up once (25600 rows: 516 us a call against 540)
   const bool wide = rows * (D / 4) <= (int64_t)c.num_sms * kJoinBlocks * 128;
   const int64_t per = wide ? 512 / D : 4;
-  cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((rows + per - 1) / per));
   cfg.blockDim = dim3(128);
-  cfg.stream = c.stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, wide ? join_kernel<D, D / 4> : join_kernel<D, 32>, view, L, o,
                             lse, s.B, rows, slots, c.status);
 }

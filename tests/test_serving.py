@@ -641,6 +641,76 @@ def test_attn_largest_row_counts(B, new, H, prefix):
 
 
 @gpu
+@pytest.mark.parametrize("captured", [False, True])
+def test_attn_sees_what_the_stream_wrote_before(captured):
+    """Lengths, tables and rows that a copy, a fill, a kernel or another stream
+    writes right before the call, which is launched early, and outputs that
+    are read and inputs that are overwritten right behind it."""
+    cases = [Case([1, 2], [40, 300], 500, 16, 512, 64, 1, seed=8),
+             Case([2, 1], [7, 900], 500, 16, 512, 64, 1, seed=9)]
+    size = max(c.table.numel() for c in cases), max(c.cfg.n_pages for c in cases)
+    for c in cases:
+        c.cfg = dataclasses.replace(c.cfg, max_blocks=15, n_pages=size[1])
+        c.table = torch.nn.functional.pad(c.table, (0, 15 - c.table.shape[1]), value=-1)
+        c.k = torch.cat([c.k, c.k[:1].expand(size[1] - c.k.shape[0], -1, -1)])
+    cfg = cases[0].cfg
+    refs = [c.plain() for c in cases]
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    src = [(i32(c.seq), i32(c.cu), c.table.to(DEV), c.prefix_table.to(DEV), c.q.to(DEV),
+            c.k.to(DEV)) for c in cases]
+    seq, cu, table, ptable, q, k = (torch.zeros_like(t) for t in src[0])
+    outs = [(torch.zeros(3, 16, 512, dtype=BF, device=DEV), torch.zeros(3, 16, device=DEV))
+            for _ in cases]
+    o, lse = torch.zeros_like(outs[0][0]), torch.zeros_like(outs[0][1])
+    ws = dsa.serve_workspace(cfg, dsa.SERVE_WS_PREFIX)
+    side = torch.cuda.Stream()
+
+    def call():
+        dsa.prefix_attn(cfg, q, k, ptable, 500, table, seq, cu, o=o, lse=lse, ws=ws)
+
+    def step(i, last):
+        s, c, t, p, x, y = src[i]
+        for dst, new in ((k, y), (q, x), (table, t), (ptable, p), (seq, s), (cu, c)):
+            if dst is not last:
+                dst.copy_(new)
+        here = torch.cuda.current_stream()
+        if last is seq:          # from another stream
+            side.wait_stream(here)
+            with torch.cuda.stream(side):
+                seq.copy_(s)
+            here.wait_stream(side)
+        elif last is cu:         # by a kernel
+            torch.add(c, 0, out=cu)
+        else:
+            last.copy_(dict(q=x, k=y)["q" if last is q else "k"])
+        call()
+        outs[i][0].copy_(o)
+        outs[i][1].copy_(lse)
+        seq.fill_(-7)            # behind it: nothing of the call may see this
+        cu.zero_()
+
+    for last in (seq, cu, q, k):
+        for out in outs:
+            out[0].zero_(), out[1].zero_()
+        if captured:
+            step(0, last)
+            torch.cuda.synchronize()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                step(0, last)
+                step(1, last)
+            for _ in range(20):
+                g.replay()
+        else:
+            for _ in range(20):
+                step(0, last)
+                step(1, last)
+        assert dsa.get_device_status(ws) == 0
+        for out, ref in zip(outs, refs):
+            check((out[0].cpu(), out[1].cpu()), ref)
+
+
+@gpu
 def test_attn_padding_rows_may_hold_anything():
     c = Case([2, 1], [70, 5], 300, 16, 512, 64, 1, pad=9, seed=12)
     c.q[3:] = math.nan
