@@ -642,6 +642,51 @@ def test_attn_largest_row_counts(B, new, H, prefix):
 
 @gpu
 @pytest.mark.parametrize("captured", [False, True])
+def test_append_sees_what_the_stream_wrote_before(captured):
+    """Slots and rows that a kernel or a copy writes right before the call,
+    which is launched early, and that are overwritten right behind it."""
+    T, d, n_pages = 1023, 256, 80
+    cfg = dsa.ServeConfig(n_pages=n_pages, max_tokens=T, batch=1, max_blocks=1, page_size=16,
+                          d_qk=d, d_v=d)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    ws = dsa.serve_workspace(cfg, dsa.SERVE_WS_APPEND)
+    slots = torch.full((T,), -1, dtype=torch.int32, device=DEV)
+    rows = torch.zeros((T, d), dtype=BF, device=DEV)
+    pages = [torch.zeros((n_pages, 16, d), dtype=BF, device=DEV) for _ in range(4)]
+    where = [torch.randperm(n_pages * 16, generator=g, device=DEV)[:T].to(torch.int32)
+             for _ in pages]
+    what = [torch.randn((T, d), generator=g, device=DEV).to(BF) for _ in pages]
+
+    def steps():
+        for i, p in enumerate(pages):
+            rows.copy_(what[i])
+            torch.add(where[i], 0, out=slots)
+            dsa.append_cache(cfg, slots, rows, p, ws=ws)
+            slots.fill_(-1)
+            rows.zero_()
+
+    steps()
+    torch.cuda.synchronize()
+    for p in pages:
+        p.zero_()
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            steps()
+        for _ in range(10):
+            graph.replay()
+    else:
+        for _ in range(10):
+            steps()
+    for p, s, x in zip(pages, where, what):
+        ref = torch.zeros_like(p).view(-1, d)
+        ref[s.long()] = x
+        assert torch.equal(p.view(-1, d), ref)
+    assert dsa.get_device_status(ws) == 0
+
+
+@gpu
+@pytest.mark.parametrize("captured", [False, True])
 def test_attn_sees_what_the_stream_wrote_before(captured):
     """Lengths, tables and rows that a copy, a fill, a kernel or another stream
     writes right before the call, which is launched early, and outputs that
