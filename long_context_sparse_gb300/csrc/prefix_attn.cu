@@ -19,12 +19,17 @@
 // columns) and O^T (128 columns per 256 dv): all 512 at d = 512.
 //
 // Softmax.  A thread owns one key (a TMEM lane) and 64 rows:
-//   P = 2^(s - m),  l += P,  O^T += V^T P^T      (O, l, m in fp32, P in bf16:
-//   the tensor core's operand type, one rounding of each weight).
+//   P = 2^((s - m) c),  l += P,  O^T += V^T P^T   (O, l, m in fp32, P in bf16:
+//   the tensor core's operand type, one rounding of each weight;
+//   c = scale log2 e).
 // m of a row is a reference near its maximum, shared by the pair: the maximum
-// over 32 keys of the first tile, afterwards raised only when a weight would
-// pass 2^20.  (Any reference gives the same result as long as nothing
-// overflows: the weights are floating point, and fp32 leaves 2^107 above.)
+// over 32 keys of the first tile, afterwards raised to a tile's maximum, only
+// when a weight would pass 2^20.  (Any reference gives the same result as long
+// as nothing overflows: the weights are floating point, and fp32 leaves 2^107
+// above.)  It is a score as the products leave it, and is taken off before the
+// multiplication by c: the difference of two scores is exact where they are
+// close, whatever their size, where s c - m c in one fused operation would be
+// off by the rounding of m c, which from 2^28 on is more than the slack.
 // So the usual tile has no maxima to exchange.  A warp that meets
 // a larger score raises a flag; the softmax warps of the pair meet once a tile,
 // behind the tensor cores' work on the tile before, and where the flag is up
@@ -42,7 +47,7 @@
 // requests are packed together.  What a pair has of a unit is an item.  Every
 // (unit, pair) that meet leaves O, m and l (fp32, not normalised) in a slot of
 // the workspace, and a second kernel joins each row's slots:
-// sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
+// sum w_i O_i / sum w_i l_i with w_i = 2^((m_i - M) c).
 //
 // Bounds.  Many rows (64 requests of 64 heads of 512 behind 128k keys, 1107
 // GFLOP): 713 us, 1553 TFLOP/s, 81% of the measured bf16 peak and 90% of the rate
@@ -501,9 +506,9 @@ __device__ __forceinline__ uint64_t pair2(float lo, float hi) {
 __device__ __forceinline__ void unpair2(uint64_t v, float& lo, float& hi) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
 }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
@@ -627,8 +632,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t sStage = sP + C::kPBufs * C::kPBytes;
   uint8_t* tail = gb + C::kQBytes + C::kPBufs * C::kPBytes + kStages * kStageBytes;
   float* nm2_s = reinterpret_cast<float*>(tail);          // [item & 1][row] -m
-  float* nmo_s = nm2_s + 2 * kRows;                       // [row] -m before it was last raised
-  uint8_t* lim_s = reinterpret_cast<uint8_t*>(nmo_s + kRows);  // [row] keys past lim_min
+  float* fac_s = nm2_s + 2 * kRows;  // [row] what raising m makes of l and O
+  uint8_t* lim_s = reinterpret_cast<uint8_t*>(fac_s + kRows);  // [row] keys past lim_min
   uint64_t* bars = reinterpret_cast<uint64_t*>(lim_s + kRows);
   // abort, tmem, beyond, issuer's tiles
   uint32_t* misc = reinterpret_cast<uint32_t*>(bars + kBars);
@@ -1063,7 +1068,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tmem_ld16(tmem + b * kRows + lane_base + h0, r);
             tmem_wait_ld_dep(r);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(r[e]) * scale_log2;
+            for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(r[e]);
             if (!whole) {
 #pragma unroll
               for (int e = 0; e < 16; ++e)
@@ -1095,9 +1100,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            x[e] = live && pos < lim_min + lim_s[h0 + e]
-                       ? fmaf(__uint_as_float(r[e]), scale_log2, nm_s[h0 + e])
-                       : -INFINITY;
+            x[e] = live && pos < lim_min + lim_s[h0 + e] ? __uint_as_float(r[e]) : -INFINITY;
           const float t = column_reduce<true>(x, lane);
           const uint32_t at = (uint32_t)(((int)rank * 4 + quad) * kRows + h0 + lane);
           if (lane < 16) {
@@ -1107,12 +1110,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (!pair_sync(true)) return false;
         if (tid < kRows) {
-          float by = red[tid];
+          float top = red[tid];
 #pragma unroll
-          for (int w = 1; w < 8; ++w) by = fmaxf(by, red[w * kRows + tid]);
+          for (int w = 1; w < 8; ++w) top = fmaxf(top, red[w * kRows + tid]);
           const float nm = nm_s[tid];
-          nmo_s[tid] = nm;
-          if (by > kSlack) nm_s[tid] = nm - by;
+          const bool up = (top + nm) * scale_log2 > kSlack;  // as weights() finds it
+          fac_s[tid] = up ? ex2((-nm - top) * scale_log2) : 1.f;
+          if (up) nm_s[tid] = -top;
         }
         return group_sync();
       };
@@ -1145,11 +1149,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           float d[32];
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            unpair2(fma2(pair2(__uint_as_float(r[h][e]), __uint_as_float(r[h][e + 1])), scale2,
-                         c[e / 4].x),
+            unpair2(mul2(add2(pair2(__uint_as_float(r[h][e]), __uint_as_float(r[h][e + 1])),
+                              c[e / 4].x),
+                         scale2),
                     d[e], d[e + 1]);
-            unpair2(fma2(pair2(__uint_as_float(r[h][e + 2]), __uint_as_float(r[h][e + 3])),
-                         scale2, c[e / 4].y),
+            unpair2(mul2(add2(pair2(__uint_as_float(r[h][e + 2]), __uint_as_float(r[h][e + 3])),
+                              c[e / 4].y),
+                         scale2),
                     d[e + 2], d[e + 3]);
           }
           if (!Plain && masked) {
@@ -1235,17 +1241,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
       };
-      // l and O^T times 2^(m_old - m_new)
+      // l and O^T times 2^((m_old - m_new) c)
       auto rescale = [&](bool o_too) {
         bool any = false;
 #pragma unroll
         for (int h = 0; h < kGroupRows / 2; ++h) {
-          const float a = nm_s[r0 + 2 * h] - nmo_s[r0 + 2 * h];
-          const float c = nm_s[r0 + 2 * h + 1] - nmo_s[r0 + 2 * h + 1];
-          any |= a != 0.f || c != 0.f;
-          float x, y;
-          unpair2(l[h], x, y);
-          l[h] = pair2(x * ex2(a), y * ex2(c));
+          const float a = fac_s[r0 + 2 * h], c = fac_s[r0 + 2 * h + 1];
+          any |= a != 1.f || c != 1.f;
+          l[h] = mul2(l[h], pair2(a, c));
         }
         if (!any || !live || !o_too) return;  // the same in every lane
 #pragma unroll 1
@@ -1257,7 +1260,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tmem_wait_ld_dep(r);
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            r[e] = __float_as_uint(__uint_as_float(r[e]) * ex2(nm_s[h0 + e] - nmo_s[h0 + e]));
+            r[e] = __float_as_uint(__uint_as_float(r[e]) * fac_s[h0 + e]);
           tmem_st16(ta, r);
         }
         tmem_wait_st();
@@ -1360,7 +1363,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------- joining
 // Row by row, Lanes threads each: the slots of the row's prefix unit and of its
-// own unit, weighted by 2^(m_i - M).  A tile at cost c belongs to pair
+// own unit, weighted by 2^((m_i - M) c).  A tile at cost c belongs to pair
 // c / chunk, so a unit's slots are those of the pairs of its first tile to its
 // last.  Each lane takes one slot's m and l; then every partial result is read
 // once, kJoin of them in flight.  1024 rows of 512: 8.7 us, latency (lookups, m
@@ -1370,7 +1373,7 @@ constexpr int kJoinBlocks = 8;  // of 128 threads on an SM
 template <int D, int Lanes>
 __global__ void __launch_bounds__(128, D == 16 * Lanes ? 6 : kJoinBlocks)
     join_kernel(PlanView view, Lens L, __nv_bfloat16* __restrict__ o, float* __restrict__ lse,
-                int B, int64_t n_rows, int64_t n_slots, uint32_t* status) {
+                int B, int64_t n_rows, int64_t n_slots, float scale, uint32_t* status) {
   constexpr int kPer = 128 / Lanes;      // rows of a block
   constexpr int kVec = D / (4 * Lanes);  // float4 of a thread in a row
   constexpr int kJoin = 8 / kVec;        // partial results in flight
@@ -1418,6 +1421,7 @@ __global__ void __launch_bounds__(128, D == 16 * Lanes ? 6 : kJoinBlocks)
     s[x] = (x ? first_unit : 0) + u + first;
   }
   const int count = n[0] + n[1];
+  const float scale_log2 = scale * kLog2e;
   float m = -INFINITY, l = 0.f;
   float4 acc[kVec], oi[kJoin][kVec];
 #pragma unroll
@@ -1446,8 +1450,8 @@ __global__ void __launch_bounds__(128, D == 16 * Lanes ? 6 : kJoinBlocks)
     float top = fmaxf(m, mi);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    const float keep = m == -INFINITY ? 0.f : ex2(m - top);
-    const float w = mi == -INFINITY ? 0.f : ex2(mi - top);
+    const float keep = m == -INFINITY ? 0.f : ex2((m - top) * scale_log2);
+    const float w = mi == -INFINITY ? 0.f : ex2((mi - top) * scale_log2);
     li *= w;
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) li += __shfl_xor_sync(0xffffffffu, li, x);
@@ -1479,7 +1483,7 @@ __global__ void __launch_bounds__(128, D == 16 * Lanes ? 6 : kJoinBlocks)
     reinterpret_cast<uint2*>(o + row * D)[v * Lanes + th] =
         make_uint2(pack_bf16(acc[v].x * inv, acc[v].y * inv),
                    pack_bf16(acc[v].z * inv, acc[v].w * inv));
-  if (th == 0) lse[row] = none ? -INFINITY : (m + log2f(l)) * kLn2;
+  if (th == 0) lse[row] = none ? -INFINITY : fmaf(m, scale, log2f(l) * kLn2);
 }
 
 template <int D>
@@ -1527,7 +1531,7 @@ cudaError_t launch_t(const LaunchCtx& c, const ServeShape& s, const CUtensorMap&
   cfg.blockDim = dim3(128);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, wide ? join_kernel<D, D / 4> : join_kernel<D, 32>, view, L, o,
-                            lse, s.B, rows, slots, c.status);
+                            lse, s.B, rows, slots, s.scale, c.status);
 }
 
 }  // namespace
