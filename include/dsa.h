@@ -456,7 +456,8 @@ DSA_API dsa_status_t dsa_append_cache(const dsa_serve_config_t* cfg,
  * among them once dsa_append_cache has run):
  *   O[t,h] = sum_j softmax_j(scale * q[t,h] . k_j) v_j,
  *   LSE[t,h] = log sum_j exp(scale * q[t,h] . k_j)          (natural log).
- * No keys (prefix_len 0 and no own token at or before it): O = 0, LSE = -inf.
+ * No keys (prefix_len 0 and no own token at or before it), or none that
+ * scores above -inf: O = 0, LSE = -inf.
  * Rows t >= cu_tokens[B] (and rows of no request) of o and lse are left as
  * they were.  Rows of a page past its request's length, or past prefix_len,
  * may hold anything, NaN included.

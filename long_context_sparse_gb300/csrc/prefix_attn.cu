@@ -88,6 +88,10 @@ constexpr uint32_t kStageBytes = 2 * kAtom;
 constexpr int kSoftRegs = 216, kServiceRegs = 72;  // of the 168 that each thread starts with
 static_assert(32 * (8 * kSoftRegs + 4 * kServiceRegs) <= kThreads * 168, "register split");
 constexpr float kSlack = 20.0f;      // log2 headroom before a row's reference is raised
+// -m of a row none of whose keys has scored above -inf so far: the least finite
+// score, which any later one is compared with and raises, and under which -inf
+// still has a weight of 0.
+constexpr float kUnset = 3.402823466e38f;
 
 // ------------------------------------------------------------------- plan
 // The division of work: every CTA of the main kernel derives it from the
@@ -1074,7 +1078,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               for (int e = 0; e < 16; ++e)
                 if (pos >= lim_min + lim_s[h0 + e]) x[e] = -INFINITY;
             }
-            const float t = column_reduce<true>(x, lane), ref = t == -INFINITY ? 0.f : -t;
+            const float t = column_reduce<true>(x, lane);
+            const float ref = t == -INFINITY ? kUnset : -t;
             float* to = nm_s + h0 + (lane & 15);
             if (lane < 16) *to = ref;
             else st_async_f32(at_rank(smem_u32(to), 1), ref, at_rank(refs, 1));

@@ -100,3 +100,22 @@ def test_first_keys_far_below_the_rest(low, best, n_low, scale):
     got = c.run()
     assert got[2] == 0
     check_rows(got, plain_on_gpu(c))
+
+
+@gpu
+@pytest.mark.parametrize("d", [128, 512])
+@pytest.mark.parametrize("n_low", [1, 32, 33, 300, 2000])
+@pytest.mark.parametrize("rest", [-1000.0, -200.0, 0.0, 100.0])
+def test_first_keys_at_minus_infinity(rest, n_low, d):
+    """The first keys of the prefix score -inf and the rest far below or above 0.
+    Request 0 of three has nothing else, where the whole prefix scores -inf."""
+    def fill(b, n):
+        x = torch.full((n,), rest)
+        x[:n_low if b < 0 else (n if b == 0 else n // 2)] = -math.inf
+        return x
+
+    c = scored(Case([1, 2, 1], [40, 700, 3], 2000, 16, d, 64, 2, seed=n_low),
+               [1.0, 0.5, 2.0], 1.0, fill)
+    got = c.run()
+    assert got[2] == 0
+    check_rows(got, plain_on_gpu(c))
