@@ -457,7 +457,8 @@ DSA_API dsa_status_t dsa_append_cache(const dsa_serve_config_t* cfg,
  *   O[t,h] = sum_j softmax_j(scale * q[t,h] . k_j) v_j,
  *   LSE[t,h] = log sum_j exp(scale * q[t,h] . k_j)          (natural log).
  * No keys (prefix_len 0 and no own token at or before it), or none that
- * scores above -inf: O = 0, LSE = -inf.
+ * scores above -inf: O = 0, LSE = -inf.  A row that meets a score of NaN or
+ * +inf is NaN in O and LSE; the rows beside it are not touched by it.
  * Rows t >= cu_tokens[B] (and rows of no request) of o and lse are left as
  * they were.  Rows of a page past its request's length, or past prefix_len,
  * may hold anything, NaN included.

@@ -1078,8 +1078,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               for (int e = 0; e < 16; ++e)
                 if (pos >= lim_min + lim_s[h0 + e]) x[e] = -INFINITY;
             }
-            const float t = column_reduce<true>(x, lane);
-            const float ref = t == -INFINITY ? kUnset : -t;
+            // (scores that are not numbers raise no reference: they reach l)
+            const float ref = -fmaxf(column_reduce<true>(x, lane), -kUnset);
             float* to = nm_s + h0 + (lane & 15);
             if (lane < 16) *to = ref;
             else st_async_f32(at_rank(smem_u32(to), 1), ref, at_rank(refs, 1));

@@ -119,3 +119,26 @@ def test_first_keys_at_minus_infinity(rest, n_low, d):
     got = c.run()
     assert got[2] == 0
     check_rows(got, plain_on_gpu(c))
+
+
+@gpu
+@pytest.mark.parametrize("prefix", [0, 100, 300, 2000])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_rows_that_are_not_numbers_stay_so(value, prefix):
+    """A query row of NaN (or with an infinite channel, which makes scores of both
+    signs infinite) is NaN in O and LSE, whatever tiles it meets; the rows beside
+    it are as they would be without."""
+    c = Case([2, 1], [300, 40], prefix, 16, 512, 64, 1, seed=prefix)
+    ref = c.plain()
+    bad = [(0, 0), (0, 15), (1, 3), (2, 7)]
+    for t, h in bad:
+        if math.isnan(value):
+            c.q[t, h] = value
+        else:
+            c.q[t, h, 5] = value
+    o, lse, st = c.run()
+    assert st == 0
+    for t, h in bad:
+        assert torch.isnan(o[t, h]).all() and torch.isnan(lse[t, h]), (t, h)
+        o[t, h], lse[t, h] = ref[0][t, h].to(BF), ref[1][t, h].float()
+    check_rows((o, lse), ref)
