@@ -466,7 +466,9 @@ DSA_API dsa_status_t dsa_append_cache(const dsa_serve_config_t* cfg,
  * prefix_table [ceil(prefix_len / page_size)] int32 (NULL when prefix_len is
  * 0), 0 <= prefix_len < 2^30; block_table [B, max_blocks], seq_lens [B],
  * cu_tokens [B+1] int32 -> o [T, H, d_v] bf16, lse [T, H] fp32.
- * T * H <= 2^20, else DSA_ERR_UNSUPPORTED_SHAPE.
+ * T * H <= 2^20, else DSA_ERR_UNSUPPORTED_SHAPE.  o, lse and the workspace must
+ * not overlap what the call reads, or one another (DSA_ERR_INVALID_ARG), but
+ * o and lse may lie over q: they are written once all of it has been read.
  * Device-side errors (latched as DSA_ERR_DEVICE_BAD_INDEX; nothing is read or
  * written out of bounds, the affected requests' results are unspecified):
  * a page id outside the cache in a place that is read, a length below 0 or

@@ -68,7 +68,7 @@ struct Span {
 
 bool overlap(const Span& a, const Span& b) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
-  return x && y && (x <= y ? y - x < a.bytes : x - y < b.bytes);
+  return x && y && a.bytes && b.bytes && (x <= y ? y - x < a.bytes : x - y < b.bytes);
 }
 
 // Whether what a call writes meets what it reads, or itself: its blocks read
@@ -176,6 +176,20 @@ dsa_status_t dsa_prefix_attn(const dsa_serve_config_t* cfg, const void* q,
                         seq_lens, cu_tokens, o, lse};
   for (const void* p : ptrs)
     if (!aligned16(p)) return DSA_ERR_MISALIGNED;
+  const size_t B = (size_t)cfg->batch, page = (size_t)cfg->page_size;
+  const size_t rows = (size_t)cfg->max_tokens * cfg->attn_heads, row = (size_t)cfg->d_qk * 2;
+  const size_t cache = (size_t)cfg->n_pages * page * row;
+  // o and lse are written by the joining kernel, which reads the lengths and the
+  // workspace but not q
+  const Span reads[] = {{k_pages, cache},
+                        {v_pages, cache},
+                        {prefix_table, ((size_t)prefix_len + page - 1) / page * 4},
+                        {block_table, B * (size_t)cfg->max_blocks * 4},
+                        {seq_lens, B * 4},
+                        {cu_tokens, (B + 1) * 4}};
+  const Span work = {ws, serve_ws_bytes(cfg, DSA_SERVE_WS_PREFIX)};
+  const Span writes[] = {{o, rows * row}, {lse, rows * 4}, work};
+  if (written_meets(writes, reads) || overlap(work, {q, rows * row})) return DSA_ERR_INVALID_ARG;
   LaunchCtx ctx;
   if ((st = make_ctx(ws, stream, &ctx)) != DSA_OK) return st;
   const ServeShape sh = serve_shape(cfg);

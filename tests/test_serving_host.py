@@ -1,0 +1,64 @@
+"""What the serving calls refuse and what they allow, and the workspaces that
+they ask for."""
+import ctypes
+
+import pytest
+import torch
+
+import long_context_sparse_gb300 as dsa
+from long_context_sparse_gb300 import build as dsa_build
+from tests.test_serving import DEV, Case
+
+P = ctypes.c_void_p
+
+
+@pytest.fixture(scope="module")
+def lib():
+    dsa_build.build()
+    return dsa._load()
+
+
+def test_attention_refuses_what_overlaps(lib):
+    """o, lse and the workspace may not meet what the call reads, or one
+    another; q is the exception for o and lse, which are written behind it."""
+    T, H, B, d, page = 8, 16, 4, 128, 64
+    c = dsa.ServeConfig(n_pages=100, max_tokens=T, batch=B, max_blocks=10, page_size=page,
+                        attn_heads=H, d_qk=d, d_v=d)
+    r = ctypes.byref(c.c())
+    nb = dsa.serve_workspace_size(c, dsa.SERVE_WS_PREFIX)
+    size = dict(q=T * H * d * 2, k=100 * page * d * 2, v=100 * page * d * 2, prefix=16,
+                table=B * 40, seq=B * 4, cu=B * 4 + 4, o=T * H * d * 2, lse=T * H * 4, ws=nb)
+    at = {n: (i + 1) << 28 for i, n in enumerate(size)}
+    assert max(size.values()) < 1 << 28
+
+    def call(prefix_len=200, **over):
+        a = {**at, **over}
+        q, k, v, pt, table, seq, cu, o, lse, ws = (P(x) for x in a.values())
+        return lib.dsa_prefix_attn(r, q, k, v, pt, prefix_len, table, seq, cu, o, lse, ws, nb,
+                                   None)
+
+    for w in ("o", "lse", "ws"):
+        step = 256 if w == "ws" else 16
+        for x in size:
+            if x == w or (x == "q" and w != "ws"):
+                continue
+            assert call(**{w: at[x]}) == 1, (w, x)                                 # the same place
+            assert call(**{w: at[x] + (size[x] - 1) // step * step}) == 1, (w, x)  # its end
+            assert call(**{x: at[w] + (size[w] - 1) // 256 * 256}) == 1, (w, x)
+
+
+@pytest.mark.gpu
+def test_outputs_over_the_queries_and_an_empty_prefix_table():
+    """o in q's place; and, behind no prefix, a prefix table that lies anywhere (it
+    is not read)."""
+    for prefix in (0, 700):
+        c = Case([1, 3, 20], [40, 300, 20], prefix, 16, 256, 64, 1, seed=prefix)
+        ref = c.run()
+        i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)
+        q, lse = c.q.to(DEV), torch.zeros(ref[1].shape, device=DEV)
+        ws = dsa.serve_workspace(c.cfg, dsa.SERVE_WS_PREFIX, DEV)
+        table = c.prefix_table.to(DEV) if prefix else lse.view(torch.int32).view(-1)
+        dsa.prefix_attn(c.cfg, q, c.k.to(DEV), table, prefix, c.table.to(DEV), i32(c.seq),
+                        i32(c.cu), o=q, lse=lse, ws=ws)
+        assert dsa.get_device_status(ws) == 0
+        assert torch.equal(q.cpu(), ref[0]) and torch.equal(lse.cpu(), ref[1])
