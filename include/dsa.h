@@ -419,9 +419,10 @@ DSA_API dsa_status_t dsa_serve_workspace_size(const dsa_serve_config_t* cfg, int
  * cached_lens, new_lens, seq_lens [B], cu_tokens [B+1], free_pages [n_free],
  * pages_taken [1], slot_map [T]: int32.  free_pages may point anywhere into
  * a longer list (4-byte alignment suffices), so that the next step can start
- * pages_taken entries further on.  What the call writes must not overlap what
- * it reads, or itself (DSA_ERR_INVALID_ARG): a step whose cached_lens are the
- * last one's seq_lens writes its own to another buffer.
+ * pages_taken entries further on.  What the call writes, the workspace among
+ * it, must not overlap what it reads, or itself (DSA_ERR_INVALID_ARG): a step
+ * whose cached_lens are the last one's seq_lens writes its own to another
+ * buffer.
  * Device-side errors (latched; nothing is written out of bounds): a negative
  * length or cached + new > max_blocks * page_size gives that request no new
  * tokens and length 0 (DSA_ERR_DEVICE_BAD_INDEX); a page id outside the
@@ -440,8 +441,8 @@ DSA_API dsa_status_t dsa_build_page_tables(
  * slot skips its row, one past the cache latches DSA_ERR_DEVICE_BAD_INDEX and
  * skips it.  v_new == NULL and v_pages == NULL: K = V, one tensor.  The slots
  * of one call must be distinct (two rows with one slot leave that slot with
- * an unspecified mix of both).  The caches must not overlap one another or what
- * the call reads (DSA_ERR_INVALID_ARG).
+ * an unspecified mix of both).  The caches and the workspace must not overlap
+ * one another or what the call reads (DSA_ERR_INVALID_ARG).
  * ws: DSA_SERVE_WS_APPEND. */
 DSA_API dsa_status_t dsa_append_cache(const dsa_serve_config_t* cfg,
                                       const int32_t* slot_map, const void* k_new,

@@ -125,7 +125,8 @@ dsa_status_t dsa_build_page_tables(const dsa_serve_config_t* cfg, const int32_t*
                          {slot_map, (size_t)cfg->max_tokens * 4},
                          {cu_tokens, (B + 1) * 4},
                          {seq_lens, B * 4},
-                         {pages_taken, 4}};
+                         {pages_taken, 4},
+                         {ws, kHeader}};
   if (written_meets(writes, reads)) return DSA_ERR_INVALID_ARG;
   LaunchCtx ctx;
   if ((st = make_ctx(ws, stream, &ctx)) != DSA_OK) return st;
@@ -148,7 +149,7 @@ dsa_status_t dsa_append_cache(const dsa_serve_config_t* cfg, const int32_t* slot
   const size_t T = (size_t)cfg->max_tokens, row = (size_t)cfg->d_qk * 2;
   const size_t cache = (size_t)cfg->n_pages * cfg->page_size * row;
   const Span reads[] = {{slot_map, T * 4}, {k_new, T * row}, {v_new, T * row}};
-  const Span writes[] = {{k_pages, cache}, {v_pages, cache}};
+  const Span writes[] = {{k_pages, cache}, {v_pages, cache}, {ws, kHeader}};
   if (written_meets(writes, reads)) return DSA_ERR_INVALID_ARG;
   LaunchCtx ctx;
   if ((st = make_ctx(ws, stream, &ctx)) != DSA_OK) return st;

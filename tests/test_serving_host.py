@@ -47,6 +47,39 @@ def test_attention_refuses_what_overlaps(lib):
             assert call(**{x: at[w] + (size[w] - 1) // 256 * 256}) == 1, (w, x)
 
 
+def test_tables_and_append_refuse_a_workspace_in_their_buffers(lib):
+    """The status word is latched while the kernels read and write: the header may
+    not lie in anything of the call's, and anything may not end in it."""
+    B, T, n_free, width, d, page = 4, 512, 100, 10, 128, 64
+    c = dsa.ServeConfig(n_pages=100, max_tokens=T, batch=B, max_blocks=width, page_size=page,
+                        d_qk=d, d_v=d)
+    r, ws = ctypes.byref(c.c()), 1 << 40
+    size = dict(cached=16, new=16, free=n_free * 4, table=B * width * 4, slots=T * 4, cu=20,
+                seq=16, taken=4)
+    at = {n: (i + 1) << 28 for i, n in enumerate(size)}
+
+    def tables(ws, **over):
+        a = [P(x) for x in {**at, **over}.values()]
+        return lib.dsa_build_page_tables(r, *a[:3], n_free, *a[3:], P(ws), 256, None)
+
+    for x in at:
+        assert tables(at[x]) == 1, x
+        assert tables(at[x] + (size[x] - 1) // 256 * 256) == 1, x
+        assert tables(ws, **{x: ws + 240}) == 1, x
+    cache = 100 * page * d * 2
+    size2 = dict(slots=T * 4, k_new=T * d * 2, v_new=T * d * 2, k=cache, v=cache)
+    at2 = {n: (i + 1) << 28 for i, n in enumerate(size2)}
+
+    def append(ws, **over):
+        a = [P(x) for x in {**at2, **over}.values()]
+        return lib.dsa_append_cache(r, *a, P(ws), 256, None)
+
+    for x in at2:
+        assert append(at2[x]) == 1, x
+        assert append(at2[x] + (size2[x] - 1) // 256 * 256) == 1, x
+        assert append(ws, **{x: ws + 240}) == 1, x
+
+
 @pytest.mark.gpu
 def test_outputs_over_the_queries_and_an_empty_prefix_table():
     """o in q's place; and, behind no prefix, a prefix table that lies anywhere (it
