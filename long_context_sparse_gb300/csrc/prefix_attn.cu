@@ -115,9 +115,11 @@ struct PlanView {
 
 size_t plan_bytes(int B) { return 256 + round_up((size_t)(B + 1) * 12, 256); }
 
+// Units of the prefix, units of the requests that have rows (at most T), and
+// a part more for each pair.
 int64_t max_slots(const ServeShape& s) {
   const int64_t n = (s.T * s.H + kRows - 1) / kRows;
-  return 2 * n + s.B + kMaxPairs;
+  return 2 * n + (s.B < s.T ? s.B : s.T) + kMaxPairs;
 }
 
 PlanView plan_view(const ServeShape& s, uint8_t* work) {

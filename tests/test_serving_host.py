@@ -7,7 +7,7 @@ import torch
 
 import long_context_sparse_gb300 as dsa
 from long_context_sparse_gb300 import build as dsa_build
-from tests.test_serving import DEV, Case
+from tests.test_serving import DEV, Case, check_case
 
 P = ctypes.c_void_p
 
@@ -80,6 +80,19 @@ def test_tables_and_append_refuse_a_workspace_in_their_buffers(lib):
         assert append(ws, **{x: ws + 240}) == 1, x
 
 
+@pytest.mark.parametrize("T,H", [(1, 16), (64, 16), (64, 128), (1000, 64)])
+def test_workspace_of_a_batch_that_is_mostly_idle(lib, T, H):
+    """A request has partial results only with rows of its own, so requests beyond
+    the query tokens add their place in the plan (12 bytes) and no more."""
+    size = lambda B: dsa.serve_workspace_size(
+        dsa.ServeConfig(n_pages=100, max_tokens=T, batch=B, max_blocks=10, attn_heads=H),
+        dsa.SERVE_WS_PREFIX)
+    assert size(65536) - size(T) <= 12 * 65536 + 256
+    # of the rows: two lists of keys a row block, a request each, a part a pair
+    slot = 128 * (4 * 512 + 16)
+    assert size(T) <= 512 + 12 * (T + 1) + 256 + (2 * (-(-T * H // 128)) + T + 80) * slot
+
+
 @pytest.mark.gpu
 def test_outputs_over_the_queries_and_an_empty_prefix_table():
     """o in q's place; and, behind no prefix, a prefix table that lies anywhere (it
@@ -95,3 +108,20 @@ def test_outputs_over_the_queries_and_an_empty_prefix_table():
                         i32(c.cu), o=q, lse=lse, ws=ws)
         assert dsa.get_device_status(ws) == 0
         assert torch.equal(q.cpu(), ref[0]) and torch.equal(lse.cpu(), ref[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,prefix", [(1, 16, 0), (7, 16, 300), (40, 128, 3000)])
+def test_nothing_is_written_past_the_workspace(T, H, prefix):
+    """More requests than query tokens, one token for each of T of them: the most
+    units that T tokens make."""
+    B = 300
+    new = [0] * B
+    for b in range(T):
+        new[7 * b] = 1
+    c = Case(new, [n + b % 90 for b, n in enumerate(new)], prefix, H, 512, 64, 1, seed=T)
+    need = dsa.serve_workspace_size(c.cfg, dsa.SERVE_WS_PREFIX)
+    ws = torch.zeros(need + (1 << 20), dtype=torch.uint8, device=DEV)
+    ws[need:] = 77
+    check_case(c, ws=ws)
+    assert (ws[need:] == 77).all()
