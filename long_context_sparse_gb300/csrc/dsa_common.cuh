@@ -39,6 +39,31 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// ------------------------------------------------------- early launches
+// A kernel that is launched while the one before it in the stream runs waits for
+// its end (griddepcontrol.wait) and reads what that may have written with these.
+// They are not non-coherent loads (__ldg): those are for data that nothing writes
+// while the kernel lives, which here begins before the writer's end, and the
+// compiler may move them ahead of the wait, which it may not do with these.
+// Ahead: for a kernel that has not waited itself, launched by one that has; from
+// the memory that all SMs share, so that no older line of this SM's is read.
+template <bool Ahead = false>
+__device__ __forceinline__ int32_t ld_input(const int32_t* p) {
+  int32_t v;
+  if (Ahead)
+    asm volatile("ld.relaxed.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
+  else
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint4 ld_input(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 // --------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));

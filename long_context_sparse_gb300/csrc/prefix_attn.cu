@@ -148,9 +148,10 @@ struct ReqShape {
   int32_t n_new;   // query tokens
 };
 
+template <bool Ahead = false>
 __device__ __forceinline__ ReqShape req_shape(const Lens& L, int b) {
-  const int32_t c0 = __ldg(L.cu + b), c1 = __ldg(L.cu + b + 1);
-  int32_t len = __ldg(L.seq + b);
+  const int32_t c0 = ld_input<Ahead>(L.cu + b), c1 = ld_input<Ahead>(L.cu + b + 1);
+  int32_t len = ld_input<Ahead>(L.seq + b);
   if (len < 0 || len > L.cap) len = 0;  // latched by CTA 0
   return {c0 * L.H, (c1 - c0) * L.H, len, (len + kKeys - 1) / kKeys, c1 - c0};
 }
@@ -302,7 +303,7 @@ __device__ __forceinline__ void divide(const Lens& L, int B, int64_t T, int32_t 
   constexpr int kWarps = kThreads / 32;
   int32_t* scratch_u = reinterpret_cast<int32_t*>(scratch + kWarps);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int32_t first = __ldg(L.cu), last = __ldg(L.cu + B);
+  const int32_t first = ld_input(L.cu), last = ld_input(L.cu + B);
   int bad = first < 0 || last > T;
   int64_t sum = 0;
   for (int b = tid; b < B; b += kThreads) {
@@ -311,7 +312,7 @@ __device__ __forceinline__ void divide(const Lens& L, int B, int64_t T, int32_t 
     const int64_t units = unit_count(r);
     sum += units * r.tiles + (units << 40);  // tiles (below 2^39), units
     if (out) {
-      const int32_t n = __ldg(L.seq + b);
+      const int32_t n = ld_input(L.seq + b);
       if (n < 0 || n > L.cap) latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
     }
   }
@@ -766,7 +767,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // page of key `half * 128 + key0` of tile j (0 where nothing is read)
       auto page_at = [&](int32_t j, int half) {
         const int32_t pos = j * kKeys + half * 128 + key0;
-        return pos < it.len ? __ldg(pages + (pos >> page_log2)) : 0;
+        return pos < it.len ? ld_input(pages + (pos >> page_log2)) : 0;
       };
       // its first cache row, or out of range past the end
       auto row_of = [&](int32_t j, int half, int32_t p) {
@@ -1388,21 +1389,23 @@ __global__ void __launch_bounds__(128, D == 16 * Lanes ? 6 : kJoinBlocks)
   const int sub = threadIdx.x / Lanes, th = threadIdx.x % Lanes;
   const int64_t row = blockIdx.x * (int64_t)kPer + sub;
   const int32_t t = (int32_t)row / L.H;  // n_rows <= 2^20
-  // the row's request, from the call's inputs: before the main kernel's end
-  const bool mine = row < n_rows && t >= __ldg(L.cu) && t < __ldg(L.cu + B);
+  // the row's request, from the call's inputs: before the main kernel's end (it
+  // let this one start when it had waited for them itself)
   // the last b in [lo, lo + n) with cu[b] <= t, a 32nd at a time (a warp has one row)
   const int lane = threadIdx.x & 31;
   int lo = 0;
-  for (int n = mine ? B : 0; n > 1;) {
+  for (int n = row < n_rows ? B : 0; n > 1;) {
     const int step = (n + 31) >> 5, x = lane * step;
-    const uint32_t le = __ballot_sync(0xffffffffu, x < n && __ldg(L.cu + lo + min(x, n - 1)) <= t);
+    const uint32_t le = __ballot_sync(
+        0xffffffffu, x < n && ld_input<true>(L.cu + lo + min(x, n - 1)) <= t);
     const int at = (31 - __clz(le | 1u)) * step;
     lo += at;
     n = min(step, n - at);
   }
   ReqShape r{};
-  if (mine) r = req_shape(L, lo);
+  if (row < n_rows) r = req_shape<true>(L, lo);
   const int32_t rel = (int32_t)row - r.row0, block = rel / kRows;
+  const bool mine = rel >= 0 && rel < r.n_rows;  // no rows: none past the last either
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the main kernel's results
   if (!mine) return;
   const Plan plan = *view.p;

@@ -189,12 +189,12 @@ __global__ void __launch_bounds__(256) append_kernel(
       const int64_t x = x0 + u * step;
       dst[u] = -1;
       if (x >= n) continue;
-      const int32_t s = __ldg(slots + x / kPieces);
+      const int32_t s = ld_input(slots + x / kPieces);
       if (s >= n_slots) latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
       if (s < 0 || s >= n_slots) continue;
       dst[u] = (int64_t)s * kPieces + x % kPieces;
-      a[u] = __ldg(k_new + x);
-      if (v_new) b[u] = __ldg(v_new + x);
+      a[u] = ld_input(k_new + x);
+      if (v_new) b[u] = ld_input(v_new + x);
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
