@@ -66,6 +66,7 @@
 
 #include "attn_common.cuh"
 #include "dsa_internal.h"
+#include "pair_common.cuh"
 
 namespace dsa {
 namespace {
@@ -403,86 +404,7 @@ __device__ __forceinline__ void divide(const Lens& L, int B, int64_t T, int32_t 
   }
 }
 
-// ---------------------------------------------------- pair (cluster) PTX
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t at_rank(uint32_t saddr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// Arrival at a barrier of either CTA.
-__device__ __forceinline__ void mbar_signal(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-__device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ void fence_cluster() {
-  asm volatile("fence.acq_rel.cluster;" ::: "memory");
-}
-__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-// 16 bytes into either CTA's shared memory; its barrier `bar` counts them.
-__device__ __forceinline__ void st_async_v4(uint32_t addr, const uint32_t (&v)[4],
-                                            uint32_t bar) {
-  asm volatile(
-      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1,%2,%3,%4}, [%5];"
-      ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void st_async_f32(uint32_t addr, float v, uint32_t bar) {
-  asm volatile(
-      "st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr),
-      "r"(__float_as_uint(v)), "r"(bar)
-      : "memory");
-}
-// TMA load into this CTA, its bytes counted by a barrier of either CTA.
-__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, int32_t c0,
-                                              int32_t c1, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
-      : "memory");
-}
-// Operands by the low words of their descriptors (the address field, 16 bytes a
-// step, does not carry out of them) and one high word.
-__device__ __forceinline__ void tc_mma2(uint32_t d, uint32_t a, uint32_t b, uint32_t hi,
-                                        uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
-      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// Arrive on the barrier at this offset in both CTAs when the MMAs so far are done.
-__device__ __forceinline__ void tc_commit2(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-      "[%0], %1;" ::"r"(bar),
-      "h"((uint16_t)3)
-      : "memory");
-}
+// --------------------------------------------------------------- warp PTX
 // One lane of a converged warp, the same one every time.  The compiler knows
 // this branch as one whose operands may stay in uniform registers, which it
 // does not of `lane == 0`: eight MMAs and their commit then issue in 517 cycles
@@ -548,33 +470,6 @@ __device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {
                :
                : "memory");
 }
-
-// Bounded waits of the pair: as Waiter, with cluster scope; a failure stops
-// both CTAs.  wait() is for whole warps and gives every lane the same answer,
-// so that no lane is left behind at a warp's barrier; wait1() is one thread's.
-struct PairWaiter {
-  volatile uint32_t* abort_flag;
-  uint32_t peer_flag;  // cluster address of the other CTA's flag
-  uint32_t* status;
-  uint64_t timeout_ns;
-  __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const {
-    return __all_sync(0xffffffffu, wait1(bar, parity));
-  }
-  __device__ __forceinline__ bool wait1(uint32_t bar, uint32_t parity) const {
-    if (mbar_try_cluster(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (;;) {
-      if (mbar_try_cluster(bar, parity)) return true;
-      if (*abort_flag) return false;
-      if (globaltimer_ns() - t0 > timeout_ns) {
-        latch_error(status, DSA_ERR_DEVICE_TIMEOUT);
-        *abort_flag = 1u;
-        st_cluster_u32(peer_flag, 1u);
-        return false;
-      }
-    }
-  }
-};
 
 // ------------------------------------------------------------ main kernel
 // Shared memory at D = 512: Q 64 KB, P 32 KB, four stages of 32 KB, 2 KB of row
