@@ -271,6 +271,12 @@ __host__ __device__ constexpr uint32_t idesc_bf16(uint32_t M, uint32_t N,
 }
 
 // ------------------------------------------------------------ misc math
+// The sum of x over a warp, in every lane.
+__device__ __forceinline__ int64_t warp_sum(int64_t x) {
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
+  return x;
+}
 __device__ __forceinline__ float bf16_lo(uint32_t x) {
   return __uint_as_float(x << 16);
 }

@@ -288,12 +288,6 @@ struct Walk {
   }
 };
 
-__device__ __forceinline__ int64_t warp_sum64(int64_t x) {
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
-  return x;
-}
-
 // The share of pair `pair` of `pairs`; all threads of the CTA, `scratch` in
 // shared memory.  The requests are summed once for the total and scanned for
 // the one at the share's start (B <= kThreads: one step each).  `out`: CTA 0
@@ -317,7 +311,7 @@ __device__ __forceinline__ void divide(const Lens& L, int B, int64_t T, int32_t 
       if (n < 0 || n > L.cap) latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
     }
   }
-  sum = warp_sum64(sum);
+  sum = warp_sum(sum);
   if (lane == 0) scratch[warp] = sum;
   bad = __syncthreads_or(bad);
   const int32_t ptiles = (prefix_len + kKeys - 1) / kKeys;

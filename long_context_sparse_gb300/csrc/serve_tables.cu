@@ -32,12 +32,6 @@ __device__ __forceinline__ ReqLens req_lens(const int32_t* cached, const int32_t
   return r;
 }
 
-__device__ __forceinline__ int64_t warp_sum(int64_t x) {
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
-  return x;
-}
-
 __global__ void __launch_bounds__(kReq) page_tables_kernel(
     const int32_t* __restrict__ cached, const int32_t* __restrict__ fresh,
     const int32_t* __restrict__ free_pages, int64_t n_free, int32_t* __restrict__ table,
