@@ -462,7 +462,14 @@ DSA_API dsa_status_t dsa_append_cache(const dsa_serve_config_t* cfg,
  * +inf is NaN in O and LSE; the rows beside it are not touched by it.
  * Rows t >= cu_tokens[B] (and rows of no request) of o and lse are left as
  * they were.  Rows of a page past its request's length, or past prefix_len,
- * may hold anything, NaN included.
+ * may hold anything, NaN included.  V (and K, where K = V) of a request's own
+ * tokens has to be finite: a weight of zero does not cancel NaN or infinity, so
+ * such a token makes NaN also of rows of its request that come before it, in
+ * those dims; other requests' rows are not touched by it.
+ * Numbers: scores, row sums and O are fp32; a weight is rounded to bf16 once, as
+ * the second product's operand (the row sum is of the unrounded weights).
+ * Weights stand at most 2^20 above their reference, so sums of O stay finite
+ * while |v| times the number of keys is below 2^107.
  * q [T, H, d_qk] bf16; k_pages, v_pages (NULL: K = V) as above;
  * prefix_table [ceil(prefix_len / page_size)] int32 (NULL when prefix_len is
  * 0), 0 <= prefix_len < 2^30; block_table [B, max_blocks], seq_lens [B],

@@ -956,7 +956,7 @@ def prefix_attn(cfg: ServeConfig, q, k_pages, prefix_table, prefix_len: int,
     the last tokens of request b's seq_lens[b]; a row sees its own place and
     those before it.  Rows of no request are not written (new outputs hold
     zeros there).  Without v_pages: K = V.  prefix_table may be None when
-    prefix_len is 0."""
+    prefix_len is 0.  o may be q itself; other buffers may not overlap."""
     T, H, B, bf, i32 = (cfg.max_tokens, cfg.attn_heads, cfg.batch, torch.bfloat16,
                         torch.int32)
     dev, p_q = _first_tensor(q, "q", bf, (T, H, cfg.d_qk))

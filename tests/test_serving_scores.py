@@ -142,3 +142,19 @@ def test_rows_that_are_not_numbers_stay_so(value, prefix):
         assert torch.isnan(o[t, h]).all() and torch.isnan(lse[t, h]), (t, h)
         o[t, h], lse[t, h] = ref[0][t, h].to(BF), ref[1][t, h].float()
     check_rows((o, lse), ref)
+
+
+@gpu
+@pytest.mark.parametrize("kv", [1, 2])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_a_token_that_is_not_finite_stays_in_its_request(value, kv):
+    """The last own token of the middle request is not finite: its own rows may
+    be anything, the other requests' are as they would be without."""
+    c = Case([2, 3, 2], [300, 40, 70], 500, 16, 256, 32, kv, seed=kv)
+    ref = c.plain()
+    at = rows_of(c, c.v, 1, 40)[-1]
+    c.v.view(-1, 256)[at, ::3] = value
+    o, lse, st = c.run()
+    assert st == 0
+    others = [0, 1, 5, 6]
+    check_rows((o[others], lse[others]), [x[others] for x in ref])
