@@ -370,7 +370,9 @@ DSA_API dsa_status_t dsa_static_device_status(void* stream, uint32_t* device_sta
  * Token Context on GLM-5.3-Flash", "Results": the trainer's log-probs are
  * compared with those of the engine that sampled the tokens).  The calls
  * below are that engine's side for a layer whose queries read every cached
- * key: a cache of pages, its tables, and the attention of a batch of requests
+ * key (the sparse layer's calls above take no page table, and their results
+ * agree with these only while the key budget covers the context): a cache of
+ * pages, its tables, and the attention of a batch of requests
  * over one shared prefix, read once for all of them, and over their own
  * tokens.  The key/value layout is the library's: one NoPE K and one V row
  * per token shared by all heads, or one tensor for both (K = V).

@@ -40,25 +40,32 @@
 // cluster-scope fence (measured: a release.cluster arrival waits about 1500
 // cycles under load, a plain one none): data that crosses is counted by a
 // barrier (TMA, st.async), and what a CTA's own threads wrote to its own
-// shared memory was handed to the relaying thread inside the CTA.
+// shared memory was handed to the relaying thread inside the CTA.  The relay's
+// arrival at the leader so publishes nothing to the leader's threads.  It leans
+// on the reader of that P being the tensor core of the SM that holds it, behind
+// the writers' proxy fences there; the memory model does not spell that out.
 //
 // Work.  Units cost their tiles plus kUnitCost; the pairs share the sum
 // evenly in unit order, so a long prefix is split over all of them and short
-// requests are packed together.  What a pair has of a unit is an item.  Every
+// requests are packed together.  A request's units all cost the tiles of its
+// longest row, also those whose rows see fewer: the charge is even and the work
+// is not where a prompt's own causal blocks are most of it (tiles of the busiest
+// of 76 pairs against the mean: 2048 tokens of 64 heads alone 110 and 61, 4096 of
+// 16 heads behind 4096 keys 217 and 165).  What a pair has of a unit is an item.  Every
 // (unit, pair) that meet leaves O, m and l (fp32, not normalised) in a slot of
 // the workspace, and a second kernel joins each row's slots:
 // sum w_i O_i / sum w_i l_i with w_i = 2^((m_i - M) c).
 //
 // Bounds.  Many rows (64 requests of 64 heads of 512 behind 128k keys, 1107
-// GFLOP): 713 us, 1553 TFLOP/s, 81% of the measured bf16 peak and 90% of the rate
+// GFLOP): 720 us, 1538 TFLOP/s, 80% of the measured bf16 peak and 89% of the rate
 // that the power limit sustains.  A tile of 256 keys takes about 4950 cycles, of
 // which its products need 4096; the rest is the loads' way into the ring (issue
 // to arrival under load about 1500 cycles, four stages of 32 KB on the way) and
 // shared memory, which a stage writes once and reads one and a half times in its
 // 512 cycles of products.  Two stages more would need the shared memory that Q
-// takes; stages of half the size took 806 us where these took 686.  Few rows
-// behind 1M keys (8 requests of 16 heads): 241 us for 1.08 GB, 4.5 TB/s, the same
-// ring with loads from HBM.  d = 256 (ragged drafts): 106 us, 1028 TFLOP/s: half the
+// takes; with stages of half the size the call took 17% longer.  Few rows
+// behind 1M keys (8 requests of 16 heads): 237 us for 1.08 GB, 4.6 TB/s, the same
+// ring with loads from HBM.  d = 256 (ragged drafts): 107 us, 1022 TFLOP/s: half the
 // products a tile for the same softmax.  Small calls: 14 us on the GPU, a chain of
 // lookups, loads and hand-overs; each further item of a pair about 10 us.
 #include <atomic>
@@ -75,10 +82,13 @@ constexpr int kRows = 128;           // rows of a unit
 constexpr int kKeys = 256;           // keys of a tile
 constexpr int kMaxPairs = 80;        // workspace bound on the pairs of a launch
 // A unit's Q load and epilogue, in tiles: 3, and 2 where shares are short, so
-// that a tile more or less for a pair weighs more than what it stands for (us a
-// call of 64 requests behind 128k keys, shares of 222 tiles: with 1 762, 2 682, 3
-// 656; ragged prompts, 146: 518, 454, 456; drafts, 46: 123, 112, 112; 16 requests
-// of 64 heads behind 16k, 8: 50.4, 43.8, 46.0).
+// that a tile more or less for a pair weighs more than what it stands for.  us a
+// call with 1, 2, 3, by the tiles of a share: 64 rows a request, d = 512, 222 (64
+// requests behind 128k keys): 770 707 705; 40: 193 145 145; 32: 160 123 122; 24:
+// 128 98.6 99.8; 20: 110 87.5 91.9; 16: 94.0 78.1 79.7; 12: 77.2 65.8 69.6; 8 (16
+// requests behind 16k): 49.3 42.4 43.7.  Ragged prompts, 146: 527 454 450.  d = 256,
+// 46 (drafts): 126 109 108; 36: 125 93.3 94.5; 28: 101 77.8 78.3; 12: 54.9 45.8
+// 47.0.  The two are alike between 28 and 46, where the line is drawn.
 constexpr int kUnitCost = 3, kShortCost = 2, kShortShare = 32;
 constexpr int kSoftWarps = 8;        // 4 TMEM lane quadrants x 2 groups of rows
 constexpr int kGroupRows = 64;
@@ -1086,8 +1096,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // P into the CTA that owns the rows.  What crosses is counted by its bytes
       // and goes 64 bytes of a key at a time: four lanes exchange their 16-byte
       // pieces so that they write one key's (lane by lane, 16 bytes of as many
-      // keys, the same took 729 us instead of 678 for 64 requests behind 128k, 503
-      // instead of 448 for ragged prompts, the exchange aside).
+      // keys, a call of 64 requests behind 128k took 8% longer and one of ragged
+      // prompts 12%, the exchange aside).
       auto hand_over = [&]() {
         tc_fence_before();  // S^T has been read
         const uint32_t p_to = p_row + (nt & (C::kPBufs - 1)) * C::kPBytes;
@@ -1263,8 +1273,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // own unit, weighted by 2^((m_i - M) c).  A tile at cost c belongs to pair
 // c / chunk, so a unit's slots are those of the pairs of its first tile to its
 // last.  Each lane takes one slot's m and l; then every partial result is read
-// once, kJoin of them in flight.  1024 rows of 512: 8.7 us, latency (lookups, m
-// and l, partial results); 25600 rows, 190 MB: 23 us.
+// once, kJoin of them in flight.  1024 rows of 512: 9.5 us, latency (lookups, m
+// and l, partial results); 25600 rows, 190 MB: 25 us.
 constexpr int kJoinBlocks = 8;  // of 128 threads on an SM
 
 template <int D, int Lanes>
@@ -1405,7 +1415,7 @@ cudaError_t launch_t(const LaunchCtx& c, const ServeShape& s, const CUtensorMap&
   const int64_t slots = max_slots(s);
   // Both kernels are launched while what is before them in the stream runs, and
   // wait for its end on the device (one request behind 1021 keys, call after call:
-  // 14.8 us, with the first launched behind it 17.4).
+  // 15.0 us, and 2.6 more with the first launched behind it).
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1421,9 +1431,9 @@ cudaError_t launch_t(const LaunchCtx& c, const ServeShape& s, const CUtensorMap&
                          (int32_t)s.n_pages, slots, s.scale * kLog2e, c.status, c.timeout_ns);
   if (e != cudaSuccess) return e;
   const int64_t rows = s.T * s.H;
-  // D / 4 threads a row while all rows are on the SMs at once (1024 rows of 512:
-  // 47.3 us a call against 50.5 with a warp each), else a warp each, which looks a
-  // row up once (25600 rows: 516 us a call against 540)
+  // D / 4 threads a row while all rows are on the SMs at once (with a warp each a
+  // call of 1024 rows of 512 took 3 us longer), else a warp each, which looks a row
+  // up once (25600 rows: 24 us less a call)
   const bool wide = rows * (D / 4) <= (int64_t)c.num_sms * kJoinBlocks * 128;
   const int64_t per = wide ? 512 / D : 4;
   cfg.gridDim = dim3((unsigned)((rows + per - 1) / per));

@@ -13,9 +13,11 @@ namespace {
 // them itself (coalesced reads that hit L2; at B = 65536 the last block
 // reads 512 KB), so no block waits for another and one launch does it all.
 // Blocks of one column (gridDim.y) share the owned requests' pages and
-// tokens.  Bound by latency: one read of the lengths, one reduction, one
-// scan, then a binary search in shared memory, a page id and a write a slot.
-// 64 requests of one token: 2.9 us; 2047 requests, 1.05M slots (4.8 MB): 8.8.
+// tokens.  64 requests of one token: 2.9 us, latency (one read of the lengths,
+// one reduction, one scan, a search, a page id and a write).  2047 requests of
+// 1.05M slots (4.8 MB, 0.7 us of HBM): 8.8 us, of which 5.9 are the slots: each
+// has its own search of eight steps, page id and 4-byte store, where those of a
+// page could share all but the store.
 constexpr int kReq = 256;
 
 struct ReqLens {
@@ -161,7 +163,7 @@ __global__ void __launch_bounds__(kReq) page_tables_kernel(
 // ---------------------------------------------------------------- append
 // One 16-byte piece of a row per thread and tensor, kUnroll rows' pieces in
 // flight: a copy, bound by HBM (each row read once and written once).
-// 131071 rows of K and V, d = 512 (537 MB): 80.6 us, 6.7 TB/s, 98% of a plain
+// 131071 rows of K and V, d = 512 (537 MB): 80.7 us, 6.7 TB/s, 98% of a plain
 // copy's rate; 64 rows of one tensor: 1.2 us.
 constexpr int kUnroll = 4;
 
@@ -207,7 +209,7 @@ cudaError_t launch_page_tables(const LaunchCtx& c, const ServeShape& s,
                                int32_t* slots, int32_t* cu, int32_t* seq, int32_t* taken) {
   const int chunks = (s.B + kReq - 1) / kReq;
   // about 4 slots a thread, at most four blocks an SM (2047 requests, 1.05M slots:
-  // 8.7 us, with two 10.8, with eight 11.0: each adds up the requests before it)
+  // with two or eight 2 us longer: each adds up the requests before it)
   int64_t y = (s.T + 4 * kReq - 1) / (4 * kReq);
   const int64_t most = 4 * (int64_t)c.num_sms / chunks;
   if (y > most) y = most;
@@ -227,8 +229,8 @@ cudaError_t launch_append(const LaunchCtx& c, const ServeShape& s, const int32_t
   if (g > cap) g = cap;
   // Launched while what is before it in the stream runs, which it waits for on the
   // device, as the attention behind it is (an append of 64 rows and the smallest
-  // attention, call after call: 17.8 us, launched in turn 19.2).  The page tables
-  // are not: their largest case took 12 us so instead of 10.9.
+  // attention, call after call: 1.4 us less).  The page tables are not: their
+  // largest case took 1 us longer so.
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
