@@ -392,7 +392,7 @@ typedef struct dsa_serve_config {
   int32_t attn_heads; /* H, 1..128 */
   int32_t d_qk;       /* NoPE q/k dim in {128,256,512} */
   int32_t d_v;        /* must equal d_qk */
-  float sm_scale;     /* softmax scale; 0 -> 1/sqrt(d_qk) */
+  float sm_scale;     /* softmax scale, log2(e) times it finite; 0 -> 1/sqrt(d_qk) */
 } dsa_serve_config_t;
 
 /* Workspace kinds for dsa_serve_workspace_size(). */

@@ -2,7 +2,7 @@
 // checks, workspace sizes and launches.  Host code only.
 #include <math.h>
 
-#include "dsa_common.cuh"
+#include "attn_common.cuh"
 #include "dsa_internal.h"
 
 namespace dsa {
@@ -14,7 +14,7 @@ dsa_status_t check_serve(const dsa_serve_config_t* c, int which) {
   if (!c) return DSA_ERR_INVALID_ARG;
   if (c->n_pages < 1 || c->max_tokens < 1 || c->page_size < 1 || c->batch < 1 ||
       c->max_blocks < 1 || c->attn_heads < 1 || c->d_qk < 1 || c->d_v < 1 ||
-      !(c->sm_scale >= 0.f) || isinf(c->sm_scale))
+      !(c->sm_scale >= 0.f) || isinf(c->sm_scale * kLog2e))
     return DSA_ERR_INVALID_ARG;
   const int p = c->page_size;
   if (p != 16 && p != 32 && p != 64 && p != 128) return DSA_ERR_UNSUPPORTED_SHAPE;

@@ -93,6 +93,19 @@ def test_workspace_of_a_batch_that_is_mostly_idle(lib, T, H):
     assert size(T) <= 512 + 12 * (T + 1) + 256 + (2 * (-(-T * H // 128)) + T + 80) * slot
 
 
+def test_a_scale_that_overflows_in_base_two_is_refused(lib):
+    """The weights are powers of 2 of scale * log2(e) times a difference of scores,
+    0 of them for the largest: 0 * inf would make every row NaN."""
+    size = lambda s: dsa.serve_workspace_size(
+        dsa.ServeConfig(n_pages=10, max_tokens=1, batch=1, max_blocks=1, sm_scale=s),
+        dsa.SERVE_WS_PREFIX)
+    for s in (2.4e38, 3.4e38):
+        with pytest.raises(dsa.DsaError) as e:
+            size(s)
+        assert e.value.code == 1
+    assert size(2.3e38) == size(0.0)
+
+
 @pytest.mark.gpu
 def test_outputs_over_the_queries_and_an_empty_prefix_table():
     """o in q's place; and, behind no prefix, a prefix table that lies anywhere (it
