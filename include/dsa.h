@@ -492,6 +492,184 @@ DSA_API dsa_status_t dsa_prefix_attn(const dsa_serve_config_t* cfg, const void* 
                                      const int32_t* cu_tokens, void* o, float* lse,
                                      void* ws, size_t ws_bytes, void* stream);
 
+/* -------------------------------------------------- drafts and budgets
+ * The calls below let a group's requests draft trees of tokens, learn what
+ * each cached token receives of the attention, and drop the tokens that
+ * receive least when a request passes its budget.  Workspaces as above. */
+#define DSA_SERVE_WS_TREE 16    /* dsa_build_tree */
+#define DSA_SERVE_WS_WEIGHTS 17 /* dsa_key_weights */
+#define DSA_SERVE_WS_EVICT 18   /* dsa_evict_cache */
+
+/* Masks of the requests' drafted trees, once a step.  The rows
+ * cu_tokens[b] .. cu_tokens[b+1]-1 are the nodes 0, 1, .. of request b's tree
+ * and parents[t] is the node that row t's token follows, below its own number,
+ * or -1: it follows the tokens that the request holds already.  Bit j % 32 of
+ * tree_bits[t, j / 32] is set where node j is row t's own or an ancestor of it,
+ * and clear elsewhere.  Rows of no request are left as they are.
+ * parents [T], cu_tokens [B+1] int32 -> tree_bits [T, words] 32-bit words, 1 <=
+ * words <= 32.  tree_bits and the workspace must not overlap what the call
+ * reads, or one another (DSA_ERR_INVALID_ARG).
+ * Device-side errors (latched as DSA_ERR_DEVICE_BAD_INDEX): a request with more
+ * than 32 * words rows (bits of further nodes are left out), a parent below -1
+ * or not below its node (taken for -1), cu_tokens that start below 0, descend
+ * or end past T (no row of such a request is written).
+ * ws: DSA_SERVE_WS_TREE. */
+DSA_API dsa_status_t dsa_build_tree(const dsa_serve_config_t* cfg, const int32_t* parents,
+                                    const int32_t* cu_tokens, int32_t words,
+                                    uint32_t* tree_bits, void* ws, size_t ws_bytes,
+                                    void* stream);
+
+/* dsa_prefix_attn for a tree of drafted tokens a request: with base_b =
+ * seq_lens[b] - new_b, row t of request b sees the prefix, b's own tokens below
+ * base_b, and of the tokens base_b + j (node j) those whose bit in
+ * tree_bits[t] is set.  The bits may be any, dsa_build_tree's or a caller's
+ * own; nodes from 32 * words on are seen by no row.  A row whose bits are all
+ * clear sees the other keys alone; one without any key has O = 0, LSE = -inf.
+ * All else is as dsa_prefix_attn has it, which is the same call for trees that
+ * are chains: rows without an own token see the prefix alone, V of a request's
+ * own tokens has to be finite, o and lse may lie over q.
+ * tree_bits [T, words], 1 <= words <= 32.  ws: DSA_SERVE_WS_PREFIX. */
+DSA_API dsa_status_t dsa_tree_attn(const dsa_serve_config_t* cfg, const void* q,
+                                   const void* k_pages, const void* v_pages,
+                                   const int32_t* prefix_table, int64_t prefix_len,
+                                   const int32_t* block_table, const int32_t* seq_lens,
+                                   const int32_t* cu_tokens, const uint32_t* tree_bits,
+                                   int32_t words, void* o, float* lse, void* ws,
+                                   size_t ws_bytes, void* stream);
+
+/* What the own tokens of each request receive of its rows' attention.  With
+ * place j's slot s = block_table[b, j / page_size] * page_size + j % page_size
+ * and the rows r = (t, h) of request b that see place j,
+ *   w_out[s] = old_j + sum_r exp(scale * q[r] . k_pages[s] - lse[r]),
+ *   old_j = decay * w_pages[s] for j < seq_lens[b] - new_b, 0 for this step's own
+ * tokens (their slots need no clearing), for 0 <= j < seq_lens[b].  Rows see what
+ * they see in dsa_prefix_attn (tree_bits NULL) or in dsa_tree_attn; lse is what
+ * that call left, the prefix and all.  A row with lse = -inf adds nothing.
+ * Requests without rows, and slots of no request, are left as they are.
+ * A row with lse = NaN makes NaN of the weights of the tokens that it sees.
+ * Numbers: scores, weights and their sums are fp32.
+ * q [T, H, d_qk] bf16, lse [T, H] fp32, k_pages as above, w_pages, w_out
+ * [n_pages, page_size] fp32, 0 <= decay <= 1.  w_out may be w_pages; what is
+ * written must not overlap what is read, or itself, in any other way
+ * (DSA_ERR_INVALID_ARG).  A page may not belong to two requests with rows.
+ * T * H <= 2^20, else DSA_ERR_UNSUPPORTED_SHAPE.  Device-side errors as
+ * dsa_prefix_attn has them (a bad page's tokens get no weight).  Results repeat bit for
+ * bit on the same inputs and device.  ws: DSA_SERVE_WS_WEIGHTS. */
+DSA_API dsa_status_t dsa_key_weights(const dsa_serve_config_t* cfg, const void* q,
+                                     const float* lse, const void* k_pages,
+                                     const int32_t* block_table, const int32_t* seq_lens,
+                                     const int32_t* cu_tokens, const uint32_t* tree_bits,
+                                     int32_t words, const float* w_pages, float decay,
+                                     float* w_out, void* ws, size_t ws_bytes, void* stream);
+
+/* Eviction of one layer's cache by weight.  Request b keeps left_b =
+ * min(seq_lens[b], keep_lens[b]) of its own tokens: those that rank first by
+ * weight, where the first n_first and the last n_last places rank as +inf, ties
+ * go to the lower place and NaN ranks below all.  A key has no position (NoPE), so
+ * kept tokens need not stay in order: with a_0 < a_1 < .. the places below left_b
+ * whose tokens are dropped and c_0 < c_1 < .. the places from left_b on whose
+ * tokens are kept (as many), the rows of k_pages (and v_pages) at c_i are copied
+ * to a_i, and
+ *   w_out[slot of place j] = w_pages[slot of j's token], 0 <= j < left_b.
+ * Nothing that is read is written, so the caches are changed in place.  Tables
+ * and lengths stay: one dsa_release_pages a step serves all layers.  Rows and
+ * weights from left_b on, and all that belongs to no request, are left as they
+ * are.  v_pages NULL: K = V.  w_out may be w_pages.
+ * keep_lens [B] int32, n_first, n_last >= 0; seq_lens, block_table as above.  What
+ * is written must not overlap what is read, or itself, in any other way
+ * (DSA_ERR_INVALID_ARG).  A page may not belong to two requests, or stand twice
+ * in one's row.
+ * Device-side errors (latched as DSA_ERR_DEVICE_BAD_INDEX; nothing is read or
+ * written out of bounds): a length below 0 or above max_blocks * page_size, or a
+ * keep_lens below 0 (the request is left as it is), a page id outside the cache
+ * (its tokens have no weight: they rank with NaN, and are not copied).
+ * ws: DSA_SERVE_WS_EVICT. */
+DSA_API dsa_status_t dsa_evict_cache(const dsa_serve_config_t* cfg, const float* w_pages,
+                                     const int32_t* block_table, const int32_t* seq_lens,
+                                     const int32_t* keep_lens, int64_t n_first, int64_t n_last,
+                                     void* k_pages, void* v_pages, float* w_out, void* ws,
+                                     size_t ws_bytes, void* stream);
+
+/* The lengths after an eviction and the pages that it leaves free, once a step:
+ *   left_b = min(seq_lens[b], keep_lens[b]),   new_lens[b] = left_b,
+ *   gone_b = ceil(seq_lens[b] / page_size) - ceil(left_b / page_size),
+ *   pages[sum_{a<b} gone_a + i] = block_table[b, ceil(left_b / page_size) + i],
+ *   n_released[0] = sum_b gone_b.
+ * block_table stays (entries past a request's length are never read), and so do
+ * entries of pages [n_max] from n_released on.  pages needs 4-byte alignment, so
+ * that it may point to the end of a list of free pages.  What is written must not
+ * overlap what is read, or itself (DSA_ERR_INVALID_ARG): a step whose seq_lens
+ * are the last one's writes its own to another buffer.
+ * Device-side errors (latched): a length below 0 or above max_blocks * page_size,
+ * or a keep_lens below 0 (DSA_ERR_DEVICE_BAD_INDEX; the request keeps its length
+ * and its pages), pages past n_max (DSA_ERR_DEVICE_NO_PAGES; n_released still
+ * counts them).  ws: DSA_SERVE_WS_TABLES. */
+DSA_API dsa_status_t dsa_release_pages(const dsa_serve_config_t* cfg, const int32_t* seq_lens,
+                                       const int32_t* keep_lens, const int32_t* block_table,
+                                       int32_t* new_lens, int32_t* pages, int64_t n_max,
+                                       int32_t* n_released, void* ws, size_t ws_bytes,
+                                       void* stream);
+
+/* ------------------------------------------------------ log probabilities
+ * The trainer's log-probs are compared with those of the engine that sampled
+ * the tokens ("Scaling Training to 1M Token Context on GLM-5.3-Flash",
+ * "Results"): both sides get them from their logits with the calls below.
+ *
+ * Layout is fixed for foreign callers: 40 bytes, natural alignment. */
+#define DSA_BF16 0
+#define DSA_FP16 1
+#define DSA_FP32 2
+typedef struct dsa_logprobs_config {
+  int64_t rows;   /* R, >= 1 (< 2^31) */
+  int64_t vocab;  /* V, >= 1 (< 2^30) */
+  int64_t ld;     /* elements from a row of logits to the next, >= V (< 2^40) */
+  int32_t dtype;  /* of logits and their gradient: DSA_BF16, DSA_FP16, DSA_FP32 */
+  int32_t n_top;  /* alternatives a row, 0 <= n_top <= min(64, V) */
+  float scale;    /* of the logits (one over the temperature), > 0; log2(e) times it finite */
+  int32_t reserved; /* 0 */
+} dsa_logprobs_config_t;
+
+/* With x = scale * logits[r, :] and p = softmax(x):
+ *   lse[r] = log sum_j exp(x_j),   logp[r] = x_tokens[r] - lse[r],
+ *   entropy[r] = -sum_j p_j log p_j   (0 log 0 = 0),
+ *   top_ids[r, 0 .. n_top-1] = the ids of the largest logits in descending order,
+ *     ties to the lower id,   top_logp[r, i] = x_top_ids[r, i] - lse[r].
+ * A token below 0 stands for none: logp = 0.  A logit of -inf has p = 0; a row of
+ * nothing else has lse = logp = top_logp = -inf and entropy 0.  A NaN or +inf
+ * among a row's logits makes NaN of its lse, logp, entropy and top_logp; its
+ * top_ids are then any ids of the row.
+ * Numbers: fp32 throughout, one pass over the logits.
+ * logits [R, ld] (rows of V elements), tokens
+ * [R] int32, logp, lse, entropy [R] fp32, top_ids [R, n_top] int32, top_logp
+ * [R, n_top] fp32 (both NULL where n_top is 0).  All need their element's
+ * alignment only, so that a call may take a range of rows.  What is written must not
+ * overlap what is read, or itself (DSA_ERR_INVALID_ARG).  A token from V on
+ * latches DSA_ERR_DEVICE_BAD_INDEX and counts as none.
+ * ws: 256 bytes, zeroed by dsa_workspace_init(). */
+DSA_API dsa_status_t dsa_token_logprobs(const dsa_logprobs_config_t* cfg, const void* logits,
+                                        const int32_t* tokens, float* logp, float* lse,
+                                        float* entropy, int32_t* top_ids, float* top_logp,
+                                        void* ws, size_t ws_bytes, void* stream);
+
+/* The gradient of sum_r (g_logp[r] * logp[r] + g_entropy[r] * entropy[r]) with
+ * respect to the logits:
+ *   dlogits[r, j] = scale * (g_logp[r] * (1[j = tokens[r]] - p_j)
+ *                            - g_entropy[r] * p_j * (log p_j + entropy[r])),
+ * p_j = exp(x_j - lse[r]), rounded once to the logits' type.  A row without a
+ * token (below 0) has no part of g_logp; one with lse = -inf has gradient 0.
+ * g_logp or g_entropy may be NULL (0), entropy too where g_entropy is.  lse and
+ * entropy are dsa_token_logprobs's of the same logits and scale; n_top is not
+ * used.  dlogits [R, ld_grad], ld_grad >= V; what lies between the rows is left
+ * as it is.  dlogits may be logits, with ld_grad = ld; what is written must not
+ * overlap what is read in any other way (DSA_ERR_INVALID_ARG).  A token from V
+ * on latches DSA_ERR_DEVICE_BAD_INDEX and counts as none.  ws: as above. */
+DSA_API dsa_status_t dsa_token_logprobs_bwd(const dsa_logprobs_config_t* cfg,
+                                            const void* logits, const int32_t* tokens,
+                                            const float* lse, const float* entropy,
+                                            const float* g_logp, const float* g_entropy,
+                                            void* dlogits, int64_t ld_grad, void* ws,
+                                            size_t ws_bytes, void* stream);
+
 /* Synchronise `stream`, read the workspace status word into *device_status
  * (a dsa_status_t value, DSA_OK if nothing was latched) and clear it. */
 DSA_API dsa_status_t dsa_get_device_status(void* ws, void* stream,

@@ -34,6 +34,9 @@ __all__ = [
     "ServeConfig", "PageTables", "serve_workspace_size", "serve_workspace",
     "build_page_tables", "append_cache", "prefix_attn", "SERVE_WS_TABLES",
     "SERVE_WS_APPEND", "SERVE_WS_PREFIX",
+    "build_tree", "tree_attn", "key_weights", "evict_cache", "ReleasedPages",
+    "release_pages", "SERVE_WS_TREE", "SERVE_WS_WEIGHTS", "SERVE_WS_EVICT",
+    "TokenLogprobs", "logprobs_workspace", "token_logprobs", "token_logprobs_bwd",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -48,6 +51,7 @@ _lib = None
 
 WS_INDEX, WS_FWD, WS_BWD, WS_STATUS, WS_STREAM, WS_BWD_ROWS, WS_STEP = range(7)
 SERVE_WS_TABLES, SERVE_WS_APPEND, SERVE_WS_PREFIX = range(3)
+SERVE_WS_TREE, SERVE_WS_WEIGHTS, SERVE_WS_EVICT = range(16, 19)
 
 STATUS_NAMES = {
     0: "DSA_OK", 1: "DSA_ERR_INVALID_ARG", 2: "DSA_ERR_UNSUPPORTED_SHAPE",
@@ -69,7 +73,9 @@ EXPORTS = [
     "dsa_sparse_attn_bwd_range", "dsa_accum_to_bf16", "dsa_step",
     "dsa_step_host", "dsa_check_wait_timeout", "dsa_static_device_status",
     "dsa_serve_workspace_size", "dsa_build_page_tables", "dsa_append_cache",
-    "dsa_prefix_attn",
+    "dsa_prefix_attn", "dsa_build_tree", "dsa_tree_attn", "dsa_key_weights",
+    "dsa_evict_cache", "dsa_release_pages", "dsa_token_logprobs",
+    "dsa_token_logprobs_bwd",
 ]
 
 
@@ -104,6 +110,18 @@ class _CServeConfig(ctypes.Structure):
 
 
 assert ctypes.sizeof(_CServeConfig) == 48
+
+
+class _CLogprobsConfig(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("vocab", ctypes.c_int64), ("ld", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("n_top", ctypes.c_int32), ("scale", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+assert ctypes.sizeof(_CLogprobsConfig) == 40
+_LOGIT_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 # dsa_step_tensors_t: the step's tensors, in declaration order
 STEP_FIELDS = ("q_idx", "k_idx", "w", "k_gate", "q", "k", "v", "dO",
@@ -197,7 +215,9 @@ def _load():
         lib = ctypes.CDLL(_LIB_PATH)
         P, I32, I64, SZ = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
                            ctypes.c_size_t)
+        F32 = ctypes.c_float
         CP, SP = ctypes.POINTER(_CConfig), ctypes.POINTER(_CServeConfig)
+        LP = ctypes.POINTER(_CLogprobsConfig)
         sig = {
             "dsa_workspace_size": [CP, I32, ctypes.POINTER(SZ)],
             "dsa_workspace_init": [P, SZ, P],
@@ -230,6 +250,13 @@ def _load():
             "dsa_build_page_tables": [SP, P, P, P, I64, P, P, P, P, P, P, SZ, P],
             "dsa_append_cache": [SP, P, P, P, P, P, P, SZ, P],
             "dsa_prefix_attn": [SP, P, P, P, P, I64, P, P, P, P, P, P, SZ, P],
+            "dsa_build_tree": [SP, P, P, I32, P, P, SZ, P],
+            "dsa_tree_attn": [SP, P, P, P, P, I64, P, P, P, P, I32, P, P, P, SZ, P],
+            "dsa_key_weights": [SP, P, P, P, P, P, P, P, I32, P, F32, P, P, SZ, P],
+            "dsa_evict_cache": [SP, P, P, P, P, I64, I64, P, P, P, P, SZ, P],
+            "dsa_release_pages": [SP, P, P, P, P, P, I64, P, P, SZ, P],
+            "dsa_token_logprobs": [LP, P, P, P, P, P, P, P, P, SZ, P],
+            "dsa_token_logprobs_bwd": [LP, P, P, P, P, P, P, P, I64, P, SZ, P],
         }
         for name, args in sig.items():
             f = getattr(lib, name)
@@ -957,6 +984,12 @@ def prefix_attn(cfg: ServeConfig, q, k_pages, prefix_table, prefix_len: int,
     those before it.  Rows of no request are not written (new outputs hold
     zeros there).  Without v_pages: K = V.  prefix_table may be None when
     prefix_len is 0.  o may be q itself; other buffers may not overlap."""
+    return _attend(cfg, q, k_pages, prefix_table, prefix_len, block_table, seq_lens, cu_tokens,
+                   None, v_pages, o, lse, ws)
+
+
+def _attend(cfg, q, k_pages, prefix_table, prefix_len, block_table, seq_lens, cu_tokens,
+            tree_bits, v_pages, o, lse, ws):
     T, H, B, bf, i32 = (cfg.max_tokens, cfg.attn_heads, cfg.batch, torch.bfloat16,
                         torch.int32)
     dev, p_q = _first_tensor(q, "q", bf, (T, H, cfg.d_qk))
@@ -979,6 +1012,8 @@ def prefix_attn(cfg: ServeConfig, q, k_pages, prefix_table, prefix_len: int,
     p_table = _check_tensor(block_table, "block_table", i32, (B, cfg.max_blocks), dev)
     p_seq = _check_tensor(seq_lens, "seq_lens", i32, (B,), dev)
     p_cu = _check_tensor(cu_tokens, "cu_tokens", i32, (B + 1,), dev)
+    if tree_bits is not None:
+        p_bits, words = _check_bits(tree_bits, T, dev)
     if o is None:
         o = torch.zeros((T, H, cfg.d_v), dtype=bf, device=dev)
     if lse is None:
@@ -986,6 +1021,224 @@ def prefix_attn(cfg: ServeConfig, q, k_pages, prefix_table, prefix_len: int,
     p_o = _check_tensor(o, "o", bf, (T, H, cfg.d_v), dev)
     p_lse = _check_tensor(lse, "lse", torch.float32, (T, H), dev)
     ws, p_ws, n_ws = _serve_ws(cfg, SERVE_WS_PREFIX, ws, dev)
-    _serve_call("dsa_prefix_attn", dev, cfg._ref, p_q, p_k, p_v, p_prefix, prefix_len,
-                p_table, p_seq, p_cu, p_o, p_lse, p_ws, n_ws)
+    if tree_bits is None:
+        _serve_call("dsa_prefix_attn", dev, cfg._ref, p_q, p_k, p_v, p_prefix, prefix_len,
+                    p_table, p_seq, p_cu, p_o, p_lse, p_ws, n_ws)
+    else:
+        _serve_call("dsa_tree_attn", dev, cfg._ref, p_q, p_k, p_v, p_prefix, prefix_len,
+                    p_table, p_seq, p_cu, p_bits, words, p_o, p_lse, p_ws, n_ws)
     return o, lse
+
+
+# ------------------------------------------------------ drafts and budgets
+
+
+def _check_bits(bits, T, dev):
+    words = bits.shape[-1] if isinstance(bits, torch.Tensor) and bits.dim() == 2 else 1
+    if not 1 <= words <= 32:
+        raise ValueError("tree_bits must be [max_tokens, 1..32]")
+    return _check_tensor(bits, "tree_bits", torch.int32, (T, words), dev), words
+
+
+def build_tree(cfg: ServeConfig, parents, cu_tokens, words: int = 2, out=None, ws=None):
+    """Masks of the requests' drafted trees, once a step: parents [T] int32 says
+    which node of its request (below its own number) each row follows, -1: the
+    tokens that the request holds already.  Returns tree_bits [T, words] int32
+    (new ones hold zeros in rows of no request; 32 * words is the most nodes of a
+    request)."""
+    T, B, i32 = cfg.max_tokens, cfg.batch, torch.int32
+    dev, p_par = _first_tensor(parents, "parents", i32, (T,))
+    p_cu = _check_tensor(cu_tokens, "cu_tokens", i32, (B + 1,), dev)
+    if out is None:
+        out = torch.zeros((T, operator.index(words)), dtype=i32, device=dev)
+    p_out, words = _check_bits(out, T, dev)
+    ws, p_ws, n_ws = _serve_ws(cfg, SERVE_WS_TREE, ws, dev)
+    _serve_call("dsa_build_tree", dev, cfg._ref, p_par, p_cu, words, p_out, p_ws, n_ws)
+    return out
+
+
+def tree_attn(cfg: ServeConfig, q, k_pages, prefix_table, prefix_len: int, block_table,
+              seq_lens, cu_tokens, tree_bits, v_pages=None, o=None, lse=None, ws=None):
+    """prefix_attn for trees of drafted tokens: a row sees the prefix, its
+    request's tokens before the step's, and of the step's own those whose bits are
+    set in its row of tree_bits [T, words] int32 (build_tree's, or any).  The
+    workspace is prefix_attn's."""
+    if tree_bits is None:
+        raise ValueError("tree_attn needs tree_bits")
+    return _attend(cfg, q, k_pages, prefix_table, prefix_len, block_table, seq_lens, cu_tokens,
+                   tree_bits, v_pages, o, lse, ws)
+
+
+def key_weights(cfg: ServeConfig, q, lse, k_pages, block_table, seq_lens, cu_tokens, w_pages,
+                tree_bits=None, decay: float = 1.0, w_out=None, ws=None):
+    """Accumulate what each request's own tokens receive of the attention of its
+    rows: w_out = decay * w_pages + sum over rows of exp(scale q.k - lse), by slot
+    [n_pages, page_size] fp32; tokens of this step start from 0.  lse [T, H] is
+    what prefix_attn (or, with tree_bits, tree_attn) left.  w_out None: in place."""
+    T, H, B, i32, f32 = cfg.max_tokens, cfg.attn_heads, cfg.batch, torch.int32, torch.float32
+    bf, slots = torch.bfloat16, (cfg.n_pages, cfg.page_size)
+    dev, p_q = _first_tensor(q, "q", bf, (T, H, cfg.d_qk))
+    p_lse = _check_tensor(lse, "lse", f32, (T, H), dev)
+    p_k = _check_tensor(k_pages, "k_pages", bf, slots + (cfg.d_qk,), dev)
+    p_table = _check_tensor(block_table, "block_table", i32, (B, cfg.max_blocks), dev)
+    p_seq = _check_tensor(seq_lens, "seq_lens", i32, (B,), dev)
+    p_cu = _check_tensor(cu_tokens, "cu_tokens", i32, (B + 1,), dev)
+    p_bits, words = (None, 0) if tree_bits is None else _check_bits(tree_bits, T, dev)
+    p_w = _check_tensor(w_pages, "w_pages", f32, slots, dev)
+    if w_out is None:
+        w_out = w_pages
+    p_out = _check_tensor(w_out, "w_out", f32, slots, dev)
+    ws, p_ws, n_ws = _serve_ws(cfg, SERVE_WS_WEIGHTS, ws, dev)
+    _serve_call("dsa_key_weights", dev, cfg._ref, p_q, p_lse, p_k, p_table, p_seq, p_cu, p_bits,
+                words, p_w, float(decay), p_out, p_ws, n_ws)
+    return w_out
+
+
+def evict_cache(cfg: ServeConfig, w_pages, block_table, seq_lens, keep_lens, k_pages,
+                v_pages=None, n_first: int = 0, n_last: int = 0, w_out=None, ws=None):
+    """Shrink each request's cache to keep_lens[b] tokens, in place: those with the
+    largest weights (the first n_first and the last n_last always rank first), the
+    kept ones from behind moved into the places of the dropped ones.  Tables and
+    lengths stay: release_pages, once for all layers.  Returns w_out (None: in
+    place).  Without v_pages: K = V."""
+    B, i32, f32, bf = cfg.batch, torch.int32, torch.float32, torch.bfloat16
+    slots = (cfg.n_pages, cfg.page_size)
+    dev, p_w = _first_tensor(w_pages, "w_pages", f32, slots)
+    p_table = _check_tensor(block_table, "block_table", i32, (B, cfg.max_blocks), dev)
+    p_seq = _check_tensor(seq_lens, "seq_lens", i32, (B,), dev)
+    p_keep = _check_tensor(keep_lens, "keep_lens", i32, (B,), dev)
+    p_k = _check_tensor(k_pages, "k_pages", bf, slots + (cfg.d_qk,), dev)
+    p_v = None
+    if v_pages is not None:
+        p_v = _check_tensor(v_pages, "v_pages", bf, slots + (cfg.d_v,), dev)
+    n_first, n_last = operator.index(n_first), operator.index(n_last)
+    if n_first < 0 or n_last < 0:
+        raise ValueError("n_first and n_last must not be negative")
+    if w_out is None:
+        w_out = w_pages
+    p_out = _check_tensor(w_out, "w_out", f32, slots, dev)
+    ws, p_ws, n_ws = _serve_ws(cfg, SERVE_WS_EVICT, ws, dev)
+    _serve_call("dsa_evict_cache", dev, cfg._ref, p_w, p_table, p_seq, p_keep, n_first, n_last,
+                p_k, p_v, p_out, p_ws, n_ws)
+    return w_out
+
+
+class ReleasedPages(typing.NamedTuple):
+    """What release_pages writes (see dsa_release_pages)."""
+    new_lens: torch.Tensor    # [batch] int32
+    pages: torch.Tensor       # [any] int32
+    n_released: torch.Tensor  # [1] int32
+
+
+def release_pages(cfg: ServeConfig, seq_lens, keep_lens, block_table,
+                  out: ReleasedPages = None, ws=None) -> ReleasedPages:
+    """Lengths after an eviction to keep_lens, and the pages that it leaves free
+    (the first n_released entries of pages; new ones hold -1 behind them).  Takes
+    build_page_tables's workspace."""
+    B, i32 = cfg.batch, torch.int32
+    dev, p_seq = _first_tensor(seq_lens, "seq_lens", i32, (B,))
+    p_keep = _check_tensor(keep_lens, "keep_lens", i32, (B,), dev)
+    p_table = _check_tensor(block_table, "block_table", i32, (B, cfg.max_blocks), dev)
+    if out is None:
+        new = lambda n: torch.full((n,), -1, dtype=i32, device=dev)
+        out = ReleasedPages(new(B), new(cfg.n_pages), new(1))
+    p_new = _check_tensor(out.new_lens, "new_lens", i32, (B,), dev)
+    n_max = out.pages.numel() if isinstance(out.pages, torch.Tensor) else 0
+    p_pages = _check_tensor(out.pages, "pages", i32, (n_max,), dev)
+    p_n = _check_tensor(out.n_released, "n_released", i32, (1,), dev)
+    ws, p_ws, n_ws = _serve_ws(cfg, SERVE_WS_TABLES, ws, dev)
+    _serve_call("dsa_release_pages", dev, cfg._ref, p_seq, p_keep, p_table, p_new, p_pages,
+                n_max, p_n, p_ws, n_ws)
+    return out
+
+
+# ------------------------------------------------------ log probabilities
+
+
+def logprobs_workspace(device="cuda") -> torch.Tensor:
+    """A zeroed workspace of the log-probability calls (their status word)."""
+    return torch.zeros(256, dtype=torch.uint8, device=torch.device(device))
+
+
+def _check_logits(t, name):
+    """(device, rows, vocab, elements between rows) of a [R, V] tensor whose rows
+    are contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _LOGIT_DTYPES \
+            or t.dim() != 2 or t.numel() == 0 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{name} must be a [rows, vocab] CUDA tensor of bf16, fp16 or fp32 "
+                         "with contiguous rows")
+    rows, vocab = t.shape
+    ld = t.stride(0) if rows > 1 else vocab
+    if ld < vocab:
+        raise ValueError(f"rows of {name} must not overlap")
+    return t.get_device(), rows, vocab, ld
+
+
+def _logprobs_ws(ws, dev):
+    if ws is None:
+        ws = logprobs_workspace(torch.device("cuda", dev))
+    n = ws.numel() if isinstance(ws, torch.Tensor) else 0
+    return ws, _check_tensor(ws, "ws", torch.uint8, (n,), dev), n
+
+
+class TokenLogprobs(typing.NamedTuple):
+    """What token_logprobs writes (see dsa_token_logprobs)."""
+    logp: torch.Tensor      # [rows] fp32
+    lse: torch.Tensor       # [rows] fp32
+    entropy: torch.Tensor   # [rows] fp32
+    top_ids: torch.Tensor   # [rows, n_top] int32
+    top_logp: torch.Tensor  # [rows, n_top] fp32
+
+
+def token_logprobs(logits, tokens, n_top: int = 0, scale: float = 1.0,
+                   out: TokenLogprobs = None, ws=None) -> TokenLogprobs:
+    """Log probabilities of tokens [rows] int32 (below 0: none, logp 0) under
+    softmax(scale * logits), logits [rows, vocab] bf16, fp16 or fp32 with any
+    stride between rows; with each row's log-sum-exp, entropy and n_top (at most
+    64) best alternatives, ties to the lower id.  One pass over the logits."""
+    dev, rows, vocab, ld = _check_logits(logits, "logits")
+    f32, i32 = torch.float32, torch.int32
+    n_top = operator.index(n_top)
+    if not 0 <= n_top <= min(64, vocab):
+        raise ValueError("n_top must be in 0 .. min(64, vocab)")
+    p_tok = _check_tensor(tokens, "tokens", i32, (rows,), dev)
+    if out is None:
+        at = torch.device("cuda", dev)
+        out = TokenLogprobs(*(torch.empty(rows, dtype=f32, device=at) for _ in range(3)),
+                            torch.empty((rows, n_top), dtype=i32, device=at),
+                            torch.empty((rows, n_top), dtype=f32, device=at))
+    p = [_check_tensor(t, name, f32, (rows,), dev)
+         for t, name in zip(out[:3], ("logp", "lse", "entropy"))]
+    p_ids = _check_tensor(out.top_ids, "top_ids", i32, (rows, n_top), dev) if n_top else None
+    p_top = _check_tensor(out.top_logp, "top_logp", f32, (rows, n_top), dev) if n_top else None
+    ws, p_ws, n_ws = _logprobs_ws(ws, dev)
+    cc = _CLogprobsConfig(rows, vocab, ld, _LOGIT_DTYPES[logits.dtype], n_top, float(scale), 0)
+    _serve_call("dsa_token_logprobs", dev, ctypes.byref(cc), logits.data_ptr(), p_tok, *p, p_ids,
+                p_top, p_ws, n_ws)
+    return out
+
+
+def token_logprobs_bwd(logits, tokens, lse, entropy, g_logp, g_entropy=None,
+                       scale: float = 1.0, dlogits=None, ws=None):
+    """The gradient of sum(g_logp * logp + g_entropy * entropy) with respect to the
+    logits, in their type: dlogits [rows, vocab] (a stride of its own between rows;
+    logits itself is allowed).  lse and entropy are token_logprobs's.  g_logp or
+    g_entropy may be None."""
+    dev, rows, vocab, ld = _check_logits(logits, "logits")
+    f32 = torch.float32
+    p_tok = _check_tensor(tokens, "tokens", torch.int32, (rows,), dev)
+    p_lse = _check_tensor(lse, "lse", f32, (rows,), dev)
+    opt = lambda t, name: None if t is None else _check_tensor(t, name, f32, (rows,), dev)
+    if g_entropy is not None and entropy is None:
+        raise ValueError("g_entropy needs entropy")
+    p_ent, p_g, p_h = opt(entropy, "entropy"), opt(g_logp, "g_logp"), opt(g_entropy, "g_entropy")
+    if dlogits is None:
+        dlogits = torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
+    d_dev, d_rows, d_vocab, d_ld = _check_logits(dlogits, "dlogits")
+    if (d_dev, d_rows, d_vocab, dlogits.dtype) != (dev, rows, vocab, logits.dtype):
+        raise ValueError("dlogits must match logits")
+    ws, p_ws, n_ws = _logprobs_ws(ws, dev)
+    cc = _CLogprobsConfig(rows, vocab, ld, _LOGIT_DTYPES[logits.dtype], 0, float(scale), 0)
+    _serve_call("dsa_token_logprobs_bwd", dev, ctypes.byref(cc), logits.data_ptr(), p_tok, p_lse,
+                p_ent, p_g, p_h, dlogits.data_ptr(), d_ld, p_ws, n_ws)
+    return dlogits

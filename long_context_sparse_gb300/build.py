@@ -19,7 +19,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdsa_gb300.so")
 LIB_CHECKS = os.path.join(PKG, "libdsa_gb300_checks.so")
 SOURCES = ["select.cu", "indexer.cu", "indexer_topk.cu", "attn_fwd_tc.cu", "attn_bwd.cu",
-           "attn_bwd_tc.cu", "serve_tables.cu", "prefix_attn.cu", "serve_api.cu",
+           "attn_bwd_tc.cu", "serve_tables.cu", "prefix_attn.cu", "key_weights.cu", "evict.cu",
+           "logprobs.cu", "serve_api.cu",
            "dsa_api.cu", "dsa_static.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",

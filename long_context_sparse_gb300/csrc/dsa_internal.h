@@ -126,6 +126,30 @@ cudaError_t launch_attn_bwd_finalize(const LaunchCtx& c, const AttnShape& s,
                                      const float* dk_acc, const float* dv_acc,
                                      __nv_bfloat16* dk, __nv_bfloat16* dv);
 
+// Buffers of a call.
+struct Span {
+  const void* at;
+  size_t bytes;
+};
+
+inline bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+  return x && y && a.bytes && b.bytes && (x <= y ? y - x < a.bytes : x - y < b.bytes);
+}
+
+// Whether what a call writes meets what it reads, or itself: its blocks read
+// and write in no order.
+template <int W, int R>
+inline bool written_meets(const Span (&w)[W], const Span (&r)[R]) {
+  for (int i = 0; i < W; ++i) {
+    for (int j = 0; j < R; ++j)
+      if (overlap(w[i], r[j])) return true;
+    for (int j = 0; j < i; ++j)
+      if (overlap(w[i], w[j])) return true;
+  }
+  return false;
+}
+
 // ------------------------------------------------------------- serving
 struct ServeShape {
   int64_t n_pages;
@@ -150,14 +174,43 @@ cudaError_t launch_append(const LaunchCtx& c, const ServeShape& s, const int32_t
 // Workspace bytes past the header of launch_prefix_attn.
 size_t prefix_attn_ws(const ServeShape& s);
 
-// Shared-prefix attention; work: the workspace past the header.  q_map: q as
+// Shared-prefix attention, of trees where tree_bits is not nullptr; work: the workspace past the header.  q_map: q as
 // [T * H, D], box {64, 64}; k_map, v_maps: the cache as [n_pages * page, D], box
 // {64, page}, and of V also {64, 8} and {64, 1}.
 cudaError_t launch_prefix_attn(const LaunchCtx& c, const ServeShape& s,
                                const CUtensorMap& q_map, const CUtensorMap& k_map,
                                const CUtensorMap (&v_maps)[3], const int32_t* prefix_table,
                                int64_t prefix_len, const int32_t* table,
-                               const int32_t* seq, const int32_t* cu, __nv_bfloat16* o,
+                               const int32_t* seq, const int32_t* cu,
+                               const uint32_t* tree_bits, int words, __nv_bfloat16* o,
                                float* lse, uint8_t* work);
+
+// Ancestor masks of the requests' drafted trees.
+cudaError_t launch_build_tree(const LaunchCtx& c, const ServeShape& s, const int32_t* parents,
+                              const int32_t* cu, int words, uint32_t* tree_bits);
+
+// Weights that cached tokens receive; q_map: q as [T * H, D], box {64, 64}; k_map:
+// the cache as [n_pages * page, D], box {64, page}.
+size_t key_weights_ws(const ServeShape& s);
+cudaError_t launch_key_weights(const LaunchCtx& c, const ServeShape& s,
+                               const CUtensorMap& q_map, const CUtensorMap& k_map,
+                               const __nv_bfloat16* q, const float* lse,
+                               const __nv_bfloat16* k_pages, const int32_t* table,
+                               const int32_t* seq, const int32_t* cu,
+                               const uint32_t* tree_bits, int words, const float* w_pages,
+                               float decay, float* w_out, uint8_t* work);
+
+// Eviction by weight; ws: the whole workspace (its header has the counters).
+size_t evict_ws(const ServeShape& s);
+cudaError_t launch_evict(const LaunchCtx& c, const ServeShape& s, const float* w_pages,
+                         const int32_t* table, const int32_t* seq, const int32_t* keep,
+                         int32_t n_first, int32_t n_last, __nv_bfloat16* k_pages,
+                         __nv_bfloat16* v_pages, float* w_out, uint8_t* ws);
+
+// Lengths after an eviction, and the pages that it leaves free.
+cudaError_t launch_release_pages(const LaunchCtx& c, const ServeShape& s, const int32_t* seq,
+                                 const int32_t* keep, const int32_t* table,
+                                 int32_t* new_lens, int32_t* pages, int64_t n_max,
+                                 int32_t* n_released);
 
 }  // namespace dsa

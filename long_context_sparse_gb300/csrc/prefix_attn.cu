@@ -151,6 +151,12 @@ struct Lens {
   int H;
 };
 
+// Of a tree's rows: which of their request's nodes they see (dsa_tree_attn).
+struct TreeBits {
+  const int32_t* bits;  // [T][words]
+  int words;
+};
+
 struct ReqShape {
   int32_t row0;    // first row (token * H)
   int32_t n_rows;  // rows
@@ -233,6 +239,7 @@ struct Walk {
   int32_t ub, b;
 
   // the next item, or one of no tiles
+  template <bool Tree>
   __device__ __forceinline__ void next(const Lens& L, int B, int32_t prefix_len, Item& it) {
     const int64_t start = sh.start, end = sh.end;
     const int32_t unit_cost = sh.unit_cost;
@@ -284,9 +291,10 @@ struct Walk {
         it.rel0 = j * kRows;
         it.row0 = r.row0 + it.rel0;
         it.n_rows = min(kRows, r.n_rows - it.rel0);
-        // keys beyond the block's last row are seen by no row of it
-        it.len = min(r.len, row_limit(r, L.H, it.rel0 + it.n_rows - 1));
-        it.lim_min = row_limit(r, L.H, it.rel0);
+        // keys beyond the block's last row are seen by no row of it; a tree's nodes
+        // may be seen by any
+        it.len = Tree ? r.len : min(r.len, row_limit(r, L.H, it.rel0 + it.n_rows - 1));
+        it.lim_min = Tree ? max(0, r.len - r.n_new) : row_limit(r, L.H, it.rel0);
         it.b = b;
         share_of(c0, tiles, unit_cost, start, end, it.tile0, last);
         last = min(last, (it.len + kKeys - 1) / kKeys);
@@ -515,7 +523,7 @@ __device__ __forceinline__ float column_reduce(float (&x)[16], int lane) {
   return MAX ? fmaxf(x[0], got) : x[0] + got;
 }
 
-template <int D>
+template <int D, bool Tree>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefix_attn_kernel(const __grid_constant__ CUtensorMap q_map,
                        const __grid_constant__ CUtensorMap k_map,
@@ -525,7 +533,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                        const int32_t* __restrict__ prefix_table, int32_t prefix_len,
                        const int32_t* __restrict__ table, int B, int64_t T,
                        int max_blocks, int page_log2, int32_t n_pages, int64_t n_slots,
-                       float scale_log2, uint32_t* status, uint64_t timeout_ns) {
+                       float scale_log2, TreeBits tree, uint32_t* status,
+                       uint64_t timeout_ns) {
   using C = PCfg<D>;
   constexpr uint32_t IDESC_S = idesc_bf16(256, 128, 0, 0);
   constexpr uint32_t IDESC_O = idesc_bf16(256, 128, 1, 1);
@@ -539,7 +548,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint8_t* tail = gb + C::kQBytes + C::kPBufs * C::kPBytes + kStages * kStageBytes;
   float* nm2_s = reinterpret_cast<float*>(tail);          // [item & 1][row] -m
   float* fac_s = nm2_s + 2 * kRows;  // [row] what raising m makes of l and O
-  uint8_t* lim_s = reinterpret_cast<uint8_t*>(fac_s + kRows);  // [row] keys past lim_min
+  // [row] keys past lim_min that it sees; of a tree: its node from the group's first
+  uint8_t* lim_s = reinterpret_cast<uint8_t*>(fac_s + kRows);
   uint64_t* bars = reinterpret_cast<uint64_t*>(lim_s + kRows);
   // abort, tmem, beyond, issuer's tiles
   uint32_t* misc = reinterpret_cast<uint32_t*>(bars + kBars);
@@ -808,7 +818,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       Walk walk{*share, share->start, share->first_cost, share->first_unit, share->first_b};
       __syncwarp();
       auto post = [&]() {  // the next item, one ahead of its tiles
-        walk.next(L, B, prefix_len, it);
+        walk.next<Tree>(L, B, prefix_len, it);
         if (!W.wait(post_free(ni), ((ni >> 1) & 1u) ^ 1u)) return false;
         if (lane == 0) {
           posts[ni & 1u] = it;
@@ -943,10 +953,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       float* nm_s = nm2_s + (ni & 1u) * kRows;
       if (tid < kRows) {  // at most one key more a row
         const int32_t pb = post->b;
-        lim_s[tid] = pb < 0 ? 0
-                            : (uint8_t)(row_limit(req_shape(L, pb), L.H,
-                                                  post->rel0 + min(tid, post->n_rows - 1)) -
-                                        lim_min);
+        if (Tree) {
+          // a group of 64 rows has at most 64 nodes
+          const int32_t row0 = post->row0, first = min(tid & kGroupRows, post->n_rows - 1);
+          lim_s[tid] = (uint8_t)((row0 + max(first, min(tid, post->n_rows - 1))) / L.H -
+                                 (row0 + first) / L.H);
+        } else {
+          lim_s[tid] = pb < 0 ? 0
+                              : (uint8_t)(row_limit(req_shape(L, pb), L.H,
+                                                    post->rel0 + min(tid, post->n_rows - 1)) -
+                                          lim_min);
+        }
         // rows without a reference have no weights
         if (tid >= (int)round16(post->n_rows)) nm_s[tid] = -INFINITY;
       }
@@ -956,16 +973,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int h = 0; h < 32; ++h) l[h] = 0ull;
       uint32_t pk[32];  // this thread's P, bf16 pairs
 
+      // Which of the nodes of this group's rows see the key of this thread in a
+      // tile of nodes: bit i is that of row h where lim_s[h] = i.  Each lane reads
+      // the bits of the warp's 32 keys in the masks of two nodes, and the warp
+      // turns the 32 x 32 bits around.
+      auto tree_mask = [&](int32_t tile) -> uint64_t {
+        const int32_t pos = tile * kKeys + key;
+        const int32_t base = lim_min, len = post->len, row0 = post->row0;
+        if (post->b < 0 || pos - lane + 31 < base) return pos < base ? ~0ull : 0ull;
+        // the request's first node is that of the token at place len - n_new, which
+        // is base but where the request has fewer own tokens than rows
+        const ReqShape rq = req_shape(L, post->b);
+        const int32_t j0 = pos - lane - (rq.len - rq.n_new);  // node of the warp's first key
+        const int32_t t0 = (row0 + r0) / L.H;
+        const int32_t n_nodes = (row0 + min(post->n_rows, r0 + kGroupRows) - 1) / L.H - t0 + 1;
+        const int32_t w0 = j0 >> 5;
+        uint32_t x[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t lo = 0u, hi = 0u;
+          if (lane + 32 * h < n_nodes) {
+            const int32_t* at = tree.bits + (int64_t)(t0 + lane + 32 * h) * tree.words;
+            if (w0 >= 0 && w0 < tree.words) lo = (uint32_t)ld_input(at + w0);
+            if (w0 + 1 >= 0 && w0 + 1 < tree.words) hi = (uint32_t)ld_input(at + w0 + 1);
+          }
+          x[h] = __funnelshift_r(lo, hi, (uint32_t)j0 & 31u);
+#pragma unroll
+          for (int s = 16; s > 0; s >>= 1) {  // columns and lanes change places
+            const uint32_t low = 0xffffffffu / ((1u << s) + 1u);
+            const uint32_t y = __shfl_xor_sync(0xffffffffu, x[h], s);
+            x[h] = lane & s ? (x[h] & ~low) | ((y & ~low) >> s) : (x[h] & low) | ((y & low) << s);
+          }
+        }
+        const uint64_t m = x[0] | ((uint64_t)x[1] << 32);
+        return pos < base ? ~0ull : pos < len ? m : 0ull;
+      };
+      // whether row h sees the key at `pos`, `m`: its tree mask
+      auto sees = [&](int32_t pos, uint64_t m, int h) {
+        return Tree ? (m >> lim_s[h] & 1ull) != 0ull : pos < lim_min + lim_s[h];
+      };
+
       // The first references, of 16 rows a warp of CTA 0: the maxima over the
       // 32 keys of its lanes in the item's first tile.  Where some row does not
       // see all of that tile, over its first 32 keys, by the first warp of the
       // group: every row that sees a key of the item sees one of those (the
-      // requests' own tokens are taken in order).  CTA 1 counts theirs by bytes.
+      // requests' own tokens are taken in order; a tree's row that sees none of
+      // them stays without a reference until its first key is beyond it).  CTA 1
+      // counts theirs by bytes.
       auto first_refs = [&](int32_t tile, uint32_t b) {
         const int n_rows = post->n_rows;
         if (rank == 0) {
           const bool whole = (tile + 1) * kKeys <= lim_min;  // uniform
           const int32_t pos = tile * kKeys + quad * 32 + lane;
+          const uint64_t tm = Tree && !whole && quad == 0 ? tree_mask(tile) : 0ull;
           const int h_end = min(n_rows, r0 + (whole ? 16 * (quad + 1) : quad ? 0 : kGroupRows));
 #pragma unroll 1
           for (int h0 = r0 + (whole ? 16 * quad : 0); h0 < h_end; h0 += 16) {
@@ -978,7 +1038,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!whole) {
 #pragma unroll
               for (int e = 0; e < 16; ++e)
-                if (pos >= lim_min + lim_s[h0 + e]) x[e] = -INFINITY;
+                if (!sees(pos, tm, h0 + e)) x[e] = -INFINITY;
             }
             // (scores that are not numbers raise no reference: they reach l)
             const float ref = -fmaxf(column_reduce<true>(x, lane), -kUnset);
@@ -997,6 +1057,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // more than the slack become its exact maxima
       auto raise = [&](int32_t tile, uint32_t b) {
         const int32_t pos = tile * kKeys + key;
+        const uint64_t tm = Tree && live ? tree_mask(tile) : 0ull;
 #pragma unroll 1
         for (int h0 = r0; h0 < r0 + kGroupRows; h0 += 16) {
           float x[16];
@@ -1007,7 +1068,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            x[e] = live && pos < lim_min + lim_s[h0 + e] ? __uint_as_float(r[e]) : -INFINITY;
+            x[e] = live && sees(pos, tm, h0 + e) ? __uint_as_float(r[e]) : -INFINITY;
           const float t = column_reduce<true>(x, lane);
           const uint32_t at = (uint32_t)(((int)rank * 4 + quad) * kRows + h0 + lane);
           if (lane < 16) {
@@ -1039,6 +1100,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int32_t pos = tile * kKeys + key;
         const bool masked = !Plain && (tile + 1) * kKeys > lim_min;  // uniform
         const bool seen = !Plain || pos < lim_min;
+        const uint64_t tm = Tree && masked ? tree_mask(tile) : 0ull;
         uint32_t r[2][32];
         const uint32_t tS = tmem + b * kRows + lane_base + r0;
         const ulonglong2* refs2 = reinterpret_cast<const ulonglong2*>(nm_s + r0);
@@ -1068,7 +1130,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (!Plain && masked) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (pos >= lim_min + lim_s[r0 + 32 * h + e]) d[e] = -INFINITY;
+              if (!sees(pos, tm, r0 + 32 * h + e)) d[e] = -INFINITY;
           }
           float top[4];
 #pragma unroll
@@ -1277,7 +1339,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // and l, partial results); 25600 rows, 190 MB: 25 us.
 constexpr int kJoinBlocks = 8;  // of 128 threads on an SM
 
-template <int D, int Lanes>
+template <int D, int Lanes, bool Tree>
 __global__ void __launch_bounds__(128, D == 16 * Lanes ? 6 : kJoinBlocks)
     join_kernel(PlanView view, Lens L, __nv_bfloat16* __restrict__ o, float* __restrict__ lse,
                 int B, int64_t n_rows, int64_t n_slots, float scale, uint32_t* status) {
@@ -1318,9 +1380,10 @@ __global__ void __launch_bounds__(128, D == 16 * Lanes ? 6 : kJoinBlocks)
     const int32_t tiles = x ? r.tiles : plan.prefix_tiles;
     // tiles that hold keys which some row of the block sees
     const int32_t used =
-        x ? (min(r.len, row_limit(r, L.H, min((block + 1) * kRows, r.n_rows) - 1)) + kKeys - 1) /
-                kKeys
-          : tiles;
+        x && !Tree
+            ? (min(r.len, row_limit(r, L.H, min((block + 1) * kRows, r.n_rows) - 1)) + kKeys -
+               1) / kKeys
+            : tiles;
     if (plan.total == 0 || used == 0) continue;
     const int32_t u = x ? block : (int32_t)(row / kRows);
     const int64_t c =
@@ -1395,19 +1458,20 @@ __global__ void __launch_bounds__(128, D == 16 * Lanes ? 6 : kJoinBlocks)
   if (th == 0) lse[row] = none ? -INFINITY : fmaf(m, scale, log2f(l) * kLn2);
 }
 
-template <int D>
+template <int D, bool Tree>
 cudaError_t launch_t(const LaunchCtx& c, const ServeShape& s, const CUtensorMap& qm,
                      const CUtensorMap& km, const CUtensorMap (&vm)[3],
                      const int32_t* prefix_table, int32_t prefix_len, const int32_t* table,
-                     const Lens& L, __nv_bfloat16* o, float* lse, uint8_t* work) {
+                     const Lens& L, const TreeBits& tree, __nv_bfloat16* o, float* lse,
+                     uint8_t* work) {
   using C = PCfg<D>;
   const PlanView view = plan_view(s, work);
   cudaError_t e;
   static std::atomic<uint64_t> prepared{0};  // devices whose kernel has its attribute
   const uint64_t bit = 1ull << (c.device & 63);
   if (!(prepared.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(prefix_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)C::kSmem);
+    e = cudaFuncSetAttribute(prefix_attn_kernel<D, Tree>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
     if (e != cudaSuccess) return e;
     prepared.fetch_or(bit, std::memory_order_relaxed);
   }
@@ -1426,9 +1490,10 @@ cudaError_t launch_t(const LaunchCtx& c, const ServeShape& s, const CUtensorMap&
   cfg.stream = c.stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, prefix_attn_kernel<D>, qm, km, vm[0], vm[1], vm[2], view, L,
+  e = cudaLaunchKernelEx(&cfg, prefix_attn_kernel<D, Tree>, qm, km, vm[0], vm[1], vm[2], view, L,
                          prefix_table, prefix_len, table, s.B, s.T, s.max_blocks, s.page_log2,
-                         (int32_t)s.n_pages, slots, s.scale * kLog2e, c.status, c.timeout_ns);
+                         (int32_t)s.n_pages, slots, s.scale * kLog2e, tree, c.status,
+                         c.timeout_ns);
   if (e != cudaSuccess) return e;
   const int64_t rows = s.T * s.H;
   // D / 4 threads a row while all rows are on the SMs at once (with a warp each a
@@ -1439,8 +1504,8 @@ cudaError_t launch_t(const LaunchCtx& c, const ServeShape& s, const CUtensorMap&
   cfg.gridDim = dim3((unsigned)((rows + per - 1) / per));
   cfg.blockDim = dim3(128);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, wide ? join_kernel<D, D / 4> : join_kernel<D, 32>, view, L, o,
-                            lse, s.B, rows, slots, s.scale, c.status);
+  return cudaLaunchKernelEx(&cfg, wide ? join_kernel<D, D / 4, Tree> : join_kernel<D, 32, Tree>,
+                            view, L, o, lse, s.B, rows, slots, s.scale, c.status);
 }
 
 }  // namespace
@@ -1453,16 +1518,23 @@ cudaError_t launch_prefix_attn(const LaunchCtx& c, const ServeShape& s,
                                const CUtensorMap& q_map, const CUtensorMap& k_map,
                                const CUtensorMap (&v_maps)[3], const int32_t* prefix_table,
                                int64_t prefix_len, const int32_t* table,
-                               const int32_t* seq, const int32_t* cu, __nv_bfloat16* o,
+                               const int32_t* seq, const int32_t* cu,
+                               const uint32_t* tree_bits, int words, __nv_bfloat16* o,
                                float* lse, uint8_t* work) {
+  const TreeBits tree{reinterpret_cast<const int32_t*>(tree_bits), words};
   const Lens L{seq, cu, s.max_blocks << s.page_log2, s.H};
   auto run = [&](auto launch) {
-    return launch(c, s, q_map, k_map, v_maps, prefix_table, (int32_t)prefix_len, table, L, o,
-                  lse, work);
+    return launch(c, s, q_map, k_map, v_maps, prefix_table, (int32_t)prefix_len, table, L, tree,
+                  o, lse, work);
   };
-  if (s.D == 128) return run(launch_t<128>);
-  if (s.D == 256) return run(launch_t<256>);
-  return run(launch_t<512>);
+  if (tree_bits) {
+    if (s.D == 128) return run(launch_t<128, true>);
+    if (s.D == 256) return run(launch_t<256, true>);
+    return run(launch_t<512, true>);
+  }
+  if (s.D == 128) return run(launch_t<128, false>);
+  if (s.D == 256) return run(launch_t<256, false>);
+  return run(launch_t<512, false>);
 }
 
 }  // namespace dsa

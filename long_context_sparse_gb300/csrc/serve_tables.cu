@@ -1,5 +1,6 @@
 // serve_tables.cu -- the paged cache around the shared-prefix attention: page
-// tables and slots from request lengths, and the append of new rows.
+// tables and slots from request lengths, the append of new rows, the masks of
+// drafted trees, and the pages that an eviction leaves free.
 #include "dsa_common.cuh"
 #include "dsa_internal.h"
 
@@ -201,6 +202,105 @@ __global__ void __launch_bounds__(256) append_kernel(
   }
 }
 
+// ----------------------------------------------------------- released pages
+// The other way round: what each request gives back begins behind what the
+// requests before it do, whose sum each block works out itself, as above.
+__global__ void __launch_bounds__(kReq) release_kernel(
+    const int32_t* __restrict__ seq, const int32_t* __restrict__ keep,
+    const int32_t* __restrict__ table, int32_t* __restrict__ new_lens,
+    int32_t* __restrict__ pages, int64_t n_max, int32_t* __restrict__ n_released, int B,
+    int max_blocks, int page_log2, uint32_t* status) {
+  __shared__ int64_t s_first[kReq + 1];
+  __shared__ int32_t s_left[kReq];  // pages that the request keeps
+  __shared__ int64_t red[kReq / 32], wtot[kReq / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int page = 1 << page_log2;
+  const int32_t cap = max_blocks << page_log2;
+  const int b0 = blockIdx.x * kReq;
+  auto lens = [&](int b, int32_t& n, int32_t& left) {
+    n = __ldg(seq + b);
+    const int32_t k = __ldg(keep + b);
+    if (n < 0 || n > cap || k < 0) latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
+    left = k < 0 || n < 0 || n > cap ? n : min(n, k);
+    return n < 0 || n > cap
+               ? 0
+               : (int32_t)(((n + page - 1) >> page_log2) - ((left + page - 1) >> page_log2));
+  };
+  int32_t n, left = 0;
+  int64_t before = 0;
+  for (int b = tid; b < b0; b += kReq) before += lens(b, n, left);
+  before = warp_sum(before);
+  if (lane == 0) red[warp] = before;
+  left = 0;
+  const int64_t mine = b0 + tid < B ? lens(b0 + tid, n, left) : 0;
+  int64_t incl = mine;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const int64_t a = __shfl_up_sync(0xffffffffu, incl, s);
+    if (lane >= s) incl += a;
+  }
+  if (lane == 31) wtot[warp] = incl;
+  __syncthreads();
+  int64_t base = 0;
+#pragma unroll
+  for (int w = 0; w < kReq / 32; ++w) {
+    base += red[w];
+    if (w < warp) incl += wtot[w];
+  }
+  s_first[tid] = base + incl - mine;
+  s_left[tid] = (left + page - 1) >> page_log2;
+  if (tid == kReq - 1) s_first[kReq] = base + incl;
+  __syncthreads();
+  if (blockIdx.y == 0 && b0 + tid < B) new_lens[b0 + tid] = left;
+  if (blockIdx.y == 0 && blockIdx.x == gridDim.x - 1 && tid == 0) {
+    n_released[0] = (int32_t)min(s_first[kReq], (int64_t)INT32_MAX);
+    if (s_first[kReq] > n_max) latch_error(status, DSA_ERR_DEVICE_NO_PAGES);
+  }
+  const int64_t end = min(s_first[kReq], n_max);
+  const int64_t step = (int64_t)gridDim.y * kReq;
+  for (int64_t x = s_first[0] + (int64_t)blockIdx.y * kReq + tid; x < end; x += step) {
+    int lo = 0;
+#pragma unroll
+    for (int s = kReq / 2; s > 0; s >>= 1)
+      if (s_first[lo + s] <= x) lo += s;
+    pages[x] = __ldg(table + (int64_t)(b0 + lo) * max_blocks + s_left[lo] + (x - s_first[lo]));
+  }
+}
+
+// ------------------------------------------------------------- tree masks
+// A thread for each word of a row's mask walks up from the row's node; numbers
+// fall on the way, so it may stop below its word.  The parents come from L1.  A
+// chain is at most 32 * words long, whatever the parents hold.
+__global__ void __launch_bounds__(256) tree_kernel(const int32_t* __restrict__ parents,
+                                                   const int32_t* __restrict__ cu, int words,
+                                                   uint32_t* __restrict__ bits, int B, int64_t T,
+                                                   uint32_t* status) {
+  for (int b = blockIdx.x; b < B; b += gridDim.x) {
+    const int32_t c0 = __ldg(cu + b), c1 = __ldg(cu + b + 1);
+    if (c0 < 0 || c1 < c0 || c1 > T) {
+      if (threadIdx.x == 0) latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
+      continue;
+    }
+    const int32_t n = c1 - c0;
+    if (n > 32 * words && threadIdx.x == 0) latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
+    const int32_t* up = parents + c0;
+    for (int64_t x = threadIdx.x; x < (int64_t)n * words; x += blockDim.x) {
+      const int32_t i = (int32_t)(x / words), lo = (int32_t)(x % words) * 32;
+      uint32_t m = 0u;
+      for (int32_t j = i; j >= lo;) {
+        if (j < lo + 32) m |= 1u << (j - lo);
+        const int32_t p = __ldg(up + j);
+        if (p < -1 || p >= j) {
+          latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
+          break;
+        }
+        j = p;
+      }
+      bits[(int64_t)c0 * words + x] = m;
+    }
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_page_tables(const LaunchCtx& c, const ServeShape& s,
@@ -250,6 +350,31 @@ cudaError_t launch_append(const LaunchCtx& c, const ServeShape& s, const int32_t
   if (s.D == 128) return run(append_kernel<128>);
   if (s.D == 256) return run(append_kernel<256>);
   return run(append_kernel<512>);
+}
+
+cudaError_t launch_build_tree(const LaunchCtx& c, const ServeShape& s, const int32_t* parents,
+                              const int32_t* cu, int words, uint32_t* tree_bits) {
+  const int most = c.num_sms * 8;
+  tree_kernel<<<s.B < most ? s.B : most, 256, 0, c.stream>>>(parents, cu, words, tree_bits, s.B,
+                                                             s.T, c.status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_release_pages(const LaunchCtx& c, const ServeShape& s, const int32_t* seq,
+                                 const int32_t* keep, const int32_t* table,
+                                 int32_t* new_lens, int32_t* pages, int64_t n_max,
+                                 int32_t* n_released) {
+  // a column for each 8 page ids a thread that the block's requests can have
+  const int chunks = (s.B + kReq - 1) / kReq;
+  const int64_t ids = (int64_t)(s.B < kReq ? s.B : kReq) * s.max_blocks;
+  int64_t y = (ids + 8 * kReq - 1) / (8 * kReq);
+  const int64_t most = 4 * (int64_t)c.num_sms / chunks;
+  if (y > most) y = most;
+  if (y < 1) y = 1;
+  release_kernel<<<dim3(chunks, (unsigned)y), kReq, 0, c.stream>>>(
+      seq, keep, table, new_lens, pages, n_max, n_released, s.B, s.max_blocks, s.page_log2,
+      c.status);
+  return cudaGetLastError();
 }
 
 }  // namespace dsa
