@@ -1,88 +1,718 @@
 // key_weights.cu -- what the cached tokens of each request receive of its rows'
-// attention: sums of weights over the rows, one for each key.
+// attention: w[j] = sum over the rows r that see j of exp(scale q_r . k_j - lse_r),
+// on 5th-generation tensor cores by pairs of SMs.
+//
+// Products of a tile of 256 keys, by a cluster of two CTAs (cta_group::2, M = 256),
+// with the keys on the accumulator's lanes and up to 256 (token, head) rows as
+// columns:  S^T[key, row] = K_tile . Q^T.  A thread has one key, so a key's sum
+// over the rows never leaves it: no exchange, no atomics on sums.  Each CTA holds
+// its 128 keys' K, which stay while the request's row blocks come by, and half of
+// each block's Q: 32 KB of Q brought in by each CTA of a pair at d = 512 feed 512
+// cycles of MMAs times 8, where a CTA alone would take in twice as much.
+//
+// Work.  A unit is a key tile against a row block, in order of request, tile, block;
+// units cost what bounds them (K's way from HBM, or the MMAs) and the pairs share
+// the sum evenly.  A tile whose blocks fall to several pairs is joined by the last
+// of them to end, which adds their sums in the order of the pairs, so that results
+// repeat.
+#include <atomic>
+
 #include "attn_common.cuh"
 #include "dsa_internal.h"
+#include "pair_common.cuh"
 
 namespace dsa {
 namespace {
 
-constexpr int kKeys = 32;  // of a block: a warp has four
+constexpr int kTile = 256;          // keys of a pair's tile
+constexpr int kBlock = 256;         // rows of a unit, at most
+constexpr int kMaxPairs = 80;
+constexpr int kEpiWarps = 8;        // 4 TMEM lane quadrants x 2 sets of columns
+constexpr int kProdWarp = 8, kScoutWarp = 9, kMmaWarp = 10;
+constexpr int kThreads = 32 * 11;
+constexpr int kKSlots = 8;          // of 128 keys x 64 dims
+constexpr uint32_t kKBytes = 16384;
+constexpr int kQSlots = 20;         // of 32 rows x 64 dims; a chunk has 1, 2 or 4
+constexpr uint32_t kQBytes = 4096;
+constexpr uint32_t kTail = 4096;
+constexpr uint32_t kSmem = 1024 + kKSlots * kKBytes + kQSlots * kQBytes + kTail;
+constexpr int kBars = 2 * kKSlots + 2 * kQSlots + 8;
+// cost of a tile against few rows, in units of 512 cycles: its K comes from HBM in
+// about 6000 (256 KB at d = 512 and at a pair's share of the rate), while the MMAs of
+// 64 rows take 1024
+constexpr int kTileCost = 12;
 
-template <int D>
-__global__ void __launch_bounds__(256) key_weights_kernel(
-    const __nv_bfloat16* q, const float* lse, const __nv_bfloat16* k, const int32_t* table,
-    const int32_t* seq, const int32_t* cu, const int32_t* tree_bits, int words, const float* w,
-    float decay, float* w_out, int H, int64_t T, int max_blocks, int page_log2, int64_t n_pages,
-    int tiles, float scale, uint32_t* status) {
-  constexpr int kPer = D / 32;
-  const int b = blockIdx.x / tiles, tile = blockIdx.x % tiles;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int32_t c0 = cu[b], c1 = cu[b + 1], n = seq[b], cap = max_blocks << page_log2;
-  if (c0 < 0 || c1 < c0 || c1 > T || n < 0 || n > cap) {
-    if (threadIdx.x == 0) latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
-    return;
-  }
-  const int32_t n_new = c1 - c0, base = n - n_new;
-  if (n_new == 0) return;
-  for (int x = 0; x < kKeys / 8; ++x) {
-    const int32_t j = tile * kKeys + warp * (kKeys / 8) + x;
-    if (j >= n) return;
-    const int32_t p = table[(int64_t)b * max_blocks + (j >> page_log2)];
-    if (p < 0 || p >= n_pages) {
-      latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
-      continue;
+// What the issuer is to do with a chunk: K slot << 12, Q slot << 24, Q slots << 8,
+// accumulator << 16, and
+constexpr uint32_t kGo = 1, kFirst = 2, kLast = 4, kFreeK = 8, kFreeQ = 16;
+
+// Counters of the pairs that have ended with a tile that began in pair p: a byte
+// each for the two CTAs, in the workspace header behind the status word.  0 between
+// calls.
+static_assert(64 + 2 * kMaxPairs <= (int)kHeader, "counters");
+
+struct Args {
+  const float* lse;
+  const int32_t *table, *seq, *cu;
+  const int32_t* bits;  // or nullptr
+  int words;
+  const float* w;
+  float* w_out;
+  float* parts;       // [pair][rank][head, tail][128]
+  uint32_t* counters;
+  float decay, scale;
+  int B, H, max_blocks, page_log2;
+  int64_t T, n_pages;
+  uint32_t* status;
+  uint64_t timeout_ns;
+};
+
+struct Req {
+  int32_t row0, rows;  // first row (token * H), rows
+  int32_t len, base;   // own tokens; place of the step's first
+  int32_t tiles, blocks;
+  int32_t cost;        // of a unit
+};
+
+__device__ __forceinline__ Req load_req(const Args& a, int b) {
+  const int32_t c0 = ld_input(a.cu + b), c1 = ld_input(a.cu + b + 1);
+  int32_t len = ld_input(a.seq + b);
+  if (len < 0 || len > a.max_blocks << a.page_log2) len = 0;  // latched by CTA 0
+  Req r;
+  r.row0 = c0 * a.H;
+  r.rows = (c1 - c0) * a.H;
+  r.len = len;
+  r.base = len - (c1 - c0);
+  r.tiles = r.rows > 0 ? (len + kTile - 1) / kTile : 0;
+  r.blocks = (r.rows + kBlock - 1) / kBlock;
+  const int32_t n64 = (r.rows + 63) / 64;
+  r.cost = r.blocks ? (max(kTileCost, 2 * n64) + r.blocks - 1) / r.blocks : 1;
+  return r;
+}
+__device__ __forceinline__ int64_t units_of(const Req& r) {
+  return (int64_t)r.tiles * r.blocks;
+}
+__device__ __forceinline__ int64_t ceil_div(int64_t x, int64_t y) {
+  return ((x | y) >> 31) == 0 ? (int64_t)(((uint32_t)x + (uint32_t)y - 1u) / (uint32_t)y)
+                              : (x + y - 1) / y;
+}
+
+// The units of one pair's share [start, end) of the cost, in order: those whose cost
+// begins there.  A whole warp, in step.
+struct Walk {
+  int64_t start, end, cb;  // cb: cost before request b
+  int64_t left;            // units of request b still to come
+  int32_t b, tile, block;
+  bool first;              // no unit of request b so far
+  Req r;
+
+  __device__ __forceinline__ void begin(const Args& a, int64_t s, int64_t e, int64_t c, int b0) {
+    start = s;
+    end = e;
+    cb = c;
+    b = b0;
+    left = 0;
+    first = true;
+    tile = block = 0;
+    r = Req{};
+    r.cost = 1;
+    if (s >= e) {
+      end = cb = 0;
+      return;
     }
-    const int64_t slot = ((int64_t)p << page_log2) + (j & ((1 << page_log2) - 1));
-    float key[kPer];
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) key[e] = __bfloat162float(k[slot * D + e * 32 + lane]);
-    float sum = 0.f;
-    for (int32_t i = 0; i < n_new; ++i) {
-      const int32_t node = j - base;
-      const bool sees =
-          node < 0 ||
-          (tree_bits ? node < 32 * words &&
-                           (tree_bits[(int64_t)(c0 + i) * words + (node >> 5)] >> (node & 31) & 1)
-                     : node <= i);
-      if (!sees) continue;
-      for (int h = 0; h < H; ++h) {
-        const int64_t r = (int64_t)(c0 + i) * H + h;
-        const float l = lse[r];
-        if (l == -INFINITY) continue;
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e)
-          s = fmaf(key[e], __bfloat162float(q[r * D + e * 32 + lane]), s);
-#pragma unroll
-        for (int y = 16; y > 0; y >>= 1) s += __shfl_xor_sync(0xffffffffu, s, y);
-        sum += expf(s * scale - l);
+    r = load_req(a, b);
+    const int64_t u0 = s > cb ? ceil_div(s - cb, r.cost) : 0;
+    left = min(units_of(r), ceil_div(end - cb, r.cost)) - u0;
+    if (left < 0) left = 0;
+    if (r.blocks > 0) {
+      tile = (int32_t)(u0 / r.blocks);
+      block = (int32_t)(u0 - (int64_t)tile * r.blocks) - 1;  // next() goes one on
+      if (block < 0) {
+        block = r.blocks - 1;
+        --tile;
       }
     }
-    if (lane == 0) w_out[slot] = (j < base ? decay * w[slot] : 0.f) + sum;
   }
+  __device__ __forceinline__ bool next(const Args& a) {
+    if (left > 0) {
+      if (++block == r.blocks) {
+        block = 0;
+        ++tile;
+      }
+      --left;
+      return true;
+    }
+    cb += units_of(r) * r.cost;
+    if (cb >= end) return false;
+    // the next request with units; idle ones are passed 32 at a time
+    uint32_t some = 0;
+    while (!some && ++b < a.B) {
+      const int x = b + (int)(threadIdx.x & 31);
+      some = __ballot_sync(0xffffffffu, x < a.B && units_of(load_req(a, x)) > 0);
+      b += some ? __ffs(some) - 1 : 31;
+    }
+    if (!some) return false;
+    r = load_req(a, b);
+    left = min(units_of(r), ceil_div(end - cb, r.cost)) - 1;
+    tile = block = 0;
+    first = true;
+    return true;
+  }
+  // rows of the unit, and the columns that they take
+  __device__ __forceinline__ int32_t rows() const { return min(kBlock, r.rows - block * kBlock); }
+  __device__ __forceinline__ int32_t slots() const {
+    const int32_t n = rows();
+    return n <= 64 ? 1 : n <= 128 ? 2 : 4;
+  }
+  // Q stays for all tiles of the request where it has one block and that fits
+  template <int D>
+  __device__ __forceinline__ bool q_stays() const {
+    return r.blocks == 1 && slots() * (D / 64) <= kQSlots;
+  }
+  // no row of the block sees a key of the tile
+  __device__ __forceinline__ bool dead(const Args& a) const {
+    return !a.bits && tile * kTile > r.base + (block * kBlock + rows() - 1) / a.H;
+  }
+  __device__ __forceinline__ bool tile_ends() const { return block == r.blocks - 1 || left == 0; }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(is));
+  return is != 0;
+}
+template <int D>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    key_weights_kernel(const __grid_constant__ CUtensorMap q_map,
+                       const __grid_constant__ CUtensorMap k_map, const Args a) {
+  constexpr int kChunks = D / 64;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sK = (raw + 1023u) & ~1023u;
+  const uint32_t sQ = sK + kKSlots * kKBytes;
+  uint8_t* tail = smem_raw + (sK - raw) + kKSlots * kKBytes + kQSlots * kQBytes;
+  float* neg_s = reinterpret_cast<float*>(tail);        // [unit & 1][column] -lse
+  float* red = neg_s + 2 * kBlock;                       // [key] the other columns' sums
+  uint32_t* live_s = reinterpret_cast<uint32_t*>(red + 128);  // [unit & 1][8] columns that count
+  uint64_t* bars = reinterpret_cast<uint64_t*>(live_s + 16);
+  uint32_t* misc = reinterpret_cast<uint32_t*>(bars + kBars);  // abort, tmem, joins
+  volatile uint32_t* cmd = misc + 4;                           // [chunk & 1], see the scout
+  int64_t* scratch = reinterpret_cast<int64_t*>(misc + 6);    // [16], then the share
+  static_assert((2 * kBlock + 128 + 16) * 4 + kBars * 8 + 24 + 24 * 8 <= kTail, "tail");
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const uint32_t rank = cluster_rank(), peer = rank ^ 1u;
+  const uint32_t bar0 = smem_u32(bars);
+  auto k_full = [&](uint32_t s) { return bar0 + 8u * s; };               // leader: both landed
+  auto k_empty = [&](uint32_t s) { return bar0 + 8u * (kKSlots + s); };
+  auto q_full = [&](uint32_t s) { return bar0 + 8u * (2 * kKSlots + s); };  // leader
+  auto q_empty = [&](uint32_t s) { return bar0 + 8u * (2 * kKSlots + kQSlots + s); };
+  const uint32_t bx = bar0 + 8u * (2 * kKSlots + 2 * kQSlots);
+  auto s_full = [&](uint32_t u) { return bx + 8u * (u & 1u); };
+  auto s_empty = [&](uint32_t u) { return bx + 16 + 8u * (u & 1u); };    // leader
+  const uint32_t epi = bx + 32, done_bar = bx + 40;
+  const PairWaiter W{misc, at_rank(smem_u32(misc), peer), a.status, a.timeout_ns};
+
+  if (tid == 0) {
+    for (uint32_t s = 0; s < kKSlots; ++s) {
+      mbar_init(k_full(s), 1);
+      mbar_init(k_empty(s), 1);
+    }
+    for (uint32_t s = 0; s < kQSlots; ++s) {
+      mbar_init(q_full(s), 1);
+      mbar_init(q_empty(s), 1);
+    }
+    for (uint32_t u = 0; u < 2; ++u) {
+      mbar_init(s_full(u), 1);
+      mbar_init(s_empty(u), 2 * kEpiWarps);
+    }
+    mbar_init(epi, kEpiWarps);
+    mbar_init(done_bar, 1);
+    misc[0] = 0u;
+    fence_mbar_init();
+    prefetch_tensormap(&q_map);
+    prefetch_tensormap(&k_map);
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(misc + 1)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_arrive();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // ---- this pair's share of the cost, and the request where it begins
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  int64_t total = 0;
+  {
+    const int32_t last = ld_input(a.cu + a.B);
+    int bad = ld_input(a.cu) < 0 || last > a.T;
+    for (int b = tid; b < a.B; b += kThreads) {
+      const Req r = load_req(a, b);
+      bad |= r.rows < 0;
+      total += units_of(r) * r.cost;
+      if (blockIdx.x == 0) {
+        const int32_t n = ld_input(a.seq + b);
+        if (n < 0 || n > a.max_blocks << a.page_log2)
+          latch_error(a.status, DSA_ERR_DEVICE_BAD_INDEX);
+      }
+    }
+    total = warp_sum(total);
+    if (lane == 0) scratch[warp] = total;
+    bad = __syncthreads_or(bad);
+    total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) total += scratch[w];
+    if (bad) {  // offsets that do not ascend within [0, T]: nothing is computed
+      total = 0;
+      if (blockIdx.x == 0 && tid == 0) latch_error(a.status, DSA_ERR_DEVICE_BAD_INDEX);
+    }
+  }
+  // (a share of a unit's cost at least: then the pairs of a tile have no gap)
+  const int64_t chunk = max(ceil_div(total, pairs), (int64_t)kTileCost);
+  const int64_t start = min(total, pair * chunk), end = min(total, start + chunk);
+  int64_t* share = scratch + 16;  // cost before the request, its number
+  {
+    int64_t c = 0;
+    for (int b0 = 0; b0 < a.B && start < end && c <= start; b0 += kThreads) {
+      const int b = b0 + tid;
+      int64_t mine = 0;
+      if (b < a.B) {
+        const Req r = load_req(a, b);
+        mine = units_of(r) * r.cost;
+      }
+      int64_t incl = mine;
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, incl, s);
+        if (lane >= s) incl += x;
+      }
+      __syncthreads();
+      if (lane == 31) scratch[warp] = incl;
+      __syncthreads();
+      int64_t all = 0;
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w == warp) incl += all;
+        all += scratch[w];
+      }
+      const int64_t c0 = c + incl - mine;
+      if (c0 <= start && start < c0 + mine) {
+        share[0] = c0;
+        share[1] = b;
+      }
+      c += all;
+    }
+  }
+  __syncthreads();
+  cluster_wait();
+  tc_fence_after();
+  constexpr uint32_t tmem = 0;  // an allocation of all 512 columns starts at column 0
+  Walk walk;
+  walk.begin(a, start, end, start < end ? share[0] : 0, start < end ? (int)share[1] : 0);
+
+  if (warp == kProdWarp) {
+    // ====================================================== TMA producer
+    const int page = 1 << a.page_log2, nb = 128 >> a.page_log2;  // page boxes of a chunk
+    const int32_t n_rows_cache = (int32_t)(a.n_pages << a.page_log2);  // out of range: zeros
+    const bool arms = rank == 0 && lane == 0;
+    const uint32_t lead = at_rank(bar0, 0);
+    uint32_t kc = 0, qs = 0, q_phase = 0;  // K chunks so far; next Q slot; phases used up
+    bool ok = true, any = false, k_here = false;
+    while (ok && walk.next(a)) {
+      if (walk.block == 0 || walk.first) k_here = false;
+      const bool load_q = !walk.q_stays<D>() || walk.first;
+      walk.first = false;
+      if (walk.dead(a)) continue;
+      any = true;
+      int32_t k_row = n_rows_cache;
+      if (!k_here) {
+        const int32_t pos = walk.tile * kTile + (int)rank * 128 + lane * page;
+        if (lane < nb && pos < walk.r.len) {
+          const int32_t p =
+              ld_input(a.table + (int64_t)walk.b * a.max_blocks + (pos >> a.page_log2));
+          if (p < 0 || p >= a.n_pages) latch_error(a.status, DSA_ERR_DEVICE_BAD_INDEX);
+          else k_row = p << a.page_log2;
+        }
+      }
+      const int n = walk.slots();
+      qs = (qs + n - 1) / n * n;
+      if (qs == kQSlots) qs = 0;
+      const int32_t q_row = walk.r.row0 + walk.block * kBlock + (int)rank * 32 * n + 32 * lane;
+#pragma unroll 1
+      for (int c = 0; c < kChunks && ok; ++c) {
+        if (!k_here) {
+          const uint32_t s = kc % kKSlots;
+          if (!(ok = W.wait(k_empty(s), ((kc / kKSlots) & 1u) ^ 1u))) break;
+          if (arms) mbar_expect_tx(k_full(s), 2 * kKBytes);
+          __syncwarp();
+          if (lane < nb)
+            tma_load_pair(sK + s * kKBytes + (uint32_t)(lane * page) * 128u, &k_map, c * 64, k_row,
+                          lead + 8u * s);
+          ++kc;
+        }
+        if (load_q) {
+          for (int i = 0; i < n && ok; ++i) {
+            ok = W.wait(q_empty(qs + i), ((q_phase >> (qs + i)) & 1u) ^ 1u);
+            if (ok && arms) mbar_expect_tx(q_full(qs + i), 2 * kQBytes);
+          }
+          if (!ok) break;
+          __syncwarp();
+          if (lane < n)
+            tma_load_pair(sQ + (qs + lane) * kQBytes, &q_map, c * 64, q_row,
+                          lead + 8u * (2 * kKSlots + qs + lane));
+          q_phase ^= ((1u << n) - 1u) << qs;
+          qs += n;
+          if (qs == kQSlots) qs = 0;
+        }
+      }
+      k_here = true;
+    }
+    // the leader's last arrival here is done_bar's: the CTA outlives it
+    if (ok && rank != 0 && any) W.wait(done_bar, 0);
+  } else if (warp == kScoutWarp && rank == 0) {
+    // ====== scout: waits for the issuer's operands and lets it in, a chunk at a
+    // time (a wait of the issuer's own would queue behind its MMAs), with a word that
+    // says what to issue.  When a wait gives up it lets the issuer through what is
+    // left, on whatever is there.
+    uint32_t kc = 0, qs = 0, q0 = 0, q_phase = 0, nu = 0, n_bar = 0;
+    bool ok = true, k_here = false;
+    auto let_in = [&](uint32_t word) {
+      if (lane == 0) cmd[n_bar & 1u] = word;
+      __syncwarp();
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + (n_bar & 1u)) : "memory");
+      ++n_bar;
+    };
+    while (walk.next(a)) {
+      if (walk.block == 0 || walk.first) k_here = false;
+      const bool stays = walk.q_stays<D>(), load_q = !stays || walk.first;
+      walk.first = false;
+      if (walk.dead(a)) continue;
+      const int n = walk.slots();
+      qs = (qs + n - 1) / n * n;
+      if (qs == kQSlots) qs = 0;
+      if (load_q) q0 = qs;
+      if (!k_here) kc += kChunks;
+      const uint32_t flags = (walk.tile_ends() ? kFreeK : 0u) |
+                             (!stays || walk.left == 0 ? kFreeQ : 0u) | (uint32_t)n << 8 |
+                             (nu & 1u) << 16;
+      if (ok) ok = W.wait(s_empty(nu), ((nu >> 1) & 1u) ^ 1u);
+      uint32_t q = q0;
+      for (uint32_t c = 0; c < kChunks; ++c) {
+        const uint32_t x = kc - kChunks + c;
+        if (!k_here && ok) ok = W.wait(k_full(x % kKSlots), (x / kKSlots) & 1u);
+        if (load_q) {
+          for (int i = 0; i < n; ++i)
+            if (ok) ok = W.wait(q_full(q + i), (q_phase >> (q + i)) & 1u);
+          q_phase ^= ((1u << n) - 1u) << q;
+        }
+        let_in(flags | kGo | (c == 0 ? kFirst : 0u) | (c == kChunks - 1 ? kLast : 0u) |
+               (x % kKSlots) << 12 | q << 24);
+        q += n;
+        if (q == kQSlots) q = 0;
+      }
+      if (load_q) qs = q;
+      k_here = true;
+      ++nu;
+    }
+    let_in(0u);
+  } else if (warp == kMmaWarp && rank == 0) {
+    // ========================================== MMA issuer (leader only)
+    const uint32_t dK = (uint32_t)sdesc_sw128(sK, 16, 1024);
+    const uint32_t dQ = (uint32_t)sdesc_sw128(sQ, 16, 1024);
+    const uint32_t hi = (uint32_t)(sdesc_sw128(0, 16, 1024) >> 32);
+    bool any = false;
+    for (uint32_t n_bar = 0;; ++n_bar) {
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + (n_bar & 1u)) : "memory");
+      const uint32_t word = cmd[n_bar & 1u];
+      if (word == 0u) break;
+      any = true;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t n = (word >> 8) & 15u, s = (word >> 12) & 15u, u = (word >> 16) & 1u;
+        const uint32_t q = word >> 24, d = tmem + u * kBlock;
+        const uint32_t idesc = idesc_bf16(256, 0, 0, 0) | (64 * n) >> 3 << 17;
+        const uint32_t da = dK + s * (kKBytes >> 4), db = dQ + q * (kQBytes >> 4);
+        tc_mma2(d, da, db, hi, idesc, word & kFirst ? 0u : 1u);
+#pragma unroll
+        for (uint32_t x = 1; x < 4; ++x) tc_mma2(d, da + 2 * x, db + 2 * x, hi, idesc, 1u);
+        if (word & kFreeK) tc_commit2(k_empty(s));
+        if (word & kFreeQ)
+          for (uint32_t i = 0; i < n; ++i) tc_commit2(q_empty(q + i));
+        if (word & kLast) tc_commit2(s_full(u));
+      }
+      __syncwarp();
+    }
+    if (any) {
+      if (elect_one()) tc_commit2(done_bar);
+      __syncwarp();
+      drain(done_bar, 0, a.timeout_ns);
+    }
+  } else if (warp < kEpiWarps) {
+    // ======================================================== epilogue
+    const int quad = warp & 3, g = warp >> 2;  // TMEM lanes, every second set of 32 columns
+    const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+    const uint64_t scale2 = pair2(a.scale, a.scale), log2e2 = pair2(kLog2e, kLog2e);
+    uint32_t nu = 0, ns = 0;
+    auto epi_sync = [&]() {  // all epilogue warps of this CTA
+      __syncwarp();
+      if (lane == 0) mbar_arrive(epi);
+      return W.wait(epi, ns++ & 1u);
+    };
+    bool ok = true, head = false;
+    uint64_t sum[2] = {0ull, 0ull};
+    while (ok && walk.next(a)) {
+      if (walk.block == 0 || walk.first) {
+        head = walk.block != 0;  // the tile began in a pair before
+        sum[0] = sum[1] = 0ull;
+      }
+      walk.first = false;
+      const int32_t pos0 = walk.tile * kTile + (int)rank * 128 + quad * 32, pos = pos0 + lane;
+      if (!walk.dead(a)) {
+        const int32_t n = walk.rows(), at = walk.block * kBlock;
+        float* neg = neg_s + (nu & 1u) * kBlock;
+        {
+          const float l = tid < n ? __int_as_float(ld_input(reinterpret_cast<const int32_t*>(
+                                        a.lse + walk.r.row0 + at + tid)))
+                                  : -INFINITY;
+          neg[tid] = -l;
+          const uint32_t live = __ballot_sync(0xffffffffu, l != -INFINITY);
+          if (lane == 0) live_s[(nu & 1u) * 8 + warp] = live;
+        }
+        if (!(ok = epi_sync())) break;
+        if (!(ok = W.wait(s_full(nu), (nu >> 1) & 1u))) break;
+        tc_fence_after();
+        const int32_t first = pos - walk.r.base;  // node, or first token that sees the key
+        const bool all_see = pos0 + 31 < walk.r.base || (!a.bits && pos0 + 31 <= walk.r.base);
+        const uint32_t tS = tmem + (nu & 1u) * kBlock + lane_base;
+        const int sets = (n + 31) >> 5;
+#pragma unroll 1
+        for (int q = g; q < sets; q += 2) {
+          uint32_t s[2][16];
+          tmem_ld16(tS + 32 * q, s[0]);
+          tmem_ld16(tS + 32 * q + 16, s[1]);
+          uint32_t mask = live_s[(nu & 1u) * 8 + q];
+          if (!all_see) {
+            const int32_t r0 = at + 32 * q;  // the set's first row, from the request's
+            if (!a.bits) {
+              // rows from (pos - base) H on
+              const int64_t skip = (int64_t)first * a.H - r0;
+              if (skip > 0) mask = skip >= 32 ? 0u : mask & (0xffffffffu << skip);
+            } else {
+              // lane l reads row r0 + l's bits of the warp's 32 keys; then the 32 x 32
+              // bits are turned around
+              const int32_t j0 = pos0 - walk.r.base, w0 = j0 >> 5;
+              uint32_t lo = 0u, hi = 0u;
+              if (32 * q + lane < n) {
+                const int32_t* bits =
+                    a.bits + (int64_t)((walk.r.row0 + r0 + lane) / a.H) * a.words;
+                if (w0 >= 0 && w0 < a.words) lo = (uint32_t)ld_input(bits + w0);
+                if (w0 + 1 >= 0 && w0 + 1 < a.words) hi = (uint32_t)ld_input(bits + w0 + 1);
+              }
+              uint32_t x = __funnelshift_r(lo, hi, (uint32_t)j0 & 31u);
+#pragma unroll
+              for (int y = 16; y > 0; y >>= 1) {
+                const uint32_t low = 0xffffffffu / ((1u << y) + 1u);
+                const uint32_t o = __shfl_xor_sync(0xffffffffu, x, y);
+                x = lane & y ? (x & ~low) | ((o & ~low) >> y) : (x & low) | ((o & low) << y);
+              }
+              if (first >= 0) mask &= x;
+            }
+          }
+          const bool plain = __all_sync(0xffffffffu, mask == 0xffffffffu);
+          const ulonglong2* neg2 = reinterpret_cast<const ulonglong2*>(neg + 32 * q);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            tmem_wait_ld_dep(s[h]);
+            uint64_t y[8];
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+              const ulonglong2 l = neg2[4 * h + e / 2];
+              y[e] = fma2(pair2(__uint_as_float(s[h][2 * e]), __uint_as_float(s[h][2 * e + 1])),
+                          scale2, l.x);
+              y[e + 1] =
+                  fma2(pair2(__uint_as_float(s[h][2 * e + 2]), __uint_as_float(s[h][2 * e + 3])),
+                       scale2, l.y);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              float p0, p1;
+              unpair2(mul2(y[e], log2e2), p0, p1);
+              p0 = ex2(p0);
+              p1 = ex2(p1);
+              if (!plain) {
+                if (!(mask >> (16 * h + 2 * e) & 1u)) p0 = 0.f;
+                if (!(mask >> (16 * h + 2 * e + 1) & 1u)) p1 = 0.f;
+              }
+              sum[e & 1] = add2(sum[e & 1], pair2(p0, p1));
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_signal(at_rank(s_empty(nu), 0));
+        ++nu;
+      }
+      if (!walk.tile_ends()) continue;
+      // ---- this CTA's part of the tile is done
+      float lo, hi, v;
+      unpair2(add2(sum[0], sum[1]), lo, hi);
+      v = lo + hi;
+      if (g == 1) red[quad * 32 + lane] = v;
+      if (!(ok = epi_sync())) break;
+      if (g == 0) v += red[quad * 32 + lane];
+      const bool whole = !head && walk.block == walk.r.blocks - 1;
+      bool mine = g == 0;
+      if (!whole) {
+        // the pairs that have a unit of the tile, and this one's sums for the others
+        const int64_t c0 = walk.cb + (int64_t)walk.tile * walk.r.blocks * walk.r.cost;
+        const int from = (int)(c0 / chunk);
+        const int to = (int)((c0 + (int64_t)(walk.r.blocks - 1) * walk.r.cost) / chunk);
+        auto part = [&](int p) {
+          return a.parts + (((int64_t)p * 2 + rank) * 2 + (p == from ? 1 : 0)) * 128 + quad * 32 +
+                 lane;
+        };
+        if (g == 0) __stcg(part(pair), v);
+        __threadfence();
+        if (!(ok = epi_sync())) break;
+        if (tid == 0) {
+          const int at = from * 2 + (int)rank, shift = 8 * (at & 3);
+          const uint32_t old = atomicAdd(a.counters + (at >> 2), 1u << shift);
+          const bool last = ((old >> shift) & 255u) == (uint32_t)(to - from);
+          if (last) atomicSub(a.counters + (at >> 2), (uint32_t)(to - from + 1) << shift);
+          __threadfence();
+          misc[2] = last ? 1u : 0u;
+        }
+        if (!(ok = epi_sync())) break;
+        mine = mine && misc[2] != 0u;
+        if (mine) {
+          v = 0.f;
+          for (int p = from; p <= to; ++p) v += __ldcg(part(p));
+        }
+      }
+      if (mine && pos < walk.r.len) {
+        const int32_t p = ld_input(a.table + (int64_t)walk.b * a.max_blocks + (pos >> a.page_log2));
+        if (p >= 0 && p < a.n_pages) {
+          const int64_t slot =
+              ((int64_t)p << a.page_log2) + (pos & ((1 << a.page_log2) - 1));
+          if (pos < walk.r.base)
+            v = fmaf(a.decay, __int_as_float(ld_input(reinterpret_cast<const int32_t*>(a.w + slot))),
+                     v);
+          a.w_out[slot] = v;
+        }
+      }
+      if (!(ok = epi_sync())) break;  // red and misc may be written again
+      sum[0] = sum[1] = 0ull;
+    }
+  }
+
+  // ---- teardown: after a wait that gave up, copies may be in flight to either CTA:
+  // they get 2 ms to land before the CTAs go
+  if (tid == 0 && *W.abort_flag) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 2000000u) __nanosleep(100000);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_arrive();
+  cluster_wait();
+  tc_fence_after();
+  if (warp == kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
+                 : "memory");
+}
+
+template <int D>
+cudaError_t launch_t(const LaunchCtx& c, const CUtensorMap& qm, const CUtensorMap& km,
+                     const Args& a) {
+  static std::atomic<uint64_t> prepared{0};
+  const uint64_t bit = 1ull << (c.device & 63);
+  if (!(prepared.load(std::memory_order_relaxed) & bit)) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        key_weights_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e != cudaSuccess) return e;
+    prepared.fetch_or(bit, std::memory_order_relaxed);
+  }
+  const int pairs = c.num_sms / 2 < kMaxPairs ? c.num_sms / 2 : kMaxPairs;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * pairs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = c.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, key_weights_kernel<D>, qm, km, a);
 }
 
 }  // namespace
 
-size_t key_weights_ws(const ServeShape&) { return 0; }
+size_t key_weights_ws(const ServeShape&) { return (size_t)kMaxPairs * 2 * 2 * 128 * 4; }
 
-cudaError_t launch_key_weights(const LaunchCtx& c, const ServeShape& s, const CUtensorMap&,
-                               const CUtensorMap&, const __nv_bfloat16* q, const float* lse,
-                               const __nv_bfloat16* k_pages, const int32_t* table,
-                               const int32_t* seq, const int32_t* cu,
-                               const uint32_t* tree_bits, int words, const float* w_pages,
-                               float decay, float* w_out, uint8_t*) {
-  const int tiles = (s.max_blocks * s.page + kKeys - 1) / kKeys;
-  auto run = [&](auto kern) {
-    kern<<<(unsigned)(s.B * tiles), 256, 0, c.stream>>>(
-        q, lse, k_pages, table, seq, cu, reinterpret_cast<const int32_t*>(tree_bits), words,
-        w_pages, decay, w_out, s.H, s.T, s.max_blocks, s.page_log2, s.n_pages, tiles, s.scale,
-        c.status);
-    return cudaGetLastError();
-  };
-  if (s.D == 128) return run(key_weights_kernel<128>);
-  if (s.D == 256) return run(key_weights_kernel<256>);
-  return run(key_weights_kernel<512>);
+cudaError_t launch_key_weights(const LaunchCtx& c, const ServeShape& s,
+                               const CUtensorMap& q_map, const CUtensorMap& k_map,
+                               const float* lse, const int32_t* table, const int32_t* seq,
+                               const int32_t* cu, const uint32_t* tree_bits, int words,
+                               const float* w_pages, float decay, float* w_out, uint8_t* ws) {
+  Args a;
+  a.lse = lse;
+  a.table = table;
+  a.seq = seq;
+  a.cu = cu;
+  a.bits = reinterpret_cast<const int32_t*>(tree_bits);
+  a.words = words;
+  a.w = w_pages;
+  a.w_out = w_out;
+  a.parts = reinterpret_cast<float*>(ws + kHeader);
+  a.counters = reinterpret_cast<uint32_t*>(ws + 64);
+  a.decay = decay;
+  a.scale = s.scale;
+  a.B = s.B;
+  a.H = s.H;
+  a.max_blocks = s.max_blocks;
+  a.page_log2 = s.page_log2;
+  a.T = s.T;
+  a.n_pages = s.n_pages;
+  a.status = c.status;
+  a.timeout_ns = c.timeout_ns;
+  if (s.D == 128) return launch_t<128>(c, q_map, k_map, a);
+  if (s.D == 256) return launch_t<256>(c, q_map, k_map, a);
+  return launch_t<512>(c, q_map, k_map, a);
 }
 
 }  // namespace dsa

@@ -272,13 +272,11 @@ dsa_status_t dsa_key_weights(const dsa_serve_config_t* cfg, const void* q, const
   const ServeShape sh = serve_shape(cfg);
   CUtensorMap qm, km;
   const uint64_t d = (uint64_t)sh.D;
-  if ((st = encode_2d(&qm, q, (uint64_t)rows, d, 64)) != DSA_OK) return st;
+  if ((st = encode_2d(&qm, q, (uint64_t)rows, d, 32)) != DSA_OK) return st;
   if ((st = encode_2d(&km, k_pages, (uint64_t)slots, d, (uint32_t)sh.page)) != DSA_OK) return st;
-  return cuda_status(launch_key_weights(ctx, sh, qm, km, static_cast<const __nv_bfloat16*>(q),
-                                        lse, static_cast<const __nv_bfloat16*>(k_pages),
-                                        block_table, seq_lens, cu_tokens, tree_bits, words,
-                                        w_pages, decay, w_out,
-                                        static_cast<uint8_t*>(ws) + kHeader));
+  return cuda_status(launch_key_weights(ctx, sh, qm, km, lse, block_table, seq_lens, cu_tokens,
+                                        tree_bits, words, w_pages, decay, w_out,
+                                        static_cast<uint8_t*>(ws)));
 }
 
 dsa_status_t dsa_evict_cache(const dsa_serve_config_t* cfg, const float* w_pages,
