@@ -189,11 +189,11 @@ cudaError_t launch_prefix_attn(const LaunchCtx& c, const ServeShape& s,
 cudaError_t launch_build_tree(const LaunchCtx& c, const ServeShape& s, const int32_t* parents,
                               const int32_t* cu, int words, uint32_t* tree_bits);
 
-// Weights that cached tokens receive; q_map: q as [T * H, D], box {64, 32}; k_map:
-// the cache as [n_pages * page, D], box {64, page}; ws: the whole workspace.
+// Weights that cached tokens receive; q_maps: q as [T * H, D], boxes {64, 32}, {64, 64}
+// and {64, 128}; k_map: the cache as [n_pages * page, D], box {64, page}; ws: the whole workspace.
 size_t key_weights_ws(const ServeShape& s);
 cudaError_t launch_key_weights(const LaunchCtx& c, const ServeShape& s,
-                               const CUtensorMap& q_map, const CUtensorMap& k_map,
+                               const CUtensorMap (&q_maps)[3], const CUtensorMap& k_map,
                                const float* lse, const int32_t* table, const int32_t* seq,
                                const int32_t* cu, const uint32_t* tree_bits, int words,
                                const float* w_pages, float decay, float* w_out, uint8_t* ws);

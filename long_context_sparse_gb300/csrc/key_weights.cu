@@ -28,22 +28,22 @@ constexpr int kTile = 256;          // keys of a pair's tile
 constexpr int kBlock = 256;         // rows of a unit, at most
 constexpr int kMaxPairs = 80;
 constexpr int kEpiWarps = 8;        // 4 TMEM lane quadrants x 2 sets of columns
-constexpr int kProdWarp = 8, kScoutWarp = 9, kMmaWarp = 10;
-constexpr int kThreads = 32 * 11;
+constexpr int kKWarp = 8, kScoutWarp = 9, kMmaWarp = 10, kQWarp = 11;
+constexpr int kThreads = 32 * 12;
 constexpr int kKSlots = 8;          // of 128 keys x 64 dims
 constexpr uint32_t kKBytes = 16384;
-constexpr int kQSlots = 20;         // of 32 rows x 64 dims; a chunk has 1, 2 or 4
+constexpr int kQParts = 20;         // of 32 rows x 64 dims; a chunk's slot has 1, 2 or 4
 constexpr uint32_t kQBytes = 4096;
 constexpr uint32_t kTail = 4096;
-constexpr uint32_t kSmem = 1024 + kKSlots * kKBytes + kQSlots * kQBytes + kTail;
-constexpr int kBars = 2 * kKSlots + 2 * kQSlots + 8;
+constexpr uint32_t kSmem = 1024 + kKSlots * kKBytes + kQParts * kQBytes + kTail;
+constexpr int kBars = 2 * kKSlots + 2 * kQParts + 8;
 // cost of a tile against few rows, in units of 512 cycles: its K comes from HBM in
 // about 6000 (256 KB at d = 512 and at a pair's share of the rate), while the MMAs of
 // 64 rows take 1024
 constexpr int kTileCost = 12;
 
-// What the issuer is to do with a chunk: K slot << 12, Q slot << 24, Q slots << 8,
-// accumulator << 16, and
+// What the issuer is to do with a chunk: its parts of Q << 8, K slot << 12, accumulator
+// << 16, parts of a Q slot << 20, Q slot << 24, and
 constexpr uint32_t kGo = 1, kFirst = 2, kLast = 4, kFreeK = 8, kFreeQ = 16;
 
 // Counters of the pairs that have ended with a tile that began in pair p: a byte
@@ -160,14 +160,16 @@ struct Walk {
   }
   // rows of the unit, and the columns that they take
   __device__ __forceinline__ int32_t rows() const { return min(kBlock, r.rows - block * kBlock); }
-  __device__ __forceinline__ int32_t slots() const {
+  __device__ __forceinline__ int32_t parts() const {
     const int32_t n = rows();
     return n <= 64 ? 1 : n <= 128 ? 2 : 4;
   }
+  // of a slot: the same for all blocks of the request
+  __device__ __forceinline__ int32_t slot_parts() const { return r.blocks > 1 ? 4 : parts(); }
   // Q stays for all tiles of the request where it has one block and that fits
   template <int D>
   __device__ __forceinline__ bool q_stays() const {
-    return r.blocks == 1 && slots() * (D / 64) <= kQSlots;
+    return r.blocks == 1 && parts() * (D / 64) <= kQParts;
   }
   // no row of the block sees a key of the tile
   __device__ __forceinline__ bool dead(const Args& a) const {
@@ -211,16 +213,48 @@ __device__ __forceinline__ bool elect_one() {
       : "=r"(is));
   return is != 0;
 }
+// The ring of Q: slots of `parts` parts.  When that changes it begins anew, once all
+// slots of the old kind are free.  A bit for each barrier: the parity of its next use.
+struct QRing {
+  uint32_t parts = 4, count = kQParts / 4, at = 0, phase = 0;
+
+  // whether slots of n parts are another kind
+  __device__ __forceinline__ bool other(uint32_t n) const { return n != parts; }
+  __device__ __forceinline__ void begin(uint32_t n) {
+    parts = n;
+    count = (uint32_t)kQParts / n;
+    at = 0;
+  }
+  __device__ __forceinline__ uint32_t parity() const { return (phase >> at) & 1u; }
+  __device__ __forceinline__ void used() {
+    phase ^= 1u << at;
+    at = at + 1 == count ? 0 : at + 1;
+  }
+};
+
+// Bounded waits for what TMA and the tensor cores do, or for TMEM that has been
+// read: no memory written by the other CTA's threads is read behind them, so that
+// they need no acquisition beyond the CTA (as PairWaiter has it).
+struct LocalWaiter {
+  PairWaiter w;
+  __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const {
+    const bool done = mbar_try_wait(bar, parity) || w.wait1(bar, parity);
+    return __all_sync(0xffffffffu, done);
+  }
+};
+
 template <int D>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     key_weights_kernel(const __grid_constant__ CUtensorMap q_map,
+                       const __grid_constant__ CUtensorMap q2_map,
+                       const __grid_constant__ CUtensorMap q4_map,
                        const __grid_constant__ CUtensorMap k_map, const Args a) {
   constexpr int kChunks = D / 64;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sK = (raw + 1023u) & ~1023u;
   const uint32_t sQ = sK + kKSlots * kKBytes;
-  uint8_t* tail = smem_raw + (sK - raw) + kKSlots * kKBytes + kQSlots * kQBytes;
+  uint8_t* tail = smem_raw + (sK - raw) + kKSlots * kKBytes + kQParts * kQBytes;
   float* neg_s = reinterpret_cast<float*>(tail);        // [unit & 1][column] -lse
   float* red = neg_s + 2 * kBlock;                       // [key] the other columns' sums
   uint32_t* live_s = reinterpret_cast<uint32_t*>(red + 128);  // [unit & 1][8] columns that count
@@ -236,19 +270,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   auto k_full = [&](uint32_t s) { return bar0 + 8u * s; };               // leader: both landed
   auto k_empty = [&](uint32_t s) { return bar0 + 8u * (kKSlots + s); };
   auto q_full = [&](uint32_t s) { return bar0 + 8u * (2 * kKSlots + s); };  // leader
-  auto q_empty = [&](uint32_t s) { return bar0 + 8u * (2 * kKSlots + kQSlots + s); };
-  const uint32_t bx = bar0 + 8u * (2 * kKSlots + 2 * kQSlots);
+  auto q_empty = [&](uint32_t s) { return bar0 + 8u * (2 * kKSlots + kQParts + s); };
+  const uint32_t bx = bar0 + 8u * (2 * kKSlots + 2 * kQParts);
   auto s_full = [&](uint32_t u) { return bx + 8u * (u & 1u); };
   auto s_empty = [&](uint32_t u) { return bx + 16 + 8u * (u & 1u); };    // leader
   const uint32_t epi = bx + 32, done_bar = bx + 40;
-  const PairWaiter W{misc, at_rank(smem_u32(misc), peer), a.status, a.timeout_ns};
+  const LocalWaiter W{{misc, at_rank(smem_u32(misc), peer), a.status, a.timeout_ns}};
 
   if (tid == 0) {
     for (uint32_t s = 0; s < kKSlots; ++s) {
       mbar_init(k_full(s), 1);
       mbar_init(k_empty(s), 1);
     }
-    for (uint32_t s = 0; s < kQSlots; ++s) {
+    for (uint32_t s = 0; s < kQParts; ++s) {
       mbar_init(q_full(s), 1);
       mbar_init(q_empty(s), 1);
     }
@@ -276,52 +310,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---- this pair's share of the cost, and the request where it begins
+  // ---- this pair's share of the cost, and the request where it begins: the requests
+  // kThreads at a time, once for the sum and, where that took more than one turn,
+  // again up to the share's start
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  int64_t total = 0;
+  int64_t total = 0, chunk = 0, start = 0, end = 0;
+  int64_t* share = scratch + 16;  // cost before the request, its number
   {
     const int32_t last = ld_input(a.cu + a.B);
     int bad = ld_input(a.cu) < 0 || last > a.T;
-    for (int b = tid; b < a.B; b += kThreads) {
-      const Req r = load_req(a, b);
-      bad |= r.rows < 0;
-      total += units_of(r) * r.cost;
-      if (blockIdx.x == 0) {
-        const int32_t n = ld_input(a.seq + b);
-        if (n < 0 || n > a.max_blocks << a.page_log2)
-          latch_error(a.status, DSA_ERR_DEVICE_BAD_INDEX);
-      }
-    }
-    total = warp_sum(total);
-    if (lane == 0) scratch[warp] = total;
-    bad = __syncthreads_or(bad);
-    total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) total += scratch[w];
-    if (bad) {  // offsets that do not ascend within [0, T]: nothing is computed
-      total = 0;
-      if (blockIdx.x == 0 && tid == 0) latch_error(a.status, DSA_ERR_DEVICE_BAD_INDEX);
-    }
-  }
-  // (a share of a unit's cost at least: then the pairs of a tile have no gap)
-  const int64_t chunk = max(ceil_div(total, pairs), (int64_t)kTileCost);
-  const int64_t start = min(total, pair * chunk), end = min(total, start + chunk);
-  int64_t* share = scratch + 16;  // cost before the request, its number
-  {
-    int64_t c = 0;
-    for (int b0 = 0; b0 < a.B && start < end && c <= start; b0 += kThreads) {
+    int64_t mine = 0, incl = 0;  // of the last turn
+    // the cost of requests b0 .. b0 + kThreads - 1, this thread's and those before it
+    auto turn = [&](int b0, bool check) {
       const int b = b0 + tid;
-      int64_t mine = 0;
+      mine = 0;
       if (b < a.B) {
         const Req r = load_req(a, b);
         mine = units_of(r) * r.cost;
+        if (check) {
+          bad |= r.rows < 0;
+          const int32_t n = blockIdx.x == 0 ? ld_input(a.seq + b) : 0;
+          if (n < 0 || n > a.max_blocks << a.page_log2)
+            latch_error(a.status, DSA_ERR_DEVICE_BAD_INDEX);
+        }
       }
-      int64_t incl = mine;
+      incl = mine;
 #pragma unroll
       for (int s = 1; s < 32; s <<= 1) {
         const int64_t x = __shfl_up_sync(0xffffffffu, incl, s);
         if (lane >= s) incl += x;
       }
-      __syncthreads();
       if (lane == 31) scratch[warp] = incl;
       __syncthreads();
       int64_t all = 0;
@@ -329,10 +347,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (w == warp) incl += all;
         all += scratch[w];
       }
+      __syncthreads();
+      return all;
+    };
+    for (int b0 = 0; b0 < a.B; b0 += kThreads) total += turn(b0, true);
+    bad = __syncthreads_or(bad);
+    if (bad) {  // offsets that do not ascend within [0, T]: nothing is computed
+      total = 0;
+      if (blockIdx.x == 0 && tid == 0) latch_error(a.status, DSA_ERR_DEVICE_BAD_INDEX);
+    }
+    // (a share of a unit's cost at least: then the pairs of a tile have no gap)
+    chunk = max(ceil_div(total, pairs), (int64_t)kTileCost);
+    start = min(total, pair * chunk);
+    end = min(total, start + chunk);
+    int64_t c = 0;
+    for (int b0 = 0; b0 < a.B && start < end && c <= start; b0 += kThreads) {
+      const int64_t all = a.B > kThreads ? turn(b0, false) : total;
       const int64_t c0 = c + incl - mine;
       if (c0 <= start && start < c0 + mine) {
         share[0] = c0;
-        share[1] = b;
+        share[1] = b0 + tid;
       }
       c += all;
     }
@@ -344,71 +378,85 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   Walk walk;
   walk.begin(a, start, end, start < end ? share[0] : 0, start < end ? (int)share[1] : 0);
 
-  if (warp == kProdWarp) {
-    // ====================================================== TMA producer
+  if (warp == kKWarp) {
+    // ============================================================ K by TMA
     const int page = 1 << a.page_log2, nb = 128 >> a.page_log2;  // page boxes of a chunk
     const int32_t n_rows_cache = (int32_t)(a.n_pages << a.page_log2);  // out of range: zeros
     const bool arms = rank == 0 && lane == 0;
     const uint32_t lead = at_rank(bar0, 0);
-    uint32_t kc = 0, qs = 0, q_phase = 0;  // K chunks so far; next Q slot; phases used up
-    bool ok = true, any = false, k_here = false;
+    uint32_t kc = 0;  // chunks so far
+    bool ok = true, here = false;
+    const int32_t key0 = (int)rank * 128 + lane * page;  // of this lane's box, in a tile
+    // page of that box in a tile of the walk's request (looked at when it is loaded)
+    auto page_at = [&](int32_t tile) {
+      const int32_t pos = tile * kTile + key0;
+      return lane < nb && pos < walk.r.len
+                 ? ld_input(a.table + (int64_t)walk.b * a.max_blocks + (pos >> a.page_log2))
+                 : -1;
+    };
+    int32_t next_page = -1;
     while (ok && walk.next(a)) {
-      if (walk.block == 0 || walk.first) k_here = false;
-      const bool load_q = !walk.q_stays<D>() || walk.first;
+      if (walk.block == 0 || walk.first) here = false;
+      if (walk.first) next_page = page_at(walk.tile);
       walk.first = false;
-      if (walk.dead(a)) continue;
-      any = true;
-      int32_t k_row = n_rows_cache;
-      if (!k_here) {
-        const int32_t pos = walk.tile * kTile + (int)rank * 128 + lane * page;
-        if (lane < nb && pos < walk.r.len) {
-          const int32_t p =
-              ld_input(a.table + (int64_t)walk.b * a.max_blocks + (pos >> a.page_log2));
-          if (p < 0 || p >= a.n_pages) latch_error(a.status, DSA_ERR_DEVICE_BAD_INDEX);
-          else k_row = p << a.page_log2;
-        }
+      if (here || walk.dead(a)) continue;
+      here = true;
+      int32_t row = n_rows_cache;
+      if (walk.tile * kTile + key0 < walk.r.len && lane < nb) {
+        if (next_page < 0 || next_page >= a.n_pages)
+          latch_error(a.status, DSA_ERR_DEVICE_BAD_INDEX);
+        else
+          row = next_page << a.page_log2;
       }
-      const int n = walk.slots();
-      qs = (qs + n - 1) / n * n;
-      if (qs == kQSlots) qs = 0;
-      const int32_t q_row = walk.r.row0 + walk.block * kBlock + (int)rank * 32 * n + 32 * lane;
+      next_page = page_at(walk.tile + 1);
 #pragma unroll 1
-      for (int c = 0; c < kChunks && ok; ++c) {
-        if (!k_here) {
-          const uint32_t s = kc % kKSlots;
-          if (!(ok = W.wait(k_empty(s), ((kc / kKSlots) & 1u) ^ 1u))) break;
-          if (arms) mbar_expect_tx(k_full(s), 2 * kKBytes);
-          __syncwarp();
-          if (lane < nb)
-            tma_load_pair(sK + s * kKBytes + (uint32_t)(lane * page) * 128u, &k_map, c * 64, k_row,
-                          lead + 8u * s);
-          ++kc;
-        }
-        if (load_q) {
-          for (int i = 0; i < n && ok; ++i) {
-            ok = W.wait(q_empty(qs + i), ((q_phase >> (qs + i)) & 1u) ^ 1u);
-            if (ok && arms) mbar_expect_tx(q_full(qs + i), 2 * kQBytes);
-          }
-          if (!ok) break;
-          __syncwarp();
-          if (lane < n)
-            tma_load_pair(sQ + (qs + lane) * kQBytes, &q_map, c * 64, q_row,
-                          lead + 8u * (2 * kKSlots + qs + lane));
-          q_phase ^= ((1u << n) - 1u) << qs;
-          qs += n;
-          if (qs == kQSlots) qs = 0;
-        }
+      for (int c = 0; c < kChunks; ++c, ++kc) {
+        const uint32_t s = kc % kKSlots;
+        if (!(ok = W.wait(k_empty(s), ((kc / kKSlots) & 1u) ^ 1u))) break;
+        if (arms) mbar_expect_tx(k_full(s), 2 * kKBytes);
+        if (lane < nb)
+          tma_load_pair(sK + s * kKBytes + (uint32_t)(lane * page) * 128u, &k_map, c * 64, row,
+                        lead + 8u * s);
       }
-      k_here = true;
     }
     // the leader's last arrival here is done_bar's: the CTA outlives it
-    if (ok && rank != 0 && any) W.wait(done_bar, 0);
+    if (ok && rank != 0 && kc > 0) W.wait(done_bar, 0);
+  } else if (warp == kQWarp) {
+    // ============================================================ Q by TMA
+    const uint32_t lead = at_rank(bar0, 0);
+    QRing ring;
+    bool ok = true;
+    while (ok && walk.next(a)) {
+      const bool load = !walk.q_stays<D>() || walk.first;
+      walk.first = false;
+      if (!load || walk.dead(a)) continue;
+      const uint32_t n = (uint32_t)walk.parts(), slot = (uint32_t)walk.slot_parts();
+      if (ring.other(slot)) {
+        for (ring.at = 0; ring.at < ring.count && ok; ++ring.at)
+          ok = W.wait(q_empty(ring.at), ring.parity() ^ 1u);
+        if (!ok) break;
+        ring.begin(slot);
+      }
+      const CUtensorMap* map = n == 4 ? &q4_map : n == 2 ? &q2_map : &q_map;
+      const int32_t row = walk.r.row0 + walk.block * kBlock + (int)(rank * n) * 32;
+#pragma unroll 1
+      for (int c = 0; c < kChunks; ++c) {
+        if (!(ok = W.wait(q_empty(ring.at), ring.parity() ^ 1u))) break;
+        if (lane == 0) {
+          if (rank == 0) mbar_expect_tx(q_full(ring.at), 2 * kQBytes * n);
+          tma_load_pair(sQ + ring.at * slot * kQBytes, map, c * 64, row,
+                        lead + 8u * (2 * kKSlots + ring.at));
+        }
+        ring.used();
+      }
+    }
   } else if (warp == kScoutWarp && rank == 0) {
     // ====== scout: waits for the issuer's operands and lets it in, a chunk at a
     // time (a wait of the issuer's own would queue behind its MMAs), with a word that
     // says what to issue.  When a wait gives up it lets the issuer through what is
     // left, on whatever is there.
-    uint32_t kc = 0, qs = 0, q0 = 0, q_phase = 0, nu = 0, n_bar = 0;
+    uint32_t kc = 0, q0 = 0, nu = 0, n_bar = 0;
+    QRing ring;
     bool ok = true, k_here = false;
     auto let_in = [&](uint32_t word) {
       if (lane == 0) cmd[n_bar & 1u] = word;
@@ -421,30 +469,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool stays = walk.q_stays<D>(), load_q = !stays || walk.first;
       walk.first = false;
       if (walk.dead(a)) continue;
-      const int n = walk.slots();
-      qs = (qs + n - 1) / n * n;
-      if (qs == kQSlots) qs = 0;
-      if (load_q) q0 = qs;
+      const uint32_t slot = (uint32_t)walk.slot_parts();
+      if (load_q && ring.other(slot)) ring.begin(slot);
+      if (load_q) q0 = ring.at;
       if (!k_here) kc += kChunks;
-      const uint32_t flags = (walk.tile_ends() ? kFreeK : 0u) |
-                             (!stays || walk.left == 0 ? kFreeQ : 0u) | (uint32_t)n << 8 |
-                             (nu & 1u) << 16;
+      const uint32_t flags = kGo | (walk.tile_ends() ? kFreeK : 0u) |
+                             (!stays || walk.left == 0 ? kFreeQ : 0u) |
+                             (uint32_t)walk.parts() << 8 | slot << 20 | (nu & 1u) << 16;
       if (ok) ok = W.wait(s_empty(nu), ((nu >> 1) & 1u) ^ 1u);
       uint32_t q = q0;
+#pragma unroll 1
       for (uint32_t c = 0; c < kChunks; ++c) {
         const uint32_t x = kc - kChunks + c;
         if (!k_here && ok) ok = W.wait(k_full(x % kKSlots), (x / kKSlots) & 1u);
         if (load_q) {
-          for (int i = 0; i < n; ++i)
-            if (ok) ok = W.wait(q_full(q + i), (q_phase >> (q + i)) & 1u);
-          q_phase ^= ((1u << n) - 1u) << q;
+          if (ok) ok = W.wait(q_full(q), ring.parity());
+          ring.used();
         }
-        let_in(flags | kGo | (c == 0 ? kFirst : 0u) | (c == kChunks - 1 ? kLast : 0u) |
+        let_in(flags | (c == 0 ? kFirst : 0u) | (c == kChunks - 1 ? kLast : 0u) |
                (x % kKSlots) << 12 | q << 24);
-        q += n;
-        if (q == kQSlots) q = 0;
+        q = q + 1 == ring.count ? 0 : q + 1;
       }
-      if (load_q) qs = q;
       k_here = true;
       ++nu;
     }
@@ -463,15 +508,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc_fence_after();
       if (elect_one()) {
         const uint32_t n = (word >> 8) & 15u, s = (word >> 12) & 15u, u = (word >> 16) & 1u;
-        const uint32_t q = word >> 24, d = tmem + u * kBlock;
+        const uint32_t q = word >> 24, slot = (word >> 20) & 15u, d = tmem + u * kBlock;
         const uint32_t idesc = idesc_bf16(256, 0, 0, 0) | (64 * n) >> 3 << 17;
-        const uint32_t da = dK + s * (kKBytes >> 4), db = dQ + q * (kQBytes >> 4);
+        const uint32_t da = dK + s * (kKBytes >> 4), db = dQ + q * slot * (kQBytes >> 4);
         tc_mma2(d, da, db, hi, idesc, word & kFirst ? 0u : 1u);
 #pragma unroll
         for (uint32_t x = 1; x < 4; ++x) tc_mma2(d, da + 2 * x, db + 2 * x, hi, idesc, 1u);
         if (word & kFreeK) tc_commit2(k_empty(s));
-        if (word & kFreeQ)
-          for (uint32_t i = 0; i < n; ++i) tc_commit2(q_empty(q + i));
+        if (word & kFreeQ) tc_commit2(q_empty(q));
         if (word & kLast) tc_commit2(s_full(u));
       }
       __syncwarp();
@@ -494,13 +538,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     bool ok = true, head = false;
     uint64_t sum[2] = {0ull, 0ull};
+    int64_t slot = -1;  // of this thread's key, or -1
+    float old = 0.f;    // what it has received before
     while (ok && walk.next(a)) {
+      const int32_t pos0 = walk.tile * kTile + (int)rank * 128 + quad * 32, pos = pos0 + lane;
       if (walk.block == 0 || walk.first) {
         head = walk.block != 0;  // the tile began in a pair before
         sum[0] = sum[1] = 0ull;
+        slot = -1;
+        old = 0.f;
+        if (g == 0 && pos < walk.r.len) {
+          const int32_t p =
+              ld_input(a.table + (int64_t)walk.b * a.max_blocks + (pos >> a.page_log2));
+          if (p >= 0 && p < a.n_pages)  // else latched where K is loaded
+            slot = ((int64_t)p << a.page_log2) + (pos & ((1 << a.page_log2) - 1));
+          if (slot >= 0 && pos < walk.r.base)
+            old = a.decay * __int_as_float(ld_input(reinterpret_cast<const int32_t*>(a.w + slot)));
+        }
       }
       walk.first = false;
-      const int32_t pos0 = walk.tile * kTile + (int)rank * 128 + quad * 32, pos = pos0 + lane;
       if (!walk.dead(a)) {
         const int32_t n = walk.rows(), at = walk.block * kBlock;
         float* neg = neg_s + (nu & 1u) * kBlock;
@@ -623,17 +679,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int p = from; p <= to; ++p) v += __ldcg(part(p));
         }
       }
-      if (mine && pos < walk.r.len) {
-        const int32_t p = ld_input(a.table + (int64_t)walk.b * a.max_blocks + (pos >> a.page_log2));
-        if (p >= 0 && p < a.n_pages) {
-          const int64_t slot =
-              ((int64_t)p << a.page_log2) + (pos & ((1 << a.page_log2) - 1));
-          if (pos < walk.r.base)
-            v = fmaf(a.decay, __int_as_float(ld_input(reinterpret_cast<const int32_t*>(a.w + slot))),
-                     v);
-          a.w_out[slot] = v;
-        }
-      }
+      if (mine && slot >= 0) a.w_out[slot] = old + v;
       if (!(ok = epi_sync())) break;  // red and misc may be written again
       sum[0] = sum[1] = 0ull;
     }
@@ -641,7 +687,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   // ---- teardown: after a wait that gave up, copies may be in flight to either CTA:
   // they get 2 ms to land before the CTAs go
-  if (tid == 0 && *W.abort_flag) {
+  if (tid == 0 && *W.w.abort_flag) {
     const uint64_t t0 = globaltimer_ns();
     while (globaltimer_ns() - t0 < 2000000u) __nanosleep(100000);
   }
@@ -656,7 +702,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 template <int D>
-cudaError_t launch_t(const LaunchCtx& c, const CUtensorMap& qm, const CUtensorMap& km,
+cudaError_t launch_t(const LaunchCtx& c, const CUtensorMap (&qm)[3], const CUtensorMap& km,
                      const Args& a) {
   static std::atomic<uint64_t> prepared{0};
   const uint64_t bit = 1ull << (c.device & 63);
@@ -677,7 +723,7 @@ cudaError_t launch_t(const LaunchCtx& c, const CUtensorMap& qm, const CUtensorMa
   cfg.stream = c.stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, key_weights_kernel<D>, qm, km, a);
+  return cudaLaunchKernelEx(&cfg, key_weights_kernel<D>, qm[0], qm[1], qm[2], km, a);
 }
 
 }  // namespace
@@ -685,7 +731,7 @@ cudaError_t launch_t(const LaunchCtx& c, const CUtensorMap& qm, const CUtensorMa
 size_t key_weights_ws(const ServeShape&) { return (size_t)kMaxPairs * 2 * 2 * 128 * 4; }
 
 cudaError_t launch_key_weights(const LaunchCtx& c, const ServeShape& s,
-                               const CUtensorMap& q_map, const CUtensorMap& k_map,
+                               const CUtensorMap (&q_maps)[3], const CUtensorMap& k_map,
                                const float* lse, const int32_t* table, const int32_t* seq,
                                const int32_t* cu, const uint32_t* tree_bits, int words,
                                const float* w_pages, float decay, float* w_out, uint8_t* ws) {
@@ -710,9 +756,9 @@ cudaError_t launch_key_weights(const LaunchCtx& c, const ServeShape& s,
   a.n_pages = s.n_pages;
   a.status = c.status;
   a.timeout_ns = c.timeout_ns;
-  if (s.D == 128) return launch_t<128>(c, q_map, k_map, a);
-  if (s.D == 256) return launch_t<256>(c, q_map, k_map, a);
-  return launch_t<512>(c, q_map, k_map, a);
+  if (s.D == 128) return launch_t<128>(c, q_maps, k_map, a);
+  if (s.D == 256) return launch_t<256>(c, q_maps, k_map, a);
+  return launch_t<512>(c, q_maps, k_map, a);
 }
 
 }  // namespace dsa

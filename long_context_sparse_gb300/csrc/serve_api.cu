@@ -270,9 +270,10 @@ dsa_status_t dsa_key_weights(const dsa_serve_config_t* cfg, const void* q, const
   LaunchCtx ctx;
   if ((st = make_ctx(ws, stream, &ctx)) != DSA_OK) return st;
   const ServeShape sh = serve_shape(cfg);
-  CUtensorMap qm, km;
+  CUtensorMap qm[3], km;
   const uint64_t d = (uint64_t)sh.D;
-  if ((st = encode_2d(&qm, q, (uint64_t)rows, d, 32)) != DSA_OK) return st;
+  for (int i = 0; i < 3; ++i)
+    if ((st = encode_2d(&qm[i], q, (uint64_t)rows, d, 32u << i)) != DSA_OK) return st;
   if ((st = encode_2d(&km, k_pages, (uint64_t)slots, d, (uint32_t)sh.page)) != DSA_OK) return st;
   return cuda_status(launch_key_weights(ctx, sh, qm, km, lse, block_table, seq_lens, cu_tokens,
                                         tree_bits, words, w_pages, decay, w_out,
