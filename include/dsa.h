@@ -575,8 +575,9 @@ DSA_API dsa_status_t dsa_key_weights(const dsa_serve_config_t* cfg, const void* 
  * and lengths stay: one dsa_release_pages a step serves all layers.  Rows and
  * weights from left_b on, and all that belongs to no request, are left as they
  * are.  v_pages NULL: K = V.  w_out may be w_pages.
- * keep_lens [B] int32, n_first, n_last >= 0; seq_lens, block_table as above.  What
- * is written must not overlap what is read, or itself, in any other way
+ * keep_lens [B] int32, n_first, n_last >= 0; seq_lens, block_table as above;
+ * max_blocks * page_size <= 2^22, else DSA_ERR_UNSUPPORTED_SHAPE.  What is written
+ * must not overlap what is read, or itself, in any other way
  * (DSA_ERR_INVALID_ARG).  A page may not belong to two requests, or stand twice
  * in one's row.
  * Device-side errors (latched as DSA_ERR_DEVICE_BAD_INDEX; nothing is read or

@@ -22,9 +22,8 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 4;      // 16-byte vectors of a thread in flight: a batch
 constexpr int kMaxTop = 64;
 constexpr int kKept = 4;        // batches that a thread remembers
-constexpr int kBuf = 512;       // candidates of a CTA; alternatives of a cluster
+constexpr int kBuf = 512;       // candidates of a CTA
 constexpr int kMaxCluster = 8;  // CTAs of a row
-static_assert(kMaxTop * kMaxCluster <= kBuf, "the leader's buffer");
 constexpr float kUnset = -3.402823466e38f;  // reference of nothing but -inf
 constexpr float kNever = -16384.f;          // 2^ of it is 0
 
@@ -49,12 +48,6 @@ __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
 __device__ __forceinline__ float ld_f(const float* p) {
   return __int_as_float(ld_input(reinterpret_cast<const int32_t*>(p)));
 }
-__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
-
 // A 32-bit word of logits as floats, their maximum, and back.
 template <typename T>
 struct Word;
@@ -135,11 +128,12 @@ __device__ __forceinline__ __half to_type(float x) {
   return __float2half_rn(x);
 }
 
-// A logit as an integer in the same order (the two zeros alike, NaN below -inf and
-// above 0, which stands for none); with its id behind it, larger for lower ids.
+// A logit as an integer in the same order, above 0 (which stands for none): the two
+// zeros alike, NaN with -inf, which also fills up a batch.  With its id behind it,
+// larger for lower ids.
 __device__ __forceinline__ uint32_t order_key(float x) {
   const uint32_t u = __float_as_uint(x + 0.0f);
-  return x != x ? 1u : u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+  return x != x ? 0x007fffffu : u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 __device__ __forceinline__ uint64_t full_key(float x, uint32_t id) {
   return ((uint64_t)order_key(x) << 32) | (0xffffffffu - id);
@@ -185,42 +179,77 @@ __device__ __forceinline__ Stat merge(const Stat& a, const Stat& b, float c) {
   return {r, fa * a.s + fb * b.s, fa * (a.t + da * a.s) + fb * (b.t + db * b.s)};
 }
 
+__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // A cluster of CTAs has a row, each a share of its vectors.
 //
 // Alternatives, exactly and in the same pass: each thread remembers its kKept
-// batches with the largest maxima.  The n-th largest of the threads' best elements
-// is a bound that the n-th largest of the share reaches, so that only batches whose
-// maximum reaches it are looked at again (they are in L2).  A thread of which more
-// batches than it remembers may reach it, or a full buffer, sends the share through
-// `slow`: n passes, each for the largest below the one before.
+// batches with the largest maxima.  A value that n of the threads' best elements
+// reach is a bound for the n best of the share (here: what k threads of each of the
+// 8 warps reach, 8 k >= n, found by k maxima over a warp), so that only the batches
+// whose maximum reaches it are looked at again, in L2, and few elements of those
+// pass.  A thread of which more batches than it remembers may reach the bound sends
+// the share through a second look at all of it.  Where more elements pass than the
+// buffer holds (rows of many equal values), ids break the ties already in the bound;
+// and should that not do either, `n` passes each look for the largest below the last.
 template <typename T, bool Top>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(
+__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
     const T* logits, int64_t ld, int32_t vocab, const int32_t* tokens, int n_top, float scale,
     float* logp, float* lse, float* entropy, int32_t* top_ids, float* top_logp,
     uint32_t* status) {
-  constexpr int kWords = 4 * kUnroll;
+  constexpr int kWords = 4 * kUnroll, kStep = kUnroll * kThreads;
   using W = Word<T>;
   __shared__ Stat stats[kWarps];
   __shared__ Stat total;
   __shared__ alignas(16) uint64_t best[Top ? kThreads : 1];
-  __shared__ uint64_t buf[Top ? kBuf : 1];
+  __shared__ alignas(16) uint64_t buf[Top ? kBuf : 2];
   __shared__ uint64_t top[Top ? kMaxTop : 1];
+  // the leader's: what the cluster's CTAs have found
+  __shared__ Stat from[kMaxCluster];
+  __shared__ alignas(16) uint64_t from_top[Top ? kMaxTop * kMaxCluster : 2];
+  __shared__ uint32_t warp_bound[kWarps];
   __shared__ uint32_t n_buf, again;
   __shared__ uint64_t bound;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t rank, size;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
+  if (size > 1) cluster_arrive();  // the leader has begun: waited for before it is written to
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t r = blockIdx.x / size;
   const Row<T> row(logits + r * ld, vocab);
   const float c = scale * kLog2e;
+  const uint64_t c2 = pair2(c, c);
   const int32_t per = (row.n_vec + (int)size - 1) / (int)size;
   const int32_t v0 = min(row.n_vec, (int)rank * per), v1 = min(row.n_vec, v0 + per);
   const int n_single = rank == 0 ? row.n_single() : 0;
+  const uint4* vec = row.vec();
 
-  Stat a{kUnset, 0.f, 0.f};
+  float ref = kUnset;
+  uint64_t s2 = 0ull, t2 = 0ull;
   uint32_t kept[kKept];  // order keys of the remembered batches' maxima, largest first
   int32_t which[kKept];  // their numbers; -1: this thread's single element
 #pragma unroll
@@ -244,28 +273,24 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(
     }
   };
   auto raise = [&](float m) {
-    if (m > a.r) {
-      const float d = max_nan((a.r - m) * c, kNever), f = ex2(d);
-      a.t = f * (a.t + d * a.s);
-      a.s *= f;
-      a.r = m;
+    if (m > ref) {
+      const float d = max_nan((ref - m) * c, kNever), f = ex2(d);
+      t2 = mul2(pair2(f, f), fma2(pair2(d, d), s2, t2));
+      s2 = mul2(pair2(f, f), s2);
+      ref = m;
     }
   };
-  auto add = [&](float x) {
-    const float y = max_nan((x - a.r) * c, kNever), e = ex2(y);
-    a.s += e;
-    a.t += e * y;
+  // two elements (of one alone: with -inf beside it)
+  auto add = [&](float a, float b, uint64_t minus_ref) {
+    float y0, y1;
+    unpair2(mul2(add2(pair2(a, b), minus_ref), c2), y0, y1);
+    y0 = max_nan(y0, kNever);
+    y1 = max_nan(y1, kNever);
+    const uint64_t e = pair2(ex2(y0), ex2(y1));
+    s2 = add2(s2, e);
+    t2 = fma2(e, pair2(y0, y1), t2);
   };
-  if (tid < n_single) {
-    const float x = load1(row.at + row.single(tid));
-    if (Top) remember(x, -1);
-    raise(x);
-    add(x);
-  }
-  const uint4* vec = row.vec();
-  int32_t batches = 0;
-  for (int32_t v = v0 + tid; v < v1; v += kUnroll * kThreads, ++batches) {
-    uint32_t w[kWords];
+  auto load = [&](int32_t v, uint32_t (&w)[kWords]) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       uint4 x = make_uint4(W::kNone, W::kNone, W::kNone, W::kNone);
@@ -275,75 +300,147 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(
       w[4 * u + 2] = x.z;
       w[4 * u + 3] = x.w;
     }
+  };
+  auto largest = [&](const uint32_t (&w)[kWords]) {
     uint32_t m[4] = {w[0], w[1], w[2], w[3]};
 #pragma unroll
     for (int i = 4; i < kWords; ++i) m[i & 3] = W::max(m[i & 3], w[i]);
     float x[W::kPer];
     W::get(W::max(W::max(m[0], m[1]), W::max(m[2], m[3])), x);
-    const float top_x = W::kPer == 2 ? fmaxf(x[0], x[W::kPer - 1]) : x[0];
-    if (Top) remember(top_x, batches);
-    raise(top_x);
+    return W::kPer == 2 ? fmaxf(x[0], x[W::kPer - 1]) : x[0];
+  };
+  int32_t batches = 0;
+  auto take_in = [&](const uint32_t (&w)[kWords]) {
+    const float m = largest(w);
+    if (Top) remember(m, batches);
+    ++batches;
+    raise(m);
+    const uint64_t minus_ref = pair2(-ref, -ref);
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      W::get(w[i], x);
-#pragma unroll
-      for (int e = 0; e < W::kPer; ++e) add(x[e]);
+    for (int i = 0; i < kWords; i += 3 - W::kPer) {
+      float x[2];
+      if constexpr (W::kPer == 2) {
+        W::get(w[i], x);
+      } else {
+        x[0] = __uint_as_float(w[i]);
+        x[1] = __uint_as_float(w[i + 1]);
+      }
+      add(x[0], x[1], minus_ref);
+    }
+  };
+  {
+    // a batch is on its way while the one before it is worked on
+    uint32_t w[2][kWords];
+    int32_t v = v0 + tid;
+    if (v < v1) load(v, w[0]);
+    if (tid < n_single) {
+      const float x = load1(row.at + row.single(tid));
+      if (Top) remember(x, -1);
+      raise(x);
+      add(x, -INFINITY, pair2(-ref, -ref));
+    }
+    for (; v < v1; v += 2 * kStep) {
+      if (v + kStep < v1) load(v + kStep, w[1]);
+      take_in(w[0]);
+      if (v + kStep >= v1) break;
+      if (v + 2 * kStep < v1) load(v + 2 * kStep, w[0]);
+      take_in(w[1]);
     }
   }
   // ---- the share's sums
-  Stat all = a;
+  Stat all;
+  {
+    float a, b;
+    all.r = ref;
+    unpair2(s2, a, b);
+    all.s = a + b;
+    unpair2(t2, a, b);
+    all.t = a + b;
+  }
+  auto merge_lanes = [&](int from) {
 #pragma unroll
-  for (int s = 16; s > 0; s >>= 1) {
-    const Stat o{__shfl_xor_sync(0xffffffffu, all.r, s), __shfl_xor_sync(0xffffffffu, all.s, s),
-                 __shfl_xor_sync(0xffffffffu, all.t, s)};
-    all = lane & s ? merge(o, all, c) : merge(all, o, c);
-  }
+    for (int s = 16; s > 0; s >>= 1) {
+      if (s > from) continue;
+      const Stat o{__shfl_xor_sync(0xffffffffu, all.r, s), __shfl_xor_sync(0xffffffffu, all.s, s),
+                   __shfl_xor_sync(0xffffffffu, all.t, s)};
+      all = lane & s ? merge(o, all, c) : merge(all, o, c);
+    }
+  };
+  merge_lanes(16);
   if (lane == 0) stats[warp] = all;
-  if (tid == 0) {
-    n_buf = again = 0u;
-    bound = 0ull;
-  }
-  // each candidate of the thread's remembered batch q: f(value, id)
-  auto visit = [&](int32_t number, auto f) {
+  if (tid == 0) n_buf = again = 0u;
+  // the elements of one of the thread's batches: f(value, id), at least of those whose
+  // order key reaches `floor`
+  auto visit = [&](int32_t number, uint32_t floor, auto f) {
     if (number < 0) {
       f(load1(row.at + row.single(tid)), (uint32_t)row.single(tid));
       return;
     }
-    const int32_t v = v0 + tid + number * kUnroll * kThreads;
+    const int32_t v = v0 + tid + number * kStep;
+    uint32_t w[kWords];
+    load(v, w);
 #pragma unroll 1
     for (int u = 0; u < kUnroll && v + u * kThreads < v1; ++u) {
-      const uint4 q = ld_input(vec + v + u * kThreads);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      const uint32_t id = (uint32_t)row.id(v + u * kThreads);
+      uint32_t four[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        four[i] = u == 0 ? w[i] : u == 1 ? w[4 + i] : u == 2 ? w[8 + i] : w[12 + i];
+      float x[W::kPer];
+      W::get(W::max(W::max(four[0], four[1]), W::max(four[2], four[3])), x);
+      if (order_key(W::kPer == 2 ? fmaxf(x[0], x[W::kPer - 1]) : x[0]) < floor) continue;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float x[W::kPer];
-        W::get(w[i], x);
+        W::get(four[i], x);
 #pragma unroll
-        for (int e = 0; e < W::kPer; ++e)
-          f(x[e], (uint32_t)(row.id(v + u * kThreads) + i * W::kPer + e));
+        for (int e = 0; e < W::kPer; ++e) f(x[e], id + i * W::kPer + e);
       }
+    }
+  };
+  auto visit_all = [&](uint32_t floor, auto f) {
+    if (tid < n_single) visit(-1, floor, f);
+    for (int32_t q = 0; q < batches; ++q) visit(q, floor, f);
+  };
+  // the n keys of `list` in order: f(key, place); all threads
+  auto in_order = [&](const uint64_t* list, int n, auto f) {
+    const int even = n & ~1;
+    for (int i = tid; i < n; i += kThreads) {
+      const uint64_t key = list[i];
+      int place = 0;
+#pragma unroll 8
+      for (int j = 0; j < even; j += 2) {
+        const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(list + j);
+        place += (o.x > key) + (o.y > key);
+      }
+      if (even < n) place += list[even] > key;
+      f(key, place);
     }
   };
   // ---- the share's alternatives, in order, into top[]
   if (Top) {
-    uint64_t mine = 0ull;
-    if (kept[0])
-      visit(which[0], [&](float x, uint32_t id) {
-        const uint64_t k = full_key(x, id);
-        mine = k > mine ? k : mine;
-      });
-    best[tid] = mine;
+    // the threads that have vectors come first; whole warps of them have k each
+    const int full = min(kThreads, v1 - v0) >> 5, k = full ? (n_top + full - 1) / full : 33;
+    if (k <= 32 && warp < full) {
+      uint32_t mine = kept[0], reached = 0u;
+      for (int i = 0; i < k; ++i) {
+        reached = __reduce_max_sync(0xffffffffu, mine);
+        const uint32_t who = __ballot_sync(0xffffffffu, mine == reached);
+        if (lane == __ffs(who) - 1) mine = 0u;
+      }
+      if (lane == 0) warp_bound[warp] = reached;
+    }
     if (tid < kMaxTop) top[tid] = 0ull;
     __syncthreads();
-    int above = 0;
-    for (int i = 0; i < kThreads; i += 2) {
-      const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(best + i);
-      above += (k.x > mine) + (k.y > mine);
-    }
-    if (mine && above == n_top - 1) bound = mine;
-    __syncthreads();
-    const uint64_t at_least = bound;
-    const uint32_t least = (uint32_t)(at_least >> 32);
+    uint32_t least = k <= 32 ? 0xffffffffu : 0u;
+    if (k <= 32)
+      for (int x = 0; x < full; ++x) least = min(least, warp_bound[x]);
+    uint64_t at_least = (uint64_t)least << 32;
+    auto push = [&](float x, uint32_t id) {
+      const uint64_t key = full_key(x, id);
+      if (key < at_least) return;
+      const uint32_t i = atomicAdd(&n_buf, 1u);
+      if (i < kBuf) buf[i] = key;
+    };
     if (kept[0] && kept[0] >= least) {
       if (kept[kKept - 1] >= least && batches + (tid < n_single) > kKept) again = 1u;
 #pragma unroll 1
@@ -351,89 +448,98 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(
         const uint32_t kq = q == 0 ? kept[0] : q == 1 ? kept[1] : q == 2 ? kept[2] : kept[3];
         const int32_t wq = q == 0 ? which[0] : q == 1 ? which[1] : q == 2 ? which[2] : which[3];
         if (kq == 0u || kq < least) break;
-        visit(wq, [&](float x, uint32_t id) {
-          const uint64_t k = full_key(x, id);
-          if (k < at_least) return;
-          const uint32_t i = atomicAdd(&n_buf, 1u);
-          if (i < kBuf) buf[i] = k;
-        });
+        visit(wq, least, push);
       }
     }
     __syncthreads();
-    if (again || n_buf > kBuf) {
+    if (again) {
+      __syncthreads();
+      if (tid == 0) n_buf = 0u;
+      __syncthreads();
+      visit_all(least, push);
+      __syncthreads();
+    }
+    if (n_buf > kBuf) {
+      // the n-th largest of the threads' best elements, by value and id
+      uint64_t mine = 0ull;
+      visit_all(0u, [&](float x, uint32_t id) {
+        const uint64_t f = full_key(x, id);
+        mine = f > mine ? f : mine;
+      });
+      best[tid] = mine;
+      if (tid == 0) bound = 0ull;
+      __syncthreads();
+      int above = 0;
+      for (int i = 0; i < kThreads; i += 2) {
+        const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(best + i);
+        above += (o.x > mine) + (o.y > mine);
+      }
+      if (mine && above == n_top - 1) bound = mine;
+      if (tid == 0) n_buf = 0u;
+      __syncthreads();
+      at_least = bound;
+      if (mine >= at_least) visit_all((uint32_t)(at_least >> 32), push);
+      __syncthreads();
+    }
+    if (n_buf > kBuf) {
       uint64_t last = ~0ull;
       for (int i = 0; i < n_top; ++i) {
-        uint64_t k = 0ull;
-        auto take = [&](float x, uint32_t id) {
+        uint64_t most = 0ull;
+        visit_all(0u, [&](float x, uint32_t id) {
           const uint64_t f = full_key(x, id);
-          if (f < last && f > k) k = f;
-        };
-        if (tid < n_single) visit(-1, take);
-        for (int32_t q = 0; q < batches; ++q) visit(q, take);
+          if (f < last && f > most) most = f;
+        });
 #pragma unroll
         for (int s = 16; s > 0; s >>= 1) {
-          const uint64_t o = __shfl_xor_sync(0xffffffffu, k, s);
-          k = o > k ? o : k;
+          const uint64_t o = __shfl_xor_sync(0xffffffffu, most, s);
+          most = o > most ? o : most;
         }
-        if (lane == 0) best[warp] = k;
+        if (lane == 0) best[warp] = most;
         __syncthreads();
-        for (int x = 0; x < kWarps; ++x) k = best[x] > k ? best[x] : k;
-        if (tid == 0) top[i] = k;
-        last = k;
+        for (int x = 0; x < kWarps; ++x) most = best[x] > most ? best[x] : most;
+        if (tid == 0) top[i] = most;
+        last = most;
         __syncthreads();
       }
     } else {
-      const int n = (int)n_buf;
-      for (int i = tid; i < n; i += kThreads) {
-        const uint64_t k = buf[i];
-        int place = 0;
-        for (int j = 0; j < n; ++j) place += buf[j] > k;
-        if (place < n_top) top[place] = k;
-      }
+      in_order(buf, (int)n_buf, [&](uint64_t key, int place) {
+        if (place < n_top) top[place] = key;
+      });
     }
   }
   __syncthreads();
-  if (tid == 0) {
-    Stat s = stats[0];
-    for (int x = 1; x < kWarps; ++x) s = merge(s, stats[x], c);
-    total = s;
+  if (warp == 0) {
+    all = lane < kWarps ? stats[lane] : Stat{kUnset, 0.f, 0.f};
+    merge_lanes(kWarps / 2);
+    if (lane == 0) total = all;
   }
-  __syncthreads();
-  // ---- the row's
+  // ---- the row's: the others write to the leader, and go
   if (size > 1) {
-    cluster_arrive();
     cluster_wait();
-    if (rank == 0) {
-      if (tid == 0) {
-        Stat s = total;
-        for (uint32_t g = 1; g < size; ++g) {
-          const uint32_t at = at_rank(smem_u32(&total), g);
-          const Stat o{__uint_as_float(ld_cluster(at)), __uint_as_float(ld_cluster(at + 4)),
-                       __uint_as_float(ld_cluster(at + 8))};
-          s = merge(s, o, c);
-        }
-        total = s;
-      }
-      if (Top) {
-        const int n = (int)size * n_top;
-        for (int i = tid; i < n; i += kThreads) {
-          const uint32_t at = at_rank(smem_u32(top + i % n_top), i / n_top);
-          buf[i] = ld_cluster(at) | ((uint64_t)ld_cluster(at + 4) << 32);
-        }
-        __syncthreads();
-        for (int i = tid; i < n; i += kThreads) {
-          const uint64_t k = buf[i];
-          int place = 0;
-          for (int j = 0; j < n; ++j) place += buf[j] > k;
-          if (k && place < n_top) top[place] = k;
-        }
-      }
-    }
     __syncthreads();
+    if (tid < 3) {
+      const float x = tid == 0 ? total.r : tid == 1 ? total.s : total.t;
+      st_cluster_u32(at_rank(smem_u32(&from[rank]) + 4 * tid, 0), __float_as_uint(x));
+    }
+    if (Top && rank != 0)
+      for (int i = tid; i < 2 * n_top; i += kThreads)
+        st_cluster_u32(at_rank(smem_u32(from_top + rank * n_top) + 4 * i, 0),
+                       reinterpret_cast<const uint32_t*>(top)[i]);
+    if (Top && rank == 0 && tid < n_top) from_top[tid] = top[tid];
     cluster_arrive();
+    if (rank != 0) return;
     cluster_wait();
+    if (warp == 0) {
+      all = lane < (int)size ? from[lane] : Stat{kUnset, 0.f, 0.f};
+      merge_lanes(kMaxCluster / 2);
+      if (lane == 0) total = all;
+    }
+    if (Top)
+      in_order(from_top, (int)size * n_top, [&](uint64_t key, int place) {
+        if (key && place < n_top) top[place] = key;
+      });
   }
-  if (rank != 0) return;
+  __syncthreads();
   const Stat s = total;
   const bool none = s.s == 0.f;  // nothing but -inf
   const float ln = logf(s.s);
@@ -448,9 +554,9 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(
     logp[r] = tok < 0 ? 0.f : none ? -INFINITY : (load1(row.at + tok) - s.r) * scale - ln;
   }
   if (Top && tid < n_top) {
-    const uint64_t k = top[tid];
-    top_ids[r * n_top + tid] = key_id(k);
-    top_logp[r * n_top + tid] = none ? -INFINITY : (key_value(k) - s.r) * scale - ln;
+    const uint64_t key = top[tid];
+    top_ids[r * n_top + tid] = key_id(key);
+    top_logp[r * n_top + tid] = none ? -INFINITY : (key_value(key) - s.r) * scale - ln;
   }
 }
 

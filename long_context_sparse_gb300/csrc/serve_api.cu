@@ -28,6 +28,8 @@ dsa_status_t check_serve(const dsa_serve_config_t* c, int which) {
     if (c->d_qk != 128 && c->d_qk != 256 && c->d_qk != 512) return DSA_ERR_UNSUPPORTED_SHAPE;
     if (c->d_v != c->d_qk) return DSA_ERR_UNSUPPORTED_SHAPE;
   }
+  if (which == DSA_SERVE_WS_EVICT && (int64_t)c->max_blocks * p > (int64_t)1 << 22)
+    return DSA_ERR_UNSUPPORTED_SHAPE;
   if (which == DSA_SERVE_WS_PREFIX || which == DSA_SERVE_WS_WEIGHTS) {
     if (c->attn_heads > 128) return DSA_ERR_UNSUPPORTED_SHAPE;
     if (c->max_tokens * c->attn_heads > kMaxRows) return DSA_ERR_UNSUPPORTED_SHAPE;

@@ -138,7 +138,7 @@ def test_evict_refusals(lib):
     assert call(at, keep=None) == 1 and call(at, k=None) == 1
     assert call(at, k=at["k"] + 8) == 4 and call(at, ws=at["ws"] + 16) == 4
     assert call(at, ws_bytes=nb - 1) == 3
-    for over in (dict(d_qk=96, d_v=96), dict(page_size=48)):
+    for over in (dict(d_qk=96, d_v=96), dict(page_size=48), dict(max_blocks=(1 << 16) + 1)):
         with pytest.raises(dsa.DsaError) as e:
             dsa.serve_workspace_size(scfg(**over), dsa.SERVE_WS_EVICT)
         assert e.value.code == 2
