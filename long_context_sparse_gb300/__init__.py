@@ -1174,6 +1174,12 @@ def _check_logits(t, name):
     return t.get_device(), rows, vocab, ld
 
 
+@functools.lru_cache(maxsize=256)
+def _logprobs_config(rows, vocab, ld, dtype, n_top, scale):
+    """The C struct by reference (the calls read it only)."""
+    return ctypes.byref(_CLogprobsConfig(rows, vocab, ld, _LOGIT_DTYPES[dtype], n_top, scale, 0))
+
+
 def _logprobs_ws(ws, dev):
     if ws is None:
         ws = logprobs_workspace(torch.device("cuda", dev))
@@ -1203,18 +1209,25 @@ def token_logprobs(logits, tokens, n_top: int = 0, scale: float = 1.0,
         raise ValueError("n_top must be in 0 .. min(64, vocab)")
     p_tok = _check_tensor(tokens, "tokens", i32, (rows,), dev)
     if out is None:
-        at = torch.device("cuda", dev)
-        out = TokenLogprobs(*(torch.empty(rows, dtype=f32, device=at) for _ in range(3)),
-                            torch.empty((rows, n_top), dtype=i32, device=at),
-                            torch.empty((rows, n_top), dtype=f32, device=at))
-    p = [_check_tensor(t, name, f32, (rows,), dev)
-         for t, name in zip(out[:3], ("logp", "lse", "entropy"))]
-    p_ids = _check_tensor(out.top_ids, "top_ids", i32, (rows, n_top), dev) if n_top else None
-    p_top = _check_tensor(out.top_logp, "top_logp", f32, (rows, n_top), dev) if n_top else None
+        # one allocation for the floats: this call is small when the rows are few
+        at = logits.device
+        flat = torch.empty(rows * (3 + n_top), dtype=f32, device=at)
+        p = flat.data_ptr()
+        logp, lse, entropy, top = flat.split_with_sizes((rows, rows, rows, rows * n_top))
+        ids = torch.empty((rows, n_top), dtype=i32, device=at)
+        out = TokenLogprobs(logp, lse, entropy, ids, top.view(rows, n_top))
+        p, p_ids, p_top = (p, p + 4 * rows, p + 8 * rows), ids.data_ptr(), p + 12 * rows
+    else:
+        p = [_check_tensor(t, name, f32, (rows,), dev)
+             for t, name in zip(out[:3], ("logp", "lse", "entropy"))]
+        p_ids = _check_tensor(out.top_ids, "top_ids", i32, (rows, n_top), dev)
+        p_top = _check_tensor(out.top_logp, "top_logp", f32, (rows, n_top), dev)
+    if n_top == 0:
+        p_ids = p_top = None
     ws, p_ws, n_ws = _logprobs_ws(ws, dev)
-    cc = _CLogprobsConfig(rows, vocab, ld, _LOGIT_DTYPES[logits.dtype], n_top, float(scale), 0)
-    _serve_call("dsa_token_logprobs", dev, ctypes.byref(cc), logits.data_ptr(), p_tok, *p, p_ids,
-                p_top, p_ws, n_ws)
+    _serve_call("dsa_token_logprobs", dev,
+                _logprobs_config(rows, vocab, ld, logits.dtype, n_top, float(scale)),
+                logits.data_ptr(), p_tok, *p, p_ids, p_top, p_ws, n_ws)
     return out
 
 
@@ -1233,12 +1246,14 @@ def token_logprobs_bwd(logits, tokens, lse, entropy, g_logp, g_entropy=None,
         raise ValueError("g_entropy needs entropy")
     p_ent, p_g, p_h = opt(entropy, "entropy"), opt(g_logp, "g_logp"), opt(g_entropy, "g_entropy")
     if dlogits is None:
-        dlogits = torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
-    d_dev, d_rows, d_vocab, d_ld = _check_logits(dlogits, "dlogits")
-    if (d_dev, d_rows, d_vocab, dlogits.dtype) != (dev, rows, vocab, logits.dtype):
-        raise ValueError("dlogits must match logits")
+        dlogits, d_ld = torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device), vocab
+    else:
+        d_dev, d_rows, d_vocab, d_ld = _check_logits(dlogits, "dlogits")
+        if (d_dev, d_rows, d_vocab, dlogits.dtype) != (dev, rows, vocab, logits.dtype):
+            raise ValueError("dlogits must match logits")
     ws, p_ws, n_ws = _logprobs_ws(ws, dev)
-    cc = _CLogprobsConfig(rows, vocab, ld, _LOGIT_DTYPES[logits.dtype], 0, float(scale), 0)
-    _serve_call("dsa_token_logprobs_bwd", dev, ctypes.byref(cc), logits.data_ptr(), p_tok, p_lse,
-                p_ent, p_g, p_h, dlogits.data_ptr(), d_ld, p_ws, n_ws)
+    _serve_call("dsa_token_logprobs_bwd", dev,
+                _logprobs_config(rows, vocab, ld, logits.dtype, 0, float(scale)),
+                logits.data_ptr(), p_tok, p_lse, p_ent, p_g, p_h, dlogits.data_ptr(), d_ld, p_ws,
+                n_ws)
     return dlogits

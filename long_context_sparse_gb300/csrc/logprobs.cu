@@ -22,8 +22,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 4;      // 16-byte vectors of a thread in flight: a batch
 constexpr int kMaxTop = 64;
 constexpr int kKept = 4;        // batches that a thread remembers
-constexpr int kBuf = 512;       // candidates of a CTA
+constexpr int kBuf = 512;       // candidates of a CTA; its cluster's alternatives
 constexpr int kMaxCluster = 8;  // CTAs of a row
+static_assert(kMaxTop * kMaxCluster <= kBuf, "the leader's buffer");
 constexpr float kUnset = -3.402823466e38f;  // reference of nothing but -inf
 constexpr float kNever = -16384.f;          // 2^ of it is 0
 
@@ -207,10 +208,10 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 //
 // Alternatives, exactly and in the same pass: each thread remembers its kKept
 // batches with the largest maxima.  A value that n of the threads' best elements
-// reach is a bound for the n best of the share (here: what k threads of each of the
-// 8 warps reach, 8 k >= n, found by k maxima over a warp), so that only the batches
-// whose maximum reaches it are looked at again, in L2, and few elements of those
-// pass.  A thread of which more batches than it remembers may reach the bound sends
+// reach is a bound for the n best of the share: here the n-th largest of what the k
+// best threads of each of the 8 warps have, 8 k >= n.  Only the batches whose maximum
+// reaches it are looked at again, in L2, an element a lane, and few elements of
+// those pass.  A thread of which more batches than it remembers may reach the bound sends
 // the share through a second look at all of it.  Where more elements pass than the
 // buffer holds (rows of many equal values), ids break the ties already in the bound;
 // and should that not do either, `n` passes each look for the largest below the last.
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
   // the leader's: what the cluster's CTAs have found
   __shared__ Stat from[kMaxCluster];
   __shared__ alignas(16) uint64_t from_top[Top ? kMaxTop * kMaxCluster : 2];
-  __shared__ uint32_t warp_bound[kWarps];
+  __shared__ uint32_t warp_best[kMaxTop + kWarps];
   __shared__ uint32_t n_buf, again;
   __shared__ uint64_t bound;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -369,37 +370,20 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
   merge_lanes(16);
   if (lane == 0) stats[warp] = all;
   if (tid == 0) n_buf = again = 0u;
-  // the elements of one of the thread's batches: f(value, id), at least of those whose
-  // order key reaches `floor`
-  auto visit = [&](int32_t number, uint32_t floor, auto f) {
-    if (number < 0) {
-      f(load1(row.at + row.single(tid)), (uint32_t)row.single(tid));
-      return;
-    }
-    const int32_t v = v0 + tid + number * kStep;
-    uint32_t w[kWords];
-    load(v, w);
-#pragma unroll 1
-    for (int u = 0; u < kUnroll && v + u * kThreads < v1; ++u) {
-      const uint32_t id = (uint32_t)row.id(v + u * kThreads);
-      uint32_t four[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        four[i] = u == 0 ? w[i] : u == 1 ? w[4 + i] : u == 2 ? w[8 + i] : w[12 + i];
-      float x[W::kPer];
-      W::get(W::max(W::max(four[0], four[1]), W::max(four[2], four[3])), x);
-      if (order_key(W::kPer == 2 ? fmaxf(x[0], x[W::kPer - 1]) : x[0]) < floor) continue;
+  // all elements of the thread's share: f(value, id)
+  auto visit_all = [&](auto f) {
+    if (tid < n_single) f(load1(row.at + row.single(tid)), (uint32_t)row.single(tid));
+    for (int32_t v = v0 + tid; v < v1; v += kThreads) {
+      const uint4 q = ld_input(vec + v);
+      const uint32_t four[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        float x[W::kPer];
         W::get(four[i], x);
 #pragma unroll
-        for (int e = 0; e < W::kPer; ++e) f(x[e], id + i * W::kPer + e);
+        for (int e = 0; e < W::kPer; ++e) f(x[e], (uint32_t)(row.id(v) + i * W::kPer + e));
       }
     }
-  };
-  auto visit_all = [&](uint32_t floor, auto f) {
-    if (tid < n_single) visit(-1, floor, f);
-    for (int32_t q = 0; q < batches; ++q) visit(q, floor, f);
   };
   // the n keys of `list` in order: f(key, place); all threads
   auto in_order = [&](const uint64_t* list, int n, auto f) {
@@ -421,19 +405,33 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
     // the threads that have vectors come first; whole warps of them have k each
     const int full = min(kThreads, v1 - v0) >> 5, k = full ? (n_top + full - 1) / full : 33;
     if (k <= 32 && warp < full) {
-      uint32_t mine = kept[0], reached = 0u;
+      uint32_t mine = kept[0];
       for (int i = 0; i < k; ++i) {
-        reached = __reduce_max_sync(0xffffffffu, mine);
+        const uint32_t reached = __reduce_max_sync(0xffffffffu, mine);
         const uint32_t who = __ballot_sync(0xffffffffu, mine == reached);
         if (lane == __ffs(who) - 1) mine = 0u;
+        if (lane == 0) warp_best[warp * k + i] = reached;
       }
-      if (lane == 0) warp_bound[warp] = reached;
     }
     if (tid < kMaxTop) top[tid] = 0ull;
     __syncthreads();
-    uint32_t least = k <= 32 ? 0xffffffffu : 0u;
-    if (k <= 32)
-      for (int x = 0; x < full; ++x) least = min(least, warp_bound[x]);
+    uint32_t least = 0u;
+    if (k <= 32) {  // full * k values, at most full - 1 of them beyond the n-th
+      const int list = full * k;
+      uint32_t a = lane < list ? warp_best[lane] : ~0u;
+      uint32_t b = lane + 32 < list ? warp_best[lane + 32] : ~0u;
+      uint32_t c3 = lane + 64 < list ? warp_best[lane + 64] : ~0u;
+      for (int i = n_top; i <= list; ++i) {
+        least = __reduce_min_sync(0xffffffffu, min(min(a, b), c3));
+        const uint32_t who =
+            __ballot_sync(0xffffffffu, a == least || b == least || c3 == least);
+        if (lane == __ffs(who) - 1) {
+          if (a == least) a = ~0u;
+          else if (b == least) b = ~0u;
+          else c3 = ~0u;
+        }
+      }
+    }
     uint64_t at_least = (uint64_t)least << 32;
     auto push = [&](float x, uint32_t id) {
       const uint64_t key = full_key(x, id);
@@ -441,14 +439,37 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
       const uint32_t i = atomicAdd(&n_buf, 1u);
       if (i < kBuf) buf[i] = key;
     };
-    if (kept[0] && kept[0] >= least) {
-      if (kept[kKept - 1] >= least && batches + (tid < n_single) > kKept) again = 1u;
-#pragma unroll 1
-      for (int q = 0; q < kKept; ++q) {
-        const uint32_t kq = q == 0 ? kept[0] : q == 1 ? kept[1] : q == 2 ? kept[2] : kept[3];
-        const int32_t wq = q == 0 ? which[0] : q == 1 ? which[1] : q == 2 ? which[2] : which[3];
-        if (kq == 0u || kq < least) break;
-        visit(wq, least, push);
+    if (kept[kKept - 1] && kept[kKept - 1] >= least && batches + (tid < n_single) > kKept)
+      again = 1u;
+    constexpr int kElems = kUnroll * Row<T>::kVec, kPerLoad = 32 / kElems, kLoads = 4;
+#pragma unroll
+    for (int q = 0; q < kKept; ++q) {
+      uint32_t who = __ballot_sync(0xffffffffu, kept[q] && kept[q] >= least);
+      while (who) {
+        float x[kLoads];
+        uint32_t id[kLoads];
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          int l = -1;  // the lane whose batch this lane looks at
+#pragma unroll
+          for (int h = 0; h < kPerLoad; ++h) {
+            if (lane / kElems == h) l = __ffs(who) - 1;
+            who &= who - 1u;
+          }
+          const int32_t number = __shfl_sync(0xffffffffu, which[q], l < 0 ? 0 : l);
+          const int e = lane % kElems, t = (warp << 5) + l;
+          id[i] = ~0u;
+          if (l >= 0 && number < 0) {
+            if (e == 0) id[i] = (uint32_t)row.single(t);
+          } else if (l >= 0) {
+            const int32_t v = v0 + t + number * kStep + e / Row<T>::kVec * kThreads;
+            if (v < v1) id[i] = (uint32_t)(row.id(v) + e % Row<T>::kVec);
+          }
+          if (id[i] != ~0u) x[i] = load1(row.at + id[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+          if (id[i] != ~0u) push(x[i], id[i]);
       }
     }
     __syncthreads();
@@ -456,13 +477,13 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
       __syncthreads();
       if (tid == 0) n_buf = 0u;
       __syncthreads();
-      visit_all(least, push);
+      visit_all(push);
       __syncthreads();
     }
     if (n_buf > kBuf) {
       // the n-th largest of the threads' best elements, by value and id
       uint64_t mine = 0ull;
-      visit_all(0u, [&](float x, uint32_t id) {
+      visit_all([&](float x, uint32_t id) {
         const uint64_t f = full_key(x, id);
         mine = f > mine ? f : mine;
       });
@@ -478,14 +499,14 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
       if (tid == 0) n_buf = 0u;
       __syncthreads();
       at_least = bound;
-      if (mine >= at_least) visit_all((uint32_t)(at_least >> 32), push);
+      if (mine >= at_least) visit_all(push);
       __syncthreads();
     }
     if (n_buf > kBuf) {
       uint64_t last = ~0ull;
       for (int i = 0; i < n_top; ++i) {
         uint64_t most = 0ull;
-        visit_all(0u, [&](float x, uint32_t id) {
+        visit_all([&](float x, uint32_t id) {
           const uint64_t f = full_key(x, id);
           if (f < last && f > most) most = f;
         });
@@ -534,10 +555,22 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
       merge_lanes(kMaxCluster / 2);
       if (lane == 0) total = all;
     }
-    if (Top)
-      in_order(from_top, (int)size * n_top, [&](uint64_t key, int place) {
-        if (key && place < n_top) top[place] = key;
+    if (Top) {
+      // none below the largest of the CTAs' n-th ones is among the row's n
+      uint64_t least = 0ull;
+      for (uint32_t g = 0; g < size; ++g) {
+        const uint64_t last = from_top[(g + 1) * n_top - 1];
+        least = last > least ? last : least;
+      }
+      if (tid == 0) n_buf = 0u;
+      __syncthreads();
+      for (int i = tid; i < (int)size * n_top; i += kThreads)
+        if (from_top[i] && from_top[i] >= least) buf[atomicAdd(&n_buf, 1u)] = from_top[i];
+      __syncthreads();
+      in_order(buf, (int)n_buf, [&](uint64_t key, int place) {
+        if (place < n_top) top[place] = key;
       });
+    }
   }
   __syncthreads();
   const Stat s = total;
