@@ -1209,14 +1209,13 @@ def token_logprobs(logits, tokens, n_top: int = 0, scale: float = 1.0,
         raise ValueError("n_top must be in 0 .. min(64, vocab)")
     p_tok = _check_tensor(tokens, "tokens", i32, (rows,), dev)
     if out is None:
-        # one allocation for the floats: this call is small when the rows are few
         at = logits.device
-        flat = torch.empty(rows * (3 + n_top), dtype=f32, device=at)
-        p = flat.data_ptr()
-        logp, lse, entropy, top = flat.split_with_sizes((rows, rows, rows, rows * n_top))
-        ids = torch.empty((rows, n_top), dtype=i32, device=at)
-        out = TokenLogprobs(logp, lse, entropy, ids, top.view(rows, n_top))
-        p, p_ids, p_top = (p, p + 4 * rows, p + 8 * rows), ids.data_ptr(), p + 12 * rows
+        new = [torch.empty(rows, dtype=f32, device=at), torch.empty(rows, dtype=f32, device=at),
+               torch.empty(rows, dtype=f32, device=at),
+               torch.empty((rows, n_top), dtype=i32, device=at),
+               torch.empty((rows, n_top), dtype=f32, device=at)]
+        out = TokenLogprobs(*new)
+        *p, p_ids, p_top = [t.data_ptr() for t in new]
     else:
         p = [_check_tensor(t, name, f32, (rows,), dev)
              for t, name in zip(out[:3], ("logp", "lse", "entropy"))]

@@ -16,11 +16,14 @@ namespace dsa {
 namespace {
 
 constexpr int kMaxThreads = 1024;  // of a CTA of the selection
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;    // where the device has room for it, else 8
 constexpr int kMaxKeys = 40960;    // keys of a CTA's share that fit shared memory (160 KB)
 constexpr int kCopies = 8;         // of a histogram, for lanes that meet in a bin
-// two words for each 32 of the 2^22 / kMaxCluster places that a share may have
-constexpr int kMaxWordBytes = (1 << 22) / kMaxCluster / 4;
+// two words for each 32 of the 2^22 / 8 places that a share may have
+constexpr int kMaxWordBytes = (1 << 22) / 8 / 4;
+// of a CTA: its keys or as many places as it may have, and the cluster's counts
+constexpr int kMaxSmem = kMaxKeys * 4 + kMaxKeys / 4 + 2048 * kMaxCluster;
+static_assert(kMaxSmem >= kMaxWordBytes + 2048 * 8, "shared memory");
 
 // In the workspace header, behind the status word; both are 0 between calls.
 struct Counters {
@@ -59,52 +62,71 @@ __device__ __forceinline__ uint32_t order_key(float w) {
 
 // The sum of x over the threads before this one, and over all of them; every thread
 // of the CTA, `sums` [32] in shared memory, which may be used again after it.
-__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* sums, uint32_t* all) {
+__device__ __forceinline__ uint64_t block_scan(uint64_t x, uint64_t* sums, uint64_t* all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  uint32_t incl = x;
+  uint64_t incl = x;
 #pragma unroll
   for (int s = 1; s < 32; s <<= 1) {
-    const uint32_t o = __shfl_up_sync(0xffffffffu, incl, s);
+    const uint64_t o = __shfl_up_sync(0xffffffffu, incl, s);
     if (lane >= s) incl += o;
   }
   if (lane == 31) sums[warp] = incl;
   __syncthreads();
-  const uint32_t w = lane < warps ? sums[lane] : 0u;
-  const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0u);
-  *all = __reduce_add_sync(0xffffffffu, w);
+  uint64_t w = lane < warps ? sums[lane] : 0ull;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const uint64_t o = __shfl_up_sync(0xffffffffu, w, s);
+    if (lane >= s) w += o;
+  }
+  *all = __shfl_sync(0xffffffffu, w, 31);
+  const uint64_t before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
   __syncthreads();
-  return before + incl - x;
+  return (warp ? before : 0ull) + incl - x;
+}
+
+__device__ __forceinline__ void st_cluster4(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x),
+               "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ uint4 add4(const uint4& a, const uint4& b) {
+  return make_uint4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
 
 // A cluster has a request, each CTA of it consecutive places.  Cached: their keys
 // lie in shared memory, else they are read again in each pass.
 //
-// Four passes of eight bits find the left-th largest key.  Then a bit for each place
-// says whether its token stays; words of 32 places are a thread's, so that two scans
-// of population counts number the equal keys, the freed places and the movers.
+// Passes of eight bits, four at most, find the left-th largest key: each CTA counts
+// its keys, one warp adds up the cluster's counts and finds the digit.  Then a bit for
+// each place says whether its token stays, and scans of population counts over groups
+// of eight places number the equal keys, the freed places and the movers.
 template <bool Cached>
 __global__ void __launch_bounds__(kMaxThreads) select_kernel(
     const float* w, const int32_t* table, const int32_t* seq, const int32_t* keep,
     int32_t n_first, int32_t n_last, float* w_out, Moves moves, int64_t list_len,
     Counters counts, int max_blocks, int page_log2, int64_t n_pages, int max_words,
     uint32_t* status) {
-  extern __shared__ uint32_t smem[];
-  uint32_t* above_w = smem;               // [word] keys above the threshold
-  uint32_t* equal_w = smem + max_words;   // [word] keys equal to it
-  uint32_t* keys = smem + 2 * max_words;
-  __shared__ uint32_t hist[kCopies][257];
-  __shared__ uint32_t sum_hist[2][256];   // of this CTA, in turns
-  __shared__ uint32_t sums[32];
+  extern __shared__ __align__(16) uint32_t smem[];
+  uint32_t rank, size;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
+  uint32_t* cluster_sums = smem;  // [turn][CTA][256] where there are several CTAs, by 16 bytes
+  uint32_t* above_w = smem + (size > 1 ? 512 * size : 0u);  // [word of 32 places] keys above
+  uint32_t* equal_w = above_w + max_words;                  // the threshold; equal to it
+  uint32_t* keys = equal_w + max_words;
+  __shared__ alignas(16) uint32_t hist[2][kCopies][256];  // in turns
+  __shared__ uint64_t sums[32];
   __shared__ uint32_t found[3];           // the digit, keys above it, keys with it
   __shared__ uint32_t totals[2];          // freed places and movers of this CTA
   __shared__ uint32_t first_move;         // of the request, in the leader
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
-  uint32_t rank, size;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
   const int b = blockIdx.x / size;
+  for (int i = tid; i < kCopies * 64; i += nt)
+    reinterpret_cast<uint4*>(hist[0])[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (size > 1) cluster_arrive();  // this CTA has begun: its shared memory may be written to
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (size > 1) cluster_wait();
   const int32_t cap = max_blocks << page_log2, in_page = (1 << page_log2) - 1;
   const int32_t n = ld_input(seq + b), want = ld_input(keep + b);
   if (n < 0 || n > cap || want < 0) {  // the same in the whole cluster
@@ -115,164 +137,247 @@ __global__ void __launch_bounds__(kMaxThreads) select_kernel(
   const int32_t* row = table + (int64_t)b * max_blocks;
   const int32_t share = ((n + (int)size - 1) / (int)size + 31) & ~31;
   const int32_t lo = min(n, (int)rank * share), hi = min(n, lo + share);
-  auto slot_of = [&](int32_t j) -> int32_t {
-    const int32_t p = ld_input(row + (j >> page_log2));
+  // the slot of place j on page p, or -1
+  auto slot_on = [&](int32_t p, int32_t j) -> int32_t {
     if (p < 0 || p >= n_pages) {
       latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
       return -1;
     }
     return (p << page_log2) + (j & in_page);
   };
+  // f(j, slot, weight) of the places j0, j0 + nt, .. below `end` that `which` picks:
+  // kAhead pages, then kAhead weights on their way at a time
+  auto weights_of = [&](int32_t j0, int32_t end, auto which, auto f) {
+    constexpr int kAhead = 4;
+    for (; j0 < end; j0 += kAhead * nt) {
+      int32_t p[kAhead], s[kAhead];
+      float x[kAhead];
+      bool on[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int32_t j = j0 + u * nt;
+        on[u] = j < end && which(j);
+        if (on[u]) p[u] = ld_input(row + (j >> page_log2));
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        s[u] = on[u] ? slot_on(p[u], j0 + u * nt) : -1;
+        if (s[u] >= 0) x[u] = ld_input_f(w + s[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (on[u]) f(j0 + u * nt, s[u], x[u]);
+    }
+  };
+  auto any = [](int32_t) { return true; };
   if (left == n || left == 0) {  // all stay, or none
     if (w_out != w)
-      for (int32_t j = lo + tid; j < min(hi, left); j += nt) {
-        const int32_t s = slot_of(j);
-        if (s >= 0) w_out[s] = ld_input_f(w + s);
-      }
+      weights_of(lo + tid, min(hi, left), any, [&](int32_t, int32_t s, float x) {
+        if (s >= 0) w_out[s] = x;
+      });
     return;
   }
-  auto read_key = [&](int32_t j) -> uint32_t {
-    if (j < n_first || j >= n - n_last) return 0xff800000u;  // +inf
-    const int32_t s = slot_of(j);
-    return s < 0 ? 0u : order_key(ld_input_f(w + s));
+  auto fixed = [&](int32_t j) { return j < n_first || j >= n - n_last; };
+  auto to_key = [&](int32_t j, int32_t s, float x) {
+    return fixed(j) ? 0xff800000u /* +inf */ : s < 0 ? 0u : order_key(x);
   };
-  auto key_of = [&](int32_t j) { return Cached ? keys[j - lo] : read_key(j); };
-  if (Cached) {
+  if (Cached)
+    weights_of(lo + tid, hi, any,
+               [&](int32_t j, int32_t s, float x) { keys[j - lo] = to_key(j, s, x); });
+  // f(j, key) of the places j0, j0 + nt, .. below hi
+  auto each_key = [&](int32_t j0, auto f) {
+    if (Cached) {
 #pragma unroll 4
-    for (int32_t j = lo + tid; j < hi; j += nt) keys[j - lo] = read_key(j);
-  }
+      for (int32_t j = j0; j < hi; j += nt) f(j, keys[j - lo]);
+    } else {
+      weights_of(j0, hi, any, [&](int32_t j, int32_t s, float x) { f(j, to_key(j, s, x)); });
+    }
+  };
 
   // ---- the left-th largest key, eight bits at a time from the top
-  uint32_t prefix = 0u;            // its bits so far
+  uint32_t prefix = 0u;            // its bits so far, the rest 0
   uint32_t rest = (uint32_t)left;  // its rank among the keys with that prefix
-  uint32_t ties = 0u;              // keys equal to it in the CTAs before
-  uint32_t* mine = hist[lane & (kCopies - 1)];
+  int last = 0;                    // the buffer of the last pass
+  __syncthreads();
   for (int pass = 0; pass < 4; ++pass) {
-    const int shift = 24 - 8 * pass;
-    for (int i = tid; i < kCopies * 257; i += nt) hist[i / 257][i % 257] = 0u;
-    __syncthreads();
+    const int shift = 24 - 8 * pass, turn = pass & 1;
     const uint32_t above = pass ? 0xffffffffu << (shift + 8) : 0u;
-#pragma unroll 4
-    for (int32_t j = lo + tid; j < hi; j += nt) {
-      const uint32_t k = key_of(j);
+    uint32_t* mine = hist[turn][lane & (kCopies - 1)];
+    each_key(lo + tid, [&](int32_t, uint32_t k) {
       if ((k & above) == prefix) atomicAdd(mine + ((k >> shift) & 255u), 1u);
-    }
+    });
     __syncthreads();
-    // of this CTA, then of the cluster; thread t has digit 255 - t
-    uint32_t* here = sum_hist[pass & 1];
-    uint32_t all = 0u;
-    if (tid < 256) {
-      for (int i = 0; i < kCopies; ++i) all += hist[i][255 - tid];
-      here[255 - tid] = all;
+    // lane l of a warp has the digits 8 l' .. 8 l' + 7, l' = 31 - l
+    const int d0 = 8 * (31 - lane);
+    uint4 a = make_uint4(0u, 0u, 0u, 0u), c = a;
+    if (warp == 0) {
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) {
+        a = add4(a, *reinterpret_cast<const uint4*>(&hist[turn][i][d0]));
+        c = add4(c, *reinterpret_cast<const uint4*>(&hist[turn][i][d0 + 4]));
+      }
+      if (size > 1) {  // to every CTA of the cluster
+        const uint32_t at = smem_u32(cluster_sums + (turn * size + rank) * 256 + d0);
+        for (uint32_t r = 0; r < size; ++r) {
+          st_cluster4(at_rank(at, r), a);
+          st_cluster4(at_rank(at, r) + 16, c);
+        }
+      }
+    } else {
+      for (int i = tid - 32; i < kCopies * 64; i += nt - 32)  // for the next pass
+        reinterpret_cast<uint4*>(hist[turn ^ 1])[i] = make_uint4(0u, 0u, 0u, 0u);
     }
     if (size > 1) {
-      // (the other buffer is read until the barrier of the next pass)
+      // (the other turn's sums are read until the barrier of the next pass)
       cluster_arrive();
       cluster_wait();
-      if (tid < 256) {
-        all = 0u;
-        const uint32_t at = smem_u32(here + 255 - tid);
-        uint32_t c[kMaxCluster];
-#pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r) c[r] = r < (int)size ? ld_cluster(at_rank(at, r)) : 0u;
-#pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r) all += c[r];
+      if (warp == 0) {
+        a = c = make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t* from = cluster_sums + turn * size * 256 + d0;
+        for (uint32_t r = 0; r < size; ++r) {
+          a = add4(a, *reinterpret_cast<const uint4*>(from + r * 256));
+          c = add4(c, *reinterpret_cast<const uint4*>(from + r * 256 + 4));
+        }
       }
     }
-    uint32_t sum;
-    const uint32_t before = block_scan(tid < 256 ? all : 0u, sums, &sum);
-    if (tid < 256 && before < rest && rest <= before + all) {
-      found[0] = 255u - tid;
-      found[1] = before;
-      found[2] = all;
+    if (warp == 0) {
+      const uint32_t n8[8] = {c.w, c.z, c.y, c.x, a.w, a.z, a.y, a.x};  // digits downwards
+      uint32_t sum = 0u;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum += n8[e];
+      uint32_t before = sum;
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) {
+        const uint32_t o = __shfl_up_sync(0xffffffffu, before, s);
+        if (lane >= s) before += o;
+      }
+      before -= sum;
+      if (before < rest && rest <= before + sum) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (before < rest && rest <= before + n8[e]) {
+            found[0] = (uint32_t)(d0 + 7 - e);
+            found[1] = before;
+            found[2] = n8[e];
+          }
+          before += n8[e];
+        }
+      }
     }
     __syncthreads();
     prefix |= found[0] << shift;
     rest -= found[1];
+    last = turn;
+    if (rest == found[2]) break;  // all keys with this prefix stay: the same in the cluster
   }
   const bool all_ties = rest == found[2];
+  uint32_t ties = 0u;  // equal keys in the CTAs before
   if (!all_ties)
     for (uint32_t r = 0; r < rank; ++r)
-      ties += ld_cluster(at_rank(smem_u32(sum_hist[1] + found[0]), r));
+      ties += cluster_sums[(last * size + r) * 256 + found[0]];
 
   // ---- which keys are above the threshold, which equal to it: a bit each
   const int words = (hi - lo + 31) >> 5;
+  {
+    const int32_t first = lo + 32 * warp + lane;  // whole warps, in step
+    auto flags = [&](int32_t j, uint32_t k) {
+      const uint32_t gt = __ballot_sync(0xffffffffu, j < hi && k > prefix);
+      const uint32_t eq = __ballot_sync(0xffffffffu, j < hi && k == prefix);
+      if (lane == 0) {
+        above_w[(j - lo) >> 5] = gt;
+        equal_w[(j - lo) >> 5] = eq;
+      }
+    };
 #pragma unroll 4
-  for (int x = warp; x < words; x += nt >> 5) {
-    const int32_t j = lo + 32 * x + lane;
-    const uint32_t k = j < hi ? key_of(j) : 0u;
-    const uint32_t gt = __ballot_sync(0xffffffffu, j < hi && k > prefix);
-    const uint32_t eq = __ballot_sync(0xffffffffu, j < hi && k == prefix);
-    if (lane == 0) {
-      above_w[x] = gt;
-      equal_w[x] = eq;
+    for (int32_t j = first; j - lane < hi; j += nt) {
+      uint32_t k = 0u;
+      if (j < hi) {
+        if (Cached) k = keys[j - lo];
+        else if (fixed(j)) k = 0xff800000u;
+        else {
+          const int32_t s = slot_on(ld_input(row + (j >> page_log2)), j);
+          k = s < 0 ? 0u : order_key(ld_input_f(w + s));
+        }
+      }
+      flags(j, k);
     }
   }
   __syncthreads();
   // ---- `rest` of the equal ones stay, those of the lowest places; each thread has
-  // consecutive words
-  const int each = (words + nt - 1) / nt, x0 = min(words, tid * each), x1 = min(words, x0 + each);
-  uint32_t all;
+  // consecutive groups of eight places
+  uint8_t* above_b = reinterpret_cast<uint8_t*>(above_w);
+  uint8_t* equal_b = reinterpret_cast<uint8_t*>(equal_w);
+  const int groups = 4 * words, each = (groups + nt - 1) / nt;
+  const int x0 = min(groups, tid * each), x1 = min(groups, x0 + each);
+  // the page of this thread's first group, on its way meanwhile
+  int32_t page = x0 < x1 && lo + 8 * x0 < n ? ld_input(row + ((lo + 8 * x0) >> page_log2)) : -1;
+  uint64_t all;
   if (!all_ties) {
     uint32_t eq = 0u;
-    for (int x = x0; x < x1; ++x) eq += __popc(equal_w[x]);
-    uint32_t at = ties + block_scan(eq, sums, &all);
+    for (int x = x0; x < x1; ++x) eq += __popc(equal_b[x]);
+    uint32_t at = ties + (uint32_t)block_scan(eq, sums, &all);
     for (int x = x0; x < x1; ++x) {
-      uint32_t e = equal_w[x], stay = 0u;
+      uint32_t e = equal_b[x], stay = 0u;
       for (; e && at < rest; ++at) {
         stay |= e & (0u - e);
         e &= e - 1u;
       }
       at += __popc(e);
-      equal_w[x] = stay;
+      equal_b[x] = (uint8_t)stay;
     }
   }
-  // the places of word x that are below `end`
+  // the places of group x that are below `end`
   auto below = [&](int x, int32_t end) {
-    const int32_t m = end - lo - 32 * x;
-    return m <= 0 ? 0u : m >= 32 ? 0xffffffffu : (1u << m) - 1u;
+    const int32_t m = end - lo - 8 * x;
+    return m <= 0 ? 0u : m >= 8 ? 0xffu : (1u << m) - 1u;
   };
-  uint32_t n_holes = 0u, n_movers = 0u;
+  uint64_t mine = 0ull;  // freed places, movers << 32
   for (int x = x0; x < x1; ++x) {
-    const uint32_t kept = above_w[x] | equal_w[x], low = below(x, left);
-    above_w[x] = kept;
-    n_holes += __popc(~kept & low & below(x, hi));
-    n_movers += __popc(kept & ~low);
+    const uint32_t kept = above_b[x] | equal_b[x], low = below(x, left);
+    above_b[x] = (uint8_t)kept;
+    mine += __popc(~kept & low & below(x, hi)) + ((uint64_t)__popc(kept & ~low) << 32);
   }
-  uint32_t h = block_scan(n_holes, sums, &all);
-  if (tid == 0) totals[0] = all;
-  uint32_t m = block_scan(n_movers, sums, &all);
-  if (tid == 0) totals[1] = all;
+  mine = block_scan(mine, sums, &all);
+  uint32_t h = (uint32_t)mine, m = (uint32_t)(mine >> 32);
+  if (tid == 0) {
+    totals[0] = (uint32_t)all;
+    totals[1] = (uint32_t)(all >> 32);
+  }
   __syncthreads();
-  uint32_t all_moves = 0u;
   if (size > 1) {
     cluster_arrive();
     cluster_wait();
-  }
-#pragma unroll
-  for (int r = 0; r < kMaxCluster; ++r)
-    if (r < (int)size) {
-      const uint32_t a = ld_cluster(at_rank(smem_u32(totals), r));
-      all_moves += a;
-      if (r < (int)rank) {
-        h += a;
-        m += ld_cluster(at_rank(smem_u32(totals + 1), r));
-      }
+    // lane r has CTA r's
+    uint32_t freed = 0u, movers = 0u;
+    if (lane < (int)size) {
+      freed = ld_cluster(at_rank(smem_u32(totals), lane));
+      movers = ld_cluster(at_rank(smem_u32(totals + 1), lane));
     }
+    h += __reduce_add_sync(0xffffffffu, lane < (int)rank ? freed : 0u);
+    m += __reduce_add_sync(0xffffffffu, lane < (int)rank ? movers : 0u);
+    all = __reduce_add_sync(0xffffffffu, freed);
+  }
   if (rank == 0 && tid == 0) {
-    const int32_t at = all_moves ? atomicAdd(counts.moves, (int32_t)all_moves) : 0;
+    const uint32_t count = (uint32_t)all;
+    const int32_t at = count ? atomicAdd(counts.moves, (int32_t)count) : 0;
     // a page that stands in two places: more moves than the cache has slots for
-    const bool fits = at >= 0 && at + (int64_t)all_moves <= list_len;
+    const bool fits = at >= 0 && at + (int64_t)count <= list_len;
     if (!fits) latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
     first_move = fits ? (uint32_t)at : 0xffffffffu;
   }
-  if (w_out != w) {  // the tokens that stay where they are
-#pragma unroll 4
-    for (int32_t j = lo + tid; j < min(hi, left); j += nt)
-      if (above_w[(j - lo) >> 5] >> ((j - lo) & 31) & 1u) {
-        const int32_t s = slot_of(j);
-        if (s >= 0) w_out[s] = ld_input_f(w + s);
-      }
+  if (w_out != w) {
+    // the tokens that stay where they are; each CTA has as many places below `left`,
+    // whosever share they lie in
+    const int32_t part = (left + (int)size - 1) / (int)size, from = min(left, (int)rank * part);
+    weights_of(
+        from + tid, min(left, from + part),
+        [&](int32_t j) {
+          const uint32_t r = (uint32_t)(j / share), i = (uint32_t)(j - (int)r * share);
+          return (ld_cluster(at_rank(smem_u32(above_w + (i >> 5)), r)) >> (i & 31u) & 1u) != 0u;
+        },
+        [&](int32_t, int32_t s, float x) {
+          if (s >= 0) w_out[s] = x;
+        });
   }
   __syncthreads();
   if (size > 1) {
@@ -284,32 +389,30 @@ __global__ void __launch_bounds__(kMaxThreads) select_kernel(
   if (size > 1) cluster_arrive();
   if (at != 0xffffffffu) {
     for (int x = x0; x < x1; ++x) {
-      const uint32_t kept = above_w[x], low = below(x, left);
+      const int32_t j = lo + 8 * x;  // eight places lie on one page
+      const uint32_t kept = above_b[x], low = below(x, left);
       uint32_t holes = ~kept & low & below(x, hi), movers = kept & ~low;
-      int32_t page = -1, first = 0;  // the page of the last place, its first slot
-      auto slot = [&](uint32_t bit) {
-        const int32_t j = lo + 32 * x + (int)bit;
-        if (j >> page_log2 != page) {
-          page = j >> page_log2;
-          first = slot_of(page << page_log2);
-        }
-        return first < 0 ? -1 : first + (j & in_page);
-      };
-      for (; holes; holes &= holes - 1u) moves.dst[at + h++] = slot(__ffs(holes) - 1);
-      for (; movers; movers &= movers - 1u) moves.src[at + m++] = slot(__ffs(movers) - 1);
+      if (x > x0 && (holes | movers)) page = ld_input(row + (j >> page_log2));
+      const int32_t slot = holes | movers ? slot_on(page, j) : -1;
+      for (; holes; holes &= holes - 1u)
+        moves.dst[at + h++] = slot < 0 ? -1 : slot + __ffs(holes) - 1;
+      for (; movers; movers &= movers - 1u)
+        moves.src[at + m++] = slot < 0 ? -1 : slot + __ffs(movers) - 1;
     }
   }
   if (size > 1) cluster_wait();
 }
 
+constexpr int kMoveBlocks = 5;  // on an SM
+
 // A warp takes kRows rows at a time, 16 bytes a lane and load; the list's entries of
 // its next rows are on their way while it copies.
 template <int D, bool V>
-__global__ void __launch_bounds__(256) move_kernel(Moves moves, int64_t list_len, uint4* k_pages,
+__global__ void __launch_bounds__(256, kMoveBlocks) move_kernel(Moves moves, int64_t list_len, uint4* k_pages,
                                                    uint4* v_pages, const float* w, float* w_out,
                                                    Counters counts, int64_t n_slots) {
   constexpr int kPieces = D / 8;                     // of a row
-  constexpr int kRows = (V ? 128 : 256) / kPieces;   // 8 loads a lane
+  constexpr int kRows = (V ? 64 : 128) / kPieces;    // 4 loads a lane
   constexpr int kLoads = kRows * kPieces / 32;       // of a tensor
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -362,35 +465,65 @@ __global__ void __launch_bounds__(256) move_kernel(Moves moves, int64_t list_len
 
 }  // namespace
 
+namespace {
+
+// Whether a cluster of kMaxCluster of the selection's largest CTAs finds room.
+bool fits_wide(int smem) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kMaxCluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kMaxCluster);
+  cfg.blockDim = dim3(kMaxThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, select_kernel<true>, &cfg) == cudaSuccess) return n > 0;
+  cudaGetLastError();
+  return false;
+}
+
+}  // namespace
+
 size_t evict_ws(const ServeShape& s) { return 2 * round_up((size_t)max_moves(s), 64) * 4; }
 
 cudaError_t launch_evict(const LaunchCtx& c, const ServeShape& s, const float* w_pages,
                          const int32_t* table, const int32_t* seq, const int32_t* keep,
                          int32_t n_first, int32_t n_last, __nv_bfloat16* k_pages,
                          __nv_bfloat16* v_pages, float* w_out, uint8_t* ws) {
+  cudaError_t e;
+  static std::atomic<uint64_t> prepared{0}, wide{0};
+  const uint64_t bit = 1ull << (c.device & 63);
+  if (!(prepared.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kMaxSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(select_kernel<false>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(select_kernel<true>, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                               1);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(select_kernel<false>,
+                               cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    if (fits_wide(kMaxSmem)) wide.fetch_or(bit, std::memory_order_relaxed);
+    prepared.fetch_or(bit, std::memory_order_release);
+  }
   // a CTA for each 4096 tokens that a request may have, at most kMaxCluster, and a
   // thread for each four of its share
   const int64_t cap = (int64_t)s.max_blocks * s.page;
+  const int most = wide.load(std::memory_order_relaxed) & bit ? kMaxCluster : 8;
   int size = 1;
-  while (size < kMaxCluster && cap > (int64_t)size * 4096) size *= 2;
+  while (size < most && cap > (int64_t)size * 4096) size *= 2;
   const int64_t share = ((cap + size - 1) / size + 31) & ~(int64_t)31;
   const int64_t words = share / 32;
   int threads = 256;
   while (threads < kMaxThreads && share > (int64_t)threads * 4) threads *= 2;
   const bool cached = share <= kMaxKeys;
-  const size_t smem = (size_t)(2 * words + (cached ? share : 0)) * 4;
-  cudaError_t e;
-  static std::atomic<uint64_t> prepared{0};
-  const uint64_t bit = 1ull << (c.device & 63);
-  if (!(prepared.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kMaxKeys * 4 + kMaxKeys / 4);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(select_kernel<false>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxWordBytes);
-    if (e != cudaSuccess) return e;
-    prepared.fetch_or(bit, std::memory_order_relaxed);
-  }
+  const size_t smem = (size_t)(2 * words + (size > 1 ? 512 * size : 0) + (cached ? share : 0)) * 4;
   const Moves moves = moves_of(s, ws);
   const Counters counts = counters(ws);
   const int64_t list_len = max_moves(s);
@@ -411,7 +544,7 @@ cudaError_t launch_evict(const LaunchCtx& c, const ServeShape& s, const float* w
                          table, seq, keep, n_first, n_last, w_out, moves, list_len, counts,
                          s.max_blocks, s.page_log2, s.n_pages, (int)words, c.status);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)(c.num_sms * 4));
+  cfg.gridDim = dim3((unsigned)(c.num_sms * kMoveBlocks));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;

@@ -206,8 +206,8 @@ __global__ void __launch_bounds__(256) append_kernel(
 // The other way round: what each request gives back begins behind what the
 // requests before it do, whose sum each block works out itself, as above.
 __global__ void __launch_bounds__(kReq) release_kernel(
-    const int32_t* __restrict__ seq, const int32_t* __restrict__ keep,
-    const int32_t* __restrict__ table, int32_t* __restrict__ new_lens,
+    const int32_t* seq, const int32_t* keep,
+    const int32_t* table, int32_t* __restrict__ new_lens,
     int32_t* __restrict__ pages, int64_t n_max, int32_t* __restrict__ n_released, int B,
     int max_blocks, int page_log2, uint32_t* status) {
   __shared__ int64_t s_first[kReq + 1];
@@ -217,9 +217,11 @@ __global__ void __launch_bounds__(kReq) release_kernel(
   const int page = 1 << page_log2;
   const int32_t cap = max_blocks << page_log2;
   const int b0 = blockIdx.x * kReq;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the stream's work before
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   auto lens = [&](int b, int32_t& n, int32_t& left) {
-    n = __ldg(seq + b);
-    const int32_t k = __ldg(keep + b);
+    n = ld_input(seq + b);
+    const int32_t k = ld_input(keep + b);
     if (n < 0 || n > cap || k < 0) latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
     left = k < 0 || n < 0 || n > cap ? n : min(n, k);
     return n < 0 || n > cap
@@ -263,7 +265,7 @@ __global__ void __launch_bounds__(kReq) release_kernel(
 #pragma unroll
     for (int s = kReq / 2; s > 0; s >>= 1)
       if (s_first[lo + s] <= x) lo += s;
-    pages[x] = __ldg(table + (int64_t)(b0 + lo) * max_blocks + s_left[lo] + (x - s_first[lo]));
+    pages[x] = ld_input(table + (int64_t)(b0 + lo) * max_blocks + s_left[lo] + (x - s_first[lo]));
   }
 }
 
@@ -271,12 +273,14 @@ __global__ void __launch_bounds__(kReq) release_kernel(
 // A thread for each word of a row's mask walks up from the row's node; numbers
 // fall on the way, so it may stop below its word.  The parents come from L1.  A
 // chain is at most 32 * words long, whatever the parents hold.
-__global__ void __launch_bounds__(256) tree_kernel(const int32_t* __restrict__ parents,
-                                                   const int32_t* __restrict__ cu, int words,
+__global__ void __launch_bounds__(256) tree_kernel(const int32_t* parents,
+                                                   const int32_t* cu, int words,
                                                    uint32_t* __restrict__ bits, int B, int64_t T,
                                                    uint32_t* status) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (int b = blockIdx.x; b < B; b += gridDim.x) {
-    const int32_t c0 = __ldg(cu + b), c1 = __ldg(cu + b + 1);
+    const int32_t c0 = ld_input(cu + b), c1 = ld_input(cu + b + 1);
     if (c0 < 0 || c1 < c0 || c1 > T) {
       if (threadIdx.x == 0) latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
       continue;
@@ -289,7 +293,7 @@ __global__ void __launch_bounds__(256) tree_kernel(const int32_t* __restrict__ p
       uint32_t m = 0u;
       for (int32_t j = i; j >= lo;) {
         if (j < lo + 32) m |= 1u << (j - lo);
-        const int32_t p = __ldg(up + j);
+        const int32_t p = ld_input(up + j);
         if (p < -1 || p >= j) {
           latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
           break;
@@ -352,12 +356,28 @@ cudaError_t launch_append(const LaunchCtx& c, const ServeShape& s, const int32_t
   return run(append_kernel<512>);
 }
 
+// A launch that may begin while what is before it in the stream runs: the kernels
+// wait for its end on the device.
+template <typename... P, typename... A>
+static cudaError_t launch_early(const LaunchCtx& c, dim3 grid, int threads, void (*kern)(P...),
+                                A... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = c.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 cudaError_t launch_build_tree(const LaunchCtx& c, const ServeShape& s, const int32_t* parents,
                               const int32_t* cu, int words, uint32_t* tree_bits) {
   const int most = c.num_sms * 8;
-  tree_kernel<<<s.B < most ? s.B : most, 256, 0, c.stream>>>(parents, cu, words, tree_bits, s.B,
-                                                             s.T, c.status);
-  return cudaGetLastError();
+  return launch_early(c, dim3(s.B < most ? s.B : most), 256, tree_kernel, parents, cu, words,
+                      tree_bits, s.B, s.T, c.status);
 }
 
 cudaError_t launch_release_pages(const LaunchCtx& c, const ServeShape& s, const int32_t* seq,
@@ -371,10 +391,9 @@ cudaError_t launch_release_pages(const LaunchCtx& c, const ServeShape& s, const 
   const int64_t most = 4 * (int64_t)c.num_sms / chunks;
   if (y > most) y = most;
   if (y < 1) y = 1;
-  release_kernel<<<dim3(chunks, (unsigned)y), kReq, 0, c.stream>>>(
-      seq, keep, table, new_lens, pages, n_max, n_released, s.B, s.max_blocks, s.page_log2,
-      c.status);
-  return cudaGetLastError();
+  return launch_early(c, dim3(chunks, (unsigned)y), kReq, release_kernel, seq, keep, table,
+                      new_lens, pages, n_max, n_released, s.B, s.max_blocks, s.page_log2,
+                      c.status);
 }
 
 }  // namespace dsa
