@@ -22,8 +22,8 @@ constexpr int kCopies = 8;         // of a histogram, for lanes that meet in a b
 // two words for each 32 of the 2^22 / 8 places that a share may have
 constexpr int kMaxWordBytes = (1 << 22) / 8 / 4;
 // of a CTA: its keys or as many places as it may have, and the cluster's counts
-constexpr int kMaxSmem = kMaxKeys * 4 + kMaxKeys / 4 + 2048 * kMaxCluster;
-static_assert(kMaxSmem >= kMaxWordBytes + 2048 * 8, "shared memory");
+constexpr int kMaxSmem = kMaxKeys * 4 + kMaxKeys / 4 + 1024 * kMaxCluster;
+static_assert(kMaxSmem >= kMaxWordBytes + 1024 * 8, "shared memory");
 
 // In the workspace header, behind the status word; both are 0 between calls.
 struct Counters {
@@ -110,13 +110,14 @@ __global__ void __launch_bounds__(kMaxThreads) select_kernel(
   uint32_t rank, size;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
-  uint32_t* cluster_sums = smem;  // [turn][CTA][256] where there are several CTAs, by 16 bytes
-  uint32_t* above_w = smem + (size > 1 ? 512 * size : 0u);  // [word of 32 places] keys above
+  uint32_t* cluster_sums = smem;  // [CTA][256] where there are several: the leader's, by 16 bytes
+  uint32_t* above_w = smem + (size > 1 ? 256 * size : 0u);  // [word of 32 places] keys above
   uint32_t* equal_w = above_w + max_words;                  // the threshold; equal to it
   uint32_t* keys = equal_w + max_words;
   __shared__ alignas(16) uint32_t hist[2][kCopies][256];  // in turns
   __shared__ uint64_t sums[32];
-  __shared__ uint32_t found[3];           // the digit, keys above it, keys with it
+  // the digit, keys above it, keys with it, and of those the ones in the CTAs before
+  __shared__ uint32_t found[4];
   __shared__ uint32_t totals[2];          // freed places and movers of this CTA
   __shared__ uint32_t first_move;         // of the request, in the leader
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
@@ -197,7 +198,6 @@ __global__ void __launch_bounds__(kMaxThreads) select_kernel(
   // ---- the left-th largest key, eight bits at a time from the top
   uint32_t prefix = 0u;            // its bits so far, the rest 0
   uint32_t rest = (uint32_t)left;  // its rank among the keys with that prefix
-  int last = 0;                    // the buffer of the last pass
   __syncthreads();
   for (int pass = 0; pass < 4; ++pass) {
     const int shift = 24 - 8 * pass, turn = pass & 1;
@@ -216,31 +216,28 @@ __global__ void __launch_bounds__(kMaxThreads) select_kernel(
         a = add4(a, *reinterpret_cast<const uint4*>(&hist[turn][i][d0]));
         c = add4(c, *reinterpret_cast<const uint4*>(&hist[turn][i][d0 + 4]));
       }
-      if (size > 1) {  // to every CTA of the cluster
-        const uint32_t at = smem_u32(cluster_sums + (turn * size + rank) * 256 + d0);
-        for (uint32_t r = 0; r < size; ++r) {
-          st_cluster4(at_rank(at, r), a);
-          st_cluster4(at_rank(at, r) + 16, c);
-        }
+      if (size > 1) {  // to the leader
+        const uint32_t at = at_rank(smem_u32(cluster_sums + rank * 256 + d0), 0);
+        st_cluster4(at, a);
+        st_cluster4(at + 16, c);
       }
     } else {
       for (int i = tid - 32; i < kCopies * 64; i += nt - 32)  // for the next pass
         reinterpret_cast<uint4*>(hist[turn ^ 1])[i] = make_uint4(0u, 0u, 0u, 0u);
     }
     if (size > 1) {
-      // (the other turn's sums are read until the barrier of the next pass)
       cluster_arrive();
       cluster_wait();
-      if (warp == 0) {
+    }
+    if (warp == 0 && rank == 0) {
+      if (size > 1) {
         a = c = make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t* from = cluster_sums + turn * size * 256 + d0;
+#pragma unroll 4
         for (uint32_t r = 0; r < size; ++r) {
-          a = add4(a, *reinterpret_cast<const uint4*>(from + r * 256));
-          c = add4(c, *reinterpret_cast<const uint4*>(from + r * 256 + 4));
+          a = add4(a, *reinterpret_cast<const uint4*>(cluster_sums + r * 256 + d0));
+          c = add4(c, *reinterpret_cast<const uint4*>(cluster_sums + r * 256 + d0 + 4));
         }
       }
-    }
-    if (warp == 0) {
       const uint32_t n8[8] = {c.w, c.z, c.y, c.x, a.w, a.z, a.y, a.x};  // digits downwards
       uint32_t sum = 0u;
 #pragma unroll
@@ -252,29 +249,55 @@ __global__ void __launch_bounds__(kMaxThreads) select_kernel(
         if (lane >= s) before += o;
       }
       before -= sum;
-      if (before < rest && rest <= before + sum) {
+      const uint32_t who =
+          __ballot_sync(0xffffffffu, before < rest && rest <= before + sum);
+      uint32_t digit = 0u, over = 0u, with = 0u;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (before < rest && rest <= before + n8[e]) {
-            found[0] = (uint32_t)(d0 + 7 - e);
-            found[1] = before;
-            found[2] = n8[e];
-          }
-          before += n8[e];
+      for (int e = 0; e < 8; ++e) {
+        if (before < rest && rest <= before + n8[e]) {
+          digit = (uint32_t)(d0 + 7 - e);
+          over = before;
+          with = n8[e];
         }
+        before += n8[e];
       }
+      digit = __shfl_sync(0xffffffffu, digit, __ffs(who) - 1);
+      over = __shfl_sync(0xffffffffu, over, __ffs(who) - 1);
+      with = __shfl_sync(0xffffffffu, with, __ffs(who) - 1);
+      if (size > 1) {
+        // lane r: to CTA r, with the keys of the CTAs before it that share the prefix
+        const uint32_t mine = lane < (int)size ? cluster_sums[lane * 256 + digit] : 0u;
+        uint32_t ties = mine;
+#pragma unroll
+        for (int s = 1; s < kMaxCluster; s <<= 1) {
+          const uint32_t o = __shfl_up_sync(0xffffffffu, ties, s);
+          if (lane >= s) ties += o;
+        }
+        if (lane < (int)size) {
+          const uint32_t at = at_rank(smem_u32(found), lane);
+          st_cluster_u32(at, digit);
+          st_cluster_u32(at + 4, over);
+          st_cluster_u32(at + 8, with);
+          st_cluster_u32(at + 12, ties - mine);
+        }
+      } else if (lane == 0) {
+        found[0] = digit;
+        found[1] = over;
+        found[2] = with;
+        found[3] = 0u;
+      }
+    }
+    if (size > 1) {
+      cluster_arrive();
+      cluster_wait();
     }
     __syncthreads();
     prefix |= found[0] << shift;
     rest -= found[1];
-    last = turn;
     if (rest == found[2]) break;  // all keys with this prefix stay: the same in the cluster
   }
   const bool all_ties = rest == found[2];
-  uint32_t ties = 0u;  // equal keys in the CTAs before
-  if (!all_ties)
-    for (uint32_t r = 0; r < rank; ++r)
-      ties += cluster_sums[(last * size + r) * 256 + found[0]];
+  const uint32_t ties = found[3];
 
   // ---- which keys are above the threshold, which equal to it: a bit each
   const int words = (hi - lo + 31) >> 5;
@@ -523,7 +546,7 @@ cudaError_t launch_evict(const LaunchCtx& c, const ServeShape& s, const float* w
   int threads = 256;
   while (threads < kMaxThreads && share > (int64_t)threads * 4) threads *= 2;
   const bool cached = share <= kMaxKeys;
-  const size_t smem = (size_t)(2 * words + (size > 1 ? 512 * size : 0) + (cached ? share : 0)) * 4;
+  const size_t smem = (size_t)(2 * words + (size > 1 ? 256 * size : 0) + (cached ? share : 0)) * 4;
   const Moves moves = moves_of(s, ws);
   const Counters counts = counters(ws);
   const int64_t list_len = max_moves(s);
