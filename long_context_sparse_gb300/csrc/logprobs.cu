@@ -370,18 +370,26 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
   merge_lanes(16);
   if (lane == 0) stats[warp] = all;
   if (tid == 0) n_buf = again = 0u;
-  // all elements of the thread's share: f(value, id)
-  auto visit_all = [&](auto f) {
+  // the elements of the thread's share, at least of the vectors whose largest order
+  // key reaches floor(): f(value, id)
+  auto visit_all = [&](auto floor, auto f) {
     if (tid < n_single) f(load1(row.at + row.single(tid)), (uint32_t)row.single(tid));
-    for (int32_t v = v0 + tid; v < v1; v += kThreads) {
-      const uint4 q = ld_input(vec + v);
-      const uint32_t four[4] = {q.x, q.y, q.z, q.w};
+    for (int32_t v = v0 + tid; v < v1; v += kStep) {
+      uint32_t w[kWords];
+      load(v, w);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int u = 0; u < kUnroll; ++u) {
+        if (v + u * kThreads >= v1) break;
         float x[W::kPer];
-        W::get(four[i], x);
+        W::get(W::max(W::max(w[4 * u], w[4 * u + 1]), W::max(w[4 * u + 2], w[4 * u + 3])), x);
+        if (order_key(W::kPer == 2 ? fmaxf(x[0], x[W::kPer - 1]) : x[0]) < floor()) continue;
 #pragma unroll
-        for (int e = 0; e < W::kPer; ++e) f(x[e], (uint32_t)(row.id(v) + i * W::kPer + e));
+        for (int i = 0; i < 4; ++i) {
+          W::get(w[4 * u + i], x);
+#pragma unroll
+          for (int e = 0; e < W::kPer; ++e)
+            f(x[e], (uint32_t)(row.id(v + u * kThreads) + i * W::kPer + e));
+        }
       }
     }
   };
@@ -433,6 +441,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
       }
     }
     uint64_t at_least = (uint64_t)least << 32;
+    auto reach = [&] { return (uint32_t)(at_least >> 32); };
     auto push = [&](float x, uint32_t id) {
       const uint64_t key = full_key(x, id);
       if (key < at_least) return;
@@ -477,13 +486,13 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
       __syncthreads();
       if (tid == 0) n_buf = 0u;
       __syncthreads();
-      visit_all(push);
+      visit_all(reach, push);
       __syncthreads();
     }
     if (n_buf > kBuf) {
       // the n-th largest of the threads' best elements, by value and id
       uint64_t mine = 0ull;
-      visit_all([&](float x, uint32_t id) {
+      visit_all([&] { return (uint32_t)(mine >> 32); }, [&](float x, uint32_t id) {
         const uint64_t f = full_key(x, id);
         mine = f > mine ? f : mine;
       });
@@ -499,14 +508,14 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
       if (tid == 0) n_buf = 0u;
       __syncthreads();
       at_least = bound;
-      if (mine >= at_least) visit_all(push);
+      if (mine >= at_least) visit_all(reach, push);
       __syncthreads();
     }
     if (n_buf > kBuf) {
       uint64_t last = ~0ull;
       for (int i = 0; i < n_top; ++i) {
         uint64_t most = 0ull;
-        visit_all([&](float x, uint32_t id) {
+        visit_all([&] { return (uint32_t)(most >> 32); }, [&](float x, uint32_t id) {
           const uint64_t f = full_key(x, id);
           if (f < last && f > most) most = f;
         });
@@ -705,7 +714,7 @@ struct Launch {
     cfg.blockDim = dim3(kThreads);
     cfg.stream = c.stream;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
   }
 };
 
@@ -737,11 +746,13 @@ dsa_status_t dsa_token_logprobs(const dsa_logprobs_config_t* cfg, const void* lo
   if (written_meets(writes, reads)) return DSA_ERR_INVALID_ARG;
   LaunchCtx ctx;
   if ((st = make_ctx(ws, stream, &ctx)) != DSA_OK) return st;
-  // a row to a CTA where that fills the GPU, else to as many as that takes, each
-  // with a batch of every thread at least
+  // A row to as many CTAs as two an SM allow, each with a batch of every thread at
+  // least.  us in a graph with 1, 2, 4, 8 CTAs a row of 131072 bf16, 20 alternatives: 16
+  // rows 16.7 14.0 12.3 11.0; 64 rows 17.5 15.3 13.5 14.9; 150 rows 18 16.9 22.3 30.7; 300
+  // rows 23.4 24.8 35.8 53.8.
   int size = 1;
   const int64_t batch = (int64_t)kThreads * kUnroll * (16 / (int64_t)elem_bytes(cfg));
-  while (size < kMaxCluster && cfg->rows * size < 4 * (int64_t)ctx.num_sms &&
+  while (size < kMaxCluster && cfg->rows * size <= ctx.num_sms &&
          cfg->vocab >= 2 * size * batch)
     size *= 2;
   if (cfg->rows * size >= (int64_t)1 << 31) return DSA_ERR_UNSUPPORTED_SHAPE;
