@@ -554,7 +554,8 @@ DSA_API dsa_status_t dsa_tree_attn(const dsa_serve_config_t* cfg, const void* q,
  * (DSA_ERR_INVALID_ARG).  A page may not belong to two requests with rows.
  * T * H <= 2^20, else DSA_ERR_UNSUPPORTED_SHAPE.  Device-side errors as
  * dsa_prefix_attn has them (a bad page's tokens get no weight).  Results repeat bit for
- * bit on the same inputs and device.  ws: DSA_SERVE_WS_WEIGHTS. */
+ * bit on the same inputs and device.  ws: DSA_SERVE_WS_WEIGHTS; after a
+ * DSA_ERR_DEVICE_TIMEOUT it has to be initialised anew. */
 DSA_API dsa_status_t dsa_key_weights(const dsa_serve_config_t* cfg, const void* q,
                                      const float* lse, const void* k_pages,
                                      const int32_t* block_table, const int32_t* seq_lens,
@@ -563,9 +564,9 @@ DSA_API dsa_status_t dsa_key_weights(const dsa_serve_config_t* cfg, const void* 
                                      float* w_out, void* ws, size_t ws_bytes, void* stream);
 
 /* Eviction of one layer's cache by weight.  Request b keeps left_b =
- * min(seq_lens[b], keep_lens[b]) of its own tokens: those that rank first by
- * weight, where the first n_first and the last n_last places rank as +inf, ties
- * go to the lower place and NaN ranks below all.  A key has no position (NoPE), so
+ * min(seq_lens[b], keep_lens[b]) of its own tokens: those that come first by
+ * rank_pages (NULL: by w_pages), where the first n_first and the last n_last
+ * places count as +inf, ties go to the lower place and NaN comes last.  A key has no position (NoPE), so
  * kept tokens need not stay in order: with a_0 < a_1 < .. the places below left_b
  * whose tokens are dropped and c_0 < c_1 < .. the places from left_b on whose
  * tokens are kept (as many), the rows of k_pages (and v_pages) at c_i are copied
@@ -575,7 +576,10 @@ DSA_API dsa_status_t dsa_key_weights(const dsa_serve_config_t* cfg, const void* 
  * and lengths stay: one dsa_release_pages a step serves all layers.  Rows and
  * weights from left_b on, and all that belongs to no request, are left as they
  * are.  v_pages NULL: K = V.  w_out may be w_pages.
- * keep_lens [B] int32, n_first, n_last >= 0; seq_lens, block_table as above;
+ * After a tree of drafts, a rank of -inf for the rejected nodes and of +inf for all
+ * other tokens, with keep_lens the lengths without the rejected ones, leaves the
+ * accepted ones with the rest.
+ * rank_pages, w_pages, w_out [n_pages, page_size] fp32, keep_lens [B] int32, n_first, n_last >= 0; seq_lens, block_table as above;
  * max_blocks * page_size <= 2^22, else DSA_ERR_UNSUPPORTED_SHAPE.  What is written
  * must not overlap what is read, or itself, in any other way
  * (DSA_ERR_INVALID_ARG).  A page may not belong to two requests, or stand twice
@@ -583,10 +587,10 @@ DSA_API dsa_status_t dsa_key_weights(const dsa_serve_config_t* cfg, const void* 
  * Device-side errors (latched as DSA_ERR_DEVICE_BAD_INDEX; nothing is read or
  * written out of bounds): a length below 0 or above max_blocks * page_size, or a
  * keep_lens below 0 (the request is left as it is), a page id outside the cache
- * (its tokens have no weight: they rank with NaN, and are not copied).
+ * (its tokens come last with NaN, and are not copied).
  * ws: DSA_SERVE_WS_EVICT. */
 DSA_API dsa_status_t dsa_evict_cache(const dsa_serve_config_t* cfg, const float* w_pages,
-                                     const int32_t* block_table, const int32_t* seq_lens,
+                                     const float* rank_pages, const int32_t* block_table, const int32_t* seq_lens,
                                      const int32_t* keep_lens, int64_t n_first, int64_t n_last,
                                      void* k_pages, void* v_pages, float* w_out, void* ws,
                                      size_t ws_bytes, void* stream);
@@ -623,7 +627,7 @@ DSA_API dsa_status_t dsa_release_pages(const dsa_serve_config_t* cfg, const int3
 typedef struct dsa_logprobs_config {
   int64_t rows;   /* R, >= 1 (< 2^31) */
   int64_t vocab;  /* V, >= 1 (< 2^30) */
-  int64_t ld;     /* elements from a row of logits to the next, >= V (< 2^40) */
+  int64_t ld;     /* elements from a row of logits to the next, >= V; R * ld <= 2^45 */
   int32_t dtype;  /* of logits and their gradient: DSA_BF16, DSA_FP16, DSA_FP32 */
   int32_t n_top;  /* alternatives a row, 0 <= n_top <= min(64, V) */
   float scale;    /* of the logits (one over the temperature), > 0; log2(e) times it finite */

@@ -253,7 +253,7 @@ def _load():
             "dsa_build_tree": [SP, P, P, I32, P, P, SZ, P],
             "dsa_tree_attn": [SP, P, P, P, P, I64, P, P, P, P, I32, P, P, P, SZ, P],
             "dsa_key_weights": [SP, P, P, P, P, P, P, P, I32, P, F32, P, P, SZ, P],
-            "dsa_evict_cache": [SP, P, P, P, P, I64, I64, P, P, P, P, SZ, P],
+            "dsa_evict_cache": [SP, P, P, P, P, P, I64, I64, P, P, P, P, SZ, P],
             "dsa_release_pages": [SP, P, P, P, P, P, I64, P, P, SZ, P],
             "dsa_token_logprobs": [LP, P, P, P, P, P, P, P, P, SZ, P],
             "dsa_token_logprobs_bwd": [LP, P, P, P, P, P, P, P, I64, P, SZ, P],
@@ -1095,12 +1095,13 @@ def key_weights(cfg: ServeConfig, q, lse, k_pages, block_table, seq_lens, cu_tok
 
 
 def evict_cache(cfg: ServeConfig, w_pages, block_table, seq_lens, keep_lens, k_pages,
-                v_pages=None, n_first: int = 0, n_last: int = 0, w_out=None, ws=None):
+                v_pages=None, n_first: int = 0, n_last: int = 0, w_out=None, ws=None,
+                rank_pages=None):
     """Shrink each request's cache to keep_lens[b] tokens, in place: those with the
-    largest weights (the first n_first and the last n_last always rank first), the
-    kept ones from behind moved into the places of the dropped ones.  Tables and
-    lengths stay: release_pages, once for all layers.  Returns w_out (None: in
-    place).  Without v_pages: K = V."""
+    largest weights, or ranks where rank_pages is given (the first n_first and the
+    last n_last always come first), the kept ones from behind moved into the places
+    of the dropped ones.  Tables and lengths stay: release_pages, once for all
+    layers.  Returns w_out (None: in place).  Without v_pages: K = V."""
     B, i32, f32, bf = cfg.batch, torch.int32, torch.float32, torch.bfloat16
     slots = (cfg.n_pages, cfg.page_size)
     dev, p_w = _first_tensor(w_pages, "w_pages", f32, slots)
@@ -1118,7 +1119,10 @@ def evict_cache(cfg: ServeConfig, w_pages, block_table, seq_lens, keep_lens, k_p
         w_out = w_pages
     p_out = _check_tensor(w_out, "w_out", f32, slots, dev)
     ws, p_ws, n_ws = _serve_ws(cfg, SERVE_WS_EVICT, ws, dev)
-    _serve_call("dsa_evict_cache", dev, cfg._ref, p_w, p_table, p_seq, p_keep, n_first, n_last,
+    p_rank = None
+    if rank_pages is not None:
+        p_rank = _check_tensor(rank_pages, "rank_pages", f32, slots, dev)
+    _serve_call("dsa_evict_cache", dev, cfg._ref, p_w, p_rank, p_table, p_seq, p_keep, n_first, n_last,
                 p_k, p_v, p_out, p_ws, n_ws)
     return w_out
 

@@ -102,8 +102,8 @@ __device__ __forceinline__ uint4 add4(const uint4& a, const uint4& b) {
 // of eight places number the equal keys, the freed places and the movers.
 template <bool Cached>
 __global__ void __launch_bounds__(kMaxThreads) select_kernel(
-    const float* w, const int32_t* table, const int32_t* seq, const int32_t* keep,
-    int32_t n_first, int32_t n_last, float* w_out, Moves moves, int64_t list_len,
+    const float* w, const float* ranks, const int32_t* table, const int32_t* seq,
+    const int32_t* keep, int32_t n_first, int32_t n_last, float* w_out, Moves moves, int64_t list_len,
     Counters counts, int max_blocks, int page_log2, int64_t n_pages, int max_words,
     uint32_t* status) {
   extern __shared__ __align__(16) uint32_t smem[];
@@ -146,9 +146,9 @@ __global__ void __launch_bounds__(kMaxThreads) select_kernel(
     }
     return (p << page_log2) + (j & in_page);
   };
-  // f(j, slot, weight) of the places j0, j0 + nt, .. below `end` that `which` picks:
-  // kAhead pages, then kAhead weights on their way at a time
-  auto weights_of = [&](int32_t j0, int32_t end, auto which, auto f) {
+  // f(j, slot, value from v) of the places j0, j0 + nt, .. below `end` that `which`
+  // picks: kAhead pages, then kAhead values on their way at a time
+  auto values_of = [&](const float* v, int32_t j0, int32_t end, auto which, auto f) {
     constexpr int kAhead = 4;
     for (; j0 < end; j0 += kAhead * nt) {
       int32_t p[kAhead], s[kAhead];
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kMaxThreads) select_kernel(
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         s[u] = on[u] ? slot_on(p[u], j0 + u * nt) : -1;
-        if (s[u] >= 0) x[u] = ld_input_f(w + s[u]);
+        if (s[u] >= 0) x[u] = ld_input_f(v + s[u]);
       }
 #pragma unroll
       for (int u = 0; u < kAhead; ++u)
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kMaxThreads) select_kernel(
   auto any = [](int32_t) { return true; };
   if (left == n || left == 0) {  // all stay, or none
     if (w_out != w)
-      weights_of(lo + tid, min(hi, left), any, [&](int32_t, int32_t s, float x) {
+      values_of(w, lo + tid, min(hi, left), any, [&](int32_t, int32_t s, float x) {
         if (s >= 0) w_out[s] = x;
       });
     return;
@@ -183,15 +183,16 @@ __global__ void __launch_bounds__(kMaxThreads) select_kernel(
     return fixed(j) ? 0xff800000u /* +inf */ : s < 0 ? 0u : order_key(x);
   };
   if (Cached)
-    weights_of(lo + tid, hi, any,
-               [&](int32_t j, int32_t s, float x) { keys[j - lo] = to_key(j, s, x); });
+    values_of(ranks, lo + tid, hi, any,
+              [&](int32_t j, int32_t s, float x) { keys[j - lo] = to_key(j, s, x); });
   // f(j, key) of the places j0, j0 + nt, .. below hi
   auto each_key = [&](int32_t j0, auto f) {
     if (Cached) {
 #pragma unroll 4
       for (int32_t j = j0; j < hi; j += nt) f(j, keys[j - lo]);
     } else {
-      weights_of(j0, hi, any, [&](int32_t j, int32_t s, float x) { f(j, to_key(j, s, x)); });
+      values_of(ranks, j0, hi, any,
+                [&](int32_t j, int32_t s, float x) { f(j, to_key(j, s, x)); });
     }
   };
 
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(kMaxThreads) select_kernel(
         else if (fixed(j)) k = 0xff800000u;
         else {
           const int32_t s = slot_on(ld_input(row + (j >> page_log2)), j);
-          k = s < 0 ? 0u : order_key(ld_input_f(w + s));
+          k = s < 0 ? 0u : order_key(ld_input_f(ranks + s));
         }
       }
       flags(j, k);
@@ -392,8 +393,8 @@ __global__ void __launch_bounds__(kMaxThreads) select_kernel(
     // the tokens that stay where they are; each CTA has as many places below `left`,
     // whosever share they lie in
     const int32_t part = (left + (int)size - 1) / (int)size, from = min(left, (int)rank * part);
-    weights_of(
-        from + tid, min(left, from + part),
+    values_of(
+        w, from + tid, min(left, from + part),
         [&](int32_t j) {
           const uint32_t r = (uint32_t)(j / share), i = (uint32_t)(j - (int)r * share);
           return (ld_cluster(at_rank(smem_u32(above_w + (i >> 5)), r)) >> (i & 31u) & 1u) != 0u;
@@ -417,10 +418,12 @@ __global__ void __launch_bounds__(kMaxThreads) select_kernel(
       uint32_t holes = ~kept & low & below(x, hi), movers = kept & ~low;
       if (x > x0 && (holes | movers)) page = ld_input(row + (j >> page_log2));
       const int32_t slot = holes | movers ? slot_on(page, j) : -1;
-      for (; holes; holes &= holes - 1u)
-        moves.dst[at + h++] = slot < 0 ? -1 : slot + __ffs(holes) - 1;
-      for (; movers; movers &= movers - 1u)
-        moves.src[at + m++] = slot < 0 ? -1 : slot + __ffs(movers) - 1;
+      for (; holes; holes &= holes - 1u, ++h)
+        if (DSA_IN_BOUNDS(at + h < list_len, status))
+          moves.dst[at + h] = slot < 0 ? -1 : slot + __ffs(holes) - 1;
+      for (; movers; movers &= movers - 1u, ++m)
+        if (DSA_IN_BOUNDS(at + m < list_len, status))
+          moves.src[at + m] = slot < 0 ? -1 : slot + __ffs(movers) - 1;
     }
   }
   if (size > 1) cluster_wait();
@@ -513,7 +516,7 @@ bool fits_wide(int smem) {
 size_t evict_ws(const ServeShape& s) { return 2 * round_up((size_t)max_moves(s), 64) * 4; }
 
 cudaError_t launch_evict(const LaunchCtx& c, const ServeShape& s, const float* w_pages,
-                         const int32_t* table, const int32_t* seq, const int32_t* keep,
+                         const float* rank_pages, const int32_t* table, const int32_t* seq, const int32_t* keep,
                          int32_t n_first, int32_t n_last, __nv_bfloat16* k_pages,
                          __nv_bfloat16* v_pages, float* w_out, uint8_t* ws) {
   cudaError_t e;
@@ -564,7 +567,7 @@ cudaError_t launch_evict(const LaunchCtx& c, const ServeShape& s, const float* w
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, cached ? select_kernel<true> : select_kernel<false>, w_pages,
-                         table, seq, keep, n_first, n_last, w_out, moves, list_len, counts,
+                         rank_pages, table, seq, keep, n_first, n_last, w_out, moves, list_len, counts,
                          s.max_blocks, s.page_log2, s.n_pages, (int)words, c.status);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)(c.num_sms * kMoveBlocks));

@@ -592,7 +592,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               // bits are turned around
               const int32_t j0 = pos0 - walk.r.base, w0 = j0 >> 5;
               uint32_t lo = 0u, hi = 0u;
-              if (32 * q + lane < n) {
+              if (32 * q + lane < n &&
+                  DSA_IN_BOUNDS((walk.r.row0 + r0 + lane) / a.H < a.T, a.status)) {
                 const int32_t* bits =
                     a.bits + (int64_t)((walk.r.row0 + r0 + lane) / a.H) * a.words;
                 if (w0 >= 0 && w0 < a.words) lo = (uint32_t)ld_input(bits + w0);
@@ -679,7 +680,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int p = from; p <= to; ++p) v += __ldcg(part(p));
         }
       }
-      if (mine && slot >= 0) a.w_out[slot] = old + v;
+      if (mine && slot >= 0 && DSA_IN_BOUNDS(slot < a.n_pages << a.page_log2, a.status))
+        a.w_out[slot] = old + v;
       if (!(ok = epi_sync())) break;  // red and misc may be written again
       sum[0] = sum[1] = 0ull;
     }

@@ -597,6 +597,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
   }
   if (Top && tid < n_top) {
     const uint64_t key = top[tid];
+    if (!DSA_IN_BOUNDS((uint32_t)key_id(key) < (uint32_t)vocab, status)) return;
     top_ids[r * n_top + tid] = key_id(key);
     top_logp[r * n_top + tid] = none ? -INFINITY : (key_value(key) - s.r) * scale - ln;
   }
@@ -674,16 +675,21 @@ __global__ void __launch_bounds__(kThreads) logprobs_bwd_kernel(
   }
 }
 
+// Rows that no address space holds.
+dsa_status_t check_ld(const dsa_logprobs_config_t* c, int64_t ld) {
+  return ld >= (int64_t)1 << 40 || c->rows > ((int64_t)1 << 45) / ld ? DSA_ERR_UNSUPPORTED_SHAPE
+                                                                    : DSA_OK;
+}
+
 dsa_status_t check_logprobs(const dsa_logprobs_config_t* c) {
   if (!c) return DSA_ERR_INVALID_ARG;
   if (c->rows < 1 || c->vocab < 1 || c->ld < c->vocab || c->dtype < DSA_BF16 ||
       c->dtype > DSA_FP32 || c->n_top < 0 || c->n_top > c->vocab || !(c->scale > 0.f) ||
       isinf(c->scale * kLog2e) || c->reserved != 0)
     return DSA_ERR_INVALID_ARG;
-  if (c->rows >= (int64_t)1 << 31 || c->vocab >= (int64_t)1 << 30 ||
-      c->ld >= (int64_t)1 << 40 || c->n_top > kMaxTop)
+  if (c->rows >= (int64_t)1 << 31 || c->vocab >= (int64_t)1 << 30 || c->n_top > kMaxTop)
     return DSA_ERR_UNSUPPORTED_SHAPE;
-  return DSA_OK;
+  return check_ld(c, c->ld);
 }
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -783,7 +789,7 @@ dsa_status_t dsa_token_logprobs_bwd(const dsa_logprobs_config_t* cfg, const void
   if (!logits || !tokens || !lse || (g_entropy && !entropy) || !dlogits ||
       ld_grad < cfg->vocab)
     return DSA_ERR_INVALID_ARG;
-  if (ld_grad >= (int64_t)1 << 40) return DSA_ERR_UNSUPPORTED_SHAPE;
+  if ((st = check_ld(cfg, ld_grad)) != DSA_OK) return st;
   if ((st = check_ws256(ws, ws_bytes)) != DSA_OK) return st;
   const void* ptrs[] = {tokens, lse, entropy, g_logp, g_entropy};
   for (const void* p : ptrs)

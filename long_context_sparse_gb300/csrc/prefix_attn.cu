@@ -992,7 +992,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t lo = 0u, hi = 0u;
-          if (lane + 32 * h < n_nodes) {
+          if (lane + 32 * h < n_nodes && DSA_IN_BOUNDS(t0 + lane + 32 * h < T, status)) {
             const int32_t* at = tree.bits + (int64_t)(t0 + lane + 32 * h) * tree.words;
             if (w0 >= 0 && w0 < tree.words) lo = (uint32_t)ld_input(at + w0);
             if (w0 + 1 >= 0 && w0 + 1 < tree.words) hi = (uint32_t)ld_input(at + w0 + 1);

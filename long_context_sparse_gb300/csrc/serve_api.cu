@@ -283,22 +283,25 @@ dsa_status_t dsa_key_weights(const dsa_serve_config_t* cfg, const void* q, const
 }
 
 dsa_status_t dsa_evict_cache(const dsa_serve_config_t* cfg, const float* w_pages,
-                             const int32_t* block_table, const int32_t* seq_lens,
-                             const int32_t* keep_lens, int64_t n_first, int64_t n_last,
-                             void* k_pages, void* v_pages, float* w_out, void* ws,
-                             size_t ws_bytes, void* stream) {
+                             const float* rank_pages, const int32_t* block_table,
+                             const int32_t* seq_lens, const int32_t* keep_lens, int64_t n_first,
+                             int64_t n_last, void* k_pages, void* v_pages, float* w_out,
+                             void* ws, size_t ws_bytes, void* stream) {
   dsa_status_t st = check_serve(cfg, DSA_SERVE_WS_EVICT);
   if (st != DSA_OK) return st;
   if (!w_pages || !block_table || !seq_lens || !keep_lens || n_first < 0 || n_last < 0 ||
       !k_pages || !w_out || v_pages == k_pages)  // K = V: v_pages null
     return DSA_ERR_INVALID_ARG;
   if ((st = check_serve_ws(cfg, DSA_SERVE_WS_EVICT, ws, ws_bytes)) != DSA_OK) return st;
-  const void* ptrs[] = {w_pages, block_table, seq_lens, keep_lens, k_pages, v_pages, w_out};
+  const void* ptrs[] = {w_pages,   rank_pages, block_table, seq_lens,
+                        keep_lens, k_pages,    v_pages,     w_out};
   for (const void* p : ptrs)
     if (!aligned16(p)) return DSA_ERR_MISALIGNED;
   const size_t B = (size_t)cfg->batch, slots = (size_t)cfg->n_pages * cfg->page_size;
   const size_t cache = slots * cfg->d_qk * 2;
+  if (rank_pages == w_pages) rank_pages = nullptr;
   const Span reads[] = {{w_pages == w_out ? nullptr : w_pages, slots * 4},
+                        {rank_pages, slots * 4},
                         {block_table, B * (size_t)cfg->max_blocks * 4},
                         {seq_lens, B * 4},
                         {keep_lens, B * 4}};
@@ -311,7 +314,7 @@ dsa_status_t dsa_evict_cache(const dsa_serve_config_t* cfg, const float* w_pages
   if ((st = make_ctx(ws, stream, &ctx)) != DSA_OK) return st;
   const int32_t most = INT32_MAX;  // lengths are below 2^30
   return cuda_status(launch_evict(
-      ctx, serve_shape(cfg), w_pages, block_table, seq_lens, keep_lens,
+      ctx, serve_shape(cfg), w_pages, rank_pages ? rank_pages : w_pages, block_table, seq_lens, keep_lens,
       (int32_t)(n_first < most ? n_first : most), (int32_t)(n_last < most ? n_last : most),
       static_cast<__nv_bfloat16*>(k_pages), static_cast<__nv_bfloat16*>(v_pages), w_out,
       static_cast<uint8_t*>(ws)));

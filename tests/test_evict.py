@@ -68,19 +68,21 @@ class Evict:
         p = torch.arange(n)
         return self.table[b][p // self.page].long() * self.page + p % self.page
 
-    def plain(self, n_first, n_last, out):
+    def plain(self, n_first, n_last, out, rank=None):
         cache, out = [c.clone().view(-1, self.d) for c in self.cache], out.clone().view(-1)
         w = self.w.view(-1)
+        rank = (self.w if rank is None else rank).view(-1)
         for b, n in enumerate(self.lens):
             slots = self.slots(b, n)
-            src = plain_keep(w[slots].tolist(), min(n, self.keep[b]), n_first, n_last)
+            src = plain_keep(rank[slots].tolist(), min(n, self.keep[b]), n_first, n_last)
             to, take = slots[: len(src)], slots[src]
             out[to] = w[take]
             for x, c in zip(cache, self.cache):
                 x[to] = c.view(-1, self.d)[take]
         return [c.view_as(self.cache[0]) for c in cache], out.view_as(self.w)
 
-    def run(self, n_first=0, n_last=0, in_place=False, ws=None, keep=None, lens=None, table=None):
+    def run(self, n_first=0, n_last=0, in_place=False, ws=None, keep=None, lens=None, table=None,
+            rank=None):
         dv = lambda t: t.to(DEV)
         cache = [dv(c) for c in self.cache]
         w = dv(self.w)
@@ -90,7 +92,8 @@ class Evict:
                               i32(self.lens if lens is None else lens),
                               i32(self.keep if keep is None else keep), cache[0],
                               v_pages=cache[1] if self.kv == 2 else None, n_first=n_first,
-                              n_last=n_last, w_out=None if in_place else out, ws=ws)
+                              n_last=n_last, w_out=None if in_place else out, ws=ws,
+                              rank_pages=None if rank is None else dv(rank))
         torch.cuda.synchronize()
         return [c.cpu() for c in cache], got.cpu(), dsa.get_device_status(ws)
 
@@ -123,12 +126,12 @@ def test_evict_refusals(lib):
     r, B, slots, d = ctypes.byref(c.c()), 4, 6400, 128
     nb = dsa.serve_workspace_size(c, dsa.SERVE_WS_EVICT)
     f = lib.dsa_evict_cache
-    size = dict(w=slots * 4, table=B * 40, seq=16, keep=16, k=slots * d * 2, v=slots * d * 2,
+    size = dict(w=slots * 4, rank=slots * 4, table=B * 40, seq=16, keep=16, k=slots * d * 2, v=slots * d * 2,
                 out=slots * 4, ws=nb)
 
     def call(at, first=0, last=0, ws_bytes=nb, **over):
-        w, table, seq, keep, k, v, out, ws = (P(x) for x in {**at, **over}.values())
-        return f(r, w, table, seq, keep, first, last, k, v, out, ws, ws_bytes, None)
+        w, rank, table, seq, keep, k, v, out, ws = (P(x) for x in {**at, **over}.values())
+        return f(r, w, rank, table, seq, keep, first, last, k, v, out, ws, ws_bytes, None)
 
     refusals(call, size, ("k", "v", "out", "ws"), (("out", "w"),))
     at = {n: (i + 1) << 28 for i, n in enumerate(size)}
@@ -209,6 +212,26 @@ def test_evict_past_shared_memory():
     check_evict(e, n_last=1000)
     e.w = torch.zeros_like(e.w)
     check_evict(e, n_first=5, n_last=1000, in_place=True)
+
+
+@gpu
+@pytest.mark.parametrize("in_place", [False, True])
+def test_ranks_of_their_own(in_place):
+    """Rejected drafts: -inf among +inf; and any ranks, the weights only carried."""
+    g = torch.Generator().manual_seed(1)
+    for n in (300, 6000):
+        e = Evict([n, n // 3, 40], [n - 20, n // 3 - 5, 10], 16, 128, 2, "odd", seed=n)
+        drafts = torch.full_like(e.w, math.inf)
+        for b, m in enumerate(e.lens):
+            s = e.slots(b, m)
+            gone = m - 40 + torch.randperm(40, generator=g)[: m - e.keep[b]]
+            drafts.view(-1)[s[gone]] = -math.inf
+        for rank in (drafts, torch.randn(e.w.shape, generator=g)):
+            cache, out, status = e.run(in_place=in_place, rank=rank)
+            ref, ref_w = e.plain(0, 0, e.w if in_place else torch.full_like(e.w, 7.0), rank)
+            assert status == 0 and same(out, ref_w)
+            for a, b in zip(cache, ref):
+                assert torch.equal(a, b)
 
 
 @gpu
