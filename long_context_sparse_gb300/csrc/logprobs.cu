@@ -215,7 +215,9 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 // the share through a second look at all of it.  Where more elements pass than the
 // buffer holds (rows of many equal values), ids break the ties already in the bound;
 // and should that not do either, `n` passes each look for the largest below the last.
-template <typename T, bool Top>
+// `Again`: the rows are few, and what is looked at again is found in L1 (64 rows of 131072
+// bf16 with 20 alternatives: 1.2 us less; with a row a CTA, 4% more).
+template <typename T, bool Top, bool Again>
 __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
     const T* logits, int64_t ld, int32_t vocab, const int32_t* tokens, int n_top, float scale,
     float* logp, float* lse, float* entropy, int32_t* top_ids, float* top_logp,
@@ -231,7 +233,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
   __shared__ Stat from[kMaxCluster];
   __shared__ alignas(16) uint64_t from_top[Top ? kMaxTop * kMaxCluster : 2];
   __shared__ uint32_t warp_best[kMaxTop + kWarps];
-  __shared__ uint32_t n_buf, again;
+  __shared__ uint32_t n_buf, again, has_token;
+  __shared__ float x_token;
   __shared__ uint64_t bound;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t rank, size;
@@ -295,7 +298,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       uint4 x = make_uint4(W::kNone, W::kNone, W::kNone, W::kNone);
-      if (v + u * kThreads < v1) x = ld_stream(vec + v + u * kThreads);
+      if (v + u * kThreads < v1)
+        x = Again ? ld_input(vec + v + u * kThreads) : ld_stream(vec + v + u * kThreads);
       w[4 * u] = x.x;
       w[4 * u + 1] = x.y;
       w[4 * u + 2] = x.z;
@@ -370,6 +374,15 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
   merge_lanes(16);
   if (lane == 0) stats[warp] = all;
   if (tid == 0) n_buf = again = 0u;
+  if (rank == 0 && tid == kThreads - 1) {  // on its way beside the rest
+    int32_t tok = ld_input(tokens + r);
+    if (tok >= vocab) {
+      latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
+      tok = -1;
+    }
+    has_token = tok >= 0 ? 1u : 0u;
+    if (tok >= 0) x_token = load1(row.at + tok);
+  }
   // the elements of the thread's share, at least of the vectors whose largest order
   // key reaches floor(): f(value, id)
   auto visit_all = [&](auto floor, auto f) {
@@ -586,14 +599,9 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
   const bool none = s.s == 0.f;  // nothing but -inf
   const float ln = logf(s.s);
   if (tid == 0) {
-    int32_t tok = ld_input(tokens + r);
-    if (tok >= vocab) {
-      latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
-      tok = -1;
-    }
     lse[r] = none ? -INFINITY : fmaf(s.r, scale, ln);
     entropy[r] = none ? 0.f : ln - kLn2 * (s.t / s.s);
-    logp[r] = tok < 0 ? 0.f : none ? -INFINITY : (load1(row.at + tok) - s.r) * scale - ln;
+    logp[r] = !has_token ? 0.f : none ? -INFINITY : (x_token - s.r) * scale - ln;
   }
   if (Top && tid < n_top) {
     const uint64_t key = top[tid];
@@ -763,20 +771,19 @@ dsa_status_t dsa_token_logprobs(const dsa_logprobs_config_t* cfg, const void* lo
     size *= 2;
   if (cfg->rows * size >= (int64_t)1 << 31) return DSA_ERR_UNSUPPORTED_SHAPE;
   Launch l(ctx, (unsigned)(cfg->rows * size), size);
-  auto run = [&](auto zero, auto with, auto without) {
+  auto run = [&](auto zero) {
     using T = decltype(zero);
-    return cuda_status(cudaLaunchKernelEx(&l.cfg, cfg->n_top ? with : without,
-                                          static_cast<const T*>(logits), cfg->ld,
+    auto kern = cfg->n_top == 0 ? logprobs_kernel<T, false, false>
+                : size > 1      ? logprobs_kernel<T, true, true>
+                                : logprobs_kernel<T, true, false>;
+    return cuda_status(cudaLaunchKernelEx(&l.cfg, kern, static_cast<const T*>(logits), cfg->ld,
                                           (int32_t)cfg->vocab, tokens, (int)cfg->n_top,
                                           cfg->scale, logp, lse, entropy, top_ids, top_logp,
                                           ctx.status));
   };
-  if (cfg->dtype == DSA_BF16)
-    return run(__nv_bfloat16(), logprobs_kernel<__nv_bfloat16, true>,
-               logprobs_kernel<__nv_bfloat16, false>);
-  if (cfg->dtype == DSA_FP16)
-    return run(__half(), logprobs_kernel<__half, true>, logprobs_kernel<__half, false>);
-  return run(float(), logprobs_kernel<float, true>, logprobs_kernel<float, false>);
+  if (cfg->dtype == DSA_BF16) return run(__nv_bfloat16());
+  if (cfg->dtype == DSA_FP16) return run(__half());
+  return run(float());
 }
 
 dsa_status_t dsa_token_logprobs_bwd(const dsa_logprobs_config_t* cfg, const void* logits,
