@@ -509,10 +509,10 @@ DSA_API dsa_status_t dsa_prefix_attn(const dsa_serve_config_t* cfg, const void* 
  * parents [T], cu_tokens [B+1] int32 -> tree_bits [T, words] 32-bit words, 1 <=
  * words <= 32.  tree_bits and the workspace must not overlap what the call
  * reads, or one another (DSA_ERR_INVALID_ARG).
- * Device-side errors (latched as DSA_ERR_DEVICE_BAD_INDEX): a request with more
- * than 32 * words rows (bits of further nodes are left out), a parent below -1
- * or not below its node (taken for -1), cu_tokens that start below 0, descend
- * or end past T (no row of such a request is written).
+ * Device-side errors (latched as DSA_ERR_DEVICE_BAD_INDEX): a parent below -1 or
+ * not below its node (taken for -1); a request with more than 32 * words rows, or
+ * whose cu_tokens start below 0, descend or end past T (none of its rows is
+ * written).
  * ws: DSA_SERVE_WS_TREE. */
 DSA_API dsa_status_t dsa_build_tree(const dsa_serve_config_t* cfg, const int32_t* parents,
                                     const int32_t* cu_tokens, int32_t words,
@@ -588,7 +588,8 @@ DSA_API dsa_status_t dsa_key_weights(const dsa_serve_config_t* cfg, const void* 
  * written out of bounds): a length below 0 or above max_blocks * page_size, or a
  * keep_lens below 0 (the request is left as it is), a page id outside the cache
  * (its tokens come last with NaN, and are not copied).
- * ws: DSA_SERVE_WS_EVICT. */
+ * ws: DSA_SERVE_WS_EVICT; after a DSA_ERR_CUDA of the call it has to be
+ * initialised anew. */
 DSA_API dsa_status_t dsa_evict_cache(const dsa_serve_config_t* cfg, const float* w_pages,
                                      const float* rank_pages, const int32_t* block_table, const int32_t* seq_lens,
                                      const int32_t* keep_lens, int64_t n_first, int64_t n_last,

@@ -84,22 +84,14 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t x, uint64_t* sums, uint6
   return (warp ? before : 0ull) + incl - x;
 }
 
-__device__ __forceinline__ void st_cluster4(uint32_t addr, const uint4& v) {
-  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x),
-               "r"(v.y), "r"(v.z), "r"(v.w)
-               : "memory");
-}
-__device__ __forceinline__ uint4 add4(const uint4& a, const uint4& b) {
-  return make_uint4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
-}
-
 // A cluster has a request, each CTA of it consecutive places.  Cached: their keys
 // lie in shared memory, else they are read again in each pass.
 //
 // Passes of eight bits, four at most, find the left-th largest key: each CTA counts
-// its keys, one warp adds up the cluster's counts and finds the digit.  Then a bit for
-// each place says whether its token stays, and scans of population counts over groups
-// of eight places number the equal keys, the freed places and the movers.
+// its keys, the cluster's leader adds up the counts, and a warp of it finds the
+// digit.  Then a bit for each place says whether its token stays, and scans of
+// population counts over groups of eight places number the equal keys, the freed
+// places and the movers.
 template <bool Cached>
 __global__ void __launch_bounds__(kMaxThreads) select_kernel(
     const float* w, const float* ranks, const int32_t* table, const int32_t* seq,
@@ -116,6 +108,7 @@ __global__ void __launch_bounds__(kMaxThreads) select_kernel(
   uint32_t* keys = equal_w + max_words;
   __shared__ alignas(16) uint32_t hist[2][kCopies][256];  // in turns
   __shared__ uint64_t sums[32];
+  __shared__ alignas(16) uint32_t sum_hist[256];          // the leader's: of the cluster
   // the digit, keys above it, keys with it, and of those the ones in the CTAs before
   __shared__ uint32_t found[4];
   __shared__ uint32_t totals[2];          // freed places and movers of this CTA
@@ -208,37 +201,30 @@ __global__ void __launch_bounds__(kMaxThreads) select_kernel(
       if ((k & above) == prefix) atomicAdd(mine + ((k >> shift) & 255u), 1u);
     });
     __syncthreads();
-    // lane l of a warp has the digits 8 l' .. 8 l' + 7, l' = 31 - l
-    const int d0 = 8 * (31 - lane);
-    uint4 a = make_uint4(0u, 0u, 0u, 0u), c = a;
-    if (warp == 0) {
+    if (tid < 256) {
+      uint32_t sum = 0u;
 #pragma unroll
-      for (int i = 0; i < kCopies; ++i) {
-        a = add4(a, *reinterpret_cast<const uint4*>(&hist[turn][i][d0]));
-        c = add4(c, *reinterpret_cast<const uint4*>(&hist[turn][i][d0 + 4]));
-      }
-      if (size > 1) {  // to the leader
-        const uint32_t at = at_rank(smem_u32(cluster_sums + rank * 256 + d0), 0);
-        st_cluster4(at, a);
-        st_cluster4(at + 16, c);
-      }
-    } else {
-      for (int i = tid - 32; i < kCopies * 64; i += nt - 32)  // for the next pass
-        reinterpret_cast<uint4*>(hist[turn ^ 1])[i] = make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < kCopies; ++i) sum += hist[turn][i][tid];
+      if (size > 1) st_cluster_u32(at_rank(smem_u32(cluster_sums + rank * 256 + tid), 0), sum);
+      else sum_hist[tid] = sum;
     }
+    for (int i = tid; i < kCopies * 64; i += nt)  // for the next pass
+      reinterpret_cast<uint4*>(hist[turn ^ 1])[i] = make_uint4(0u, 0u, 0u, 0u);
     if (size > 1) {
       cluster_arrive();
       cluster_wait();
-    }
-    if (warp == 0 && rank == 0) {
-      if (size > 1) {
-        a = c = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll 4
-        for (uint32_t r = 0; r < size; ++r) {
-          a = add4(a, *reinterpret_cast<const uint4*>(cluster_sums + r * 256 + d0));
-          c = add4(c, *reinterpret_cast<const uint4*>(cluster_sums + r * 256 + d0 + 4));
-        }
+      if (rank == 0 && tid < 256) {
+        uint32_t sum = 0u;
+#pragma unroll 8
+        for (uint32_t r = 0; r < size; ++r) sum += cluster_sums[r * 256 + tid];
+        sum_hist[tid] = sum;
       }
+    }
+    if (rank == 0) __syncthreads();
+    if (warp == 0 && rank == 0) {
+      const int d0 = 8 * (31 - lane);  // lane l has the digits d0 .. d0 + 7
+      const uint4 a = *reinterpret_cast<const uint4*>(sum_hist + d0);
+      const uint4 c = *reinterpret_cast<const uint4*>(sum_hist + d0 + 4);
       const uint32_t n8[8] = {c.w, c.z, c.y, c.x, a.w, a.z, a.y, a.x};  // digits downwards
       uint32_t sum = 0u;
 #pragma unroll

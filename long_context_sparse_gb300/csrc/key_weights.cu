@@ -293,6 +293,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(epi, kEpiWarps);
     mbar_init(done_bar, 1);
     misc[0] = 0u;
+    scratch[16] = scratch[17] = 0;  // the share, should the lengths change under the kernel
     fence_mbar_init();
     prefetch_tensormap(&q_map);
     prefetch_tensormap(&k_map);
