@@ -17,8 +17,6 @@
 namespace dsa {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 4;      // 16-byte vectors of a thread in flight: a batch
 constexpr int kMaxTop = 64;
 constexpr int kKept = 4;        // batches that a thread remembers
@@ -209,20 +207,21 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 // Alternatives, exactly and in the same pass: each thread remembers its kKept
 // batches with the largest maxima.  A value that n of the threads' best elements
 // reach is a bound for the n best of the share: here the n-th largest of what the k
-// best threads of each of the 8 warps have, 8 k >= n.  Only the batches whose maximum
-// reaches it are looked at again, in L2, an element a lane, and few elements of
-// those pass.  A thread of which more batches than it remembers may reach the bound sends
-// the share through a second look at all of it.  Where more elements pass than the
-// buffer holds (rows of many equal values), ids break the ties already in the bound;
-// and should that not do either, `n` passes each look for the largest below the last.
-// `Again`: the rows are few, and what is looked at again is found in L1 (64 rows of 131072
-// bf16 with 20 alternatives: 1.2 us less; with a row a CTA, 4% more).
-template <typename T, bool Top, bool Again>
-__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
+// best threads of each warp have, two more than n in all need.  Only the batches whose
+// maximum reaches it are looked at again, in L2, an element a lane and eight batches
+// on their way at a time, and few elements of those pass.  A thread of which more
+// batches than it remembers may reach the bound sends the share through a second look
+// at all of it.  Where more elements pass than the buffer holds (rows of many equal
+// values), ids break the ties already in the bound; and should that not do either, `n`
+// passes each look for the largest below the last.
+// Wide: the rows are few and have a cluster each; what is looked at again is found in
+// L1 (64 rows of 131072 bf16 with 20 alternatives: 1.2 us less; with a row a CTA, 4% more).
+template <typename T, bool Top, bool Wide, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(
     const T* logits, int64_t ld, int32_t vocab, const int32_t* tokens, int n_top, float scale,
     float* logp, float* lse, float* entropy, int32_t* top_ids, float* top_logp,
     uint32_t* status) {
-  constexpr int kWords = 4 * kUnroll, kStep = kUnroll * kThreads;
+  constexpr int kWarps = kThreads / 32, kWords = 4 * kUnroll, kStep = kUnroll * kThreads;
   using W = Word<T>;
   __shared__ Stat stats[kWarps];
   __shared__ Stat total;
@@ -231,16 +230,18 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
   __shared__ uint64_t top[Top ? kMaxTop : 1];
   // the leader's: what the cluster's CTAs have found
   __shared__ Stat from[kMaxCluster];
-  __shared__ alignas(16) uint64_t from_top[Top ? kMaxTop * kMaxCluster : 2];
-  __shared__ uint32_t warp_best[kMaxTop + kWarps];
-  __shared__ uint32_t n_buf, again, has_token;
-  __shared__ float x_token;
+  __shared__ alignas(16) uint64_t from_top[Wide && Top ? kMaxTop * kMaxCluster : 2];
+  __shared__ uint32_t warp_best[96];
+  // [warp][lanes and numbers of the batches that are looked at again]
+  __shared__ uint32_t again_list[Top ? kWarps : 1][Top ? 32 * kKept : 1];
+  __shared__ uint32_t n_buf, again, tok_at, tok_word;
+  __shared__ int32_t token;
   __shared__ uint64_t bound;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t rank, size;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
-  if (size > 1) cluster_arrive();  // the leader has begun: waited for before it is written to
+  if (Wide) cluster_arrive();  // the leader has begun: waited for before it is written to
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t r = blockIdx.x / size;
@@ -251,6 +252,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
   const int32_t v0 = min(row.n_vec, (int)rank * per), v1 = min(row.n_vec, v0 + per);
   const int n_single = rank == 0 ? row.n_single() : 0;
   const uint4* vec = row.vec();
+  const bool has_token = rank == 0 && tid == kThreads - 1;  // the thread that sees to it
 
   float ref = kUnset;
   uint64_t s2 = 0ull, t2 = 0ull;
@@ -299,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
     for (int u = 0; u < kUnroll; ++u) {
       uint4 x = make_uint4(W::kNone, W::kNone, W::kNone, W::kNone);
       if (v + u * kThreads < v1)
-        x = Again ? ld_input(vec + v + u * kThreads) : ld_stream(vec + v + u * kThreads);
+        x = Wide && Top ? ld_input(vec + v + u * kThreads) : ld_stream(vec + v + u * kThreads);
       w[4 * u] = x.x;
       w[4 * u + 1] = x.y;
       w[4 * u + 2] = x.z;
@@ -338,6 +340,10 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
     uint32_t w[2][kWords];
     int32_t v = v0 + tid;
     if (v < v1) load(v, w[0]);
+    if (has_token)  // on its way to shared memory beside the row
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&token)),
+                   "l"(tokens + r)
+                   : "memory");
     if (tid < n_single) {
       const float x = load1(row.at + row.single(tid));
       if (Top) remember(x, -1);
@@ -371,18 +377,23 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
       all = lane & s ? merge(o, all, c) : merge(all, o, c);
     }
   };
-  merge_lanes(16);
-  if (lane == 0) stats[warp] = all;
-  if (tid == 0) n_buf = again = 0u;
-  if (rank == 0 && tid == kThreads - 1) {  // on its way beside the rest
-    int32_t tok = ld_input(tokens + r);
+  if (has_token) {  // and the word that holds its logit beside what follows
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    int32_t tok = token;
     if (tok >= vocab) {
       latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
       tok = -1;
     }
-    has_token = tok >= 0 ? 1u : 0u;
-    if (tok >= 0) x_token = load1(row.at + tok);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row.at + (tok < 0 ? 0 : tok));
+    tok_at = tok < 0 ? ~0u : (uint32_t)(at & 3u);
+    if (tok >= 0)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&tok_word)),
+                   "l"(at & ~(uintptr_t)3)
+                   : "memory");
   }
+  merge_lanes(16);
+  if (lane == 0) stats[warp] = all;
+  if (tid == 0) n_buf = again = 0u;
   // the elements of the thread's share, at least of the vectors whose largest order
   // key reaches floor(): f(value, id)
   auto visit_all = [&](auto floor, auto f) {
@@ -424,7 +435,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
   // ---- the share's alternatives, in order, into top[]
   if (Top) {
     // the threads that have vectors come first; whole warps of them have k each
-    const int full = min(kThreads, v1 - v0) >> 5, k = full ? (n_top + full - 1) / full : 33;
+    const int full = min(kThreads, v1 - v0) >> 5;
+    const int k = full ? min((n_top + full - 1) / full + (n_top > 24 ? 2 : 1), 96 / full) : 33;
     if (k <= 32 && warp < full) {
       uint32_t mine = kept[0];
       for (int i = 0; i < k; ++i) {
@@ -434,24 +446,29 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
         if (lane == 0) warp_best[warp * k + i] = reached;
       }
     }
-    if (tid < kMaxTop) top[tid] = 0ull;
+    for (int i = tid; i < kMaxTop; i += kThreads) top[i] = 0ull;
     __syncthreads();
     uint32_t least = 0u;
-    if (k <= 32) {  // full * k values, at most full - 1 of them beyond the n-th
+    if (k <= 32) {  // full * k values, n_top or more: from the nearer end
       const int list = full * k;
-      uint32_t a = lane < list ? warp_best[lane] : ~0u;
-      uint32_t b = lane + 32 < list ? warp_best[lane + 32] : ~0u;
-      uint32_t c3 = lane + 64 < list ? warp_best[lane + 64] : ~0u;
-      for (int i = n_top; i <= list; ++i) {
-        least = __reduce_min_sync(0xffffffffu, min(min(a, b), c3));
+      uint32_t x[3];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) x[i] = lane + 32 * i < list ? warp_best[lane + 32 * i] : 0u;
+      // counted from above 0 stands for none, from below (of what is left of ~0) too
+      const bool up = n_top > list - n_top;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) x[i] = up && x[i] ? ~x[i] : x[i];
+      for (int i = up ? list - n_top + 1 : n_top; i > 0; --i) {
+        least = __reduce_max_sync(0xffffffffu, max(max(x[0], x[1]), x[2]));
         const uint32_t who =
-            __ballot_sync(0xffffffffu, a == least || b == least || c3 == least);
+            __ballot_sync(0xffffffffu, x[0] == least || x[1] == least || x[2] == least);
         if (lane == __ffs(who) - 1) {
-          if (a == least) a = ~0u;
-          else if (b == least) b = ~0u;
-          else c3 = ~0u;
+          if (x[0] == least) x[0] = 0u;
+          else if (x[1] == least) x[1] = 0u;
+          else x[2] = 0u;
         }
       }
+      if (up) least = ~least;
     }
     uint64_t at_least = (uint64_t)least << 32;
     auto reach = [&] { return (uint32_t)(at_least >> 32); };
@@ -463,36 +480,39 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
     };
     if (kept[kKept - 1] && kept[kKept - 1] >= least && batches + (tid < n_single) > kKept)
       again = 1u;
-    constexpr int kElems = kUnroll * Row<T>::kVec, kPerLoad = 32 / kElems, kLoads = 4;
+    constexpr int kElems = kUnroll * Row<T>::kVec, kPerLoad = 32 / kElems, kLoads = 8;
+    int listed = 0;
 #pragma unroll
     for (int q = 0; q < kKept; ++q) {
-      uint32_t who = __ballot_sync(0xffffffffu, kept[q] && kept[q] >= least);
-      while (who) {
-        float x[kLoads];
-        uint32_t id[kLoads];
+      const uint32_t who = __ballot_sync(0xffffffffu, kept[q] && kept[q] >= least);
+      if (who >> lane & 1u)
+        again_list[warp][listed + __popc(who & ((1u << lane) - 1u))] =
+            (uint32_t)lane | (uint32_t)(which[q] + 1) << 5;
+      listed += __popc(who);
+    }
+    __syncwarp();
+    for (int i0 = 0; i0 < listed; i0 += kLoads * kPerLoad) {
+      float x[kLoads];
+      uint32_t id[kLoads];
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-          int l = -1;  // the lane whose batch this lane looks at
-#pragma unroll
-          for (int h = 0; h < kPerLoad; ++h) {
-            if (lane / kElems == h) l = __ffs(who) - 1;
-            who &= who - 1u;
-          }
-          const int32_t number = __shfl_sync(0xffffffffu, which[q], l < 0 ? 0 : l);
-          const int e = lane % kElems, t = (warp << 5) + l;
-          id[i] = ~0u;
-          if (l >= 0 && number < 0) {
+      for (int i = 0; i < kLoads; ++i) {
+        const int at = i0 + i * kPerLoad + lane / kElems, e = lane % kElems;
+        id[i] = ~0u;
+        if (at < listed) {
+          const uint32_t entry = again_list[warp][at];
+          const int t = (warp << 5) + (int)(entry & 31u), number = (int)(entry >> 5) - 1;
+          if (number < 0) {
             if (e == 0) id[i] = (uint32_t)row.single(t);
-          } else if (l >= 0) {
+          } else {
             const int32_t v = v0 + t + number * kStep + e / Row<T>::kVec * kThreads;
             if (v < v1) id[i] = (uint32_t)(row.id(v) + e % Row<T>::kVec);
           }
-          if (id[i] != ~0u) x[i] = load1(row.at + id[i]);
         }
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-          if (id[i] != ~0u) push(x[i], id[i]);
+        if (id[i] != ~0u) x[i] = load1(row.at + id[i]);
       }
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        if (id[i] != ~0u) push(x[i], id[i]);
     }
     __syncthreads();
     if (again) {
@@ -557,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
     if (lane == 0) total = all;
   }
   // ---- the row's: the others write to the leader, and go
-  if (size > 1) {
+  if (Wide) {
     cluster_wait();
     __syncthreads();
     if (tid < 3) {
@@ -570,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
                        reinterpret_cast<const uint32_t*>(top)[i]);
     if (Top && rank == 0 && tid < n_top) from_top[tid] = top[tid];
     cluster_arrive();
-    if (rank != 0) return;
+      if (rank != 0) return;
     cluster_wait();
     if (warp == 0) {
       all = lane < (int)size ? from[lane] : Stat{kUnset, 0.f, 0.f};
@@ -594,6 +614,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
       });
     }
   }
+  if (has_token) asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
   const Stat s = total;
   const bool none = s.s == 0.f;  // nothing but -inf
@@ -601,43 +622,83 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(
   if (tid == 0) {
     lse[r] = none ? -INFINITY : fmaf(s.r, scale, ln);
     entropy[r] = none ? 0.f : ln - kLn2 * (s.t / s.s);
-    logp[r] = !has_token ? 0.f : none ? -INFINITY : (x_token - s.r) * scale - ln;
+    float x[W::kPer];
+    W::get(tok_word, x);
+    logp[r] = tok_at == ~0u ? 0.f
+              : none        ? -INFINITY
+                            : (x[W::kPer == 2 && tok_at ? 1 : 0] - s.r) * scale - ln;
   }
-  if (Top && tid < n_top) {
-    const uint64_t key = top[tid];
-    if (!DSA_IN_BOUNDS((uint32_t)key_id(key) < (uint32_t)vocab, status)) return;
-    top_ids[r * n_top + tid] = key_id(key);
-    top_logp[r * n_top + tid] = none ? -INFINITY : (key_value(key) - s.r) * scale - ln;
-  }
+  if (Top)
+    for (int i = tid; i < n_top; i += kThreads) {
+      const uint64_t key = top[i];
+      if (!DSA_IN_BOUNDS((uint32_t)key_id(key) < (uint32_t)vocab, status)) continue;
+      top_ids[r * n_top + i] = key_id(key);
+      top_logp[r * n_top + i] = none ? -INFINITY : (key_value(key) - s.r) * scale - ln;
+    }
 }
 
 // Backward.  With l = log p = scale x - lse:  dx = 2^(l log2 e) (A + B l) + 1[tok] G,
 //   A = -scale (g + h H),  B = -scale h,  G = scale g.
-// A block takes kUnroll vectors a thread of one row; a row whose logits and
-// gradients lie differently in their 16 bytes goes element by element.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) logprobs_bwd_kernel(
+// A block takes kUnroll vectors a thread of one row, as the gradient lies in its 16
+// bytes.  Where the logits lie differently, a vector of them is put together from the
+// two that hold it: the neighbour's second is this one's first, and comes from L1.
+constexpr int kBwdThreads = 256;
+
+// 16 bytes from byte 4 * words + 2 * half on of the 32 in lo, hi
+__device__ __forceinline__ uint4 shifted(const uint4& lo, const uint4& hi, uint32_t words,
+                                         uint32_t half) {
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+  for (int i = 0; i < 7; ++i) w[i] = words & 1u ? w[i + 1] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = words & 2u ? w[i + 2] : w[i];
+  return make_uint4(__funnelshift_r(w[0], w[1], 16u * half), __funnelshift_r(w[1], w[2], 16u * half),
+                    __funnelshift_r(w[2], w[3], 16u * half),
+                    __funnelshift_r(w[3], w[4], 16u * half));
+}
+
+// Alike: every row's logits lie as its gradient does (the path aside costs 12 registers
+// and 6% of 8192 rows of 131072).
+template <typename T, bool Alike>
+__global__ void __launch_bounds__(kBwdThreads) logprobs_bwd_kernel(
     const T* logits, int64_t ld, int64_t rows, int32_t vocab, int32_t segs,
     const int32_t* tokens, const float* lse, const float* entropy, const float* g_logp,
     const float* g_entropy, float scale, T* dlogits, int64_t ld_grad, uint32_t* status) {
   using W = Word<T>;
-  constexpr int kVec = Row<T>::kVec, kSeg = kUnroll * kThreads;
+  constexpr int kVec = Row<T>::kVec, kSeg = kUnroll * kBwdThreads;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x;
   for (int64_t item = blockIdx.x; item < rows * segs; item += gridDim.x) {
     const int64_t r = item / segs;
     const int32_t seg = (int32_t)(item - r * segs);
-    const Row<T> row(logits + r * ld, vocab);
+    const T* x_row = logits + r * ld;
     T* out = dlogits + r * ld_grad;
-    const bool alike =
-        ((reinterpret_cast<uintptr_t>(row.at) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
-    const uint4* vec = row.vec() + (int64_t)seg * kSeg + tid;
+    const Row<T> row(out, vocab);  // divided as the gradient lies
+    const T* first = x_row + row.head;
+    const uint32_t off =
+        Alike ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(first) & 15u);
+    const uint4* vec = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(first) - off) +
+                       (int64_t)seg * kSeg + tid;
     const int32_t v0 = seg * kSeg + tid;
     uint4 in[kUnroll];
+    if (Alike || off == 0u) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (alike && v0 + u * kThreads < row.n_vec) in[u] = ld_stream(vec + u * kThreads);
+      for (int u = 0; u < kUnroll; ++u)
+        if (v0 + u * kBwdThreads < row.n_vec) in[u] = ld_stream(vec + u * kBwdThreads);
+    } else {  // (each of the two vectors holds some of the row)
+      uint4 hi[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        if (v0 + u * kBwdThreads < row.n_vec) {
+          in[u] = ld_input(vec + u * kBwdThreads);
+          hi[u] = ld_input(vec + u * kBwdThreads + 1);
+        }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        if (v0 + u * kBwdThreads < row.n_vec)
+          in[u] = shifted(in[u], hi[u], off >> 2, (off >> 1) & 1u);
+    }
     int32_t tok = ld_input(tokens + r);
     if (tok >= vocab) {
       if (tid == 0 && seg == 0) latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
@@ -655,30 +716,24 @@ __global__ void __launch_bounds__(kThreads) logprobs_bwd_kernel(
       if (id == tok) d += G;
       return none ? 0.f : d;
     };
-    if (alike) {
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int32_t v = v0 + u * kThreads;
-        if (v >= row.n_vec) break;
-        uint32_t w[4] = {in[u].x, in[u].y, in[u].z, in[u].w};
+    for (int u = 0; u < kUnroll; ++u) {
+      const int32_t v = v0 + u * kBwdThreads;
+      if (v >= row.n_vec) break;
+      uint32_t w[4] = {in[u].x, in[u].y, in[u].z, in[u].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float x[W::kPer];
-          W::get(w[i], x);
+      for (int i = 0; i < 4; ++i) {
+        float x[W::kPer];
+        W::get(w[i], x);
 #pragma unroll
-          for (int e = 0; e < W::kPer; ++e) x[e] = grad(x[e], row.id(v) + i * W::kPer + e);
-          w[i] = W::put(x);
-        }
-        reinterpret_cast<uint4*>(out + row.head)[v] = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int e = 0; e < W::kPer; ++e) x[e] = grad(x[e], row.id(v) + i * W::kPer + e);
+        w[i] = W::put(x);
       }
-      if (seg == 0 && tid < row.n_single()) {
-        const int32_t id = row.single(tid);
-        out[id] = to_type<T>(grad(load1(row.at + id), id));
-      }
-    } else {
-      const int32_t end = min((int64_t)vocab, ((int64_t)seg + 1) * kSeg * kVec);
-      for (int32_t id = seg * kSeg * kVec + tid; id < end; id += kThreads)
-        out[id] = to_type<T>(grad(load1(row.at + id), id));
+      reinterpret_cast<uint4*>(out + row.head)[v] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    if (seg == 0 && tid < row.n_single()) {
+      const int32_t id = row.single(tid);
+      out[id] = to_type<T>(grad(load1(x_row + id), id));
     }
   }
 }
@@ -718,14 +773,14 @@ dsa_status_t check_ws256(void* ws, size_t ws_bytes) {
 struct Launch {
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = {};
-  Launch(const LaunchCtx& c, unsigned grid, int cluster) {
+  Launch(const LaunchCtx& c, unsigned grid, int threads, int cluster) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = (unsigned)cluster;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.stream = c.stream;
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
@@ -765,17 +820,31 @@ dsa_status_t dsa_token_logprobs(const dsa_logprobs_config_t* cfg, const void* lo
   // rows 16.7 14.0 12.3 11.0; 64 rows 17.5 15.3 13.5 14.9; 150 rows 18 16.9 22.3 30.7; 300
   // rows 23.4 24.8 35.8 53.8.
   int size = 1;
-  const int64_t batch = (int64_t)kThreads * kUnroll * (16 / (int64_t)elem_bytes(cfg));
+  const int64_t one = kUnroll * (16 / (int64_t)elem_bytes(cfg)), batch = 256 * one;
   while (size < kMaxCluster && cfg->rows * size <= ctx.num_sms &&
          cfg->vocab >= 2 * size * batch)
     size *= 2;
   if (cfg->rows * size >= (int64_t)1 << 31) return DSA_ERR_UNSUPPORTED_SHAPE;
-  Launch l(ctx, (unsigned)(cfg->rows * size), size);
+  // Many rows: the steps behind a row's last logit are waits more than work, so that
+  // short rows want few threads and many CTAs an SM; where a thread's batches are many
+  // the second looks take over.  us with 32, 128, 256 threads, 20 alternatives, bf16: 8192
+  // rows of 1000 28 67 119; 4000 of 4096 27 35 55; 2000 of 16384 54 31 38; 4000 of 32000 -
+  // 90 89; 4096 of 131072 - 230 208; with 64 alternatives 8192 of 1000 500 127 215.
+  int threads = 256;
+  if (cfg->rows > ctx.num_sms && cfg->vocab <= 16 * 32 * one) threads = 128;
+  if (cfg->rows > ctx.num_sms && cfg->vocab <= 4 * 32 * one && cfg->n_top <= 24) threads = 32;
+  Launch l(ctx, (unsigned)(cfg->rows * size), threads, size);
   auto run = [&](auto zero) {
     using T = decltype(zero);
-    auto kern = cfg->n_top == 0 ? logprobs_kernel<T, false, false>
-                : size > 1      ? logprobs_kernel<T, true, true>
-                                : logprobs_kernel<T, true, false>;
+    const bool top = cfg->n_top > 0;
+    auto kern = size > 1         ? (top ? logprobs_kernel<T, true, true, 256>
+                                        : logprobs_kernel<T, false, true, 256>)
+                : threads == 32  ? (top ? logprobs_kernel<T, true, false, 32>
+                                        : logprobs_kernel<T, false, false, 32>)
+                : threads == 128 ? (top ? logprobs_kernel<T, true, false, 128>
+                                        : logprobs_kernel<T, false, false, 128>)
+                                 : (top ? logprobs_kernel<T, true, false, 256>
+                                        : logprobs_kernel<T, false, false, 256>);
     return cuda_status(cudaLaunchKernelEx(&l.cfg, kern, static_cast<const T*>(logits), cfg->ld,
                                           (int32_t)cfg->vocab, tokens, (int)cfg->n_top,
                                           cfg->scale, logp, lse, entropy, top_ids, top_logp,
@@ -816,20 +885,24 @@ dsa_status_t dsa_token_logprobs_bwd(const dsa_logprobs_config_t* cfg, const void
   if (written_meets(writes, reads)) return DSA_ERR_INVALID_ARG;
   LaunchCtx ctx;
   if ((st = make_ctx(ws, stream, &ctx)) != DSA_OK) return st;
-  const int64_t per = (int64_t)kThreads * kUnroll * (16 / (int64_t)elem_bytes(cfg));
+  const int64_t per = (int64_t)kBwdThreads * kUnroll * (16 / (int64_t)elem_bytes(cfg));
   const int32_t segs = (int32_t)((cfg->vocab + per - 1) / per);
   const int64_t items = cfg->rows * segs, most = ((int64_t)1 << 31) - 1;
-  Launch l(ctx, (unsigned)(items < most ? items : most), 1);
-  auto run = [&](auto zero, auto kern) {
+  Launch l(ctx, (unsigned)(items < most ? items : most), kBwdThreads, 1);
+  const size_t e = elem_bytes(cfg);
+  const bool alike =
+      ((reinterpret_cast<uintptr_t>(logits) ^ reinterpret_cast<uintptr_t>(dlogits)) & 15u) == 0 &&
+      (cfg->rows == 1 || ((size_t)(cfg->ld - ld_grad) * e & 15u) == 0);
+  auto run = [&](auto zero) {
     using T = decltype(zero);
     return cuda_status(cudaLaunchKernelEx(
-        &l.cfg, kern, static_cast<const T*>(logits), cfg->ld, cfg->rows, (int32_t)cfg->vocab,
-        segs, tokens, lse, entropy, g_logp, g_entropy, cfg->scale, static_cast<T*>(dlogits),
-        ld_grad, ctx.status));
+        &l.cfg, alike ? logprobs_bwd_kernel<T, true> : logprobs_bwd_kernel<T, false>,
+        static_cast<const T*>(logits), cfg->ld, cfg->rows, (int32_t)cfg->vocab, segs, tokens, lse,
+        entropy, g_logp, g_entropy, cfg->scale, static_cast<T*>(dlogits), ld_grad, ctx.status));
   };
-  if (cfg->dtype == DSA_BF16) return run(__nv_bfloat16(), logprobs_bwd_kernel<__nv_bfloat16>);
-  if (cfg->dtype == DSA_FP16) return run(__half(), logprobs_bwd_kernel<__half>);
-  return run(float(), logprobs_bwd_kernel<float>);
+  if (cfg->dtype == DSA_BF16) return run(__nv_bfloat16());
+  if (cfg->dtype == DSA_FP16) return run(__half());
+  return run(float());
 }
 
 }  // extern "C"
