@@ -403,19 +403,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (here || walk.dead(a)) continue;
       here = true;
       int32_t row = n_rows_cache;
-      if (walk.tile * kTile + key0 < walk.r.len && lane < nb) {
+      const bool has = lane < nb && walk.tile * kTile + key0 < walk.r.len;
+      if (has) {
         if (next_page < 0 || next_page >= a.n_pages)
           latch_error(a.status, DSA_ERR_DEVICE_BAD_INDEX);
         else
           row = next_page << a.page_log2;
       }
       next_page = page_at(walk.tile + 1);
+      // boxes behind the last token are left out: what lies there gives sums of keys
+      // that are not, and stays with them
+      const int32_t keys = min(kTile, walk.r.len - walk.tile * kTile);
+      const uint32_t bytes = (uint32_t)((keys + page - 1) & -page) * 128u;
 #pragma unroll 1
       for (int c = 0; c < kChunks; ++c, ++kc) {
         const uint32_t s = kc % kKSlots;
         if (!(ok = W.wait(k_empty(s), ((kc / kKSlots) & 1u) ^ 1u))) break;
-        if (arms) mbar_expect_tx(k_full(s), 2 * kKBytes);
-        if (lane < nb)
+        if (arms) mbar_expect_tx(k_full(s), bytes);
+        if (has)
           tma_load_pair(sK + s * kKBytes + (uint32_t)(lane * page) * 128u, &k_map, c * 64, row,
                         lead + 8u * s);
       }
