@@ -566,11 +566,11 @@ DSA_API dsa_status_t dsa_key_weights(const dsa_serve_config_t* cfg, const void* 
 /* Eviction of one layer's cache by weight.  Request b keeps left_b =
  * min(seq_lens[b], keep_lens[b]) of its own tokens: those that come first by
  * rank_pages (NULL: by w_pages), where the first n_first and the last n_last
- * places count as +inf, ties go to the lower place and NaN comes last.  A key has no position (NoPE), so
- * kept tokens need not stay in order: with a_0 < a_1 < .. the places below left_b
- * whose tokens are dropped and c_0 < c_1 < .. the places from left_b on whose
- * tokens are kept (as many), the rows of k_pages (and v_pages) at c_i are copied
- * to a_i, and
+ * places count as +inf, ties go to the lower place and NaN comes last.  A key has
+ * no position (NoPE), so kept tokens need not stay in order: with a_0 < a_1 < ..
+ * the places below left_b whose tokens are dropped and c_0 < c_1 < .. the places
+ * from left_b on whose tokens are kept (as many), the rows of k_pages (and
+ * v_pages) at c_i are copied to a_i, and
  *   w_out[slot of place j] = w_pages[slot of j's token], 0 <= j < left_b.
  * Nothing that is read is written, so the caches are changed in place.  Tables
  * and lengths stay: one dsa_release_pages a step serves all layers.  Rows and
@@ -579,7 +579,8 @@ DSA_API dsa_status_t dsa_key_weights(const dsa_serve_config_t* cfg, const void* 
  * After a tree of drafts, a rank of -inf for the rejected nodes and of +inf for all
  * other tokens, with keep_lens the lengths without the rejected ones, leaves the
  * accepted ones with the rest.
- * rank_pages, w_pages, w_out [n_pages, page_size] fp32, keep_lens [B] int32, n_first, n_last >= 0; seq_lens, block_table as above;
+ * rank_pages, w_pages, w_out [n_pages, page_size] fp32, keep_lens [B] int32,
+ * n_first, n_last >= 0; seq_lens, block_table as above;
  * max_blocks * page_size <= 2^22, else DSA_ERR_UNSUPPORTED_SHAPE.  What is written
  * must not overlap what is read, or itself, in any other way
  * (DSA_ERR_INVALID_ARG).  A page may not belong to two requests, or stand twice
@@ -591,10 +592,11 @@ DSA_API dsa_status_t dsa_key_weights(const dsa_serve_config_t* cfg, const void* 
  * ws: DSA_SERVE_WS_EVICT; after a DSA_ERR_CUDA of the call it has to be
  * initialised anew. */
 DSA_API dsa_status_t dsa_evict_cache(const dsa_serve_config_t* cfg, const float* w_pages,
-                                     const float* rank_pages, const int32_t* block_table, const int32_t* seq_lens,
-                                     const int32_t* keep_lens, int64_t n_first, int64_t n_last,
-                                     void* k_pages, void* v_pages, float* w_out, void* ws,
-                                     size_t ws_bytes, void* stream);
+                                     const float* rank_pages, const int32_t* block_table,
+                                     const int32_t* seq_lens, const int32_t* keep_lens,
+                                     int64_t n_first, int64_t n_last, void* k_pages,
+                                     void* v_pages, float* w_out, void* ws, size_t ws_bytes,
+                                     void* stream);
 
 /* The lengths after an eviction and the pages that it leaves free, once a step:
  *   left_b = min(seq_lens[b], keep_lens[b]),   new_lens[b] = left_b,
@@ -662,7 +664,8 @@ DSA_API dsa_status_t dsa_token_logprobs(const dsa_logprobs_config_t* cfg, const 
  *   dlogits[r, j] = scale * (g_logp[r] * (1[j = tokens[r]] - p_j)
  *                            - g_entropy[r] * p_j * (log p_j + entropy[r])),
  * p_j = exp(x_j - lse[r]), rounded once to the logits' type.  A row without a
- * token (below 0) has no part of g_logp; one with lse = -inf has gradient 0.
+ * token (below 0) has no part of g_logp.  Where both parts are 0 or lse is -inf the
+ * gradient is 0, whatever the row's logits are.
  * g_logp or g_entropy may be NULL (0), entropy too where g_entropy is.  lse and
  * entropy are dsa_token_logprobs's of the same logits and scale; n_top is not
  * used.  dlogits [R, ld_grad], ld_grad >= V; what lies between the rows is left

@@ -1122,8 +1122,8 @@ def evict_cache(cfg: ServeConfig, w_pages, block_table, seq_lens, keep_lens, k_p
     p_rank = None
     if rank_pages is not None:
         p_rank = _check_tensor(rank_pages, "rank_pages", f32, slots, dev)
-    _serve_call("dsa_evict_cache", dev, cfg._ref, p_w, p_rank, p_table, p_seq, p_keep, n_first, n_last,
-                p_k, p_v, p_out, p_ws, n_ws)
+    _serve_call("dsa_evict_cache", dev, cfg._ref, p_w, p_rank, p_table, p_seq, p_keep, n_first,
+                n_last, p_k, p_v, p_out, p_ws, n_ws)
     return w_out
 
 
@@ -1239,7 +1239,7 @@ def token_logprobs_bwd(logits, tokens, lse, entropy, g_logp, g_entropy=None,
     """The gradient of sum(g_logp * logp + g_entropy * entropy) with respect to the
     logits, in their type: dlogits [rows, vocab] (a stride of its own between rows;
     logits itself is allowed).  lse and entropy are token_logprobs's.  g_logp or
-    g_entropy may be None."""
+    g_entropy may be None.  Rows where both are 0 get 0, whatever their logits."""
     dev, rows, vocab, ld = _check_logits(logits, "logits")
     f32 = torch.float32
     p_tok = _check_tensor(tokens, "tokens", torch.int32, (rows,), dev)

@@ -174,9 +174,9 @@ cudaError_t launch_append(const LaunchCtx& c, const ServeShape& s, const int32_t
 // Workspace bytes past the header of launch_prefix_attn.
 size_t prefix_attn_ws(const ServeShape& s);
 
-// Shared-prefix attention, of trees where tree_bits is not nullptr; work: the workspace past the header.  q_map: q as
-// [T * H, D], box {64, 64}; k_map, v_maps: the cache as [n_pages * page, D], box
-// {64, page}, and of V also {64, 8} and {64, 1}.
+// Shared-prefix attention, of trees where tree_bits is not nullptr; work: the
+// workspace past the header.  q_map: q as [T * H, D], box {64, 64}; k_map, v_maps: the
+// cache as [n_pages * page, D], box {64, page}, and of V also {64, 8} and {64, 1}.
 cudaError_t launch_prefix_attn(const LaunchCtx& c, const ServeShape& s,
                                const CUtensorMap& q_map, const CUtensorMap& k_map,
                                const CUtensorMap (&v_maps)[3], const int32_t* prefix_table,
@@ -190,7 +190,8 @@ cudaError_t launch_build_tree(const LaunchCtx& c, const ServeShape& s, const int
                               const int32_t* cu, int words, uint32_t* tree_bits);
 
 // Weights that cached tokens receive; q_maps: q as [T * H, D], boxes {64, 32}, {64, 64}
-// and {64, 128}; k_map: the cache as [n_pages * page, D], box {64, page}; ws: the whole workspace.
+// and {64, 128}; k_map: the cache as [n_pages * page, D], box {64, page}; ws: the whole
+// workspace.
 size_t key_weights_ws(const ServeShape& s);
 cudaError_t launch_key_weights(const LaunchCtx& c, const ServeShape& s,
                                const CUtensorMap (&q_maps)[3], const CUtensorMap& k_map,
@@ -198,12 +199,14 @@ cudaError_t launch_key_weights(const LaunchCtx& c, const ServeShape& s,
                                const int32_t* cu, const uint32_t* tree_bits, int words,
                                const float* w_pages, float decay, float* w_out, uint8_t* ws);
 
-// Eviction by rank (which may be the weights); ws: the whole workspace (its header has the counters).
+// Eviction by rank (which may be the weights); ws: the whole workspace (its header has
+// the counters).
 size_t evict_ws(const ServeShape& s);
 cudaError_t launch_evict(const LaunchCtx& c, const ServeShape& s, const float* w_pages,
-                         const float* rank_pages, const int32_t* table, const int32_t* seq, const int32_t* keep,
-                         int32_t n_first, int32_t n_last, __nv_bfloat16* k_pages,
-                         __nv_bfloat16* v_pages, float* w_out, uint8_t* ws);
+                         const float* rank_pages, const int32_t* table, const int32_t* seq,
+                         const int32_t* keep, int32_t n_first, int32_t n_last,
+                         __nv_bfloat16* k_pages, __nv_bfloat16* v_pages, float* w_out,
+                         uint8_t* ws);
 
 // Lengths after an eviction, and the pages that it leaves free.
 cudaError_t launch_release_pages(const LaunchCtx& c, const ServeShape& s, const int32_t* seq,

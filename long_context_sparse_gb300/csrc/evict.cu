@@ -95,9 +95,9 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t x, uint64_t* sums, uint6
 template <bool Cached>
 __global__ void __launch_bounds__(kMaxThreads) select_kernel(
     const float* w, const float* ranks, const int32_t* table, const int32_t* seq,
-    const int32_t* keep, int32_t n_first, int32_t n_last, float* w_out, Moves moves, int64_t list_len,
-    Counters counts, int max_blocks, int page_log2, int64_t n_pages, int max_words,
-    uint32_t* status) {
+    const int32_t* keep, int32_t n_first, int32_t n_last, float* w_out, Moves moves,
+    int64_t list_len, Counters counts, int max_blocks, int page_log2, int64_t n_pages,
+    int max_words, uint32_t* status) {
   extern __shared__ __align__(16) uint32_t smem[];
   uint32_t rank, size;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -420,9 +420,9 @@ constexpr int kMoveBlocks = 5;  // on an SM
 // A warp takes kRows rows at a time, 16 bytes a lane and load; the list's entries of
 // its next rows are on their way while it copies.
 template <int D, bool V>
-__global__ void __launch_bounds__(256, kMoveBlocks) move_kernel(Moves moves, int64_t list_len, uint4* k_pages,
-                                                   uint4* v_pages, const float* w, float* w_out,
-                                                   Counters counts, int64_t n_slots) {
+__global__ void __launch_bounds__(256, kMoveBlocks)
+    move_kernel(Moves moves, int64_t list_len, uint4* k_pages, uint4* v_pages, const float* w,
+                float* w_out, Counters counts, int64_t n_slots) {
   constexpr int kPieces = D / 8;                     // of a row
   constexpr int kRows = (V ? 64 : 128) / kPieces;    // 4 loads a lane
   constexpr int kLoads = kRows * kPieces / 32;       // of a tensor
@@ -475,10 +475,6 @@ __global__ void __launch_bounds__(256, kMoveBlocks) move_kernel(Moves moves, int
     *counts.moves = 0;
 }
 
-}  // namespace
-
-namespace {
-
 // Whether a cluster of kMaxCluster of the selection's largest CTAs finds room.
 bool fits_wide(int smem) {
   cudaLaunchAttribute attr[1];
@@ -502,9 +498,10 @@ bool fits_wide(int smem) {
 size_t evict_ws(const ServeShape& s) { return 2 * round_up((size_t)max_moves(s), 64) * 4; }
 
 cudaError_t launch_evict(const LaunchCtx& c, const ServeShape& s, const float* w_pages,
-                         const float* rank_pages, const int32_t* table, const int32_t* seq, const int32_t* keep,
-                         int32_t n_first, int32_t n_last, __nv_bfloat16* k_pages,
-                         __nv_bfloat16* v_pages, float* w_out, uint8_t* ws) {
+                         const float* rank_pages, const int32_t* table, const int32_t* seq,
+                         const int32_t* keep, int32_t n_first, int32_t n_last,
+                         __nv_bfloat16* k_pages, __nv_bfloat16* v_pages, float* w_out,
+                         uint8_t* ws) {
   cudaError_t e;
   static std::atomic<uint64_t> prepared{0}, wide{0};
   const uint64_t bit = 1ull << (c.device & 63);
@@ -553,8 +550,8 @@ cudaError_t launch_evict(const LaunchCtx& c, const ServeShape& s, const float* w
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, cached ? select_kernel<true> : select_kernel<false>, w_pages,
-                         rank_pages, table, seq, keep, n_first, n_last, w_out, moves, list_len, counts,
-                         s.max_blocks, s.page_log2, s.n_pages, (int)words, c.status);
+                         rank_pages, table, seq, keep, n_first, n_last, w_out, moves, list_len,
+                         counts, s.max_blocks, s.page_log2, s.n_pages, (int)words, c.status);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)(c.num_sms * kMoveBlocks));
   cfg.blockDim = dim3(256);

@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(
                        reinterpret_cast<const uint32_t*>(top)[i]);
     if (Top && rank == 0 && tid < n_top) from_top[tid] = top[tid];
     cluster_arrive();
-      if (rank != 0) return;
+    if (rank != 0) return;
     cluster_wait();
     if (warp == 0) {
       all = lane < (int)size ? from[lane] : Stat{kUnset, 0.f, 0.f};
@@ -652,9 +652,9 @@ __device__ __forceinline__ uint4 shifted(const uint4& lo, const uint4& hi, uint3
   for (int i = 0; i < 7; ++i) w[i] = words & 1u ? w[i + 1] : w[i];
 #pragma unroll
   for (int i = 0; i < 5; ++i) w[i] = words & 2u ? w[i + 2] : w[i];
-  return make_uint4(__funnelshift_r(w[0], w[1], 16u * half), __funnelshift_r(w[1], w[2], 16u * half),
-                    __funnelshift_r(w[2], w[3], 16u * half),
-                    __funnelshift_r(w[3], w[4], 16u * half));
+  const uint32_t s = 16u * half;
+  return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s),
+                    __funnelshift_r(w[2], w[3], s), __funnelshift_r(w[3], w[4], s));
 }
 
 // Alike: every row's logits lie as its gradient does (the path aside costs 12 registers
@@ -709,7 +709,8 @@ __global__ void __launch_bounds__(kBwdThreads) logprobs_bwd_kernel(
     const float h = g_entropy ? ld_f(g_entropy + r) : 0.f;
     const float A = -scale * (g_entropy ? fmaf(h, ld_f(entropy + r), g) : g);
     const float B = -scale * h, G = scale * g;
-    const bool none = l0 == -INFINITY;
+    // (a padding row's logits may be anything)
+    const bool none = l0 == -INFINITY || (g == 0.f && h == 0.f);
     auto grad = [&](float x, int32_t id) {
       const float l = max_nan(fmaf(x, scale, -l0), kNever);
       float d = ex2(l * kLog2e) * fmaf(B, l, A);

@@ -314,10 +314,10 @@ dsa_status_t dsa_evict_cache(const dsa_serve_config_t* cfg, const float* w_pages
   if ((st = make_ctx(ws, stream, &ctx)) != DSA_OK) return st;
   const int32_t most = INT32_MAX;  // lengths are below 2^30
   return cuda_status(launch_evict(
-      ctx, serve_shape(cfg), w_pages, rank_pages ? rank_pages : w_pages, block_table, seq_lens, keep_lens,
-      (int32_t)(n_first < most ? n_first : most), (int32_t)(n_last < most ? n_last : most),
-      static_cast<__nv_bfloat16*>(k_pages), static_cast<__nv_bfloat16*>(v_pages), w_out,
-      static_cast<uint8_t*>(ws)));
+      ctx, serve_shape(cfg), w_pages, rank_pages ? rank_pages : w_pages, block_table, seq_lens,
+      keep_lens, (int32_t)(n_first < most ? n_first : most),
+      (int32_t)(n_last < most ? n_last : most), static_cast<__nv_bfloat16*>(k_pages),
+      static_cast<__nv_bfloat16*>(v_pages), w_out, static_cast<uint8_t*>(ws)));
 }
 
 dsa_status_t dsa_release_pages(const dsa_serve_config_t* cfg, const int32_t* seq_lens,

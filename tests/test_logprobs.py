@@ -366,6 +366,29 @@ def test_gradient_in_place_masked_and_without_tokens(dtype):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("shift", [0, 1])
+def test_rows_without_gradient_are_zero_whatever_their_logits(dtype, shift):
+    """Padding rows: logits, lse and entropy that are not numbers, no token or a
+    gradient of 0, on both ways to read the logits."""
+    x, tok = logits_of(8, 1003, dtype, 12)
+    x[1], x[2, 5], x[3] = math.nan, math.inf, torch.finfo(dtype).max
+    tok[1], tok[3] = -1, -1
+    g, h = torch.ones(8, device=DEV), torch.ones(8, device=DEV)
+    h[1:4], g[2] = 0.0, 0.0
+    p = dsa.token_logprobs(x, tok)
+    out = torch.full((8, 1003 + shift), 9.0, dtype=dtype, device=DEV)[:, shift:]
+    dsa.token_logprobs_bwd(x, tok, p.lse, p.entropy, g, h, dlogits=out)
+    assert (out[1:4] == 0).all() and out[[0, 4, 5, 6, 7]].isfinite().all()
+    assert (out[[0, 4, 5, 6, 7]] != 0).any(1).all()
+    dsa.token_logprobs_bwd(x, tok, p.lse, None, g, dlogits=out)
+    assert (out[1:4] == 0).all()
+    y = x.clone()
+    dsa.token_logprobs_bwd(y, tok, p.lse, p.entropy, g, h, dlogits=y)
+    assert (y[1:4] == 0).all()
+
+
+@gpu
 def test_gradient_against_differences_and_the_forward():
     """The kernels' own lse and entropy into the kernel's gradient; against central
     differences in fp64 and against autograd through the definition."""
