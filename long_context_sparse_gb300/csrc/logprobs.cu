@@ -709,13 +709,22 @@ __global__ void __launch_bounds__(kBwdThreads) logprobs_bwd_kernel(
     const float h = g_entropy ? ld_f(g_entropy + r) : 0.f;
     const float A = -scale * (g_entropy ? fmaf(h, ld_f(entropy + r), g) : g);
     const float B = -scale * h, G = scale * g;
-    // (a padding row's logits may be anything)
-    const bool none = l0 == -INFINITY || (g == 0.f && h == 0.f);
+    // a padding row's logits may be anything.  (They are on their way by now: looking
+    // before they are asked for costs all other rows, 667 us at 606 for 8192 of 131072.)
+    if (l0 == -INFINITY || (g == 0.f && h == 0.f)) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        if (v0 + u * kBwdThreads < row.n_vec)
+          reinterpret_cast<uint4*>(out + row.head)[v0 + u * kBwdThreads] =
+              make_uint4(0u, 0u, 0u, 0u);
+      if (seg == 0 && tid < row.n_single()) out[row.single(tid)] = to_type<T>(0.f);
+      continue;
+    }
     auto grad = [&](float x, int32_t id) {
       const float l = max_nan(fmaf(x, scale, -l0), kNever);
       float d = ex2(l * kLog2e) * fmaf(B, l, A);
       if (id == tok) d += G;
-      return none ? 0.f : d;
+      return d;
     };
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
