@@ -85,9 +85,15 @@ __device__ __forceinline__ Req load_req(const Args& a, int b) {
   r.base = len - (c1 - c0);
   r.tiles = r.rows > 0 ? (len + kTile - 1) / kTile : 0;
   r.blocks = (r.rows + kBlock - 1) / kBlock;
-  const int32_t n64 = (r.rows + 63) / 64;
-  r.cost = r.blocks ? (max(kTileCost, 2 * n64) + r.blocks - 1) / r.blocks : 1;
+  // (a division is a long chain; most requests have one block)
+  r.cost = max(kTileCost, (r.rows + 63) / 64 * 2);
+  if (r.blocks > 1) r.cost = (r.cost + r.blocks - 1) / r.blocks;
   return r;
+}
+__device__ __forceinline__ bool has_units(const Args& a, int b) {
+  const int32_t len = ld_input(a.seq + b);
+  return ld_input(a.cu + b) < ld_input(a.cu + b + 1) && len > 0 &&
+         len <= a.max_blocks << a.page_log2;
 }
 __device__ __forceinline__ int64_t units_of(const Req& r) {
   return (int64_t)r.tiles * r.blocks;
@@ -106,6 +112,11 @@ struct Walk {
   bool first;              // no unit of request b so far
   Req r;
 
+  // units of request b that begin before the share's end
+  __device__ __forceinline__ int64_t units_before_end() const {
+    const int64_t n = units_of(r);
+    return n * r.cost <= end - cb ? n : ceil_div(end - cb, r.cost);
+  }
   __device__ __forceinline__ void begin(const Args& a, int64_t s, int64_t e, int64_t c, int b0) {
     start = s;
     end = e;
@@ -122,7 +133,7 @@ struct Walk {
     }
     r = load_req(a, b);
     const int64_t u0 = s > cb ? ceil_div(s - cb, r.cost) : 0;
-    left = min(units_of(r), ceil_div(end - cb, r.cost)) - u0;
+    left = units_before_end() - u0;
     if (left < 0) left = 0;
     if (r.blocks > 0) {
       tile = (int32_t)(u0 / r.blocks);
@@ -148,12 +159,12 @@ struct Walk {
     uint32_t some = 0;
     while (!some && ++b < a.B) {
       const int x = b + (int)(threadIdx.x & 31);
-      some = __ballot_sync(0xffffffffu, x < a.B && units_of(load_req(a, x)) > 0);
+      some = __ballot_sync(0xffffffffu, x < a.B && has_units(a, x));
       b += some ? __ffs(some) - 1 : 31;
     }
     if (!some) return false;
     r = load_req(a, b);
-    left = min(units_of(r), ceil_div(end - cb, r.cost)) - 1;
+    left = units_before_end() - 1;
     tile = block = 0;
     first = true;
     return true;
@@ -173,7 +184,8 @@ struct Walk {
   }
   // no row of the block sees a key of the tile
   __device__ __forceinline__ bool dead(const Args& a) const {
-    return !a.bits && tile * kTile > r.base + (block * kBlock + rows() - 1) / a.H;
+    return !a.bits &&
+           (int64_t)(tile * kTile - r.base) * a.H > (int64_t)(block * kBlock + rows() - 1);
   }
   __device__ __forceinline__ bool tile_ends() const { return block == r.blocks - 1 || left == 0; }
 };
@@ -548,6 +560,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     float old = 0.f;    // what it has received before
     while (ok && walk.next(a)) {
       const int32_t pos0 = walk.tile * kTile + (int)rank * 128 + quad * 32, pos = pos0 + lane;
+      const bool dead = walk.dead(a);
+      float l = -INFINITY;  // asked for ahead of the table's word, which w_pages' waits for
+      if (!dead && tid < walk.rows())
+        l = __int_as_float(ld_input(reinterpret_cast<const int32_t*>(
+            a.lse + walk.r.row0 + walk.block * kBlock + tid)));
       if (walk.block == 0 || walk.first) {
         head = walk.block != 0;  // the tile began in a pair before
         sum[0] = sum[1] = 0ull;
@@ -563,17 +580,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       walk.first = false;
-      if (!walk.dead(a)) {
+      if (!dead) {
         const int32_t n = walk.rows(), at = walk.block * kBlock;
         float* neg = neg_s + (nu & 1u) * kBlock;
-        {
-          const float l = tid < n ? __int_as_float(ld_input(reinterpret_cast<const int32_t*>(
-                                        a.lse + walk.r.row0 + at + tid)))
-                                  : -INFINITY;
-          neg[tid] = -l;
-          const uint32_t live = __ballot_sync(0xffffffffu, l != -INFINITY);
-          if (lane == 0) live_s[(nu & 1u) * 8 + warp] = live;
-        }
+        neg[tid] = -l;
+        const uint32_t live = __ballot_sync(0xffffffffu, l != -INFINITY);
+        if (lane == 0) live_s[(nu & 1u) * 8 + warp] = live;
         if (!(ok = epi_sync())) break;
         if (!(ok = W.wait(s_full(nu), (nu >> 1) & 1u))) break;
         tc_fence_after();
