@@ -29,14 +29,16 @@ constexpr int kBlock = 256;         // rows of a unit, at most
 constexpr int kMaxPairs = 80;
 constexpr int kEpiWarps = 8;        // 4 TMEM lane quadrants x 2 sets of columns
 constexpr int kKWarp = 8, kScoutWarp = 9, kMmaWarp = 10, kQWarp = 11;
-constexpr int kThreads = 32 * 12;
+constexpr int kPlanWarp = 12;
+constexpr int kThreads = 32 * 13;
 constexpr int kKSlots = 8;          // of 128 keys x 64 dims
 constexpr uint32_t kKBytes = 16384;
 constexpr int kQParts = 20;         // of 32 rows x 64 dims; a chunk's slot has 1, 2 or 4
 constexpr uint32_t kQBytes = 4096;
-constexpr uint32_t kTail = 4096;
+constexpr int kUnits = 4;            // units that are planned ahead
+constexpr uint32_t kTail = 8192;
 constexpr uint32_t kSmem = 1024 + kKSlots * kKBytes + kQParts * kQBytes + kTail;
-constexpr int kBars = 2 * kKSlots + 2 * kQParts + 8;
+constexpr int kBars = 2 * kKSlots + 2 * kQParts + 6 + 2 * kUnits;
 // cost of a tile against few rows, in units of 512 cycles: its K comes from HBM in
 // about 6000 (256 KB at d = 512 and at a pair's share of the rate), while the MMAs of
 // 64 rows take 1024
@@ -45,6 +47,25 @@ constexpr int kTileCost = 12;
 // What the issuer is to do with a chunk: its parts of Q << 8, K slot << 12, accumulator
 // << 16, parts of a Q slot << 20, Q slot << 24, and
 constexpr uint32_t kGo = 1, kFirst = 2, kLast = 4, kFreeK = 8, kFreeQ = 16;
+
+// A unit as the planner tells it to the other warps of its CTA.
+struct alignas(16) Unit {
+  int32_t row0, rows;  // first of all rows, rows
+  int32_t at;          // first row, from the request's
+  int32_t pos;         // place of the tile's first key
+  int32_t len, base;   // of the request
+  uint32_t what;       // bits below; parts << 16, a slot's parts << 20
+  uint32_t pairs;      // first and (<< 8) last pair that have units of the tile
+  // first cache row of the pages of this CTA's keys; n_pages * page_size: none
+  int32_t page_row[8];
+};
+constexpr uint32_t kDead = 1;    // no row of it sees a key of the tile
+constexpr uint32_t kBegins = 2;  // the first of this pair's units of the tile
+constexpr uint32_t kEnds = 4;    // the last of them
+constexpr uint32_t kWhole = 8;   // (with kEnds) there are no others
+constexpr uint32_t kLoadK = 16, kLoadQ = 32;
+constexpr uint32_t kDropQ = 64;  // its Q is not used again
+constexpr uint32_t kEnd = 128;   // no unit: there are no more
 
 // Counters of the pairs that have ended with a tile that began in pair p: a byte
 // each for the two CTAs, in the workspace header behind the status word.  0 between
@@ -238,11 +259,21 @@ struct QRing {
     at = 0;
   }
   __device__ __forceinline__ uint32_t parity() const { return (phase >> at) & 1u; }
-  __device__ __forceinline__ void used() {
-    phase ^= 1u << at;
-    at = at + 1 == count ? 0 : at + 1;
+  // the slot of the c-th chunk from `from` on, and the parity of that use of it
+  __device__ __forceinline__ uint32_t slot(uint32_t from, uint32_t c) const {
+    uint32_t q = from + c;
+    if (q >= count) q -= count;
+    return q >= count ? q - count : q;  // 5 slots of 8 chunks: round twice
+  }
+  __device__ __forceinline__ uint32_t parity(uint32_t q, uint32_t c) const {
+    return ((phase >> q) & 1u) ^ (c >= count ? 1u : 0u);
+  }
+  __device__ __forceinline__ void used(uint32_t n) {
+    for (uint32_t u = ((1u << n) - 1u) << at; u; u >>= count) phase ^= u & ((1u << count) - 1u);
+    at = slot(at, n);
   }
 };
+static_assert(kQParts / 4 * 2 >= 8 && kQParts + 8 < 32, "chunks that go round the ring");
 
 // Bounded waits for what TMA and the tensor cores do, or for TMEM that has been
 // read: no memory written by the other CTA's threads is read behind them, so that
@@ -254,6 +285,23 @@ struct LocalWaiter {
     return __all_sync(0xffffffffu, done);
   }
 };
+
+// Whether the phase is over; does not wait.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// How many chunks from `done` on are ready, of those below `end`, where bit c of `mask`
+// says that of chunk c.
+__device__ __forceinline__ uint32_t run_of(uint32_t mask, uint32_t done, uint32_t end) {
+  return min((uint32_t)__ffs(~(mask >> done)) - 1u, end - done);
+}
 
 template <int D>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -267,14 +315,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t sK = (raw + 1023u) & ~1023u;
   const uint32_t sQ = sK + kKSlots * kKBytes;
   uint8_t* tail = smem_raw + (sK - raw) + kKSlots * kKBytes + kQParts * kQBytes;
-  float* neg_s = reinterpret_cast<float*>(tail);        // [unit & 1][column] -lse
-  float* red = neg_s + 2 * kBlock;                       // [key] the other columns' sums
-  uint32_t* live_s = reinterpret_cast<uint32_t*>(red + 128);  // [unit & 1][8] columns that count
-  uint64_t* bars = reinterpret_cast<uint64_t*>(live_s + 16);
+  Unit* units = reinterpret_cast<Unit*>(tail);
+  float* neg_s = reinterpret_cast<float*>(units + kUnits);  // [unit % kUnits][column] -lse
+  float* red_s = neg_s + kUnits * kBlock;          // [tile & 1][key] the other columns' sums
+  uint32_t* live_s = reinterpret_cast<uint32_t*>(red_s + 256);  // [unit][8] columns that count
+  uint64_t* bars = reinterpret_cast<uint64_t*>(live_s + 8 * kUnits);
   uint32_t* misc = reinterpret_cast<uint32_t*>(bars + kBars);  // abort, tmem, joins
-  volatile uint32_t* cmd = misc + 4;                           // [chunk & 1], see the scout
-  int64_t* scratch = reinterpret_cast<int64_t*>(misc + 6);    // [16], then the share
-  static_assert((2 * kBlock + 128 + 16) * 4 + kBars * 8 + 24 + 24 * 8 <= kTail, "tail");
+  volatile uint32_t* cmd = misc + 4;                           // [turn & 1][8], see the scout
+  int64_t* scratch = reinterpret_cast<int64_t*>(misc + 20);   // [16], then the share
+  static_assert(kUnits * (sizeof(Unit) + 4 * kBlock + 32) + 1024 + kBars * 8 + 80 + 24 * 8 <= kTail,
+                "tail");
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const uint32_t rank = cluster_rank(), peer = rank ^ 1u;
@@ -287,6 +337,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   auto s_full = [&](uint32_t u) { return bx + 8u * (u & 1u); };
   auto s_empty = [&](uint32_t u) { return bx + 16 + 8u * (u & 1u); };    // leader
   const uint32_t epi = bx + 32, done_bar = bx + 40;
+  auto u_full = [&](uint32_t n) { return bx + 48 + 8u * (n % kUnits); };
+  auto u_empty = [&](uint32_t n) { return bx + 48 + 8u * (kUnits + n % kUnits); };
   const LocalWaiter W{{misc, at_rank(smem_u32(misc), peer), a.status, a.timeout_ns}};
 
   if (tid == 0) {
@@ -301,6 +353,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (uint32_t u = 0; u < 2; ++u) {
       mbar_init(s_full(u), 1);
       mbar_init(s_empty(u), 2 * kEpiWarps);
+    }
+    for (uint32_t u = 0; u < kUnits; ++u) {
+      mbar_init(u_full(u), 1);
+      mbar_init(u_empty(u), kEpiWarps + (rank == 0 ? 3 : 2));  // K, Q; scout
     }
     mbar_init(epi, kEpiWarps);
     mbar_init(done_bar, 1);
@@ -388,54 +444,163 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_wait();
   tc_fence_after();
   constexpr uint32_t tmem = 0;  // an allocation of all 512 columns starts at column 0
-  Walk walk;
-  walk.begin(a, start, end, start < end ? share[0] : 0, start < end ? (int)share[1] : 0);
+  const int page = 1 << a.page_log2, nb_log2 = 7 - a.page_log2;
+  const int nb = 1 << nb_log2;  // page boxes of a chunk
+  const int32_t no_row = (int32_t)(a.n_pages << a.page_log2);  // out of range: zeros
+  // the n-th unit, for those that are told of it
+  auto unit = [&](uint32_t n, Unit& u) {
+    if (!W.wait(u_full(n), (n / kUnits) & 1u)) return false;
+    const uint4* from = reinterpret_cast<const uint4*>(units + n % kUnits);
+    reinterpret_cast<uint4*>(&u)[0] = from[0];
+    reinterpret_cast<uint4*>(&u)[1] = from[1];
+    return !(u.what & kEnd);
+  };
+  auto seen = [&](uint32_t n) {  // by this warp, which does not look at it again
+    __syncwarp();
+    if (lane == 0) mbar_arrive(u_empty(n));
+  };
 
-  if (warp == kKWarp) {
+  if (warp == kPlanWarp) {
+    // ====== planner: walks through the units, a unit ahead of what it tells, so that
+    // its questions to memory (lengths, pages, lse) are answered by then.  (Each warp
+    // walked for itself before: a step to another request is some 700 cycles of one warp,
+    // which small units do not hide.)
+    Walk walk;
+    walk.begin(a, start, end, start < end ? share[0] : 0, start < end ? (int)share[1] : 0);
+    float l[kBlock / 32] = {};
+    int32_t page_id = -1, row = no_row;
+    uint32_t nu = 0;
+    bool ok = true, have = false, k_here = false, head = false;
+    for (bool started = false;; started = true) {
+      const Walk x = walk;
+      const bool told = have;
+      float neg[kBlock / 32];
+#pragma unroll
+      for (int i = 0; i < kBlock / 32; ++i) neg[i] = -l[i];
+      const int32_t id = page_id;
+      if (told) walk.first = false;
+      if (!started || told) {
+        have = walk.next(a);
+        if (have) {
+          const int32_t n = walk.dead(a) ? 0 : walk.rows();
+          const float* from = a.lse + walk.r.row0 + walk.block * kBlock;
+#pragma unroll
+          for (int i = 0; i < kBlock / 32; ++i) {
+            l[i] = -INFINITY;
+            if (32 * i + lane < n)
+              l[i] = __int_as_float(ld_input(reinterpret_cast<const int32_t*>(from + 32 * i + lane)));
+          }
+          if (walk.block == 0 || walk.first) {
+            const int32_t pos = walk.tile * kTile + (int)rank * 128 + lane * page;
+            page_id = 0;
+            if (lane < nb && pos < walk.r.len)
+              page_id = ld_input(a.table + (int64_t)walk.b * a.max_blocks + (pos >> a.page_log2));
+          }
+        }
+      }
+      if (!told) {
+        if (started || !have) break;
+        continue;
+      }
+      uint32_t what = (x.dead(a) ? kDead : 0u) | (x.tile_ends() ? kEnds : 0u);
+      if (x.block == 0 || x.first) {
+        what |= kBegins;
+        k_here = false;
+        head = x.block != 0;  // the tile began in a pair before
+        row = no_row;
+        if (lane < nb && x.tile * kTile + (int)rank * 128 + lane * page < x.r.len) {
+          if (id < 0 || id >= a.n_pages) latch_error(a.status, DSA_ERR_DEVICE_BAD_INDEX);
+          else row = id << a.page_log2;
+        }
+      }
+      if (what == kDead) continue;
+      const bool stays = x.q_stays<D>();
+      if (!(what & kDead)) {
+        if (!k_here) what |= kLoadK;
+        k_here = true;
+        if (!stays || x.first) what |= kLoadQ;
+        if (!stays || x.left == 0) what |= kDropQ;
+      }
+      uint32_t between = 0;
+      if (what & kEnds) {
+        if (!head && x.block == x.r.blocks - 1) {
+          what |= kWhole;
+        } else {
+          const int64_t c0 = x.cb + (int64_t)x.tile * x.r.blocks * x.r.cost;
+          between = (uint32_t)(c0 / chunk) |
+                    (uint32_t)((c0 + (int64_t)(x.r.blocks - 1) * x.r.cost) / chunk) << 8;
+        }
+      }
+      if (!(ok = W.wait(u_empty(nu), ((nu / kUnits) & 1u) ^ 1u))) break;
+      Unit* u = units + nu % kUnits;
+      if (lane == 0) {
+        u->row0 = x.r.row0 + x.block * kBlock;
+        u->rows = x.rows();
+        u->at = x.block * kBlock;
+        u->pos = x.tile * kTile;
+        u->len = x.r.len;
+        u->base = x.r.base;
+        u->what = what | (uint32_t)x.parts() << 16 | (uint32_t)x.slot_parts() << 20;
+        u->pairs = between;
+      }
+      if (lane < nb) u->page_row[lane] = row;
+#pragma unroll
+      for (int i = 0; i < kBlock / 32; ++i) {
+        neg_s[nu % kUnits * kBlock + 32 * i + lane] = neg[i];
+        const uint32_t live = __ballot_sync(0xffffffffu, neg[i] != INFINITY);
+        if (lane == 0) live_s[nu % kUnits * 8 + i] = live;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(u_full(nu));
+      ++nu;
+    }
+    if (ok && W.wait(u_empty(nu), ((nu / kUnits) & 1u) ^ 1u)) {
+      if (lane == 0) {
+        units[nu % kUnits].what = kEnd;
+        mbar_arrive(u_full(nu));
+      }
+      __syncwarp();
+    }
+  } else if (warp == kKWarp) {
     // ============================================================ K by TMA
-    const int page = 1 << a.page_log2, nb = 128 >> a.page_log2;  // page boxes of a chunk
-    const int32_t n_rows_cache = (int32_t)(a.n_pages << a.page_log2);  // out of range: zeros
-    const bool arms = rank == 0 && lane == 0;
     const uint32_t lead = at_rank(bar0, 0);
     uint32_t kc = 0;  // chunks so far
-    bool ok = true, here = false;
-    const int32_t key0 = (int)rank * 128 + lane * page;  // of this lane's box, in a tile
-    // page of that box in a tile of the walk's request (looked at when it is loaded)
-    auto page_at = [&](int32_t tile) {
-      const int32_t pos = tile * kTile + key0;
-      return lane < nb && pos < walk.r.len
-                 ? ld_input(a.table + (int64_t)walk.b * a.max_blocks + (pos >> a.page_log2))
-                 : -1;
-    };
-    int32_t next_page = -1;
-    while (ok && walk.next(a)) {
-      if (walk.block == 0 || walk.first) here = false;
-      if (walk.first) next_page = page_at(walk.tile);
-      walk.first = false;
-      if (here || walk.dead(a)) continue;
-      here = true;
-      int32_t row = n_rows_cache;
-      const bool has = lane < nb && walk.tile * kTile + key0 < walk.r.len;
-      if (has) {
-        if (next_page < 0 || next_page >= a.n_pages)
-          latch_error(a.status, DSA_ERR_DEVICE_BAD_INDEX);
-        else
-          row = next_page << a.page_log2;
-      }
-      next_page = page_at(walk.tile + 1);
+    bool ok = true;
+    Unit u;
+    for (uint32_t nu = 0; ok && unit(nu, u); ++nu) {
+      const int32_t row = units[nu % kUnits].page_row[lane & (nb - 1)];
+      seen(nu);
+      if (!(u.what & kLoadK)) continue;
       // boxes behind the last token are left out: what lies there gives sums of keys
       // that are not, and stays with them
-      const int32_t keys = min(kTile, walk.r.len - walk.tile * kTile);
+      const int32_t keys = min(kTile, u.len - u.pos);
       const uint32_t bytes = (uint32_t)((keys + page - 1) & -page) * 128u;
-#pragma unroll 1
-      for (int c = 0; c < kChunks; ++c, ++kc) {
-        const uint32_t s = kc % kKSlots;
-        if (!(ok = W.wait(k_empty(s), ((kc / kKSlots) & 1u) ^ 1u))) break;
-        if (arms) mbar_expect_tx(k_full(s), bytes);
-        if (has)
-          tma_load_pair(sK + s * kKBytes + (uint32_t)(lane * page) * 128u, &k_map, c * 64, row,
-                        lead + 8u * s);
+      const int32_t boxes = (keys - (int)rank * 128 + page - 1) >> a.page_log2;  // of this CTA
+      // all chunks whose slots are free at once: lane c looks at chunk c's, and the lanes
+      // take the boxes of them
+      const uint32_t mine = kc + (uint32_t)lane;
+      uint32_t done = 0;
+      while (done < kChunks) {
+        const bool is = lane < kChunks && mbar_test(k_empty(mine % kKSlots),
+                                                    ((mine / kKSlots) & 1u) ^ 1u);
+        uint32_t n = run_of(__ballot_sync(0xffffffffu, is), done, kChunks);
+        if (n == 0) {
+          const uint32_t x = kc + done;
+          if (!(ok = W.wait(k_empty(x % kKSlots), ((x / kKSlots) & 1u) ^ 1u))) break;
+          n = 1;
+        }
+        if (rank == 0 && (uint32_t)lane - done < n) mbar_expect_tx(k_full(mine % kKSlots), bytes);
+        for (uint32_t i = 0; i < n << nb_log2; i += 32) {
+          const uint32_t c = done + ((i + lane) >> nb_log2), box = lane & (nb - 1);
+          if (c < done + n && (int32_t)box < boxes) {
+            const uint32_t s = (kc + c) % kKSlots;
+            tma_load_pair(sK + s * kKBytes + box * (uint32_t)page * 128u, &k_map, (int)c * 64, row,
+                          lead + 8u * s);
+          }
+        }
+        done += n;
       }
+      kc += kChunks;
     }
     // the leader's last arrival here is done_bar's: the CTA outlives it
     if (ok && rank != 0 && kc > 0) W.wait(done_bar, 0);
@@ -444,11 +609,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t lead = at_rank(bar0, 0);
     QRing ring;
     bool ok = true;
-    while (ok && walk.next(a)) {
-      const bool load = !walk.q_stays<D>() || walk.first;
-      walk.first = false;
-      if (!load || walk.dead(a)) continue;
-      const uint32_t n = (uint32_t)walk.parts(), slot = (uint32_t)walk.slot_parts();
+    Unit u;
+    for (uint32_t nu = 0; ok && unit(nu, u); ++nu) {
+      seen(nu);
+      if (!(u.what & kLoadQ)) continue;
+      const uint32_t n = (u.what >> 16) & 15u, slot = u.what >> 20;
       if (ring.other(slot)) {
         for (ring.at = 0; ring.at < ring.count && ok; ++ring.at)
           ok = W.wait(q_empty(ring.at), ring.parity() ^ 1u);
@@ -456,60 +621,86 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ring.begin(slot);
       }
       const CUtensorMap* map = n == 4 ? &q4_map : n == 2 ? &q2_map : &q_map;
-      const int32_t row = walk.r.row0 + walk.block * kBlock + (int)(rank * n) * 32;
-#pragma unroll 1
-      for (int c = 0; c < kChunks; ++c) {
-        if (!(ok = W.wait(q_empty(ring.at), ring.parity() ^ 1u))) break;
-        if (lane == 0) {
-          if (rank == 0) mbar_expect_tx(q_full(ring.at), 2 * kQBytes * n);
-          tma_load_pair(sQ + ring.at * slot * kQBytes, map, c * 64, row,
-                        lead + 8u * (2 * kKSlots + ring.at));
+      const int32_t row = u.row0 + (int)(rank * n) * 32;
+      // as K: lane c has chunk c, whose slot's use before has to be this unit's or older
+      const uint32_t q = ring.slot(ring.at, lane & 7), par = ring.parity(q, lane & 7);
+      uint32_t done = 0;
+      while (done < kChunks) {
+        const uint32_t upto = min((uint32_t)kChunks, done + ring.count);
+        const bool is = (uint32_t)lane >= done && (uint32_t)lane < upto &&
+                        mbar_test(q_empty(q), par ^ 1u);
+        uint32_t m = run_of(__ballot_sync(0xffffffffu, is), done, upto);
+        if (m == 0) {
+          const uint32_t x = __shfl_sync(0xffffffffu, q, done);
+          if (!(ok = W.wait(q_empty(x), __shfl_sync(0xffffffffu, par, done) ^ 1u))) break;
+          m = 1;
         }
-        ring.used();
+        if ((uint32_t)lane - done < m) {
+          if (rank == 0) mbar_expect_tx(q_full(q), 2 * kQBytes * n);
+          tma_load_pair(sQ + q * slot * kQBytes, map, lane * 64, row,
+                        lead + 8u * (2 * kKSlots + q));
+        }
+        done += m;
       }
+      ring.used(kChunks);
     }
   } else if (warp == kScoutWarp && rank == 0) {
-    // ====== scout: waits for the issuer's operands and lets it in, a chunk at a
-    // time (a wait of the issuer's own would queue behind its MMAs), with a word that
-    // says what to issue.  When a wait gives up it lets the issuer through what is
-    // left, on whatever is there.
-    uint32_t kc = 0, q0 = 0, nu = 0, n_bar = 0;
+    // ====== scout: looks for the issuer's operands (a wait of the issuer's own would
+    // queue behind its MMAs) and lets it in to all chunks that are there, with a word
+    // for each that says what to issue.  (A chunk at a time, each with two waits and a
+    // barrier, took 520 cycles a chunk, where the MMAs take up to 512.)
+    uint32_t kc = 0, q0 = 0, ns = 0, n_bar = 0;
     QRing ring;
-    bool ok = true, k_here = false;
-    auto let_in = [&](uint32_t word) {
-      if (lane == 0) cmd[n_bar & 1u] = word;
+    bool ok = true;
+    auto let_in = [&](uint32_t word) {  // lane i's, i < 8; 0 ends them
+      if (lane < 8) cmd[(n_bar & 1u) * 8 + lane] = word;
       __syncwarp();
       asm volatile("bar.sync %0, 64;" ::"r"(1 + (n_bar & 1u)) : "memory");
       ++n_bar;
     };
-    while (walk.next(a)) {
-      if (walk.block == 0 || walk.first) k_here = false;
-      const bool stays = walk.q_stays<D>(), load_q = !stays || walk.first;
-      walk.first = false;
-      if (walk.dead(a)) continue;
-      const uint32_t slot = (uint32_t)walk.slot_parts();
+    Unit u;
+    for (uint32_t nu = 0; ok && unit(nu, u); ++nu) {
+      seen(nu);
+      if (u.what & kDead) continue;
+      const bool load_q = u.what & kLoadQ, load_k = u.what & kLoadK;
+      const uint32_t slot = u.what >> 20;
       if (load_q && ring.other(slot)) ring.begin(slot);
       if (load_q) q0 = ring.at;
-      if (!k_here) kc += kChunks;
-      const uint32_t flags = kGo | (walk.tile_ends() ? kFreeK : 0u) |
-                             (!stays || walk.left == 0 ? kFreeQ : 0u) |
-                             (uint32_t)walk.parts() << 8 | slot << 20 | (nu & 1u) << 16;
-      if (ok) ok = W.wait(s_empty(nu), ((nu >> 1) & 1u) ^ 1u);
-      uint32_t q = q0;
-#pragma unroll 1
-      for (uint32_t c = 0; c < kChunks; ++c) {
-        const uint32_t x = kc - kChunks + c;
-        if (!k_here && ok) ok = W.wait(k_full(x % kKSlots), (x / kKSlots) & 1u);
-        if (load_q) {
-          if (ok) ok = W.wait(q_full(q), ring.parity());
-          ring.used();
+      if (load_k) kc += kChunks;
+      const uint32_t flags = kGo | (u.what & kEnds ? kFreeK : 0u) |
+                             (u.what & kDropQ ? kFreeQ : 0u) | ((u.what >> 16) & 15u) << 8 |
+                             slot << 20 | (ns & 1u) << 16;
+      if (!(ok = W.wait(s_empty(ns), ((ns >> 1) & 1u) ^ 1u))) break;
+      ++ns;
+      // lane c looks for chunk c's K, lane 8 + c for its Q
+      const uint32_t c = lane & 7u, x = kc - kChunks + c, q = ring.slot(q0, c);
+      const uint32_t bar = lane < 8 ? k_full(x % kKSlots) : q_full(q);
+      const uint32_t par = lane < 8 ? (x / kKSlots) & 1u : ring.parity(q, c);
+      const bool need = c < kChunks && (lane < 8 ? load_k : lane < 16 && load_q);
+      const uint32_t word = flags | (c == 0 ? kFirst : 0u) | (c == kChunks - 1 ? kLast : 0u) |
+                            (x % kKSlots) << 12 | q << 24;
+      uint32_t done = 0;
+      while (done < kChunks) {
+        // (a slot's next use is not looked for before this one is here)
+        const uint32_t upto = load_q ? min((uint32_t)kChunks, done + ring.count) : kChunks;
+        const bool is = !need || (c >= done && c < upto && mbar_test(bar, par));
+        const uint32_t m = __ballot_sync(0xffffffffu, is);
+        uint32_t n = run_of(m & (m >> 8), done, upto);
+        if (n == 0) {
+          const uint32_t k_bar = __shfl_sync(0xffffffffu, bar, done);
+          const uint32_t k_par = __shfl_sync(0xffffffffu, par, done);
+          const uint32_t q_bar = __shfl_sync(0xffffffffu, bar, 8 + done);
+          const uint32_t q_par = __shfl_sync(0xffffffffu, par, 8 + done);
+          if (load_k) ok = W.wait(k_bar, k_par);
+          if (load_q && ok) ok = W.wait(q_bar, q_par);
+          if (!ok) break;
+          n = 1;
         }
-        let_in(flags | (c == 0 ? kFirst : 0u) | (c == kChunks - 1 ? kLast : 0u) |
-               (x % kKSlots) << 12 | q << 24);
-        q = q + 1 == ring.count ? 0 : q + 1;
+        const uint32_t w = __shfl_sync(0xffffffffu, word, done + c);
+        let_in(c < n ? w : 0u);
+        done += n;
       }
-      k_here = true;
-      ++nu;
+      if (load_q) ring.used(kChunks);
     }
     let_in(0u);
   } else if (warp == kMmaWarp && rank == 0) {
@@ -520,23 +711,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool any = false;
     for (uint32_t n_bar = 0;; ++n_bar) {
       asm volatile("bar.sync %0, 64;" ::"r"(1 + (n_bar & 1u)) : "memory");
-      const uint32_t word = cmd[n_bar & 1u];
+      const uint32_t mine = cmd[(n_bar & 1u) * 8 + (lane & 7)];
+      uint32_t word = __shfl_sync(0xffffffffu, mine, 0);
       if (word == 0u) break;
       any = true;
       tc_fence_after();
-      if (elect_one()) {
-        const uint32_t n = (word >> 8) & 15u, s = (word >> 12) & 15u, u = (word >> 16) & 1u;
-        const uint32_t q = word >> 24, slot = (word >> 20) & 15u, d = tmem + u * kBlock;
-        const uint32_t idesc = idesc_bf16(256, 0, 0, 0) | (64 * n) >> 3 << 17;
-        const uint32_t da = dK + s * (kKBytes >> 4), db = dQ + q * slot * (kQBytes >> 4);
-        tc_mma2(d, da, db, hi, idesc, word & kFirst ? 0u : 1u);
+#pragma unroll 1
+      for (int i = 1; word; ++i) {
+        if (elect_one()) {
+          const uint32_t n = (word >> 8) & 15u, s = (word >> 12) & 15u, u = (word >> 16) & 1u;
+          const uint32_t q = word >> 24, slot = (word >> 20) & 15u, d = tmem + u * kBlock;
+          const uint32_t idesc = idesc_bf16(256, 0, 0, 0) | (64 * n) >> 3 << 17;
+          const uint32_t da = dK + s * (kKBytes >> 4), db = dQ + q * slot * (kQBytes >> 4);
+          tc_mma2(d, da, db, hi, idesc, word & kFirst ? 0u : 1u);
 #pragma unroll
-        for (uint32_t x = 1; x < 4; ++x) tc_mma2(d, da + 2 * x, db + 2 * x, hi, idesc, 1u);
-        if (word & kFreeK) tc_commit2(k_empty(s));
-        if (word & kFreeQ) tc_commit2(q_empty(q));
-        if (word & kLast) tc_commit2(s_full(u));
+          for (uint32_t x = 1; x < 4; ++x) tc_mma2(d, da + 2 * x, db + 2 * x, hi, idesc, 1u);
+          if (word & kFreeK) tc_commit2(k_empty(s));
+          if (word & kFreeQ) tc_commit2(q_empty(q));
+          if (word & kLast) tc_commit2(s_full(u));
+        }
+        __syncwarp();
+        if (i == 8) break;
+        word = __shfl_sync(0xffffffffu, mine, i);
       }
-      __syncwarp();
     }
     if (any) {
       if (elect_one()) tc_commit2(done_bar);
@@ -548,57 +745,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int quad = warp & 3, g = warp >> 2;  // TMEM lanes, every second set of 32 columns
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
     const uint64_t scale2 = pair2(a.scale, a.scale), log2e2 = pair2(kLog2e, kLog2e);
-    uint32_t nu = 0, ns = 0;
+    uint32_t ns = 0, n_sync = 0, n_tiles = 0;
     auto epi_sync = [&]() {  // all epilogue warps of this CTA
       __syncwarp();
       if (lane == 0) mbar_arrive(epi);
-      return W.wait(epi, ns++ & 1u);
+      return W.wait(epi, n_sync++ & 1u);
     };
-    bool ok = true, head = false;
+    bool ok = true;
     uint64_t sum[2] = {0ull, 0ull};
     int64_t slot = -1;  // of this thread's key, or -1
-    float old = 0.f;    // what it has received before
-    while (ok && walk.next(a)) {
-      const int32_t pos0 = walk.tile * kTile + (int)rank * 128 + quad * 32, pos = pos0 + lane;
-      const bool dead = walk.dead(a);
-      float l = -INFINITY;  // asked for ahead of the table's word, which w_pages' waits for
-      if (!dead && tid < walk.rows())
-        l = __int_as_float(ld_input(reinterpret_cast<const int32_t*>(
-            a.lse + walk.r.row0 + walk.block * kBlock + tid)));
-      if (walk.block == 0 || walk.first) {
-        head = walk.block != 0;  // the tile began in a pair before
+    float old = 0.f;    // what it has received before (used last: the load is long)
+    Unit u;
+    for (uint32_t nu = 0; ok && unit(nu, u); ++nu) {
+      const int32_t pos0 = u.pos + (int)rank * 128 + quad * 32, pos = pos0 + lane;
+      if (u.what & kBegins) {
         sum[0] = sum[1] = 0ull;
         slot = -1;
         old = 0.f;
-        if (g == 0 && pos < walk.r.len) {
-          const int32_t p =
-              ld_input(a.table + (int64_t)walk.b * a.max_blocks + (pos >> a.page_log2));
-          if (p >= 0 && p < a.n_pages)  // else latched where K is loaded
-            slot = ((int64_t)p << a.page_log2) + (pos & ((1 << a.page_log2) - 1));
-          if (slot >= 0 && pos < walk.r.base)
-            old = a.decay * __int_as_float(ld_input(reinterpret_cast<const int32_t*>(a.w + slot)));
+        if (g == 0 && pos < u.len) {
+          const int32_t row = units[nu % kUnits].page_row[(quad * 32 + lane) >> a.page_log2];
+          if (row != no_row) slot = (int64_t)row + (pos & (page - 1));
+          if (slot >= 0 && pos < u.base)
+            old = __int_as_float(ld_input(reinterpret_cast<const int32_t*>(a.w + slot)));
         }
       }
-      walk.first = false;
-      if (!dead) {
-        const int32_t n = walk.rows(), at = walk.block * kBlock;
-        float* neg = neg_s + (nu & 1u) * kBlock;
-        neg[tid] = -l;
-        const uint32_t live = __ballot_sync(0xffffffffu, l != -INFINITY);
-        if (lane == 0) live_s[(nu & 1u) * 8 + warp] = live;
-        if (!(ok = epi_sync())) break;
-        if (!(ok = W.wait(s_full(nu), (nu >> 1) & 1u))) break;
+      if (!(u.what & kDead)) {
+        const int32_t n = u.rows, at = u.at;
+        const float* neg = neg_s + nu % kUnits * kBlock;
+        if (!(ok = W.wait(s_full(ns), (ns >> 1) & 1u))) break;
         tc_fence_after();
-        const int32_t first = pos - walk.r.base;  // node, or first token that sees the key
-        const bool all_see = pos0 + 31 < walk.r.base || (!a.bits && pos0 + 31 <= walk.r.base);
-        const uint32_t tS = tmem + (nu & 1u) * kBlock + lane_base;
+        const int32_t first = pos - u.base;  // node, or first token that sees the key
+        const bool all_see = pos0 + 31 < u.base || (!a.bits && pos0 + 31 <= u.base);
+        const uint32_t tS = tmem + (ns & 1u) * kBlock + lane_base;
         const int sets = (n + 31) >> 5;
 #pragma unroll 1
         for (int q = g; q < sets; q += 2) {
           uint32_t s[2][16];
           tmem_ld16(tS + 32 * q, s[0]);
           tmem_ld16(tS + 32 * q + 16, s[1]);
-          uint32_t mask = live_s[(nu & 1u) * 8 + q];
+          uint32_t mask = live_s[nu % kUnits * 8 + q];
           if (!all_see) {
             const int32_t r0 = at + 32 * q;  // the set's first row, from the request's
             if (!a.bits) {
@@ -608,12 +793,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             } else {
               // lane l reads row r0 + l's bits of the warp's 32 keys; then the 32 x 32
               // bits are turned around
-              const int32_t j0 = pos0 - walk.r.base, w0 = j0 >> 5;
+              const int32_t j0 = pos0 - u.base, w0 = j0 >> 5;
               uint32_t lo = 0u, hi = 0u;
               if (32 * q + lane < n &&
-                  DSA_IN_BOUNDS((walk.r.row0 + r0 + lane) / a.H < a.T, a.status)) {
+                  DSA_IN_BOUNDS((u.row0 - at + r0 + lane) / a.H < a.T, a.status)) {
                 const int32_t* bits =
-                    a.bits + (int64_t)((walk.r.row0 + r0 + lane) / a.H) * a.words;
+                    a.bits + (int64_t)((u.row0 - at + r0 + lane) / a.H) * a.words;
                 if (w0 >= 0 && w0 < a.words) lo = (uint32_t)ld_input(bits + w0);
                 if (w0 + 1 >= 0 && w0 + 1 < a.words) hi = (uint32_t)ld_input(bits + w0 + 1);
               }
@@ -658,24 +843,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_signal(at_rank(s_empty(nu), 0));
-        ++nu;
+        if (lane == 0) mbar_signal(at_rank(s_empty(ns), 0));
+        ++ns;
       }
-      if (!walk.tile_ends()) continue;
+      seen(nu);
+      if (!(u.what & kEnds)) continue;
       // ---- this CTA's part of the tile is done
       float lo, hi, v;
       unpair2(add2(sum[0], sum[1]), lo, hi);
       v = lo + hi;
+      float* red = red_s + (n_tiles++ & 1u) * 128;
       if (g == 1) red[quad * 32 + lane] = v;
       if (!(ok = epi_sync())) break;
       if (g == 0) v += red[quad * 32 + lane];
-      const bool whole = !head && walk.block == walk.r.blocks - 1;
       bool mine = g == 0;
-      if (!whole) {
+      if (!(u.what & kWhole)) {
         // the pairs that have a unit of the tile, and this one's sums for the others
-        const int64_t c0 = walk.cb + (int64_t)walk.tile * walk.r.blocks * walk.r.cost;
-        const int from = (int)(c0 / chunk);
-        const int to = (int)((c0 + (int64_t)(walk.r.blocks - 1) * walk.r.cost) / chunk);
+        const int from = (int)(u.pairs & 255u), to = (int)(u.pairs >> 8);
         auto part = [&](int p) {
           return a.parts + (((int64_t)p * 2 + rank) * 2 + (p == from ? 1 : 0)) * 128 + quad * 32 +
                  lane;
@@ -699,8 +883,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       if (mine && slot >= 0 && DSA_IN_BOUNDS(slot < a.n_pages << a.page_log2, a.status))
-        a.w_out[slot] = old + v;
-      if (!(ok = epi_sync())) break;  // red and misc may be written again
+        a.w_out[slot] = a.decay * old + v;
       sum[0] = sum[1] = 0ull;
     }
   }
