@@ -7,6 +7,12 @@
 // and places that are written (below it) are disjoint, so the rows move in place,
 // in any order, and only about left (1 - left / n) of them move, where keeping the
 // order would move nearly all.
+//
+// Bounds.  64 requests of up to 4096 tokens of 512: 30 us with the pages' release (4),
+// of which the copy 12 (73 MB) and the selection 15; 131071 tokens to 32768, K and V: 51
+// us, of which the copy 17 (102 MB, 6 TB/s) and the selection 31.  The selection reads
+// next to nothing: it is a chain of lookups, four histograms, their exchanges through the
+// cluster (about 5000 cycles each with 16 CTAs), scans and a reservation.
 #include <atomic>
 
 #include "dsa_internal.h"
@@ -17,13 +23,12 @@ namespace {
 
 constexpr int kMaxThreads = 1024;  // of a CTA of the selection
 constexpr int kMaxCluster = 16;    // where the device has room for it, else 8
-constexpr int kMaxKeys = 40960;    // keys of a CTA's share that fit shared memory (160 KB)
 constexpr int kCopies = 8;         // of a histogram, for lanes that meet in a bin
-// two words for each 32 of the 2^22 / 8 places that a share may have
-constexpr int kMaxWordBytes = (1 << 22) / 8 / 4;
-// of a CTA: its keys or as many places as it may have, and the cluster's counts
-constexpr int kMaxSmem = kMaxKeys * 4 + kMaxKeys / 4 + 1024 * kMaxCluster;
-static_assert(kMaxSmem >= kMaxWordBytes + 1024 * 8, "shared memory");
+constexpr int kMaxShare = 1 << 19;  // places of a CTA, at most: its masks take a bit each, twice
+// shared memory of a CTA that has an SM to itself, and of one of two, beside the
+// histograms (17 KB)
+constexpr int kMaxSmem = 192 * 1024, kTwoSmem = 92 * 1024;
+static_assert(kMaxSmem >= kMaxShare / 4 + 1024 * kMaxCluster, "masks and the cluster's counts");
 
 // In the workspace header, behind the status word; both are 0 between calls.
 struct Counters {
@@ -84,28 +89,24 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t x, uint64_t* sums, uint6
   return (warp ? before : 0ull) + incl - x;
 }
 
-// A cluster has a request, each CTA of it consecutive places.  Cached: their keys
-// lie in shared memory, else they are read again in each pass.
+// A cluster has a request, each CTA of it consecutive places.  Where their masks and keys
+// fit `room` words the keys lie in shared memory, else they are read again in each pass.
 //
 // Passes of eight bits, four at most, find the left-th largest key: each CTA counts
 // its keys, the cluster's leader adds up the counts, and a warp of it finds the
 // digit.  Then a bit for each place says whether its token stays, and scans of
 // population counts over groups of eight places number the equal keys, the freed
 // places and the movers.
-template <bool Cached>
 __global__ void __launch_bounds__(kMaxThreads) select_kernel(
     const float* w, const float* ranks, const int32_t* table, const int32_t* seq,
     const int32_t* keep, int32_t n_first, int32_t n_last, float* w_out, Moves moves,
     int64_t list_len, Counters counts, int max_blocks, int page_log2, int64_t n_pages,
-    int max_words, uint32_t* status) {
+    int32_t room, uint32_t* status) {
   extern __shared__ __align__(16) uint32_t smem[];
   uint32_t rank, size;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(size));
   uint32_t* cluster_sums = smem;  // [CTA][256] where there are several: the leader's, by 16 bytes
-  uint32_t* above_w = smem + (size > 1 ? 256 * size : 0u);  // [word of 32 places] keys above
-  uint32_t* equal_w = above_w + max_words;                  // the threshold; equal to it
-  uint32_t* keys = equal_w + max_words;
   __shared__ alignas(16) uint32_t hist[2][kCopies][256];  // in turns
   __shared__ uint64_t sums[32];
   __shared__ alignas(16) uint32_t sum_hist[256];          // the leader's: of the cluster
@@ -131,6 +132,10 @@ __global__ void __launch_bounds__(kMaxThreads) select_kernel(
   const int32_t* row = table + (int64_t)b * max_blocks;
   const int32_t share = ((n + (int)size - 1) / (int)size + 31) & ~31;
   const int32_t lo = min(n, (int)rank * share), hi = min(n, lo + share);
+  uint32_t* above_w = smem + (size > 1 ? 256 * size : 0u);  // [word of 32 places] keys above
+  uint32_t* equal_w = above_w + (share >> 5);               // the threshold; equal to it
+  uint32_t* keys = equal_w + (share >> 5);
+  const bool cached = share + (share >> 5) * 2 <= room;
   // the slot of place j on page p, or -1
   auto slot_on = [&](int32_t p, int32_t j) -> int32_t {
     if (p < 0 || p >= n_pages) {
@@ -175,12 +180,12 @@ __global__ void __launch_bounds__(kMaxThreads) select_kernel(
   auto to_key = [&](int32_t j, int32_t s, float x) {
     return fixed(j) ? 0xff800000u /* +inf */ : s < 0 ? 0u : order_key(x);
   };
-  if (Cached)
+  if (cached)
     values_of(ranks, lo + tid, hi, any,
               [&](int32_t j, int32_t s, float x) { keys[j - lo] = to_key(j, s, x); });
   // f(j, key) of the places j0, j0 + nt, .. below hi
   auto each_key = [&](int32_t j0, auto f) {
-    if (Cached) {
+    if (cached) {
 #pragma unroll 4
       for (int32_t j = j0; j < hi; j += nt) f(j, keys[j - lo]);
     } else {
@@ -302,7 +307,7 @@ __global__ void __launch_bounds__(kMaxThreads) select_kernel(
     for (int32_t j = first; j - lane < hi; j += nt) {
       uint32_t k = 0u;
       if (j < hi) {
-        if (Cached) k = keys[j - lo];
+        if (cached) k = keys[j - lo];
         else if (fixed(j)) k = 0xff800000u;
         else {
           const int32_t s = slot_on(ld_input(row + (j >> page_log2)), j);
@@ -488,7 +493,7 @@ bool fits_wide(int smem) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, select_kernel<true>, &cfg) == cudaSuccess) return n > 0;
+  if (cudaOccupancyMaxActiveClusters(&n, select_kernel, &cfg) == cudaSuccess) return n > 0;
   cudaGetLastError();
   return false;
 }
@@ -506,33 +511,35 @@ cudaError_t launch_evict(const LaunchCtx& c, const ServeShape& s, const float* w
   static std::atomic<uint64_t> prepared{0}, wide{0};
   const uint64_t bit = 1ull << (c.device & 63);
   if (!(prepared.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kMaxSmem);
+    e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(select_kernel<false>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(select_kernel<true>, cudaFuncAttributeNonPortableClusterSizeAllowed,
-                               1);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(select_kernel<false>,
-                               cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     if (fits_wide(kMaxSmem)) wide.fetch_or(bit, std::memory_order_relaxed);
     prepared.fetch_or(bit, std::memory_order_release);
   }
-  // a CTA for each 4096 tokens that a request may have, at most kMaxCluster, and a
-  // thread for each four of its share
+  // A CTA for each 4096 tokens that a request may have, at most kMaxCluster, while an SM
+  // has one (which a CTA of 1024 threads takes to itself): a cache is seldom as long as it
+  // may get, and clusters that queue for SMs cost all.  us of the call with CTAs up to
+  // one, two an SM and without that limit: 64 requests of up to 4096 tokens that may have
+  // 131072 21 32 117; 16 of up to 65536 85 112 111; 64 of 100000 to 131072 730 686 -.  One
+  // request of 131071 with 4, 8, 16 CTAs 75 54 47; 64 that may have 4096 with 1, 2, 4, 8
+  // CTAs 23.1 25.7 25.8 28.5.  A thread for each four places of a share (for 64 of 4096
+  // 23.1, with eight 24.0, with sixteen 27.7).
   const int64_t cap = (int64_t)s.max_blocks * s.page;
   const int most = wide.load(std::memory_order_relaxed) & bit ? kMaxCluster : 8;
   int size = 1;
-  while (size < most && cap > (int64_t)size * 4096) size *= 2;
+  while (size < most && ((cap > (int64_t)size * 4096 && s.B * size * 2 <= c.num_sms) ||
+                         cap > (int64_t)size * kMaxShare))
+    size *= 2;
   const int64_t share = ((cap + size - 1) / size + 31) & ~(int64_t)31;
-  const int64_t words = share / 32;
   int threads = 256;
   while (threads < kMaxThreads && share > (int64_t)threads * 4) threads *= 2;
-  const bool cached = share <= kMaxKeys;
-  const size_t smem = (size_t)(2 * words + (size > 1 ? 256 * size : 0) + (cached ? share : 0)) * 4;
+  // masks of the longest cache, and its keys or as many as there is room for
+  const int64_t sums = size > 1 ? 1024 * size : 0, masks = share / 4;
+  const int64_t limit = s.B * size <= c.num_sms ? kMaxSmem : kTwoSmem;
+  const int64_t full = sums + masks + share * 4;
+  const int64_t smem = full <= limit ? full : sums + masks > limit ? sums + masks : limit;
   const Moves moves = moves_of(s, ws);
   const Counters counts = counters(ws);
   const int64_t list_len = max_moves(s);
@@ -545,13 +552,13 @@ cudaError_t launch_evict(const LaunchCtx& c, const ServeShape& s, const float* w
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(s.B * size));
   cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = c.stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, cached ? select_kernel<true> : select_kernel<false>, w_pages,
-                         rank_pages, table, seq, keep, n_first, n_last, w_out, moves, list_len,
-                         counts, s.max_blocks, s.page_log2, s.n_pages, (int)words, c.status);
+  e = cudaLaunchKernelEx(&cfg, select_kernel, w_pages, rank_pages, table, seq, keep, n_first,
+                         n_last, w_out, moves, list_len, counts, s.max_blocks, s.page_log2,
+                         s.n_pages, (int32_t)((smem - sums) / 4), c.status);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)(c.num_sms * kMoveBlocks));
   cfg.blockDim = dim3(256);

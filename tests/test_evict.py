@@ -215,6 +215,17 @@ def test_evict_past_shared_memory():
 
 
 @gpu
+@pytest.mark.parametrize("weights", ["random", "few"])
+def test_evict_more_than_the_gpu_has_room_for(weights):
+    """Many requests, some of whose shares pass shared memory while others' do not: a CTA
+    each, and clusters as the longest cache that is allowed wants them."""
+    check_evict(Evict([60000, 100, 0, 40000] + [50] * 77, [30000, 60, 5, 39000] + [20] * 77, 16,
+                      128, 1, weights, seed=11), n_first=1, n_last=40)
+    check_evict(Evict([300000, 100000, 7] + [40] * 97, [1000, 50000, 3] + [30] * 97, 128, 128, 1,
+                      weights, seed=12, extra=(1 << 15) - 2344), n_last=9, in_place=True)
+
+
+@gpu
 @pytest.mark.parametrize("in_place", [False, True])
 def test_ranks_of_their_own(in_place):
     """Rejected drafts: -inf among +inf; and any ranks, the weights only carried."""
