@@ -15,6 +15,22 @@
 // the sum evenly.  A tile whose blocks fall to several pairs is joined by the last
 // of them to end, which adds their sums in the order of the pairs, so that results
 // repeat.
+//
+// Warps.  A planner walks through the units and tells the others of the next four: what
+// to load, the pages, -lse.  One warp loads K, one Q; a scout lets the issuer in to the
+// chunks (64 dims) that are there; eight warps take the accumulators, two of 256 columns
+// in turns, exponentiate and add up.
+//
+// Numbers.  Scores, weights and sums are fp32; against fp64 the weights are off by 1e-6 at
+// most, which is how the tensor cores add up 512 products.
+//
+// Bounds.  64 requests of one token, 64 heads of 512, up to 8192 tokens: 49 us for 275 MB, 5 of
+// them to start, then 6.3 TB/s.  Windows of 20 to 64 tokens over up to 20000: 67 to 72 us for
+// 117 GFLOP (68% of the time the tensor pipe works); a chunk of 256 columns takes its MMAs
+// 512 cycles, and the reads of TMEM beside them hold them up.  Small units: 16 rows against
+// 100 tokens 1.5 us each at d = 128 and 2.0 at d = 512, of a planner's step, loads, MMAs and
+// sums one behind the other.  d = 128: the exponentials (64 trees of 8 nodes, 64 heads, up to 4000
+// tokens: 35 us, of which 14 are theirs alone).
 #include <atomic>
 
 #include "attn_common.cuh"

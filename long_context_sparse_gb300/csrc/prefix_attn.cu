@@ -68,6 +68,12 @@
 // ring with loads from HBM.  d = 256 (ragged drafts): 107 us, 1022 TFLOP/s: half the
 // products a tile for the same softmax.  Small calls: 14 us on the GPU, a chain of
 // lookups, loads and hand-overs; each further item of a pair about 10 us.
+//
+// Trees.  Of drafted trees a row sees the nodes whose bits are set, in place of a limit on
+// the keys' places.  A group of 64 rows has 64 nodes at most, so that a thread (a key) needs
+// 64 bits: each lane reads those of the warp's 32 keys for two nodes, and the warp turns
+// them around.  Tiles without nodes take the usual path; against the limits on the same
+// lengths 20.6 and 18.4 us (7 nodes), 461 and 455, 1022 and 1038.
 #include <atomic>
 #include <type_traits>
 
