@@ -3,6 +3,7 @@ receive, against plain definitions (masks by walking up, products in fp64)."""
 import ctypes
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -489,6 +490,30 @@ def test_weights_sum_to_the_rows():
         slots = [int(c.table[b, p // 32]) * 32 + p % 32 for p in range(n)]
         assert abs(got.view(-1)[slots].double().sum() - 16 * c.new[b]) < 16 * c.new[b] * 2e-3
     assert out.shape == got.shape
+
+
+@gpu
+@pytest.mark.parametrize("d,page", [(128, 16), (256, 64), (512, 16), (512, 128)])
+def test_weights_of_many_short_requests(d, page):
+    """Several units a pair, with rows of all sizes behind one another; and one request's
+    NaN stays with it, whatever the others' tiles find in its place."""
+    rng = np.random.default_rng(d + page)
+    B = 330
+    new = [int(x) for x in rng.choice([0, 1, 1, 2, 4, 9, 30], B)]
+    seq = [max(n, int(x)) for n, x in zip(new, rng.integers(1, 300, B))]
+    new[7], seq[7] = 3, 200
+    c = Case(new, seq, 0, 16, d, page, 1, seed=d)
+    clean = weights_case(c, None, 0.5, 9)
+    lse = torch.nan_to_num(c.plain()[1], nan=5.0, neginf=-math.inf).float().to(DEV)
+    w = torch.rand(c.k.shape[:2], generator=torch.Generator().manual_seed(9)).to(DEV)
+    k = c.k.clone()
+    mine = torch.zeros(c.k.shape[:2], dtype=torch.bool)
+    for p in range(seq[7]):
+        at = int(c.table[7, p // page]), p % page
+        k[at], mine[at] = math.nan, True
+    got = dsa.key_weights(c.cfg, c.q.to(DEV), lse, k.to(DEV), c.table.to(DEV), i32(seq),
+                          i32(c.cu), w, decay=0.5, w_out=torch.full_like(w, 7.0)).cpu()
+    assert torch.equal(got[~mine], clean[~mine]) and got[mine].isnan().all()
 
 
 @gpu
