@@ -51,7 +51,7 @@ constexpr int kKSlots = 8;          // of 128 keys x 64 dims
 constexpr uint32_t kKBytes = 16384;
 constexpr int kQParts = 20;         // of 32 rows x 64 dims; a chunk's slot has 1, 2 or 4
 constexpr uint32_t kQBytes = 4096;
-constexpr int kUnits = 4;            // units that are planned ahead
+constexpr int kUnits = 4;           // units that are planned ahead
 constexpr uint32_t kTail = 8192;
 constexpr uint32_t kSmem = 1024 + kKSlots * kKBytes + kQParts * kQBytes + kTail;
 constexpr int kBars = 2 * kKSlots + 2 * kQParts + 6 + 2 * kUnits;
@@ -499,12 +499,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         have = walk.next(a);
         if (have) {
           const int32_t n = walk.dead(a) ? 0 : walk.rows();
-          const float* from = a.lse + walk.r.row0 + walk.block * kBlock;
+          const int32_t* from =
+              reinterpret_cast<const int32_t*>(a.lse) + walk.r.row0 + walk.block * kBlock;
 #pragma unroll
           for (int i = 0; i < kBlock / 32; ++i) {
             l[i] = -INFINITY;
-            if (32 * i + lane < n)
-              l[i] = __int_as_float(ld_input(reinterpret_cast<const int32_t*>(from + 32 * i + lane)));
+            if (32 * i + lane < n) l[i] = __int_as_float(ld_input(from + 32 * i + lane));
           }
           if (walk.block == 0 || walk.first) {
             const int32_t pos = walk.tile * kTile + (int)rank * 128 + lane * page;
