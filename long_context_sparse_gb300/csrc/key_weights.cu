@@ -395,68 +395,86 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---- this pair's share of the cost, and the request where it begins: the requests
-  // kThreads at a time, once for the sum and, where that took more than one turn,
-  // again up to the share's start
+  // ---- this pair's share of the cost, and the request where it begins.  Up to 32
+  // requests: the planner by itself, while the others go on to wait for it.  More: all
+  // threads, kThreads requests at a time, once for the sum and, where that took more than
+  // one turn, again up to the share's start.
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   int64_t total = 0, chunk = 0, start = 0, end = 0;
-  int64_t* share = scratch + 16;  // cost before the request, its number
+  int64_t first_cost = 0;  // cost before the request
+  int first_b = 0;         // its number
   {
-    const int32_t last = ld_input(a.cu + a.B);
-    int bad = ld_input(a.cu) < 0 || last > a.T;
-    int64_t mine = 0, incl = 0;  // of the last turn
-    // the cost of requests b0 .. b0 + kThreads - 1, this thread's and those before it
-    auto turn = [&](int b0, bool check) {
-      const int b = b0 + tid;
-      mine = 0;
-      if (b < a.B) {
-        const Req r = load_req(a, b);
-        mine = units_of(r) * r.cost;
-        if (check) {
-          bad |= r.rows < 0;
-          const int32_t n = blockIdx.x == 0 ? ld_input(a.seq + b) : 0;
-          if (n < 0 || n > a.max_blocks << a.page_log2)
-            latch_error(a.status, DSA_ERR_DEVICE_BAD_INDEX);
-        }
-      }
-      incl = mine;
+    // the cost of request b
+    auto cost_of = [&](int b, int& bad) -> int64_t {
+      if (b >= a.B) return 0;
+      const Req r = load_req(a, b);
+      bad |= r.rows < 0;
+      const int32_t n = blockIdx.x == 0 ? ld_input(a.seq + b) : 0;
+      if (n < 0 || n > a.max_blocks << a.page_log2)
+        latch_error(a.status, DSA_ERR_DEVICE_BAD_INDEX);
+      return units_of(r) * r.cost;
+    };
+    auto before = [&](int64_t x) {  // the sum over this lane and those before it
 #pragma unroll
       for (int s = 1; s < 32; s <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, incl, s);
-        if (lane >= s) incl += x;
+        const int64_t o = __shfl_up_sync(0xffffffffu, x, s);
+        if (lane >= s) x += o;
       }
-      if (lane == 31) scratch[warp] = incl;
-      __syncthreads();
-      int64_t all = 0;
-      for (int w = 0; w < kThreads / 32; ++w) {
-        if (w == warp) incl += all;
-        all += scratch[w];
-      }
-      __syncthreads();
-      return all;
+      return x;
     };
-    for (int b0 = 0; b0 < a.B; b0 += kThreads) total += turn(b0, true);
-    bad = __syncthreads_or(bad);
-    if (bad) {  // offsets that do not ascend within [0, T]: nothing is computed
-      total = 0;
-      if (blockIdx.x == 0 && tid == 0) latch_error(a.status, DSA_ERR_DEVICE_BAD_INDEX);
-    }
-    // (a share of a unit's cost at least: then the pairs of a tile have no gap)
-    chunk = max(ceil_div(total, pairs), (int64_t)kTileCost);
-    start = min(total, pair * chunk);
-    end = min(total, start + chunk);
-    int64_t c = 0;
-    for (int b0 = 0; b0 < a.B && start < end && c <= start; b0 += kThreads) {
-      const int64_t all = a.B > kThreads ? turn(b0, false) : total;
-      const int64_t c0 = c + incl - mine;
-      if (c0 <= start && start < c0 + mine) {
-        share[0] = c0;
-        share[1] = b0 + tid;
+    auto divide = [&](int bad, int64_t all) {
+      total = bad ? 0 : all;  // offsets that do not ascend within [0, T]: nothing is computed
+      if (bad && blockIdx.x == 0 && lane == 0) latch_error(a.status, DSA_ERR_DEVICE_BAD_INDEX);
+      // (a share of a unit's cost at least: then the pairs of a tile have no gap)
+      chunk = max(ceil_div(total, pairs), (int64_t)kTileCost);
+      start = min(total, pair * chunk);
+      end = min(total, start + chunk);
+    };
+    int bad = ld_input(a.cu) < 0 || ld_input(a.cu + a.B) > a.T;
+    if (a.B <= 32) {
+      if (warp == kPlanWarp) {
+        const int64_t mine = cost_of(lane, bad), incl = before(mine);
+        divide(__any_sync(0xffffffffu, bad), __shfl_sync(0xffffffffu, incl, 31));
+        const uint32_t who = __ballot_sync(0xffffffffu, start < end && incl > start);
+        first_b = who ? __ffs(who) - 1 : 0;  // the first whose end is beyond it
+        first_cost = __shfl_sync(0xffffffffu, incl - mine, first_b);
       }
-      c += all;
+    } else {
+      int64_t mine = 0, incl = 0, all = 0;  // of the last turn
+      auto turn = [&](int b0) {
+        mine = cost_of(b0 + tid, bad);
+        incl = before(mine);
+        if (lane == 31) scratch[warp] = incl;
+        __syncthreads();
+        all = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+          if (w == warp) incl += all;
+          all += scratch[w];
+        }
+        __syncthreads();
+      };
+      int64_t sum = 0;
+      for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+        turn(b0);
+        sum += all;
+      }
+      divide(__syncthreads_or(bad), sum);
+      int64_t* share = scratch + 16;
+      int64_t c = 0;
+      for (int b0 = 0; b0 < a.B && start < end && c <= start; b0 += kThreads) {
+        if (a.B > kThreads) turn(b0);
+        const int64_t c0 = c + incl - mine;
+        if (c0 <= start && start < c0 + mine) {
+          share[0] = c0;
+          share[1] = b0 + tid;
+        }
+        c += all;
+      }
+      __syncthreads();
+      first_cost = share[0];
+      first_b = (int)share[1];
     }
   }
-  __syncthreads();
   cluster_wait();
   tc_fence_after();
   constexpr uint32_t tmem = 0;  // an allocation of all 512 columns starts at column 0
@@ -482,7 +500,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // walked for itself before: a step to another request is some 700 cycles of one warp,
     // which small units do not hide.)
     Walk walk;
-    walk.begin(a, start, end, start < end ? share[0] : 0, start < end ? (int)share[1] : 0);
+    walk.begin(a, start, end, first_cost, first_b);
     float l[kBlock / 32] = {};
     int32_t page_id = -1, row = no_row;
     uint32_t nu = 0;
