@@ -105,7 +105,7 @@ struct Args {
 };
 
 struct Req {
-  int32_t row0, rows;  // first row (token * H), rows
+  int32_t row0, rows;  // first row (token * H), rows; rows < 0: offsets out of order or range
   int32_t len, base;   // own tokens; place of the step's first
   int32_t tiles, blocks;
   int32_t cost;        // of a unit
@@ -115,11 +115,13 @@ __device__ __forceinline__ Req load_req(const Args& a, int b) {
   const int32_t c0 = ld_input(a.cu + b), c1 = ld_input(a.cu + b + 1);
   int32_t len = ld_input(a.seq + b);
   if (len < 0 || len > a.max_blocks << a.page_log2) len = 0;  // latched by CTA 0
+  // (compared before any difference or product of them, which may wrap)
+  const bool ok = c0 >= 0 && c0 <= c1 && c1 <= a.T;
   Req r;
-  r.row0 = c0 * a.H;
-  r.rows = (c1 - c0) * a.H;
+  r.row0 = ok ? c0 * a.H : 0;
+  r.rows = ok ? (c1 - c0) * a.H : -1;
   r.len = len;
-  r.base = len - (c1 - c0);
+  r.base = ok ? len - (c1 - c0) : len;
   r.tiles = r.rows > 0 ? (len + kTile - 1) / kTile : 0;
   r.blocks = (r.rows + kBlock - 1) / kBlock;
   // (a division is a long chain; most requests have one block)
@@ -430,7 +432,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       start = min(total, pair * chunk);
       end = min(total, start + chunk);
     };
-    int bad = ld_input(a.cu) < 0 || ld_input(a.cu + a.B) > a.T;
+    int bad = 0;
     if (a.B <= 32) {
       if (warp == kPlanWarp) {
         const int64_t mine = cost_of(lane, bad), incl = before(mine);
