@@ -155,6 +155,7 @@ struct Lens {
   const int32_t *seq, *cu;
   int32_t cap;  // tokens that a table row holds
   int H;
+  int32_t T;    // query tokens, at most
 };
 
 // Of a tree's rows: which of their request's nodes they see (dsa_tree_attn).
@@ -168,7 +169,7 @@ struct ReqShape {
   int32_t n_rows;  // rows
   int32_t len;     // own tokens
   int32_t tiles;   // of its longest row
-  int32_t n_new;   // query tokens
+  int32_t n_new;   // query tokens; -1: offsets out of order or range
 };
 
 template <bool Ahead = false>
@@ -176,6 +177,8 @@ __device__ __forceinline__ ReqShape req_shape(const Lens& L, int b) {
   const int32_t c0 = ld_input<Ahead>(L.cu + b), c1 = ld_input<Ahead>(L.cu + b + 1);
   int32_t len = ld_input<Ahead>(L.seq + b);
   if (len < 0 || len > L.cap) len = 0;  // latched by CTA 0
+  // (compared before any difference or product of them, which may wrap)
+  if (c0 < 0 || c1 < c0 || c1 > L.T) return {0, 0, len, (len + kKeys - 1) / kKeys, -1};
   return {c0 * L.H, (c1 - c0) * L.H, len, (len + kKeys - 1) / kKeys, c1 - c0};
 }
 
@@ -316,14 +319,14 @@ struct Walk {
 // shared memory.  The requests are summed once for the total and scanned for
 // the one at the share's start (B <= kThreads: one step each).  `out`: CTA 0
 // writes the plan down and latches what is wrong with the lengths.
-__device__ __forceinline__ void divide(const Lens& L, int B, int64_t T, int32_t prefix_len,
+__device__ __forceinline__ void divide(const Lens& L, int B, int32_t prefix_len,
                                        int64_t pair, int pairs, const PlanView* out,
                                        uint32_t* status, Share* share, int64_t* scratch) {
   constexpr int kWarps = kThreads / 32;
   int32_t* scratch_u = reinterpret_cast<int32_t*>(scratch + kWarps);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int32_t first = ld_input(L.cu), last = ld_input(L.cu + B);
-  int bad = first < 0 || last > T;
+  const int32_t last = ld_input(L.cu + B);
+  int bad = 0;
   int64_t sum = 0;
   for (int b = tid; b < B; b += kThreads) {
     const ReqShape r = req_shape(L, b);
@@ -635,7 +638,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t pair = blockIdx.x >> 1;
-  divide(L, B, T, prefix_len, pair, gridDim.x >> 1, blockIdx.x == 0 ? &view : nullptr, status,
+  divide(L, B, prefix_len, pair, gridDim.x >> 1, blockIdx.x == 0 ? &view : nullptr, status,
          share, reinterpret_cast<int64_t*>(red));
   __syncthreads();
   cluster_wait();
@@ -1528,7 +1531,7 @@ cudaError_t launch_prefix_attn(const LaunchCtx& c, const ServeShape& s,
                                const uint32_t* tree_bits, int words, __nv_bfloat16* o,
                                float* lse, uint8_t* work) {
   const TreeBits tree{reinterpret_cast<const int32_t*>(tree_bits), words};
-  const Lens L{seq, cu, s.max_blocks << s.page_log2, s.H};
+  const Lens L{seq, cu, s.max_blocks << s.page_log2, s.H, (int32_t)s.T};
   auto run = [&](auto launch) {
     return launch(c, s, q_map, k_map, v_maps, prefix_table, (int32_t)prefix_len, table, L, tree,
                   o, lse, work);

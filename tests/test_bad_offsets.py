@@ -61,3 +61,27 @@ def test_weights_latch_offsets_that_wrap(H, T, cu, spread):
                               tree_bits=bits, w_out=torch.full_like(w, 7.0), ws=ws)
         assert dsa.get_device_status(ws) == 7
         assert (out == 7.0).all()
+
+
+@gpu
+@pytest.mark.parametrize("spread", [False, True])
+@pytest.mark.parametrize("H,T,cu", WRAPPED)
+def test_attention_latches_offsets_that_wrap(H, T, cu, spread):
+    """By trees and in order, with a prefix and without: nothing behind the results or the
+    workspace is written."""
+    cfg, k, q, table, seq, cu = requests(H, T, cu, spread)
+    need = dsa.serve_workspace_size(cfg, dsa.SERVE_WS_PREFIX)
+    for prefix in (0, 40):
+        for bits in (None, torch.full((T, 1), -1, dtype=torch.int32, device=DEV)):
+            ws = torch.zeros(need + 4096, dtype=torch.uint8, device=DEV)
+            ws[need:] = 85
+            o = torch.full((T + 8, H, 128), 7.0, dtype=BF, device=DEV)
+            lse = torch.full((T + 8, H), 7.0, device=DEV)
+            args = (cfg, q, k, i32([3, 4, 5]), prefix, table, seq, cu)
+            out = dict(o=o[:T], lse=lse[:T], ws=ws)
+            if bits is None:
+                dsa.prefix_attn(*args, **out)
+            else:
+                dsa.tree_attn(*args, bits, **out)
+            assert dsa.get_device_status(ws) == 7
+            assert (o[T:] == 7.0).all() and (lse[T:] == 7.0).all() and (ws[need:] == 85).all()
