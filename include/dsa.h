@@ -584,7 +584,8 @@ DSA_API dsa_status_t dsa_key_weights(const dsa_serve_config_t* cfg, const void* 
  * max_blocks * page_size <= 2^22, else DSA_ERR_UNSUPPORTED_SHAPE.  What is written
  * must not overlap what is read, or itself, in any other way
  * (DSA_ERR_INVALID_ARG).  A page may not belong to two requests, or stand twice
- * in one's row.
+ * in one's row; where that makes more moves than there can be of distinct slots,
+ * DSA_ERR_DEVICE_BAD_INDEX is latched and no token of any request moves.
  * Device-side errors (latched as DSA_ERR_DEVICE_BAD_INDEX; nothing is read or
  * written out of bounds): a length below 0 or above max_blocks * page_size, or a
  * keep_lens below 0 (the request is left as it is), a page id outside the cache

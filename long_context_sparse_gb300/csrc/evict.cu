@@ -32,11 +32,13 @@ static_assert(kMaxSmem >= kMaxShare / 4 + 1024 * kMaxCluster, "masks and the clu
 
 // In the workspace header, behind the status word; both are 0 between calls.
 struct Counters {
-  int32_t* moves;   // moves listed so far
+  // moves listed so far; past the list's end (where a page stands twice) none is made.
+  // 64 bits: 65536 requests of 2^21 moves
+  unsigned long long* moves;
   uint32_t* ended;  // blocks of the moving kernel that have ended
 };
 __host__ __device__ __forceinline__ Counters counters(uint8_t* ws) {
-  return {reinterpret_cast<int32_t*>(ws + 64), reinterpret_cast<uint32_t*>(ws + 128)};
+  return {reinterpret_cast<unsigned long long*>(ws + 64), reinterpret_cast<uint32_t*>(ws + 128)};
 }
 
 // Moves are of distinct slots, from and to distinct places: at most half the cache.
@@ -57,6 +59,11 @@ __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
 }
 __device__ __forceinline__ float ld_input_f(const float* p) {
   return __int_as_float(ld_input(reinterpret_cast<const int32_t*>(p)));
+}
+__device__ __forceinline__ uint64_t ld_input_u64(const unsigned long long* p) {
+  uint64_t v;
+  asm volatile("ld.global.b64 %0, [%1];" : "=l"(v) : "l"(p));
+  return v;
 }
 
 // A weight as an integer in the same order, the two zeros alike, NaN below all.
@@ -374,9 +381,9 @@ __global__ void __launch_bounds__(kMaxThreads) select_kernel(
   }
   if (rank == 0 && tid == 0) {
     const uint32_t count = (uint32_t)all;
-    const int32_t at = count ? atomicAdd(counts.moves, (int32_t)count) : 0;
+    const uint64_t at = count ? atomicAdd(counts.moves, (unsigned long long)count) : 0ull;
     // a page that stands in two places: more moves than the cache has slots for
-    const bool fits = at >= 0 && at + (int64_t)count <= list_len;
+    const bool fits = at + count <= (uint64_t)list_len;
     if (!fits) latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
     first_move = fits ? (uint32_t)at : 0xffffffffu;
   }
@@ -434,8 +441,10 @@ __global__ void __launch_bounds__(256, kMoveBlocks)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
-  const int32_t listed = ld_input(counts.moves);
-  const int64_t n = listed < 0 || listed > list_len ? list_len : listed;
+  // (past the list's end: the requests that did not fit are not in it, and what stands
+  // in their place is an older call's)
+  const uint64_t listed = ld_input_u64(counts.moves);
+  const int64_t n = listed > (uint64_t)list_len ? 0 : (int64_t)listed;
   const int64_t step = (int64_t)gridDim.x * (blockDim.x / 32) * kRows;
   int64_t x = ((int64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5)) * kRows;
   // lane l < kRows has the slots of the rows x + l; src < 0: nothing to move
@@ -445,7 +454,7 @@ __global__ void __launch_bounds__(256, kMoveBlocks)
     if (lane < kRows && at + lane < n) {
       src = ld_input(moves.src + at + lane);
       dst = ld_input(moves.dst + at + lane);
-      // bad pages; and entries that no request wrote, where a page stands twice
+      // bad pages
       if ((uint32_t)src >= n_slots || (uint32_t)dst >= n_slots) src = -1;
     }
   };
@@ -477,7 +486,7 @@ __global__ void __launch_bounds__(256, kMoveBlocks)
   // the last block to end leaves the counters as the next call wants them
   __syncthreads();
   if (threadIdx.x == 0 && atomicInc(counts.ended, gridDim.x - 1) == gridDim.x - 1)
-    *counts.moves = 0;
+    *counts.moves = 0ull;
 }
 
 // Whether a cluster of kMaxCluster of the selection's largest CTAs finds room.
