@@ -589,7 +589,8 @@ DSA_API dsa_status_t dsa_key_weights(const dsa_serve_config_t* cfg, const void* 
  * Device-side errors (latched as DSA_ERR_DEVICE_BAD_INDEX; nothing is read or
  * written out of bounds): a length below 0 or above max_blocks * page_size, or a
  * keep_lens below 0 (the request is left as it is), a page id outside the cache
- * (its tokens come last with NaN, and are not copied).
+ * (its tokens come last, behind NaN and wherever they stand, none of them is copied,
+ * and a kept token whose new place is on it is lost).
  * ws: DSA_SERVE_WS_EVICT; after a DSA_ERR_CUDA of the call it has to be
  * initialised anew. */
 DSA_API dsa_status_t dsa_evict_cache(const dsa_serve_config_t* cfg, const float* w_pages,

@@ -41,8 +41,9 @@ __host__ __device__ __forceinline__ Counters counters(uint8_t* ws) {
   return {reinterpret_cast<unsigned long long*>(ws + 64), reinterpret_cast<uint32_t*>(ws + 128)};
 }
 
-// Moves are of distinct slots, from and to distinct places: at most half the cache.
-int64_t max_moves(const ServeShape& s) { return s.n_pages * s.page / 2 + 1; }
+// Each move takes its row from a slot of its own (a request whose tokens on bad pages
+// are to move lists none).  Where no page is bad, to one of its own too: half as many.
+int64_t max_moves(const ServeShape& s) { return s.n_pages * s.page; }
 
 struct Moves {
   int32_t *src, *dst;
@@ -66,10 +67,12 @@ __device__ __forceinline__ uint64_t ld_input_u64(const unsigned long long* p) {
   return v;
 }
 
-// A weight as an integer in the same order, the two zeros alike, NaN below all.
+// A weight as an integer in the same order, the two zeros alike, NaN below all, but
+// above kBadPage, the key of a token on a page outside the cache.
+constexpr uint32_t kBadPage = 0u;
 __device__ __forceinline__ uint32_t order_key(float w) {
   const uint32_t u = __float_as_uint(w + 0.0f);
-  return w != w ? 0u : u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+  return w != w ? 1u : u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
 // The sum of x over the threads before this one, and over all of them; every thread
@@ -185,7 +188,7 @@ __global__ void __launch_bounds__(kMaxThreads) select_kernel(
   }
   auto fixed = [&](int32_t j) { return j < n_first || j >= n - n_last; };
   auto to_key = [&](int32_t j, int32_t s, float x) {
-    return fixed(j) ? 0xff800000u /* +inf */ : s < 0 ? 0u : order_key(x);
+    return s < 0 ? kBadPage : fixed(j) ? 0xff800000u /* +inf */ : order_key(x);
   };
   if (cached)
     values_of(ranks, lo + tid, hi, any,
@@ -315,10 +318,9 @@ __global__ void __launch_bounds__(kMaxThreads) select_kernel(
       uint32_t k = 0u;
       if (j < hi) {
         if (cached) k = keys[j - lo];
-        else if (fixed(j)) k = 0xff800000u;
         else {
           const int32_t s = slot_on(ld_input(row + (j >> page_log2)), j);
-          k = s < 0 ? 0u : order_key(ld_input_f(ranks + s));
+          k = to_key(j, s, s < 0 ? 0.f : ld_input_f(ranks + s));
         }
       }
       flags(j, k);
@@ -380,12 +382,14 @@ __global__ void __launch_bounds__(kMaxThreads) select_kernel(
     all = __reduce_add_sync(0xffffffffu, freed);
   }
   if (rank == 0 && tid == 0) {
-    const uint32_t count = (uint32_t)all;
+    // where tokens on bad pages stay, all others do, and those that leave are on bad pages
+    // too: nothing to copy
+    const uint32_t count = prefix == kBadPage ? 0u : (uint32_t)all;
     const uint64_t at = count ? atomicAdd(counts.moves, (unsigned long long)count) : 0ull;
     // a page that stands in two places: more moves than the cache has slots for
     const bool fits = at + count <= (uint64_t)list_len;
     if (!fits) latch_error(status, DSA_ERR_DEVICE_BAD_INDEX);
-    first_move = fits ? (uint32_t)at : 0xffffffffu;
+    first_move = fits && count ? (uint32_t)at : 0xffffffffu;
   }
   if (w_out != w) {
     // the tokens that stay where they are; each CTA has as many places below `left`,
@@ -454,7 +458,7 @@ __global__ void __launch_bounds__(256, kMoveBlocks)
     if (lane < kRows && at + lane < n) {
       src = ld_input(moves.src + at + lane);
       dst = ld_input(moves.dst + at + lane);
-      // bad pages
+      // (a move to a bad page)
       if ((uint32_t)src >= n_slots || (uint32_t)dst >= n_slots) src = -1;
     }
   };
