@@ -17,10 +17,15 @@ __device__ __forceinline__ uint32_t at_rank(uint32_t saddr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
   return r;
 }
+// For whole warps: the aligned forms want all lanes of a warp at the instruction
+// together, which behind a loop or branch that lanes leave apart nothing but the warp's
+// own barrier promises.
 __device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // Arrival at a barrier of either CTA.

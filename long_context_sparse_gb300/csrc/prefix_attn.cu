@@ -631,7 +631,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   // the barriers and TMEM are ready: the CTAs meet while they divide the work
   tc_fence_before();
-  __syncwarp();
   cluster_arrive();
   // the stream's work before; then the joining kernel may start, which reads the
   // lengths before it waits for this kernel's end
