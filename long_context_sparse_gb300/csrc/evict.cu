@@ -25,9 +25,7 @@ constexpr int kMaxThreads = 1024;  // of a CTA of the selection
 constexpr int kMaxCluster = 16;    // where the device has room for it, else 8
 constexpr int kCopies = 8;         // of a histogram, for lanes that meet in a bin
 constexpr int kMaxShare = 1 << 19;  // places of a CTA, at most: its masks take a bit each, twice
-// shared memory of a CTA that has an SM to itself, and of one of two, beside the
-// histograms (17 KB)
-constexpr int kMaxSmem = 192 * 1024, kTwoSmem = 92 * 1024;
+constexpr int kMaxSmem = 192 * 1024;  // of a CTA, beside the histograms (17 KB)
 static_assert(kMaxSmem >= kMaxShare / 4 + 1024 * kMaxCluster, "masks and the cluster's counts");
 
 // In the workspace header, behind the status word; both are 0 between calls.
@@ -548,11 +546,13 @@ cudaError_t launch_evict(const LaunchCtx& c, const ServeShape& s, const float* w
   const int64_t share = ((cap + size - 1) / size + 31) & ~(int64_t)31;
   int threads = 256;
   while (threads < kMaxThreads && share > (int64_t)threads * 4) threads *= 2;
-  // masks of the longest cache, and its keys or as many as there is room for
+  // Masks of the longest cache, and its keys or as many as there is room for: a share whose
+  // keys take more than half an SM's shared memory has a CTA of 1024 threads, whose registers
+  // leave no room for a second one (200 requests of 20000 to 32768 tokens to 8192: 185 us,
+  // with half the memory and keys read again in each pass 210).
   const int64_t sums = size > 1 ? 1024 * size : 0, masks = share / 4;
-  const int64_t limit = s.B * size <= c.num_sms ? kMaxSmem : kTwoSmem;
   const int64_t full = sums + masks + share * 4;
-  const int64_t smem = full <= limit ? full : sums + masks > limit ? sums + masks : limit;
+  const int64_t smem = full <= kMaxSmem ? full : kMaxSmem;
   const Moves moves = moves_of(s, ws);
   const Counters counts = counters(ws);
   const int64_t list_len = max_moves(s);

@@ -139,3 +139,19 @@ def test_bad_pages_leave_the_others_their_moves():
                             d_qk=128, d_v=128)
     for n_last in (0, 30, 320):
         check_bad_pages(e, t, 0, n_last)
+
+
+@gpu
+def test_more_long_requests_than_sms():
+    """A CTA a request, whose keys take more than half of an SM's shared memory."""
+    lens = [22000 + 97 * b % 9000 for b in range(160)]
+    e = Evict(lens, [n // 3 if b % 3 else n - 5 for b, n in enumerate(lens)], 128, 128, 1, "few",
+              seed=41)
+    cache, out, status = e.run(3, 50)
+    assert status == 0
+    for b in range(0, 160, 13):
+        s = e.slots(b, lens[b])
+        src = plain_keep(e.w.view(-1)[s].tolist(), e.keep[b], 3, 50)
+        assert same(out.view(-1)[s[: len(src)]], e.w.view(-1)[s[src]])
+        assert torch.equal(cache[0].view(-1, 128)[s[: len(src)]],
+                           e.cache[0].view(-1, 128)[s[src]])
