@@ -576,6 +576,9 @@ DSA_API dsa_status_t dsa_key_weights(const dsa_serve_config_t* cfg, const void* 
  * and lengths stay: one dsa_release_pages a step serves all layers.  Rows and
  * weights from left_b on, and all that belongs to no request, are left as they
  * are.  v_pages NULL: K = V.  w_out may be w_pages.
+ * Places are in the order of time until tokens move: from then on the last n_last places
+ * hold the newest tokens only where at least n_last have come since the last eviction.
+ * A request that is evicted more often keeps its newest by dsa_evict_cache_aged.
  * After a tree of drafts, a rank of -inf for the rejected nodes and of +inf for all
  * other tokens, with keep_lens the lengths without the rejected ones, leaves the
  * accepted ones with the rest.
@@ -599,6 +602,25 @@ DSA_API dsa_status_t dsa_evict_cache(const dsa_serve_config_t* cfg, const float*
                                      int64_t n_first, int64_t n_last, void* k_pages,
                                      void* v_pages, float* w_out, void* ws, size_t ws_bytes,
                                      void* stream);
+
+/* dsa_evict_cache that knows which tokens are the newest however often the request has
+ * been evicted: pos_pages says of each slot's token which of its request's tokens it is,
+ * next_pos[b] which one request b's next will be, and the first n_first and the last
+ * n_last are those of the positions
+ *   pos_pages[slot] < n_first   or   pos_pages[slot] >= next_pos[b] - n_last.
+ * pos_pages goes with the tokens: at a_i it becomes what it was at c_i.  The caller enters
+ * the new tokens' positions as it appends them (layers that are evicted alike can not
+ * share pos_pages: each call moves its own).  More tokens protected than left_b: as
+ * above, the lower places.  All else is as dsa_evict_cache has it.
+ * pos_pages [n_pages, page_size], next_pos [B] int32, of any values.
+ * ws: DSA_SERVE_WS_EVICT. */
+DSA_API dsa_status_t dsa_evict_cache_aged(const dsa_serve_config_t* cfg, const float* w_pages,
+                                          const float* rank_pages, int32_t* pos_pages,
+                                          const int32_t* next_pos, const int32_t* block_table,
+                                          const int32_t* seq_lens, const int32_t* keep_lens,
+                                          int64_t n_first, int64_t n_last, void* k_pages,
+                                          void* v_pages, float* w_out, void* ws,
+                                          size_t ws_bytes, void* stream);
 
 /* The lengths after an eviction and the pages that it leaves free, once a step:
  *   left_b = min(seq_lens[b], keep_lens[b]),   new_lens[b] = left_b,

@@ -74,7 +74,7 @@ EXPORTS = [
     "dsa_step_host", "dsa_check_wait_timeout", "dsa_static_device_status",
     "dsa_serve_workspace_size", "dsa_build_page_tables", "dsa_append_cache",
     "dsa_prefix_attn", "dsa_build_tree", "dsa_tree_attn", "dsa_key_weights",
-    "dsa_evict_cache", "dsa_release_pages", "dsa_token_logprobs",
+    "dsa_evict_cache", "dsa_evict_cache_aged", "dsa_release_pages", "dsa_token_logprobs",
     "dsa_token_logprobs_bwd",
 ]
 
@@ -254,6 +254,7 @@ def _load():
             "dsa_tree_attn": [SP, P, P, P, P, I64, P, P, P, P, I32, P, P, P, SZ, P],
             "dsa_key_weights": [SP, P, P, P, P, P, P, P, I32, P, F32, P, P, SZ, P],
             "dsa_evict_cache": [SP, P, P, P, P, P, I64, I64, P, P, P, P, SZ, P],
+            "dsa_evict_cache_aged": [SP, P, P, P, P, P, P, P, I64, I64, P, P, P, P, SZ, P],
             "dsa_release_pages": [SP, P, P, P, P, P, I64, P, P, SZ, P],
             "dsa_token_logprobs": [LP, P, P, P, P, P, P, P, P, SZ, P],
             "dsa_token_logprobs_bwd": [LP, P, P, P, P, P, P, P, I64, P, SZ, P],
@@ -1096,12 +1097,16 @@ def key_weights(cfg: ServeConfig, q, lse, k_pages, block_table, seq_lens, cu_tok
 
 def evict_cache(cfg: ServeConfig, w_pages, block_table, seq_lens, keep_lens, k_pages,
                 v_pages=None, n_first: int = 0, n_last: int = 0, w_out=None, ws=None,
-                rank_pages=None):
+                rank_pages=None, pos_pages=None, next_pos=None):
     """Shrink each request's cache to keep_lens[b] tokens, in place: those with the
     largest weights, or ranks where rank_pages is given (the first n_first and the
     last n_last always come first), the kept ones from behind moved into the places
     of the dropped ones.  Tables and lengths stay: release_pages, once for all
-    layers.  Returns w_out (None: in place).  Without v_pages: K = V."""
+    layers.  Returns w_out (None: in place).  Without v_pages: K = V.
+    The first and last are so by place, which is not by age any more once tokens have
+    moved.  With pos_pages [n_pages, page_size] int32 (which of its request's tokens
+    each slot holds: entered by the caller with new tokens, moved along here) and
+    next_pos [batch] int32 (which one the next will be) they are so by position."""
     B, i32, f32, bf = cfg.batch, torch.int32, torch.float32, torch.bfloat16
     slots = (cfg.n_pages, cfg.page_size)
     dev, p_w = _first_tensor(w_pages, "w_pages", f32, slots)
@@ -1122,8 +1127,16 @@ def evict_cache(cfg: ServeConfig, w_pages, block_table, seq_lens, keep_lens, k_p
     p_rank = None
     if rank_pages is not None:
         p_rank = _check_tensor(rank_pages, "rank_pages", f32, slots, dev)
-    _serve_call("dsa_evict_cache", dev, cfg._ref, p_w, p_rank, p_table, p_seq, p_keep, n_first,
-                n_last, p_k, p_v, p_out, p_ws, n_ws)
+    if (pos_pages is None) != (next_pos is None):
+        raise ValueError("pos_pages and next_pos go together")
+    if pos_pages is None:
+        _serve_call("dsa_evict_cache", dev, cfg._ref, p_w, p_rank, p_table, p_seq, p_keep, n_first,
+                    n_last, p_k, p_v, p_out, p_ws, n_ws)
+    else:
+        p_pos = _check_tensor(pos_pages, "pos_pages", i32, slots, dev)
+        p_next = _check_tensor(next_pos, "next_pos", i32, (B,), dev)
+        _serve_call("dsa_evict_cache_aged", dev, cfg._ref, p_w, p_rank, p_pos, p_next, p_table,
+                    p_seq, p_keep, n_first, n_last, p_k, p_v, p_out, p_ws, n_ws)
     return w_out
 
 

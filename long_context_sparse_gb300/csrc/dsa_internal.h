@@ -199,14 +199,14 @@ cudaError_t launch_key_weights(const LaunchCtx& c, const ServeShape& s,
                                const int32_t* cu, const uint32_t* tree_bits, int words,
                                const float* w_pages, float decay, float* w_out, uint8_t* ws);
 
-// Eviction by rank (which may be the weights); ws: the whole workspace (its header has
-// the counters).
+// Eviction by rank (which may be the weights), the first and last tokens by position where
+// pos_pages is not nullptr; ws: the whole workspace (its header has the counters).
 size_t evict_ws(const ServeShape& s);
 cudaError_t launch_evict(const LaunchCtx& c, const ServeShape& s, const float* w_pages,
-                         const float* rank_pages, const int32_t* table, const int32_t* seq,
-                         const int32_t* keep, int32_t n_first, int32_t n_last,
-                         __nv_bfloat16* k_pages, __nv_bfloat16* v_pages, float* w_out,
-                         uint8_t* ws);
+                         const float* rank_pages, int32_t* pos_pages, const int32_t* next_pos,
+                         const int32_t* table, const int32_t* seq, const int32_t* keep,
+                         int64_t n_first, int64_t n_last, __nv_bfloat16* k_pages,
+                         __nv_bfloat16* v_pages, float* w_out, uint8_t* ws);
 
 // Lengths after an eviction, and the pages that it leaves free.
 cudaError_t launch_release_pages(const LaunchCtx& c, const ServeShape& s, const int32_t* seq,

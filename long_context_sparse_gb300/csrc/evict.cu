@@ -13,6 +13,7 @@
 // us, of which the copy 17 (102 MB, 6 TB/s) and the selection 31.  The selection reads
 // next to nothing: it is a chain of lookups, four histograms, their exchanges through the
 // cluster (about 5000 cycles each with 16 CTAs), scans and a reservation.
+#include <algorithm>
 #include <atomic>
 
 #include "dsa_internal.h"
@@ -45,6 +46,18 @@ int64_t max_moves(const ServeShape& s) { return s.n_pages * s.page; }
 
 struct Moves {
   int32_t *src, *dst;
+};
+
+// Of each slot's token the position in its request, and of each request the next one; or
+// nullptr.
+struct Ages {
+  int32_t* pos;
+  const int32_t* next;
+};
+// What a token is ranked by.
+struct Ranked {
+  float x;
+  int32_t pos;
 };
 Moves moves_of(const ServeShape& s, uint8_t* ws) {
   int32_t* at = reinterpret_cast<int32_t*>(ws + kHeader);
@@ -105,9 +118,14 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t x, uint64_t* sums, uint6
 // digit.  Then a bit for each place says whether its token stays, and scans of
 // population counts over groups of eight places number the equal keys, the freed
 // places and the movers.
+//
+// The first (up to end_first) and the last n_last tokens are so by place or, Aged, by their
+// positions, which are looked up beside the ranks (64 requests of 1500 to 4096 tokens, none
+// protected: 21.1 us at 20.6; 131071 tokens 40.8 at 39.5).
+template <bool Aged>
 __global__ void __launch_bounds__(kMaxThreads) select_kernel(
-    const float* w, const float* ranks, const int32_t* table, const int32_t* seq,
-    const int32_t* keep, int32_t n_first, int32_t n_last, float* w_out, Moves moves,
+    const float* w, const float* ranks, Ages ages, const int32_t* table, const int32_t* seq,
+    const int32_t* keep, int32_t end_first, int64_t n_last, float* w_out, Moves moves,
     int64_t list_len, Counters counts, int max_blocks, int page_log2, int64_t n_pages,
     int32_t room, uint32_t* status) {
   extern __shared__ __align__(16) uint32_t smem[];
@@ -152,13 +170,13 @@ __global__ void __launch_bounds__(kMaxThreads) select_kernel(
     }
     return (p << page_log2) + (j & in_page);
   };
-  // f(j, slot, value from v) of the places j0, j0 + nt, .. below `end` that `which`
+  // f(j, slot, value(slot)) of the places j0, j0 + nt, .. below `end` that `which`
   // picks: kAhead pages, then kAhead values on their way at a time
-  auto values_of = [&](const float* v, int32_t j0, int32_t end, auto which, auto f) {
+  auto values_of = [&](auto value, int32_t j0, int32_t end, auto which, auto f) {
     constexpr int kAhead = 4;
     for (; j0 < end; j0 += kAhead * nt) {
       int32_t p[kAhead], s[kAhead];
-      float x[kAhead];
+      decltype(value(0)) x[kAhead];
       bool on[kAhead];
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
@@ -169,7 +187,7 @@ __global__ void __launch_bounds__(kMaxThreads) select_kernel(
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         s[u] = on[u] ? slot_on(p[u], j0 + u * nt) : -1;
-        if (s[u] >= 0) x[u] = ld_input_f(v + s[u]);
+        if (s[u] >= 0) x[u] = value(s[u]);
       }
 #pragma unroll
       for (int u = 0; u < kAhead; ++u)
@@ -177,28 +195,36 @@ __global__ void __launch_bounds__(kMaxThreads) select_kernel(
     }
   };
   auto any = [](int32_t) { return true; };
+  auto weight = [&](int32_t s) { return ld_input_f(w + s); };
+  auto ranked = [&](int32_t s) {
+    return Ranked{ld_input_f(ranks + s), Aged ? ld_input(ages.pos + s) : 0};
+  };
   if (left == n || left == 0) {  // all stay, or none
     if (w_out != w)
-      values_of(w, lo + tid, min(hi, left), any, [&](int32_t, int32_t s, float x) {
+      values_of(weight, lo + tid, min(hi, left), any, [&](int32_t, int32_t s, float x) {
         if (s >= 0) w_out[s] = x;
       });
     return;
   }
-  auto fixed = [&](int32_t j) { return j < n_first || j >= n - n_last; };
-  auto to_key = [&](int32_t j, int32_t s, float x) {
-    return s < 0 ? kBadPage : fixed(j) ? 0xff800000u /* +inf */ : order_key(x);
+  // the first of the last n_last, by position or by place
+  const int32_t recent =
+      (int32_t)max((Aged ? ld_input(ages.next + b) : n) - n_last, (int64_t)INT32_MIN);
+  auto to_key = [&](int32_t j, int32_t s, const Ranked& r) {
+    if (s < 0) return kBadPage;
+    const int32_t at = Aged ? r.pos : j;
+    return at <= end_first || at >= recent ? 0xff800000u /* +inf */ : order_key(r.x);
   };
   if (cached)
-    values_of(ranks, lo + tid, hi, any,
-              [&](int32_t j, int32_t s, float x) { keys[j - lo] = to_key(j, s, x); });
+    values_of(ranked, lo + tid, hi, any,
+              [&](int32_t j, int32_t s, const Ranked& r) { keys[j - lo] = to_key(j, s, r); });
   // f(j, key) of the places j0, j0 + nt, .. below hi
   auto each_key = [&](int32_t j0, auto f) {
     if (cached) {
 #pragma unroll 4
       for (int32_t j = j0; j < hi; j += nt) f(j, keys[j - lo]);
     } else {
-      values_of(ranks, j0, hi, any,
-                [&](int32_t j, int32_t s, float x) { f(j, to_key(j, s, x)); });
+      values_of(ranked, j0, hi, any,
+                [&](int32_t j, int32_t s, const Ranked& r) { f(j, to_key(j, s, r)); });
     }
   };
 
@@ -318,7 +344,7 @@ __global__ void __launch_bounds__(kMaxThreads) select_kernel(
         if (cached) k = keys[j - lo];
         else {
           const int32_t s = slot_on(ld_input(row + (j >> page_log2)), j);
-          k = to_key(j, s, s < 0 ? 0.f : ld_input_f(ranks + s));
+          k = s < 0 ? kBadPage : to_key(j, s, ranked(s));
         }
       }
       flags(j, k);
@@ -394,7 +420,7 @@ __global__ void __launch_bounds__(kMaxThreads) select_kernel(
     // whosever share they lie in
     const int32_t part = (left + (int)size - 1) / (int)size, from = min(left, (int)rank * part);
     values_of(
-        w, from + tid, min(left, from + part),
+        weight, from + tid, min(left, from + part),
         [&](int32_t j) {
           const uint32_t r = (uint32_t)(j / share), i = (uint32_t)(j - (int)r * share);
           return (ld_cluster(at_rank(smem_u32(above_w + (i >> 5)), r)) >> (i & 31u) & 1u) != 0u;
@@ -436,7 +462,7 @@ constexpr int kMoveBlocks = 5;  // on an SM
 template <int D, bool V>
 __global__ void __launch_bounds__(256, kMoveBlocks)
     move_kernel(Moves moves, int64_t list_len, uint4* k_pages, uint4* v_pages, const float* w,
-                float* w_out, Counters counts, int64_t n_slots) {
+                float* w_out, int32_t* pos, Counters counts, int64_t n_slots) {
   constexpr int kPieces = D / 8;                     // of a row
   constexpr int kRows = (V ? 64 : 128) / kPieces;    // 4 loads a lane
   constexpr int kLoads = kRows * kPieces / 32;       // of a tensor
@@ -475,7 +501,11 @@ __global__ void __launch_bounds__(256, kMoveBlocks)
     }
     const int32_t w_src = src, w_dst = dst;
     float weight = 0.f;
-    if (w_src >= 0) weight = ld_input_f(w + w_src);
+    int32_t place = 0;
+    if (w_src >= 0) {
+      weight = ld_input_f(w + w_src);
+      if (pos) place = ld_input(pos + w_src);
+    }
     entry(x + step);
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
@@ -483,7 +513,10 @@ __global__ void __launch_bounds__(256, kMoveBlocks)
       k_pages[to[u]] = a[u];
       if (V) v_pages[to[u]] = v[u];
     }
-    if (w_src >= 0) w_out[w_dst] = weight;
+    if (w_src >= 0) {
+      w_out[w_dst] = weight;
+      if (pos) pos[w_dst] = place;
+    }
   }
   // the last block to end leaves the counters as the next call wants them
   __syncthreads();
@@ -492,6 +525,7 @@ __global__ void __launch_bounds__(256, kMoveBlocks)
 }
 
 // Whether a cluster of kMaxCluster of the selection's largest CTAs finds room.
+template <bool Aged>
 bool fits_wide(int smem) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -504,9 +538,28 @@ bool fits_wide(int smem) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, select_kernel, &cfg) == cudaSuccess) return n > 0;
+  if (cudaOccupancyMaxActiveClusters(&n, select_kernel<Aged>, &cfg) == cudaSuccess) return n > 0;
   cudaGetLastError();
   return false;
+}
+
+// Once on a device: whether clusters of the selection may have kMaxCluster CTAs.
+template <bool Aged>
+cudaError_t prepare(int device, bool* is_wide) {
+  static std::atomic<uint64_t> prepared{0}, wide{0};
+  const uint64_t bit = 1ull << (device & 63);
+  if (!(prepared.load(std::memory_order_acquire) & bit)) {
+    cudaError_t e = cudaFuncSetAttribute(select_kernel<Aged>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(select_kernel<Aged>,
+                               cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    if (fits_wide<Aged>(kMaxSmem)) wide.fetch_or(bit, std::memory_order_relaxed);
+    prepared.fetch_or(bit, std::memory_order_release);
+  }
+  *is_wide = wide.load(std::memory_order_relaxed) & bit;
+  return cudaSuccess;
 }
 
 }  // namespace
@@ -514,21 +567,14 @@ bool fits_wide(int smem) {
 size_t evict_ws(const ServeShape& s) { return 2 * round_up((size_t)max_moves(s), 64) * 4; }
 
 cudaError_t launch_evict(const LaunchCtx& c, const ServeShape& s, const float* w_pages,
-                         const float* rank_pages, const int32_t* table, const int32_t* seq,
-                         const int32_t* keep, int32_t n_first, int32_t n_last,
-                         __nv_bfloat16* k_pages, __nv_bfloat16* v_pages, float* w_out,
-                         uint8_t* ws) {
-  cudaError_t e;
-  static std::atomic<uint64_t> prepared{0}, wide{0};
-  const uint64_t bit = 1ull << (c.device & 63);
-  if (!(prepared.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    if (fits_wide(kMaxSmem)) wide.fetch_or(bit, std::memory_order_relaxed);
-    prepared.fetch_or(bit, std::memory_order_release);
-  }
+                         const float* rank_pages, int32_t* pos_pages, const int32_t* next_pos,
+                         const int32_t* table, const int32_t* seq, const int32_t* keep,
+                         int64_t n_first, int64_t n_last, __nv_bfloat16* k_pages,
+                         __nv_bfloat16* v_pages, float* w_out, uint8_t* ws) {
+  const bool aged = pos_pages != nullptr;
+  bool wide;
+  cudaError_t e = aged ? prepare<true>(c.device, &wide) : prepare<false>(c.device, &wide);
+  if (e != cudaSuccess) return e;
   // A CTA for each 4096 tokens that a request may have, at most kMaxCluster, while an SM
   // has one (which a CTA of 1024 threads takes to itself): a cache is seldom as long as it
   // may get, and clusters that queue for SMs cost all.  us of the call with CTAs up to
@@ -538,7 +584,7 @@ cudaError_t launch_evict(const LaunchCtx& c, const ServeShape& s, const float* w
   // CTAs 23.1 25.7 25.8 28.5.  A thread for each four places of a share (for 64 of 4096
   // 23.1, with eight 24.0, with sixteen 27.7).
   const int64_t cap = (int64_t)s.max_blocks * s.page;
-  const int most = wide.load(std::memory_order_relaxed) & bit ? kMaxCluster : 8;
+  const int most = wide ? kMaxCluster : 8;
   int size = 1;
   while (size < most && ((cap > (int64_t)size * 4096 && s.B * size * 2 <= c.num_sms) ||
                          cap > (int64_t)size * kMaxShare))
@@ -569,9 +615,11 @@ cudaError_t launch_evict(const LaunchCtx& c, const ServeShape& s, const float* w
   cfg.stream = c.stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, select_kernel, w_pages, rank_pages, table, seq, keep, n_first,
-                         n_last, w_out, moves, list_len, counts, s.max_blocks, s.page_log2,
-                         s.n_pages, (int32_t)((smem - sums) / 4), c.status);
+  e = cudaLaunchKernelEx(&cfg, aged ? select_kernel<true> : select_kernel<false>, w_pages,
+                         rank_pages, Ages{pos_pages, next_pos}, table, seq, keep,
+                         (int32_t)std::min(n_first - 1, (int64_t)INT32_MAX), n_last, w_out,
+                         moves, list_len, counts, s.max_blocks, s.page_log2, s.n_pages,
+                         (int32_t)((smem - sums) / 4), c.status);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)(c.num_sms * kMoveBlocks));
   cfg.blockDim = dim3(256);
@@ -579,7 +627,7 @@ cudaError_t launch_evict(const LaunchCtx& c, const ServeShape& s, const float* w
   cfg.numAttrs = 1;
   auto run = [&](auto kern) {
     return cudaLaunchKernelEx(&cfg, kern, moves, list_len, reinterpret_cast<uint4*>(k_pages),
-                              reinterpret_cast<uint4*>(v_pages), w_pages, w_out, counts,
+                              reinterpret_cast<uint4*>(v_pages), w_pages, w_out, pos_pages, counts,
                               (int64_t)(s.n_pages * s.page));
   };
   if (v_pages) {

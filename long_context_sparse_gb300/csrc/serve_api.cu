@@ -120,6 +120,45 @@ dsa_status_t attend(const dsa_serve_config_t* cfg, const void* q, const void* k_
                                         static_cast<uint8_t*>(ws) + kHeader));
 }
 
+// Both evictions; pos_pages and next_pos NULL: the first and last tokens by place.
+dsa_status_t evict(const dsa_serve_config_t* cfg, const float* w_pages, const float* rank_pages,
+                   int32_t* pos_pages, const int32_t* next_pos, const int32_t* block_table,
+                   const int32_t* seq_lens, const int32_t* keep_lens, int64_t n_first,
+                   int64_t n_last, void* k_pages, void* v_pages, float* w_out, void* ws,
+                   size_t ws_bytes, void* stream) {
+  dsa_status_t st = check_serve(cfg, DSA_SERVE_WS_EVICT);
+  if (st != DSA_OK) return st;
+  if (!w_pages || !block_table || !seq_lens || !keep_lens || n_first < 0 || n_last < 0 ||
+      !k_pages || !w_out || v_pages == k_pages)  // K = V: v_pages null
+    return DSA_ERR_INVALID_ARG;
+  if ((st = check_serve_ws(cfg, DSA_SERVE_WS_EVICT, ws, ws_bytes)) != DSA_OK) return st;
+  const void* ptrs[] = {w_pages,  rank_pages, pos_pages, next_pos, block_table,
+                        seq_lens, keep_lens,  k_pages,   v_pages,  w_out};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return DSA_ERR_MISALIGNED;
+  const size_t B = (size_t)cfg->batch, slots = (size_t)cfg->n_pages * cfg->page_size;
+  const size_t cache = slots * cfg->d_qk * 2;
+  if (rank_pages == w_pages) rank_pages = nullptr;
+  const Span reads[] = {{w_pages == w_out ? nullptr : w_pages, slots * 4},
+                        {rank_pages, slots * 4},
+                        {next_pos, B * 4},
+                        {block_table, B * (size_t)cfg->max_blocks * 4},
+                        {seq_lens, B * 4},
+                        {keep_lens, B * 4}};
+  const Span writes[] = {{k_pages, cache},
+                         {v_pages, cache},
+                         {pos_pages, slots * 4},
+                         {w_out, slots * 4},
+                         {ws, serve_ws_bytes(cfg, DSA_SERVE_WS_EVICT)}};
+  if (written_meets(writes, reads)) return DSA_ERR_INVALID_ARG;
+  LaunchCtx ctx;
+  if ((st = make_ctx(ws, stream, &ctx)) != DSA_OK) return st;
+  return cuda_status(launch_evict(
+      ctx, serve_shape(cfg), w_pages, rank_pages ? rank_pages : w_pages, pos_pages, next_pos,
+      block_table, seq_lens, keep_lens, n_first, n_last, static_cast<__nv_bfloat16*>(k_pages),
+      static_cast<__nv_bfloat16*>(v_pages), w_out, static_cast<uint8_t*>(ws)));
+}
+
 }  // namespace
 }  // namespace dsa
 
@@ -287,37 +326,20 @@ dsa_status_t dsa_evict_cache(const dsa_serve_config_t* cfg, const float* w_pages
                              const int32_t* seq_lens, const int32_t* keep_lens, int64_t n_first,
                              int64_t n_last, void* k_pages, void* v_pages, float* w_out,
                              void* ws, size_t ws_bytes, void* stream) {
-  dsa_status_t st = check_serve(cfg, DSA_SERVE_WS_EVICT);
-  if (st != DSA_OK) return st;
-  if (!w_pages || !block_table || !seq_lens || !keep_lens || n_first < 0 || n_last < 0 ||
-      !k_pages || !w_out || v_pages == k_pages)  // K = V: v_pages null
-    return DSA_ERR_INVALID_ARG;
-  if ((st = check_serve_ws(cfg, DSA_SERVE_WS_EVICT, ws, ws_bytes)) != DSA_OK) return st;
-  const void* ptrs[] = {w_pages,   rank_pages, block_table, seq_lens,
-                        keep_lens, k_pages,    v_pages,     w_out};
-  for (const void* p : ptrs)
-    if (!aligned16(p)) return DSA_ERR_MISALIGNED;
-  const size_t B = (size_t)cfg->batch, slots = (size_t)cfg->n_pages * cfg->page_size;
-  const size_t cache = slots * cfg->d_qk * 2;
-  if (rank_pages == w_pages) rank_pages = nullptr;
-  const Span reads[] = {{w_pages == w_out ? nullptr : w_pages, slots * 4},
-                        {rank_pages, slots * 4},
-                        {block_table, B * (size_t)cfg->max_blocks * 4},
-                        {seq_lens, B * 4},
-                        {keep_lens, B * 4}};
-  const Span writes[] = {{k_pages, cache},
-                         {v_pages, cache},
-                         {w_out, slots * 4},
-                         {ws, serve_ws_bytes(cfg, DSA_SERVE_WS_EVICT)}};
-  if (written_meets(writes, reads)) return DSA_ERR_INVALID_ARG;
-  LaunchCtx ctx;
-  if ((st = make_ctx(ws, stream, &ctx)) != DSA_OK) return st;
-  const int32_t most = INT32_MAX;  // lengths are below 2^30
-  return cuda_status(launch_evict(
-      ctx, serve_shape(cfg), w_pages, rank_pages ? rank_pages : w_pages, block_table, seq_lens,
-      keep_lens, (int32_t)(n_first < most ? n_first : most),
-      (int32_t)(n_last < most ? n_last : most), static_cast<__nv_bfloat16*>(k_pages),
-      static_cast<__nv_bfloat16*>(v_pages), w_out, static_cast<uint8_t*>(ws)));
+  return evict(cfg, w_pages, rank_pages, nullptr, nullptr, block_table, seq_lens, keep_lens,
+               n_first, n_last, k_pages, v_pages, w_out, ws, ws_bytes, stream);
+}
+
+dsa_status_t dsa_evict_cache_aged(const dsa_serve_config_t* cfg, const float* w_pages,
+                                  const float* rank_pages, int32_t* pos_pages,
+                                  const int32_t* next_pos, const int32_t* block_table,
+                                  const int32_t* seq_lens, const int32_t* keep_lens,
+                                  int64_t n_first, int64_t n_last, void* k_pages,
+                                  void* v_pages, float* w_out, void* ws, size_t ws_bytes,
+                                  void* stream) {
+  if (!pos_pages || !next_pos) return DSA_ERR_INVALID_ARG;
+  return evict(cfg, w_pages, rank_pages, pos_pages, next_pos, block_table, seq_lens, keep_lens,
+               n_first, n_last, k_pages, v_pages, w_out, ws, ws_bytes, stream);
 }
 
 dsa_status_t dsa_release_pages(const dsa_serve_config_t* cfg, const int32_t* seq_lens,
