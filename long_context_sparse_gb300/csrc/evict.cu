@@ -8,8 +8,8 @@
 // in any order, and only about left (1 - left / n) of them move, where keeping the
 // order would move nearly all.
 //
-// Bounds.  64 requests of up to 4096 tokens of 512: 30 us with the pages' release (4),
-// of which the copy 12 (73 MB) and the selection 15; 131071 tokens to 32768, K and V: 51
+// Bounds (in a graph).  64 requests of up to 4096 tokens of 512: 30 us with the pages' release
+// (4), of which the copy 12 (73 MB) and the selection 15; 131071 tokens to 32768, K and V: 52
 // us, of which the copy 17 (102 MB, 6 TB/s) and the selection 31.  The selection reads
 // next to nothing: it is a chain of lookups, four histograms, their exchanges through the
 // cluster (about 5000 cycles each with 16 CTAs), scans and a reservation.

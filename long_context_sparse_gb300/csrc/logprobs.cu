@@ -8,9 +8,11 @@
 // (no term of H cancels another: y <= 0 but for the first batch's own rounding).
 // The reference is taken off before the scale, so that large logits lose nothing.
 //
-// Bounds.  4095 rows of 100277 fp32 with 5 alternatives: 249 us, 6.6 TB/s, as a plain copy.
-// 64 rows of 131072 bf16 with 20: 12.4 us, of which the pass 5.8 and six short steps of the
-// alternatives, each behind a barrier, the rest.
+// Bounds (in a graph).  4095 rows of 100277 fp32 with 5 alternatives: 246 to 249 us, 6.6 TB/s,
+// as a plain copy.  64 rows of 131072 bf16 with 20: 12.4 us, of which the pass 6.1 and six
+// short steps of the alternatives, each behind a barrier, the rest; the eager call 22 to 26,
+// 15 where the caller has its results (`out`).  4096 rows of 131072 bf16 with 0, 1, 5, 20, 32,
+// 48, 64 alternatives: 158 188 192 209 227 262 288.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -643,7 +645,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprobs_kernel(
 
 // Backward.  With l = log p = scale x - lse:  dx = 2^(l log2 e) (A + B l) + 1[tok] G,
 //   A = -scale (g + h H),  B = -scale h,  G = scale g.
-// 8192 rows of 131072 bf16: 606 us, 7.1 TB/s; 301 of 50257 fp16 10 us.
+// 8192 rows of 131072 bf16: 607 us, 7.1 TB/s (as long where half of them have no gradient:
+// their logits are read all the same); 301 of 50257 fp16 10 us (in a graph; eager 15).
 // A block takes kUnroll vectors a thread of one row, as the gradient lies in its 16
 // bytes.  Where the logits lie differently, a vector of them is put together from the
 // two that hold it: the neighbour's second is this one's first, and comes from L1
@@ -671,7 +674,7 @@ __global__ void __launch_bounds__(kBwdThreads) logprobs_bwd_kernel(
     const int32_t* tokens, const float* lse, const float* entropy, const float* g_logp,
     const float* g_entropy, float scale, T* dlogits, int64_t ld_grad, uint32_t* status) {
   using W = Word<T>;
-  constexpr int kVec = Row<T>::kVec, kSeg = kUnroll * kBwdThreads;
+  constexpr int kSeg = kUnroll * kBwdThreads;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x;

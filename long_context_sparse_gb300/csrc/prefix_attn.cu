@@ -72,8 +72,10 @@
 // Trees.  Of drafted trees a row sees the nodes whose bits are set, in place of a limit on
 // the keys' places.  A group of 64 rows has 64 nodes at most, so that a thread (a key) needs
 // 64 bits: each lane reads those of the warp's 32 keys for two nodes, and the warp turns
-// them around.  Tiles without nodes take the usual path; against the limits on the same
-// lengths 20.6 and 18.4 us (7 nodes), 461 and 455, 1022 and 1038.
+// them around.  Tiles without nodes take the usual path.  In a graph, and by limits on the
+// same lengths: 20.6 us at 18.4 (7 nodes, 12% more), 461 at 455, 1022 at 1038.  33 to 64 nodes
+// of 16 heads behind 65535, 24 requests, d = 128: 909 us (d = 256 1025), of the same softmax
+// against half the products.
 #include <atomic>
 #include <type_traits>
 

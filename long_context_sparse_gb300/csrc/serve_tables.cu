@@ -273,8 +273,9 @@ __global__ void __launch_bounds__(kReq) release_kernel(
 // ------------------------------------------------------------- tree masks
 // A thread for each word of a row's mask walks up from the row's node; numbers
 // fall on the way, so it may stop below its word: at most 32 * words steps,
-// whatever the parents hold.  7 nodes: 1.6 us, 24 trees of up to 64: 3.7 us (in a graph), latency
-// (offsets, then a parent from L1 for each step).
+// whatever the parents hold.  In a graph: 7 nodes 1.6 us, 24 random trees of up to 64 2 to 4,
+// latency (offsets, then a parent from L1 for each step).  Long chains are slow, since each
+// word of a row walks for itself: 64 nodes (2 words) 4.9 us, 256 (8) 65, 1024 (32) 3540.
 __global__ void __launch_bounds__(256) tree_kernel(const int32_t* parents,
                                                    const int32_t* cu, int words,
                                                    uint32_t* __restrict__ bits, int B, int64_t T,
